@@ -553,6 +553,202 @@ uint32_t bs_plan_waves_per_block(const bs_plan* plan);
  * range out of bounds. */
 uint32_t bs_plan_packs(const bs_plan* plan, uint32_t first, uint32_t count);
 
+/* ------------------------------------------------- adapters of many requests
+ *
+ * Low-rank adapters beside a shared projection W (rows x cols): y_t += s_a
+ * B_a (A_a x_t), a the adapter of token t.  A pack holds all adapters of one
+ * projection, a batch says which token has which; a batch is made once per
+ * step and serves every projection that the step's tokens go through.
+ * Nothing here allocates or synchronises; device buffers are the caller's. */
+enum { BS_T_BF16 = 1, BS_T_FP32 = 2 };   /* element types of activations */
+
+typedef struct {
+    uint32_t adapters;      /* 1..4096 */
+    uint32_t rank;          /* 16, 32, 64 or 128: the rank that storage is laid out for */
+    uint32_t rows, cols;    /* of the projection, below 2^26 */
+    const void* d_a;        /* BF16 [adapters][rank][cols rounded up to 32], zeros past an adapter's rank and past cols; 16-B aligned */
+    const void* d_b;        /* BF16 [adapters][rows][rank], zeros past an adapter's rank; 16-B aligned */
+    const int32_t* d_ranks; /* each adapter's own rank, 1..rank */
+    const float* d_factor;  /* s */
+} bs_lora_pack;
+
+/* Device bytes of a batch of `tokens` tokens over `adapters` adapters; 0 for
+ * sizes out of range (tokens above 2^24). */
+uint64_t bs_lora_batch_bytes(uint32_t tokens, uint32_t adapters);
+
+/* Make a batch: d_adapter_of[t] is token t's adapter, or -1 for none; an
+ * index out of range counts as none and is counted in word 2 of the batch.
+ * d_batch: 16-B aligned, batch_bytes of it.  One kernel launch on `stream`.
+ * Errors: BS_E_INVAL, BS_E_HIP. */
+bs_status bs_lora_batch_async(const int32_t* d_adapter_of, uint32_t tokens, uint32_t adapters, int32_t* d_batch,
+                              uint64_t batch_bytes, void* stream);
+
+/* Workspace of bs_lora_add_async for `tokens` tokens (0: a pack or count that
+ * it refuses). */
+uint64_t bs_lora_work_bytes(const bs_lora_pack* pack, uint32_t tokens);
+
+/* y_out[t] = y_in[t] + s_a B_a (A_a x_t) for every token of the batch (one
+ * made for this many tokens and this pack's number of adapters); tokens
+ * without an adapter keep y_in.  x: BF16 rows of cols, x_stride elements
+ * apart; y: rows of `rows` elements of y_type, y_stride apart, in and out
+ * the same buffer or two that do not overlap.  Sums are held in fp32 in one
+ * fixed order (the same result on every run) and y is rounded once.  Two
+ * kernel launches on `stream`; calls that share d_work (16-B aligned) must
+ * not overlap.  Errors: BS_E_INVAL, BS_E_HIP. */
+bs_status bs_lora_add_async(const bs_lora_pack* pack, const int32_t* d_batch, uint32_t tokens, const void* d_x,
+                            uint64_t x_stride, const void* d_y_in, void* d_y_out, uint64_t y_stride, uint32_t y_type,
+                            void* d_work, uint64_t work_bytes, void* stream);
+
+/* bs_fixed_gemm_async with adapters: Y[b] = W X[b] + s_a B_a (A_a X[b]), W the
+ * weights of a fixed-width blob, decoded where they are used.  The adapters'
+ * second product also joins the two halves of the split product, so no
+ * launch and no pass over Y is added for it.  d_work: 256-B aligned, at least
+ * bs_fixed_gemm_lora_work_bytes (0: a shape or pack that is refused).  Other
+ * arguments and errors as for bs_fixed_gemm_async and bs_lora_add_async. */
+uint64_t bs_fixed_gemm_lora_work_bytes(uint64_t rows, uint64_t cols, uint32_t batch, const bs_lora_pack* pack);
+bs_status bs_fixed_gemm_lora_async(const bs_fixed_info* info, const void* d_blob, uint64_t rows, uint64_t cols,
+                                   uint32_t batch, const void* d_x, float* d_y, uint32_t* d_status,
+                                   const bs_lora_pack* pack, const int32_t* d_batch, void* d_work, uint64_t work_bytes,
+                                   void* stream);
+
+/* ------------------------------------------------- paged key/value cache
+ *
+ * Keys and values of many sequences in 8 bits, in pages of page_tokens
+ * tokens, for all layers of a model; every buffer is the caller's.  Rows of
+ * the table are sequences: token p of row r is slot p mod page_tokens of page
+ * table[r][p / page_tokens], the same page number in every layer.
+ *   d_k     [layers][n_pages][kv_heads][page_tokens][wide] codes
+ *   d_v     [layers][n_pages][kv_heads][wide][page_tokens] codes (a channel's
+ *           tokens side by side: the order in which the product with the
+ *           probabilities reads them)
+ *   d_scale [layers][n_pages][kv_heads][2] fp32 (keys, values)
+ *   d_refs  [n_pages]: rows that hold the page (0: free)
+ *   d_table [max_seqs][max_pages], d_lens [max_seqs]
+ * wide is head_dim rounded up to a multiple of 64; d_k must hold zeros past
+ * head_dim (bs_kv_append_async writes them).  A stored value is code times
+ * scale, the scale a power of two: the least 2^e, e >= -60, with |x| <= Q 2^e
+ * for all values of the page, head and side (Q = 448 for e4m3, 127 for
+ * int8).  When new tokens need a larger scale, those already in the page are
+ * rounded again, each time by at most half a step of the new scale, so by at
+ * most one step of the last in all.  Non-finite inputs are stored as 0 (NaN)
+ * or the largest value (infinities) and flagged.
+ *
+ * Before first use d_refs and d_lens hold zeros.  A free page has count 0 and
+ * the lowest free pages are taken first.  A page that more than one row
+ * holds is full, so rows can go on growing without copies.
+ *
+ * Conditions found on the GPU are OR-ed into *d_status (may be NULL), which
+ * the caller clears: BS_KV_NO_PAGES, BS_KV_ROW_FULL, BS_KV_BAD_ID (a row, page
+ * or token range that does not exist), BS_KV_ROW_IN_USE (a child row that is
+ * not empty), BS_KV_NOT_FINITE, BS_KV_BAD_COUNT (a page freed more often than
+ * held).  Nothing out of range is read or written in any of these cases.
+ *
+ * All calls enqueue kernels on `stream`, allocate nothing and can be captured
+ * in a graph.  Calls on one cache must not overlap, except that attention
+ * calls may overlap each other.  Errors: BS_E_INVAL (shape, alignment, NULL),
+ * BS_E_HIP. */
+enum { BS_KV_E4M3 = 1, BS_KV_INT8 = 2 };
+enum {
+    BS_KV_NO_PAGES = 1, BS_KV_ROW_FULL = 2, BS_KV_BAD_ID = 4, BS_KV_ROW_IN_USE = 8, BS_KV_NOT_FINITE = 16,
+    BS_KV_BAD_COUNT = 32
+};
+
+typedef struct {
+    uint32_t layers, n_pages, max_seqs, max_pages;   /* max_pages: of one row */
+    uint32_t kv_heads, head_dim;                     /* head_dim 1..256 */
+    uint32_t page_tokens;                            /* 16, 32, 64, 128 or 256 */
+    uint32_t type;                                   /* BS_KV_E4M3 (OCP, finite) or BS_KV_INT8 */
+    void* d_k;                                       /* 16-B aligned */
+    void* d_v;                                       /* 16-B aligned */
+    float* d_scale;
+    int32_t* d_refs;                                 /* 16-B aligned */
+    int32_t* d_table;
+    int32_t* d_lens;
+    uint32_t* d_status;
+} bs_kv_cache;
+
+typedef struct {
+    uint64_t side_bytes;    /* of d_k, and of d_v */
+    uint64_t scale_bytes;   /* of d_scale */
+    uint64_t page_bytes;    /* one page of one layer: keys, values and scales */
+    uint32_t wide, reserved;
+} bs_kv_sizes;
+
+/* Buffer sizes of a cache of this shape (pointers are not looked at). */
+bs_status bs_kv_sizes_get(const bs_kv_cache* cache, bs_kv_sizes* out);
+
+/* Grow rows d_seqs[i] (distinct) by d_counts[i] >= 0 tokens: lengths are
+ * advanced and pages taken where they are needed, in the order of the list.
+ * Either every row grows, or none does and the status says why.  d_work:
+ * bs_kv_pages_work_bytes(cache, n), 16-B aligned. */
+bs_status bs_kv_extend_async(const bs_kv_cache* cache, uint32_t n, const int32_t* d_seqs, const int32_t* d_counts,
+                             void* d_work, uint64_t work_bytes, void* stream);
+
+/* Make rows d_children[i] (empty, distinct, none of them a parent) hold the
+ * tokens of rows d_parents[i]: whole pages are shared, a last, partly filled
+ * page is copied in every layer to a page of the child's own.  All or none,
+ * as for bs_kv_extend_async. */
+bs_status bs_kv_fork_async(const bs_kv_cache* cache, uint32_t n, const int32_t* d_parents, const int32_t* d_children,
+                           void* d_work, uint64_t work_bytes, void* stream);
+
+/* Empty rows: their pages' counts fall by one. */
+bs_status bs_kv_free_async(const bs_kv_cache* cache, uint32_t n, const int32_t* d_seqs, void* stream);
+
+/* Copy pages d_from[i] to d_to[i] (distinct, none of them among d_from) in
+ * every layer: codes and scales, no counts. */
+bs_status bs_kv_copy_pages_async(const bs_kv_cache* cache, uint32_t n, const int32_t* d_from, const int32_t* d_to,
+                                 void* stream);
+
+/* Move the pages in use to the lowest places: with n of them, the k-th one at
+ * n or above goes to the k-th free place below n, in every layer.  The new
+ * table (entries past a row's pages: -1) and counts go to buffers of their
+ * own, which the caller uses from then on. */
+bs_status bs_kv_compact_async(const bs_kv_cache* cache, int32_t* d_table_out, int32_t* d_refs_out, void* d_work,
+                              uint64_t work_bytes, void* stream);
+
+/* Workspace of the calls above for n rows or pairs (0: a shape they refuse). */
+uint64_t bs_kv_pages_work_bytes(const bs_kv_cache* cache, uint32_t n);
+
+/* Store the keys and values of the last tokens of rows d_seqs[i] (distinct,
+ * already extended) in layer `layer`: tokens d_starts[i] .. d_starts[i + 1] -
+ * 1 of the input are the last ones of row d_seqs[i] (d_starts NULL: one token
+ * each, in order).  total: tokens in all; max_new: the most of one row.  d_k,
+ * d_v: [total][kv_heads][head_dim] of dtype (BS_T_BF16 or BS_T_FP32), a
+ * token's values side by side, k_stride and v_stride elements between
+ * tokens.  One kernel launch. */
+bs_status bs_kv_append_async(const bs_kv_cache* cache, uint32_t layer, uint32_t n_seqs, const int32_t* d_seqs,
+                             const int32_t* d_starts, uint32_t total, uint32_t max_new, const void* d_k, uint64_t k_stride,
+                             const void* d_v, uint64_t v_stride, uint32_t dtype, void* stream);
+
+typedef struct {
+    uint32_t layer, n_seqs;
+    uint32_t heads;             /* query heads, a multiple of kv_heads: head h reads key head h / (heads / kv_heads) */
+    uint32_t total_q, max_new;  /* query tokens in all, and the most of one row */
+    uint32_t max_len;           /* no row in the call is longer (0: max_pages pages); only splits the work */
+    const int32_t* d_seqs;      /* rows (a row may be named more than once) */
+    const int32_t* d_starts;    /* n_seqs + 1 offsets into the queries, or NULL: one each */
+    const void* d_q;            /* BF16 [total_q][heads][head_dim], q_stride elements between tokens */
+    void* d_out;                /* BF16, the same shape, out_stride elements between tokens */
+    float* d_lse;               /* NULL, or [total_q][heads]: the natural logarithm of the softmax sum */
+    uint64_t q_stride, out_stride;
+    float scale;                /* of q k (0: 1 / sqrt(head_dim)) */
+    float softcap;              /* 0: none; else logits become softcap tanh(logit / softcap) */
+    uint32_t window;            /* 0: all tokens up to the query's own; else the last `window` of them, */
+    uint32_t sinks;             /* and the first `sinks` tokens of the row */
+} bs_kv_attend_args;
+
+/* Attention of new tokens over the cache, their own keys and values included:
+ * query j of n new ones of a row of length L stands at place L - n + j and
+ * sees the tokens up to it.  A query that sees nothing gives 0 and a
+ * logarithm of -infinity.  Scores and sums are held in fp32; probabilities
+ * enter the second product in BF16, the type of the result.  What slots past
+ * a row's length hold does not matter.  The same result on every run.
+ * d_work (16-B aligned): bs_kv_attend_work_bytes, which gives 0 where rows
+ * need not be split; without it (NULL) they are not. */
+bs_status bs_kv_attend_async(const bs_kv_cache* cache, const bs_kv_attend_args* args, void* d_work, uint64_t work_bytes,
+                             void* stream);
+uint64_t bs_kv_attend_work_bytes(const bs_kv_cache* cache, const bs_kv_attend_args* args);
+
 /* ------------------------------------------------------- layer streaming
  *
  * Layers streamed on demand under a budget of device memory [Gemma 2 9B

@@ -28,6 +28,13 @@ NOALLOC_MAX_WEIGHTS = 1 << 36   # words per bs_build_tables_noalloc call
 KIND_BF16 = 1
 KIND_RAW = 2
 
+T_BF16 = 1                   # element types of activations
+T_FP32 = 2
+KV_TYPES = {"e4m3": 1, "int8": 2}
+KV_STATUS = {1: "out of free pages", 2: "a row is full", 4: "a row, page or token range that does not exist",
+             8: "a child row is in use", 16: "non-finite values were stored as finite ones",
+             32: "a page was freed more often than held"}
+
 VERIFY_STATUS = 1
 VERIFY_COMPARE = 2
 VERIFY_SHA256 = 4
@@ -86,6 +93,31 @@ class StreamerStats(C.Structure):
                 ("misses", C.c_uint64), ("evictions", C.c_uint64), ("h2d_bytes", C.c_uint64)]
 
 
+class LoraPack(C.Structure):
+    _fields_ = [("adapters", C.c_uint32), ("rank", C.c_uint32), ("rows", C.c_uint32), ("cols", C.c_uint32),
+                ("d_a", C.c_void_p), ("d_b", C.c_void_p), ("d_ranks", C.c_void_p), ("d_factor", C.c_void_p)]
+
+
+class KvCache(C.Structure):
+    _fields_ = [("layers", C.c_uint32), ("n_pages", C.c_uint32), ("max_seqs", C.c_uint32), ("max_pages", C.c_uint32),
+                ("kv_heads", C.c_uint32), ("head_dim", C.c_uint32), ("page_tokens", C.c_uint32), ("type", C.c_uint32),
+                ("d_k", C.c_void_p), ("d_v", C.c_void_p), ("d_scale", C.c_void_p), ("d_refs", C.c_void_p),
+                ("d_table", C.c_void_p), ("d_lens", C.c_void_p), ("d_status", C.c_void_p)]
+
+
+class KvSizes(C.Structure):
+    _fields_ = [("side_bytes", C.c_uint64), ("scale_bytes", C.c_uint64), ("page_bytes", C.c_uint64),
+                ("wide", C.c_uint32), ("reserved", C.c_uint32)]
+
+
+class KvAttendArgs(C.Structure):
+    _fields_ = [("layer", C.c_uint32), ("n_seqs", C.c_uint32), ("heads", C.c_uint32), ("total_q", C.c_uint32),
+                ("max_new", C.c_uint32), ("max_len", C.c_uint32), ("d_seqs", C.c_void_p), ("d_starts", C.c_void_p),
+                ("d_q", C.c_void_p), ("d_out", C.c_void_p), ("d_lse", C.c_void_p), ("q_stride", C.c_uint64),
+                ("out_stride", C.c_uint64), ("scale", C.c_float), ("softcap", C.c_float), ("window", C.c_uint32),
+                ("sinks", C.c_uint32)]
+
+
 # every symbol declared in include/bs.h, with (restype, argtypes)
 SIGNATURES = {
     "bs_params_default": (None, [C.POINTER(Params)]),
@@ -139,6 +171,28 @@ SIGNATURES = {
     "bs_fixed_gemm_async": (C.c_int, [C.POINTER(FixedInfo), C.c_void_p, C.c_uint64, C.c_uint64, C.c_uint32,
                                       C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_uint64, C.c_void_p]),
     "bs_fixed_gemm_work_bytes": (C.c_uint64, [C.c_uint64, C.c_uint64, C.c_uint32]),
+    "bs_lora_batch_bytes": (C.c_uint64, [C.c_uint32, C.c_uint32]),
+    "bs_lora_batch_async": (C.c_int, [C.c_void_p, C.c_uint32, C.c_uint32, C.c_void_p, C.c_uint64, C.c_void_p]),
+    "bs_lora_work_bytes": (C.c_uint64, [C.POINTER(LoraPack), C.c_uint32]),
+    "bs_lora_add_async": (C.c_int, [C.POINTER(LoraPack), C.c_void_p, C.c_uint32, C.c_void_p, C.c_uint64, C.c_void_p,
+                                    C.c_void_p, C.c_uint64, C.c_uint32, C.c_void_p, C.c_uint64, C.c_void_p]),
+    "bs_fixed_gemm_lora_work_bytes": (C.c_uint64, [C.c_uint64, C.c_uint64, C.c_uint32, C.POINTER(LoraPack)]),
+    "bs_fixed_gemm_lora_async": (C.c_int, [C.POINTER(FixedInfo), C.c_void_p, C.c_uint64, C.c_uint64, C.c_uint32,
+                                           C.c_void_p, C.c_void_p, C.c_void_p, C.POINTER(LoraPack), C.c_void_p,
+                                           C.c_void_p, C.c_uint64, C.c_void_p]),
+    "bs_kv_sizes_get": (C.c_int, [C.POINTER(KvCache), C.POINTER(KvSizes)]),
+    "bs_kv_extend_async": (C.c_int, [C.POINTER(KvCache), C.c_uint32, C.c_void_p, C.c_void_p, C.c_void_p, C.c_uint64,
+                                     C.c_void_p]),
+    "bs_kv_fork_async": (C.c_int, [C.POINTER(KvCache), C.c_uint32, C.c_void_p, C.c_void_p, C.c_void_p, C.c_uint64,
+                                   C.c_void_p]),
+    "bs_kv_free_async": (C.c_int, [C.POINTER(KvCache), C.c_uint32, C.c_void_p, C.c_void_p]),
+    "bs_kv_copy_pages_async": (C.c_int, [C.POINTER(KvCache), C.c_uint32, C.c_void_p, C.c_void_p, C.c_void_p]),
+    "bs_kv_compact_async": (C.c_int, [C.POINTER(KvCache), C.c_void_p, C.c_void_p, C.c_void_p, C.c_uint64, C.c_void_p]),
+    "bs_kv_pages_work_bytes": (C.c_uint64, [C.POINTER(KvCache), C.c_uint32]),
+    "bs_kv_append_async": (C.c_int, [C.POINTER(KvCache), C.c_uint32, C.c_uint32, C.c_void_p, C.c_void_p, C.c_uint32,
+                                     C.c_uint32, C.c_void_p, C.c_uint64, C.c_void_p, C.c_uint64, C.c_uint32, C.c_void_p]),
+    "bs_kv_attend_async": (C.c_int, [C.POINTER(KvCache), C.POINTER(KvAttendArgs), C.c_void_p, C.c_uint64, C.c_void_p]),
+    "bs_kv_attend_work_bytes": (C.c_uint64, [C.POINTER(KvCache), C.POINTER(KvAttendArgs)]),
     "bs_plan_waves_per_block": (C.c_uint32, [C.c_void_p]),
     "bs_plan_packs": (C.c_uint32, [C.c_void_p, C.c_uint32, C.c_uint32]),
     "bs_verify": (C.c_int, [C.c_void_p, C.c_uint32, C.c_uint32, C.c_void_p, C.c_void_p, C.c_void_p, C.c_uint32,

@@ -545,6 +545,30 @@ class FixedPlan:
         self.gemm_into(y, x, rows, cols, stream=stream)
         return y
 
+    def gemm_lora(self, x: torch.Tensor, rows: int, cols: int, pack, batch, out: torch.Tensor | None = None,
+                  status: bool = True, stream=None) -> torch.Tensor:
+        """Y = X W^T with each token's low-rank adapter added
+        (bs_fixed_gemm_lora_async): x a (tokens, cols) bfloat16 (or int16)
+        tensor of 1..64 tokens, pack a lora.LoraPack, batch a lora.LoraBatch
+        made for these tokens; returns (tokens, rows) float32 (out, if given).
+        The plan keeps the workspace: products of one plan go on one stream."""
+        if x.dtype not in (torch.bfloat16, torch.int16) or x.dim() != 2 or x.shape[1] != cols or not x.is_contiguous():
+            raise ValueError(f"x must be a contiguous (tokens, {cols}) bfloat16 tensor")
+        batch.check_for(pack, x.shape[0])
+        if out is None:
+            out = torch.empty(x.shape[0], rows, dtype=torch.float32, device=self.dev.device)
+        elif out.dtype != torch.float32 or tuple(out.shape) != (x.shape[0], rows) or not out.is_contiguous():
+            raise ValueError(f"out must be a contiguous ({x.shape[0]}, {rows}) float32 tensor")
+        need = int(L.lib().bs_fixed_gemm_lora_work_bytes(rows, cols, x.shape[0], C.byref(pack.c)))
+        if getattr(self, "_lora_work", None) is None or self._lora_work.numel() < need:
+            self._lora_work = torch.empty(max(need, 256), dtype=torch.uint8, device=self.dev.device)
+        rc = L.lib().bs_fixed_gemm_lora_async(C.byref(self.info), self.dev.data_ptr(), rows, cols, x.shape[0],
+                                              x.data_ptr(), out.data_ptr(), self.status.data_ptr() if status else None,
+                                              C.byref(pack.c), batch.dev.data_ptr(), self._lora_work.data_ptr(),
+                                              self._lora_work.numel(), _stream_handle(stream))
+        L.check(rc, "bs_fixed_gemm_lora_async")
+        return out
+
     def block_status(self) -> np.ndarray:
         return self.status[: self.info.n_blocks].cpu().numpy().view(np.uint32)
 

@@ -374,9 +374,11 @@ uint64_t bs_fixed_gemm_work_bytes(uint64_t rows, uint64_t cols, uint32_t batch) 
     return 4ull * batch * rows;
 }
 
-bs_status bs_fixed_gemm_async(const bs_fixed_info* info, const void* d_blob, uint64_t rows, uint64_t cols,
-                              uint32_t batch, const void* d_x, float* d_y, uint32_t* d_status, void* d_work,
-                              uint64_t work_bytes, void* stream) {
+}  // extern "C"
+
+bs_status bs::fixed_gemm(const bs_fixed_info* info, const void* d_blob, uint64_t rows, uint64_t cols, uint32_t batch,
+                         const void* d_x, float* d_y, uint32_t* d_status, void* d_work, uint64_t work_bytes,
+                         bool combine, void* stream) {
     bsd::FixedArgs a;
     const bs_status rc = fixed_args(info, d_blob, a);
     if (rc != BS_OK) return rc;
@@ -417,9 +419,13 @@ bs_status bs_fixed_gemm_async(const bs_fixed_info* info, const void* d_blob, uin
     if (bsk_device_cus(&cus) != 0 || cus <= 0) cus = 256;
     const uint64_t items = split ? 2 * groups32 : (rows + 15) / 16;
     const uint32_t groups = (uint32_t)std::min<uint64_t>(items, 8ull * (uint64_t)cus);
-    const int e = bsk_fixed_gemm(&a, groups, split ? 1 : 0, stream);
+    const int e = bsk_fixed_gemm(&a, groups, split ? 1 : 0, combine ? 1 : 0, stream);
     if (e != 0) { set_error("fixed batched product launch: %s", hipGetErrorString((hipError_t)e)); return BS_E_HIP; }
     return BS_OK;
 }
 
-}  // extern "C"
+extern "C" bs_status bs_fixed_gemm_async(const bs_fixed_info* info, const void* d_blob, uint64_t rows, uint64_t cols,
+                                         uint32_t batch, const void* d_x, float* d_y, uint32_t* d_status, void* d_work,
+                                         uint64_t work_bytes, void* stream) {
+    return fixed_gemm(info, d_blob, rows, cols, batch, d_x, d_y, d_status, d_work, work_bytes, true, stream);
+}

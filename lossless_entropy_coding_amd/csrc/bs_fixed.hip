@@ -519,7 +519,7 @@ extern "C" int bsk_fixed_decode_many(const FixedMany* m, void* stream) {
     return (int)hipGetLastError();
 }
 
-extern "C" int bsk_fixed_gemm(const FixedArgs* args, uint32_t n_groups, int rows32, void* stream) {
+extern "C" int bsk_fixed_gemm(const FixedArgs* args, uint32_t n_groups, int rows32, int combine, void* stream) {
     if (n_groups == 0 || args->rows == 0) return 0;
     const dim3 grid(n_groups), block(64 * kGemmWaves);
     hipStream_t st = (hipStream_t)stream;
@@ -534,7 +534,7 @@ extern "C" int bsk_fixed_gemm(const FixedArgs* args, uint32_t n_groups, int rows
             case 4: hipLaunchKernelGGL((fixed_gemm_kernel<4, 2>), grid, block, 0, st, *args); break;
             default: return (int)hipErrorInvalidValue;
         }
-        if (args->ksplit == 2) {
+        if (args->ksplit == 2 && combine) {
             const uint64_t n = (uint64_t)args->batch * args->rows;
             const uint32_t cgrid = (uint32_t)std::min<uint64_t>((n / 4 + 255) / 256 + 1, 2048);
             hipLaunchKernelGGL(combine_kernel, dim3(cgrid), dim3(256), 0, st, args->gy, args->gpart, n);

@@ -71,8 +71,9 @@ int bsk_fixed_decode_many(const bsd::FixedMany* m, void* stream);
 // the fused product of a fixed-width blob with a batch of vectors: one
 // workgroup of kGemmWaves waves per 16 rows (rows32 0), or per 32 rows and
 // args->ksplit shares of the panels (rows32 1; with 2 shares a second launch
-// adds the workspace's sums into Y); n_groups workgroups, striding
-int bsk_fixed_gemm(const bsd::FixedArgs* args, uint32_t n_groups, int rows32, void* stream);
+// adds the workspace's sums into Y unless combine is 0: then the caller adds
+// them); n_groups workgroups, striding
+int bsk_fixed_gemm(const bsd::FixedArgs* args, uint32_t n_groups, int rows32, int combine, void* stream);
 // the fused product of a fixed-width blob with a vector: n_groups workgroups
 // of kFixWaves waves, each workgroup striding over the row groups
 int bsk_fixed_gemv(const bsd::FixedArgs* args, uint32_t n_groups, void* stream);

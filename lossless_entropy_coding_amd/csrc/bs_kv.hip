@@ -1,0 +1,532 @@
+// bs_kv.hip -- the paged 8-bit key/value cache (gfx950): storing new tokens,
+// and the upkeep of its pages.  Layouts and rules are in bs.h.
+//
+// append: one workgroup per (touched page, head, side).  The scale of a page
+// is a power of two, so x / scale and the change from an old scale to a new
+// one are exact in fp32 and each stored value is rounded once (ties to even),
+// whatever the order of the tokens.
+//
+// Pages: a page is free when its count is 0, and the lowest free page is
+// taken first, so the state after any sequence of calls is one value and no
+// list of free pages has to be kept.  extend and fork allocate in a single
+// workgroup (a scan over the counts, 4096 at a time, that ends with the last
+// page wanted); the copies and the rows of the table are filled by as many
+// workgroups as they need.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "bs_kv_device.h"
+
+using namespace bsd;
+
+namespace {
+
+typedef unsigned int v4u __attribute__((ext_vector_type(4)));
+
+enum : uint32_t {
+    kStPages = 1, kStRow = 2, kStId = 4, kStBusy = 8, kStValue = 16, kStCount = 32
+};
+
+__device__ __forceinline__ void flag(uint32_t* status, uint32_t bit) {
+    if (status) atomicOr(status, bit);
+}
+
+__device__ __forceinline__ float load_x(const void* x, uint64_t i, int f32) {
+    if (f32) return ((const float*)x)[i];
+    return __builtin_bit_cast(float, (uint32_t)((const uint16_t*)x)[i] << 16);
+}
+
+// the least exponent e >= -60 with amax <= Q 2^e: with amax = m 2^x, m in
+// [1, 2), Q = 1.75 2^8 (e4m3) or 127/64 2^6 (int8); amax 0 gives -60
+__device__ __forceinline__ int need_exp(float amax, bool e4m3) {
+    if (!(amax > 0.f)) return -60;
+    const uint32_t b = __builtin_bit_cast(uint32_t, amax);
+    const int x = (int)(b >> 23) - 127;
+    const uint32_t m = b & 0x7FFFFFu;
+    const int e = e4m3 ? x - 8 + (m > 0x600000u) : x - 6 + (m > 0x7E0000u);
+    return e < -60 ? -60 : e;
+}
+
+__device__ __forceinline__ float pow2(int e) { return __builtin_bit_cast(float, (uint32_t)(e + 127) << 23); }
+
+// nearest code (ties to even) of y, |y| within the type's range
+__device__ __forceinline__ uint32_t to_code(float y, bool e4m3) {
+    if (e4m3) {
+        y = fminf(fmaxf(y, -448.f), 448.f);
+        return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(y, y, 0, false) & 0xFFu;
+    }
+    y = fminf(fmaxf(rintf(y), -127.f), 127.f);
+    return (uint32_t)(int)y & 0xFFu;
+}
+
+__device__ __forceinline__ float of_code(uint32_t c, bool e4m3) {
+    if (e4m3) return __builtin_amdgcn_cvt_f32_fp8((int)c, 0);
+    return (float)(int)(int8_t)(c & 0xFFu);
+}
+
+// grid: (pages a sequence can touch, 2 kv_heads, sequences)
+template <bool E4M3>
+__global__ __launch_bounds__(256) void append_kernel(KvAppend a) {
+    const KvView& c = a.c;
+    const uint32_t t = threadIdx.x, seq_i = blockIdx.z, head = blockIdx.y >> 1, side = blockIdx.y & 1u;
+    const int32_t row = a.seqs[seq_i];
+    if (row < 0 || (uint32_t)row >= c.max_seqs) {
+        if (t == 0) flag(c.status, kStId);
+        return;
+    }
+    const int32_t s0 = a.starts ? a.starts[seq_i] : (int32_t)seq_i;
+    const int32_t s1 = a.starts ? a.starts[seq_i + 1] : (int32_t)seq_i + 1;
+    const int32_t len = c.lens[row];
+    if (s0 < 0 || s1 < s0 || (uint32_t)s1 > a.total || s1 - s0 > len || (uint32_t)(s1 - s0) > a.max_new) {
+        if (t == 0) flag(c.status, kStId);
+        return;
+    }
+    if (s1 == s0) return;
+    const uint32_t begin = (uint32_t)(len - (s1 - s0));      // the first new token's place
+    const uint32_t pg = (begin >> c.lp) + blockIdx.x;
+    if ((uint64_t)pg << c.lp >= (uint32_t)len) return;
+    if (pg >= c.max_pages) {
+        if (t == 0) flag(c.status, kStRow);
+        return;
+    }
+    const int32_t pid = c.table[(uint64_t)row * c.max_pages + pg];
+    if (pid < 0 || (uint32_t)pid >= c.n_pages) {
+        if (t == 0) flag(c.status, kStId);
+        return;
+    }
+    const uint32_t lo = max(begin, pg << c.lp) - (pg << c.lp);                 // the page's new slots
+    const uint32_t hi = min((uint32_t)len - (pg << c.lp), c.page);
+    const uint64_t tok0 = (uint64_t)s0 + ((pg << c.lp) + lo - begin);          // the first of them in the input
+    const void* x = side ? a.xv : a.xk;
+    const uint64_t xs = side ? a.v_stride : a.k_stride;
+    const uint32_t nt = hi - lo;
+
+    // the largest finite magnitude
+    float m = 0.f;
+    bool odd = false;
+    for (uint32_t i = t; i < nt * c.dim; i += 256) {
+        const uint32_t tk = i / c.dim, d = i - tk * c.dim;
+        const float v = fabsf(load_x(x, (tok0 + tk) * xs + (uint64_t)head * c.dim + d, a.f32));
+        if (v < __builtin_inff()) m = fmaxf(m, v);
+        else odd = true;
+    }
+    if (odd) flag(c.status, kStValue);
+    __shared__ float red[4];
+#pragma unroll
+    for (int s = 32; s; s >>= 1) m = fmaxf(m, __shfl_xor(m, s));
+    if ((t & 63u) == 0) red[t >> 6] = m;
+    float* sp = c.scale + (((uint64_t)a.layer * c.n_pages + (uint32_t)pid) * c.kv_heads + head) * 2 + side;
+    const float old = lo ? *sp : 0.f;
+    __syncthreads();
+    m = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+    const float now = fmaxf(old, pow2(need_exp(m, E4M3)));
+    const float inv = 1.f / now;                                               // exact: a power of two
+    uint8_t* base = (side ? c.v : c.k) + ((uint64_t)a.layer * c.n_pages + (uint32_t)pid) * c.side_bytes +
+                    (uint64_t)head * c.page * c.wide;
+    if (lo && old < now) {                                                     // older tokens: rounded again
+        const float f = old * inv;
+        for (uint32_t i = t; i < lo * c.wide; i += 256) {
+            const uint32_t d = side ? i / lo : i % c.wide, s = side ? i - d * lo : i / c.wide;
+            uint8_t* p = base + (side ? d * c.page + s : s * c.wide + d);
+            *p = (uint8_t)to_code(of_code(*p, E4M3) * f, E4M3);
+        }
+    }
+    for (uint32_t i = t; i < nt * c.wide; i += 256) {
+        const uint32_t d = side ? i / nt : i % c.wide, s = side ? i - d * nt : i / c.wide;
+        float v = 0.f;
+        if (d < c.dim) {
+            v = load_x(x, (tok0 + s) * xs + (uint64_t)head * c.dim + d, a.f32);
+            v = v != v ? 0.f : v * inv;
+        }
+        base[side ? d * c.page + lo + s : (lo + s) * c.wide + d] = (uint8_t)to_code(v, E4M3);
+    }
+    if (t == 0) *sp = now;
+}
+
+// ------------------------------------------------------------------ pages
+constexpr uint32_t kScan = 1024;             // threads of the allocating workgroup
+
+// exclusive prefix over the workgroup of v, and its total
+__device__ __forceinline__ uint32_t block_prefix(uint32_t v, uint32_t* sums, uint32_t& total) {
+    const uint32_t t = threadIdx.x, lane = t & 63u, w = t >> 6;
+    uint32_t x = v;
+#pragma unroll
+    for (int s = 1; s < 64; s <<= 1) {
+        const uint32_t y = __shfl_up(x, s);
+        if (lane >= (uint32_t)s) x += y;
+    }
+    __syncthreads();
+    if (lane == 63) sums[w] = x;
+    __syncthreads();
+    uint32_t before = 0, all = 0;
+    for (uint32_t i = 0; i < blockDim.x / 64; i++) {
+        const uint32_t y = sums[i];
+        if (i < w) before += y;
+        all += y;
+    }
+    total = all;
+    return before + x - v;
+}
+
+// The lowest `want` free pages, in order, to list; returns how many there
+// are (at most want).
+__device__ uint32_t find_free(const KvView& c, uint32_t want, int32_t* list, uint32_t* sums) {
+    uint32_t got = 0;
+    for (uint32_t base = 0; base < c.n_pages && got < want; base += 4 * kScan) {
+        const uint32_t i = base + 4 * threadIdx.x;
+        uint32_t f[4], n = 0;
+#pragma unroll
+        for (uint32_t k = 0; k < 4; k++) {
+            f[k] = i + k < c.n_pages && c.refs[i + k] == 0;
+            n += f[k];
+        }
+        uint32_t total;
+        uint32_t at = got + block_prefix(n, sums, total);
+#pragma unroll
+        for (uint32_t k = 0; k < 4; k++)
+            if (f[k]) {
+                if (at < want) list[at] = (int32_t)(i + k);
+                at++;
+            }
+        got += total;
+    }
+    return min(got, want);
+}
+
+__device__ __forceinline__ uint32_t pages_of(const KvView& c, uint32_t tokens) { return (tokens + c.page - 1) >> c.lp; }
+
+// work: [0] 1 if the call goes through, [1..] the free pages found, then for
+// each row the first of them that is its own, then its length before the
+// call (read once: a row that is named twice cannot take a page that was not
+// counted)
+// extend: rows a[i] grow by b[i] tokens
+// fork: children b[i] of rows a[i]
+template <bool FORK>
+__global__ __launch_bounds__(kScan) void alloc_kernel(KvPages p) {
+    const KvView& c = p.c;
+    __shared__ uint32_t sums[kScan / 64];
+    __shared__ uint32_t bad;
+    const uint32_t t = threadIdx.x;
+    if (t == 0) bad = 0;
+    __syncthreads();
+    int32_t* list = p.work + 1;
+    int32_t* offs = list + c.n_pages;
+    int32_t* lens = offs + p.n;
+    uint32_t total = 0;
+    for (uint32_t base = 0; base < p.n; base += kScan) {
+        const uint32_t i = base + t;
+        uint32_t need = 0, err = 0;
+        int32_t had = 0;
+        if (i < p.n) {
+            const int32_t r = p.a[i], x = p.b[i];
+            if (r < 0 || (uint32_t)r >= c.max_seqs) err = kStId;
+            else if (FORK) {
+                if (x < 0 || (uint32_t)x >= c.max_seqs || x == r) err = kStId;
+                else if (c.lens[x] != 0) err = kStBusy;
+                else {
+                    had = max(c.lens[r], 0);
+                    if (pages_of(c, (uint32_t)had) > c.max_pages) err = kStRow;
+                    else need = ((uint32_t)had & (c.page - 1)) != 0;
+                }
+            } else {
+                had = max(c.lens[r], 0);
+                const int64_t to = (int64_t)had + x;
+                if (x < 0) err = kStId;
+                else if (to > (int64_t)c.max_pages << c.lp) err = kStRow;
+                else need = pages_of(c, (uint32_t)to) - pages_of(c, (uint32_t)had);
+            }
+        }
+        if (err) atomicOr(&bad, err);
+        uint32_t sum;
+        const uint32_t at = block_prefix(need, sums, sum);
+        if (i < p.n) {
+            offs[i] = (int32_t)(total + at);
+            lens[i] = had;
+        }
+        total += sum;
+        if (total > c.n_pages) {               // the same in every thread; keeps the sum from wrapping
+            if (t == 0) atomicOr(&bad, (uint32_t)kStPages);
+            break;
+        }
+    }
+    __syncthreads();
+    const bool early = bad != 0;
+    const uint32_t got = early ? 0 : find_free(c, total, list, sums);
+    __syncthreads();
+    const bool ok = !early && got == total;
+    if (t == 0) {
+        p.work[0] = ok;
+        if (!ok) flag(c.status, early ? bad : (uint32_t)kStPages);
+    }
+    if (!ok) return;
+    if (FORK) {
+        for (uint32_t i = t; i < p.n; i += kScan) {
+            const uint32_t dst = (uint32_t)p.b[i], len = (uint32_t)lens[i];
+            if (len & (c.page - 1)) {
+                const int32_t pg = list[offs[i]];
+                c.refs[pg] = 1;
+                c.table[(uint64_t)dst * c.max_pages + (len >> c.lp)] = pg;
+            }
+            c.lens[dst] = (int32_t)len;
+        }
+    } else {
+        // page j of the list goes to the last row whose first page is not after j
+        for (uint32_t j = t; j < total; j += kScan) {
+            uint32_t lo = 0, hi = p.n;
+            while (hi - lo > 1) {
+                const uint32_t mid = (lo + hi) / 2;
+                if ((uint32_t)offs[mid] <= j) lo = mid;
+                else hi = mid;
+            }
+            const uint32_t r = (uint32_t)p.a[lo];
+            const uint32_t col = pages_of(c, (uint32_t)lens[lo]) + (j - (uint32_t)offs[lo]);
+            c.table[(uint64_t)r * c.max_pages + col] = list[j];
+            c.refs[list[j]] = 1;
+        }
+        __syncthreads();
+        for (uint32_t i = t; i < p.n; i += kScan) {
+            c.lens[p.a[i]] = lens[i] + p.b[i];
+        }
+    }
+}
+
+// copies part of one page (keys, values, scales) of one layer
+__device__ __forceinline__ void copy_page(const KvView& c, uint64_t layer, uint32_t from, uint32_t to, uint32_t part,
+                                          uint32_t parts) {
+    const uint64_t n16 = c.side_bytes / 16;
+    const v4u* ks = (const v4u*)(c.k + (layer * c.n_pages + from) * c.side_bytes);
+    const v4u* vs = (const v4u*)(c.v + (layer * c.n_pages + from) * c.side_bytes);
+    v4u* kd = (v4u*)(c.k + (layer * c.n_pages + to) * c.side_bytes);
+    v4u* vd = (v4u*)(c.v + (layer * c.n_pages + to) * c.side_bytes);
+    const uint64_t step = (uint64_t)parts * 256;
+    for (uint64_t i = (uint64_t)part * 256 + threadIdx.x; i < n16; i += step) {
+        const v4u x = ks[i], y = vs[i];
+        kd[i] = x;
+        vd[i] = y;
+    }
+    if (part == 0)
+        for (uint32_t i = threadIdx.x; i < 2 * c.kv_heads; i += 256)
+            c.scale[(layer * c.n_pages + to) * c.kv_heads * 2 + i] = c.scale[(layer * c.n_pages + from) * c.kv_heads * 2 + i];
+}
+
+// fork's second half: x < parts copies of the last page per layer, then the
+// rows of the table.  grid: (layers * parts + 1, pairs)
+__global__ __launch_bounds__(256) void fork_fill_kernel(KvPages p, uint32_t parts) {
+    const KvView& c = p.c;
+    if (!p.work[0]) return;
+    const uint32_t i = blockIdx.y;
+    const uint32_t src = (uint32_t)p.a[i], dst = (uint32_t)p.b[i];
+    const uint32_t len = (uint32_t)c.lens[dst], whole = len >> c.lp;
+    const int32_t* from = c.table + (uint64_t)src * c.max_pages;
+    int32_t* to = c.table + (uint64_t)dst * c.max_pages;
+    if (blockIdx.x == c.layers * parts) {
+        for (uint32_t j = threadIdx.x; j < whole; j += 256) {
+            const int32_t pid = from[j];
+            to[j] = pid;
+            if (pid >= 0 && (uint32_t)pid < c.n_pages) atomicAdd(c.refs + pid, 1);
+            else flag(c.status, kStId);
+        }
+        return;
+    }
+    if ((len & (c.page - 1)) == 0) return;
+    const int32_t s = from[whole], d = to[whole];
+    if (s < 0 || (uint32_t)s >= c.n_pages || d < 0 || (uint32_t)d >= c.n_pages) {
+        if (threadIdx.x == 0) flag(c.status, kStId);
+        return;
+    }
+    copy_page(c, blockIdx.x / parts, (uint32_t)s, (uint32_t)d, blockIdx.x % parts, parts);
+}
+
+// grid: rows
+__global__ __launch_bounds__(256) void free_kernel(KvPages p) {
+    const KvView& c = p.c;
+    __shared__ int32_t len;
+    const int32_t r = p.a[blockIdx.x];
+    if (r < 0 || (uint32_t)r >= c.max_seqs) {
+        if (threadIdx.x == 0) flag(c.status, kStId);
+        return;
+    }
+    if (threadIdx.x == 0) len = atomicExch(c.lens + r, 0);   // a row named twice is freed once
+    __syncthreads();
+    const uint32_t n = min(pages_of(c, (uint32_t)max(len, 0)), c.max_pages);
+    for (uint32_t j = threadIdx.x; j < n; j += 256) {
+        const int32_t pid = c.table[(uint64_t)r * c.max_pages + j];
+        if (pid < 0 || (uint32_t)pid >= c.n_pages) {
+            flag(c.status, kStId);
+        } else if (atomicSub(c.refs + pid, 1) <= 0) {
+            atomicAdd(c.refs + pid, 1);
+            flag(c.status, kStCount);
+        }
+    }
+}
+
+// grid: (layers * parts, pages)
+__global__ __launch_bounds__(256) void copy_kernel(KvPages p, uint32_t parts) {
+    const KvView& c = p.c;
+    const int32_t s = p.a[blockIdx.y], d = p.b[blockIdx.y];
+    if (s < 0 || (uint32_t)s >= c.n_pages || d < 0 || (uint32_t)d >= c.n_pages) {
+        if (threadIdx.x == 0) flag(c.status, kStId);
+        return;
+    }
+    if (s != d) copy_page(c, blockIdx.x / parts, (uint32_t)s, (uint32_t)d, blockIdx.x % parts, parts);
+}
+
+// ---------------------------------------------------------------- compact
+// work: [0] pages in use, [1] pages to move, [2] pages in use below [0],
+// [4 ..] block counts, then the list of movers and the list of holes
+constexpr uint32_t kCompactBlock = 4096;
+
+__device__ __forceinline__ uint32_t live_count(const KvView& c, uint32_t lo, uint32_t hi, uint32_t* sums) {
+    uint32_t n = 0;
+    for (uint32_t i = lo + threadIdx.x; i < hi; i += 256) n += c.refs[i] > 0;
+    uint32_t total;
+    block_prefix(n, sums, total);
+    return total;
+}
+
+__global__ __launch_bounds__(256) void compact_count_kernel(KvPages p) {
+    __shared__ uint32_t sums[4];
+    const uint32_t lo = blockIdx.x * kCompactBlock, hi = min(lo + kCompactBlock, p.c.n_pages);
+    const uint32_t n = live_count(p.c, lo, hi, sums);
+    if (threadIdx.x == 0) p.work[4 + blockIdx.x] = (int32_t)n;
+}
+
+__global__ __launch_bounds__(256) void compact_rank_kernel(KvPages p, uint32_t blocks) {
+    const KvView& c = p.c;
+    __shared__ uint32_t sums[4];
+    uint32_t n = 0, before = 0;
+    for (uint32_t b = threadIdx.x; b < blocks; b += 256) {
+        const uint32_t x = (uint32_t)p.work[4 + b];
+        n += x;
+        if (b < blockIdx.x) before += x;
+    }
+    uint32_t live, mine, low = 0;
+    block_prefix(n, sums, live);
+    block_prefix(before, sums, mine);
+    // pages in use below `live`
+    const uint32_t bl = live / kCompactBlock;
+    for (uint32_t b = threadIdx.x; b < min(bl, blocks); b += 256) low += (uint32_t)p.work[4 + b];
+    uint32_t below;
+    block_prefix(low, sums, below);
+    below += live_count(c, min(bl * kCompactBlock, live), live, sums);
+    int32_t* movers = p.work + 4 + blocks;
+    int32_t* holes = movers + c.n_pages;
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+        p.work[0] = (int32_t)live;
+        p.work[1] = (int32_t)(live - below);
+    }
+    uint32_t seen = mine;                    // pages in use before this step
+    const uint32_t lo = blockIdx.x * kCompactBlock, hi = min(lo + kCompactBlock, c.n_pages);
+    for (uint32_t base = lo; base < hi; base += 256) {
+        const uint32_t i = base + threadIdx.x;
+        const int32_t r = i < hi ? c.refs[i] : 0;
+        uint32_t total;
+        const uint32_t at = seen + block_prefix(r > 0, sums, total);
+        if (i < hi) {
+            if (i >= live) p.refs_out[i] = 0;
+            if (r > 0 && i >= live) movers[at - below] = (int32_t)i;
+            if (r > 0 && i < live) p.refs_out[i] = r;
+            if (r <= 0 && i < live) holes[i - at] = (int32_t)i;
+        }
+        seen += total;
+    }
+}
+
+// the place of page i after the move: movers is ascending
+__device__ __forceinline__ int32_t new_place(int32_t i, uint32_t live, uint32_t moves, const int32_t* movers,
+                                             const int32_t* holes) {
+    if ((uint32_t)i < live) return i;
+    uint32_t lo = 0, hi = moves;
+    while (lo < hi) {
+        const uint32_t mid = (lo + hi) / 2;
+        if (movers[mid] < i) lo = mid + 1;
+        else hi = mid;
+    }
+    return lo < moves && movers[lo] == i ? holes[lo] : -1;
+}
+
+// grid: (layers * parts + 1, max moves at most): the copies and the movers' counts
+__global__ __launch_bounds__(256) void compact_move_kernel(KvPages p, uint32_t blocks, uint32_t parts) {
+    const KvView& c = p.c;
+    const uint32_t moves = (uint32_t)p.work[1];
+    const int32_t* movers = p.work + 4 + blocks;
+    const int32_t* holes = movers + c.n_pages;
+    for (uint32_t m = blockIdx.y; m < moves; m += gridDim.y) {
+        const uint32_t s = (uint32_t)movers[m], d = (uint32_t)holes[m];
+        if (blockIdx.x == c.layers * parts) {
+            if (threadIdx.x == 0) p.refs_out[d] = c.refs[s];
+        } else {
+            copy_page(c, blockIdx.x / parts, s, d, blockIdx.x % parts, parts);
+        }
+    }
+}
+
+// grid: rows
+__global__ __launch_bounds__(256) void compact_table_kernel(KvPages p, uint32_t blocks) {
+    const KvView& c = p.c;
+    const uint32_t live = (uint32_t)p.work[0], moves = (uint32_t)p.work[1];
+    const int32_t* movers = p.work + 4 + blocks;
+    const int32_t* holes = movers + c.n_pages;
+    const uint64_t at = (uint64_t)blockIdx.x * c.max_pages;
+    const uint32_t n = min(pages_of(c, (uint32_t)max(c.lens[blockIdx.x], 0)), c.max_pages);
+    for (uint32_t j = threadIdx.x; j < c.max_pages; j += 256) {
+        int32_t to = -1;
+        if (j < n) {
+            const int32_t pid = c.table[at + j];
+            if (pid >= 0 && (uint32_t)pid < c.n_pages) to = new_place(pid, live, moves, movers, holes);
+            if (to < 0) flag(c.status, kStId);
+        }
+        p.table_out[at + j] = to;
+    }
+}
+
+// workgroups per page and layer: 16 B per thread and side, at most 8 of them
+uint32_t copy_parts(const KvView& c) {
+    return (uint32_t)std::max<uint64_t>(1, std::min<uint64_t>(8, c.side_bytes / 16 / 256));
+}
+
+}  // namespace
+
+extern "C" int bsk_kv_append(const KvAppend* a, void* stream) {
+    const uint32_t touch = (a->max_new + 2 * a->c.page - 2) >> a->c.lp;
+    const dim3 grid(touch, 2 * a->c.kv_heads, a->n_seqs);
+    if (a->c.type == 1) hipLaunchKernelGGL(append_kernel<true>, grid, dim3(256), 0, (hipStream_t)stream, *a);
+    else hipLaunchKernelGGL(append_kernel<false>, grid, dim3(256), 0, (hipStream_t)stream, *a);
+    return (int)hipGetLastError();
+}
+
+extern "C" int bsk_kv_extend(const KvPages* p, void* stream) {
+    hipLaunchKernelGGL(alloc_kernel<false>, dim3(1), dim3(kScan), 0, (hipStream_t)stream, *p);
+    return (int)hipGetLastError();
+}
+
+extern "C" int bsk_kv_fork(const KvPages* p, void* stream) {
+    hipLaunchKernelGGL(alloc_kernel<true>, dim3(1), dim3(kScan), 0, (hipStream_t)stream, *p);
+    const uint32_t parts = copy_parts(p->c);
+    hipLaunchKernelGGL(fork_fill_kernel, dim3(p->c.layers * parts + 1, p->n), dim3(256), 0, (hipStream_t)stream, *p, parts);
+    return (int)hipGetLastError();
+}
+
+extern "C" int bsk_kv_free(const KvPages* p, void* stream) {
+    hipLaunchKernelGGL(free_kernel, dim3(p->n), dim3(256), 0, (hipStream_t)stream, *p);
+    return (int)hipGetLastError();
+}
+
+extern "C" int bsk_kv_copy(const KvPages* p, void* stream) {
+    const uint32_t parts = copy_parts(p->c);
+    hipLaunchKernelGGL(copy_kernel, dim3(p->c.layers * parts, p->n), dim3(256), 0, (hipStream_t)stream, *p, parts);
+    return (int)hipGetLastError();
+}
+
+extern "C" int bsk_kv_compact(const KvPages* p, void* stream) {
+    const uint32_t blocks = (p->c.n_pages + kCompactBlock - 1) / kCompactBlock, parts = copy_parts(p->c);
+    hipStream_t st = (hipStream_t)stream;
+    hipLaunchKernelGGL(compact_count_kernel, dim3(blocks), dim3(256), 0, st, *p);
+    hipLaunchKernelGGL(compact_rank_kernel, dim3(blocks), dim3(256), 0, st, *p, blocks);
+    const uint32_t most = std::min<uint32_t>((p->c.n_pages + 1) / 2, 1024);
+    hipLaunchKernelGGL(compact_move_kernel, dim3(p->c.layers * parts + 1, most), dim3(256), 0, st, *p, blocks, parts);
+    hipLaunchKernelGGL(compact_table_kernel, dim3(p->c.max_seqs), dim3(256), 0, st, *p, blocks);
+    return (int)hipGetLastError();
+}

@@ -1,0 +1,414 @@
+// bs_kv_attend.hip -- attention over the paged 8-bit key/value cache (gfx950).
+//
+// Rows are the queries that share a key head: row r of a sequence is token
+// r / group, head r % group of the key head's group.  A wave takes 64 tokens
+// of one sequence and key head at a time against 16 rows:
+//
+//   S^T = K Q^T     v_mfma_f32_16x16x32_bf16, A = 16 tokens x 32 channels,
+//                   B = 32 channels x 16 rows.  An 8-bit code is exact in
+//                   BF16 (e4m3 has 4 significant bits, int8 7), so the
+//                   products are exact and summed in fp32; the page's scale
+//                   multiplies the sum.
+//   O^T += V^T P^T  A = 16 channels x 32 tokens, B = 32 tokens x 16 rows.
+//                   P (times the scale of V's page, a power of two) is
+//                   rounded to BF16, the type of the result: the rounding
+//                   errors of the tokens are independent, so the sum's is
+//                   below the result's own.  The sum of P is kept in fp32
+//                   from the unrounded values.
+//
+// The tokens of a 64-token tile are dealt to the four 16-token steps of S^T
+// such that lane group g (lanes 16 g ..) ends up with tokens 16 g .. 16 g +
+// 15 of its row, four of each step.  These are the tokens that the lane has
+// to hold for the second product, in the order in which it reads V (kept
+// with a channel's tokens side by side), so P goes from one product to the
+// other without leaving the lane, and one lane's tokens are always of one
+// page.  Keys and values are read 16 B per lane.
+//
+// The running maximum and sum of a row's softmax are held per row (a lane's
+// column), the result is scaled when the maximum grows.  The waves of a
+// workgroup take the tiles in turn and are joined in wave order; where there
+// are too few rows to fill the GPU, a row's tiles are also split over
+// workgroups, and a second kernel joins their results in order.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "bs_kv_device.h"
+
+using namespace bsd;
+
+namespace {
+
+typedef unsigned int v4u __attribute__((ext_vector_type(4)));
+typedef unsigned int v2u __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+    const bf16x2 r = {(__bf16)a, (__bf16)b};
+    return __builtin_bit_cast(uint32_t, r);
+}
+
+// four 8-bit codes to four BF16 (exact)
+template <bool E4M3>
+__device__ __forceinline__ v2u widen4(uint32_t c) {
+    if (E4M3) {
+        const bf16x2 lo = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c, 1.f, false);
+        const bf16x2 hi = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c, 1.f, true);
+        return v2u{__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi)};
+    }
+    const float a = (float)(int8_t)c, b = (float)(int8_t)(c >> 8), d = (float)(int8_t)(c >> 16), e = (float)(int8_t)(c >> 24);
+    return v2u{pack_bf16(a, b), pack_bf16(d, e)};
+}
+
+template <bool E4M3>
+__device__ __forceinline__ bf16x8 widen8(uint32_t a, uint32_t b) {
+    const v2u x = widen4<E4M3>(a), y = widen4<E4M3>(b);
+    return __builtin_bit_cast(bf16x8, v4u{x.x, x.y, y.x, y.y});
+}
+
+// x of this lane and of the lane 32 (16) away, in either order: the swap
+// exchanges halves (rows) between two copies.  (The elements go through
+// variables of their own: a bit cast of a vector's element reads element 0.)
+struct Pair {
+    float a, b;
+};
+
+__device__ __forceinline__ Pair swap32(float x) {
+    const uint32_t u = __builtin_bit_cast(uint32_t, x);
+    auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    const uint32_t a = r[0], b = r[1];
+    return Pair{__builtin_bit_cast(float, a), __builtin_bit_cast(float, b)};
+}
+
+__device__ __forceinline__ Pair swap16(float x) {
+    const uint32_t u = __builtin_bit_cast(uint32_t, x);
+    auto r = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+    const uint32_t a = r[0], b = r[1];
+    return Pair{__builtin_bit_cast(float, a), __builtin_bit_cast(float, b)};
+}
+
+// maximum and sum over the four lane groups (lanes l, l + 16, l + 32, l + 48)
+__device__ __forceinline__ float max_groups(float x) {
+    Pair p = swap32(x);
+    p = swap16(fmaxf(p.a, p.b));
+    return fmaxf(p.a, p.b);
+}
+
+__device__ __forceinline__ float sum_groups(float x) {
+    Pair p = swap32(x);
+    p = swap16(p.a + p.b);
+    return p.a + p.b;
+}
+
+// One sequence's part of a call, checked.
+struct Seq {
+    int32_t row, s0, count, len;    // cache row, first query token, query tokens, length
+    bool ok;
+};
+
+__device__ __forceinline__ Seq get_seq(const KvAttend& a, uint32_t i) {
+    Seq s;
+    s.row = a.seqs[i];
+    s.s0 = a.starts ? a.starts[i] : (int32_t)i;
+    const int32_t s1 = a.starts ? a.starts[i + 1] : (int32_t)i + 1;
+    s.count = s1 - s.s0;
+    s.ok = s.s0 >= 0 && s1 >= s.s0 && (uint32_t)s1 <= a.total && (uint32_t)s.count <= a.max_new;
+    if (!s.ok) s.count = 0;
+    s.len = 0;
+    if (s.row >= 0 && (uint32_t)s.row < a.c.max_seqs)
+        s.len = (int32_t)min((uint64_t)(uint32_t)max(a.c.lens[s.row], 0), (uint64_t)a.c.max_pages << a.c.lp);
+    else s.ok = false;
+    return s;
+}
+
+// the tiles that rows at places lo .. hi (lo may be negative) of a sequence see:
+// tiles 0 .. ns - 1 and t0 .. t1 - 1
+struct Tiles {
+    uint32_t ns, t0, n;             // n: how many in all
+    __device__ __forceinline__ uint32_t at(uint32_t i) const { return i < ns ? i : t0 + (i - ns); }
+};
+
+__device__ __forceinline__ Tiles get_tiles(const KvAttend& a, int32_t lo, int32_t hi) {
+    Tiles t{0, 0, 0};
+    if (hi < 0) return t;
+    const uint32_t t1 = (uint32_t)hi / kKvTile + 1;
+    if (a.window) {
+        const int64_t first = max((int64_t)max(lo, 0) - (int64_t)a.window + 1, (int64_t)0);
+        t.t0 = (uint32_t)first / kKvTile;
+        t.ns = min((uint32_t)(((uint64_t)a.sinks + kKvTile - 1) / kKvTile), t.t0);
+    }
+    t.n = t.ns + (t1 - t.t0);
+    return t;
+}
+
+// grid: (sequences * row tiles, key heads, splits); NW waves.  The bound of
+// two waves per SIMD keeps the kernel within 256 registers and so the
+// products' accumulators out of the AGPRs: with them there, the compiler here
+// reads a product's later elements at a block's join without the wait that
+// it puts before the first, and they come back stale.
+template <int DW, bool E4M3, int NW>
+__global__ __launch_bounds__(64 * NW, 2) void attend_kernel(KvAttend a, uint32_t row_tiles) {
+    const KvView& c = a.c;
+    constexpr uint32_t D = 64 * DW;
+    __shared__ float ml[NW][2][16];
+    __shared__ __attribute__((aligned(16))) float os[NW > 1 ? NW / 2 : 1][16][D + 4];
+
+    const uint32_t t = threadIdx.x, lane = t & 63u, m = lane & 15u, g = lane >> 4;
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(t >> 6);
+    const uint32_t split = blockIdx.z, head = blockIdx.y;
+    const uint32_t seq_i = blockIdx.x / row_tiles, rt = blockIdx.x % row_tiles;
+    const Seq sq = get_seq(a, seq_i);
+    if (!sq.ok && t == 0 && split == 0) {
+        if (c.status) atomicOr(c.status, 4u);
+    }
+    const uint32_t rows = (uint32_t)sq.count * a.group;
+    if (16 * rt >= rows) return;
+    const int32_t base = sq.len - sq.count;                         // the first query's place
+    const uint32_t r_last = min(16 * rt + 15, rows - 1);
+    const int32_t lo = base + (int32_t)(16 * rt / a.group), hi = base + (int32_t)(r_last / a.group);
+    const Tiles tl = get_tiles(a, lo, hi);
+    const uint32_t i0 = split * a.chunk;
+    if (split > 0 && i0 >= tl.n) return;
+    const uint32_t i1 = a.splits > 1 ? min(tl.n, i0 + a.chunk) : tl.n;
+
+    // this lane's row
+    const uint32_t r = min(16 * rt + m, rows - 1);
+    const uint32_t tok = (uint32_t)sq.s0 + r / a.group, qh = head * a.group + r % a.group;
+    const int32_t pos = base + (int32_t)(r / a.group);
+
+    // Q: for channels 64 x + 16 g + 8 y ..: 8 values
+    bf16x8 q[DW][2];
+    {
+        const uint16_t* qp = a.q + (uint64_t)tok * a.q_stride + (uint64_t)qh * c.dim;
+#pragma unroll
+        for (uint32_t x = 0; x < DW; x++)
+#pragma unroll
+            for (uint32_t y = 0; y < 2; y++) {
+                const uint32_t d = 64 * x + 16 * g + 8 * y;
+                if (a.aligned && d + 8 <= c.dim) {
+                    q[x][y] = *(const bf16x8*)(qp + d);
+                } else {
+                    uint32_t w[4];
+#pragma unroll
+                    for (uint32_t e = 0; e < 4; e++) {
+                        const uint32_t u = d + 2 * e < c.dim ? qp[d + 2 * e] : 0u, v = d + 2 * e + 1 < c.dim ? qp[d + 2 * e + 1] : 0u;
+                        w[e] = u | v << 16;
+                    }
+                    q[x][y] = __builtin_bit_cast(bf16x8, v4u{w[0], w[1], w[2], w[3]});
+                }
+            }
+    }
+    const float sc = a.softcap > 0.f ? a.qscale : a.qscale * kLog2e;
+    const float cap_in = a.softcap > 0.f ? 2.f * kLog2e / a.softcap : 0.f, cap_out = a.softcap * kLog2e;
+
+    f32x4 o[4 * DW];
+#pragma unroll
+    for (int d = 0; d < 4 * DW; d++) o[d] = f32x4{0.f, 0.f, 0.f, 0.f};
+    float mx = -__builtin_inff(), sum = 0.f;
+    const int32_t* trow = c.table + (uint64_t)(uint32_t)max(sq.row, 0) * c.max_pages;
+    const uint64_t hoff = (uint64_t)head * c.page * c.wide;
+    const uint32_t end = (uint32_t)(hi + 1);                        // tokens past it are seen by no row
+    uint32_t bad = 0;
+
+    for (uint32_t i = i0 + wave; i < i1; i += NW) {
+        const uint32_t tile0 = tl.at(i) * kKvTile;
+        // the lane's 16-token chunks: its keys' (by step row m) and its own tokens' (by group)
+        const uint32_t ck = tile0 + 16 * (m >> 2), cv = tile0 + 16 * g;
+        int32_t pk = ck < end ? trow[ck >> c.lp] : -1, pv = cv < end ? trow[cv >> c.lp] : -1;
+        const bool okk = (uint32_t)pk < c.n_pages, okv = (uint32_t)pv < c.n_pages;
+        if (cv < end && !okv) bad = 1;
+        const uint32_t ipk = okk ? (uint32_t)pk : 0u, ipv = okv ? (uint32_t)pv : 0u;
+        const uint8_t* kp = a.k + (uint64_t)ipk * c.side_bytes + hoff + (uint64_t)((ck + (m & 3u)) & (c.page - 1)) * D + 16 * g;
+        const uint8_t* vp = a.v + (uint64_t)ipv * c.side_bytes + hoff + (uint64_t)m * c.page + (cv & (c.page - 1));
+        v4u kr[4][DW], vr[4 * DW];
+#pragma unroll
+        for (uint32_t h = 0; h < 4; h++)
+#pragma unroll
+            for (uint32_t x = 0; x < DW; x++) kr[h][x] = *(const v4u*)(kp + 4 * h * D + 64 * x);
+#pragma unroll
+        for (uint32_t d = 0; d < 4 * DW; d++) vr[d] = *(const v4u*)(vp + (uint64_t)(16 * d) * c.page);
+        const float* sp = a.scale + ((uint64_t)ipv * c.kv_heads + head) * 2;
+        const float ks = sp[0] * sc, vs = okv ? sp[1] : 0.f;
+
+        f32x4 s[4];
+#pragma unroll
+        for (uint32_t h = 0; h < 4; h++) {
+            s[h] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (uint32_t x = 0; x < DW; x++) {
+                s[h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen8<E4M3>(kr[h][x].x, kr[h][x].y), q[x][0], s[h], 0, 0, 0);
+                s[h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen8<E4M3>(kr[h][x].z, kr[h][x].w), q[x][1], s[h], 0, 0, 0);
+            }
+        }
+        // step h's element e is token cv + 4 h + e
+        float p[16];
+        float top = -__builtin_inff();
+#pragma unroll
+        for (uint32_t h = 0; h < 4; h++)
+#pragma unroll
+            for (uint32_t e = 0; e < 4; e++) {
+                float x = s[h][e] * ks;
+                if (a.softcap > 0.f) x = cap_out * (1.f - 2.f * __builtin_amdgcn_rcpf(exp2_fast(x * cap_in) + 1.f));
+                const int32_t tk = (int32_t)(cv + 4 * h + e);
+                const bool seen = okv && tk <= pos &&
+                                  (a.window == 0 || (int64_t)tk > (int64_t)pos - (int64_t)a.window || (uint32_t)tk < a.sinks);
+                x = seen ? x : -__builtin_inff();
+                p[4 * h + e] = x;
+                top = fmaxf(top, x);
+            }
+        // what no row sees may hold anything: its values count as 0
+        if (cv + 16 > end || !okv) {
+            const int32_t left = okv ? (int32_t)(end - cv) : 0;      // tokens of the chunk that are kept
+#pragma unroll
+            for (int d = 0; d < 4 * DW; d++)
+#pragma unroll
+                for (int w = 0; w < 4; w++) {
+                    const int32_t nb = left - 4 * w;
+                    const uint32_t mask = nb >= 4 ? ~0u : nb <= 0 ? 0u : (1u << (8 * nb)) - 1u;
+                    vr[d][w] &= mask;
+                }
+        }
+        top = fmaxf(max_groups(top), mx);
+        const float sub = top == -__builtin_inff() ? 0.f : top;
+        const float alpha = exp2_fast(mx - sub);
+        mx = top;
+        float part = 0.f;
+#pragma unroll
+        for (int e = 0; e < 16; e++) {
+            p[e] = exp2_fast(p[e] - sub);
+            part += p[e];
+        }
+        sum = sum * alpha + part;
+        bf16x8 pb[2];
+#pragma unroll
+        for (int y = 0; y < 2; y++)
+            pb[y] = __builtin_bit_cast(bf16x8, v4u{pack_bf16(p[8 * y] * vs, p[8 * y + 1] * vs), pack_bf16(p[8 * y + 2] * vs, p[8 * y + 3] * vs),
+                                                   pack_bf16(p[8 * y + 4] * vs, p[8 * y + 5] * vs), pack_bf16(p[8 * y + 6] * vs, p[8 * y + 7] * vs)});
+#pragma unroll
+        for (int d = 0; d < 4 * DW; d++) {
+            o[d] *= alpha;
+            o[d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen8<E4M3>(vr[d].x, vr[d].y), pb[0], o[d], 0, 0, 0);
+            o[d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen8<E4M3>(vr[d].z, vr[d].w), pb[1], o[d], 0, 0, 0);
+        }
+    }
+    if (bad && c.status) atomicOr(c.status, 4u);
+
+    // join the waves: maxima and sums, then the results in wave order
+    sum = sum_groups(sum);
+    if (g == 0) {
+        ml[wave][0][m] = mx;
+        ml[wave][1][m] = sum;
+    }
+    __syncthreads();
+    float top = -__builtin_inff(), total = 0.f;
+#pragma unroll
+    for (int w = 0; w < NW; w++) top = fmaxf(top, ml[w][0][m]);
+    const float sub = top == -__builtin_inff() ? 0.f : top;
+#pragma unroll
+    for (int w = 0; w < NW; w++) total += ml[w][1][m] * exp2_fast(ml[w][0][m] - sub);
+    const float f = exp2_fast(mx - sub);
+#pragma unroll
+    for (int d = 0; d < 4 * DW; d++) o[d] *= f;
+#pragma unroll
+    for (int half = NW / 2; half >= 1; half /= 2) {
+        __syncthreads();
+        if ((int)wave >= half && (int)wave < 2 * half) {
+#pragma unroll
+            for (int d = 0; d < 4 * DW; d++) *(f32x4*)&os[wave - half][m][16 * d + 4 * g] = o[d];
+        }
+        __syncthreads();
+        if ((int)wave < half) {
+#pragma unroll
+            for (int d = 0; d < 4 * DW; d++) o[d] += *(f32x4*)&os[wave][m][16 * d + 4 * g];
+        }
+    }
+    if (wave != 0 || 16 * rt + m >= rows) return;
+    if (a.splits > 1) {
+        float* pp = a.part + (((uint64_t)tok * a.heads + qh) * a.splits + split) * (D + 2);
+        for (int d = 0; d < 4 * DW; d++)
+#pragma unroll
+            for (int e = 0; e < 4; e++) pp[16 * d + 4 * g + e] = o[d][e];
+        if (g == 0) {
+            pp[D] = top;
+            pp[D + 1] = total;
+        }
+        return;
+    }
+    const float inv = total > 0.f ? 1.f / total : 0.f;
+    uint16_t* op = a.out + (uint64_t)tok * a.out_stride + (uint64_t)qh * c.dim;
+#pragma unroll
+    for (int d = 0; d < 4 * DW; d++)
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+            const uint32_t ch = 16 * d + 4 * g + e;
+            if (ch < c.dim) op[ch] = __builtin_bit_cast(uint16_t, (__bf16)(o[d][e] * inv));
+        }
+    if (a.lse && g == 0) a.lse[(uint64_t)tok * a.heads + qh] = total > 0.f ? (top + __builtin_amdgcn_logf(total)) * kLn2 : -__builtin_inff();
+}
+
+// Joins the splits of one row in order.  grid: (sequences * max_new, heads);
+// 64 threads
+template <int DW>
+__global__ __launch_bounds__(64) void join_kernel(KvAttend a) {
+    constexpr uint32_t D = 64 * DW;
+    const uint32_t seq_i = blockIdx.x / a.max_new, j = blockIdx.x % a.max_new, qh = blockIdx.y, lane = threadIdx.x;
+    const Seq sq = get_seq(a, seq_i);
+    if (j >= (uint32_t)sq.count) return;
+    // the splits that the row's tile of 16 rows has
+    const uint32_t rt = (j * a.group + qh % a.group) / 16;
+    const int32_t base = sq.len - sq.count;
+    const uint32_t r_last = min(16 * rt + 15, (uint32_t)sq.count * a.group - 1);
+    const Tiles tl = get_tiles(a, base + (int32_t)(16 * rt / a.group), base + (int32_t)(r_last / a.group));
+    const uint32_t n = max(1u, (tl.n + a.chunk - 1) / a.chunk);
+    const uint32_t tok = (uint32_t)sq.s0 + j;
+    const float* pp = a.part + ((uint64_t)tok * a.heads + qh) * a.splits * (D + 2);
+    float top = -__builtin_inff();
+    for (uint32_t s = 0; s < n; s++) top = fmaxf(top, pp[s * (D + 2) + D]);
+    const float sub = top == -__builtin_inff() ? 0.f : top;
+    float total = 0.f, o[DW];
+#pragma unroll
+    for (int x = 0; x < DW; x++) o[x] = 0.f;
+    for (uint32_t s = 0; s < n; s++) {
+        const float* ps = pp + s * (D + 2);
+        const float f = exp2_fast(ps[D] - sub);
+        total += f * ps[D + 1];
+#pragma unroll
+        for (int x = 0; x < DW; x++) o[x] += f * ps[64 * x + lane];
+    }
+    const float inv = total > 0.f ? 1.f / total : 0.f;
+    uint16_t* op = a.out + (uint64_t)tok * a.out_stride + (uint64_t)qh * a.c.dim;
+#pragma unroll
+    for (int x = 0; x < DW; x++)
+        if (64 * x + lane < a.c.dim) op[64 * x + lane] = __builtin_bit_cast(uint16_t, (__bf16)(o[x] * inv));
+    if (a.lse && lane == 0) a.lse[(uint64_t)tok * a.heads + qh] = total > 0.f ? (top + __builtin_amdgcn_logf(total)) * kLn2 : -__builtin_inff();
+}
+
+template <int DW>
+int launch(const KvAttend& a, hipStream_t st) {
+    const uint32_t row_tiles = (a.max_new * a.group + 15) / 16;
+    const dim3 grid(a.n_seqs * row_tiles, a.c.kv_heads, a.splits);
+    if (a.c.type == 1) hipLaunchKernelGGL((attend_kernel<DW, true, 4>), grid, dim3(256), 0, st, a, row_tiles);
+    else hipLaunchKernelGGL((attend_kernel<DW, false, 4>), grid, dim3(256), 0, st, a, row_tiles);
+    if (a.splits > 1) hipLaunchKernelGGL(join_kernel<DW>, dim3(a.n_seqs * a.max_new, a.heads), dim3(64), 0, st, a);
+    return (int)hipGetLastError();
+}
+
+}  // namespace
+
+extern "C" int bsk_kv_attend(const KvAttend* a, void* stream) {
+    switch (a->c.wide / 64) {
+        case 1: return launch<1>(*a, (hipStream_t)stream);
+        case 2: return launch<2>(*a, (hipStream_t)stream);
+        case 3: return launch<3>(*a, (hipStream_t)stream);
+        case 4: return launch<4>(*a, (hipStream_t)stream);
+        default: return (int)hipErrorInvalidValue;
+    }
+}

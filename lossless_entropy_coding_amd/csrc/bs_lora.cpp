@@ -1,0 +1,200 @@
+// bs_lora.cpp -- host side of the low-rank adapters: argument checks, the
+// choice of launch shapes, and the entry points of bs.h.
+#include <hip/hip_runtime.h>
+#include <string.h>
+
+#include <algorithm>
+
+#include "bs_device.h"
+#include "bs_internal.h"
+#include "bs_lora_device.h"
+
+using namespace bs;
+
+namespace {
+
+bool aligned(const void* p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
+
+bs_status launched(int e, const char* what) {
+    if (e == 0) return BS_OK;
+    set_error("%s launch: %s", what, hipGetErrorString((hipError_t)e));
+    return BS_E_HIP;
+}
+
+// tiles of 16 tokens at most: one for each 16 tokens, and one begun for each
+// adapter in use (tokens without one count as an adapter of their own)
+uint32_t max_tiles(uint32_t tokens, uint32_t adapters) {
+    return tokens / bsd::kLoraTile + std::min<uint32_t>(tokens, adapters + 1);
+}
+
+bs_status check_pack(const bs_lora_pack* p) {
+    if (!p) { set_error("NULL pack"); return BS_E_INVAL; }
+    if (p->adapters == 0 || p->adapters > bsd::kLoraAdapters) {
+        set_error("%u adapters (1..%u)", p->adapters, bsd::kLoraAdapters);
+        return BS_E_INVAL;
+    }
+    if (p->rank != 16 && p->rank != 32 && p->rank != 64 && p->rank != 128) {
+        set_error("rank %u: 16, 32, 64 or 128 (smaller adapters are padded)", p->rank);
+        return BS_E_INVAL;
+    }
+    if (p->rows == 0 || p->cols == 0 || p->rows >= (1u << 26) || p->cols >= (1u << 26)) {
+        set_error("a %u x %u projection", p->rows, p->cols);
+        return BS_E_INVAL;
+    }
+    if (!p->d_a || !p->d_b || !p->d_ranks || !p->d_factor) { set_error("NULL buffer in the pack"); return BS_E_INVAL; }
+    if (!aligned(p->d_a, 16) || !aligned(p->d_b, 16) || !aligned(p->d_ranks, 4) || !aligned(p->d_factor, 4)) {
+        set_error("a misaligned buffer in the pack");
+        return BS_E_INVAL;
+    }
+    return BS_OK;
+}
+
+bool check_tokens(uint64_t tokens) {
+    if (tokens <= (1u << 24)) return true;
+    set_error("%llu tokens in one call (at most 2^24)", (unsigned long long)tokens);
+    return false;
+}
+
+// Workgroups that share the columns of a tile: about two workgroups per CU in
+// all, with 4 or more steps of 32 columns for each of their 4 waves.
+uint32_t share_rule(const bs_lora_pack* p, uint32_t tiles) {
+    int cus = 0;
+    if (bsk_device_cus(&cus) != 0 || cus <= 0) cus = 256;
+    const uint32_t steps = (p->cols + 31) / 32;
+    const uint32_t want = std::max<uint32_t>(1, 2u * (uint32_t)cus / std::max(tiles, 1u));
+    return std::max<uint32_t>(1, std::min({want, steps / 16, bsd::kLoraSplits}));
+}
+
+uint64_t inner_bytes(const bs_lora_pack* p, uint32_t tokens) {
+    return align_up(4ull * share_rule(p, max_tiles(tokens, p->adapters)) * tokens * p->rank, 256);
+}
+
+void fill(const bs_lora_pack* p, const int32_t* d_batch, uint32_t tokens, const void* d_x, uint64_t x_stride, float* t,
+          bsd::LoraArgs& a) {
+    memset(&a, 0, sizeof a);
+    a.a = (const uint16_t*)p->d_a;
+    a.b = (const uint16_t*)p->d_b;
+    a.ranks = p->d_ranks;
+    a.factor = p->d_factor;
+    a.batch = d_batch;
+    a.x = (const uint16_t*)d_x;
+    a.x_stride = x_stride;
+    a.t = t;
+    a.adapters = p->adapters;
+    a.rank = p->rank;
+    a.rows = p->rows;
+    a.cols = p->cols;
+    a.cols_pad = (uint32_t)align_up(p->cols, 32);
+    a.tokens = tokens;
+    a.max_tiles = max_tiles(tokens, p->adapters);
+    a.ksplit = share_rule(p, a.max_tiles);
+    a.x_aligned = aligned(d_x, 16) && x_stride % 8 == 0;
+}
+
+}  // namespace
+
+extern "C" {
+
+uint64_t bs_lora_batch_bytes(uint32_t tokens, uint32_t adapters) {
+    if (!check_tokens(tokens) || adapters == 0 || adapters > bsd::kLoraAdapters) return 0;
+    return align_up(4ull * (bsd::kLoraHead + 4ull * max_tiles(tokens, adapters) + tokens), 16);
+}
+
+bs_status bs_lora_batch_async(const int32_t* d_adapter_of, uint32_t tokens, uint32_t adapters, int32_t* d_batch,
+                              uint64_t batch_bytes, void* stream) {
+    if (!check_tokens(tokens)) return BS_E_INVAL;
+    if (adapters == 0 || adapters > bsd::kLoraAdapters) {
+        set_error("%u adapters (1..%u)", adapters, bsd::kLoraAdapters);
+        return BS_E_INVAL;
+    }
+    if ((tokens && !d_adapter_of) || !d_batch) { set_error("NULL argument"); return BS_E_INVAL; }
+    if (!aligned(d_adapter_of, 4) || !aligned(d_batch, 16)) { set_error("a misaligned buffer"); return BS_E_INVAL; }
+    if (batch_bytes < bs_lora_batch_bytes(tokens, adapters)) {
+        set_error("batch of %llu B, %llu B needed", (unsigned long long)batch_bytes,
+                  (unsigned long long)bs_lora_batch_bytes(tokens, adapters));
+        return BS_E_INVAL;
+    }
+    return launched(bsk_lora_batch(d_adapter_of, tokens, adapters, max_tiles(tokens, adapters), d_batch, stream), "adapter batch");
+}
+
+uint64_t bs_lora_work_bytes(const bs_lora_pack* pack, uint32_t tokens) {
+    if (check_pack(pack) != BS_OK || !check_tokens(tokens)) return 0;
+    return inner_bytes(pack, tokens);
+}
+
+bs_status bs_lora_add_async(const bs_lora_pack* pack, const int32_t* d_batch, uint32_t tokens, const void* d_x,
+                            uint64_t x_stride, const void* d_y_in, void* d_y_out, uint64_t y_stride, uint32_t y_type,
+                            void* d_work, uint64_t work_bytes, void* stream) {
+    const bs_status rc = check_pack(pack);
+    if (rc != BS_OK) return rc;
+    if (!check_tokens(tokens)) return BS_E_INVAL;
+    if (y_type != BS_T_BF16 && y_type != BS_T_FP32) { set_error("Y type %u", y_type); return BS_E_INVAL; }
+    if (tokens == 0) return BS_OK;
+    if (!d_batch || !d_x || !d_y_in || !d_y_out || !d_work) { set_error("NULL argument"); return BS_E_INVAL; }
+    const uintptr_t el = y_type == BS_T_FP32 ? 4 : 2;
+    if (!aligned(d_batch, 16) || !aligned(d_x, 2) || !aligned(d_y_in, el) || !aligned(d_y_out, el) || !aligned(d_work, 16)) {
+        set_error("a misaligned buffer");
+        return BS_E_INVAL;
+    }
+    if (x_stride < pack->cols || y_stride < pack->rows) {
+        set_error("token strides %llu and %llu for %u columns and %u rows", (unsigned long long)x_stride,
+                  (unsigned long long)y_stride, pack->cols, pack->rows);
+        return BS_E_INVAL;
+    }
+    if (work_bytes < inner_bytes(pack, tokens)) {
+        set_error("workspace of %llu B, %llu B needed", (unsigned long long)work_bytes,
+                  (unsigned long long)inner_bytes(pack, tokens));
+        return BS_E_INVAL;
+    }
+    bsd::LoraArgs a;
+    fill(pack, d_batch, tokens, d_x, x_stride, (float*)d_work, a);
+    a.y_in = d_y_in;
+    a.y_out = d_y_out;
+    a.y_stride = y_stride;
+    a.y32 = y_type == BS_T_FP32;
+    const bs_status r2 = launched(bsk_lora_inner(&a, stream), "adapters' inner product");
+    if (r2 != BS_OK) return r2;
+    return launched(bsk_lora_outer(&a, stream), "adapters' outer product");
+}
+
+uint64_t bs_fixed_gemm_lora_work_bytes(uint64_t rows, uint64_t cols, uint32_t batch, const bs_lora_pack* pack) {
+    if (check_pack(pack) != BS_OK || batch == 0 || batch > 64) return 0;
+    return align_up(bs_fixed_gemm_work_bytes(rows, cols, batch), 256) + inner_bytes(pack, batch);
+}
+
+bs_status bs_fixed_gemm_lora_async(const bs_fixed_info* info, const void* d_blob, uint64_t rows, uint64_t cols,
+                                   uint32_t batch, const void* d_x, float* d_y, uint32_t* d_status,
+                                   const bs_lora_pack* pack, const int32_t* d_batch, void* d_work, uint64_t work_bytes,
+                                   void* stream) {
+    const bs_status rc = check_pack(pack);
+    if (rc != BS_OK) return rc;
+    if (pack->rows != rows || pack->cols != cols) {
+        set_error("adapters of a %u x %u projection beside a %llu x %llu one", pack->rows, pack->cols,
+                  (unsigned long long)rows, (unsigned long long)cols);
+        return BS_E_INVAL;
+    }
+    if (batch == 0 || batch > 64) { set_error("batch %u outside 1..64", batch); return BS_E_INVAL; }
+    if (!d_batch || !d_work) { set_error("NULL argument"); return BS_E_INVAL; }
+    if (!aligned(d_batch, 16) || !aligned(d_work, 256) || !aligned(d_y, 4)) { set_error("a misaligned buffer"); return BS_E_INVAL; }
+    if (work_bytes < bs_fixed_gemm_lora_work_bytes(rows, cols, batch, pack)) {
+        set_error("workspace of %llu B, %llu B needed", (unsigned long long)work_bytes,
+                  (unsigned long long)bs_fixed_gemm_lora_work_bytes(rows, cols, batch, pack));
+        return BS_E_INVAL;
+    }
+    const uint64_t split = bs_fixed_gemm_work_bytes(rows, cols, batch);
+    void* part = split ? d_work : nullptr;
+    const bs_status r1 = fixed_gemm(info, d_blob, rows, cols, batch, d_x, d_y, d_status, part, split, false, stream);
+    if (r1 != BS_OK) return r1;
+    bsd::LoraArgs a;
+    fill(pack, d_batch, batch, d_x, cols, (float*)((uint8_t*)d_work + align_up(split, 256)), a);
+    a.y_in = d_y;
+    a.y_out = d_y;
+    a.y_stride = rows;
+    a.y32 = 1;
+    a.part = (const float*)part;
+    const bs_status r2 = launched(bsk_lora_inner(&a, stream), "adapters' inner product");
+    if (r2 != BS_OK) return r2;
+    return launched(bsk_lora_outer(&a, stream), "adapters' outer product");
+}
+
+}  // extern "C"

@@ -1,0 +1,230 @@
+"""A paged key/value cache held in 8 bits, and attention over it: thin wrappers
+over the C ABI (include/bs.h, bs_kv_*).
+
+One cache serves all layers of a model.  Its rows are sequences; each holds
+pages of `page_tokens` tokens, the same page numbers in every layer.  A decode
+step extends the rows by one token, then for each layer appends the layer's
+keys and values and attends:
+
+    cache = KvCache(layers=42, kv_heads=8, head_dim=256, n_pages=4096, max_seqs=64, max_pages=512)
+    cache.extend(rows, ones)
+    for layer in range(42):
+        cache.append(layer, k, v, rows)
+        out = cache.attend(layer, q, rows)
+
+Everything is enqueued on the current (or given) stream and nothing
+synchronises except check().  The cache keeps its workspaces, so its calls go
+on one stream, or on several that wait for each other.
+"""
+from __future__ import annotations
+
+import ctypes as C
+
+import torch
+
+from . import _lib as L
+from .codec import _stream_handle
+
+
+def _wide(head_dim: int) -> int:
+    return -(-head_dim // 64) * 64
+
+
+def _ids(t: torch.Tensor, name: str) -> torch.Tensor:
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 vector on the device")
+    return t
+
+
+class KvCache:
+    """A cache (bs_kv_cache) and the tensors that it is made of: k, v, scale,
+    refs, table, lens and status."""
+
+    def __init__(self, layers: int, kv_heads: int, head_dim: int, n_pages: int, max_seqs: int, max_pages: int,
+                 page_tokens: int = 64, dtype: str = "e4m3", device: str = "cuda"):
+        if not 1 <= head_dim <= 256:
+            raise ValueError("head_dim goes from 1 to 256")
+        z = lambda *shape, t=torch.int32: torch.zeros(*shape, dtype=t, device=device)   # noqa: E731
+        wide = _wide(head_dim)
+        self._bind(z(layers, n_pages, kv_heads, page_tokens, wide, t=torch.uint8),
+                   z(layers, n_pages, kv_heads, wide, page_tokens, t=torch.uint8),
+                   z(layers, n_pages, kv_heads, 2, t=torch.float32), z(n_pages), z(max_seqs, max_pages), z(max_seqs),
+                   head_dim, dtype)
+
+    @classmethod
+    def over(cls, k, v, scale, refs, table, lens, head_dim: int, dtype: str = "e4m3") -> "KvCache":
+        """A cache over existing tensors (shapes and types as the constructor's)."""
+        self = cls.__new__(cls)
+        self._bind(k, v, scale, refs, table, lens, head_dim, dtype)
+        return self
+
+    def _bind(self, k, v, scale, refs, table, lens, head_dim, dtype):
+        if dtype not in L.KV_TYPES:
+            raise ValueError(f"dtype {dtype!r}: one of {', '.join(L.KV_TYPES)}")
+        if k.dim() != 5 or not 1 <= head_dim <= 256:
+            raise ValueError("k must be (layers, pages, kv_heads, page, wide), head_dim from 1 to 256")
+        layers, n_pages, heads, page, wide = k.shape
+        want = {"k": (k, torch.uint8, (layers, n_pages, heads, page, _wide(head_dim))),
+                "v": (v, torch.uint8, (layers, n_pages, heads, _wide(head_dim), page)),
+                "scale": (scale, torch.float32, (layers, n_pages, heads, 2)), "refs": (refs, torch.int32, (n_pages,)),
+                "table": (table, torch.int32, (lens.numel(), table.shape[-1])), "lens": (lens, torch.int32, (lens.numel(),))}
+        for name, (t, kind, shape) in want.items():
+            if t.dtype != kind or tuple(t.shape) != shape or not t.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous {kind} tensor of shape {shape}")
+        self.k, self.v, self.scale, self.refs, self.table, self.lens = k, v, scale, refs, table, lens
+        self.layers, self.n_pages, self.kv_heads, self.page_tokens = layers, n_pages, heads, page
+        self.head_dim, self.dtype, self.max_seqs, self.max_pages = head_dim, dtype, lens.numel(), table.shape[1]
+        self.status = torch.zeros(1, dtype=torch.int32, device=k.device)
+        self.c = L.KvCache(layers, n_pages, self.max_seqs, self.max_pages, heads, head_dim, page, L.KV_TYPES[dtype],
+                           k.data_ptr(), v.data_ptr(), scale.data_ptr(), refs.data_ptr(), table.data_ptr(),
+                           lens.data_ptr(), self.status.data_ptr())
+        sizes = L.KvSizes()
+        L.check(L.lib().bs_kv_sizes_get(C.byref(self.c), C.byref(sizes)), "bs_kv_sizes_get")
+        self.page_bytes = int(sizes.page_bytes)
+        self._page_work = self._attend_work = None
+
+    # ------------------------------------------------------------ pages
+    def _work(self, n: int) -> torch.Tensor:
+        need = int(L.lib().bs_kv_pages_work_bytes(C.byref(self.c), n))
+        if self._page_work is None or self._page_work.numel() < need:
+            self._page_work = torch.empty(max(need, 256), dtype=torch.uint8, device=self.k.device)
+        return self._page_work
+
+    def extend(self, rows: torch.Tensor, counts: torch.Tensor, stream=None) -> None:
+        """Make room for counts[i] more tokens in row rows[i] (distinct rows);
+        all rows grow, or none (bs_kv_extend_async)."""
+        _ids(rows, "rows"), _ids(counts, "counts")
+        if rows.numel() != counts.numel():
+            raise ValueError("one count per row")
+        w = self._work(rows.numel())
+        L.check(L.lib().bs_kv_extend_async(C.byref(self.c), rows.numel(), rows.data_ptr(), counts.data_ptr(), w.data_ptr(),
+                                           w.numel(), _stream_handle(stream)), "bs_kv_extend_async")
+
+    def fork(self, parents: torch.Tensor, children: torch.Tensor, stream=None) -> None:
+        """Empty rows children[i] become copies of rows parents[i], sharing
+        their whole pages (bs_kv_fork_async)."""
+        _ids(parents, "parents"), _ids(children, "children")
+        if parents.numel() != children.numel():
+            raise ValueError("one parent per child")
+        w = self._work(parents.numel())
+        L.check(L.lib().bs_kv_fork_async(C.byref(self.c), parents.numel(), parents.data_ptr(), children.data_ptr(),
+                                         w.data_ptr(), w.numel(), _stream_handle(stream)), "bs_kv_fork_async")
+
+    def free(self, rows: torch.Tensor, stream=None) -> None:
+        """Empty rows (bs_kv_free_async)."""
+        _ids(rows, "rows")
+        L.check(L.lib().bs_kv_free_async(C.byref(self.c), rows.numel(), rows.data_ptr(), _stream_handle(stream)),
+                "bs_kv_free_async")
+
+    def copy_pages(self, source: torch.Tensor, target: torch.Tensor, stream=None) -> None:
+        """Copy pages in every layer (bs_kv_copy_pages_async)."""
+        _ids(source, "source"), _ids(target, "target")
+        if source.numel() != target.numel():
+            raise ValueError("one target per source")
+        L.check(L.lib().bs_kv_copy_pages_async(C.byref(self.c), source.numel(), source.data_ptr(), target.data_ptr(),
+                                               _stream_handle(stream)), "bs_kv_copy_pages_async")
+
+    def compact(self, table_out: torch.Tensor | None = None, refs_out: torch.Tensor | None = None, stream=None) -> None:
+        """Move the pages in use to the lowest places (bs_kv_compact_async).
+        With table_out and refs_out the new table and counts go there and the
+        cache keeps its own; without, the cache goes on with the new ones in
+        tensors of its own, kept for the next time."""
+        if (table_out is None) != (refs_out is None):
+            raise ValueError("table_out and refs_out go together")
+        swap = table_out is None
+        if swap:
+            if getattr(self, "_spare", None) is None:
+                self._spare = (torch.empty_like(self.table), torch.empty_like(self.refs))
+            table_out, refs_out = self._spare
+        for t, like, name in ((table_out, self.table, "table_out"), (refs_out, self.refs, "refs_out")):
+            if t.dtype != like.dtype or t.shape != like.shape or not t.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous int32 tensor of shape {tuple(like.shape)}")
+        w = self._work(0)
+        L.check(L.lib().bs_kv_compact_async(C.byref(self.c), table_out.data_ptr(), refs_out.data_ptr(), w.data_ptr(),
+                                            w.numel(), _stream_handle(stream)), "bs_kv_compact_async")
+        if swap:
+            self._spare = (self.table, self.refs)
+            self.table, self.refs = table_out, refs_out
+            self.c.d_table, self.c.d_refs = table_out.data_ptr(), refs_out.data_ptr()
+
+    # ------------------------------------------------------------ tokens
+    def _tokens(self, t: torch.Tensor, heads: int | None, name: str) -> int:
+        """Checks a (tokens, heads, head_dim) tensor with a token's values side
+        by side; returns its token stride."""
+        if t.dim() != 3 or t.shape[2] != self.head_dim or (heads is not None and t.shape[1] != heads):
+            raise ValueError(f"{name} must be (tokens, {heads or 'heads'}, {self.head_dim})")
+        if t.numel() and ((t.shape[2] > 1 and t.stride(2) != 1) or (t.shape[1] > 1 and t.stride(1) != self.head_dim)):
+            raise ValueError(f"the values of a token must be side by side in {name}")
+        return t.shape[1] * t.shape[2] if t.shape[0] <= 1 else t.stride(0)
+
+    def _rows(self, rows, starts, total, max_new):
+        _ids(rows, "rows")
+        if starts is None:
+            if rows.numel() != total:
+                raise ValueError(f"{total} tokens for {rows.numel()} rows: give starts")
+            return 1
+        _ids(starts, "starts")
+        if starts.numel() != rows.numel() + 1:
+            raise ValueError("starts holds one offset per row and the end")
+        return max(1, min(total, total if max_new is None else max_new))
+
+    def append(self, layer: int, k: torch.Tensor, v: torch.Tensor, rows: torch.Tensor, starts: torch.Tensor | None = None,
+               max_new: int | None = None, stream=None) -> None:
+        """Store the keys and values of the rows' last tokens
+        (bs_kv_append_async): k and v (tokens, kv_heads, head_dim) bfloat16 or
+        float32, tokens starts[i] .. starts[i + 1] - 1 of row rows[i] (without
+        starts one each); max_new: the most of one row, if it is known."""
+        if k.dtype != v.dtype or k.dtype not in (torch.bfloat16, torch.float32) or k.shape != v.shape:
+            raise ValueError("k and v must have one shape and be bfloat16 or float32")
+        ks, vs = self._tokens(k, self.kv_heads, "k"), self._tokens(v, self.kv_heads, "v")
+        most = self._rows(rows, starts, k.shape[0], max_new)
+        rc = L.lib().bs_kv_append_async(C.byref(self.c), layer, rows.numel(), rows.data_ptr(),
+                                        None if starts is None else starts.data_ptr(), k.shape[0], most, k.data_ptr(), ks,
+                                        v.data_ptr(), vs, L.T_FP32 if k.dtype == torch.float32 else L.T_BF16,
+                                        _stream_handle(stream))
+        L.check(rc, "bs_kv_append_async")
+
+    def attend(self, layer: int, q: torch.Tensor, rows: torch.Tensor, starts: torch.Tensor | None = None,
+               max_new: int | None = None, max_len: int = 0, scale: float = 0.0, window: int = 0, sinks: int = 0,
+               softcap: float = 0.0, out: torch.Tensor | None = None, lse: bool | torch.Tensor = False, stream=None):
+        """Attention of the rows' last tokens over all that they see
+        (bs_kv_attend_async): q (tokens, heads, head_dim) bfloat16, tokens as in
+        append.  window: 0 or how many of the last tokens a query sees, besides
+        the first `sinks`; softcap c: logits become c tanh(logit / c); scale 0:
+        1 / sqrt(head_dim).  max_len: no row is longer, if it is known.  Returns
+        the result (q's shape, bfloat16), and with lse the logarithms of the
+        softmax sums (tokens, heads) as float32."""
+        if q.dtype != torch.bfloat16:
+            raise ValueError("q must be bfloat16")
+        qs = self._tokens(q, None, "q")
+        if out is None:
+            out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+        elif out.dtype != torch.bfloat16 or out.shape != q.shape:
+            raise ValueError("out must be bfloat16 of q's shape")
+        os = self._tokens(out, None, "out")
+        if lse is True:
+            lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+        elif lse is not False and (lse.dtype != torch.float32 or lse.shape != q.shape[:2] or not lse.is_contiguous()):
+            raise ValueError("lse must be a contiguous float32 tensor of (tokens, heads)")
+        if window < 0 or sinks < 0 or max_len < 0:
+            raise ValueError("window, sinks and max_len are not negative")
+        most = self._rows(rows, starts, q.shape[0], max_new)
+        a = L.KvAttendArgs(layer, rows.numel(), q.shape[1], q.shape[0], most, max_len, rows.data_ptr(),
+                           None if starts is None else starts.data_ptr(), q.data_ptr(), out.data_ptr(),
+                           None if lse is False else lse.data_ptr(), qs, os, scale, softcap, window, sinks)
+        need = int(L.lib().bs_kv_attend_work_bytes(C.byref(self.c), C.byref(a)))
+        if need and (self._attend_work is None or self._attend_work.numel() < need):
+            self._attend_work = torch.empty(need, dtype=torch.uint8, device=self.k.device)
+        w = self._attend_work if need else None
+        rc = L.lib().bs_kv_attend_async(C.byref(self.c), C.byref(a), w.data_ptr() if need else None,
+                                        w.numel() if need else 0, _stream_handle(stream))
+        L.check(rc, "bs_kv_attend_async")
+        return out if lse is False else (out, lse)
+
+    def check(self) -> None:
+        """Raise if a call met one of the conditions that bs.h lists, and clear
+        it; synchronises."""
+        bits = int(self.status.item())
+        if bits:
+            self.status.zero_()
+            raise RuntimeError("key/value cache: " + "; ".join(v for b, v in L.KV_STATUS.items() if bits & b))
