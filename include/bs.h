@@ -566,7 +566,9 @@ typedef struct {
     uint32_t adapters;      /* 1..4096 */
     uint32_t rank;          /* 16, 32, 64 or 128: the rank that storage is laid out for */
     uint32_t rows, cols;    /* of the projection, below 2^26 */
-    const void* d_a;        /* BF16 [adapters][rank][cols rounded up to 32], zeros past an adapter's rank and past cols; 16-B aligned */
+    const void* d_a;        /* BF16 [adapters][rank / 16][ceil(cols / 32)][64][8], 16-B aligned: entry [a][i][j][16 g + m][e] is
+                             * A_a[16 i + m][32 j + 8 g + e] (the order of the matrix product's operand), zeros past an
+                             * adapter's rank and past cols */
     const void* d_b;        /* BF16 [adapters][rows][rank], zeros past an adapter's rank; 16-B aligned */
     const int32_t* d_ranks; /* each adapter's own rank, 1..rank */
     const float* d_factor;  /* s */

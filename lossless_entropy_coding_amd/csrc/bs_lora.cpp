@@ -55,14 +55,21 @@ bool check_tokens(uint64_t tokens) {
     return false;
 }
 
-// Workgroups that share the columns of a tile: about two workgroups per CU in
-// all, with 4 or more steps of 32 columns for each of their 4 waves.
+// the outer product's grid: tiles times blocks of at most 4096 rows
+bool check_grid(const bs_lora_pack* p, uint32_t tokens) {
+    if ((uint64_t)max_tiles(tokens, p->adapters) * ((p->rows + 4095) / 4096) <= 0x7FFFFFFFull) return true;
+    set_error("%u tokens of %u rows are too many for one call", tokens, p->rows);
+    return false;
+}
+
+// Workgroups that share the columns of a tile: about eight workgroups per CU
+// in all, with 128 columns or more for each of their 4 waves.
 uint32_t share_rule(const bs_lora_pack* p, uint32_t tiles) {
     int cus = 0;
     if (bsk_device_cus(&cus) != 0 || cus <= 0) cus = 256;
-    const uint32_t steps = (p->cols + 31) / 32;
-    const uint32_t want = std::max<uint32_t>(1, 2u * (uint32_t)cus / std::max(tiles, 1u));
-    return std::max<uint32_t>(1, std::min({want, steps / 16, bsd::kLoraSplits}));
+    const uint32_t want = std::min(std::max<uint32_t>(1, 8u * (uint32_t)cus / std::max(tiles, 1u)), bsd::kLoraSplits);
+    const uint32_t blocks = (p->cols + 511) / 512, turns = (blocks + want - 1) / want;
+    return (blocks + turns - 1) / turns;         // as many turns of 512 columns with the fewest workgroups
 }
 
 uint64_t inner_bytes(const bs_lora_pack* p, uint32_t tokens) {
@@ -127,7 +134,7 @@ bs_status bs_lora_add_async(const bs_lora_pack* pack, const int32_t* d_batch, ui
                             void* d_work, uint64_t work_bytes, void* stream) {
     const bs_status rc = check_pack(pack);
     if (rc != BS_OK) return rc;
-    if (!check_tokens(tokens)) return BS_E_INVAL;
+    if (!check_tokens(tokens) || !check_grid(pack, tokens)) return BS_E_INVAL;
     if (y_type != BS_T_BF16 && y_type != BS_T_FP32) { set_error("Y type %u", y_type); return BS_E_INVAL; }
     if (tokens == 0) return BS_OK;
     if (!d_batch || !d_x || !d_y_in || !d_y_out || !d_work) { set_error("NULL argument"); return BS_E_INVAL; }
@@ -152,6 +159,7 @@ bs_status bs_lora_add_async(const bs_lora_pack* pack, const int32_t* d_batch, ui
     a.y_out = d_y_out;
     a.y_stride = y_stride;
     a.y32 = y_type == BS_T_FP32;
+    a.y_vec = aligned(d_y_in, 16) && aligned(d_y_out, 16) && y_stride % (16 / el) == 0;
     const bs_status r2 = launched(bsk_lora_inner(&a, stream), "adapters' inner product");
     if (r2 != BS_OK) return r2;
     return launched(bsk_lora_outer(&a, stream), "adapters' outer product");
@@ -191,6 +199,7 @@ bs_status bs_fixed_gemm_lora_async(const bs_fixed_info* info, const void* d_blob
     a.y_out = d_y;
     a.y_stride = rows;
     a.y32 = 1;
+    a.y_vec = aligned(d_y, 16) && rows % 4 == 0;
     a.part = (const float*)part;
     const bs_status r2 = launched(bsk_lora_inner(&a, stream), "adapters' inner product");
     if (r2 != BS_OK) return r2;

@@ -15,6 +15,7 @@
 
 #include <algorithm>
 
+#include "bs_device.h"
 #include "bs_lora_device.h"
 
 using namespace bsd;
@@ -22,6 +23,7 @@ using namespace bsd;
 namespace {
 
 typedef unsigned int v4u __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
@@ -99,12 +101,13 @@ struct Tile {
 };
 
 __device__ __forceinline__ bool get_tile(const LoraArgs& p, uint32_t i, Tile& tl) {
-    if (i >= p.max_tiles || i >= (uint32_t)p.batch[0]) return false;
-    const int32_t* e = p.batch + kLoraHead + 4 * i;
-    tl.adapter = e[0];
-    tl.first = (uint32_t)e[1];
-    tl.count = (uint32_t)e[2];
-    return tl.adapter >= -1 && tl.adapter < (int32_t)p.adapters && tl.count >= 1 && tl.count <= kLoraTile &&
+    // both loads go out together (tile i lies inside the batch's buffer)
+    const int32_t tiles = p.batch[0];
+    const v4u e = *(const v4u*)(p.batch + kLoraHead + 4 * i);
+    tl.adapter = (int32_t)e[0];
+    tl.first = e[1];
+    tl.count = e[2];
+    return i < (uint32_t)tiles && tl.adapter >= -1 && tl.adapter < (int32_t)p.adapters && tl.count >= 1 && tl.count <= kLoraTile &&
            tl.first < p.tokens && tl.count <= p.tokens - tl.first;
 }
 
@@ -117,7 +120,22 @@ __device__ __forceinline__ uint32_t token_at(const LoraArgs& p, uint32_t i) {
 // here reads a product's later elements at a block's join without the wait
 // that it puts before the first, and they come back stale.
 
-// grid: (tiles, shares of the columns); RT: 16-row tiles of the rank
+// 8 elements of a row of x from column c, zeros past the last
+__device__ __forceinline__ bf16x8 load_x(const LoraArgs& p, const uint16_t* xp, uint32_t c) {
+    if (p.x_aligned && c + 8 <= p.cols) return *(const bf16x8*)(xp + c);
+    uint32_t w[4];
+#pragma unroll
+    for (uint32_t e = 0; e < 4; e++) {
+        const uint32_t lo = c + 2 * e < p.cols ? xp[c + 2 * e] : 0u, hi = c + 2 * e + 1 < p.cols ? xp[c + 2 * e + 1] : 0u;
+        w[e] = lo | hi << 16;
+    }
+    return __builtin_bit_cast(bf16x8, v4u{w[0], w[1], w[2], w[3]});
+}
+
+// grid: (tiles, shares of the columns); RT: 16-row tiles of the rank.  A wave
+// takes 128 columns at a time, all their loads issued before the first
+// product.  A is kept in the order of the product's operand, so a wave reads
+// 4 KiB on end of each 16 rows.
 template <int RT>
 __global__ __launch_bounds__(256, 2) void inner_kernel(LoraArgs p) {
     Tile tl;
@@ -128,31 +146,31 @@ __global__ __launch_bounds__(256, 2) void inner_kernel(LoraArgs p) {
     const uint32_t nr = min((uint32_t)(p.ranks[tl.adapter] + 15) / 16, (uint32_t)RT);
     const uint32_t tok = token_at(p, tl.first + min(m, tl.count - 1));
     const uint16_t* xp = p.x + (uint64_t)tok * p.x_stride;
-    const uint16_t* ap = p.a + ((uint64_t)tl.adapter * p.rank + m) * p.cols_pad;
+    const uint32_t steps = p.cols_pad / 32;
+    const uint16_t* ap = p.a + (uint64_t)tl.adapter * p.rank * p.cols_pad + 8 * lane;
     f32x4 acc[RT];
 #pragma unroll
     for (int r = 0; r < RT; r++) acc[r] = f32x4{0.f, 0.f, 0.f, 0.f};
-    const uint32_t steps = p.cols_pad / 32, step = 4 * p.ksplit;
-    for (uint32_t k = blockIdx.y * 4 + wave; k < steps; k += step) {
-        const uint32_t c = 32 * k + 8 * g;
-        bf16x8 xv;
-        if (p.x_aligned && c + 8 <= p.cols) {
-            xv = *(const bf16x8*)(xp + c);
-        } else {
-            uint32_t w[4];
+    const uint32_t step = 4 * p.ksplit;
+    constexpr uint32_t U = RT == 8 ? 2 : 4;      // 64 columns at rank 128, where 128 would not fit the registers
+    for (uint32_t k = blockIdx.y * 4 + wave; 32 * U * k < p.cols_pad; k += step) {
+        const uint32_t c0 = 32 * U * k + 8 * g;
+        bf16x8 xv[U], av[U][RT];
 #pragma unroll
-            for (uint32_t e = 0; e < 4; e++) {
-                const uint32_t lo = c + 2 * e < p.cols ? xp[c + 2 * e] : 0u, hi = c + 2 * e + 1 < p.cols ? xp[c + 2 * e + 1] : 0u;
-                w[e] = lo | hi << 16;
-            }
-            xv = __builtin_bit_cast(bf16x8, v4u{w[0], w[1], w[2], w[3]});
+        for (uint32_t u = 0; u < U; u++) {
+            // steps past the last: zeros of x against the last one's A
+            const uint32_t c = c0 + 32 * u;
+            const uint32_t st = min(U * k + u, steps - 1);
+            xv[u] = load_x(p, xp, c);
+#pragma unroll
+            for (uint32_t r = 0; r < RT; r++)
+                if (r < nr) av[u][r] = *(const bf16x8*)(ap + ((uint64_t)r * steps + st) * 512);
         }
 #pragma unroll
-        for (uint32_t r = 0; r < RT; r++)
-            if (r < nr) {
-                const bf16x8 av = *(const bf16x8*)(ap + (uint64_t)(16 * r) * p.cols_pad + c);
-                acc[r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av, xv, acc[r], 0, 0, 0);
-            }
+        for (uint32_t u = 0; u < U; u++)
+#pragma unroll
+            for (uint32_t r = 0; r < RT; r++)
+                if (r < nr) acc[r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av[u][r], xv[u], acc[r], 0, 0, 0);
     }
     if (wave > 0) {
 #pragma unroll
@@ -181,73 +199,197 @@ __device__ __forceinline__ void three(float v, __bf16& a, __bf16& b, __bf16& c) 
     c = (__bf16)(r - (float)b);
 }
 
-// grid: (tiles, row blocks of 64 R); a wave takes R steps of 16 rows
-template <int RT, bool Y32>
-__global__ __launch_bounds__(256, 2) void outer_kernel(LoraArgs p, uint32_t rows_per_wave) {
-    Tile tl;
-    if (!get_tile(p, blockIdx.x, tl)) return;
-    const uint32_t t = threadIdx.x, lane = t & 63u, m = lane & 15u, g = lane >> 4;
-    const uint32_t wave = __builtin_amdgcn_readfirstlane(t >> 6);
-    const uint32_t tok = token_at(p, tl.first + min(m, tl.count - 1));
-    constexpr int KC = (RT + 1) / 2;             // steps of 32 ranks
-    bf16x8 b0[KC], b1[KC], b2[KC];
-    if (tl.adapter >= 0) {
-        const float f = p.factor[tl.adapter];
+// y of 4 (fp32) or 8 (BF16) rows from element `at`, n of them inside
+template <bool Y32>
+__device__ __forceinline__ void load_y(const LoraArgs& p, uint64_t at, uint32_t n, float* y) {
+    constexpr uint32_t N = Y32 ? 4 : 8;
+    if (p.y_vec && n >= N) {
+        if (Y32) {
+            const f32x4 v = *(const f32x4*)((const float*)p.y_in + at);
 #pragma unroll
-        for (int k = 0; k < KC; k++) {
-            const uint32_t r0 = 32 * k + 8 * g;
+            for (uint32_t e = 0; e < 4; e++) y[e] = v[e];
+            if (p.part) {
+                const f32x4 w = *(const f32x4*)(p.part + at);
 #pragma unroll
-            for (uint32_t e = 0; e < 8; e++) {
-                float v = 0.f;
-                if (r0 + e < 16 * RT && m < tl.count) {
-                    const float* tp = p.t + ((uint64_t)tl.first + m) * p.rank + r0 + e;
-                    for (uint32_t s = 0; s < p.ksplit; s++) v += tp[(uint64_t)s * p.tokens * p.rank];
-                }
-                __bf16 x, y, z;
-                three(v * f, x, y, z);
-                b0[k][e] = x;
-                b1[k][e] = y;
-                b2[k][e] = z;
+                for (uint32_t e = 0; e < 4; e++) y[e] += w[e];
             }
-        }
-    }
-    const uint32_t r_begin = (blockIdx.y * 4 + wave) * rows_per_wave;
-    for (uint32_t r0 = r_begin; r0 < min(r_begin + rows_per_wave, p.rows); r0 += 16) {
-        f32x4 acc = f32x4{0.f, 0.f, 0.f, 0.f};
-        if (tl.adapter >= 0) {
-            const uint32_t row = min(r0 + m, p.rows - 1);
-            const uint16_t* bp = p.b + ((uint64_t)tl.adapter * p.rows + row) * p.rank;
-#pragma unroll
-            for (int k = 0; k < KC; k++) {
-                const uint32_t c = 32 * k + 8 * g;
-                const bf16x8 bv = *(const bf16x8*)(bp + (c < 16 * RT ? c : 0u));
-                acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bv, b2[k], acc, 0, 0, 0);
-                acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bv, b1[k], acc, 0, 0, 0);
-                acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bv, b0[k], acc, 0, 0, 0);
-            }
-        }
-        if (m < tl.count) {
-            const uint64_t at = (uint64_t)tok * p.y_stride + r0 + 4 * g;
+        } else {
+            const v4u v = *(const v4u*)((const uint16_t*)p.y_in + at);
 #pragma unroll
             for (uint32_t e = 0; e < 4; e++) {
-                if (r0 + 4 * g + e >= p.rows) continue;
-                float y = Y32 ? ((const float*)p.y_in)[at + e] : bf(((const uint16_t*)p.y_in)[at + e]);
-                if (p.part) y += p.part[at + e];
-                y += acc[e];
-                if (Y32) ((float*)p.y_out)[at + e] = y;
-                else ((uint16_t*)p.y_out)[at + e] = __builtin_bit_cast(uint16_t, (__bf16)y);
+                const uint32_t w = v[e];
+                y[2 * e] = bf(w & 0xFFFFu);
+                y[2 * e + 1] = __builtin_bit_cast(float, w & 0xFFFF0000u);
             }
+        }
+        return;
+    }
+#pragma unroll
+    for (uint32_t e = 0; e < N; e++)
+        if (e < n) {
+            y[e] = Y32 ? ((const float*)p.y_in)[at + e] : bf(((const uint16_t*)p.y_in)[at + e]);
+            if (Y32 && p.part) y[e] += p.part[at + e];
+        }
+}
+
+template <bool Y32>
+__device__ __forceinline__ void store_y(const LoraArgs& p, uint64_t at, uint32_t n, const float* y) {
+    constexpr uint32_t N = Y32 ? 4 : 8;
+    if (p.y_vec && n >= N) {
+        if (Y32) *(f32x4*)((float*)p.y_out + at) = f32x4{y[0], y[1], y[2], y[3]};
+        else {
+            v4u v;
+#pragma unroll
+            for (uint32_t e = 0; e < 4; e++) {
+                const bf16x2 w = {(__bf16)y[2 * e], (__bf16)y[2 * e + 1]};
+                v[e] = __builtin_bit_cast(uint32_t, w);
+            }
+            *(v4u*)((uint16_t*)p.y_out + at) = v;
+        }
+        return;
+    }
+#pragma unroll
+    for (uint32_t e = 0; e < N; e++)
+        if (e < n) {
+            if (Y32) ((float*)p.y_out)[at + e] = y[e];
+            else ((uint16_t*)p.y_out)[at + e] = __builtin_bit_cast(uint16_t, (__bf16)y[e]);
+        }
+}
+
+// grid: blocks of rows x tiles, the blocks of a tile side by side, so that
+// neighbouring workgroups fill whole rows of y; a workgroup's waves take `strips` strips of 64 rows in turn.  The
+// workgroup first adds the shares of t and leaves its three BF16 parts in
+// LDS, in the order of the product's operand.  The 64 rows of a strip are
+// dealt to the four 16-row products such that a lane ends up with rows that
+// lie side by side in y: 4 (fp32, 16 j + 4 g ..) or 8 (BF16, 32 j + 8 g ..)
+// to each 16-B access, and the four lane groups fill 64 B of a token's row.
+// The next strip's y is loaded before this one's is stored.
+template <int RT, bool Y32>
+__global__ __launch_bounds__(256, 2) void outer_kernel(LoraArgs p, uint32_t strips, uint32_t blocks) {
+    constexpr int KC = (RT + 1) / 2;             // steps of 32 ranks
+    constexpr int NB = RT == 1 ? 2 : 3;
+    // part n of step k, lane's 8 ranks
+    __shared__ __attribute__((aligned(16))) __bf16 tb[NB][KC][64][8];
+    Tile tl;
+    const uint32_t tile = blockIdx.x / blocks, rb = blockIdx.x % blocks;
+    if (!get_tile(p, tile, tl)) return;
+    if (tl.adapter < 0 && p.y_in == p.y_out && !p.part) return;
+    const uint32_t t = threadIdx.x, lane = t & 63u, m = lane & 15u, g = lane >> 4;
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(t >> 6);
+    const uint32_t begin = (rb * 4 * strips + wave) * 64;
+    const bool mine = m < tl.count;
+    const uint32_t tok = token_at(p, tl.first + min(m, tl.count - 1));
+    const uint64_t yrow = (uint64_t)tok * p.y_stride;
+    constexpr uint32_t N = Y32 ? 4 : 8, NY = 16 / N;
+    // rows of the lane's access i of the strip at s0, and how many are inside
+    auto row_of = [&](uint32_t s0, uint32_t i) { return s0 + (Y32 ? 16 * i + 4 * g : 32 * i + 8 * g); };
+    auto left_of = [&](uint32_t r) { return mine && r < p.rows ? p.rows - r : 0u; };
+    float next[16];
+#pragma unroll
+    for (uint32_t i = 0; i < NY; i++) {
+        const uint32_t r = row_of(begin, i), n = left_of(r);
+        if (n) load_y<Y32>(p, yrow + r, n, next + N * i);
+    }
+    bf16x8 a[4][KC], b[NB][KC];
+    uint32_t nk = 0;
+    auto load_b = [&](uint32_t s0) {
+#pragma unroll
+        for (uint32_t j = 0; j < 4; j++) {
+            // row m of product j: lane group m / 4, element m % 4
+            const uint32_t r = s0 + (Y32 ? 16 * j + m : 32 * (j >> 1) + 8 * (m >> 2) + 4 * (j & 1u) + (m & 3u));
+            const uint16_t* bp = p.b + ((uint64_t)tl.adapter * p.rows + min(r, p.rows - 1)) * p.rank;
+#pragma unroll
+            for (uint32_t k = 0; k < KC; k++)
+                if (k < nk) a[j][k] = *(const bf16x8*)(bp + (RT == 1 ? 8 * (g & 1u) : 32 * k + 8 * g));
+        }
+    };
+    if (tl.adapter >= 0) {
+        nk = min((uint32_t)(p.ranks[tl.adapter] + 31) / 32, (uint32_t)KC);
+        const float f = p.factor[tl.adapter];
+        load_b(begin);
+        // t[token q][rank r] for the tile's 16 tokens
+#pragma unroll
+        for (uint32_t i = t; i < 256 * RT; i += 256) {
+            const uint32_t q = i / (16 * RT), r = i % (16 * RT);
+            float v = 0.f;
+            if (q < tl.count) {
+                const float* tp = p.t + ((uint64_t)tl.first + q) * p.rank + r;
+                float w[kLoraSplits];            // the shares' loads go out together
+#pragma unroll
+                for (uint32_t s = 0; s < kLoraSplits; s++) w[s] = s < p.ksplit ? tp[(uint64_t)s * p.tokens * p.rank] : 0.f;
+#pragma unroll
+                for (uint32_t s = 0; s < kLoraSplits; s++) v += w[s];
+            }
+            __bf16 x, y, z;
+            three(v * f, x, y, z);
+            const uint32_t l = 16 * ((r >> 3) & 3u) + q, e = r & 7u;
+            tb[0][r >> 5][l][e] = x;
+            if (RT == 1) {
+                // a rank of 16 fills half of a step: lane groups 2 and 3
+                // take the second parts of the same ranks
+                tb[0][0][l + 32][e] = y;
+                tb[1][0][l][e] = z;
+                tb[1][0][l + 32][e] = (__bf16)0.f;
+            } else {
+                tb[1][r >> 5][l][e] = y;
+                tb[NB - 1][r >> 5][l][e] = z;
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int n = 0; n < NB; n++)
+#pragma unroll
+            for (int k = 0; k < KC; k++) b[n][k] = *(const bf16x8*)tb[n][k][lane];
+    }
+    for (uint32_t s = 0; s < strips; s++) {
+        const uint32_t s0 = begin + 256 * s;
+        if (s0 >= p.rows) break;
+        float y[16];
+#pragma unroll
+        for (int e = 0; e < 16; e++) y[e] = next[e];
+        if (s + 1 < strips) {
+#pragma unroll
+            for (uint32_t i = 0; i < NY; i++) {
+                const uint32_t r = row_of(s0 + 256, i), n = left_of(r);
+                if (n) load_y<Y32>(p, yrow + r, n, next + N * i);
+            }
+        }
+        if (tl.adapter >= 0) {
+#pragma unroll
+            for (uint32_t j = 0; j < 4; j++) {
+                f32x4 acc = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (uint32_t k = 0; k < KC; k++)
+                    if (k < nk) {
+#pragma unroll
+                        for (int n = NB - 1; n >= 0; n--)
+                            acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[j][k], b[n][k], acc, 0, 0, 0);
+                    }
+#pragma unroll
+                for (uint32_t e = 0; e < 4; e++) y[4 * j + e] += acc[e];
+            }
+            if (s + 1 < strips) load_b(s0 + 256);
+        }
+#pragma unroll
+        for (uint32_t i = 0; i < NY; i++) {
+            const uint32_t r = row_of(s0, i), n = left_of(r);
+            if (n) store_y<Y32>(p, yrow + r, n, y + N * i);
         }
     }
 }
 
 template <int RT>
 int outer(const LoraArgs& a, hipStream_t st) {
-    // rows of a wave: 16 for few tiles, more where the tiles fill the GPU
-    const uint32_t rw = a.max_tiles >= 64 ? 64 : 16;
-    const dim3 grid(a.max_tiles, (a.rows + 4 * rw - 1) / (4 * rw));
-    if (a.y32) hipLaunchKernelGGL((outer_kernel<RT, true>), grid, dim3(256), 0, st, a, rw);
-    else hipLaunchKernelGGL((outer_kernel<RT, false>), grid, dim3(256), 0, st, a, rw);
+    // strips of a wave: as many as leave about five workgroups per CU (at
+    // most 16), since each workgroup first finds its tile and joins t
+    int cus = 0;
+    if (bsk_device_cus(&cus) != 0 || cus <= 0) cus = 256;
+    const uint64_t all = (uint64_t)a.max_tiles * ((a.rows + 255) / 256);
+    const uint32_t strips = (uint32_t)std::min<uint64_t>(16, std::max<uint64_t>(1, all / (5ull * (uint64_t)cus)));
+    const uint32_t blocks = (a.rows + 256 * strips - 1) / (256 * strips);
+    const dim3 grid(blocks * a.max_tiles);
+    if (a.y32) hipLaunchKernelGGL((outer_kernel<RT, true>), grid, dim3(256), 0, st, a, strips, blocks);
+    else hipLaunchKernelGGL((outer_kernel<RT, false>), grid, dim3(256), 0, st, a, strips, blocks);
     return (int)hipGetLastError();
 }
 

@@ -9,10 +9,10 @@ namespace bsd {
 constexpr uint32_t kLoraTile = 16;           // tokens of one adapter that are taken together
 constexpr uint32_t kLoraAdapters = 4096;     // adapters of a pack
 constexpr uint32_t kLoraHead = 4;            // words before a batch's tiles: tiles, tokens, bad indices, 0
-constexpr uint32_t kLoraSplits = 32;         // shares of the columns at most
+constexpr uint32_t kLoraSplits = 8;          // shares of the columns at most
 
 struct LoraArgs {
-    const uint16_t* a;          // [adapters][rank][cols_pad]
+    const uint16_t* a;          // [adapters][rank / 16][cols_pad / 32][64][8] (bs.h)
     const uint16_t* b;          // [adapters][rows][rank]
     const int32_t* ranks;       // each adapter's own rank
     const float* factor;
@@ -28,6 +28,7 @@ struct LoraArgs {
     uint32_t tokens, max_tiles, ksplit;
     int x_aligned;              // rows of x can be read 16 B at a time
     int y32;
+    int y_vec;                  // y (and part) can be read and written 16 B at a time
 };
 
 }  // namespace bsd

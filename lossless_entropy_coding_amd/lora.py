@@ -37,11 +37,14 @@ class LoraPack:
             raise ValueError("ranks go from 1 to 128")
         self.rows, self.cols, self.adapters = rows, cols, len(adapters)
         self.rank = next(r for r in (16, 32, 64, 128) if r >= max(ranks))
-        self.a = torch.zeros(len(adapters), self.rank, -(-cols // 32) * 32, dtype=torch.bfloat16, device=device)
+        steps = -(-cols // 32)
+        rows_of_a = torch.zeros(len(adapters), self.rank, 32 * steps, dtype=torch.bfloat16, device=device)
         self.b = torch.zeros(len(adapters), rows, self.rank, dtype=torch.bfloat16, device=device)
         for i, (a, b, _) in enumerate(adapters):
-            self.a[i, :ranks[i], :cols] = a
+            rows_of_a[i, :ranks[i], :cols] = a
             self.b[i, :, :ranks[i]] = b
+        # the operand order of bs.h: (adapter, 16 rows, 32 columns, lane group, row, 8 columns)
+        self.a = rows_of_a.view(len(adapters), self.rank // 16, 16, steps, 4, 8).permute(0, 1, 3, 4, 2, 5).contiguous()
         self.ranks = torch.tensor(ranks, dtype=torch.int32, device=device)
         self.factor = torch.tensor([float(s) for _, _, s in adapters], dtype=torch.float32, device=device)
         self.c = L.LoraPack(self.adapters, self.rank, rows, cols, self.a.data_ptr(), self.b.data_ptr(),
