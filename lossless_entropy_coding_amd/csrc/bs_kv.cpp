@@ -83,14 +83,15 @@ bs_status view(const bs_kv_cache* c, bsd::KvView& v) {
 void split_rule(const bsd::KvAttend& a, uint32_t max_len, uint32_t& chunk, uint32_t& splits) {
     int cus = 0;
     if (bsk_device_cus(&cus) != 0 || cus <= 0) cus = 256;
-    const uint64_t rows = (uint64_t)a.max_new * a.group, row_tiles = (rows + 15) / 16;
+    const uint64_t rows = (uint64_t)a.max_new * a.group;
+    const uint64_t block_rows = a.many ? (a.c.wide <= 128 ? 256 : 128) : 16, row_tiles = (rows + block_rows - 1) / block_rows;
     uint64_t tiles = ((uint64_t)max_len + bsd::kKvTile - 1) / bsd::kKvTile;
     if (a.window) {
         const uint64_t span = (uint64_t)a.window + a.max_new + bsd::kKvTile;
         tiles = std::min<uint64_t>(tiles, span / bsd::kKvTile + 1 + ((uint64_t)a.sinks + bsd::kKvTile - 1) / bsd::kKvTile);
     }
     const uint64_t groups = (uint64_t)a.n_seqs * row_tiles * a.c.kv_heads;
-    const uint64_t want = std::max<uint64_t>(1, 4ull * (uint64_t)cus / std::max<uint64_t>(groups, 1));
+    const uint64_t want = std::max<uint64_t>(1, (a.many ? 1ull : 4ull) * (uint64_t)cus / std::max<uint64_t>(groups, 1));
     uint64_t ch = std::max<uint64_t>(8, (tiles + want - 1) / want);
     splits = (uint32_t)std::max<uint64_t>(1, (tiles + ch - 1) / ch);
     if (splits > kGridYZ) {
@@ -150,7 +151,9 @@ bs_status attend_args(const bs_kv_cache* cache, const bs_kv_attend_args* x, bsd:
     a.sinks = x->sinks;
     a.aligned = aligned(x->d_q, 16) && x->q_stride % 8 == 0 && a.c.dim % 8 == 0;
     const uint64_t row_tiles = ((uint64_t)a.max_new * a.group + 15) / 16;
-    if ((uint64_t)a.max_new * a.group > 0x7FFFFFFFull || row_tiles * a.n_seqs > kGridX || (uint64_t)a.n_seqs * a.max_new > kGridX) {
+    a.out8 = aligned(x->d_out, 8) && x->out_stride % 4 == 0 && a.c.dim % 4 == 0;
+    a.many = (uint64_t)a.max_new * a.group >= 64;
+    if ((uint64_t)a.max_new * a.group > 0x7FFFFFFFull || row_tiles * a.n_seqs * a.c.kv_heads > kGridX / 8 || (uint64_t)a.n_seqs * a.max_new > kGridX) {
         set_error("%u sequences of %u new tokens are too many for one call", a.n_seqs, a.max_new);
         return BS_E_INVAL;
     }
@@ -160,7 +163,7 @@ bs_status attend_args(const bs_kv_cache* cache, const bs_kv_attend_args* x, bsd:
 }
 
 uint64_t part_bytes(const bsd::KvAttend& a, uint32_t splits) {
-    return splits > 1 ? 4ull * a.total * a.heads * splits * (a.c.wide + 2) : 0;
+    return splits > 1 ? 4ull * a.total * a.heads * splits * (a.c.wide + 4) : 0;
 }
 
 uint64_t page_work(const bsd::KvView& v, uint64_t n) {

@@ -149,6 +149,65 @@ __device__ __forceinline__ Tiles get_tiles(const KvAttend& a, int32_t lo, int32_
     return t;
 }
 
+// a query's channels 64 x + 16 g + 8 y ..: 8 values, zeros past head_dim
+template <int DW>
+__device__ __forceinline__ void load_q(const KvAttend& a, uint32_t tok, uint32_t qh, uint32_t g, bf16x8 (&q)[DW][2]) {
+    const uint32_t dim = a.c.dim;
+    const uint16_t* qp = a.q + (uint64_t)tok * a.q_stride + (uint64_t)qh * dim;
+#pragma unroll
+    for (uint32_t x = 0; x < DW; x++)
+#pragma unroll
+        for (uint32_t y = 0; y < 2; y++) {
+            const uint32_t d = 64 * x + 16 * g + 8 * y;
+            if (a.aligned && d + 8 <= dim) {
+                q[x][y] = *(const bf16x8*)(qp + d);
+            } else {
+                uint32_t w[4];
+#pragma unroll
+                for (uint32_t e = 0; e < 4; e++) {
+                    const uint32_t u = d + 2 * e < dim ? qp[d + 2 * e] : 0u, v = d + 2 * e + 1 < dim ? qp[d + 2 * e + 1] : 0u;
+                    w[e] = u | v << 16;
+                }
+                q[x][y] = __builtin_bit_cast(bf16x8, v4u{w[0], w[1], w[2], w[3]});
+            }
+        }
+}
+
+// A row's result: channels 16 d + 4 g + e in o[d][e], the maximum and the sum
+// of its exponentials; with splits it goes to the workspace.
+template <int DW>
+__device__ __forceinline__ void finish_row(const KvAttend& a, uint32_t tok, uint32_t qh, uint32_t split, uint32_t g, float top,
+                                           float total, const f32x4 (&o)[4 * DW]) {
+    constexpr uint32_t D = 64 * DW;
+    if (a.splits > 1) {
+        float* pp = a.part + (((uint64_t)tok * a.heads + qh) * a.splits + split) * (D + 4);
+#pragma unroll
+        for (int d = 0; d < 4 * DW; d++) *(f32x4*)(pp + 16 * d + 4 * g) = o[d];
+        if (g == 0) {
+            pp[D] = top;
+            pp[D + 1] = total;
+        }
+        return;
+    }
+    const uint32_t dim = a.c.dim;
+    const float inv = total > 0.f ? 1.f / total : 0.f;
+    uint16_t* op = a.out + (uint64_t)tok * a.out_stride + (uint64_t)qh * dim;
+#pragma unroll
+    for (int d = 0; d < 4 * DW; d++) {
+        const uint32_t ch = 16 * d + 4 * g;
+        const uint32_t lo = pack_bf16(o[d][0] * inv, o[d][1] * inv), hi = pack_bf16(o[d][2] * inv, o[d][3] * inv);
+        if (a.out8 && ch + 4 <= dim) {
+            *(v2u*)(op + ch) = v2u{lo, hi};
+        } else {
+            if (ch < dim) op[ch] = (uint16_t)lo;
+            if (ch + 1 < dim) op[ch + 1] = (uint16_t)(lo >> 16);
+            if (ch + 2 < dim) op[ch + 2] = (uint16_t)hi;
+            if (ch + 3 < dim) op[ch + 3] = (uint16_t)(hi >> 16);
+        }
+    }
+    if (a.lse && g == 0) a.lse[(uint64_t)tok * a.heads + qh] = total > 0.f ? (top + __builtin_amdgcn_logf(total)) * kLn2 : -__builtin_inff();
+}
+
 // grid: (sequences * row tiles, key heads, splits); NW waves.  The bound of
 // two waves per SIMD keeps the kernel within 256 registers and so the
 // products' accumulators out of the AGPRs: with them there, the compiler here
@@ -184,28 +243,8 @@ __global__ __launch_bounds__(64 * NW, 2) void attend_kernel(KvAttend a, uint32_t
     const uint32_t tok = (uint32_t)sq.s0 + r / a.group, qh = head * a.group + r % a.group;
     const int32_t pos = base + (int32_t)(r / a.group);
 
-    // Q: for channels 64 x + 16 g + 8 y ..: 8 values
     bf16x8 q[DW][2];
-    {
-        const uint16_t* qp = a.q + (uint64_t)tok * a.q_stride + (uint64_t)qh * c.dim;
-#pragma unroll
-        for (uint32_t x = 0; x < DW; x++)
-#pragma unroll
-            for (uint32_t y = 0; y < 2; y++) {
-                const uint32_t d = 64 * x + 16 * g + 8 * y;
-                if (a.aligned && d + 8 <= c.dim) {
-                    q[x][y] = *(const bf16x8*)(qp + d);
-                } else {
-                    uint32_t w[4];
-#pragma unroll
-                    for (uint32_t e = 0; e < 4; e++) {
-                        const uint32_t u = d + 2 * e < c.dim ? qp[d + 2 * e] : 0u, v = d + 2 * e + 1 < c.dim ? qp[d + 2 * e + 1] : 0u;
-                        w[e] = u | v << 16;
-                    }
-                    q[x][y] = __builtin_bit_cast(bf16x8, v4u{w[0], w[1], w[2], w[3]});
-                }
-            }
-    }
+    load_q<DW>(a, tok, qh, g, q);
     const float sc = a.softcap > 0.f ? a.qscale : a.qscale * kLog2e;
     const float cap_in = a.softcap > 0.f ? 2.f * kLog2e / a.softcap : 0.f, cap_out = a.softcap * kLog2e;
 
@@ -331,57 +370,309 @@ __global__ __launch_bounds__(64 * NW, 2) void attend_kernel(KvAttend a, uint32_t
         }
     }
     if (wave != 0 || 16 * rt + m >= rows) return;
-    if (a.splits > 1) {
-        float* pp = a.part + (((uint64_t)tok * a.heads + qh) * a.splits + split) * (D + 2);
-        for (int d = 0; d < 4 * DW; d++)
-#pragma unroll
-            for (int e = 0; e < 4; e++) pp[16 * d + 4 * g + e] = o[d][e];
-        if (g == 0) {
-            pp[D] = top;
-            pp[D + 1] = total;
-        }
-        return;
-    }
-    const float inv = total > 0.f ? 1.f / total : 0.f;
-    uint16_t* op = a.out + (uint64_t)tok * a.out_stride + (uint64_t)qh * c.dim;
-#pragma unroll
-    for (int d = 0; d < 4 * DW; d++)
-#pragma unroll
-        for (int e = 0; e < 4; e++) {
-            const uint32_t ch = 16 * d + 4 * g + e;
-            if (ch < c.dim) op[ch] = __builtin_bit_cast(uint16_t, (__bf16)(o[d][e] * inv));
-        }
-    if (a.lse && g == 0) a.lse[(uint64_t)tok * a.heads + qh] = total > 0.f ? (top + __builtin_amdgcn_logf(total)) * kLn2 : -__builtin_inff();
+    finish_row<DW>(a, tok, qh, split, g, top, total, o);
 }
 
-// Joins the splits of one row in order.  grid: (sequences * max_new, heads);
-// 64 threads
+// ---------------------------------------------------------------- many rows
+//
+// From 64 rows on (prompts, long drafts) a workgroup of 8 waves takes 128 NR
+// rows of one key head, 16 NR to a wave, and all of them use one copy of a
+// tile's keys and values: each wave loads an eighth of the next tile while
+// the current one is multiplied, widens it to BF16 once and leaves it in LDS
+// as the operands of the products, 1 KiB to each, so that every read of them
+// is 16 B per lane on end.  Two tiles are in LDS, one barrier per tile.
+//
+// The result is scaled only when a row's maximum has grown by more than 2^8
+// (the exponentials then reach 2^8, as exact in fp32 and BF16 as below 1).
+// The scale of V's page is a power of two and goes into the exponent: with
+// p 2^k in the product, k the page's, the sum of p is that of p 2^k times
+// 2^-k.
+constexpr float kGrow = 8.f;
+
+template <int DW, bool E4M3, int NR>
+__global__ __launch_bounds__(512, 2) void attend_rows_kernel(KvAttend a, uint32_t row_blocks, uint32_t combos) {
+    const KvView& c = a.c;
+    constexpr uint32_t D = 64 * DW, kFrags = 8 * DW;                // 1-KiB operands of a side of a tile
+    __shared__ __attribute__((aligned(16))) uint8_t buf[2][2 * kFrags][1024];
+
+    const uint32_t t = threadIdx.x, lane = t & 63u, m = lane & 15u, g = lane >> 4;
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(t >> 6);
+    // workgroups of one sequence and key head share an XCD's L2 (consecutive
+    // workgroups go to the 8 XCDs in turn), the longest rows first
+    const uint32_t xcd = blockIdx.x & 7u, j = blockIdx.x >> 3;
+    const uint32_t combo = xcd + 8 * (j / row_blocks), rb = row_blocks - 1 - j % row_blocks, split = blockIdx.y;
+    if (combo >= combos) return;
+    const uint32_t seq_i = combo / c.kv_heads, head = combo % c.kv_heads;
+    const Seq sq = get_seq(a, seq_i);
+    if (!sq.ok && t == 0 && split == 0 && c.status) atomicOr(c.status, 4u);
+    const uint32_t rows = (uint32_t)sq.count * a.group, wg0 = 128 * NR * rb;
+    if (wg0 >= rows) return;
+    const int32_t base = sq.len - sq.count;
+    const uint32_t wg1 = min(wg0 + 128 * NR, rows);                 // the workgroup's rows
+    const Tiles tl = get_tiles(a, base + (int32_t)(wg0 / a.group), base + (int32_t)((wg1 - 1) / a.group));
+    const uint32_t i0 = split * a.chunk;
+    if (split > 0 && i0 >= tl.n) return;
+    const uint32_t i1 = a.splits > 1 ? min(tl.n, i0 + a.chunk) : tl.n;
+    const uint32_t end = (uint32_t)(base + (int32_t)((wg1 - 1) / a.group) + 1);   // (only read where tiles exist)
+
+    const uint32_t w0 = wg0 + 16 * NR * wave;                       // the wave's first row
+    int32_t pos[NR];
+    uint32_t tok[NR], qh[NR];
+    bf16x8 q[NR][DW][2];
+#pragma unroll
+    for (uint32_t n = 0; n < NR; n++) {
+        const uint32_t r = min(w0 + 16 * n + m, rows - 1);
+        tok[n] = (uint32_t)sq.s0 + r / a.group;
+        qh[n] = head * a.group + r % a.group;
+        pos[n] = base + (int32_t)(r / a.group);
+        load_q<DW>(a, tok[n], qh[n], g, q[n]);
+    }
+    const bool active = w0 < rows;
+    const int32_t wlo = base + (int32_t)(min(w0, rows - 1) / a.group);
+    const int32_t whi = base + (int32_t)(min(w0 + 16 * NR - 1, rows - 1) / a.group);
+    const bool flip = a.qscale < 0.f;                               // the largest product is then the least
+    const float sc = (a.softcap > 0.f ? 1.f : kLog2e) * fabsf(a.qscale);
+    const float cap_in = a.softcap > 0.f ? 2.f * kLog2e / a.softcap : 0.f, cap_out = a.softcap * kLog2e;
+
+    f32x4 o[NR][4 * DW];
+    float mx[NR], sum[NR];
+#pragma unroll
+    for (uint32_t n = 0; n < NR; n++) {
+#pragma unroll
+        for (int d = 0; d < 4 * DW; d++) o[n][d] = f32x4{0.f, 0.f, 0.f, 0.f};
+        mx[n] = -__builtin_inff();
+        sum[n] = 0.f;
+    }
+    const int32_t* trow = c.table + (uint64_t)(uint32_t)max(sq.row, 0) * c.max_pages;
+    const uint64_t hoff = (uint64_t)head * c.page * c.wide;
+
+    // What a wave stages of a tile: waves 0..3 keys (the 16 tokens of step
+    // `wave`), waves 4..7 values (channel blocks (wave - 4) DW ..).
+    const bool vside = wave >= 4;
+    const uint32_t part = wave & 3u;
+    struct Next {
+        v4u r[DW];
+        uint32_t keep;          // values: tokens of the lane's chunk that count
+    };
+    uint32_t bad = 0;
+    // page of the lane's chunk of tile i (its staged part's, then its own tokens')
+    auto chunk_page = [&](uint32_t i, uint32_t ch, bool& ok) {
+        ok = false;
+        if (i >= i1) return 0u;
+        const uint32_t at = tl.at(i) * kKvTile + 16 * ch;
+        if (at >= end) return 0u;
+        const int32_t p = trow[at >> c.lp];
+        ok = (uint32_t)p < c.n_pages;
+        if (!ok) bad = 1;
+        return ok ? (uint32_t)p : 0u;
+    };
+    auto stage_load = [&](uint32_t i, Next& x) {
+        x.keep = 0;
+        if (i >= i1) return;
+        const uint32_t tile0 = tl.at(i) * kKvTile;
+        bool ok;
+        if (vside) {
+            const uint32_t cv = tile0 + 16 * g;
+            const uint32_t p = chunk_page(i, g, ok);
+            x.keep = ok ? min(end - cv, 16u) : 0u;
+            const uint8_t* vp = a.v + (uint64_t)p * c.side_bytes + hoff + (uint64_t)(16 * part * DW + m) * c.page + (cv & (c.page - 1));
+#pragma unroll
+            for (uint32_t d = 0; d < DW; d++) x.r[d] = *(const v4u*)(vp + (uint64_t)(16 * d) * c.page);
+        } else {
+            const uint32_t ck = tile0 + 16 * (m >> 2);
+            const uint32_t p = chunk_page(i, m >> 2, ok);
+            const uint8_t* kp = a.k + (uint64_t)p * c.side_bytes + hoff + (uint64_t)((ck + 4 * part + (m & 3u)) & (c.page - 1)) * D + 16 * g;
+#pragma unroll
+            for (uint32_t d = 0; d < DW; d++) x.r[d] = *(const v4u*)(kp + 64 * d);
+        }
+    };
+    auto stage_store = [&](uint32_t i, Next& x) {
+        if (i >= i1) return;
+        if (vside && x.keep < 16) {
+#pragma unroll
+            for (uint32_t d = 0; d < DW; d++)
+#pragma unroll
+                for (int w = 0; w < 4; w++) {
+                    const int32_t nb = (int32_t)x.keep - 4 * w;
+                    x.r[d][w] &= nb >= 4 ? ~0u : nb <= 0 ? 0u : (1u << (8 * nb)) - 1u;
+                }
+        }
+        // operand 2 (part DW + d) + half of its side
+        uint8_t* to = buf[(i - i0) & 1u][(vside ? kFrags : 0) + 2 * part * DW] + 16 * lane;
+#pragma unroll
+        for (uint32_t d = 0; d < DW; d++) {
+            *(bf16x8*)(to + 2048 * d) = widen8<E4M3>(x.r[d].x, x.r[d].y);
+            *(bf16x8*)(to + 2048 * d + 1024) = widen8<E4M3>(x.r[d].z, x.r[d].w);
+        }
+    };
+
+    Next nx;
+    stage_load(i0, nx);
+    stage_store(i0, nx);
+    stage_load(i0 + 1, nx);
+    // scales of the lane's own 16 tokens, a tile ahead
+    bool oks;
+    uint32_t ps = chunk_page(i0, g, oks);
+    float ks1 = 1.f, vs1 = 1.f;
+    if (i0 < i1) {
+        const float* sp = a.scale + ((uint64_t)ps * c.kv_heads + head) * 2;
+        ks1 = sp[0];
+        vs1 = sp[1];
+    }
+    __syncthreads();
+    for (uint32_t i = i0; i < i1; i++) {
+        stage_store(i + 1, nx);
+        stage_load(i + 2, nx);
+        const uint32_t tile0 = tl.at(i) * kKvTile;
+        const bool okv = oks;
+        // the scales are powers of two, so log2 of V's is exact
+        // (at least 2^-120: a masked logit times it stays -infinity)
+        const float ks = fmaxf(ks1 * sc, 0x1p-120f), kexp = okv ? (float)((int32_t)(__builtin_bit_cast(uint32_t, vs1) >> 23) - 127) : 0.f;
+        ps = chunk_page(i + 1, g, oks);
+        if (i + 1 < i1) {
+            const float* sp = a.scale + ((uint64_t)ps * c.kv_heads + head) * 2;
+            ks1 = sp[0];
+            vs1 = sp[1];
+        }
+        // does the wave see any of the tile, or all of it?
+        bool any = active && (int32_t)tile0 <= whi;
+        bool all = (int32_t)(tile0 + kKvTile - 1) <= wlo;
+        if (a.window) {
+            any = any && ((int64_t)tile0 + kKvTile - 1 > (int64_t)wlo - a.window || tile0 < a.sinks);
+            all = all && ((int64_t)tile0 > (int64_t)whi - a.window || tile0 + kKvTile <= a.sinks);
+        }
+        all = all && __builtin_amdgcn_ballot_w64(!okv) == 0;
+        if (any) {
+            const uint8_t* kb = buf[(i - i0) & 1u][0] + 16 * lane;
+            const uint8_t* vb = buf[(i - i0) & 1u][kFrags] + 16 * lane;
+            f32x4 s[NR][4];
+#pragma unroll
+            for (uint32_t h = 0; h < 4; h++) {
+#pragma unroll
+                for (uint32_t n = 0; n < NR; n++) s[n][h] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (uint32_t x = 0; x < 2 * DW; x++) {
+                    const bf16x8 kf = *(const bf16x8*)(kb + 1024 * (2 * DW * h + x));
+#pragma unroll
+                    for (uint32_t n = 0; n < NR; n++)
+                        s[n][h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, q[n][x >> 1][x & 1], s[n][h], 0, 0, 0);
+                }
+            }
+            bf16x8 pb[NR][2];
+#pragma unroll
+            for (uint32_t n = 0; n < NR; n++) {
+                float p[16], mul = ks;
+#pragma unroll
+                for (uint32_t e = 0; e < 16; e++) p[e] = s[n][e >> 2][e & 3];
+                if (flip) {
+#pragma unroll
+                    for (uint32_t e = 0; e < 16; e++) p[e] = -p[e];
+                }
+                if (a.softcap > 0.f) {
+                    const float in = ks * cap_in;
+#pragma unroll
+                    for (uint32_t e = 0; e < 16; e++)
+                        p[e] = cap_out - 2.f * cap_out * __builtin_amdgcn_rcpf(exp2_fast(p[e] * in) + 1.f);
+                    mul = 1.f;
+                }
+                if (!all) {
+#pragma unroll
+                    for (uint32_t e = 0; e < 16; e++) {
+                        const int32_t tk = (int32_t)(tile0 + 16 * g + e);
+                        const bool seen = okv && tk <= pos[n] &&
+                                          (a.window == 0 || (int64_t)tk > (int64_t)pos[n] - (int64_t)a.window || (uint32_t)tk < a.sinks);
+                        p[e] = seen ? p[e] : -__builtin_inff();
+                    }
+                }
+                float top = p[0];
+#pragma unroll
+                for (uint32_t e = 1; e < 16; e++) top = fmaxf(top, p[e]);
+                top = max_groups(top * mul);
+                // mx: what the exponentials are taken against
+                if (__builtin_amdgcn_ballot_w64(top > mx[n] + kGrow) != 0) {
+                    const float now = fmaxf(top, mx[n]), sub = now == -__builtin_inff() ? 0.f : now;
+                    const float alpha = exp2_fast(mx[n] - sub);
+                    mx[n] = now;
+                    sum[n] *= alpha;
+#pragma unroll
+                    for (int d = 0; d < 4 * DW; d++) o[n][d] *= alpha;
+                }
+                const float sub = (mx[n] == -__builtin_inff() ? 0.f : mx[n]) - kexp;
+                float tot = 0.f;
+#pragma unroll
+                for (uint32_t e = 0; e < 16; e++) {
+                    p[e] = exp2_fast(p[e] * mul - sub);
+                    tot += p[e];
+                }
+                sum[n] += tot * exp2_fast(-kexp);
+#pragma unroll
+                for (int y = 0; y < 2; y++)
+                    pb[n][y] = __builtin_bit_cast(bf16x8, v4u{pack_bf16(p[8 * y], p[8 * y + 1]), pack_bf16(p[8 * y + 2], p[8 * y + 3]),
+                                                              pack_bf16(p[8 * y + 4], p[8 * y + 5]), pack_bf16(p[8 * y + 6], p[8 * y + 7])});
+            }
+#pragma unroll
+            for (int d = 0; d < 4 * DW; d++)
+#pragma unroll
+                for (int y = 0; y < 2; y++) {
+                    const bf16x8 vf = *(const bf16x8*)(vb + 1024 * (2 * d + y));
+#pragma unroll
+                    for (uint32_t n = 0; n < NR; n++)
+                        o[n][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, pb[n][y], o[n][d], 0, 0, 0);
+                }
+        }
+        __syncthreads();
+    }
+    if (bad && c.status) atomicOr(c.status, 4u);
+    if (!active) return;
+#pragma unroll
+    for (uint32_t n = 0; n < NR; n++) {
+        const float total = sum_groups(sum[n]);
+        if (w0 + 16 * n + m >= rows) continue;
+        finish_row<DW>(a, tok[n], qh[n], split, g, mx[n], total, o[n]);
+    }
+}
+
+// Joins the splits of one row in order: a wave per row, its lanes over the
+// channels and the splits' loads 8 at a time.  grid: (sequences * max_new,
+// heads); block_rows: rows that share a split's tiles.
 template <int DW>
-__global__ __launch_bounds__(64) void join_kernel(KvAttend a) {
+__global__ __launch_bounds__(64) void join_kernel(KvAttend a, uint32_t block_rows) {
     constexpr uint32_t D = 64 * DW;
     const uint32_t seq_i = blockIdx.x / a.max_new, j = blockIdx.x % a.max_new, qh = blockIdx.y, lane = threadIdx.x;
     const Seq sq = get_seq(a, seq_i);
     if (j >= (uint32_t)sq.count) return;
-    // the splits that the row's tile of 16 rows has
-    const uint32_t rt = (j * a.group + qh % a.group) / 16;
+    const uint32_t r0 = (j * a.group + qh % a.group) / block_rows * block_rows;
     const int32_t base = sq.len - sq.count;
-    const uint32_t r_last = min(16 * rt + 15, (uint32_t)sq.count * a.group - 1);
-    const Tiles tl = get_tiles(a, base + (int32_t)(16 * rt / a.group), base + (int32_t)(r_last / a.group));
+    const uint32_t r1 = min(r0 + block_rows, (uint32_t)sq.count * a.group) - 1;
+    const Tiles tl = get_tiles(a, base + (int32_t)(r0 / a.group), base + (int32_t)(r1 / a.group));
     const uint32_t n = max(1u, (tl.n + a.chunk - 1) / a.chunk);
     const uint32_t tok = (uint32_t)sq.s0 + j;
-    const float* pp = a.part + ((uint64_t)tok * a.heads + qh) * a.splits * (D + 2);
+    const float* pp = a.part + ((uint64_t)tok * a.heads + qh) * a.splits * (D + 4);
     float top = -__builtin_inff();
-    for (uint32_t s = 0; s < n; s++) top = fmaxf(top, pp[s * (D + 2) + D]);
+    for (uint32_t s = lane; s < n; s += 64) top = fmaxf(top, pp[s * (D + 4) + D]);
+#pragma unroll
+    for (int k = 32; k; k >>= 1) top = fmaxf(top, __shfl_xor(top, k));
     const float sub = top == -__builtin_inff() ? 0.f : top;
     float total = 0.f, o[DW];
 #pragma unroll
     for (int x = 0; x < DW; x++) o[x] = 0.f;
-    for (uint32_t s = 0; s < n; s++) {
-        const float* ps = pp + s * (D + 2);
-        const float f = exp2_fast(ps[D] - sub);
-        total += f * ps[D + 1];
+    for (uint32_t s0 = 0; s0 < n; s0 += 8) {
+        float v[8][DW], f[8], l[8];
 #pragma unroll
-        for (int x = 0; x < DW; x++) o[x] += f * ps[64 * x + lane];
+        for (uint32_t u = 0; u < 8; u++) {
+            const float* ps = pp + min(s0 + u, n - 1) * (D + 4);
+            f[u] = ps[D];
+            l[u] = ps[D + 1];
+#pragma unroll
+            for (int x = 0; x < DW; x++) v[u][x] = ps[64 * x + lane];
+        }
+#pragma unroll
+        for (uint32_t u = 0; u < 8; u++) {
+            const float w = s0 + u < n ? exp2_fast(f[u] - sub) : 0.f;
+            total += w * l[u];
+#pragma unroll
+            for (int x = 0; x < DW; x++) o[x] += w * v[u][x];
+        }
     }
     const float inv = total > 0.f ? 1.f / total : 0.f;
     uint16_t* op = a.out + (uint64_t)tok * a.out_stride + (uint64_t)qh * a.c.dim;
@@ -391,13 +682,28 @@ __global__ __launch_bounds__(64) void join_kernel(KvAttend a) {
     if (a.lse && lane == 0) a.lse[(uint64_t)tok * a.heads + qh] = total > 0.f ? (top + __builtin_amdgcn_logf(total)) * kLn2 : -__builtin_inff();
 }
 
+// rows of a workgroup of attend_rows_kernel: two row tiles to a wave where
+// the accumulators leave room (head_dim up to 128)
+template <int DW>
+constexpr int kRowTiles = DW <= 2 ? 2 : 1;
+
 template <int DW>
 int launch(const KvAttend& a, hipStream_t st) {
+    if (a.many) {
+        constexpr int NR = kRowTiles<DW>;
+        const uint32_t row_blocks = (uint32_t)(((uint64_t)a.max_new * a.group + 128 * NR - 1) / (128 * NR));
+        const uint32_t combos = a.n_seqs * a.c.kv_heads;
+        const dim3 grid((combos + 7) / 8 * 8 * row_blocks, a.splits);
+        if (a.c.type == 1) hipLaunchKernelGGL((attend_rows_kernel<DW, true, NR>), grid, dim3(512), 0, st, a, row_blocks, combos);
+        else hipLaunchKernelGGL((attend_rows_kernel<DW, false, NR>), grid, dim3(512), 0, st, a, row_blocks, combos);
+        if (a.splits > 1) hipLaunchKernelGGL(join_kernel<DW>, dim3(a.n_seqs * a.max_new, a.heads), dim3(64), 0, st, a, 128u * NR);
+        return (int)hipGetLastError();
+    }
     const uint32_t row_tiles = (a.max_new * a.group + 15) / 16;
     const dim3 grid(a.n_seqs * row_tiles, a.c.kv_heads, a.splits);
     if (a.c.type == 1) hipLaunchKernelGGL((attend_kernel<DW, true, 4>), grid, dim3(256), 0, st, a, row_tiles);
     else hipLaunchKernelGGL((attend_kernel<DW, false, 4>), grid, dim3(256), 0, st, a, row_tiles);
-    if (a.splits > 1) hipLaunchKernelGGL(join_kernel<DW>, dim3(a.n_seqs * a.max_new, a.heads), dim3(64), 0, st, a);
+    if (a.splits > 1) hipLaunchKernelGGL(join_kernel<DW>, dim3(a.n_seqs * a.max_new, a.heads), dim3(64), 0, st, a, 16u);
     return (int)hipGetLastError();
 }
 
