@@ -255,6 +255,8 @@ bs_status bs_kv_append_async(const bs_kv_cache* cache, uint32_t layer, uint32_t 
     a.k_stride = k_stride;
     a.v_stride = v_stride;
     a.f32 = dtype == BS_T_FP32;
+    const uint64_t unit = 16 / el;
+    a.vec = aligned(d_k, 16) && aligned(d_v, 16) && k_stride % unit == 0 && v_stride % unit == 0 && a.c.dim % 8 == 0;
     return launched(bsk_kv_append(&a, stream), "append");
 }
 

@@ -16,6 +16,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "bs_kv_device.h"
 
@@ -24,6 +25,8 @@ using namespace bsd;
 namespace {
 
 typedef unsigned int v4u __attribute__((ext_vector_type(4)));
+typedef unsigned int v2u __attribute__((ext_vector_type(2)));
+typedef float v4f __attribute__((ext_vector_type(4)));
 
 enum : uint32_t {
     kStPages = 1, kStRow = 2, kStId = 4, kStBusy = 8, kStValue = 16, kStCount = 32
@@ -66,18 +69,61 @@ __device__ __forceinline__ float of_code(uint32_t c, bool e4m3) {
     return (float)(int)(int8_t)(c & 0xFFu);
 }
 
-// grid: (pages a sequence can touch, 2 kv_heads, sequences)
+// four codes times f (a power of two, at most 1), rounded again; bytes past
+// the first n stay as they are
 template <bool E4M3>
+__device__ __forceinline__ uint32_t again4(uint32_t c, float f, int32_t n) {
+    if (n <= 0) return c;
+    uint32_t r = 0;
+#pragma unroll
+    for (int b = 0; b < 4; b++) r |= to_code(of_code(c >> (8 * b), E4M3) * f, E4M3) << (8 * b);
+    const uint32_t keep = n >= 4 ? 0u : ~0u << (8 * n);
+    return (r & ~keep) | (c & keep);
+}
+
+// 8 values of the input from element i
+template <bool F32>
+__device__ __forceinline__ void load8(const void* x, uint64_t i, float* v) {
+    if (F32) {
+        const v4f a = *(const v4f*)((const float*)x + i), b = *(const v4f*)((const float*)x + i + 4);
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+            v[e] = a[e];
+            v[4 + e] = b[e];
+        }
+    } else {
+        const v4u a = *(const v4u*)((const uint16_t*)x + i);
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+            const uint32_t w = a[e];
+            v[2 * e] = __builtin_bit_cast(float, w << 16);
+            v[2 * e + 1] = __builtin_bit_cast(float, w & 0xFFFF0000u);
+        }
+    }
+}
+
+template <bool E4M3>
+__device__ __forceinline__ uint32_t code_of(float v, float inv) {
+    return to_code(v != v ? 0.f : v * inv, E4M3);
+}
+
+// grid: (pages a sequence can touch, 2 kv_heads, sequences).  Two passes over
+// the page's new tokens: the largest magnitude, then the codes (the second
+// finds them in the L2).  VEC: rows of the input can be read 16 B at a time;
+// a thread then takes 8 channels of a token (keys) or of four tokens on end
+// (values: its 8 x 4 codes are stored as 4 tokens' bytes per channel, and
+// threads on end fill a channel's row).
+template <bool E4M3, bool VEC, bool F32>
 __global__ __launch_bounds__(256) void append_kernel(KvAppend a) {
     const KvView& c = a.c;
     const uint32_t t = threadIdx.x, seq_i = blockIdx.z, head = blockIdx.y >> 1, side = blockIdx.y & 1u;
     const int32_t row = a.seqs[seq_i];
+    const int32_t s0 = a.starts ? a.starts[seq_i] : (int32_t)seq_i;
+    const int32_t s1 = a.starts ? a.starts[seq_i + 1] : (int32_t)seq_i + 1;
     if (row < 0 || (uint32_t)row >= c.max_seqs) {
         if (t == 0) flag(c.status, kStId);
         return;
     }
-    const int32_t s0 = a.starts ? a.starts[seq_i] : (int32_t)seq_i;
-    const int32_t s1 = a.starts ? a.starts[seq_i + 1] : (int32_t)seq_i + 1;
     const int32_t len = c.lens[row];
     if (s0 < 0 || s1 < s0 || (uint32_t)s1 > a.total || s1 - s0 > len || (uint32_t)(s1 - s0) > a.max_new) {
         if (t == 0) flag(c.status, kStId);
@@ -98,27 +144,42 @@ __global__ __launch_bounds__(256) void append_kernel(KvAppend a) {
     }
     const uint32_t lo = max(begin, pg << c.lp) - (pg << c.lp);                 // the page's new slots
     const uint32_t hi = min((uint32_t)len - (pg << c.lp), c.page);
-    const uint64_t tok0 = (uint64_t)s0 + ((pg << c.lp) + lo - begin);          // the first of them in the input
     const void* x = side ? a.xv : a.xk;
     const uint64_t xs = side ? a.v_stride : a.k_stride;
-    const uint32_t nt = hi - lo;
+    // the input's element of slot 0, channel 0 of the page (slots below lo are not read)
+    const int64_t x0 = ((int64_t)s0 + (int64_t)(pg << c.lp) - (int64_t)begin) * (int64_t)xs + (int64_t)head * c.dim;
+    const uint32_t nt = hi - lo, d8 = c.dim / 8;
+    float* sp = c.scale + (((uint64_t)a.layer * c.n_pages + (uint32_t)pid) * c.kv_heads + head) * 2 + side;
+    const float old = lo ? *sp : 0.f;
 
     // the largest finite magnitude
     float m = 0.f;
     bool odd = false;
-    for (uint32_t i = t; i < nt * c.dim; i += 256) {
-        const uint32_t tk = i / c.dim, d = i - tk * c.dim;
-        const float v = fabsf(load_x(x, (tok0 + tk) * xs + (uint64_t)head * c.dim + d, a.f32));
-        if (v < __builtin_inff()) m = fmaxf(m, v);
-        else odd = true;
+    if (VEC) {
+        for (uint32_t i = t; i < nt * d8; i += 256) {
+            const uint32_t tk = i / d8, g = i - tk * d8;
+            float v[8];
+            load8<F32>(x, (uint64_t)(x0 + (int64_t)((uint64_t)(lo + tk) * xs + 8 * g)), v);
+#pragma unroll
+            for (int e = 0; e < 8; e++) {
+                const float u = fabsf(v[e]);
+                if (u < __builtin_inff()) m = fmaxf(m, u);
+                else odd = true;
+            }
+        }
+    } else {
+        for (uint32_t i = t; i < nt * c.dim; i += 256) {
+            const uint32_t tk = i / c.dim, d = i - tk * c.dim;
+            const float v = fabsf(load_x(x, (uint64_t)(x0 + (int64_t)((uint64_t)(lo + tk) * xs + d)), F32));
+            if (v < __builtin_inff()) m = fmaxf(m, v);
+            else odd = true;
+        }
     }
     if (odd) flag(c.status, kStValue);
     __shared__ float red[4];
 #pragma unroll
     for (int s = 32; s; s >>= 1) m = fmaxf(m, __shfl_xor(m, s));
     if ((t & 63u) == 0) red[t >> 6] = m;
-    float* sp = c.scale + (((uint64_t)a.layer * c.n_pages + (uint32_t)pid) * c.kv_heads + head) * 2 + side;
-    const float old = lo ? *sp : 0.f;
     __syncthreads();
     m = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
     const float now = fmaxf(old, pow2(need_exp(m, E4M3)));
@@ -127,20 +188,66 @@ __global__ __launch_bounds__(256) void append_kernel(KvAppend a) {
                     (uint64_t)head * c.page * c.wide;
     if (lo && old < now) {                                                     // older tokens: rounded again
         const float f = old * inv;
-        for (uint32_t i = t; i < lo * c.wide; i += 256) {
-            const uint32_t d = side ? i / lo : i % c.wide, s = side ? i - d * lo : i / c.wide;
-            uint8_t* p = base + (side ? d * c.page + s : s * c.wide + d);
-            *p = (uint8_t)to_code(of_code(*p, E4M3) * f, E4M3);
+        // 16 B at a time: lo rows of keys on end; of each channel of values the chunks that begin below lo
+        const uint32_t per = side ? (lo + 15) / 16 : 0, n = side ? c.wide * per : lo * c.wide / 16;
+        for (uint32_t i = t; i < n; i += 256) {
+            const uint32_t ch = side ? i / per : 0, q = side ? i - ch * per : 0;
+            v4u* p = (v4u*)(base + (side ? ch * c.page + 16 * q : 16 * i));
+            const int32_t keep = side ? (int32_t)(lo - 16 * q) : 16;
+            v4u w = *p;
+#pragma unroll
+            for (int e = 0; e < 4; e++) w[e] = again4<E4M3>(w[e], f, keep - 4 * e);
+            *p = w;
         }
+        __syncthreads();                                                       // before new tokens of the same chunks
     }
-    for (uint32_t i = t; i < nt * c.wide; i += 256) {
-        const uint32_t d = side ? i / nt : i % c.wide, s = side ? i - d * nt : i / c.wide;
-        float v = 0.f;
-        if (d < c.dim) {
-            v = load_x(x, (tok0 + s) * xs + (uint64_t)head * c.dim + d, a.f32);
-            v = v != v ? 0.f : v * inv;
+    if (VEC && side == 0) {
+        const uint32_t w8 = c.wide / 8;
+        for (uint32_t i = t; i < nt * w8; i += 256) {
+            const uint32_t tk = i / w8, g = i - tk * w8;
+            uint32_t r[2] = {0u, 0u};
+            if (g < d8) {
+                float v[8];
+                load8<F32>(x, (uint64_t)(x0 + (int64_t)((uint64_t)(lo + tk) * xs + 8 * g)), v);
+#pragma unroll
+                for (int e = 0; e < 8; e++) r[e >> 2] |= code_of<E4M3>(v[e], inv) << (8 * (e & 3));
+            }
+            *(v2u*)(base + (lo + tk) * c.wide + 8 * g) = v2u{r[0], r[1]};
         }
-        base[side ? d * c.page + lo + s : (lo + s) * c.wide + d] = (uint8_t)to_code(v, E4M3);
+    } else if (VEC) {
+        const uint32_t q0 = lo / 4, nq = (hi + 3) / 4 - q0;                    // quads of slots
+        for (uint32_t i = t; i < nq * (c.wide / 8); i += 256) {
+            const uint32_t g = i / nq, q = q0 + (i - g * nq);
+            uint32_t r[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+#pragma unroll
+            for (uint32_t k = 0; k < 4; k++) {
+                const uint32_t slot = 4 * q + k;
+                if (g < d8 && slot >= lo && slot < hi) {
+                    float v[8];
+                    load8<F32>(x, (uint64_t)(x0 + (int64_t)((uint64_t)slot * xs + 8 * g)), v);
+#pragma unroll
+                    for (int e = 0; e < 8; e++) r[e] |= code_of<E4M3>(v[e], inv) << (8 * k);
+                }
+            }
+            uint8_t* p = base + 8 * g * c.page + 4 * q;
+            if (4 * q >= lo && 4 * q + 4 <= hi) {
+#pragma unroll
+                for (int e = 0; e < 8; e++) *(uint32_t*)(p + e * c.page) = r[e];
+            } else {
+                for (uint32_t k = 0; k < 4; k++)
+                    if (4 * q + k >= lo && 4 * q + k < hi) {
+#pragma unroll
+                        for (int e = 0; e < 8; e++) p[e * c.page + k] = (uint8_t)(r[e] >> (8 * k));
+                    }
+            }
+        }
+    } else {
+        for (uint32_t i = t; i < nt * c.wide; i += 256) {
+            const uint32_t d = side ? i / nt : i % c.wide, s = lo + (side ? i - d * nt : i / c.wide);
+            uint32_t r = 0;
+            if (d < c.dim) r = code_of<E4M3>(load_x(x, (uint64_t)(x0 + (int64_t)((uint64_t)s * xs + d)), F32), inv);
+            base[side ? d * c.page + s : s * c.wide + d] = (uint8_t)r;
+        }
     }
     if (t == 0) *sp = now;
 }
@@ -492,8 +599,16 @@ uint32_t copy_parts(const KvView& c) {
 extern "C" int bsk_kv_append(const KvAppend* a, void* stream) {
     const uint32_t touch = (a->max_new + 2 * a->c.page - 2) >> a->c.lp;
     const dim3 grid(touch, 2 * a->c.kv_heads, a->n_seqs);
-    if (a->c.type == 1) hipLaunchKernelGGL(append_kernel<true>, grid, dim3(256), 0, (hipStream_t)stream, *a);
-    else hipLaunchKernelGGL(append_kernel<false>, grid, dim3(256), 0, (hipStream_t)stream, *a);
+    hipStream_t st = (hipStream_t)stream;
+    auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(256), 0, st, *a); };
+    auto typed = [&](auto vec, auto f32) {
+        if (a->c.type == 1) go(append_kernel<true, decltype(vec)::value, decltype(f32)::value>);
+        else go(append_kernel<false, decltype(vec)::value, decltype(f32)::value>);
+    };
+    if (a->vec && a->f32) typed(std::true_type{}, std::true_type{});
+    else if (a->vec) typed(std::true_type{}, std::false_type{});
+    else if (a->f32) typed(std::false_type{}, std::true_type{});
+    else typed(std::false_type{}, std::false_type{});
     return (int)hipGetLastError();
 }
 

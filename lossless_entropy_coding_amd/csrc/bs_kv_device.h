@@ -32,6 +32,7 @@ struct KvAppend {
     const void* xv;
     uint64_t k_stride, v_stride;   // elements between tokens
     int f32;                    // inputs in fp32 (else BF16)
+    int vec;                    // 8 channels of a token can be read 16 B at a time
 };
 
 struct KvAttend {
