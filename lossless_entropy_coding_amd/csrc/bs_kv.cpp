@@ -13,6 +13,10 @@ using namespace bs;
 
 namespace {
 
+#ifndef BS_KV_PER
+#define BS_KV_PER 4
+#endif
+
 constexpr uint64_t kGridX = 0x7FFFFFFFull, kGridYZ = 65535;
 
 bs_status launched(int e, const char* what) {
@@ -77,10 +81,9 @@ bs_status view(const bs_kv_cache* c, bsd::KvView& v) {
     return BS_OK;
 }
 
-// The tiles that a split takes and how many splits there are.  One split
-// where the workgroups of whole rows fill the GPU; else as many as make
-// about 4 workgroups of 4 waves per CU, with 2 tiles or more to a wave.
-void split_rule(const bsd::KvAttend& a, uint32_t max_len, uint32_t& chunk, uint32_t& splits) {
+// The tiles that a split takes, how many splits there are, and the waves of a
+// workgroup.
+void split_rule(bsd::KvAttend& a, uint32_t max_len, uint32_t& chunk, uint32_t& splits) {
     int cus = 0;
     if (bsk_device_cus(&cus) != 0 || cus <= 0) cus = 256;
     const uint64_t rows = (uint64_t)a.max_new * a.group;
@@ -90,15 +93,20 @@ void split_rule(const bsd::KvAttend& a, uint32_t max_len, uint32_t& chunk, uint3
         const uint64_t span = (uint64_t)a.window + a.max_new + bsd::kKvTile;
         tiles = std::min<uint64_t>(tiles, span / bsd::kKvTile + 1 + ((uint64_t)a.sinks + bsd::kKvTile - 1) / bsd::kKvTile);
     }
-    const uint64_t groups = (uint64_t)a.n_seqs * row_tiles * a.c.kv_heads;
-    const uint64_t want = std::max<uint64_t>(1, (a.many ? 1ull : 4ull) * (uint64_t)cus / std::max<uint64_t>(groups, 1));
-    uint64_t ch = std::max<uint64_t>(8, (tiles + want - 1) / want);
+    const uint64_t groups = std::max<uint64_t>(1, (uint64_t)a.n_seqs * row_tiles * a.c.kv_heads);
+    // workgroups per CU that are aimed at, and the fewest tiles of one: a
+    // split costs a pass through the workspace and a second launch
+    const uint64_t per = a.many ? 1 : BS_KV_PER, least = a.many ? 8 : 16;
+    const uint64_t want = std::max<uint64_t>(1, per * (uint64_t)cus / groups);
+    uint64_t ch = std::max<uint64_t>(least, (tiles + want - 1) / want);
     splits = (uint32_t)std::max<uint64_t>(1, (tiles + ch - 1) / ch);
     if (splits > kGridYZ) {
         ch = (tiles + kGridYZ - 1) / kGridYZ;
         splits = (uint32_t)((tiles + ch - 1) / ch);
     }
     chunk = (uint32_t)ch;
+    // 8 waves where the workgroups are too few to fill the CUs by themselves
+    a.waves = groups * splits <= (uint64_t)cus ? 8 : 4;
 }
 
 bs_status attend_args(const bs_kv_cache* cache, const bs_kv_attend_args* x, bsd::KvAttend& a, uint32_t& chunk,

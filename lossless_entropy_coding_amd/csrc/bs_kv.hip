@@ -137,11 +137,7 @@ __global__ __launch_bounds__(256) void append_kernel(KvAppend a) {
         if (t == 0) flag(c.status, kStRow);
         return;
     }
-    const int32_t pid = c.table[(uint64_t)row * c.max_pages + pg];
-    if (pid < 0 || (uint32_t)pid >= c.n_pages) {
-        if (t == 0) flag(c.status, kStId);
-        return;
-    }
+    const int32_t pid = c.table[(uint64_t)row * c.max_pages + pg];             // looked at after the first pass
     const uint32_t lo = max(begin, pg << c.lp) - (pg << c.lp);                 // the page's new slots
     const uint32_t hi = min((uint32_t)len - (pg << c.lp), c.page);
     const void* x = side ? a.xv : a.xk;
@@ -149,8 +145,6 @@ __global__ __launch_bounds__(256) void append_kernel(KvAppend a) {
     // the input's element of slot 0, channel 0 of the page (slots below lo are not read)
     const int64_t x0 = ((int64_t)s0 + (int64_t)(pg << c.lp) - (int64_t)begin) * (int64_t)xs + (int64_t)head * c.dim;
     const uint32_t nt = hi - lo, d8 = c.dim / 8;
-    float* sp = c.scale + (((uint64_t)a.layer * c.n_pages + (uint32_t)pid) * c.kv_heads + head) * 2 + side;
-    const float old = lo ? *sp : 0.f;
 
     // the largest finite magnitude
     float m = 0.f;
@@ -176,6 +170,12 @@ __global__ __launch_bounds__(256) void append_kernel(KvAppend a) {
         }
     }
     if (odd) flag(c.status, kStValue);
+    if (pid < 0 || (uint32_t)pid >= c.n_pages) {
+        if (t == 0) flag(c.status, kStId);
+        return;
+    }
+    float* sp = c.scale + (((uint64_t)a.layer * c.n_pages + (uint32_t)pid) * c.kv_heads + head) * 2 + side;
+    const float old = lo ? *sp : 0.f;
     __shared__ float red[4];
 #pragma unroll
     for (int s = 32; s; s >>= 1) m = fmaxf(m, __shfl_xor(m, s));

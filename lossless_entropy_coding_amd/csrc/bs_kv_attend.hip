@@ -149,41 +149,45 @@ __device__ __forceinline__ Tiles get_tiles(const KvAttend& a, int32_t lo, int32_
     return t;
 }
 
-// a query's channels 64 x + 16 g + 8 y ..: 8 values, zeros past head_dim
+// a query's channels 64 x + 16 g + 8 y ..: 8 values, zeros past head_dim.
+// Every load goes out at once, from a place inside the row.
 template <int DW>
 __device__ __forceinline__ void load_q(const KvAttend& a, uint32_t tok, uint32_t qh, uint32_t g, bf16x8 (&q)[DW][2]) {
     const uint32_t dim = a.c.dim;
     const uint16_t* qp = a.q + (uint64_t)tok * a.q_stride + (uint64_t)qh * dim;
+    if (a.aligned) {                                                // dim is a multiple of 8
+        v4u w[2 * DW];
 #pragma unroll
-    for (uint32_t x = 0; x < DW; x++)
+        for (uint32_t x = 0; x < 2 * DW; x++) w[x] = *(const v4u*)(qp + min(64 * (x >> 1) + 16 * g + 8 * (x & 1u), dim - 8));
 #pragma unroll
-        for (uint32_t y = 0; y < 2; y++) {
-            const uint32_t d = 64 * x + 16 * g + 8 * y;
-            if (a.aligned && d + 8 <= dim) {
-                q[x][y] = *(const bf16x8*)(qp + d);
-            } else {
-                uint32_t w[4];
-#pragma unroll
-                for (uint32_t e = 0; e < 4; e++) {
-                    const uint32_t u = d + 2 * e < dim ? qp[d + 2 * e] : 0u, v = d + 2 * e + 1 < dim ? qp[d + 2 * e + 1] : 0u;
-                    w[e] = u | v << 16;
-                }
-                q[x][y] = __builtin_bit_cast(bf16x8, v4u{w[0], w[1], w[2], w[3]});
-            }
+        for (uint32_t x = 0; x < 2 * DW; x++) {
+            const bool in = 64 * (x >> 1) + 16 * g + 8 * (x & 1u) < dim;
+            q[x >> 1][x & 1u] = __builtin_bit_cast(bf16x8, v4u{in ? w[x].x : 0u, in ? w[x].y : 0u, in ? w[x].z : 0u, in ? w[x].w : 0u});
         }
+        return;
+    }
+#pragma unroll
+    for (uint32_t x = 0; x < 2 * DW; x++) {
+        uint32_t u[8];
+        const uint32_t d = 64 * (x >> 1) + 16 * g + 8 * (x & 1u);
+#pragma unroll
+        for (uint32_t e = 0; e < 8; e++) u[e] = qp[min(d + e, dim - 1)];
+#pragma unroll
+        for (uint32_t e = 0; e < 8; e++) u[e] = d + e < dim ? u[e] : 0u;
+        q[x >> 1][x & 1u] = __builtin_bit_cast(bf16x8, v4u{u[0] | u[1] << 16, u[2] | u[3] << 16, u[4] | u[5] << 16, u[6] | u[7] << 16});
+    }
 }
 
-// A row's result: channels 16 d + 4 g + e in o[d][e], the maximum and the sum
-// of its exponentials; with splits it goes to the workspace.
+// Four channels of a row's result from channel ch, the row's maximum and the
+// sum of its exponentials; with splits they go to the workspace.
 template <int DW>
-__device__ __forceinline__ void finish_row(const KvAttend& a, uint32_t tok, uint32_t qh, uint32_t split, uint32_t g, float top,
-                                           float total, const f32x4 (&o)[4 * DW]) {
+__device__ __forceinline__ void finish_part(const KvAttend& a, uint32_t tok, uint32_t qh, uint32_t split, uint32_t ch, float top,
+                                            float total, f32x4 v) {
     constexpr uint32_t D = 64 * DW;
     if (a.splits > 1) {
         float* pp = a.part + (((uint64_t)tok * a.heads + qh) * a.splits + split) * (D + 4);
-#pragma unroll
-        for (int d = 0; d < 4 * DW; d++) *(f32x4*)(pp + 16 * d + 4 * g) = o[d];
-        if (g == 0) {
+        *(f32x4*)(pp + ch) = v;
+        if (ch == 0) {
             pp[D] = top;
             pp[D + 1] = total;
         }
@@ -192,20 +196,16 @@ __device__ __forceinline__ void finish_row(const KvAttend& a, uint32_t tok, uint
     const uint32_t dim = a.c.dim;
     const float inv = total > 0.f ? 1.f / total : 0.f;
     uint16_t* op = a.out + (uint64_t)tok * a.out_stride + (uint64_t)qh * dim;
-#pragma unroll
-    for (int d = 0; d < 4 * DW; d++) {
-        const uint32_t ch = 16 * d + 4 * g;
-        const uint32_t lo = pack_bf16(o[d][0] * inv, o[d][1] * inv), hi = pack_bf16(o[d][2] * inv, o[d][3] * inv);
-        if (a.out8 && ch + 4 <= dim) {
-            *(v2u*)(op + ch) = v2u{lo, hi};
-        } else {
-            if (ch < dim) op[ch] = (uint16_t)lo;
-            if (ch + 1 < dim) op[ch + 1] = (uint16_t)(lo >> 16);
-            if (ch + 2 < dim) op[ch + 2] = (uint16_t)hi;
-            if (ch + 3 < dim) op[ch + 3] = (uint16_t)(hi >> 16);
-        }
+    const uint32_t lo = pack_bf16(v[0] * inv, v[1] * inv), hi = pack_bf16(v[2] * inv, v[3] * inv);
+    if (a.out8 && ch + 4 <= dim) {
+        *(v2u*)(op + ch) = v2u{lo, hi};
+    } else {
+        if (ch < dim) op[ch] = (uint16_t)lo;
+        if (ch + 1 < dim) op[ch + 1] = (uint16_t)(lo >> 16);
+        if (ch + 2 < dim) op[ch + 2] = (uint16_t)hi;
+        if (ch + 3 < dim) op[ch + 3] = (uint16_t)(hi >> 16);
     }
-    if (a.lse && g == 0) a.lse[(uint64_t)tok * a.heads + qh] = total > 0.f ? (top + __builtin_amdgcn_logf(total)) * kLn2 : -__builtin_inff();
+    if (a.lse && ch == 0) a.lse[(uint64_t)tok * a.heads + qh] = total > 0.f ? (top + __builtin_amdgcn_logf(total)) * kLn2 : -__builtin_inff();
 }
 
 // grid: (sequences * row tiles, key heads, splits); NW waves.  The bound of
@@ -217,8 +217,14 @@ template <int DW, bool E4M3, int NW>
 __global__ __launch_bounds__(64 * NW, 2) void attend_kernel(KvAttend a, uint32_t row_tiles) {
     const KvView& c = a.c;
     constexpr uint32_t D = 64 * DW;
+    // values loaded with the keys; the rest follow when the keys' registers
+    // are free (all at once, head_dim 256 spills registers)
+    constexpr uint32_t kFirst = DW >= 3 ? 2 * DW : 4 * DW;
     __shared__ float ml[NW][2][16];
-    __shared__ __attribute__((aligned(16))) float os[NW > 1 ? NW / 2 : 1][16][D + 4];
+    __shared__ __attribute__((aligned(16))) float os[NW][16][D + 4];
+    // Q as operands of the product: in registers it would leave too few for
+    // a tile's keys and values in flight at head_dim 256
+    __shared__ __attribute__((aligned(16))) uint8_t qs[2 * DW][1024];
 
     const uint32_t t = threadIdx.x, lane = t & 63u, m = lane & 15u, g = lane >> 4;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(t >> 6);
@@ -230,21 +236,39 @@ __global__ __launch_bounds__(64 * NW, 2) void attend_kernel(KvAttend a, uint32_t
     }
     const uint32_t rows = (uint32_t)sq.count * a.group;
     if (16 * rt >= rows) return;
+    const uint32_t nrows = min(16u, rows - 16 * rt);
     const int32_t base = sq.len - sq.count;                         // the first query's place
-    const uint32_t r_last = min(16 * rt + 15, rows - 1);
-    const int32_t lo = base + (int32_t)(16 * rt / a.group), hi = base + (int32_t)(r_last / a.group);
+    const int32_t lo = base + (int32_t)(16 * rt / a.group), hi = base + (int32_t)((16 * rt + nrows - 1) / a.group);
     const Tiles tl = get_tiles(a, lo, hi);
     const uint32_t i0 = split * a.chunk;
     if (split > 0 && i0 >= tl.n) return;
     const uint32_t i1 = a.splits > 1 ? min(tl.n, i0 + a.chunk) : tl.n;
+    const int32_t* trow = c.table + (uint64_t)(uint32_t)max(sq.row, 0) * c.max_pages;
+    const uint64_t hoff = (uint64_t)head * c.page * c.wide;
+    const uint32_t end = (uint32_t)(hi + 1);                        // tokens past it are seen by no row
+    // pages of the lane's 16-token chunks of tile i: its keys' (by step row m)
+    // and its own tokens' (by group); -1 past the end
+    auto pages = [&](uint32_t i, int32_t& pk, int32_t& pv) {
+        pk = pv = -1;
+        if (i >= i1) return;
+        const uint32_t tile0 = tl.at(i) * kKvTile, ck = tile0 + 16 * (m >> 2), cv = tile0 + 16 * g;
+        if (ck < end) pk = trow[ck >> c.lp];
+        if (cv < end) pv = trow[cv >> c.lp];
+    };
+    int32_t pk1, pv1;
+    pages(i0 + wave, pk1, pv1);
 
     // this lane's row
-    const uint32_t r = min(16 * rt + m, rows - 1);
+    const uint32_t r = 16 * rt + min(m, nrows - 1);
     const uint32_t tok = (uint32_t)sq.s0 + r / a.group, qh = head * a.group + r % a.group;
     const int32_t pos = base + (int32_t)(r / a.group);
-
-    bf16x8 q[DW][2];
-    load_q<DW>(a, tok, qh, g, q);
+    if (wave == 0) {
+        bf16x8 q[DW][2];
+        load_q<DW>(a, tok, qh, g, q);
+#pragma unroll
+        for (uint32_t x = 0; x < 2 * DW; x++) *(bf16x8*)(qs[x] + 16 * lane) = q[x >> 1][x & 1];
+    }
+    __syncthreads();
     const float sc = a.softcap > 0.f ? a.qscale : a.qscale * kLog2e;
     const float cap_in = a.softcap > 0.f ? 2.f * kLog2e / a.softcap : 0.f, cap_out = a.softcap * kLog2e;
 
@@ -252,19 +276,14 @@ __global__ __launch_bounds__(64 * NW, 2) void attend_kernel(KvAttend a, uint32_t
 #pragma unroll
     for (int d = 0; d < 4 * DW; d++) o[d] = f32x4{0.f, 0.f, 0.f, 0.f};
     float mx = -__builtin_inff(), sum = 0.f;
-    const int32_t* trow = c.table + (uint64_t)(uint32_t)max(sq.row, 0) * c.max_pages;
-    const uint64_t hoff = (uint64_t)head * c.page * c.wide;
-    const uint32_t end = (uint32_t)(hi + 1);                        // tokens past it are seen by no row
     uint32_t bad = 0;
 
     for (uint32_t i = i0 + wave; i < i1; i += NW) {
         const uint32_t tile0 = tl.at(i) * kKvTile;
-        // the lane's 16-token chunks: its keys' (by step row m) and its own tokens' (by group)
         const uint32_t ck = tile0 + 16 * (m >> 2), cv = tile0 + 16 * g;
-        int32_t pk = ck < end ? trow[ck >> c.lp] : -1, pv = cv < end ? trow[cv >> c.lp] : -1;
-        const bool okk = (uint32_t)pk < c.n_pages, okv = (uint32_t)pv < c.n_pages;
+        const bool okk = (uint32_t)pk1 < c.n_pages, okv = (uint32_t)pv1 < c.n_pages;
         if (cv < end && !okv) bad = 1;
-        const uint32_t ipk = okk ? (uint32_t)pk : 0u, ipv = okv ? (uint32_t)pv : 0u;
+        const uint32_t ipk = okk ? (uint32_t)pk1 : 0u, ipv = okv ? (uint32_t)pv1 : 0u;
         const uint8_t* kp = a.k + (uint64_t)ipk * c.side_bytes + hoff + (uint64_t)((ck + (m & 3u)) & (c.page - 1)) * D + 16 * g;
         const uint8_t* vp = a.v + (uint64_t)ipv * c.side_bytes + hoff + (uint64_t)m * c.page + (cv & (c.page - 1));
         v4u kr[4][DW], vr[4 * DW];
@@ -272,10 +291,11 @@ __global__ __launch_bounds__(64 * NW, 2) void attend_kernel(KvAttend a, uint32_t
         for (uint32_t h = 0; h < 4; h++)
 #pragma unroll
             for (uint32_t x = 0; x < DW; x++) kr[h][x] = *(const v4u*)(kp + 4 * h * D + 64 * x);
-#pragma unroll
-        for (uint32_t d = 0; d < 4 * DW; d++) vr[d] = *(const v4u*)(vp + (uint64_t)(16 * d) * c.page);
         const float* sp = a.scale + ((uint64_t)ipv * c.kv_heads + head) * 2;
         const float ks = sp[0] * sc, vs = okv ? sp[1] : 0.f;
+#pragma unroll
+        for (uint32_t d = 0; d < kFirst; d++) vr[d] = *(const v4u*)(vp + (uint64_t)(16 * d) * c.page);
+        pages(i + NW, pk1, pv1);
 
         f32x4 s[4];
 #pragma unroll
@@ -283,10 +303,14 @@ __global__ __launch_bounds__(64 * NW, 2) void attend_kernel(KvAttend a, uint32_t
             s[h] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (uint32_t x = 0; x < DW; x++) {
-                s[h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen8<E4M3>(kr[h][x].x, kr[h][x].y), q[x][0], s[h], 0, 0, 0);
-                s[h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen8<E4M3>(kr[h][x].z, kr[h][x].w), q[x][1], s[h], 0, 0, 0);
+                const bf16x8 q0 = *(const bf16x8*)(qs[2 * x] + 16 * lane), q1 = *(const bf16x8*)(qs[2 * x + 1] + 16 * lane);
+                s[h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen8<E4M3>(kr[h][x].x, kr[h][x].y), q0, s[h], 0, 0, 0);
+                s[h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen8<E4M3>(kr[h][x].z, kr[h][x].w), q1, s[h], 0, 0, 0);
             }
         }
+        if (kFirst < 4 * DW) __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (uint32_t d = kFirst; d < 4 * DW; d++) vr[d] = *(const v4u*)(vp + (uint64_t)(16 * d) * c.page);
         // step h's element e is token cv + 4 h + e
         float p[16];
         float top = -__builtin_inff();
@@ -317,15 +341,20 @@ __global__ __launch_bounds__(64 * NW, 2) void attend_kernel(KvAttend a, uint32_t
         }
         top = fmaxf(max_groups(top), mx);
         const float sub = top == -__builtin_inff() ? 0.f : top;
-        const float alpha = exp2_fast(mx - sub);
-        mx = top;
+        if (__builtin_amdgcn_ballot_w64(top > mx) != 0) {
+            const float alpha = exp2_fast(mx - sub);
+            mx = top;
+            sum *= alpha;
+#pragma unroll
+            for (int d = 0; d < 4 * DW; d++) o[d] *= alpha;
+        }
         float part = 0.f;
 #pragma unroll
         for (int e = 0; e < 16; e++) {
             p[e] = exp2_fast(p[e] - sub);
             part += p[e];
         }
-        sum = sum * alpha + part;
+        sum += part;
         bf16x8 pb[2];
 #pragma unroll
         for (int y = 0; y < 2; y++)
@@ -333,44 +362,40 @@ __global__ __launch_bounds__(64 * NW, 2) void attend_kernel(KvAttend a, uint32_t
                                                    pack_bf16(p[8 * y + 4] * vs, p[8 * y + 5] * vs), pack_bf16(p[8 * y + 6] * vs, p[8 * y + 7] * vs)});
 #pragma unroll
         for (int d = 0; d < 4 * DW; d++) {
-            o[d] *= alpha;
             o[d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen8<E4M3>(vr[d].x, vr[d].y), pb[0], o[d], 0, 0, 0);
             o[d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen8<E4M3>(vr[d].z, vr[d].w), pb[1], o[d], 0, 0, 0);
         }
     }
     if (bad && c.status) atomicOr(c.status, 4u);
 
-    // join the waves: maxima and sums, then the results in wave order
+    // join the waves, in wave order: every wave leaves its rows, its maxima
+    // and sums in LDS, then each thread adds four channels of a row
     sum = sum_groups(sum);
     if (g == 0) {
         ml[wave][0][m] = mx;
         ml[wave][1][m] = sum;
     }
-    __syncthreads();
-    float top = -__builtin_inff(), total = 0.f;
+    if (m < nrows) {
 #pragma unroll
-    for (int w = 0; w < NW; w++) top = fmaxf(top, ml[w][0][m]);
-    const float sub = top == -__builtin_inff() ? 0.f : top;
-#pragma unroll
-    for (int w = 0; w < NW; w++) total += ml[w][1][m] * exp2_fast(ml[w][0][m] - sub);
-    const float f = exp2_fast(mx - sub);
-#pragma unroll
-    for (int d = 0; d < 4 * DW; d++) o[d] *= f;
-#pragma unroll
-    for (int half = NW / 2; half >= 1; half /= 2) {
-        __syncthreads();
-        if ((int)wave >= half && (int)wave < 2 * half) {
-#pragma unroll
-            for (int d = 0; d < 4 * DW; d++) *(f32x4*)&os[wave - half][m][16 * d + 4 * g] = o[d];
-        }
-        __syncthreads();
-        if ((int)wave < half) {
-#pragma unroll
-            for (int d = 0; d < 4 * DW; d++) o[d] += *(f32x4*)&os[wave][m][16 * d + 4 * g];
-        }
+        for (int d = 0; d < 4 * DW; d++) *(f32x4*)&os[wave][m][16 * d + 4 * g] = o[d];
     }
-    if (wave != 0 || 16 * rt + m >= rows) return;
-    finish_row<DW>(a, tok, qh, split, g, top, total, o);
+    __syncthreads();
+    for (uint32_t i = t; i < nrows * (D / 4); i += 64 * NW) {
+        const uint32_t n = i / (D / 4), ch = 4 * (i % (D / 4));
+        float top = -__builtin_inff(), total = 0.f;
+#pragma unroll
+        for (int w = 0; w < NW; w++) top = fmaxf(top, ml[w][0][n]);
+        const float sub = top == -__builtin_inff() ? 0.f : top;
+        f32x4 v = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int w = 0; w < NW; w++) {
+            const float f = exp2_fast(ml[w][0][n] - sub);
+            total += f * ml[w][1][n];
+            v += f * *(const f32x4*)&os[w][n][ch];
+        }
+        const uint32_t rr = 16 * rt + n;
+        finish_part<DW>(a, (uint32_t)sq.s0 + rr / a.group, head * a.group + rr % a.group, split, ch, top, total, v);
+    }
 }
 
 // ---------------------------------------------------------------- many rows
@@ -628,7 +653,8 @@ __global__ __launch_bounds__(512, 2) void attend_rows_kernel(KvAttend a, uint32_
     for (uint32_t n = 0; n < NR; n++) {
         const float total = sum_groups(sum[n]);
         if (w0 + 16 * n + m >= rows) continue;
-        finish_row<DW>(a, tok[n], qh[n], split, g, mx[n], total, o[n]);
+#pragma unroll
+        for (uint32_t d = 0; d < 4 * DW; d++) finish_part<DW>(a, tok[n], qh[n], split, 16 * d + 4 * g, mx[n], total, o[n][d]);
     }
 }
 
@@ -701,8 +727,13 @@ int launch(const KvAttend& a, hipStream_t st) {
     }
     const uint32_t row_tiles = (a.max_new * a.group + 15) / 16;
     const dim3 grid(a.n_seqs * row_tiles, a.c.kv_heads, a.splits);
-    if (a.c.type == 1) hipLaunchKernelGGL((attend_kernel<DW, true, 4>), grid, dim3(256), 0, st, a, row_tiles);
-    else hipLaunchKernelGGL((attend_kernel<DW, false, 4>), grid, dim3(256), 0, st, a, row_tiles);
+    if (a.waves == 8) {
+        if (a.c.type == 1) hipLaunchKernelGGL((attend_kernel<DW, true, 8>), grid, dim3(512), 0, st, a, row_tiles);
+        else hipLaunchKernelGGL((attend_kernel<DW, false, 8>), grid, dim3(512), 0, st, a, row_tiles);
+    } else {
+        if (a.c.type == 1) hipLaunchKernelGGL((attend_kernel<DW, true, 4>), grid, dim3(256), 0, st, a, row_tiles);
+        else hipLaunchKernelGGL((attend_kernel<DW, false, 4>), grid, dim3(256), 0, st, a, row_tiles);
+    }
     if (a.splits > 1) hipLaunchKernelGGL(join_kernel<DW>, dim3(a.n_seqs * a.max_new, a.heads), dim3(64), 0, st, a, 16u);
     return (int)hipGetLastError();
 }

@@ -53,6 +53,7 @@ struct KvAttend {
     int aligned;                // q can be read 16 B at a time
     int out8;                   // four channels of out can be written at a time
     int many;                   // the kernel for many rows
+    int waves;                  // of a workgroup of the other: 4 or 8
     uint32_t chunk;             // tiles of a split
     uint32_t splits;            // 1: no partial results
     float* part;                // splits > 1: [total * heads][splits][wide + 4]: the result, its maximum and sum, 2 unused
