@@ -746,7 +746,9 @@ typedef struct {
  * enter the second product in BF16, the type of the result.  What slots past
  * a row's length hold does not matter.  The same result on every run.
  * d_work (16-B aligned): bs_kv_attend_work_bytes, which gives 0 where rows
- * need not be split; without it (NULL) they are not. */
+ * need not be split; without it (NULL) they are not.  Its first 4096 bytes
+ * are zero before the first call that is given it, and every call leaves
+ * them so; calls that share it must not overlap. */
 bs_status bs_kv_attend_async(const bs_kv_cache* cache, const bs_kv_attend_args* args, void* d_work, uint64_t work_bytes,
                              void* stream);
 uint64_t bs_kv_attend_work_bytes(const bs_kv_cache* cache, const bs_kv_attend_args* args);

@@ -13,10 +13,6 @@ using namespace bs;
 
 namespace {
 
-#ifndef BS_KV_PER
-#define BS_KV_PER 4
-#endif
-
 constexpr uint64_t kGridX = 0x7FFFFFFFull, kGridYZ = 65535;
 
 bs_status launched(int e, const char* what) {
@@ -81,9 +77,8 @@ bs_status view(const bs_kv_cache* c, bsd::KvView& v) {
     return BS_OK;
 }
 
-// The tiles that a split takes, how many splits there are, and the waves of a
-// workgroup.
-void split_rule(bsd::KvAttend& a, uint32_t max_len, uint32_t& chunk, uint32_t& splits) {
+// The tiles that a split takes, and how many splits there are.
+void split_rule(const bsd::KvAttend& a, uint32_t max_len, uint32_t& chunk, uint32_t& splits) {
     int cus = 0;
     if (bsk_device_cus(&cus) != 0 || cus <= 0) cus = 256;
     const uint64_t rows = (uint64_t)a.max_new * a.group;
@@ -94,9 +89,10 @@ void split_rule(bsd::KvAttend& a, uint32_t max_len, uint32_t& chunk, uint32_t& s
         tiles = std::min<uint64_t>(tiles, span / bsd::kKvTile + 1 + ((uint64_t)a.sinks + bsd::kKvTile - 1) / bsd::kKvTile);
     }
     const uint64_t groups = std::max<uint64_t>(1, (uint64_t)a.n_seqs * row_tiles * a.c.kv_heads);
-    // workgroups per CU that are aimed at, and the fewest tiles of one: a
-    // split costs a pass through the workspace and a second launch
-    const uint64_t per = a.many ? 1 : BS_KV_PER, least = a.many ? 8 : 16;
+    // workgroups per CU that are aimed at (4 of the few-row kernel: 8 and 16
+    // made 4 x 131071 tokens 2 and 9% slower), and the fewest tiles of one:
+    // one to a wave, so that short rows are read by many CUs
+    const uint64_t per = a.many ? 1 : 4, least = a.many ? 8 : 4;
     const uint64_t want = std::max<uint64_t>(1, per * (uint64_t)cus / groups);
     uint64_t ch = std::max<uint64_t>(least, (tiles + want - 1) / want);
     splits = (uint32_t)std::max<uint64_t>(1, (tiles + ch - 1) / ch);
@@ -105,8 +101,7 @@ void split_rule(bsd::KvAttend& a, uint32_t max_len, uint32_t& chunk, uint32_t& s
         splits = (uint32_t)((tiles + ch - 1) / ch);
     }
     chunk = (uint32_t)ch;
-    // 8 waves where the workgroups are too few to fill the CUs by themselves
-    a.waves = groups * splits <= (uint64_t)cus ? 8 : 4;
+    if (groups > bsd::kKvCounters && !a.many) { splits = 1; chunk = (uint32_t)std::max<uint64_t>(1, tiles); }
 }
 
 bs_status attend_args(const bs_kv_cache* cache, const bs_kv_attend_args* x, bsd::KvAttend& a, uint32_t& chunk,
@@ -171,7 +166,7 @@ bs_status attend_args(const bs_kv_cache* cache, const bs_kv_attend_args* x, bsd:
 }
 
 uint64_t part_bytes(const bsd::KvAttend& a, uint32_t splits) {
-    return splits > 1 ? 4ull * a.total * a.heads * splits * (a.c.wide + 4) : 0;
+    return splits > 1 ? 4ull * (bsd::kKvCounters + (uint64_t)a.total * a.heads * splits * (a.c.wide + 4)) : 0;
 }
 
 uint64_t page_work(const bsd::KvView& v, uint64_t n) {
@@ -294,7 +289,8 @@ bs_status bs_kv_attend_async(const bs_kv_cache* cache, const bs_kv_attend_args* 
             return BS_E_INVAL;
         }
         a.splits = splits;
-        a.part = (float*)d_work;
+        a.counters = (uint32_t*)d_work;
+        a.part = (float*)d_work + bsd::kKvCounters;
     }
     return launched(bsk_kv_attend(&a, stream), "attention");
 }

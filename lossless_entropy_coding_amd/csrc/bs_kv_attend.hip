@@ -28,7 +28,7 @@
 // column), the result is scaled when the maximum grows.  The waves of a
 // workgroup take the tiles in turn and are joined in wave order; where there
 // are too few rows to fill the GPU, a row's tiles are also split over
-// workgroups, and a second kernel joins their results in order.
+// workgroups, and the one that ends last joins their results in order.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -178,21 +178,33 @@ __device__ __forceinline__ void load_q(const KvAttend& a, uint32_t tok, uint32_t
     }
 }
 
+__device__ __forceinline__ void store_through(float* p, float a, float b) {
+    const uint64_t v = (uint64_t)__builtin_bit_cast(uint32_t, a) | (uint64_t)__builtin_bit_cast(uint32_t, b) << 32;
+    __hip_atomic_store((uint64_t*)p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
 // Four channels of a row's result from channel ch, the row's maximum and the
-// sum of its exponentials; with splits they go to the workspace.
-template <int DW>
-__device__ __forceinline__ void finish_part(const KvAttend& a, uint32_t tok, uint32_t qh, uint32_t split, uint32_t ch, float top,
-                                            float total, f32x4 v) {
+// sum of its exponentials: to the workspace, or divided to the output.
+// THROUGH: stores that other XCDs see once they are done.
+template <int DW, bool THROUGH>
+__device__ __forceinline__ void part_write(const KvAttend& a, uint32_t tok, uint32_t qh, uint32_t split, uint32_t ch, float top,
+                                           float total, f32x4 v) {
     constexpr uint32_t D = 64 * DW;
-    if (a.splits > 1) {
-        float* pp = a.part + (((uint64_t)tok * a.heads + qh) * a.splits + split) * (D + 4);
-        *(f32x4*)(pp + ch) = v;
-        if (ch == 0) {
-            pp[D] = top;
-            pp[D + 1] = total;
-        }
+    float* pp = a.part + (((uint64_t)tok * a.heads + qh) * a.splits + split) * (D + 4);
+    if (THROUGH) {
+        store_through(pp + ch, v[0], v[1]);
+        store_through(pp + ch + 2, v[2], v[3]);
+        if (ch == 0) store_through(pp + D, top, total);
         return;
     }
+    *(f32x4*)(pp + ch) = v;
+    if (ch == 0) {
+        pp[D] = top;
+        pp[D + 1] = total;
+    }
+}
+
+__device__ __forceinline__ void out_write(const KvAttend& a, uint32_t tok, uint32_t qh, uint32_t ch, float top, float total, f32x4 v) {
     const uint32_t dim = a.c.dim;
     const float inv = total > 0.f ? 1.f / total : 0.f;
     uint16_t* op = a.out + (uint64_t)tok * a.out_stride + (uint64_t)qh * dim;
@@ -206,6 +218,42 @@ __device__ __forceinline__ void finish_part(const KvAttend& a, uint32_t tok, uin
         if (ch + 3 < dim) op[ch + 3] = (uint16_t)(hi >> 16);
     }
     if (a.lse && ch == 0) a.lse[(uint64_t)tok * a.heads + qh] = total > 0.f ? (top + __builtin_amdgcn_logf(total)) * kLn2 : -__builtin_inff();
+}
+
+// Four channels of a row from its n parts, in order, 8 loads at a time.
+template <int DW>
+__device__ __forceinline__ void join_row(const KvAttend& a, uint32_t tok, uint32_t qh, uint32_t ch, uint32_t n) {
+    constexpr uint32_t D = 64 * DW;
+    const float* pp = a.part + ((uint64_t)tok * a.heads + qh) * a.splits * (D + 4);
+    float top = -__builtin_inff();
+    for (uint32_t s0 = 0; s0 < n; s0 += 8) {
+        float f[8];
+#pragma unroll
+        for (uint32_t u = 0; u < 8; u++) f[u] = pp[min(s0 + u, n - 1) * (D + 4) + D];
+#pragma unroll
+        for (uint32_t u = 0; u < 8; u++) top = fmaxf(top, f[u]);
+    }
+    const float sub = top == -__builtin_inff() ? 0.f : top;
+    float total = 0.f;
+    f32x4 o = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (uint32_t s0 = 0; s0 < n; s0 += 8) {
+        f32x4 v[8];
+        float f[8], l[8];
+#pragma unroll
+        for (uint32_t u = 0; u < 8; u++) {
+            const float* ps = pp + min(s0 + u, n - 1) * (D + 4);
+            v[u] = *(const f32x4*)(ps + ch);
+            f[u] = ps[D];
+            l[u] = ps[D + 1];
+        }
+#pragma unroll
+        for (uint32_t u = 0; u < 8; u++) {
+            const float w = s0 + u < n ? exp2_fast(f[u] - sub) : 0.f;
+            total += w * l[u];
+            o += w * v[u];
+        }
+    }
+    out_write(a, tok, qh, ch, top, total, o);
 }
 
 // grid: (sequences * row tiles, key heads, splits); NW waves.  The bound of
@@ -380,6 +428,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attend_kernel(KvAttend a, uint32_t
         for (int d = 0; d < 4 * DW; d++) *(f32x4*)&os[wave][m][16 * d + 4 * g] = o[d];
     }
     __syncthreads();
+    const uint32_t parts = a.splits > 1 ? max(1u, (tl.n + a.chunk - 1) / a.chunk) : 1u;   // workgroups of these rows
     for (uint32_t i = t; i < nrows * (D / 4); i += 64 * NW) {
         const uint32_t n = i / (D / 4), ch = 4 * (i % (D / 4));
         float top = -__builtin_inff(), total = 0.f;
@@ -393,9 +442,33 @@ __global__ __launch_bounds__(64 * NW, 2) void attend_kernel(KvAttend a, uint32_t
             total += f * ml[w][1][n];
             v += f * *(const f32x4*)&os[w][n][ch];
         }
-        const uint32_t rr = 16 * rt + n;
-        finish_part<DW>(a, (uint32_t)sq.s0 + rr / a.group, head * a.group + rr % a.group, split, ch, top, total, v);
+        const uint32_t rr = 16 * rt + n, tk = (uint32_t)sq.s0 + rr / a.group, h = head * a.group + rr % a.group;
+        if (parts > 1) part_write<DW, true>(a, tk, h, split, ch, top, total, v);
+        else out_write(a, tk, h, ch, top, total, v);
     }
+    if (parts == 1) return;
+
+    // The workgroup that ends last joins them all, in split order; counters are
+    // 0 between calls.  The parts are stored through the L2 (the XCDs' L2s do
+    // not see each other's lines) and waited for before the workgroup counts
+    // itself.  A release at the GPU's scope would write back the whole L2 each
+    // time: with it, 4 x 131071 tokens took 388 us instead of 201 with a
+    // second launch for the join.
+    __shared__ uint32_t last;
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup");
+    __builtin_amdgcn_s_waitcnt(0);
+    __syncthreads();
+    uint32_t* counter = a.counters + blockIdx.x * c.kv_heads + head;
+    if (t == 0) last = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == parts - 1;
+    __syncthreads();
+    if (!last) return;
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
+    for (uint32_t i = t; i < nrows * (D / 4); i += 64 * NW) {
+        const uint32_t n = i / (D / 4), ch = 4 * (i % (D / 4));
+        const uint32_t rr = 16 * rt + n, tk = (uint32_t)sq.s0 + rr / a.group, h = head * a.group + rr % a.group;
+        join_row<DW>(a, tk, h, ch, parts);
+    }
+    if (t == 0) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
 // ---------------------------------------------------------------- many rows
@@ -654,58 +727,27 @@ __global__ __launch_bounds__(512, 2) void attend_rows_kernel(KvAttend a, uint32_
         const float total = sum_groups(sum[n]);
         if (w0 + 16 * n + m >= rows) continue;
 #pragma unroll
-        for (uint32_t d = 0; d < 4 * DW; d++) finish_part<DW>(a, tok[n], qh[n], split, 16 * d + 4 * g, mx[n], total, o[n][d]);
+        for (uint32_t d = 0; d < 4 * DW; d++) {
+            if (a.splits > 1) part_write<DW, false>(a, tok[n], qh[n], split, 16 * d + 4 * g, mx[n], total, o[n][d]);
+            else out_write(a, tok[n], qh[n], 16 * d + 4 * g, mx[n], total, o[n][d]);
+        }
     }
 }
 
-// Joins the splits of one row in order: a wave per row, its lanes over the
-// channels and the splits' loads 8 at a time.  grid: (sequences * max_new,
-// heads); block_rows: rows that share a split's tiles.
+// Joins the splits of attend_rows_kernel: four channels to a thread.  grid:
+// (sequences * max_new, blocks of 64 / (16 DW) heads)
 template <int DW>
 __global__ __launch_bounds__(64) void join_kernel(KvAttend a, uint32_t block_rows) {
-    constexpr uint32_t D = 64 * DW;
-    const uint32_t seq_i = blockIdx.x / a.max_new, j = blockIdx.x % a.max_new, qh = blockIdx.y, lane = threadIdx.x;
+    constexpr uint32_t kLanes = 16 * DW, kHeads = 64 / kLanes > 0 ? 64 / kLanes : 1;   // 3: 48 lanes of 64
+    const uint32_t seq_i = blockIdx.x / a.max_new, j = blockIdx.x % a.max_new;
+    const uint32_t qh = blockIdx.y * kHeads + threadIdx.x / kLanes, ch = 4 * (threadIdx.x % kLanes);
     const Seq sq = get_seq(a, seq_i);
-    if (j >= (uint32_t)sq.count) return;
+    if (j >= (uint32_t)sq.count || qh >= a.heads || threadIdx.x >= kHeads * kLanes) return;
     const uint32_t r0 = (j * a.group + qh % a.group) / block_rows * block_rows;
     const int32_t base = sq.len - sq.count;
     const uint32_t r1 = min(r0 + block_rows, (uint32_t)sq.count * a.group) - 1;
     const Tiles tl = get_tiles(a, base + (int32_t)(r0 / a.group), base + (int32_t)(r1 / a.group));
-    const uint32_t n = max(1u, (tl.n + a.chunk - 1) / a.chunk);
-    const uint32_t tok = (uint32_t)sq.s0 + j;
-    const float* pp = a.part + ((uint64_t)tok * a.heads + qh) * a.splits * (D + 4);
-    float top = -__builtin_inff();
-    for (uint32_t s = lane; s < n; s += 64) top = fmaxf(top, pp[s * (D + 4) + D]);
-#pragma unroll
-    for (int k = 32; k; k >>= 1) top = fmaxf(top, __shfl_xor(top, k));
-    const float sub = top == -__builtin_inff() ? 0.f : top;
-    float total = 0.f, o[DW];
-#pragma unroll
-    for (int x = 0; x < DW; x++) o[x] = 0.f;
-    for (uint32_t s0 = 0; s0 < n; s0 += 8) {
-        float v[8][DW], f[8], l[8];
-#pragma unroll
-        for (uint32_t u = 0; u < 8; u++) {
-            const float* ps = pp + min(s0 + u, n - 1) * (D + 4);
-            f[u] = ps[D];
-            l[u] = ps[D + 1];
-#pragma unroll
-            for (int x = 0; x < DW; x++) v[u][x] = ps[64 * x + lane];
-        }
-#pragma unroll
-        for (uint32_t u = 0; u < 8; u++) {
-            const float w = s0 + u < n ? exp2_fast(f[u] - sub) : 0.f;
-            total += w * l[u];
-#pragma unroll
-            for (int x = 0; x < DW; x++) o[x] += w * v[u][x];
-        }
-    }
-    const float inv = total > 0.f ? 1.f / total : 0.f;
-    uint16_t* op = a.out + (uint64_t)tok * a.out_stride + (uint64_t)qh * a.c.dim;
-#pragma unroll
-    for (int x = 0; x < DW; x++)
-        if (64 * x + lane < a.c.dim) op[64 * x + lane] = __builtin_bit_cast(uint16_t, (__bf16)(o[x] * inv));
-    if (a.lse && lane == 0) a.lse[(uint64_t)tok * a.heads + qh] = total > 0.f ? (top + __builtin_amdgcn_logf(total)) * kLn2 : -__builtin_inff();
+    join_row<DW>(a, (uint32_t)sq.s0 + j, qh, ch, max(1u, (tl.n + a.chunk - 1) / a.chunk));
 }
 
 // rows of a workgroup of attend_rows_kernel: two row tiles to a wave where
@@ -722,19 +764,14 @@ int launch(const KvAttend& a, hipStream_t st) {
         const dim3 grid((combos + 7) / 8 * 8 * row_blocks, a.splits);
         if (a.c.type == 1) hipLaunchKernelGGL((attend_rows_kernel<DW, true, NR>), grid, dim3(512), 0, st, a, row_blocks, combos);
         else hipLaunchKernelGGL((attend_rows_kernel<DW, false, NR>), grid, dim3(512), 0, st, a, row_blocks, combos);
-        if (a.splits > 1) hipLaunchKernelGGL(join_kernel<DW>, dim3(a.n_seqs * a.max_new, a.heads), dim3(64), 0, st, a, 128u * NR);
+        constexpr uint32_t heads = 64 / (16 * DW) > 0 ? 64 / (16 * DW) : 1;
+        if (a.splits > 1) hipLaunchKernelGGL(join_kernel<DW>, dim3(a.n_seqs * a.max_new, (a.heads + heads - 1) / heads), dim3(64), 0, st, a, 128u * NR);
         return (int)hipGetLastError();
     }
     const uint32_t row_tiles = (a.max_new * a.group + 15) / 16;
     const dim3 grid(a.n_seqs * row_tiles, a.c.kv_heads, a.splits);
-    if (a.waves == 8) {
-        if (a.c.type == 1) hipLaunchKernelGGL((attend_kernel<DW, true, 8>), grid, dim3(512), 0, st, a, row_tiles);
-        else hipLaunchKernelGGL((attend_kernel<DW, false, 8>), grid, dim3(512), 0, st, a, row_tiles);
-    } else {
-        if (a.c.type == 1) hipLaunchKernelGGL((attend_kernel<DW, true, 4>), grid, dim3(256), 0, st, a, row_tiles);
-        else hipLaunchKernelGGL((attend_kernel<DW, false, 4>), grid, dim3(256), 0, st, a, row_tiles);
-    }
-    if (a.splits > 1) hipLaunchKernelGGL(join_kernel<DW>, dim3(a.n_seqs * a.max_new, a.heads), dim3(64), 0, st, a, 16u);
+    if (a.c.type == 1) hipLaunchKernelGGL((attend_kernel<DW, true, 4>), grid, dim3(256), 0, st, a, row_tiles);
+    else hipLaunchKernelGGL((attend_kernel<DW, false, 4>), grid, dim3(256), 0, st, a, row_tiles);
     return (int)hipGetLastError();
 }
 

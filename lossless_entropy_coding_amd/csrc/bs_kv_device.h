@@ -6,6 +6,7 @@
 
 namespace bsd {
 
+constexpr uint32_t kKvCounters = 1024;       // words before a workspace's partial results
 constexpr uint32_t kKvTile = 64;             // tokens that a wave takes at a time (4 chunks of 16)
 
 // one cache as a kernel sees it (layouts in bs.h)
@@ -53,9 +54,9 @@ struct KvAttend {
     int aligned;                // q can be read 16 B at a time
     int out8;                   // four channels of out can be written at a time
     int many;                   // the kernel for many rows
-    int waves;                  // of a workgroup of the other: 4 or 8
     uint32_t chunk;             // tiles of a split
     uint32_t splits;            // 1: no partial results
+    uint32_t* counters;         // splits > 1: workgroups done of each tile of rows and key head
     float* part;                // splits > 1: [total * heads][splits][wide + 4]: the result, its maximum and sum, 2 unused
 };
 

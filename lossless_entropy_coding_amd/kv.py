@@ -214,7 +214,7 @@ class KvCache:
                            None if lse is False else lse.data_ptr(), qs, os, scale, softcap, window, sinks)
         need = int(L.lib().bs_kv_attend_work_bytes(C.byref(self.c), C.byref(a)))
         if need and (self._attend_work is None or self._attend_work.numel() < need):
-            self._attend_work = torch.empty(need, dtype=torch.uint8, device=self.k.device)
+            self._attend_work = torch.zeros(need, dtype=torch.uint8, device=self.k.device)
         w = self._attend_work if need else None
         rc = L.lib().bs_kv_attend_async(C.byref(self.c), C.byref(a), w.data_ptr() if need else None,
                                         w.numel() if need else 0, _stream_handle(stream))
