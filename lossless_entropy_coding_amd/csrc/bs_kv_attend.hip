@@ -553,33 +553,32 @@ __global__ __launch_bounds__(512, 2) void attend_rows_kernel(KvAttend a, uint32_
         uint32_t keep;          // values: tokens of the lane's chunk that count
     };
     uint32_t bad = 0;
-    // page of the lane's chunk of tile i (its staged part's, then its own tokens')
-    auto chunk_page = [&](uint32_t i, uint32_t ch, bool& ok) {
-        ok = false;
-        if (i >= i1) return 0u;
+    // the table's entry for chunk ch of tile i, -1 past the end
+    auto entry = [&](uint32_t i, uint32_t ch) {
+        if (i >= i1) return -1;
         const uint32_t at = tl.at(i) * kKvTile + 16 * ch;
-        if (at >= end) return 0u;
-        const int32_t p = trow[at >> c.lp];
-        ok = (uint32_t)p < c.n_pages;
-        if (!ok) bad = 1;
-        return ok ? (uint32_t)p : 0u;
+        return at < end ? trow[at >> c.lp] : -1;
     };
-    auto stage_load = [&](uint32_t i, Next& x) {
+    // an entry's page (0 where there is none: nothing of it is used)
+    auto page_of = [&](uint32_t i, uint32_t ch, int32_t e, bool& ok) {
+        ok = (uint32_t)e < c.n_pages;
+        if (!ok && i < i1 && tl.at(i) * kKvTile + 16 * ch < end) bad = 1;
+        return ok ? (uint32_t)e : 0u;
+    };
+    const uint32_t chst = vside ? g : m >> 2;                       // the lane's chunk of what it stages
+    auto stage_load = [&](uint32_t i, int32_t e, Next& x) {
         x.keep = 0;
         if (i >= i1) return;
-        const uint32_t tile0 = tl.at(i) * kKvTile;
+        const uint32_t tile0 = tl.at(i) * kKvTile, at = tile0 + 16 * chst;
         bool ok;
+        const uint32_t p = page_of(i, chst, e, ok);
         if (vside) {
-            const uint32_t cv = tile0 + 16 * g;
-            const uint32_t p = chunk_page(i, g, ok);
-            x.keep = ok ? min(end - cv, 16u) : 0u;
-            const uint8_t* vp = a.v + (uint64_t)p * c.side_bytes + hoff + (uint64_t)(16 * part * DW + m) * c.page + (cv & (c.page - 1));
+            x.keep = ok ? min(end - at, 16u) : 0u;
+            const uint8_t* vp = a.v + (uint64_t)p * c.side_bytes + hoff + (uint64_t)(16 * part * DW + m) * c.page + (at & (c.page - 1));
 #pragma unroll
             for (uint32_t d = 0; d < DW; d++) x.r[d] = *(const v4u*)(vp + (uint64_t)(16 * d) * c.page);
         } else {
-            const uint32_t ck = tile0 + 16 * (m >> 2);
-            const uint32_t p = chunk_page(i, m >> 2, ok);
-            const uint8_t* kp = a.k + (uint64_t)p * c.side_bytes + hoff + (uint64_t)((ck + 4 * part + (m & 3u)) & (c.page - 1)) * D + 16 * g;
+            const uint8_t* kp = a.k + (uint64_t)p * c.side_bytes + hoff + (uint64_t)((at + 4 * part + (m & 3u)) & (c.page - 1)) * D + 16 * g;
 #pragma unroll
             for (uint32_t d = 0; d < DW; d++) x.r[d] = *(const v4u*)(kp + 64 * d);
         }
@@ -604,34 +603,39 @@ __global__ __launch_bounds__(512, 2) void attend_rows_kernel(KvAttend a, uint32_
         }
     };
 
+    // Ahead of the tile that is multiplied: its successor's operands wait in
+    // registers, the one after that is being loaded, and the table's entries
+    // are read one more tile ahead, so that no load waits for another.
+    int32_t e0 = entry(i0, chst), e1 = entry(i0 + 1, chst), est = entry(i0 + 2, chst);
+    int32_t es = entry(i0, g), esc = entry(i0 + 1, g);
     Next nx;
-    stage_load(i0, nx);
+    stage_load(i0, e0, nx);
     stage_store(i0, nx);
-    stage_load(i0 + 1, nx);
+    stage_load(i0 + 1, e1, nx);
     // scales of the lane's own 16 tokens, a tile ahead
     bool oks;
-    uint32_t ps = chunk_page(i0, g, oks);
     float ks1 = 1.f, vs1 = 1.f;
-    if (i0 < i1) {
-        const float* sp = a.scale + ((uint64_t)ps * c.kv_heads + head) * 2;
+    {
+        const float* sp = a.scale + ((uint64_t)page_of(i0, g, es, oks) * c.kv_heads + head) * 2;
         ks1 = sp[0];
         vs1 = sp[1];
     }
     __syncthreads();
     for (uint32_t i = i0; i < i1; i++) {
         stage_store(i + 1, nx);
-        stage_load(i + 2, nx);
+        stage_load(i + 2, est, nx);
+        est = entry(i + 3, chst);
         const uint32_t tile0 = tl.at(i) * kKvTile;
         const bool okv = oks;
         // the scales are powers of two, so log2 of V's is exact
         // (at least 2^-120: a masked logit times it stays -infinity)
         const float ks = fmaxf(ks1 * sc, 0x1p-120f), kexp = okv ? (float)((int32_t)(__builtin_bit_cast(uint32_t, vs1) >> 23) - 127) : 0.f;
-        ps = chunk_page(i + 1, g, oks);
-        if (i + 1 < i1) {
-            const float* sp = a.scale + ((uint64_t)ps * c.kv_heads + head) * 2;
+        {
+            const float* sp = a.scale + ((uint64_t)page_of(i + 1, g, esc, oks) * c.kv_heads + head) * 2;
             ks1 = sp[0];
             vs1 = sp[1];
         }
+        esc = entry(i + 2, g);
         // does the wave see any of the tile, or all of it?
         bool any = active && (int32_t)tile0 <= whi;
         bool all = (int32_t)(tile0 + kKvTile - 1) <= wlo;
