@@ -475,10 +475,10 @@ __global__ __launch_bounds__(64 * NW, 2) void attend_kernel(KvAttend a, uint32_t
 //
 // From 64 rows on (prompts, long drafts) a workgroup of 8 waves takes 128 NR
 // rows of one key head, 16 NR to a wave, and all of them use one copy of a
-// tile's keys and values: each wave loads an eighth of the next tile while
-// the current one is multiplied, widens it to BF16 once and leaves it in LDS
-// as the operands of the products, 1 KiB to each, so that every read of them
-// is 16 B per lane on end.  Two tiles are in LDS, one barrier per tile.
+// tile's keys and values: each wave loads a quarter of a side of the tile
+// ahead while the current one is multiplied, widens it to BF16 once and
+// leaves it in LDS as the operands of the products, 1 KiB to each, so that
+// every read of them is 16 B per lane on end.  Two tiles are in LDS.
 //
 // The result is scaled only when a row's maximum has grown by more than 2^8
 // (the exponentials then reach 2^8, as exact in fp32 and BF16 as below 1).
@@ -524,11 +524,18 @@ __global__ __launch_bounds__(512, 2) void attend_rows_kernel(KvAttend a, uint32_
         qh[n] = head * a.group + r % a.group;
         pos[n] = base + (int32_t)(r / a.group);
         load_q<DW>(a, tok[n], qh[n], g, q[n]);
+        if (a.qscale < 0.f) {                                       // the scale's sign goes into Q
+#pragma unroll
+            for (uint32_t x = 0; x < 2 * DW; x++) {
+                v4u w = __builtin_bit_cast(v4u, q[n][x >> 1][x & 1]);
+                w ^= 0x80008000u;
+                q[n][x >> 1][x & 1] = __builtin_bit_cast(bf16x8, w);
+            }
+        }
     }
     const bool active = w0 < rows;
     const int32_t wlo = base + (int32_t)(min(w0, rows - 1) / a.group);
     const int32_t whi = base + (int32_t)(min(w0 + 16 * NR - 1, rows - 1) / a.group);
-    const bool flip = a.qscale < 0.f;                               // the largest product is then the least
     const float sc = (a.softcap > 0.f ? 1.f : kLog2e) * fabsf(a.qscale);
     const float cap_in = a.softcap > 0.f ? 2.f * kLog2e / a.softcap : 0.f, cap_out = a.softcap * kLog2e;
 
@@ -583,49 +590,132 @@ __global__ __launch_bounds__(512, 2) void attend_rows_kernel(KvAttend a, uint32_
             for (uint32_t d = 0; d < DW; d++) x.r[d] = *(const v4u*)(kp + 64 * d);
         }
     };
-    auto stage_store = [&](uint32_t i, Next& x) {
+    // operand 2 (part DW + d) of its side, and the next one
+    auto stage_store = [&](uint32_t i, Next& x, uint32_t d) {
         if (i >= i1) return;
         if (vside && x.keep < 16) {
 #pragma unroll
-            for (uint32_t d = 0; d < DW; d++)
-#pragma unroll
-                for (int w = 0; w < 4; w++) {
-                    const int32_t nb = (int32_t)x.keep - 4 * w;
-                    x.r[d][w] &= nb >= 4 ? ~0u : nb <= 0 ? 0u : (1u << (8 * nb)) - 1u;
-                }
+            for (int w = 0; w < 4; w++) {
+                const int32_t nb = (int32_t)x.keep - 4 * w;
+                x.r[d][w] &= nb >= 4 ? ~0u : nb <= 0 ? 0u : (1u << (8 * nb)) - 1u;
+            }
         }
-        // operand 2 (part DW + d) + half of its side
-        uint8_t* to = buf[(i - i0) & 1u][(vside ? kFrags : 0) + 2 * part * DW] + 16 * lane;
-#pragma unroll
-        for (uint32_t d = 0; d < DW; d++) {
-            *(bf16x8*)(to + 2048 * d) = widen8<E4M3>(x.r[d].x, x.r[d].y);
-            *(bf16x8*)(to + 2048 * d + 1024) = widen8<E4M3>(x.r[d].z, x.r[d].w);
-        }
+        uint8_t* to = buf[(i - i0) & 1u][(vside ? kFrags : 0) + 2 * (part * DW + d)] + 16 * lane;
+        *(bf16x8*)to = widen8<E4M3>(x.r[d].x, x.r[d].y);
+        *(bf16x8*)(to + 1024) = widen8<E4M3>(x.r[d].z, x.r[d].w);
     };
 
     // Ahead of the tile that is multiplied: its successor's operands wait in
     // registers, the one after that is being loaded, and the table's entries
-    // are read one more tile ahead, so that no load waits for another.
-    int32_t e0 = entry(i0, chst), e1 = entry(i0 + 1, chst), est = entry(i0 + 2, chst);
-    int32_t es = entry(i0, g), esc = entry(i0 + 1, g);
+    // are read one more tile ahead, so that no load waits for another.  A wave
+    // of the first half stages keys of tile i + 1, one of the second half
+    // values of tile i, in its products' phase of tile i.
+    const uint32_t off = vside ? 0u : 1u;
     Next nx;
-    stage_load(i0, e0, nx);
-    stage_store(i0, nx);
-    stage_load(i0 + 1, e1, nx);
+    {
+        const int32_t e0 = entry(i0, chst), e1 = entry(i0 + off, chst);
+        if (!vside) {
+            stage_load(i0, e0, nx);
+#pragma unroll
+            for (uint32_t d = 0; d < DW; d++) stage_store(i0, nx, d);
+        }
+        stage_load(i0 + off, e1, nx);
+    }
+    int32_t est = entry(i0 + off + 1, chst), esc = entry(i0 + 1, g);
     // scales of the lane's own 16 tokens, a tile ahead
     bool oks;
     float ks1 = 1.f, vs1 = 1.f;
     {
-        const float* sp = a.scale + ((uint64_t)page_of(i0, g, es, oks) * c.kv_heads + head) * 2;
+        const float* sp = a.scale + ((uint64_t)page_of(i0, g, entry(i0, g), oks) * c.kv_heads + head) * 2;
         ks1 = sp[0];
         vs1 = sp[1];
     }
+    bf16x8 pb[NR][2];
+    f32x4 s[NR][4];
+    bool prev = false;                                              // pb holds the last tile's probabilities
+    // Operands are read from LDS four at a time, a group ahead of the products
+    // (left to itself, the compiler reads two and waits for them).
+    // Between the groups of the first product, in the shadow of its
+    // instructions, a wave does a step of its staging (for tile i1 nothing).
+    auto stage_step = [&](uint32_t i, uint32_t b) {
+        if (b < DW) stage_store(i + off, nx, b);
+        if (b + 1 == DW) stage_load(i + off + 1, est, nx);
+        if (b == DW) est = entry(i + off + 2, chst);
+    };
+    auto pv_product = [&](uint32_t i) {
+        const uint8_t* vb = buf[(i - i0) & 1u][kFrags] + 16 * lane;
+        bf16x8 f[2][4];
+#pragma unroll
+        for (uint32_t u = 0; u < 4; u++) f[0][u] = *(const bf16x8*)(vb + 1024 * u);
+#pragma unroll
+        for (uint32_t b = 0; b < kFrags / 4; b++) {
+            if (b + 1 < kFrags / 4) {
+#pragma unroll
+                for (uint32_t u = 0; u < 4; u++) f[(b + 1) & 1][u] = *(const bf16x8*)(vb + 1024 * (4 * b + 4 + u));
+            }
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (uint32_t u = 0; u < 4; u++)
+#pragma unroll
+                for (uint32_t n = 0; n < NR; n++)
+                    o[n][2 * b + (u >> 1)] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f[b & 1][u], pb[n][u & 1], o[n][2 * b + (u >> 1)], 0, 0, 0);
+            stage_step(i + 1, b);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+    auto qk_product = [&](uint32_t i) {
+        const uint8_t* kb = buf[(i - i0) & 1u][0] + 16 * lane;
+        bf16x8 f[2][4];
+#pragma unroll
+        for (uint32_t u = 0; u < 4; u++) f[0][u] = *(const bf16x8*)(kb + 1024 * u);
+#pragma unroll
+        for (uint32_t h = 0; h < 4; h++)
+#pragma unroll
+            for (uint32_t n = 0; n < NR; n++) s[n][h] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (uint32_t b = 0; b < kFrags / 4; b++) {
+            if (b + 1 < kFrags / 4) {
+#pragma unroll
+                for (uint32_t u = 0; u < 4; u++) f[(b + 1) & 1][u] = *(const bf16x8*)(kb + 1024 * (4 * b + 4 + u));
+            }
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (uint32_t u = 0; u < 4; u++)
+#pragma unroll
+                for (uint32_t n = 0; n < NR; n++) {
+                    const uint32_t x = 4 * b + u, h = x / (2 * DW), y = x % (2 * DW);
+                    s[n][h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f[b & 1][u], q[n][y >> 1][y & 1], s[n][h], 0, 0, 0);
+                }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+    // The two waves of a SIMD are half a tile apart: while one multiplies (O
+    // += V P of the last tile, S = K Q of this one), the other takes its
+    // exponentials.  Barriers part the phases; in phase 2 i (2 i + 1 for the
+    // second half) tile i's keys and tile i - 1's values are read, so keys of
+    // tile i + 1 and values of tile i can be written to the buffers that
+    // tiles i - 1 and i - 2 have left.
     __syncthreads();
+    if (vside) __syncthreads();
     for (uint32_t i = i0; i < i1; i++) {
-        stage_store(i + 1, nx);
-        stage_load(i + 2, est, nx);
-        est = entry(i + 3, chst);
         const uint32_t tile0 = tl.at(i) * kKvTile;
+        // does the wave see any of the tile, or all of it?
+        bool any = active && (int32_t)tile0 <= whi;
+        bool all = (int32_t)(tile0 + kKvTile - 1) <= wlo;
+        if (a.window) {
+            any = any && ((int64_t)tile0 + kKvTile - 1 > (int64_t)wlo - a.window || tile0 < a.sinks);
+            all = all && ((int64_t)tile0 > (int64_t)whi - a.window || tile0 + kKvTile <= a.sinks);
+        }
+        __builtin_amdgcn_s_setprio(1);
+        if (prev) {
+            pv_product(i - 1);
+        } else {
+#pragma unroll
+            for (uint32_t b = 0; b <= DW; b++) stage_step(i, b);
+        }
+        if (any) qk_product(i);
+        __builtin_amdgcn_s_setprio(0);
+        __syncthreads();
         const bool okv = oks;
         // the scales are powers of two, so log2 of V's is exact
         // (at least 2^-120: a masked logit times it stays -infinity)
@@ -636,40 +726,13 @@ __global__ __launch_bounds__(512, 2) void attend_rows_kernel(KvAttend a, uint32_
             vs1 = sp[1];
         }
         esc = entry(i + 2, g);
-        // does the wave see any of the tile, or all of it?
-        bool any = active && (int32_t)tile0 <= whi;
-        bool all = (int32_t)(tile0 + kKvTile - 1) <= wlo;
-        if (a.window) {
-            any = any && ((int64_t)tile0 + kKvTile - 1 > (int64_t)wlo - a.window || tile0 < a.sinks);
-            all = all && ((int64_t)tile0 > (int64_t)whi - a.window || tile0 + kKvTile <= a.sinks);
-        }
         all = all && __builtin_amdgcn_ballot_w64(!okv) == 0;
         if (any) {
-            const uint8_t* kb = buf[(i - i0) & 1u][0] + 16 * lane;
-            const uint8_t* vb = buf[(i - i0) & 1u][kFrags] + 16 * lane;
-            f32x4 s[NR][4];
-#pragma unroll
-            for (uint32_t h = 0; h < 4; h++) {
-#pragma unroll
-                for (uint32_t n = 0; n < NR; n++) s[n][h] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (uint32_t x = 0; x < 2 * DW; x++) {
-                    const bf16x8 kf = *(const bf16x8*)(kb + 1024 * (2 * DW * h + x));
-#pragma unroll
-                    for (uint32_t n = 0; n < NR; n++)
-                        s[n][h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, q[n][x >> 1][x & 1], s[n][h], 0, 0, 0);
-                }
-            }
-            bf16x8 pb[NR][2];
 #pragma unroll
             for (uint32_t n = 0; n < NR; n++) {
                 float p[16], mul = ks;
 #pragma unroll
                 for (uint32_t e = 0; e < 16; e++) p[e] = s[n][e >> 2][e & 3];
-                if (flip) {
-#pragma unroll
-                    for (uint32_t e = 0; e < 16; e++) p[e] = -p[e];
-                }
                 if (a.softcap > 0.f) {
                     const float in = ks * cap_in;
 #pragma unroll
@@ -712,18 +775,12 @@ __global__ __launch_bounds__(512, 2) void attend_rows_kernel(KvAttend a, uint32_
                     pb[n][y] = __builtin_bit_cast(bf16x8, v4u{pack_bf16(p[8 * y], p[8 * y + 1]), pack_bf16(p[8 * y + 2], p[8 * y + 3]),
                                                               pack_bf16(p[8 * y + 4], p[8 * y + 5]), pack_bf16(p[8 * y + 6], p[8 * y + 7])});
             }
-#pragma unroll
-            for (int d = 0; d < 4 * DW; d++)
-#pragma unroll
-                for (int y = 0; y < 2; y++) {
-                    const bf16x8 vf = *(const bf16x8*)(vb + 1024 * (2 * d + y));
-#pragma unroll
-                    for (uint32_t n = 0; n < NR; n++)
-                        o[n][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, pb[n][y], o[n][d], 0, 0, 0);
-                }
         }
+        prev = any;
         __syncthreads();
     }
+    if (prev) pv_product(i1 - 1);
+    if (!vside) __syncthreads();
     if (bad && c.status) atomicOr(c.status, 4u);
     if (!active) return;
 #pragma unroll
