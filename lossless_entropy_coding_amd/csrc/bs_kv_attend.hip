@@ -56,21 +56,21 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
     return __builtin_bit_cast(uint32_t, r);
 }
 
-// four 8-bit codes to four BF16 (exact)
+// four 8-bit codes times a power of two to four BF16 (exact)
 template <bool E4M3>
-__device__ __forceinline__ v2u widen4(uint32_t c) {
+__device__ __forceinline__ v2u widen4(uint32_t c, float scale) {
     if (E4M3) {
-        const bf16x2 lo = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c, 1.f, false);
-        const bf16x2 hi = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c, 1.f, true);
+        const bf16x2 lo = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c, scale, false);
+        const bf16x2 hi = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c, scale, true);
         return v2u{__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi)};
     }
     const float a = (float)(int8_t)c, b = (float)(int8_t)(c >> 8), d = (float)(int8_t)(c >> 16), e = (float)(int8_t)(c >> 24);
-    return v2u{pack_bf16(a, b), pack_bf16(d, e)};
+    return v2u{pack_bf16(a * scale, b * scale), pack_bf16(d * scale, e * scale)};
 }
 
 template <bool E4M3>
-__device__ __forceinline__ bf16x8 widen8(uint32_t a, uint32_t b) {
-    const v2u x = widen4<E4M3>(a), y = widen4<E4M3>(b);
+__device__ __forceinline__ bf16x8 widen8(uint32_t a, uint32_t b, float scale = 1.f) {
+    const v2u x = widen4<E4M3>(a, scale), y = widen4<E4M3>(b, scale);
     return __builtin_bit_cast(bf16x8, v4u{x.x, x.y, y.x, y.y});
 }
 
@@ -480,12 +480,13 @@ __global__ __launch_bounds__(64 * NW, 2) void attend_kernel(KvAttend a, uint32_t
 // leaves it in LDS as the operands of the products, 1 KiB to each, so that
 // every read of them is 16 B per lane on end.  Two tiles are in LDS.
 //
-// The result is scaled only when a row's maximum has grown by more than 2^8
-// (the exponentials then reach 2^8, as exact in fp32 and BF16 as below 1).
-// The scale of V's page is a power of two and goes into the exponent: with
-// p 2^k in the product, k the page's, the sum of p is that of p 2^k times
-// 2^-k.
-constexpr float kGrow = 8.f;
+// Codes times their page's scale, a power of two, are exact in BF16, so the
+// scales go into the operands.  The exponentials are taken against the
+// maximum of earlier tiles, as long as a lane's 16 of them sum to 2^10 or
+// less (as exact in fp32 and BF16 as below 1); then neither the tile's
+// maximum nor a scaling of the result is needed.  The VALU bounds the loop:
+// 16 exponentials take as long as 64 other instructions.
+constexpr float kGrow = 1024.f;
 
 template <int DW, bool E4M3, int NR>
 __global__ __launch_bounds__(512, 2) void attend_rows_kernel(KvAttend a, uint32_t row_blocks, uint32_t combos) {
@@ -536,8 +537,9 @@ __global__ __launch_bounds__(512, 2) void attend_rows_kernel(KvAttend a, uint32_
     const bool active = w0 < rows;
     const int32_t wlo = base + (int32_t)(min(w0, rows - 1) / a.group);
     const int32_t whi = base + (int32_t)(min(w0 + 16 * NR - 1, rows - 1) / a.group);
-    const float sc = (a.softcap > 0.f ? 1.f : kLog2e) * fabsf(a.qscale);
-    const float cap_in = a.softcap > 0.f ? 2.f * kLog2e / a.softcap : 0.f, cap_out = a.softcap * kLog2e;
+    // to powers of 2 (at least 2^-120: a masked logit times it stays -infinity)
+    const float mul = a.softcap > 0.f ? 1.f : fmaxf(kLog2e * fabsf(a.qscale), 0x1p-120f);
+    const float cap_in = a.softcap > 0.f ? 2.f * kLog2e / a.softcap * fabsf(a.qscale) : 0.f, cap_out = a.softcap * kLog2e;
 
     f32x4 o[NR][4 * DW];
     float mx[NR], sum[NR];
@@ -557,7 +559,8 @@ __global__ __launch_bounds__(512, 2) void attend_rows_kernel(KvAttend a, uint32_
     const uint32_t part = wave & 3u;
     struct Next {
         v4u r[DW];
-        uint32_t keep;          // values: tokens of the lane's chunk that count
+        float scale;
+        uint32_t keep;          // tokens of the lane's chunk that count (keys: 0 or 16)
     };
     uint32_t bad = 0;
     // the table's entry for chunk ch of tile i, -1 past the end
@@ -579,8 +582,9 @@ __global__ __launch_bounds__(512, 2) void attend_rows_kernel(KvAttend a, uint32_
         const uint32_t tile0 = tl.at(i) * kKvTile, at = tile0 + 16 * chst;
         bool ok;
         const uint32_t p = page_of(i, chst, e, ok);
+        x.scale = a.scale[((uint64_t)p * c.kv_heads + head) * 2 + (vside ? 1 : 0)];
+        x.keep = ok ? (vside ? min(end - at, 16u) : 16u) : 0u;
         if (vside) {
-            x.keep = ok ? min(end - at, 16u) : 0u;
             const uint8_t* vp = a.v + (uint64_t)p * c.side_bytes + hoff + (uint64_t)(16 * part * DW + m) * c.page + (at & (c.page - 1));
 #pragma unroll
             for (uint32_t d = 0; d < DW; d++) x.r[d] = *(const v4u*)(vp + (uint64_t)(16 * d) * c.page);
@@ -593,7 +597,7 @@ __global__ __launch_bounds__(512, 2) void attend_rows_kernel(KvAttend a, uint32_
     // operand 2 (part DW + d) of its side, and the next one
     auto stage_store = [&](uint32_t i, Next& x, uint32_t d) {
         if (i >= i1) return;
-        if (vside && x.keep < 16) {
+        if (x.keep < 16) {
 #pragma unroll
             for (int w = 0; w < 4; w++) {
                 const int32_t nb = (int32_t)x.keep - 4 * w;
@@ -601,8 +605,9 @@ __global__ __launch_bounds__(512, 2) void attend_rows_kernel(KvAttend a, uint32_
             }
         }
         uint8_t* to = buf[(i - i0) & 1u][(vside ? kFrags : 0) + 2 * (part * DW + d)] + 16 * lane;
-        *(bf16x8*)to = widen8<E4M3>(x.r[d].x, x.r[d].y);
-        *(bf16x8*)(to + 1024) = widen8<E4M3>(x.r[d].z, x.r[d].w);
+        const float f = x.keep ? x.scale : 1.f;
+        *(bf16x8*)to = widen8<E4M3>(x.r[d].x, x.r[d].y, f);
+        *(bf16x8*)(to + 1024) = widen8<E4M3>(x.r[d].z, x.r[d].w, f);
     };
 
     // Ahead of the tile that is multiplied: its successor's operands wait in
@@ -621,15 +626,7 @@ __global__ __launch_bounds__(512, 2) void attend_rows_kernel(KvAttend a, uint32_
         }
         stage_load(i0 + off, e1, nx);
     }
-    int32_t est = entry(i0 + off + 1, chst), esc = entry(i0 + 1, g);
-    // scales of the lane's own 16 tokens, a tile ahead
-    bool oks;
-    float ks1 = 1.f, vs1 = 1.f;
-    {
-        const float* sp = a.scale + ((uint64_t)page_of(i0, g, entry(i0, g), oks) * c.kv_heads + head) * 2;
-        ks1 = sp[0];
-        vs1 = sp[1];
-    }
+    int32_t est = entry(i0 + off + 1, chst);
     bf16x8 pb[NR][2];
     f32x4 s[NR][4];
     bool prev = false;                                              // pb holds the last tile's probabilities
@@ -716,64 +713,57 @@ __global__ __launch_bounds__(512, 2) void attend_rows_kernel(KvAttend a, uint32_
         if (any) qk_product(i);
         __builtin_amdgcn_s_setprio(0);
         __syncthreads();
-        const bool okv = oks;
-        // the scales are powers of two, so log2 of V's is exact
-        // (at least 2^-120: a masked logit times it stays -infinity)
-        const float ks = fmaxf(ks1 * sc, 0x1p-120f), kexp = okv ? (float)((int32_t)(__builtin_bit_cast(uint32_t, vs1) >> 23) - 127) : 0.f;
-        {
-            const float* sp = a.scale + ((uint64_t)page_of(i + 1, g, esc, oks) * c.kv_heads + head) * 2;
-            ks1 = sp[0];
-            vs1 = sp[1];
-        }
-        esc = entry(i + 2, g);
-        all = all && __builtin_amdgcn_ballot_w64(!okv) == 0;
         if (any) {
 #pragma unroll
             for (uint32_t n = 0; n < NR; n++) {
-                float p[16], mul = ks;
+                float p[16];
 #pragma unroll
                 for (uint32_t e = 0; e < 16; e++) p[e] = s[n][e >> 2][e & 3];
                 if (a.softcap > 0.f) {
-                    const float in = ks * cap_in;
 #pragma unroll
                     for (uint32_t e = 0; e < 16; e++)
-                        p[e] = cap_out - 2.f * cap_out * __builtin_amdgcn_rcpf(exp2_fast(p[e] * in) + 1.f);
-                    mul = 1.f;
+                        p[e] = cap_out - 2.f * cap_out * __builtin_amdgcn_rcpf(exp2_fast(p[e] * cap_in) + 1.f);
                 }
                 if (!all) {
 #pragma unroll
                     for (uint32_t e = 0; e < 16; e++) {
                         const int32_t tk = (int32_t)(tile0 + 16 * g + e);
-                        const bool seen = okv && tk <= pos[n] &&
+                        const bool seen = tk <= pos[n] &&
                                           (a.window == 0 || (int64_t)tk > (int64_t)pos[n] - (int64_t)a.window || (uint32_t)tk < a.sinks);
                         p[e] = seen ? p[e] : -__builtin_inff();
                     }
                 }
-                float top = p[0];
+                // against the maximum so far; only where a row's sum shows
+                // that it has been passed by far (or there is none yet: the
+                // sum is then infinite or NaN) is the new one looked for
+                float x[16], tot = 0.f;
 #pragma unroll
-                for (uint32_t e = 1; e < 16; e++) top = fmaxf(top, p[e]);
-                top = max_groups(top * mul);
-                // mx: what the exponentials are taken against
-                if (__builtin_amdgcn_ballot_w64(top > mx[n] + kGrow) != 0) {
-                    const float now = fmaxf(top, mx[n]), sub = now == -__builtin_inff() ? 0.f : now;
+                for (uint32_t e = 0; e < 16; e++) {
+                    x[e] = exp2_fast(p[e] * mul - mx[n]);
+                    tot += x[e];
+                }
+                if (__builtin_amdgcn_ballot_w64(!(tot <= kGrow)) != 0) {
+                    float top = p[0];
+#pragma unroll
+                    for (uint32_t e = 1; e < 16; e++) top = fmaxf(top, p[e]);
+                    const float now = fmaxf(max_groups(top * mul), mx[n]), sub = now == -__builtin_inff() ? 0.f : now;
                     const float alpha = exp2_fast(mx[n] - sub);
                     mx[n] = now;
                     sum[n] *= alpha;
 #pragma unroll
                     for (int d = 0; d < 4 * DW; d++) o[n][d] *= alpha;
-                }
-                const float sub = (mx[n] == -__builtin_inff() ? 0.f : mx[n]) - kexp;
-                float tot = 0.f;
+                    tot = 0.f;
 #pragma unroll
-                for (uint32_t e = 0; e < 16; e++) {
-                    p[e] = exp2_fast(p[e] * mul - sub);
-                    tot += p[e];
+                    for (uint32_t e = 0; e < 16; e++) {
+                        x[e] = exp2_fast(p[e] * mul - sub);
+                        tot += x[e];
+                    }
                 }
-                sum[n] += tot * exp2_fast(-kexp);
+                sum[n] += tot;
 #pragma unroll
                 for (int y = 0; y < 2; y++)
-                    pb[n][y] = __builtin_bit_cast(bf16x8, v4u{pack_bf16(p[8 * y], p[8 * y + 1]), pack_bf16(p[8 * y + 2], p[8 * y + 3]),
-                                                              pack_bf16(p[8 * y + 4], p[8 * y + 5]), pack_bf16(p[8 * y + 6], p[8 * y + 7])});
+                    pb[n][y] = __builtin_bit_cast(bf16x8, v4u{pack_bf16(x[8 * y], x[8 * y + 1]), pack_bf16(x[8 * y + 2], x[8 * y + 3]),
+                                                              pack_bf16(x[8 * y + 4], x[8 * y + 5]), pack_bf16(x[8 * y + 6], x[8 * y + 7])});
             }
         }
         prev = any;
