@@ -23,17 +23,20 @@ import ctypes as C
 import torch
 
 from . import _lib as L
-from .codec import _stream_handle
+from .codec import _stream_of
+
+_INT32, _BF16, _FP32 = torch.int32, torch.bfloat16, torch.float32
 
 
 def _wide(head_dim: int) -> int:
     return -(-head_dim // 64) * 64
 
 
-def _ids(t: torch.Tensor, name: str) -> torch.Tensor:
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous():
+def _ids(t: torch.Tensor, name: str) -> int:
+    """Checks a vector of row numbers, counts or offsets; returns its length."""
+    if t.dtype is not _INT32 or t.dim() != 1 or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous int32 vector on the device")
-    return t
+    return t.numel()
 
 
 class KvCache:
@@ -82,10 +85,15 @@ class KvCache:
         L.check(L.lib().bs_kv_sizes_get(C.byref(self.c), C.byref(sizes)), "bs_kv_sizes_get")
         self.page_bytes = int(sizes.page_bytes)
         self._page_work = self._attend_work = None
+        self._ref, self._args = C.byref(self.c), L.KvAttendArgs()
+        self._args_ref = C.byref(self._args)
+        self._page_need, self._attend_need = {}, {}        # workspace bytes by the sizes of a call
 
     # ------------------------------------------------------------ pages
     def _work(self, n: int) -> torch.Tensor:
-        need = int(L.lib().bs_kv_pages_work_bytes(C.byref(self.c), n))
+        need = self._page_need.get(n)
+        if need is None:
+            need = self._page_need[n] = int(L.lib().bs_kv_pages_work_bytes(self._ref, n))
         if self._page_work is None or self._page_work.numel() < need:
             self._page_work = torch.empty(max(need, 256), dtype=torch.uint8, device=self.k.device)
         return self._page_work
@@ -93,36 +101,41 @@ class KvCache:
     def extend(self, rows: torch.Tensor, counts: torch.Tensor, stream=None) -> None:
         """Make room for counts[i] more tokens in row rows[i] (distinct rows);
         all rows grow, or none (bs_kv_extend_async)."""
-        _ids(rows, "rows"), _ids(counts, "counts")
-        if rows.numel() != counts.numel():
+        n = _ids(rows, "rows")
+        if _ids(counts, "counts") != n:
             raise ValueError("one count per row")
-        w = self._work(rows.numel())
-        L.check(L.lib().bs_kv_extend_async(C.byref(self.c), rows.numel(), rows.data_ptr(), counts.data_ptr(), w.data_ptr(),
-                                           w.numel(), _stream_handle(stream)), "bs_kv_extend_async")
+        w = self._work(n)
+        rc = L.lib().bs_kv_extend_async(self._ref, n, rows.data_ptr(), counts.data_ptr(), w.data_ptr(), w.numel(),
+                                        _stream_of(rows.device, stream))
+        if rc:
+            L.check(rc, "bs_kv_extend_async")
 
     def fork(self, parents: torch.Tensor, children: torch.Tensor, stream=None) -> None:
         """Empty rows children[i] become copies of rows parents[i], sharing
         their whole pages (bs_kv_fork_async)."""
-        _ids(parents, "parents"), _ids(children, "children")
-        if parents.numel() != children.numel():
+        n = _ids(parents, "parents")
+        if _ids(children, "children") != n:
             raise ValueError("one parent per child")
-        w = self._work(parents.numel())
-        L.check(L.lib().bs_kv_fork_async(C.byref(self.c), parents.numel(), parents.data_ptr(), children.data_ptr(),
-                                         w.data_ptr(), w.numel(), _stream_handle(stream)), "bs_kv_fork_async")
+        w = self._work(n)
+        rc = L.lib().bs_kv_fork_async(self._ref, n, parents.data_ptr(), children.data_ptr(), w.data_ptr(), w.numel(),
+                                      _stream_of(parents.device, stream))
+        if rc:
+            L.check(rc, "bs_kv_fork_async")
 
     def free(self, rows: torch.Tensor, stream=None) -> None:
         """Empty rows (bs_kv_free_async)."""
-        _ids(rows, "rows")
-        L.check(L.lib().bs_kv_free_async(C.byref(self.c), rows.numel(), rows.data_ptr(), _stream_handle(stream)),
-                "bs_kv_free_async")
+        n = _ids(rows, "rows")
+        rc = L.lib().bs_kv_free_async(self._ref, n, rows.data_ptr(), _stream_of(rows.device, stream))
+        if rc:
+            L.check(rc, "bs_kv_free_async")
 
     def copy_pages(self, source: torch.Tensor, target: torch.Tensor, stream=None) -> None:
         """Copy pages in every layer (bs_kv_copy_pages_async)."""
-        _ids(source, "source"), _ids(target, "target")
-        if source.numel() != target.numel():
+        n = _ids(source, "source")
+        if _ids(target, "target") != n:
             raise ValueError("one target per source")
-        L.check(L.lib().bs_kv_copy_pages_async(C.byref(self.c), source.numel(), source.data_ptr(), target.data_ptr(),
-                                               _stream_handle(stream)), "bs_kv_copy_pages_async")
+        L.check(L.lib().bs_kv_copy_pages_async(self._ref, n, source.data_ptr(), target.data_ptr(),
+                                               _stream_of(source.device, stream)), "bs_kv_copy_pages_async")
 
     def compact(self, table_out: torch.Tensor | None = None, refs_out: torch.Tensor | None = None, stream=None) -> None:
         """Move the pages in use to the lowest places (bs_kv_compact_async).
@@ -140,8 +153,8 @@ class KvCache:
             if t.dtype != like.dtype or t.shape != like.shape or not t.is_contiguous():
                 raise ValueError(f"{name} must be a contiguous int32 tensor of shape {tuple(like.shape)}")
         w = self._work(0)
-        L.check(L.lib().bs_kv_compact_async(C.byref(self.c), table_out.data_ptr(), refs_out.data_ptr(), w.data_ptr(),
-                                            w.numel(), _stream_handle(stream)), "bs_kv_compact_async")
+        L.check(L.lib().bs_kv_compact_async(self._ref, table_out.data_ptr(), refs_out.data_ptr(), w.data_ptr(), w.numel(),
+                                            _stream_of(self.k.device, stream)), "bs_kv_compact_async")
         if swap:
             self._spare = (self.table, self.refs)
             self.table, self.refs = table_out, refs_out
@@ -153,20 +166,23 @@ class KvCache:
         by side; returns its token stride."""
         if t.dim() != 3 or t.shape[2] != self.head_dim or (heads is not None and t.shape[1] != heads):
             raise ValueError(f"{name} must be (tokens, {heads or 'heads'}, {self.head_dim})")
-        if t.numel() and ((t.shape[2] > 1 and t.stride(2) != 1) or (t.shape[1] > 1 and t.stride(1) != self.head_dim)):
+        n, h, d = t.shape
+        if t.is_contiguous():
+            return h * d
+        s = t.stride()
+        if t.numel() and ((d > 1 and s[2] != 1) or (h > 1 and s[1] != d)):
             raise ValueError(f"the values of a token must be side by side in {name}")
-        return t.shape[1] * t.shape[2] if t.shape[0] <= 1 else t.stride(0)
+        return h * d if n <= 1 else s[0]
 
     def _rows(self, rows, starts, total, max_new):
-        _ids(rows, "rows")
+        n = _ids(rows, "rows")
         if starts is None:
-            if rows.numel() != total:
-                raise ValueError(f"{total} tokens for {rows.numel()} rows: give starts")
-            return 1
-        _ids(starts, "starts")
-        if starts.numel() != rows.numel() + 1:
+            if n != total:
+                raise ValueError(f"{total} tokens for {n} rows: give starts")
+            return n, 1, None
+        if _ids(starts, "starts") != n + 1:
             raise ValueError("starts holds one offset per row and the end")
-        return max(1, min(total, total if max_new is None else max_new))
+        return n, max(1, min(total, total if max_new is None else max_new)), starts.data_ptr()
 
     def append(self, layer: int, k: torch.Tensor, v: torch.Tensor, rows: torch.Tensor, starts: torch.Tensor | None = None,
                max_new: int | None = None, stream=None) -> None:
@@ -174,15 +190,16 @@ class KvCache:
         (bs_kv_append_async): k and v (tokens, kv_heads, head_dim) bfloat16 or
         float32, tokens starts[i] .. starts[i + 1] - 1 of row rows[i] (without
         starts one each); max_new: the most of one row, if it is known."""
-        if k.dtype != v.dtype or k.dtype not in (torch.bfloat16, torch.float32) or k.shape != v.shape:
+        kind = k.dtype
+        if v.dtype is not kind or (kind is not _BF16 and kind is not _FP32) or k.shape != v.shape:
             raise ValueError("k and v must have one shape and be bfloat16 or float32")
-        ks, vs = self._tokens(k, self.kv_heads, "k"), self._tokens(v, self.kv_heads, "v")
-        most = self._rows(rows, starts, k.shape[0], max_new)
-        rc = L.lib().bs_kv_append_async(C.byref(self.c), layer, rows.numel(), rows.data_ptr(),
-                                        None if starts is None else starts.data_ptr(), k.shape[0], most, k.data_ptr(), ks,
-                                        v.data_ptr(), vs, L.T_FP32 if k.dtype == torch.float32 else L.T_BF16,
-                                        _stream_handle(stream))
-        L.check(rc, "bs_kv_append_async")
+        ks, vs, total = self._tokens(k, self.kv_heads, "k"), self._tokens(v, self.kv_heads, "v"), k.shape[0]
+        n, most, at = self._rows(rows, starts, total, max_new)
+        rc = L.lib().bs_kv_append_async(self._ref, layer, n, rows.data_ptr(), at, total, most, k.data_ptr(), ks,
+                                        v.data_ptr(), vs, L.T_FP32 if kind is _FP32 else L.T_BF16,
+                                        _stream_of(k.device, stream))
+        if rc:
+            L.check(rc, "bs_kv_append_async")
 
     def attend(self, layer: int, q: torch.Tensor, rows: torch.Tensor, starts: torch.Tensor | None = None,
                max_new: int | None = None, max_len: int = 0, scale: float = 0.0, window: int = 0, sinks: int = 0,
@@ -194,31 +211,43 @@ class KvCache:
         1 / sqrt(head_dim).  max_len: no row is longer, if it is known.  Returns
         the result (q's shape, bfloat16), and with lse the logarithms of the
         softmax sums (tokens, heads) as float32."""
-        if q.dtype != torch.bfloat16:
+        if q.dtype is not _BF16:
             raise ValueError("q must be bfloat16")
-        qs = self._tokens(q, None, "q")
+        qs = os = self._tokens(q, None, "q")
+        total, heads, _ = shape = q.shape
         if out is None:
-            out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
-        elif out.dtype != torch.bfloat16 or out.shape != q.shape:
+            out = torch.empty(shape, dtype=_BF16, device=q.device)
+            os = heads * self.head_dim
+        elif out.dtype is not _BF16 or out.shape != shape:
             raise ValueError("out must be bfloat16 of q's shape")
-        os = self._tokens(out, None, "out")
+        else:
+            os = self._tokens(out, None, "out")
         if lse is True:
-            lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
-        elif lse is not False and (lse.dtype != torch.float32 or lse.shape != q.shape[:2] or not lse.is_contiguous()):
+            lse = torch.empty(shape[:2], dtype=_FP32, device=q.device)
+        elif lse is not False and (lse.dtype is not _FP32 or lse.shape != shape[:2] or not lse.is_contiguous()):
             raise ValueError("lse must be a contiguous float32 tensor of (tokens, heads)")
         if window < 0 or sinks < 0 or max_len < 0:
             raise ValueError("window, sinks and max_len are not negative")
-        most = self._rows(rows, starts, q.shape[0], max_new)
-        a = L.KvAttendArgs(layer, rows.numel(), q.shape[1], q.shape[0], most, max_len, rows.data_ptr(),
-                           None if starts is None else starts.data_ptr(), q.data_ptr(), out.data_ptr(),
-                           None if lse is False else lse.data_ptr(), qs, os, scale, softcap, window, sinks)
-        need = int(L.lib().bs_kv_attend_work_bytes(C.byref(self.c), C.byref(a)))
-        if need and (self._attend_work is None or self._attend_work.numel() < need):
-            self._attend_work = torch.zeros(need, dtype=torch.uint8, device=self.k.device)
-        w = self._attend_work if need else None
-        rc = L.lib().bs_kv_attend_async(C.byref(self.c), C.byref(a), w.data_ptr() if need else None,
-                                        w.numel() if need else 0, _stream_handle(stream))
-        L.check(rc, "bs_kv_attend_async")
+        n, most, at = self._rows(rows, starts, total, max_new)
+        a = self._args
+        a.layer, a.n_seqs, a.heads, a.total_q, a.max_new, a.max_len = layer, n, heads, total, most, max_len
+        a.d_seqs, a.d_starts, a.d_q, a.d_out = rows.data_ptr(), at, q.data_ptr(), out.data_ptr()
+        a.d_lse = None if lse is False else lse.data_ptr()
+        a.q_stride, a.out_stride, a.scale, a.softcap, a.window, a.sinks = qs, os, scale, softcap, window, sinks
+        sizes = (n, heads, total, most, max_len, window, sinks)
+        need = self._attend_need.get(sizes)
+        if need is None:
+            if len(self._attend_need) > 4096:              # lengths that grow token by token
+                self._attend_need.clear()
+            need = int(L.lib().bs_kv_attend_work_bytes(self._ref, self._args_ref))
+            self._attend_need[sizes] = need
+        w = self._attend_work
+        if need and (w is None or w.numel() < need):
+            w = self._attend_work = torch.zeros(need, dtype=torch.uint8, device=self.k.device)
+        rc = L.lib().bs_kv_attend_async(self._ref, self._args_ref, w.data_ptr() if need else None, need,
+                                        _stream_of(q.device, stream))
+        if rc:
+            L.check(rc, "bs_kv_attend_async")
         return out if lse is False else (out, lse)
 
     def check(self) -> None:

@@ -16,7 +16,7 @@ import ctypes as C
 import torch
 
 from . import _lib as L
-from .codec import _stream_handle
+from .codec import _stream_of
 
 
 class LoraPack:
@@ -49,7 +49,15 @@ class LoraPack:
         self.factor = torch.tensor([float(s) for _, _, s in adapters], dtype=torch.float32, device=device)
         self.c = L.LoraPack(self.adapters, self.rank, rows, cols, self.a.data_ptr(), self.b.data_ptr(),
                             self.ranks.data_ptr(), self.factor.data_ptr())
-        self._work = None
+        self.ref = C.byref(self.c)
+        self._work, self._need = None, {}
+
+    def work_bytes(self, tokens: int) -> int:
+        """Workspace of add() for this many tokens (bs_lora_work_bytes)."""
+        need = self._need.get(tokens)
+        if need is None:
+            need = self._need[tokens] = int(L.lib().bs_lora_work_bytes(self.ref, tokens))
+        return need
 
     def add(self, y: torch.Tensor, x: torch.Tensor, batch: "LoraBatch", out: torch.Tensor | None = None,
             stream=None) -> torch.Tensor:
@@ -68,16 +76,17 @@ class LoraPack:
         batch.check_for(self, x.shape[0])
         if x.shape[0] == 0:
             return out
-        need = int(L.lib().bs_lora_work_bytes(C.byref(self.c), x.shape[0]))
+        need = self.work_bytes(x.shape[0])
         if self._work is None or self._work.numel() < need:
             self._work = torch.empty(need, dtype=torch.uint8, device=self.a.device)
         one = x.shape[0] == 1
-        rc = L.lib().bs_lora_add_async(C.byref(self.c), batch.dev.data_ptr(), x.shape[0], x.data_ptr(),
+        rc = L.lib().bs_lora_add_async(self.ref, batch.dev.data_ptr(), x.shape[0], x.data_ptr(),
                                        self.cols if one else x.stride(0), y.data_ptr(), out.data_ptr(),
                                        self.rows if one else y.stride(0),
                                        L.T_FP32 if y.dtype == torch.float32 else L.T_BF16, self._work.data_ptr(),
-                                       self._work.numel(), _stream_handle(stream))
-        L.check(rc, "bs_lora_add_async")
+                                       self._work.numel(), _stream_of(x.device, stream))
+        if rc:
+            L.check(rc, "bs_lora_add_async")
         return out
 
 
@@ -99,7 +108,7 @@ class LoraBatch:
         if adapter_of.dtype != torch.int32 or adapter_of.numel() != self.tokens or not adapter_of.is_contiguous():
             raise ValueError(f"adapter_of must be a contiguous int32 vector of {self.tokens}")
         rc = L.lib().bs_lora_batch_async(adapter_of.data_ptr(), self.tokens, self.adapters, self.dev.data_ptr(),
-                                         4 * self.dev.numel(), _stream_handle(stream))
+                                         4 * self.dev.numel(), _stream_of(adapter_of.device, stream))
         L.check(rc, "bs_lora_batch_async")
 
     def bad_indices(self) -> int:
