@@ -55,9 +55,9 @@ bool check_tokens(uint64_t tokens) {
     return false;
 }
 
-// the outer product's grid: tiles times blocks of at most 4096 rows
+// the outer product's grid: tiles times blocks of 256 rows or more
 bool check_grid(const bs_lora_pack* p, uint32_t tokens) {
-    if ((uint64_t)max_tiles(tokens, p->adapters) * ((p->rows + 4095) / 4096) <= 0x7FFFFFFFull) return true;
+    if ((uint64_t)max_tiles(tokens, p->adapters) * ((p->rows + 255) / 256) <= 0x7FFFFFFFull) return true;
     set_error("%u tokens of %u rows are too many for one call", tokens, p->rows);
     return false;
 }

@@ -380,12 +380,13 @@ __global__ __launch_bounds__(256, 2) void outer_kernel(LoraArgs p, uint32_t stri
 
 template <int RT>
 int outer(const LoraArgs& a, hipStream_t st) {
-    // strips of a wave: as many as leave about five workgroups per CU (at
-    // most 16), since each workgroup first finds its tile and joins t
+    // strips of a wave: each workgroup first finds its tile and joins t, so up
+    // to three where 16 workgroups per CU are left (4097 tokens x 14336 rows:
+    // 85 us with 1, 78 with 2 to 4, 85 with 6 or 8)
     int cus = 0;
     if (bsk_device_cus(&cus) != 0 || cus <= 0) cus = 256;
     const uint64_t all = (uint64_t)a.max_tiles * ((a.rows + 255) / 256);
-    const uint32_t strips = (uint32_t)std::min<uint64_t>(16, std::max<uint64_t>(1, all / (5ull * (uint64_t)cus)));
+    const uint32_t strips = (uint32_t)std::min<uint64_t>(3, std::max<uint64_t>(1, all / (16ull * (uint64_t)cus)));
     const uint32_t blocks = (a.rows + 256 * strips - 1) / (256 * strips);
     const dim3 grid(blocks * a.max_tiles);
     if (a.y32) hipLaunchKernelGGL((outer_kernel<RT, true>), grid, dim3(256), 0, st, a, strips, blocks);
