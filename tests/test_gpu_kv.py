@@ -357,6 +357,43 @@ def test_long_rows_are_split(dtype):
         _check(cache, model, rng, [2, 0], [3, 2], 8, **kw)
 
 
+@pytest.mark.parametrize("heads,new", [(4, 1), (16, 40)])
+def test_without_a_workspace(heads, new):
+    """The C call with no workspace: rows are not split, the results hold the same bound."""
+    import ctypes as C
+    from lossless_entropy_coding_amd import _lib as L
+    rng = np.random.default_rng(heads)
+    cache, model = _pair(layers=1, kv_heads=1, head_dim=128, n_pages=60, max_seqs=2, max_pages=40, page_tokens=64, dtype="e4m3")
+    _fill(cache, model, rng, [0, 1], [2300, 700])
+    q = _bf16(rng, 2 * new, heads, 128)
+    qd, out, starts, rows = q.cuda(), torch.zeros(2 * new, heads, 128, dtype=torch.bfloat16, device="cuda"), _ids(0, new, 2 * new), _ids(0, 1)
+    a = L.KvAttendArgs(0, 2, heads, 2 * new, new, 0, rows.data_ptr(), starts.data_ptr(), qd.data_ptr(), out.data_ptr(), None,
+                       heads * 128, heads * 128, 0.0, 0.0, 0, 0)
+    assert L.lib().bs_kv_attend_work_bytes(C.byref(cache.c), C.byref(a)) > 0
+    assert L.lib().bs_kv_attend_async(C.byref(cache.c), C.byref(a), None, 0, None) == L.BS_OK
+    torch.cuda.synchronize()
+    want, _, slack, spread = model.attend(0, _f64(q), [0, 1], [0, new, 2 * new])
+    assert np.all(np.abs(_f64(out) - want) <= S.attend_bound(want, slack, spread))
+
+
+def test_many_rows_of_many_lengths():
+    """Blocks of rows that two, three and more workgroups share, whole ones
+    between them, rows that see nothing, bad table entries elsewhere."""
+    rng = np.random.default_rng(21)
+    lens, new = [3000, 1, 900, 64, 2100, 0], [90, 70, 200, 1, 33, 3]
+    cache, model = _pair(layers=1, kv_heads=2, head_dim=64, n_pages=120, max_seqs=6, max_pages=50, page_tokens=64, dtype="int8")
+    _fill(cache, model, rng, [0, 1, 2, 3, 4], lens[:5])
+    for kw in ({}, dict(window=500, sinks=70), dict(scale=-0.2), dict(softcap=9.0)):
+        for _ in range(2):                          # the counters are back at zero
+            _check(cache, model, rng, [0, 1, 2, 3, 4, 5], new, 6, **kw)
+    cache.table[3, 0] = -7
+    out = cache.attend(0, _bf16(rng, sum(new), 6, 64).cuda(), _ids(0, 1, 2, 3, 4, 5),
+                       _ids(*([0] + [int(x) for x in np.cumsum(new)])), max_new=max(new))
+    assert torch.isfinite(out.float()).all()
+    with pytest.raises(RuntimeError, match="does not exist"):
+        cache.check()
+
+
 def test_children_share_and_diverge():
     """A forked row gives its parent's results, then both go their own ways; compaction moves neither."""
     rng = np.random.default_rng(15)
