@@ -378,7 +378,7 @@ uint64_t bs_fixed_gemm_work_bytes(uint64_t rows, uint64_t cols, uint32_t batch) 
 
 bs_status bs::fixed_gemm(const bs_fixed_info* info, const void* d_blob, uint64_t rows, uint64_t cols, uint32_t batch,
                          const void* d_x, float* d_y, uint32_t* d_status, void* d_work, uint64_t work_bytes,
-                         bool combine, void* stream) {
+                         const bsd::LoraArgs* lora, bool check_only, void* stream) {
     bsd::FixedArgs a;
     const bs_status rc = fixed_args(info, d_blob, a);
     if (rc != BS_OK) return rc;
@@ -419,7 +419,8 @@ bs_status bs::fixed_gemm(const bs_fixed_info* info, const void* d_blob, uint64_t
     if (bsk_device_cus(&cus) != 0 || cus <= 0) cus = 256;
     const uint64_t items = split ? 2 * groups32 : (rows + 15) / 16;
     const uint32_t groups = (uint32_t)std::min<uint64_t>(items, 8ull * (uint64_t)cus);
-    const int e = bsk_fixed_gemm(&a, groups, split ? 1 : 0, combine ? 1 : 0, stream);
+    if (check_only) return BS_OK;
+    const int e = bsk_fixed_gemm(&a, groups, split ? 1 : 0, lora, stream);
     if (e != 0) { set_error("fixed batched product launch: %s", hipGetErrorString((hipError_t)e)); return BS_E_HIP; }
     return BS_OK;
 }
@@ -427,5 +428,5 @@ bs_status bs::fixed_gemm(const bs_fixed_info* info, const void* d_blob, uint64_t
 extern "C" bs_status bs_fixed_gemm_async(const bs_fixed_info* info, const void* d_blob, uint64_t rows, uint64_t cols,
                                          uint32_t batch, const void* d_x, float* d_y, uint32_t* d_status, void* d_work,
                                          uint64_t work_bytes, void* stream) {
-    return fixed_gemm(info, d_blob, rows, cols, batch, d_x, d_y, d_status, d_work, work_bytes, true, stream);
+    return fixed_gemm(info, d_blob, rows, cols, batch, d_x, d_y, d_status, d_work, work_bytes, nullptr, false, stream);
 }

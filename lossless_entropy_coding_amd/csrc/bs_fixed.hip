@@ -37,6 +37,7 @@
 
 #include "bs_device.h"
 #include "bs_fixed_device.h"
+#include "bs_lora_device.h"
 #include "bs_wave.h"
 
 using namespace bsd;
@@ -375,8 +376,55 @@ __global__ __launch_bounds__(256) void combine_kernel(float* __restrict__ y, con
     for (uint64_t i = 4 * n4 + t; i < n; i += stride) y[i] += part[i];
 }
 
-template <int NT, int MF>
-__global__ __launch_bounds__(64 * kGemmWaves) void fixed_gemm_kernel(FixedArgs a) {
+typedef unsigned int v2u __attribute__((ext_vector_type(2)));
+
+// The adapters' part of four rows r .. r + 3 of token n: s_a times the rows of
+// B with the token's inner product, whose shares are added first.  Up to 8
+// shares, 8 ranks at a time, all loads of a step issued together.
+__device__ __forceinline__ f32x4 lora_rows(const LoraArgs& p, uint32_t n, uint32_t r) {
+    f32x4 y = f32x4{0.f, 0.f, 0.f, 0.f};
+    const v2u pair = *(const v2u*)(p.batch + lora_pairs(p.max_tiles, p.tokens) + 2 * n);   // adapter, place
+    if (pair.x >= p.adapters || pair.y >= p.tokens) return y;       // no adapter
+    const uint32_t rank = std::min<uint32_t>((uint32_t)p.ranks[pair.x], p.rank);
+    const float f = p.factor[pair.x];
+    const float* tp = p.t + (uint64_t)pair.y * p.rank;
+    const uint16_t* bp = p.b + (uint64_t)pair.x * p.rows * p.rank;
+    for (uint32_t k = 0; k < rank; k += 8) {
+        v4u b[4];
+#pragma unroll
+        for (uint32_t i = 0; i < 4; i++) b[i] = *(const v4u*)(bp + (uint64_t)std::min(r + i, p.rows - 1) * p.rank + k);
+        f32x4 lo[kLoraSplits], hi[kLoraSplits];
+#pragma unroll
+        for (uint32_t s = 0; s < kLoraSplits; s++) {
+            const float* ts = tp + (uint64_t)std::min(s, p.ksplit - 1) * p.tokens * p.rank + k;
+            lo[s] = *(const f32x4*)ts;
+            hi[s] = *(const f32x4*)(ts + 4);
+        }
+        f32x4 t0 = lo[0], t1 = hi[0];
+#pragma unroll
+        for (uint32_t s = 1; s < kLoraSplits; s++) {
+            if (s >= p.ksplit) break;
+            t0 += lo[s];
+            t1 += hi[s];
+        }
+#pragma unroll
+        for (uint32_t i = 0; i < 4; i++)
+#pragma unroll
+            for (uint32_t e = 0; e < 4; e++) {
+                const uint32_t w = b[i][e];
+                const float x0 = e < 2 ? t0[2 * (e & 1)] : t1[2 * (e & 1)], x1 = e < 2 ? t0[2 * (e & 1) + 1] : t1[2 * (e & 1) + 1];
+                y[i] = __builtin_fmaf(__builtin_bit_cast(float, w << 16), x0, y[i]);
+                y[i] = __builtin_fmaf(__builtin_bit_cast(float, w & 0xFFFF0000u), x1, y[i]);
+            }
+    }
+    return y * f;
+}
+
+// LORA (MF 1): the adapters' outer products are added in the epilogue, whose
+// lanes hold four rows of a token each; a launch of its own for them takes 4
+// us more of the 22 of a lone token on a 4096 x 4096 matrix.
+template <int NT, int MF, bool LORA>
+__global__ __launch_bounds__(64 * kGemmWaves) void fixed_gemm_kernel(FixedArgs a, LoraArgs lora) {
     constexpr uint32_t kRows = 16 * MF;               // rows of a work item
     __shared__ uint32_t lut[256];
     __shared__ __attribute__((aligned(16))) uint8_t wbuf[kRows][kGemmRowBytes];
@@ -499,6 +547,7 @@ __global__ __launch_bounds__(64 * kGemmWaves) void fixed_gemm_kernel(FixedArgs a
         float* dst = split == 2 && kh == 1 ? a.gpart : a.gy;
         if (ks == 0) {
             const uint32_t rows = (uint32_t)a.rows, rg = (uint32_t)r0 + 4 * (lane >> 4);
+            if (LORA && n < a.batch && rg < rows) sum[0] += lora_rows(lora, n, rg);
 #pragma unroll
             for (int m = 0; m < MF; m++)
 #pragma unroll
@@ -519,33 +568,38 @@ extern "C" int bsk_fixed_decode_many(const FixedMany* m, void* stream) {
     return (int)hipGetLastError();
 }
 
-extern "C" int bsk_fixed_gemm(const FixedArgs* args, uint32_t n_groups, int rows32, int combine, void* stream) {
+extern "C" int bsk_fixed_gemm(const FixedArgs* args, uint32_t n_groups, int rows32, const LoraArgs* lora, void* stream) {
     if (n_groups == 0 || args->rows == 0) return 0;
     const dim3 grid(n_groups), block(64 * kGemmWaves);
     hipStream_t st = (hipStream_t)stream;
     const uint32_t nt = (args->batch + 15) / 16;
+    const LoraArgs none = {};
     if (rows32) {
         if (args->ksplit != 1 && args->ksplit != 2) return (int)hipErrorInvalidValue;
         if (args->ksplit == 2 && (!args->gpart || args->cols < 2 * kFixBlockW)) return (int)hipErrorInvalidValue;
         switch (nt) {
-            case 1: hipLaunchKernelGGL((fixed_gemm_kernel<1, 2>), grid, block, 0, st, *args); break;
-            case 2: hipLaunchKernelGGL((fixed_gemm_kernel<2, 2>), grid, block, 0, st, *args); break;
+            case 1: hipLaunchKernelGGL((fixed_gemm_kernel<1, 2, false>), grid, block, 0, st, *args, none); break;
+            case 2: hipLaunchKernelGGL((fixed_gemm_kernel<2, 2, false>), grid, block, 0, st, *args, none); break;
             case 3:
-            case 4: hipLaunchKernelGGL((fixed_gemm_kernel<4, 2>), grid, block, 0, st, *args); break;
+            case 4: hipLaunchKernelGGL((fixed_gemm_kernel<4, 2, false>), grid, block, 0, st, *args, none); break;
             default: return (int)hipErrorInvalidValue;
         }
-        if (args->ksplit == 2 && combine) {
+        if (args->ksplit == 2 && !lora) {
             const uint64_t n = (uint64_t)args->batch * args->rows;
             const uint32_t cgrid = (uint32_t)std::min<uint64_t>((n / 4 + 255) / 256 + 1, 2048);
             hipLaunchKernelGGL(combine_kernel, dim3(cgrid), dim3(256), 0, st, args->gy, args->gpart, n);
         }
         return (int)hipGetLastError();
     }
+    auto go = [&](auto with, auto without) {
+        if (lora) hipLaunchKernelGGL(with, grid, block, 0, st, *args, *lora);
+        else hipLaunchKernelGGL(without, grid, block, 0, st, *args, none);
+    };
     switch (nt) {
-        case 1: hipLaunchKernelGGL((fixed_gemm_kernel<1, 1>), grid, block, 0, st, *args); break;
-        case 2: hipLaunchKernelGGL((fixed_gemm_kernel<2, 1>), grid, block, 0, st, *args); break;
+        case 1: go(fixed_gemm_kernel<1, 1, true>, fixed_gemm_kernel<1, 1, false>); break;
+        case 2: go(fixed_gemm_kernel<2, 1, true>, fixed_gemm_kernel<2, 1, false>); break;
         case 3:
-        case 4: hipLaunchKernelGGL((fixed_gemm_kernel<4, 1>), grid, block, 0, st, *args); break;
+        case 4: go(fixed_gemm_kernel<4, 1, true>, fixed_gemm_kernel<4, 1, false>); break;
         default: return (int)hipErrorInvalidValue;
     }
     return (int)hipGetLastError();

@@ -6,6 +6,8 @@
 
 namespace bsd {
 
+struct LoraArgs;
+
 // fixed-width lane-stream form (layout in bs.h): one wavefront decodes a
 // block of 2048 weights (64 lanes x 32) at a time
 constexpr uint32_t kFixHeader = 96;
@@ -71,9 +73,10 @@ int bsk_fixed_decode_many(const bsd::FixedMany* m, void* stream);
 // the fused product of a fixed-width blob with a batch of vectors: one
 // workgroup of kGemmWaves waves per 16 rows (rows32 0), or per 32 rows and
 // args->ksplit shares of the panels (rows32 1; with 2 shares a second launch
-// adds the workspace's sums into Y unless combine is 0: then the caller adds
-// them); n_groups workgroups, striding
-int bsk_fixed_gemm(const bsd::FixedArgs* args, uint32_t n_groups, int rows32, int combine, void* stream);
+// adds the workspace's sums into Y); n_groups workgroups, striding.  With
+// lora, the rows32 0 form adds the adapters' outer products, and the other
+// leaves the second launch to the caller
+int bsk_fixed_gemm(const bsd::FixedArgs* args, uint32_t n_groups, int rows32, const bsd::LoraArgs* lora, void* stream);
 // the fused product of a fixed-width blob with a vector: n_groups workgroups
 // of kFixWaves waves, each workgroup striding over the row groups
 int bsk_fixed_gemv(const bsd::FixedArgs* args, uint32_t n_groups, void* stream);

@@ -10,6 +10,10 @@
 
 #include "bs.h"
 
+namespace bsd {
+struct LoraArgs;
+}
+
 namespace bs {
 
 // container constants (the layout is documented in bs.h)
@@ -92,12 +96,14 @@ uint64_t plan_device_bytes(const bs_plan* plan);   // device memory the plan all
 uint64_t plan_status_words(const bs_plan* plan);   // status words a full decode writes
 uint32_t plan_records(const bs_plan* plan);
 
-// bs_fixed_gemm_async; with combine false the split product's second half
+// bs_fixed_gemm_async with adapters whose inner products are in lora->t: the
+// product adds them where it is not split; the split product's second half
 // (given a workspace and cols >= 4096) stays in the workspace, batch x rows
-// floats, for the caller to add into Y (bs_fixed.cpp).
+// floats, for the caller to add into Y (bs_fixed.cpp).  lora NULL: the plain
+// product.  check_only: nothing is enqueued.
 bs_status fixed_gemm(const bs_fixed_info* info, const void* d_blob, uint64_t rows, uint64_t cols, uint32_t batch,
-                     const void* d_x, float* d_y, uint32_t* d_status, void* d_work, uint64_t work_bytes, bool combine,
-                     void* stream);
+                     const void* d_x, float* d_y, uint32_t* d_status, void* d_work, uint64_t work_bytes,
+                     const bsd::LoraArgs* lora, bool check_only, void* stream);
 
 // Validate h (len bytes) completely (header, directory, tables, chunk index
 // and payload bounds) and fill c.  Returns BS_OK or an error with a message.

@@ -104,7 +104,7 @@ extern "C" {
 
 uint64_t bs_lora_batch_bytes(uint32_t tokens, uint32_t adapters) {
     if (!check_tokens(tokens) || adapters == 0 || adapters > bsd::kLoraAdapters) return 0;
-    return align_up(4ull * (bsd::kLoraHead + 4ull * max_tiles(tokens, adapters) + tokens), 16);
+    return align_up(4ull * (bsd::lora_pairs(max_tiles(tokens, adapters), tokens) + 2ull * tokens), 16);
 }
 
 bs_status bs_lora_batch_async(const int32_t* d_adapter_of, uint32_t tokens, uint32_t adapters, int32_t* d_batch,
@@ -191,8 +191,6 @@ bs_status bs_fixed_gemm_lora_async(const bs_fixed_info* info, const void* d_blob
     }
     const uint64_t split = bs_fixed_gemm_work_bytes(rows, cols, batch);
     void* part = split ? d_work : nullptr;
-    const bs_status r1 = fixed_gemm(info, d_blob, rows, cols, batch, d_x, d_y, d_status, part, split, false, stream);
-    if (r1 != BS_OK) return r1;
     bsd::LoraArgs a;
     fill(pack, d_batch, batch, d_x, cols, (float*)((uint8_t*)d_work + align_up(split, 256)), a);
     a.y_in = d_y;
@@ -201,8 +199,14 @@ bs_status bs_fixed_gemm_lora_async(const bs_fixed_info* info, const void* d_blob
     a.y32 = 1;
     a.y_vec = aligned(d_y, 16) && rows % 4 == 0;
     a.part = (const float*)part;
-    const bs_status r2 = launched(bsk_lora_inner(&a, stream), "adapters' inner product");
-    if (r2 != BS_OK) return r2;
+    // the projection's arguments are checked before anything is enqueued
+    const bs_status r0 = fixed_gemm(info, d_blob, rows, cols, batch, d_x, d_y, d_status, part, split, &a, true, stream);
+    if (r0 != BS_OK) return r0;
+    const bs_status r1 = launched(bsk_lora_inner(&a, stream), "adapters' inner product");
+    if (r1 != BS_OK) return r1;
+    // without the split, the projection's own epilogue adds the outer product
+    const bs_status r2 = fixed_gemm(info, d_blob, rows, cols, batch, d_x, d_y, d_status, part, split, &a, false, stream);
+    if (r2 != BS_OK || !split) return r2;
     return launched(bsk_lora_outer(&a, stream), "adapters' outer product");
 }
 

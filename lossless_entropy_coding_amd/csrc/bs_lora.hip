@@ -84,7 +84,11 @@ __global__ __launch_bounds__(1024) void batch_kernel(const int32_t* idx, uint32_
     for (uint32_t i = t; i < tokens; i += 1024) {
         int32_t a = idx[i];
         if (a < -1 || a >= (int32_t)adapters) a = -1;
-        out[kLoraHead + 4 * max_tiles + atomicAdd(&cur[a + 1], 1u)] = (int32_t)i;
+        const uint32_t at = atomicAdd(&cur[a + 1], 1u);
+        out[kLoraHead + 4 * max_tiles + at] = (int32_t)i;
+        int32_t* pair = out + lora_pairs(max_tiles, tokens) + 2 * i;
+        pair[0] = a;
+        pair[1] = (int32_t)at;
     }
     if (t == 0) {
         out[0] = (int32_t)til;

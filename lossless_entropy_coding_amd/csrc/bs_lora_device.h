@@ -16,7 +16,9 @@ struct LoraArgs {
     const uint16_t* b;          // [adapters][rows][rank]
     const int32_t* ranks;       // each adapter's own rank
     const float* factor;
-    const int32_t* batch;       // head, tiles of 4 words (adapter, first, count, 0), then the tokens in tile order
+    // head, tiles of 4 words (adapter, first, count, 0), the tokens in tile
+    // order, then each token's adapter and place in that order
+    const int32_t* batch;
     const uint16_t* x;
     uint64_t x_stride;
     const void* y_in;           // BF16 or fp32
@@ -30,6 +32,9 @@ struct LoraArgs {
     int y32;
     int y_vec;                  // y (and part) can be read and written 16 B at a time
 };
+
+// the first word of a batch's per-token pairs (16-B aligned)
+inline constexpr uint32_t lora_pairs(uint32_t max_tiles, uint32_t tokens) { return (kLoraHead + 4 * max_tiles + tokens + 3) / 4 * 4; }
 
 }  // namespace bsd
 
