@@ -603,8 +603,10 @@ bs_status bs_lora_add_async(const bs_lora_pack* pack, const int32_t* d_batch, ui
 
 /* bs_fixed_gemm_async with adapters: Y[b] = W X[b] + s_a B_a (A_a X[b]), W the
  * weights of a fixed-width blob, decoded where they are used.  The adapters'
- * second product also joins the two halves of the split product, so no
- * launch and no pass over Y is added for it.  d_work: 256-B aligned, at least
+ * second product is added in the product's own epilogue, or, where the
+ * columns are shared out over workgroups, by the launch that adds the
+ * shares.  Entries of tokens without an adapter equal bs_fixed_gemm_async's
+ * within the fp32 bound (bit for bit where the shares are the same).  d_work: 256-B aligned, at least
  * bs_fixed_gemm_lora_work_bytes (0: a shape or pack that is refused).  Other
  * arguments and errors as for bs_fixed_gemm_async and bs_lora_add_async. */
 uint64_t bs_fixed_gemm_lora_work_bytes(uint64_t rows, uint64_t cols, uint32_t batch, const bs_lora_pack* pack);

@@ -17,6 +17,7 @@
 #include "bs_fixed_device.h"
 #include "bs_encode_device.h"
 #include "bs_internal.h"
+#include "bs_lora_device.h"
 
 using namespace bs;
 
@@ -402,22 +403,24 @@ bs_status bs::fixed_gemm(const bs_fixed_info* info, const void* d_blob, uint64_t
     // the split product: 32 rows per work item, two items per group of rows
     // (cols >= 4096), given a workspace for the second half's sums
     const uint64_t groups32 = (rows + 31) / 32;
-    const bool split = d_work != nullptr && cols >= 2 * bsd::kFixBlockW;
+    // (beside adapters: as many shares as the caller has decided)
+    const bool split = lora ? lora->nparts > 0 : d_work != nullptr && cols >= 2 * bsd::kFixBlockW;
     if (split) {
+        const uint32_t parts = lora ? lora->nparts : 1;
         if ((uintptr_t)d_work & 255) { set_error("the workspace must be 256-B aligned"); return BS_E_INVAL; }
-        if (work_bytes < 4ull * batch * rows) {
+        if (work_bytes < 4ull * parts * batch * rows) {
             set_error("workspace of %llu B, %llu B needed", (unsigned long long)work_bytes,
-                      (unsigned long long)(4ull * batch * rows));
+                      (unsigned long long)(4ull * parts * batch * rows));
             return BS_E_INVAL;
         }
         const uintptr_t w0 = (uintptr_t)d_work, y0 = (uintptr_t)d_y, sz = (uintptr_t)(4ull * batch * rows);
-        if (w0 < y0 + sz && y0 < w0 + sz) { set_error("the workspace overlaps Y"); return BS_E_INVAL; }
-        a.ksplit = 2;
+        if (w0 < y0 + sz && y0 < w0 + sz * parts) { set_error("the workspace overlaps Y"); return BS_E_INVAL; }
+        a.ksplit = parts + 1;
         a.gpart = (float*)d_work;
     }
     int cus = 0;
     if (bsk_device_cus(&cus) != 0 || cus <= 0) cus = 256;
-    const uint64_t items = split ? 2 * groups32 : (rows + 15) / 16;
+    const uint64_t items = split ? a.ksplit * groups32 : (rows + 15) / 16;
     const uint32_t groups = (uint32_t)std::min<uint64_t>(items, 8ull * (uint64_t)cus);
     if (check_only) return BS_OK;
     const int e = bsk_fixed_gemm(&a, groups, split ? 1 : 0, lora, stream);

@@ -349,7 +349,8 @@ __global__ __launch_bounds__(64 * kFixWaves) void fixed_gemv_kernel(FixedArgs a)
 // panels to one work item and the second half to another.  The first stores its partial sums
 // in Y, the second in the workspace, and combine_kernel, launched next on the
 // same stream, adds the second into the first: every Y entry is P0 + P1, one
-// value on every run.  (Combining in this kernel, by whichever work item
+// value on every run.  (Beside adapters ksplit may be larger, for few rows;
+// the launch that adds the adapters' part adds the shares, too.)  (Combining in this kernel, by whichever work item
 // arrives second, needs an agent-scope acquire, which invalidates the XCD's
 // L2 and with it the X lines the other workgroups are reading; it measured
 // slower than the second launch.)
@@ -443,15 +444,13 @@ __global__ __launch_bounds__(64 * kGemmWaves) void fixed_gemm_kernel(FixedArgs a
     constexpr uint32_t kSlice = kFixBlockW / kWpt; // panel columns per wave
     const uint32_t nt = wave / kWpt, ks = wave % kWpt;
     const uint32_t bpr = a.cols / kFixBlockW;
-    const uint32_t split = MF == 2 && a.ksplit == 2 && bpr >= 2 ? 2u : 1u;   // every share holds a panel
-    const uint32_t p_mid = (bpr + 1) / 2;          // the first share's panels: 0 .. p_mid - 1
+    const uint32_t split = MF == 2 ? std::min(a.ksplit, bpr) : 1u;           // every share holds a panel
     const uint64_t groups = (a.rows + kRows - 1) / kRows;
     const uint64_t items = groups * split;
     for (uint64_t item = blockIdx.x; item < items; item += gridDim.x) {
         const uint64_t g = item / split;
         const uint32_t kh = (uint32_t)(item % split);
-        const uint32_t p0 = split == 1 ? 0u : (kh == 0 ? 0u : p_mid);
-        const uint32_t p1 = split == 1 ? bpr : (kh == 0 ? p_mid : bpr);
+        const uint32_t p0 = (kh * bpr + split - 1) / split, p1 = ((kh + 1) * bpr + split - 1) / split;   // its panels
         const uint64_t r0 = kRows * g;
         f32x4 acc[MF];
 #pragma unroll
@@ -544,7 +543,7 @@ __global__ __launch_bounds__(64 * kGemmWaves) void fixed_gemm_kernel(FixedArgs a
             }
         }
         // D row 4 (lane / 16) + i of row tile m, column lane % 16
-        float* dst = split == 2 && kh == 1 ? a.gpart : a.gy;
+        float* dst = kh ? a.gpart + (uint64_t)(kh - 1) * a.batch * a.rows : a.gy;
         if (ks == 0) {
             const uint32_t rows = (uint32_t)a.rows, rg = (uint32_t)r0 + 4 * (lane >> 4);
             if (LORA && n < a.batch && rg < rows) sum[0] += lora_rows(lora, n, rg);
@@ -575,8 +574,8 @@ extern "C" int bsk_fixed_gemm(const FixedArgs* args, uint32_t n_groups, int rows
     const uint32_t nt = (args->batch + 15) / 16;
     const LoraArgs none = {};
     if (rows32) {
-        if (args->ksplit != 1 && args->ksplit != 2) return (int)hipErrorInvalidValue;
-        if (args->ksplit == 2 && (!args->gpart || args->cols < 2 * kFixBlockW)) return (int)hipErrorInvalidValue;
+        if (args->ksplit == 0 || (!lora && args->ksplit > 2)) return (int)hipErrorInvalidValue;
+        if (args->ksplit > 1 && (!args->gpart || args->cols < args->ksplit * kFixBlockW)) return (int)hipErrorInvalidValue;
         switch (nt) {
             case 1: hipLaunchKernelGGL((fixed_gemm_kernel<1, 2, false>), grid, block, 0, st, *args, none); break;
             case 2: hipLaunchKernelGGL((fixed_gemm_kernel<2, 2, false>), grid, block, 0, st, *args, none); break;

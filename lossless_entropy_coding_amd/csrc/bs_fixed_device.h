@@ -40,9 +40,9 @@ struct FixedArgs {
     // (row-major BF16), Y batch x rows in gy (row-major fp32), cols a
     // multiple of 2048 so that every row starts on a block
     uint32_t batch;
-    uint32_t ksplit;        // 1, or 2: two workgroups share a group of rows, one half of its panels each
-    // the split product's workspace: the second half's partial sums
-    // (batch x rows fp32, laid out as Y)
+    uint32_t ksplit;        // workgroups that share a group of rows, a part of its panels each (2 at most without adapters)
+    // the split product's workspace: the partial sums of the shares after the
+    // first (each batch x rows fp32, laid out as Y)
     float* gpart;
 };
 

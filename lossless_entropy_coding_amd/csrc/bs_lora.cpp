@@ -72,6 +72,30 @@ uint32_t share_rule(const bs_lora_pack* p, uint32_t tiles) {
     return (blocks + turns - 1) / turns;         // as many turns of 512 columns with the fewest workgroups
 }
 
+// Shares of the columns' panels (of 2048) in the product beside adapters.
+// With few rows there are fewer groups of 32 rows than CUs, so as many shares
+// as the CUs take at once (at most 8: each is a pass over Y in the last
+// launch; a third share of 112 groups, more than the CUs take, made 64 tokens
+// on 3584 x 14336 20% slower).  54 tokens on 163 x 14336: 63 us with two
+// shares, 38 with seven.  From 8 tokens on at least two, as in the plain
+// product; below, one wherever that is as fast, since the product's epilogue
+// then adds the adapters (4 tokens on 2000 x 4096: 17.1 us with one, 18.8
+// with two).
+uint32_t panel_shares(uint64_t rows, uint64_t cols, uint32_t tokens) {
+    int cus = 0;
+    if (bsk_device_cus(&cus) != 0 || cus <= 0) cus = 256;
+    const uint64_t panels = cols / 2048, groups = (rows + 31) / 32;
+    if (panels < 2 || (tokens < 8 && (panels < 4 || (rows + 15) / 16 * 2 >= (uint64_t)cus))) return 1;
+    const uint64_t want = std::max<uint64_t>(1, std::min<uint64_t>({(uint64_t)cus / groups, panels, 8}));
+    const uint64_t turns = (panels + want - 1) / want, shares = (panels + turns - 1) / turns;
+    return (uint32_t)std::max<uint64_t>(shares, tokens >= 8 ? 2 : 1);
+}
+
+// the partial sums of the shares after the first
+uint64_t shares_bytes(uint64_t rows, uint64_t cols, uint32_t tokens) {
+    return 4ull * (panel_shares(rows, cols, tokens) - 1) * tokens * rows;
+}
+
 uint64_t inner_bytes(const bs_lora_pack* p, uint32_t tokens) {
     return align_up(4ull * share_rule(p, max_tiles(tokens, p->adapters)) * tokens * p->rank, 256);
 }
@@ -167,7 +191,7 @@ bs_status bs_lora_add_async(const bs_lora_pack* pack, const int32_t* d_batch, ui
 
 uint64_t bs_fixed_gemm_lora_work_bytes(uint64_t rows, uint64_t cols, uint32_t batch, const bs_lora_pack* pack) {
     if (check_pack(pack) != BS_OK || batch == 0 || batch > 64) return 0;
-    return align_up(bs_fixed_gemm_work_bytes(rows, cols, batch), 256) + inner_bytes(pack, batch);
+    return align_up(shares_bytes(rows, cols, batch), 256) + inner_bytes(pack, batch);
 }
 
 bs_status bs_fixed_gemm_lora_async(const bs_fixed_info* info, const void* d_blob, uint64_t rows, uint64_t cols,
@@ -189,7 +213,7 @@ bs_status bs_fixed_gemm_lora_async(const bs_fixed_info* info, const void* d_blob
                   (unsigned long long)bs_fixed_gemm_lora_work_bytes(rows, cols, batch, pack));
         return BS_E_INVAL;
     }
-    const uint64_t split = bs_fixed_gemm_work_bytes(rows, cols, batch);
+    const uint64_t split = shares_bytes(rows, cols, batch);
     void* part = split ? d_work : nullptr;
     bsd::LoraArgs a;
     fill(pack, d_batch, batch, d_x, cols, (float*)((uint8_t*)d_work + align_up(split, 256)), a);
@@ -199,6 +223,8 @@ bs_status bs_fixed_gemm_lora_async(const bs_fixed_info* info, const void* d_blob
     a.y32 = 1;
     a.y_vec = aligned(d_y, 16) && rows % 4 == 0;
     a.part = (const float*)part;
+    a.part_stride = (uint64_t)batch * rows;
+    a.nparts = panel_shares(rows, cols, batch) - 1;
     // the projection's arguments are checked before anything is enqueued
     const bs_status r0 = fixed_gemm(info, d_blob, rows, cols, batch, d_x, d_y, d_status, part, split, &a, true, stream);
     if (r0 != BS_OK) return r0;

