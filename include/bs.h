@@ -728,7 +728,7 @@ typedef struct {
     uint32_t layer, n_seqs;
     uint32_t heads;             /* query heads, a multiple of kv_heads: head h reads key head h / (heads / kv_heads) */
     uint32_t total_q, max_new;  /* query tokens in all, and the most of one row */
-    uint32_t max_len;           /* no row in the call is longer (0: max_pages pages); only splits the work */
+    uint32_t max_len;           /* how long rows are at most (0: max_pages pages); only splits the work */
     const int32_t* d_seqs;      /* rows (a row may be named more than once) */
     const int32_t* d_starts;    /* n_seqs + 1 offsets into the queries, or NULL: one each */
     const void* d_q;            /* BF16 [total_q][heads][head_dim], q_stride elements between tokens */

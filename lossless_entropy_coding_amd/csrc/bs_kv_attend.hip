@@ -290,7 +290,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attend_kernel(KvAttend a, uint32_t
     const Tiles tl = get_tiles(a, lo, hi);
     const uint32_t i0 = split * a.chunk;
     if (split > 0 && i0 >= tl.n) return;
-    const uint32_t i1 = a.splits > 1 ? min(tl.n, i0 + a.chunk) : tl.n;
+    const uint32_t i1 = split + 1 < a.splits ? min(tl.n, i0 + a.chunk) : tl.n;   // the last takes what is left
     const int32_t* trow = c.table + (uint64_t)(uint32_t)max(sq.row, 0) * c.max_pages;
     const uint64_t hoff = (uint64_t)head * c.page * c.wide;
     const uint32_t end = (uint32_t)(hi + 1);                        // tokens past it are seen by no row
@@ -428,7 +428,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attend_kernel(KvAttend a, uint32_t
         for (int d = 0; d < 4 * DW; d++) *(f32x4*)&os[wave][m][16 * d + 4 * g] = o[d];
     }
     __syncthreads();
-    const uint32_t parts = a.splits > 1 ? max(1u, (tl.n + a.chunk - 1) / a.chunk) : 1u;   // workgroups of these rows
+    const uint32_t parts = min(max(1u, (tl.n + a.chunk - 1) / a.chunk), a.splits);   // workgroups of these rows
     for (uint32_t i = t; i < nrows * (D / 4); i += 64 * NW) {
         const uint32_t n = i / (D / 4), ch = 4 * (i % (D / 4));
         float top = -__builtin_inff(), total = 0.f;
@@ -511,7 +511,7 @@ __global__ __launch_bounds__(512, 2) void attend_rows_kernel(KvAttend a, uint32_
     const Tiles tl = get_tiles(a, base + (int32_t)(wg0 / a.group), base + (int32_t)((wg1 - 1) / a.group));
     const uint32_t i0 = split * a.chunk;
     if (split > 0 && i0 >= tl.n) return;
-    const uint32_t i1 = a.splits > 1 ? min(tl.n, i0 + a.chunk) : tl.n;
+    const uint32_t i1 = split + 1 < a.splits ? min(tl.n, i0 + a.chunk) : tl.n;   // the last takes what is left
     const uint32_t end = (uint32_t)(base + (int32_t)((wg1 - 1) / a.group) + 1);   // (only read where tiles exist)
 
     const uint32_t w0 = wg0 + 16 * NR * wave;                       // the wave's first row
@@ -798,7 +798,7 @@ __global__ __launch_bounds__(64) void join_kernel(KvAttend a, uint32_t block_row
     const int32_t base = sq.len - sq.count;
     const uint32_t r1 = min(r0 + block_rows, (uint32_t)sq.count * a.group) - 1;
     const Tiles tl = get_tiles(a, base + (int32_t)(r0 / a.group), base + (int32_t)(r1 / a.group));
-    join_row<DW>(a, (uint32_t)sq.s0 + j, qh, ch, max(1u, (tl.n + a.chunk - 1) / a.chunk));
+    join_row<DW>(a, (uint32_t)sq.s0 + j, qh, ch, min(max(1u, (tl.n + a.chunk - 1) / a.chunk), a.splits));
 }
 
 // rows of a workgroup of attend_rows_kernel: two row tiles to a wave where

@@ -208,7 +208,8 @@ class KvCache:
         (bs_kv_attend_async): q (tokens, heads, head_dim) bfloat16, tokens as in
         append.  window: 0 or how many of the last tokens a query sees, besides
         the first `sinks`; softcap c: logits become c tanh(logit / c); scale 0:
-        1 / sqrt(head_dim).  max_len: no row is longer, if it is known.  Returns
+        1 / sqrt(head_dim).  max_len: how long the rows are at most, if it is
+        known (it decides how the work is split, not the result).  Returns
         the result (q's shape, bfloat16), and with lse the logarithms of the
         softmax sums (tokens, heads) as float32."""
         if q.dtype is not _BF16:

@@ -394,6 +394,33 @@ def test_many_rows_of_many_lengths():
         cache.check()
 
 
+@pytest.mark.parametrize("new", [1, 30])
+def test_rows_longer_than_said(new):
+    rng = np.random.default_rng(31)
+    cache, model = _pair(layers=1, kv_heads=1, head_dim=64, n_pages=150, max_seqs=2, max_pages=140, page_tokens=64, dtype="int8")
+    _fill(cache, model, rng, [0, 1], [8500, 40])
+    for max_len in (1, 300, 3000):
+        for _ in range(2):
+            _check(cache, model, rng, [0, 1], [new, new], 8, max_len=max_len)
+
+
+def test_query_ranges_that_do_not_exist():
+    rng = np.random.default_rng(32)
+    cache, model = _pair(layers=1, kv_heads=1, head_dim=64, n_pages=10, max_seqs=2, max_pages=4, page_tokens=16, dtype="int8")
+    _fill(cache, model, rng, [0, 1], [40, 20])
+    for heads in (2, 64):                           # few and many rows
+        q = _bf16(rng, 3, heads, 64).cuda()
+        want = cache.attend(0, q, _ids(0, 1), _ids(0, 2, 3), max_new=3)
+        for starts in ((0, 2, 4), (-1, 2, 3), (2, 0, 3), (0, 2, 1)):
+            out = torch.zeros_like(q)
+            cache.attend(0, q, _ids(0, 1), _ids(*starts), max_new=3, out=out)
+            torch.cuda.synchronize()
+            assert int(cache.status.item()) == 4
+            cache.status.zero_()
+            if starts[:2] == (0, 2):
+                assert torch.equal(out[:2], want[:2])       # the other row is as it was
+
+
 def test_children_share_and_diverge():
     """A forked row gives its parent's results, then both go their own ways; compaction moves neither."""
     rng = np.random.default_rng(15)
