@@ -5,6 +5,7 @@ Usage: python -m lossless_entropy_coding_amd.build [--asm DIR]
 from __future__ import annotations
 
 import argparse
+import concurrent.futures
 import os
 import shutil
 import subprocess
@@ -36,8 +37,7 @@ def hipcc() -> str:
 def build_lib(asm_dir: str | None = None, verbose: bool = False) -> str:
     cc = hipcc()
     with tempfile.TemporaryDirectory() as tmp:
-        objs = []
-        for src in SOURCES:
+        def compile_one(src: str) -> str:
             obj = os.path.join(tmp, src + ".o")
             cmd = [cc, *HIP_FLAGS, "-c", os.path.join(CSRC, src), "-o", obj]
             if asm_dir and src.endswith(".hip"):
@@ -51,7 +51,10 @@ def build_lib(asm_dir: str | None = None, verbose: bool = False) -> str:
             if r.returncode != 0:
                 sys.stderr.write(r.stdout + r.stderr)
                 raise RuntimeError(f"compiling {src} failed")
-            objs.append(obj)
+            return obj
+
+        with concurrent.futures.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 1)) as pool:
+            objs = list(pool.map(compile_one, SOURCES))
         tmp_lib = LIB + ".tmp"
         r = subprocess.run([cc, "-shared", "-fPIC", f"--offload-arch={ARCH}", *objs, "-o", tmp_lib, "-lpthread"],
                            capture_output=True, text=True)
