@@ -203,37 +203,23 @@ __device__ __forceinline__ void three(float v, __bf16& a, __bf16& b, __bf16& c) 
     c = (__bf16)(r - (float)b);
 }
 
-// y of 4 (fp32) or 8 (BF16) rows from element `at`, n of them inside
+// y of 4 (fp32) or 8 (BF16) rows from element `at`, n of them inside, as it
+// is in memory (FROM: y or one of the parts)
 template <bool Y32>
-__device__ __forceinline__ void load_y(const LoraArgs& p, uint64_t at, uint32_t n, float* y) {
-    constexpr uint32_t N = Y32 ? 4 : 8;
-    if (p.y_vec && n >= N) {
-        if (Y32) {
-            const f32x4 v = *(const f32x4*)((const float*)p.y_in + at);
+__device__ __forceinline__ v4u load_some(const void* from, uint64_t at, uint32_t n) {
+    v4u v = {0, 0, 0, 0};
 #pragma unroll
-            for (uint32_t e = 0; e < 4; e++) y[e] = v[e];
-            for (uint32_t k = 0; k < p.nparts; k++) {
-                const f32x4 w = *(const f32x4*)(p.part + k * p.part_stride + at);
-#pragma unroll
-                for (uint32_t e = 0; e < 4; e++) y[e] += w[e];
-            }
-        } else {
-            const v4u v = *(const v4u*)((const uint16_t*)p.y_in + at);
-#pragma unroll
-            for (uint32_t e = 0; e < 4; e++) {
-                const uint32_t w = v[e];
-                y[2 * e] = bf(w & 0xFFFFu);
-                y[2 * e + 1] = __builtin_bit_cast(float, w & 0xFFFF0000u);
-            }
-        }
-        return;
-    }
-#pragma unroll
-    for (uint32_t e = 0; e < N; e++)
+    for (uint32_t e = 0; e < (Y32 ? 4u : 8u); e++)
         if (e < n) {
-            y[e] = Y32 ? ((const float*)p.y_in)[at + e] : bf(((const uint16_t*)p.y_in)[at + e]);
-            for (uint32_t k = 0; Y32 && k < p.nparts; k++) y[e] += p.part[k * p.part_stride + at + e];
+            if (Y32) v[e] = ((const uint32_t*)from)[at + e];
+            else v[e / 2] |= (uint32_t)((const uint16_t*)from)[at + e] << (16 * (e & 1u));
         }
+    return v;
+}
+
+template <bool Y32>
+__device__ __forceinline__ v4u load_all(const void* from, uint64_t at) {
+    return *(const v4u*)((const uint8_t*)from + at * (Y32 ? 4 : 2));
 }
 
 template <bool Y32>
@@ -260,16 +246,29 @@ __device__ __forceinline__ void store_y(const LoraArgs& p, uint64_t at, uint32_t
         }
 }
 
+// x of lane l ^ 1
+__device__ __forceinline__ float from_neighbour(float x) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, x), 0xB1, 0xF, 0xF, true));
+}
+
 // grid: blocks of rows x tiles, the blocks of a tile side by side, so that
-// neighbouring workgroups fill whole rows of y; a workgroup's waves take `strips` strips of 64 rows in turn.  The
-// workgroup first adds the shares of t and leaves its three BF16 parts in
-// LDS, in the order of the product's operand.  The 64 rows of a strip are
-// dealt to the four 16-row products such that a lane ends up with rows that
-// lie side by side in y: 4 (fp32, 16 j + 4 g ..) or 8 (BF16, 32 j + 8 g ..)
-// to each 16-B access, and the four lane groups fill 64 B of a token's row.
-// The next strip's y is loaded before this one's is stored.
+// neighbouring workgroups fill whole rows of y; a workgroup's waves take
+// `strips` strips of 64 rows in turn.  The workgroup first adds the shares of
+// t and leaves its three BF16 parts in LDS, in the order of the product's
+// operand.  The 64 rows of a strip are dealt to the four 16-row products such
+// that a lane ends up with rows that lie side by side in y: 4 (fp32, 16 j +
+// 4 g ..) or 8 (BF16, 32 j + 8 g ..) to each 16-B access, and the four lane
+// groups fill 64 B of a token's row.  In BF16 two neighbouring lanes then swap
+// halves, so that each access fills whole lines of 128 B (62.7 instead of 64.8
+// us on the case below; in fp32 it gained nothing).
+//
+// y's traffic bounds it: 235 MB of 4097 tokens x 14336 rows in BF16 in 50.5 us,
+// 4.7 TB/s, as fast as a large copy.  What is read ahead stays as it is in
+// memory until it is added (a conversion beside the load made every load wait
+// for the one before: 62.7 us).  Four waves per SIMD: 64 tokens of a decode
+// batch are 3.5 waves per SIMD on 3584 rows, one more round with less.
 template <int RT, bool Y32>
-__global__ __launch_bounds__(256, 2) void outer_kernel(LoraArgs p, uint32_t strips, uint32_t blocks) {
+__global__ __launch_bounds__(256, RT <= 4 ? 4 : 2) void outer_kernel(LoraArgs p, uint32_t strips, uint32_t blocks) {
     constexpr int KC = (RT + 1) / 2;             // steps of 32 ranks
     constexpr int NB = RT == 1 ? 2 : 3;
     // part n of step k, lane's 8 ranks
@@ -281,27 +280,44 @@ __global__ __launch_bounds__(256, 2) void outer_kernel(LoraArgs p, uint32_t stri
     const uint32_t t = threadIdx.x, lane = t & 63u, m = lane & 15u, g = lane >> 4;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(t >> 6);
     const uint32_t begin = (rb * 4 * strips + wave) * 64;
-    const bool mine = m < tl.count;
-    const uint32_t tok = token_at(p, tl.first + min(m, tl.count - 1));
-    const uint64_t yrow = (uint64_t)tok * p.y_stride;
+    // lanes 2 q and 2 q + 1 go to tokens 2 q and 2 q + 1 in turn, half a line each
+    constexpr bool kPairs = !Y32;
     constexpr uint32_t N = Y32 ? 4 : 8, NY = 16 / N;
+    const uint32_t odd = m & 1u, q0 = kPairs ? m - odd : m, q1 = kPairs ? q0 + 1 : m;
+    const uint64_t yrow[2] = {(uint64_t)token_at(p, tl.first + min(q0, tl.count - 1)) * p.y_stride,
+                              (uint64_t)token_at(p, tl.first + min(q1, tl.count - 1)) * p.y_stride};
+    const bool mine[2] = {q0 < tl.count, q1 < tl.count};
     // rows of the lane's access i of the strip at s0, and how many are inside
-    auto row_of = [&](uint32_t s0, uint32_t i) { return s0 + (Y32 ? 16 * i + 4 * g : 32 * i + 8 * g); };
-    auto left_of = [&](uint32_t r) { return mine && r < p.rows ? p.rows - r : 0u; };
-    float next[16];
+    auto row_of = [&](uint32_t s0, uint32_t i) { return s0 + 4 * N * (kPairs ? (i & ~1u) + odd : i) + N * g; };
+    auto left_of = [&](uint32_t r, uint32_t i) { return mine[i & 1u] && r < p.rows ? p.rows - r : 0u; };
+    // what is read ahead stays as it is in memory until it is added: a
+    // conversion beside the load waits for each load before the next
+    v4u next[NY];
+    auto load_y = [&](uint32_t s0) {
+        const bool whole = p.y_vec && s0 + 64 <= p.rows;
+        if (whole) {
 #pragma unroll
-    for (uint32_t i = 0; i < NY; i++) {
-        const uint32_t r = row_of(begin, i), n = left_of(r);
-        if (n) load_y<Y32>(p, yrow + r, n, next + N * i);
-    }
-    bf16x8 a[4][KC], b[NB][KC];
+            for (uint32_t i = 0; i < NY; i++)
+                if (mine[i & 1u]) next[i] = load_all<Y32>(p.y_in, yrow[i & 1u] + row_of(s0, i));
+        } else {
+#pragma unroll
+            for (uint32_t i = 0; i < NY; i++) {
+                const uint32_t r = row_of(s0, i), n = left_of(r, i);
+                next[i] = load_some<Y32>(p.y_in, yrow[i & 1u] + r, n);
+            }
+        }
+    };
+    load_y(begin);
+    bf16x8 a[4][KC];
     uint32_t nk = 0;
     auto load_b = [&](uint32_t s0) {
+        const uint32_t in = min(s0, p.rows - 1), left = p.rows - 1 - in;
+        const uint16_t* base = p.b + ((uint64_t)(uint32_t)tl.adapter * p.rows + in) * p.rank;
 #pragma unroll
         for (uint32_t j = 0; j < 4; j++) {
             // row m of product j: lane group m / 4, element m % 4
-            const uint32_t r = s0 + (Y32 ? 16 * j + m : 32 * (j >> 1) + 8 * (m >> 2) + 4 * (j & 1u) + (m & 3u));
-            const uint16_t* bp = p.b + ((uint64_t)tl.adapter * p.rows + min(r, p.rows - 1)) * p.rank;
+            const uint32_t r = Y32 ? 16 * j + m : 32 * (j >> 1) + 8 * (m >> 2) + 4 * (j & 1u) + (m & 3u);
+            const uint16_t* bp = base + min(r, left) * p.rank;
 #pragma unroll
             for (uint32_t k = 0; k < KC; k++)
                 if (k < nk) a[j][k] = *(const bf16x8*)(bp + (RT == 1 ? 8 * (g & 1u) : 32 * k + 8 * g));
@@ -311,19 +327,24 @@ __global__ __launch_bounds__(256, 2) void outer_kernel(LoraArgs p, uint32_t stri
         nk = min((uint32_t)(p.ranks[tl.adapter] + 31) / 32, (uint32_t)KC);
         const float f = p.factor[tl.adapter];
         load_b(begin);
-        // t[token q][rank r] for the tile's 16 tokens
+        // t[token q][rank r] for the tile's 16 tokens; all loads go out together
+        float w[RT][kLoraSplits];
 #pragma unroll
-        for (uint32_t i = t; i < 256 * RT; i += 256) {
-            const uint32_t q = i / (16 * RT), r = i % (16 * RT);
+        for (uint32_t i = 0; i < RT; i++) {
+            const uint32_t q = (t + 256 * i) / (16 * RT), r = (t + 256 * i) % (16 * RT);
+            const uint32_t at = q * p.rank + r;
+#pragma unroll
+            for (uint32_t s = 0; s < kLoraSplits; s++)
+                if (s < p.ksplit && q < tl.count) w[i][s] = (p.t + ((uint64_t)s * p.tokens + tl.first) * p.rank)[at];
+        }
+#pragma unroll
+        for (uint32_t i = 0; i < RT; i++) {
+            const uint32_t q = (t + 256 * i) / (16 * RT), r = (t + 256 * i) % (16 * RT);
             float v = 0.f;
-            if (q < tl.count) {
-                const float* tp = p.t + ((uint64_t)tl.first + q) * p.rank + r;
-                float w[kLoraSplits];            // the shares' loads go out together
 #pragma unroll
-                for (uint32_t s = 0; s < kLoraSplits; s++) w[s] = s < p.ksplit ? tp[(uint64_t)s * p.tokens * p.rank] : 0.f;
-#pragma unroll
-                for (uint32_t s = 0; s < kLoraSplits; s++) v += w[s];
-            }
+            for (uint32_t s = 0; s < kLoraSplits; s++)
+                if (s < p.ksplit) v += w[i][s];
+            if (q >= tl.count) v = 0.f;
             __bf16 x, y, z;
             three(v * f, x, y, z);
             const uint32_t l = 16 * ((r >> 3) & 3u) + q, e = r & 7u;
@@ -340,44 +361,91 @@ __global__ __launch_bounds__(256, 2) void outer_kernel(LoraArgs p, uint32_t stri
             }
         }
         __syncthreads();
-#pragma unroll
-        for (int n = 0; n < NB; n++)
-#pragma unroll
-            for (int k = 0; k < KC; k++) b[n][k] = *(const bf16x8*)tb[n][k][lane];
     }
     for (uint32_t s = 0; s < strips; s++) {
         const uint32_t s0 = begin + 256 * s;
         if (s0 >= p.rows) break;
-        float y[16];
+        float y[16], add[16];
+        const bool more = s + 1 < strips && s0 + 256 < p.rows;
+        auto take_y = [&]() {
 #pragma unroll
-        for (int e = 0; e < 16; e++) y[e] = next[e];
-        if (s + 1 < strips) {
+            for (uint32_t i = 0; i < NY; i++)
 #pragma unroll
-            for (uint32_t i = 0; i < NY; i++) {
-                const uint32_t r = row_of(s0 + 256, i), n = left_of(r);
-                if (n) load_y<Y32>(p, yrow + r, n, next + N * i);
-            }
-        }
-        if (tl.adapter >= 0) {
-#pragma unroll
-            for (uint32_t j = 0; j < 4; j++) {
-                f32x4 acc = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (uint32_t k = 0; k < KC; k++)
-                    if (k < nk) {
-#pragma unroll
-                        for (int n = NB - 1; n >= 0; n--)
-                            acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[j][k], b[n][k], acc, 0, 0, 0);
+                for (uint32_t e = 0; e < 4; e++) {
+                    const uint32_t w = next[i][e];
+                    if (Y32) y[4 * i + e] = __builtin_bit_cast(float, w);
+                    else {
+                        y[8 * i + 2 * e] = bf(w & 0xFFFFu);
+                        y[8 * i + 2 * e + 1] = __builtin_bit_cast(float, w & 0xFFFF0000u);
                     }
+                }
+            for (uint32_t k = 0; Y32 && k < p.nparts; k++) {
+                const float* from = p.part + k * p.part_stride;
+                v4u w[NY];
 #pragma unroll
-                for (uint32_t e = 0; e < 4; e++) y[4 * j + e] += acc[e];
+                for (uint32_t i = 0; i < NY; i++) {
+                    const uint32_t r = row_of(s0, i);
+                    if (p.y_vec && s0 + 64 <= p.rows) {
+                        if (mine[i & 1u]) w[i] = load_all<true>(from, yrow[i & 1u] + r);
+                    } else w[i] = load_some<true>(from, yrow[i & 1u] + r, left_of(r, i));
+                }
+#pragma unroll
+                for (uint32_t i = 0; i < NY; i++)
+#pragma unroll
+                    for (uint32_t e = 0; e < 4; e++) {
+                        const uint32_t u = w[i][e];
+                        y[4 * i + e] += __builtin_bit_cast(float, u);
+                    }
             }
-            if (s + 1 < strips) load_b(s0 + 256);
+            if (more) load_y(s0 + 256);
+        };
+        auto multiply = [&]() {
+            if (tl.adapter >= 0) {
+                // t is read again for each strip: kept in registers it would cost a wave of each SIMD
+                asm volatile("" ::: "memory");
+                bf16x8 b[NB][KC];
+#pragma unroll
+                for (int n = 0; n < NB; n++)
+#pragma unroll
+                    for (int k = 0; k < KC; k++) b[n][k] = *(const bf16x8*)tb[n][k][lane];
+#pragma unroll
+                for (uint32_t j = 0; j < 4; j++) {
+                    f32x4 acc = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (uint32_t k = 0; k < KC; k++)
+                        if (k < nk) {
+#pragma unroll
+                            for (int n = NB - 1; n >= 0; n--)
+                                acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[j][k], b[n][k], acc, 0, 0, 0);
+                        }
+#pragma unroll
+                    for (uint32_t e = 0; e < 4; e++) add[4 * j + e] = acc[e];
+                }
+            }
+        };
+        // the next strip's y is asked for as early as the registers allow: in
+        // fp32, before the products, it would spill
+        if (!Y32) take_y();
+        multiply();
+        if (Y32) take_y();
+        if (more && tl.adapter >= 0) load_b(s0 + 256);
+        if (tl.adapter >= 0) {
+            if (kPairs) {
+#pragma unroll
+                for (uint32_t e = 0; e < 8; e++) {
+                    const float keep = odd ? add[8 + e] : add[e], other = from_neighbour(odd ? add[e] : add[8 + e]);
+                    y[e] += odd ? other : keep;
+                    y[8 + e] += odd ? keep : other;
+                }
+            } else {
+#pragma unroll
+                for (uint32_t e = 0; e < 16; e++) y[e] += add[e];
+            }
         }
 #pragma unroll
         for (uint32_t i = 0; i < NY; i++) {
-            const uint32_t r = row_of(s0, i), n = left_of(r);
-            if (n) store_y<Y32>(p, yrow + r, n, y + N * i);
+            const uint32_t r = row_of(s0, i), n = left_of(r, i);
+            if (n) store_y<Y32>(p, yrow[i & 1u] + r, n, y + N * i);
         }
     }
 }
@@ -385,12 +453,12 @@ __global__ __launch_bounds__(256, 2) void outer_kernel(LoraArgs p, uint32_t stri
 template <int RT>
 int outer(const LoraArgs& a, hipStream_t st) {
     // strips of a wave: each workgroup first finds its tile and joins t, so up
-    // to three where 16 workgroups per CU are left (4097 tokens x 14336 rows:
-    // 85 us with 1, 78 with 2 to 4, 85 with 6 or 8)
+    // to four where 16 workgroups per CU are left (4097 tokens x 14336 rows in
+    // BF16: 58.4 us with 1, 52.6, 51.8 and 50.5 with 2, 3 and 4, 54.1 with 5)
     int cus = 0;
     if (bsk_device_cus(&cus) != 0 || cus <= 0) cus = 256;
     const uint64_t all = (uint64_t)a.max_tiles * ((a.rows + 255) / 256);
-    const uint32_t strips = (uint32_t)std::min<uint64_t>(3, std::max<uint64_t>(1, all / (16ull * (uint64_t)cus)));
+    const uint32_t strips = (uint32_t)std::min<uint64_t>(4, std::max<uint64_t>(1, all / (16ull * (uint64_t)cus)));
     const uint32_t blocks = (a.rows + 256 * strips - 1) / (256 * strips);
     const dim3 grid(blocks * a.max_tiles);
     if (a.y32) hipLaunchKernelGGL((outer_kernel<RT, true>), grid, dim3(256), 0, st, a, strips, blocks);
