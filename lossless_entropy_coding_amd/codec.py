@@ -13,6 +13,7 @@ copies non-BF16 spans verbatim.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes as C
 from dataclasses import dataclass
 
@@ -32,6 +33,23 @@ def _stream_of(device: torch.device, stream) -> int:
     """The handle of `stream`, or of the device's current stream, without
     making a Stream object (2.7 us of each call of a decode step)."""
     return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else int(stream.cuda_stream)
+
+
+def _on(stream):
+    """The context in which memory for a call on `stream` is allocated and
+    filled: on another stream it could be reused, or zeroed, too late."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def _grown(old: torch.Tensor | None, need: int, device, stream, kept: list, zero: bool = False) -> torch.Tensor:
+    """A workspace of `need` bytes or more in place of `old`, which goes to
+    `kept`: a captured graph or another stream may still use it.  Each is at
+    least twice as large as the one before, so those kept are smaller in all."""
+    size = max(need, 256, 2 * old.numel() if old is not None else 0)
+    if old is not None:
+        kept.append(old)
+    with _on(stream):
+        return (torch.zeros if zero else torch.empty)(size, dtype=torch.uint8, device=device)
 
 
 def params(chunk_weights: int = 65536, lanes: int = 128, m_s: int = 12, m_f: int = 10, max_tables: int = 6,
@@ -562,12 +580,16 @@ class FixedPlan:
             raise ValueError(f"x must be a contiguous (tokens, {cols}) bfloat16 tensor")
         batch.check_for(pack, x.shape[0])
         if out is None:
-            out = torch.empty(x.shape[0], rows, dtype=torch.float32, device=self.dev.device)
+            with _on(stream):
+                out = torch.empty(x.shape[0], rows, dtype=torch.float32, device=self.dev.device)
         elif out.dtype != torch.float32 or tuple(out.shape) != (x.shape[0], rows) or not out.is_contiguous():
             raise ValueError(f"out must be a contiguous ({x.shape[0]}, {rows}) float32 tensor")
         need = int(L.lib().bs_fixed_gemm_lora_work_bytes(rows, cols, x.shape[0], pack.ref))
-        if getattr(self, "_lora_work", None) is None or self._lora_work.numel() < need:
-            self._lora_work = torch.empty(max(need, 256), dtype=torch.uint8, device=self.dev.device)
+        old = getattr(self, "_lora_work", None)
+        if old is None:
+            self._lora_kept = []
+        if old is None or old.numel() < need:
+            self._lora_work = _grown(old, need, self.dev.device, stream, self._lora_kept)
         rc = L.lib().bs_fixed_gemm_lora_async(C.byref(self.info), self.dev.data_ptr(), rows, cols, x.shape[0],
                                               x.data_ptr(), out.data_ptr(), self.status.data_ptr() if status else None,
                                               pack.ref, batch.dev.data_ptr(), self._lora_work.data_ptr(),

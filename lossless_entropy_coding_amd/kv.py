@@ -23,7 +23,7 @@ import ctypes as C
 import torch
 
 from . import _lib as L
-from .codec import _stream_of
+from .codec import _grown, _on, _stream_of
 
 _INT32, _BF16, _FP32 = torch.int32, torch.bfloat16, torch.float32
 
@@ -84,18 +84,18 @@ class KvCache:
         sizes = L.KvSizes()
         L.check(L.lib().bs_kv_sizes_get(C.byref(self.c), C.byref(sizes)), "bs_kv_sizes_get")
         self.page_bytes = int(sizes.page_bytes)
-        self._page_work = self._attend_work = None
+        self._page_work, self._attend_work, self._kept = None, None, []
         self._ref, self._args = C.byref(self.c), L.KvAttendArgs()
         self._args_ref = C.byref(self._args)
         self._page_need, self._attend_need = {}, {}        # workspace bytes by the sizes of a call
 
     # ------------------------------------------------------------ pages
-    def _work(self, n: int) -> torch.Tensor:
+    def _work(self, n: int, stream) -> torch.Tensor:
         need = self._page_need.get(n)
         if need is None:
             need = self._page_need[n] = int(L.lib().bs_kv_pages_work_bytes(self._ref, n))
         if self._page_work is None or self._page_work.numel() < need:
-            self._page_work = torch.empty(max(need, 256), dtype=torch.uint8, device=self.k.device)
+            self._page_work = _grown(self._page_work, need, self.k.device, stream, self._kept)
         return self._page_work
 
     def extend(self, rows: torch.Tensor, counts: torch.Tensor, stream=None) -> None:
@@ -104,7 +104,7 @@ class KvCache:
         n = _ids(rows, "rows")
         if _ids(counts, "counts") != n:
             raise ValueError("one count per row")
-        w = self._work(n)
+        w = self._work(n, stream)
         rc = L.lib().bs_kv_extend_async(self._ref, n, rows.data_ptr(), counts.data_ptr(), w.data_ptr(), w.numel(),
                                         _stream_of(rows.device, stream))
         if rc:
@@ -116,7 +116,7 @@ class KvCache:
         n = _ids(parents, "parents")
         if _ids(children, "children") != n:
             raise ValueError("one parent per child")
-        w = self._work(n)
+        w = self._work(n, stream)
         rc = L.lib().bs_kv_fork_async(self._ref, n, parents.data_ptr(), children.data_ptr(), w.data_ptr(), w.numel(),
                                       _stream_of(parents.device, stream))
         if rc:
@@ -141,18 +141,20 @@ class KvCache:
         """Move the pages in use to the lowest places (bs_kv_compact_async).
         With table_out and refs_out the new table and counts go there and the
         cache keeps its own; without, the cache goes on with the new ones in
-        tensors of its own, kept for the next time."""
+        tensors of its own, kept for the next time (a captured graph goes on
+        with those it was captured with: capture it again)."""
         if (table_out is None) != (refs_out is None):
             raise ValueError("table_out and refs_out go together")
         swap = table_out is None
         if swap:
             if getattr(self, "_spare", None) is None:
-                self._spare = (torch.empty_like(self.table), torch.empty_like(self.refs))
+                with _on(stream):
+                    self._spare = (torch.empty_like(self.table), torch.empty_like(self.refs))
             table_out, refs_out = self._spare
         for t, like, name in ((table_out, self.table, "table_out"), (refs_out, self.refs, "refs_out")):
             if t.dtype != like.dtype or t.shape != like.shape or not t.is_contiguous():
                 raise ValueError(f"{name} must be a contiguous int32 tensor of shape {tuple(like.shape)}")
-        w = self._work(0)
+        w = self._work(0, stream)
         L.check(L.lib().bs_kv_compact_async(self._ref, table_out.data_ptr(), refs_out.data_ptr(), w.data_ptr(), w.numel(),
                                             _stream_of(self.k.device, stream)), "bs_kv_compact_async")
         if swap:
@@ -217,14 +219,16 @@ class KvCache:
         qs = os = self._tokens(q, None, "q")
         total, heads, _ = shape = q.shape
         if out is None:
-            out = torch.empty(shape, dtype=_BF16, device=q.device)
+            with _on(stream):
+                out = torch.empty(shape, dtype=_BF16, device=q.device)
             os = heads * self.head_dim
         elif out.dtype is not _BF16 or out.shape != shape:
             raise ValueError("out must be bfloat16 of q's shape")
         else:
             os = self._tokens(out, None, "out")
         if lse is True:
-            lse = torch.empty(shape[:2], dtype=_FP32, device=q.device)
+            with _on(stream):
+                lse = torch.empty(shape[:2], dtype=_FP32, device=q.device)
         elif lse is not False and (lse.dtype is not _FP32 or lse.shape != shape[:2] or not lse.is_contiguous()):
             raise ValueError("lse must be a contiguous float32 tensor of (tokens, heads)")
         if window < 0 or sinks < 0 or max_len < 0:
@@ -244,7 +248,7 @@ class KvCache:
             self._attend_need[sizes] = need
         w = self._attend_work
         if need and (w is None or w.numel() < need):
-            w = self._attend_work = torch.zeros(need, dtype=torch.uint8, device=self.k.device)
+            w = self._attend_work = _grown(w, need, self.k.device, stream, self._kept, zero=True)
         rc = L.lib().bs_kv_attend_async(self._ref, self._args_ref, w.data_ptr() if need else None, need,
                                         _stream_of(q.device, stream))
         if rc:

@@ -16,7 +16,7 @@ import ctypes as C
 import torch
 
 from . import _lib as L
-from .codec import _stream_of
+from .codec import _grown, _on, _stream_of
 
 
 class LoraPack:
@@ -50,7 +50,7 @@ class LoraPack:
         self.c = L.LoraPack(self.adapters, self.rank, rows, cols, self.a.data_ptr(), self.b.data_ptr(),
                             self.ranks.data_ptr(), self.factor.data_ptr())
         self.ref = C.byref(self.c)
-        self._work, self._need = None, {}
+        self._work, self._kept, self._need = None, [], {}
 
     def work_bytes(self, tokens: int) -> int:
         """Workspace of add() for this many tokens (bs_lora_work_bytes)."""
@@ -78,7 +78,7 @@ class LoraPack:
             return out
         need = self.work_bytes(x.shape[0])
         if self._work is None or self._work.numel() < need:
-            self._work = torch.empty(need, dtype=torch.uint8, device=self.a.device)
+            self._work = _grown(self._work, need, self.a.device, stream, self._kept)
         one = x.shape[0] == 1
         rc = L.lib().bs_lora_add_async(self.ref, batch.dev.data_ptr(), x.shape[0], x.data_ptr(),
                                        self.cols if one else x.stride(0), y.data_ptr(), out.data_ptr(),
@@ -100,7 +100,8 @@ class LoraBatch:
             raise ValueError("adapter_of must be a contiguous int32 vector")
         self.tokens, self.adapters = int(adapter_of.numel()), int(adapters)
         need = int(L.lib().bs_lora_batch_bytes(self.tokens, self.adapters)) if 1 <= adapters <= 4096 else 0
-        self.dev = torch.empty(max(need // 4, 4), dtype=torch.int32, device=adapter_of.device)
+        with _on(stream):
+            self.dev = torch.empty(max(need // 4, 4), dtype=torch.int32, device=adapter_of.device)
         self.update(adapter_of, stream)
 
     def update(self, adapter_of: torch.Tensor, stream=None) -> None:

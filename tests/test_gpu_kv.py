@@ -543,3 +543,51 @@ def test_work_on_another_stream():
     out, ref, slack, spread = model.attend(0, _f64(q), [0, 1])
     assert np.all(np.abs(_f64(got) - out) <= S.attend_bound(out, slack, spread))
     _same(cache, model)
+
+
+def test_a_call_on_another_stream_waits_for_nothing_on_this_one():
+    rng = np.random.default_rng(33)
+    cache, model = _pair(layers=1, kv_heads=1, head_dim=64, n_pages=130, max_seqs=2, max_pages=100, page_tokens=64, dtype="int8")
+    _fill(cache, model, rng, [0, 1], [5000, 700])
+    q, rows = _bf16(rng, 2, 4, 64).cuda(), _ids(0, 1)
+    want = cache.attend(0, q, rows)
+    fresh = kv.KvCache.over(cache.k, cache.v, cache.scale, cache.refs, cache.table, cache.lens, 64, "int8")
+    full = torch.full((1 << 22,), 0x5A, dtype=torch.uint8, device="cuda")
+    a = torch.zeros(4096, 4096, device="cuda")
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    del full                                         # memory that is not zero, for whoever asks next
+    for _ in range(20):
+        a = a @ a                                    # keeps the current stream busy
+    got = fresh.attend(0, q, rows, stream=s)
+    s.synchronize()
+    assert torch.equal(got, want)
+    torch.cuda.synchronize()
+
+
+def test_a_graph_outlives_a_larger_workspace():
+    rng = np.random.default_rng(34)
+    cache, model = _pair(layers=1, kv_heads=1, head_dim=64, n_pages=130, max_seqs=8, max_pages=100, page_tokens=64, dtype="e4m3")
+    _fill(cache, model, rng, [0, 1], [3000, 2000])
+    q, rows, out = _bf16(rng, 1, 4, 64).cuda(), _ids(0), torch.empty(1, 4, 64, dtype=torch.bfloat16, device="cuda")
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        cache.attend(0, q, rows, out=out)
+    torch.cuda.synchronize()
+    small, want = cache._attend_work, out.clone()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        cache.attend(0, q, rows, out=out)
+    address = small.data_ptr()
+    del small
+    many = _ids(*([0, 1] * 40))
+    cache.attend(0, _bf16(rng, 80, 32, 64).cuda(), many)
+    assert cache._attend_work.data_ptr() != address
+    others = [torch.full((1 << k,), 7, dtype=torch.uint8, device="cuda") for k in range(9, 22)]
+    for _ in range(3):
+        out.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+    assert all(bool((t == 7).all()) for t in others)
