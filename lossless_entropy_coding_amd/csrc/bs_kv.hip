@@ -12,6 +12,12 @@
 // workgroup (a scan over the counts, 4096 at a time, that ends with the last
 // page wanted); the copies and the rows of the table are filled by as many
 // workgroups as they need.
+//
+// Measured: copies run at a large copy's rate (compaction of 42 layers, 0.7 GB
+// read and as much written: 290 us, 4.8 TB/s; fork's copies of 42 layers, 32
+// children: 29 us).  A scan of 1000 pages' counts takes 3 to 6 us, a chain of
+// loads and barriers, so one workgroup: calls on few rows are bound by that
+// and by their launches.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

@@ -7,7 +7,8 @@
 // of the adapter, B operand: the tile's 16 tokens), the columns split over
 // workgroups and over the waves of each; the shares' sums are left in a
 // workspace and added, in order, by
-// outer: y += s B t.  t is kept to fp32's precision: it enters the product
+// outer: y += s B t (or the epilogue of the product that makes y, for a few
+// tokens).  t is kept to fp32's precision: it enters the product
 // as the sum of three BF16 numbers (8 + 8 + 8 significant bits), since the
 // product is a few MFMAs beside the loads of B and y.
 #include <hip/hip_runtime.h>
@@ -139,7 +140,9 @@ __device__ __forceinline__ bf16x8 load_x(const LoraArgs& p, const uint16_t* xp, 
 // grid: (tiles, shares of the columns); RT: 16-row tiles of the rank.  A wave
 // takes 128 columns at a time, all their loads issued before the first
 // product.  A is kept in the order of the product's operand, so a wave reads
-// 4 KiB on end of each 16 rows.
+// 4 KiB on end of each 16 rows.  A's bytes bound it: 64 tokens, each with an
+// adapter of up to 64 ranks of its own, on 14336 columns: 82 MB in 19 us, 4.4
+// TB/s.  4097 tokens with 5 adapters on 3584 columns: 29 MB of x in 10.5 us.
 template <int RT>
 __global__ __launch_bounds__(256, 2) void inner_kernel(LoraArgs p) {
     Tile tl;
