@@ -235,6 +235,8 @@ bs_status bs_kv_append_async(const bs_kv_cache* cache, uint32_t layer, uint32_t 
     if (!d_seqs || !d_k || !d_v) { set_error("NULL argument"); return BS_E_INVAL; }
     if (n_seqs > kGridYZ) { set_error("%u sequences in one call (at most 65535)", n_seqs); return BS_E_INVAL; }
     if (total > 0x7FFFFFFFu || max_new == 0 || max_new > total) { set_error("max_new %u of %u tokens", max_new, total); return BS_E_INVAL; }
+    const uint64_t touch = ((uint64_t)max_new + 2ull * a.c.page - 2) >> a.c.lp;
+    if (touch * 2 * a.c.kv_heads > kGridX / 256) { set_error("max_new %u is too many tokens for one call", max_new); return BS_E_INVAL; }
     if (!d_starts && (total != n_seqs || max_new != 1)) {
         set_error("%u tokens for %u sequences without starts", total, n_seqs);
         return BS_E_INVAL;

@@ -205,6 +205,18 @@ def test_append_stores_the_rule(dtype, dim, page, heads, f32):
 
 
 @pytest.mark.parametrize("dtype", ["e4m3", "int8"])
+@pytest.mark.parametrize("dim,page", [(64, 256), (96, 64), (128, 64), (256, 64), (256, 128), (8, 16)])
+@pytest.mark.parametrize("f32", [False, True])
+def test_append_of_chunks_anywhere_in_a_page(dtype, dim, page, f32):
+    print("append chunks", dtype, dim, page, f32, flush=True)
+    rng = np.random.default_rng(dim * page)
+    cache, model = _pair(layers=1, kv_heads=2, head_dim=dim, n_pages=30, max_seqs=3, max_pages=10, page_tokens=page, dtype=dtype)
+    for counts in ([1, 2, 3], [3, 5, 7], [4, 16, 17], [9, 30, 33], [page, page - 1, page + 1], [1, 4, 2 * page], [31, 2, 6]):
+        _fill(cache, model, rng, [2, 0, 1], counts, (1.0, 0.01, 20.0), f32)
+        _same(cache, model)
+
+
+@pytest.mark.parametrize("dtype", ["e4m3", "int8"])
 def test_append_of_non_finite_values(dtype):
     cache, model = _pair(layers=1, kv_heads=2, head_dim=64, n_pages=4, max_seqs=1, max_pages=4, page_tokens=16, dtype=dtype)
     rng = np.random.default_rng(3)
