@@ -418,6 +418,7 @@ bs_status bs::fixed_gemm(const bs_fixed_info* info, const void* d_blob, uint64_t
         a.ksplit = parts + 1;
         a.gpart = (float*)d_work;
     }
+    if (lora && lora->x_tiles) a.gx = lora->x_ops;
     int cus = 0;
     if (bsk_device_cus(&cus) != 0 || cus <= 0) cus = 256;
     const uint64_t items = split ? a.ksplit * groups32 : (rows + 15) / 16;

@@ -474,7 +474,15 @@ __global__ __launch_bounds__(64 * kGemmWaves) void fixed_gemm_kernel(FixedArgs a
         // and a panel's first group is issued before its blocks are decoded.
         // offsets in 32 bits (batch <= 64 and cols < 2^26; batch x rows < 2^32)
         const uint32_t n = nt * 16 + (lane & 15);
-        const uint16_t* xrow = a.gx + ((n < a.batch ? n : 0u) * a.cols + ks * kSlice + 8 * (lane >> 4));
+        // Beside adapters X comes in operand order, kStep elements to a k step
+        // (the inner product's launch, before this one, lays it out): a load is
+        // 1 KiB on end, 8 line requests instead of 16.  64 tokens on 3584 x
+        // 14336: 48 us instead of 65, and 1.5 us more in the inner product.
+        // (Four loads in flight instead of two: 49 us, the registers spill.)
+        constexpr bool kOps = LORA && (MF == 2 || NT >= 2);
+        constexpr uint32_t kStep = kOps ? 512 : 32, kPanel = kFixBlockW / 32 * kStep;
+        const uint16_t* xrow = a.gx + (kOps ? (nt * (a.cols / 32) + ks * (kSlice / 32)) * 512 + 8 * lane
+                                            : (n < a.batch ? n : 0u) * a.cols + ks * kSlice + 8 * (lane >> 4));
         constexpr uint32_t kNs = kSlice / 32;               // k steps per wave and panel
         // X loads in flight per group: 8, or 2 where each feeds two row tiles
         // (4 made the compiler spill 6 registers at NT 4 and ran 13% slower
@@ -484,7 +492,7 @@ __global__ __launch_bounds__(64 * kGemmWaves) void fixed_gemm_kernel(FixedArgs a
         bf16x8 bv[kU];
         for (uint32_t p = p0; p < p1; p++) {
 #pragma unroll
-            for (uint32_t u = 0; u < kU; u++) bv[u] = *(const bf16x8*)(xrow + (uint64_t)p * kFixBlockW + 32 * u);
+            for (uint32_t u = 0; u < kU; u++) bv[u] = *(const bf16x8*)(xrow + (uint64_t)p * kPanel + kStep * u);
             __syncthreads();          // the previous panel (or K-slice table) is consumed, the table built
 #pragma unroll
             for (uint32_t h = 0; h < kRpw; h++) {
@@ -505,7 +513,7 @@ __global__ __launch_bounds__(64 * kGemmWaves) void fixed_gemm_kernel(FixedArgs a
                 for (uint32_t h = 0; h < kRpw; h++)
                     if (has[h]) in[h] = load_block(a, (r0 + mr[h]) * bpr + p + 1, lane);
             }
-            const uint16_t* xr = xrow + (uint64_t)p * kFixBlockW;
+            const uint16_t* xr = xrow + (uint64_t)p * kPanel;
 #pragma unroll
             for (uint32_t s0 = 0; s0 < kNs; s0 += kU) {
                 bf16x8 cur[kU];
@@ -513,7 +521,7 @@ __global__ __launch_bounds__(64 * kGemmWaves) void fixed_gemm_kernel(FixedArgs a
                 for (uint32_t u = 0; u < kU; u++) cur[u] = bv[u];
                 if (s0 + kU < kNs) {
 #pragma unroll
-                    for (uint32_t u = 0; u < kU; u++) bv[u] = *(const bf16x8*)(xr + 32 * (s0 + kU + u));
+                    for (uint32_t u = 0; u < kU; u++) bv[u] = *(const bf16x8*)(xr + kStep * (s0 + kU + u));
                 }
 #pragma unroll
                 for (uint32_t u = 0; u < kU; u++) {
@@ -547,7 +555,7 @@ __global__ __launch_bounds__(64 * kGemmWaves) void fixed_gemm_kernel(FixedArgs a
         float* dst = kh ? a.gpart + (uint64_t)(kh - 1) * a.batch * a.rows : a.gy;
         if (ks == 0) {
             const uint32_t rows = (uint32_t)a.rows, rg = (uint32_t)r0 + 4 * (lane >> 4);
-            if (LORA && n < a.batch && rg < rows) sum[0] += lora_rows(lora, n, rg);
+            if (LORA && MF == 1 && n < a.batch && rg < rows) sum[0] += lora_rows(lora, n, rg);
 #pragma unroll
             for (int m = 0; m < MF; m++)
 #pragma unroll
@@ -574,14 +582,18 @@ extern "C" int bsk_fixed_gemm(const FixedArgs* args, uint32_t n_groups, int rows
     hipStream_t st = (hipStream_t)stream;
     const uint32_t nt = (args->batch + 15) / 16;
     const LoraArgs none = {};
+    auto go = [&](auto with, auto without) {
+        if (lora) hipLaunchKernelGGL(with, grid, block, 0, st, *args, *lora);
+        else hipLaunchKernelGGL(without, grid, block, 0, st, *args, none);
+    };
     if (rows32) {
         if (args->ksplit == 0 || (!lora && args->ksplit > 2)) return (int)hipErrorInvalidValue;
         if (args->ksplit > 1 && (!args->gpart || args->cols < args->ksplit * kFixBlockW)) return (int)hipErrorInvalidValue;
         switch (nt) {
-            case 1: hipLaunchKernelGGL((fixed_gemm_kernel<1, 2, false>), grid, block, 0, st, *args, none); break;
-            case 2: hipLaunchKernelGGL((fixed_gemm_kernel<2, 2, false>), grid, block, 0, st, *args, none); break;
+            case 1: go(fixed_gemm_kernel<1, 2, true>, fixed_gemm_kernel<1, 2, false>); break;
+            case 2: go(fixed_gemm_kernel<2, 2, true>, fixed_gemm_kernel<2, 2, false>); break;
             case 3:
-            case 4: hipLaunchKernelGGL((fixed_gemm_kernel<4, 2, false>), grid, block, 0, st, *args, none); break;
+            case 4: go(fixed_gemm_kernel<4, 2, true>, fixed_gemm_kernel<4, 2, false>); break;
             default: return (int)hipErrorInvalidValue;
         }
         if (args->ksplit == 2 && !lora) {
@@ -591,10 +603,6 @@ extern "C" int bsk_fixed_gemm(const FixedArgs* args, uint32_t n_groups, int rows
         }
         return (int)hipGetLastError();
     }
-    auto go = [&](auto with, auto without) {
-        if (lora) hipLaunchKernelGGL(with, grid, block, 0, st, *args, *lora);
-        else hipLaunchKernelGGL(without, grid, block, 0, st, *args, none);
-    };
     switch (nt) {
         case 1: go(fixed_gemm_kernel<1, 1, true>, fixed_gemm_kernel<1, 1, false>); break;
         case 2: go(fixed_gemm_kernel<2, 1, true>, fixed_gemm_kernel<2, 1, false>); break;

@@ -96,6 +96,16 @@ uint64_t shares_bytes(uint64_t rows, uint64_t cols, uint32_t tokens) {
     return 4ull * (panel_shares(rows, cols, tokens) - 1) * tokens * rows;
 }
 
+// X as the product's operand, in batch tiles as its kernels take them; up to
+// 16 tokens in one share read X as it is
+uint32_t x_tiles(uint64_t rows, uint64_t cols, uint32_t tokens) {
+    const uint32_t nt = (tokens + 15) / 16;
+    if (nt == 1 && panel_shares(rows, cols, tokens) == 1) return 0;
+    return nt == 3 ? 4 : nt;
+}
+
+uint64_t x_bytes(uint64_t rows, uint64_t cols, uint32_t tokens) { return 32ull * x_tiles(rows, cols, tokens) * cols; }
+
 uint64_t inner_bytes(const bs_lora_pack* p, uint32_t tokens) {
     return align_up(4ull * share_rule(p, max_tiles(tokens, p->adapters)) * tokens * p->rank, 256);
 }
@@ -191,7 +201,7 @@ bs_status bs_lora_add_async(const bs_lora_pack* pack, const int32_t* d_batch, ui
 
 uint64_t bs_fixed_gemm_lora_work_bytes(uint64_t rows, uint64_t cols, uint32_t batch, const bs_lora_pack* pack) {
     if (check_pack(pack) != BS_OK || batch == 0 || batch > 64) return 0;
-    return align_up(shares_bytes(rows, cols, batch), 256) + inner_bytes(pack, batch);
+    return align_up(shares_bytes(rows, cols, batch), 256) + inner_bytes(pack, batch) + x_bytes(rows, cols, batch);
 }
 
 bs_status bs_fixed_gemm_lora_async(const bs_fixed_info* info, const void* d_blob, uint64_t rows, uint64_t cols,
@@ -225,6 +235,8 @@ bs_status bs_fixed_gemm_lora_async(const bs_fixed_info* info, const void* d_blob
     a.part = (const float*)part;
     a.part_stride = (uint64_t)batch * rows;
     a.nparts = panel_shares(rows, cols, batch) - 1;
+    a.x_tiles = x_tiles(rows, cols, batch);
+    a.x_ops = (uint16_t*)((uint8_t*)a.t + inner_bytes(pack, batch));
     // the projection's arguments are checked before anything is enqueued
     const bs_status r0 = fixed_gemm(info, d_blob, rows, cols, batch, d_x, d_y, d_status, part, split, &a, true, stream);
     if (r0 != BS_OK) return r0;

@@ -137,7 +137,8 @@ __device__ __forceinline__ bf16x8 load_x(const LoraArgs& p, const uint16_t* xp, 
     return __builtin_bit_cast(bf16x8, v4u{w[0], w[1], w[2], w[3]});
 }
 
-// grid: (tiles, shares of the columns); RT: 16-row tiles of the rank.  A wave
+// grid: (tiles, shares of the columns), and before the tiles the workgroups that
+// lay x out for the product beside it; RT: 16-row tiles of the rank.  A wave
 // takes 128 columns at a time, all their loads issued before the first
 // product.  A is kept in the order of the product's operand, so a wave reads
 // 4 KiB on end of each 16 rows.  A's bytes bound it: 64 tokens, each with an
@@ -145,11 +146,23 @@ __device__ __forceinline__ bf16x8 load_x(const LoraArgs& p, const uint16_t* xp, 
 // TB/s.  4097 tokens with 5 adapters on 3584 columns: 29 MB of x in 10.5 us.
 template <int RT>
 __global__ __launch_bounds__(256, 2) void inner_kernel(LoraArgs p) {
-    Tile tl;
-    if (!get_tile(p, blockIdx.x, tl) || tl.adapter < 0) return;
-    __shared__ f32x4 red[3][RT][64];
     const uint32_t t = threadIdx.x, lane = t & 63u, m = lane & 15u, g = lane >> 4;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(t >> 6);
+    const uint32_t packs = gridDim.x - p.max_tiles;
+    if (blockIdx.x < packs) {
+        const uint32_t steps = p.cols / 32, all = p.x_tiles * steps;
+        const uint32_t w = (blockIdx.y * packs + blockIdx.x) * 4 + wave, waves = packs * gridDim.y * 4;
+        for (uint32_t u = w; u < all; u += waves) {
+            const uint32_t tile = u / steps, tok = 16 * tile + m;
+            v4u v = {0, 0, 0, 0};
+            if (tok < p.tokens) v = *(const v4u*)(p.x + (uint64_t)tok * p.x_stride + 32 * (u - tile * steps) + 8 * g);
+            *(v4u*)(p.x_ops + ((uint64_t)u * 64 + lane) * 8) = v;
+        }
+        return;
+    }
+    Tile tl;
+    if (!get_tile(p, blockIdx.x - packs, tl) || tl.adapter < 0) return;
+    __shared__ f32x4 red[3][RT][64];
     const uint32_t nr = min((uint32_t)(p.ranks[tl.adapter] + 15) / 16, (uint32_t)RT);
     const uint32_t tok = token_at(p, tl.first + min(m, tl.count - 1));
     const uint16_t* xp = p.x + (uint64_t)tok * p.x_stride;
@@ -478,7 +491,8 @@ extern "C" int bsk_lora_batch(const int32_t* idx, uint32_t tokens, uint32_t adap
 }
 
 extern "C" int bsk_lora_inner(const LoraArgs* a, void* stream) {
-    const dim3 grid(a->max_tiles, a->ksplit);
+    const uint32_t units = a->x_tiles * (a->cols / 32), four = 16 * a->ksplit;   // four units to a wave
+    const dim3 grid(a->max_tiles + (units + four - 1) / four, a->ksplit);
     hipStream_t st = (hipStream_t)stream;
     switch (a->rank / 16) {
         case 1: hipLaunchKernelGGL(inner_kernel<1>, grid, dim3(256), 0, st, *a); break;

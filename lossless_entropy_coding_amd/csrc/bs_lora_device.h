@@ -30,6 +30,11 @@ struct LoraArgs {
     uint64_t y_stride;          // elements between tokens (in and out)
     uint32_t adapters, rank, rows, cols, cols_pad;
     uint32_t tokens, max_tiles, ksplit;
+    // where the inner product leaves x for the product beside it (x_tiles 0:
+    // nowhere): [x_tiles][cols / 32][64][8], the operand of 16 tokens and 32
+    // columns in lane order, zeros for tokens past the last
+    uint16_t* x_ops;
+    uint32_t x_tiles;
     int x_aligned;              // rows of x can be read 16 B at a time
     int y32;
     int y_vec;                  // y (and part) can be read and written 16 B at a time
