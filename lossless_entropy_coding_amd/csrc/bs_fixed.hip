@@ -486,8 +486,9 @@ __global__ __launch_bounds__(64 * kGemmWaves) void fixed_gemm_kernel(FixedArgs a
         constexpr uint32_t kNs = kSlice / 32;               // k steps per wave and panel
         // X loads in flight per group: 8, or 2 where each feeds two row tiles
         // (4 made the compiler spill 6 registers at NT 4 and ran 13% slower
-        // at batch 64)
-        constexpr uint32_t kUmax = MF == 2 ? 2 : 8;
+        // at batch 64); 4 from operand order, where 8 spill (63 tokens on
+        // 8673 x 2048: 37.7 us with 4, 42.7 with 8)
+        constexpr uint32_t kUmax = MF == 2 ? 2 : kOps ? 4 : 8;
         constexpr uint32_t kU = kNs < kUmax ? kNs : kUmax;
         bf16x8 bv[kU];
         for (uint32_t p = p0; p < p1; p++) {
