@@ -445,14 +445,15 @@ __global__ __launch_bounds__(64 * kGemmWaves) void fixed_gemm_kernel(FixedArgs a
     constexpr uint32_t kSlice = kFixBlockW / kWpt; // panel columns per wave
     const uint32_t nt = wave / kWpt, ks = wave % kWpt;
     const uint32_t bpr = a.cols / kFixBlockW;
-    const uint32_t split = MF == 2 ? std::min(a.ksplit, bpr) : 1u;           // every share holds a panel
+    // every share holds a panel (two shares at most without adapters: a
+    // division by a constant)
+    const uint32_t split = MF == 1 ? 1u : LORA ? std::min(a.ksplit, bpr) : a.ksplit == 2 && bpr >= 2 ? 2u : 1u;
     const uint64_t groups = (a.rows + kRows - 1) / kRows;
     const uint64_t items = groups * split;
     for (uint64_t item = blockIdx.x; item < items; item += gridDim.x) {
-        const uint64_t g = item / split;
-        const uint32_t kh = (uint32_t)(item % split);
+        const uint32_t g = (uint32_t)item / split, kh = (uint32_t)item - g * split;   // 2^24 items at most
         const uint32_t p0 = (kh * bpr + split - 1) / split, p1 = ((kh + 1) * bpr + split - 1) / split;   // its panels
-        const uint64_t r0 = kRows * g;
+        const uint64_t r0 = (uint64_t)kRows * g;
         f32x4 acc[MF];
 #pragma unroll
         for (int m = 0; m < MF; m++) acc[m] = f32x4{0.f, 0.f, 0.f, 0.f};

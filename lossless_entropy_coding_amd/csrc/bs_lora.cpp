@@ -77,8 +77,8 @@ uint32_t share_rule(const bs_lora_pack* p, uint32_t tiles) {
 // as the CUs take at once (at most 8: each is a pass over Y in the last
 // launch; a third share of 112 groups, more than the CUs take, made 64 tokens
 // on 3584 x 14336 20% slower).  54 tokens on 163 x 14336: 63 us with two
-// shares, 38 with seven.  From 8 tokens on at least two, as in the plain
-// product; below, one wherever that is as fast, since the product's epilogue
+// shares, 38 with seven (both before X was laid out; 32 since).  From 8 tokens
+// on at least two, as in the plain product; below, one wherever that is as fast, since the product's epilogue
 // then adds the adapters (4 tokens on 2000 x 4096: 17.1 us with one, 18.8
 // with two).
 uint32_t panel_shares(uint64_t rows, uint64_t cols, uint32_t tokens) {
