@@ -72,23 +72,29 @@ uint32_t share_rule(const bs_lora_pack* p, uint32_t tiles) {
     return (blocks + turns - 1) / turns;         // as many turns of 512 columns with the fewest workgroups
 }
 
-// Shares of the columns' panels (of 2048) in the product beside adapters.
-// With few rows there are fewer groups of 32 rows than CUs, so as many shares
-// as the CUs take at once (at most 8: each is a pass over Y in the last
-// launch; a third share of 112 groups, more than the CUs take, made 64 tokens
-// on 3584 x 14336 20% slower).  54 tokens on 163 x 14336: 63 us with two
-// shares, 38 with seven (both before X was laid out; 32 since).  From 8 tokens
-// on at least two, as in the plain product; below, one wherever that is as fast, since the product's epilogue
-// then adds the adapters (4 tokens on 2000 x 4096: 17.1 us with one, 18.8
-// with two).
+// Shares of the columns' panels (of 2048) in the product beside adapters.  A
+// CU takes one workgroup (32 rows and a share) at a time, so the time goes by
+// rounds of workgroups times the panels of a share (and a quarter of a panel to
+// start each): the shares that make it least, the fewest of these, at most 8
+// (each is a pass over Y in the last launch).  54 tokens on 163 x 14336: 63 us
+// with two shares, 38 with seven (both before X was laid out; 32 since); 26 on
+// 5182 x 12288: 66 us with two, 55 with three; 64 on 3584 x 14336: 54 with two,
+// a fifth more with three, a second round.  From 8 tokens on at least two, as
+// in the plain product; below, one wherever that is as fast, since the
+// product's epilogue then adds the adapters (4 tokens on 2000 x 4096: 17.1 us
+// with one, 18.8 with two).
 uint32_t panel_shares(uint64_t rows, uint64_t cols, uint32_t tokens) {
     int cus = 0;
     if (bsk_device_cus(&cus) != 0 || cus <= 0) cus = 256;
     const uint64_t panels = cols / 2048, groups = (rows + 31) / 32;
     if (panels < 2 || (tokens < 8 && (panels < 4 || (rows + 15) / 16 * 2 >= (uint64_t)cus))) return 1;
-    const uint64_t want = std::max<uint64_t>(1, std::min<uint64_t>({(uint64_t)cus / groups, panels, 8}));
-    const uint64_t turns = (panels + want - 1) / want, shares = (panels + turns - 1) / turns;
-    return (uint32_t)std::max<uint64_t>(shares, tokens >= 8 ? 2 : 1);
+    uint64_t best = 0, least = ~0ull;
+    for (uint64_t shares = 2; shares <= std::min<uint64_t>(panels, 8); shares++) {
+        const uint64_t rounds = (groups * shares + cus - 1) / cus, turns = (panels + shares - 1) / shares;
+        const uint64_t cost = rounds * (4 * turns + 1);
+        if (cost < least) { least = cost; best = shares; }
+    }
+    return (uint32_t)best;
 }
 
 // the partial sums of the shares after the first
