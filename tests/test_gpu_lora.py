@@ -145,6 +145,12 @@ def test_product_with_adapters(rows, cols, tokens):
         assert torch.equal(a[none], plan.gemm(x.cuda(), rows, cols)[none])
 
 
+@pytest.mark.parametrize("rows,cols,tokens", [(4200, 6144, 20), (4100, 10240, 12), (100, 2048, 33), (3001, 2048, 20), (77, 2048, 48)])
+def test_product_with_adapters_in_rounds(rows, cols, tokens):
+    """More workgroups than run at once, in two or three shares; one share with X in operand order."""
+    test_product_with_adapters(rows, cols, tokens)
+
+
 def test_graph_replays():
     rng = np.random.default_rng(9)
     rows, cols, tokens = 256, 4096, 12
