@@ -15,6 +15,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes as C
+import threading
 from dataclasses import dataclass
 
 import numpy as np
@@ -449,6 +450,8 @@ class FixedPlan:
         self.n = self.info.n
         self.bytes = self.info.bytes
         self.status = torch.zeros(max(self.info.n_blocks, 1), dtype=torch.int32, device=self.dev.device)
+        # gemm_lora's workspace, one call's until its launches are enqueued
+        self._lora_lock, self._lora_work, self._lora_kept = threading.Lock(), None, []
 
     def new_output(self) -> torch.Tensor:
         return torch.empty(max(self.n, 8), dtype=torch.int16, device=self.dev.device)
@@ -575,7 +578,8 @@ class FixedPlan:
         (bs_fixed_gemm_lora_async): x a (tokens, cols) bfloat16 (or int16)
         tensor of 1..64 tokens, pack a lora.LoraPack, batch a lora.LoraBatch
         made for these tokens; returns (tokens, rows) float32 (out, if given).
-        The plan keeps the workspace: products of one plan go on one stream."""
+        The plan keeps the workspace: products of one plan go on one stream,
+        from any thread."""
         if x.dtype not in (torch.bfloat16, torch.int16) or x.dim() != 2 or x.shape[1] != cols or not x.is_contiguous():
             raise ValueError(f"x must be a contiguous (tokens, {cols}) bfloat16 tensor")
         batch.check_for(pack, x.shape[0])
@@ -584,16 +588,14 @@ class FixedPlan:
                 out = torch.empty(x.shape[0], rows, dtype=torch.float32, device=self.dev.device)
         elif out.dtype != torch.float32 or tuple(out.shape) != (x.shape[0], rows) or not out.is_contiguous():
             raise ValueError(f"out must be a contiguous ({x.shape[0]}, {rows}) float32 tensor")
-        need = int(L.lib().bs_fixed_gemm_lora_work_bytes(rows, cols, x.shape[0], pack.ref))
-        old = getattr(self, "_lora_work", None)
-        if old is None:
-            self._lora_kept = []
-        if old is None or old.numel() < need:
-            self._lora_work = _grown(old, need, self.dev.device, stream, self._lora_kept)
-        rc = L.lib().bs_fixed_gemm_lora_async(C.byref(self.info), self.dev.data_ptr(), rows, cols, x.shape[0],
-                                              x.data_ptr(), out.data_ptr(), self.status.data_ptr() if status else None,
-                                              pack.ref, batch.dev.data_ptr(), self._lora_work.data_ptr(),
-                                              self._lora_work.numel(), _stream_of(x.device, stream))
+        with self._lora_lock:
+            need = int(L.lib().bs_fixed_gemm_lora_work_bytes(rows, cols, x.shape[0], pack.ref))
+            if self._lora_work is None or self._lora_work.numel() < need:
+                self._lora_work = _grown(self._lora_work, need, self.dev.device, stream, self._lora_kept)
+            rc = L.lib().bs_fixed_gemm_lora_async(C.byref(self.info), self.dev.data_ptr(), rows, cols, x.shape[0],
+                                                  x.data_ptr(), out.data_ptr(), self.status.data_ptr() if status else None,
+                                                  pack.ref, batch.dev.data_ptr(), self._lora_work.data_ptr(),
+                                                  self._lora_work.numel(), _stream_of(x.device, stream))
         if rc:
             L.check(rc, "bs_fixed_gemm_lora_async")
         return out

@@ -14,11 +14,13 @@ keys and values and attends:
 
 Everything is enqueued on the current (or given) stream and nothing
 synchronises except check().  The cache keeps its workspaces, so its calls go
-on one stream, or on several that wait for each other.
+on one stream, or on several that wait for each other.  Threads may share a
+cache: a call's launches are enqueued together, under the cache's lock.
 """
 from __future__ import annotations
 
 import ctypes as C
+import threading
 
 import torch
 
@@ -87,6 +89,9 @@ class KvCache:
         self._page_work, self._attend_work, self._kept = None, None, []
         self._ref, self._args = C.byref(self.c), L.KvAttendArgs()
         self._args_ref = C.byref(self._args)
+        # the argument block and the workspaces are one call's at a time: held
+        # until the C call, which lets other threads run, has enqueued its work
+        self._lock = threading.Lock()
         self._page_need, self._attend_need = {}, {}        # workspace bytes by the sizes of a call
 
     # ------------------------------------------------------------ pages
@@ -104,9 +109,10 @@ class KvCache:
         n = _ids(rows, "rows")
         if _ids(counts, "counts") != n:
             raise ValueError("one count per row")
-        w = self._work(n, stream)
-        rc = L.lib().bs_kv_extend_async(self._ref, n, rows.data_ptr(), counts.data_ptr(), w.data_ptr(), w.numel(),
-                                        _stream_of(rows.device, stream))
+        with self._lock:
+            w = self._work(n, stream)
+            rc = L.lib().bs_kv_extend_async(self._ref, n, rows.data_ptr(), counts.data_ptr(), w.data_ptr(), w.numel(),
+                                            _stream_of(rows.device, stream))
         if rc:
             L.check(rc, "bs_kv_extend_async")
 
@@ -116,9 +122,10 @@ class KvCache:
         n = _ids(parents, "parents")
         if _ids(children, "children") != n:
             raise ValueError("one parent per child")
-        w = self._work(n, stream)
-        rc = L.lib().bs_kv_fork_async(self._ref, n, parents.data_ptr(), children.data_ptr(), w.data_ptr(), w.numel(),
-                                      _stream_of(parents.device, stream))
+        with self._lock:
+            w = self._work(n, stream)
+            rc = L.lib().bs_kv_fork_async(self._ref, n, parents.data_ptr(), children.data_ptr(), w.data_ptr(), w.numel(),
+                                          _stream_of(parents.device, stream))
         if rc:
             L.check(rc, "bs_kv_fork_async")
 
@@ -145,22 +152,23 @@ class KvCache:
         with those it was captured with: capture it again)."""
         if (table_out is None) != (refs_out is None):
             raise ValueError("table_out and refs_out go together")
-        swap = table_out is None
-        if swap:
-            if getattr(self, "_spare", None) is None:
-                with _on(stream):
-                    self._spare = (torch.empty_like(self.table), torch.empty_like(self.refs))
-            table_out, refs_out = self._spare
-        for t, like, name in ((table_out, self.table, "table_out"), (refs_out, self.refs, "refs_out")):
-            if t.dtype != like.dtype or t.shape != like.shape or not t.is_contiguous():
-                raise ValueError(f"{name} must be a contiguous int32 tensor of shape {tuple(like.shape)}")
-        w = self._work(0, stream)
-        L.check(L.lib().bs_kv_compact_async(self._ref, table_out.data_ptr(), refs_out.data_ptr(), w.data_ptr(), w.numel(),
-                                            _stream_of(self.k.device, stream)), "bs_kv_compact_async")
-        if swap:
-            self._spare = (self.table, self.refs)
-            self.table, self.refs = table_out, refs_out
-            self.c.d_table, self.c.d_refs = table_out.data_ptr(), refs_out.data_ptr()
+        with self._lock:
+            swap = table_out is None
+            if swap:
+                if getattr(self, "_spare", None) is None:
+                    with _on(stream):
+                        self._spare = (torch.empty_like(self.table), torch.empty_like(self.refs))
+                table_out, refs_out = self._spare
+            for t, like, name in ((table_out, self.table, "table_out"), (refs_out, self.refs, "refs_out")):
+                if t.dtype != like.dtype or t.shape != like.shape or not t.is_contiguous():
+                    raise ValueError(f"{name} must be a contiguous int32 tensor of shape {tuple(like.shape)}")
+            w = self._work(0, stream)
+            L.check(L.lib().bs_kv_compact_async(self._ref, table_out.data_ptr(), refs_out.data_ptr(), w.data_ptr(), w.numel(),
+                                                _stream_of(self.k.device, stream)), "bs_kv_compact_async")
+            if swap:
+                self._spare = (self.table, self.refs)
+                self.table, self.refs = table_out, refs_out
+                self.c.d_table, self.c.d_refs = table_out.data_ptr(), refs_out.data_ptr()
 
     # ------------------------------------------------------------ tokens
     def _tokens(self, t: torch.Tensor, heads: int | None, name: str) -> int:
@@ -234,23 +242,24 @@ class KvCache:
         if window < 0 or sinks < 0 or max_len < 0:
             raise ValueError("window, sinks and max_len are not negative")
         n, most, at = self._rows(rows, starts, total, max_new)
-        a = self._args
-        a.layer, a.n_seqs, a.heads, a.total_q, a.max_new, a.max_len = layer, n, heads, total, most, max_len
-        a.d_seqs, a.d_starts, a.d_q, a.d_out = rows.data_ptr(), at, q.data_ptr(), out.data_ptr()
-        a.d_lse = None if lse is False else lse.data_ptr()
-        a.q_stride, a.out_stride, a.scale, a.softcap, a.window, a.sinks = qs, os, scale, softcap, window, sinks
-        sizes = (n, heads, total, most, max_len, window, sinks)
-        need = self._attend_need.get(sizes)
-        if need is None:
-            if len(self._attend_need) > 4096:              # lengths that grow token by token
-                self._attend_need.clear()
-            need = int(L.lib().bs_kv_attend_work_bytes(self._ref, self._args_ref))
-            self._attend_need[sizes] = need
-        w = self._attend_work
-        if need and (w is None or w.numel() < need):
-            w = self._attend_work = _grown(w, need, self.k.device, stream, self._kept, zero=True)
-        rc = L.lib().bs_kv_attend_async(self._ref, self._args_ref, w.data_ptr() if need else None, need,
-                                        _stream_of(q.device, stream))
+        with self._lock:
+            a = self._args
+            a.layer, a.n_seqs, a.heads, a.total_q, a.max_new, a.max_len = layer, n, heads, total, most, max_len
+            a.d_seqs, a.d_starts, a.d_q, a.d_out = rows.data_ptr(), at, q.data_ptr(), out.data_ptr()
+            a.d_lse = None if lse is False else lse.data_ptr()
+            a.q_stride, a.out_stride, a.scale, a.softcap, a.window, a.sinks = qs, os, scale, softcap, window, sinks
+            sizes = (n, heads, total, most, max_len, window, sinks)
+            need = self._attend_need.get(sizes)
+            if need is None:
+                if len(self._attend_need) > 4096:              # lengths that grow token by token
+                    self._attend_need.clear()
+                need = int(L.lib().bs_kv_attend_work_bytes(self._ref, self._args_ref))
+                self._attend_need[sizes] = need
+            w = self._attend_work
+            if need and (w is None or w.numel() < need):
+                w = self._attend_work = _grown(w, need, self.k.device, stream, self._kept, zero=True)
+            rc = L.lib().bs_kv_attend_async(self._ref, self._args_ref, w.data_ptr() if need else None, need,
+                                            _stream_of(q.device, stream))
         if rc:
             L.check(rc, "bs_kv_attend_async")
         return out if lse is False else (out, lse)

@@ -12,6 +12,7 @@ LoraPack.add adds the adapters' part to a projection made elsewhere.
 from __future__ import annotations
 
 import ctypes as C
+import threading
 
 import torch
 
@@ -51,6 +52,7 @@ class LoraPack:
                             self.ranks.data_ptr(), self.factor.data_ptr())
         self.ref = C.byref(self.c)
         self._work, self._kept, self._need = None, [], {}
+        self._lock = threading.Lock()            # the workspace is one call's until its launches are enqueued
 
     def work_bytes(self, tokens: int) -> int:
         """Workspace of add() for this many tokens (bs_lora_work_bytes)."""
@@ -64,7 +66,8 @@ class LoraPack:
         """y plus each token's adapter (bs_lora_add_async): x (tokens, cols)
         bfloat16, y (tokens, rows) float32 or bfloat16; rows of x and y may be
         strided.  Written to `out` (y's shape, type and strides), by default y
-        itself.  The pack keeps the workspace: calls go on one stream."""
+        itself.  The pack keeps the workspace: calls go on one stream, from any
+        thread."""
         out = y if out is None else out
         if x.dtype != torch.bfloat16 or x.dim() != 2 or x.shape[1] != self.cols or (x.shape[0] and x.stride(1) != 1):
             raise ValueError(f"x must be a (tokens, {self.cols}) bfloat16 tensor with adjacent columns")
@@ -76,15 +79,16 @@ class LoraPack:
         batch.check_for(self, x.shape[0])
         if x.shape[0] == 0:
             return out
-        need = self.work_bytes(x.shape[0])
-        if self._work is None or self._work.numel() < need:
-            self._work = _grown(self._work, need, self.a.device, stream, self._kept)
-        one = x.shape[0] == 1
-        rc = L.lib().bs_lora_add_async(self.ref, batch.dev.data_ptr(), x.shape[0], x.data_ptr(),
-                                       self.cols if one else x.stride(0), y.data_ptr(), out.data_ptr(),
-                                       self.rows if one else y.stride(0),
-                                       L.T_FP32 if y.dtype == torch.float32 else L.T_BF16, self._work.data_ptr(),
-                                       self._work.numel(), _stream_of(x.device, stream))
+        with self._lock:
+            need = self.work_bytes(x.shape[0])
+            if self._work is None or self._work.numel() < need:
+                self._work = _grown(self._work, need, self.a.device, stream, self._kept)
+            one = x.shape[0] == 1
+            rc = L.lib().bs_lora_add_async(self.ref, batch.dev.data_ptr(), x.shape[0], x.data_ptr(),
+                                           self.cols if one else x.stride(0), y.data_ptr(), out.data_ptr(),
+                                           self.rows if one else y.stride(0),
+                                           L.T_FP32 if y.dtype == torch.float32 else L.T_BF16, self._work.data_ptr(),
+                                           self._work.numel(), _stream_of(x.device, stream))
         if rc:
             L.check(rc, "bs_lora_add_async")
         return out

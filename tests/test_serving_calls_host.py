@@ -1,0 +1,120 @@
+"""What the serving operators' Python calls hand to the library, on the CPU: a
+stand-in takes the place of the library's launches, so no pointer is followed."""
+import sys
+import threading
+import time
+
+import numpy as np
+import pytest
+import torch
+
+from lossless_entropy_coding_amd import _lib as L
+from lossless_entropy_coding_amd import codec, kv, lora
+
+LAUNCHES = ("bs_kv_extend_async", "bs_kv_fork_async", "bs_kv_compact_async", "bs_kv_append_async", "bs_kv_attend_async",
+            "bs_kv_free_async", "bs_kv_copy_pages_async", "bs_lora_add_async", "bs_lora_batch_async",
+            "bs_fixed_gemm_lora_async")
+
+
+class Stub:
+    """The library, except that its launches call `seen(name, args)`."""
+
+    def __init__(self, seen):
+        self._real, self._seen = L.lib(), seen
+
+    def __getattr__(self, name):
+        if name in LAUNCHES:
+            return lambda *args: self._seen(name, args) or 0
+        return getattr(self._real, name)
+
+
+@pytest.fixture
+def stub(monkeypatch):
+    def start(seen):
+        lib = Stub(seen)
+        monkeypatch.setattr(L, "lib", lambda: lib)
+        for m in (kv, lora, codec):
+            monkeypatch.setattr(m, "_stream_of", lambda device, stream: 0)
+    return start
+
+
+def _run(*workers):
+    """Each worker in a thread of its own, switched as often as they can be."""
+    failed, old = [], sys.getswitchinterval()
+
+    def guard(f):
+        try:
+            f()
+        except BaseException as e:                   # noqa: BLE001
+            failed.append(e)
+    threads = [threading.Thread(target=guard, args=(w,)) for w in workers]
+    sys.setswitchinterval(1e-6)
+    try:
+        for t in threads:
+            t.start()
+        for t in threads:
+            t.join()
+    finally:
+        sys.setswitchinterval(old)
+    if failed:
+        raise failed[0]
+
+
+def _bf16(*shape):
+    return torch.zeros(*shape, dtype=torch.bfloat16)
+
+
+def test_threads_that_attend_over_one_cache_send_their_own_arguments(stub):
+    """The library reads its arguments after it has let other threads run."""
+    sent = {}
+
+    def seen(name, args):
+        time.sleep(2e-5)
+        a = args[1]._obj
+        sent[threading.get_ident()].append((a.layer, a.total_q, a.d_seqs, a.d_q, a.d_out, a.d_lse, a.window, args[2], args[3]))
+    stub(seen)
+    cache = kv.KvCache(4, 1, 64, 16, 8, 400, device="cpu")
+
+    def worker(i):
+        def go():
+            sent[threading.get_ident()] = mine = []
+            q, rows, out, lse = _bf16(i + 1, 4, 64), torch.zeros(i + 1, dtype=torch.int32), _bf16(i + 1, 4, 64), torch.zeros(i + 1, 4)
+            for _ in range(200):
+                cache.attend(i, q, rows, window=i, out=out, lse=lse)
+                got = mine.pop()
+                assert got[:7] == (i, i + 1, rows.data_ptr(), q.data_ptr(), out.data_ptr(), lse.data_ptr(), i)
+                assert got[7] is None or got[8] > 0
+        return go
+    _run(*[worker(i) for i in range(4)])
+
+
+def test_calls_that_share_a_workspace_enqueue_their_launches_one_after_another(stub, monkeypatch):
+    """A call of two launches must not have another's between them: both would
+    use the one workspace."""
+    inside = {}
+
+    def seen(name, args):
+        key = "page" if name in ("bs_kv_extend_async", "bs_kv_fork_async", "bs_kv_compact_async") else name
+        assert not inside.get(key), name
+        inside[key] = True
+        time.sleep(2e-5)
+        inside[key] = False
+    stub(seen)
+    monkeypatch.setattr(lora.LoraBatch, "update", lambda self, of, stream=None: None)
+    cache = kv.KvCache(1, 1, 64, 16, 8, 4, device="cpu")
+    ads = [(_bf16(4, 2048), _bf16(32, 4), 1.0)]
+    pack = lora.LoraPack(ads, device="cpu")
+    plan = codec.FixedPlan(codec.fixed_encode(np.full(32 * 2048, 0x3F80, np.uint16)), device="cpu")
+    ids = torch.zeros(2, dtype=torch.int32)
+
+    def pages():
+        for _ in range(100):
+            cache.extend(ids, ids), cache.fork(ids, ids), cache.compact(), cache.attend(0, _bf16(2, 1, 64), ids)
+
+    def products():
+        for n in range(1, 51):
+            batch = lora.LoraBatch(torch.zeros(n, dtype=torch.int32), 1)
+            pack.add(torch.zeros(n, 32), _bf16(n, 2048), batch)
+            plan.gemm_lora(_bf16(n, 2048), 32, 2048, pack, batch)
+
+    _run(pages, pages, products, products)
