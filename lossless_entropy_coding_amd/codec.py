@@ -42,6 +42,11 @@ def _on(stream):
     return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
 
 
+def _capturing(device: torch.device) -> bool:
+    """Whether the current stream's work is being recorded into a graph."""
+    return device.type == "cuda" and torch.cuda.is_current_stream_capturing()
+
+
 def _grown(old: torch.Tensor | None, need: int, device, stream, kept: list, zero: bool = False) -> torch.Tensor:
     """A workspace of `need` bytes or more in place of `old`, which goes to
     `kept`: a captured graph or another stream may still use it.  Each is at

@@ -25,7 +25,7 @@ import threading
 import torch
 
 from . import _lib as L
-from .codec import _grown, _on, _stream_of
+from .codec import _capturing, _grown, _on, _stream_of
 
 _INT32, _BF16, _FP32 = torch.int32, torch.bfloat16, torch.float32
 
@@ -257,12 +257,25 @@ class KvCache:
                 self._attend_need[sizes] = need
             w = self._attend_work
             if need and (w is None or w.numel() < need):
-                w = self._attend_work = _grown(w, need, self.k.device, stream, self._kept, zero=True)
+                w = self._counted_work(need, stream)
             rc = L.lib().bs_kv_attend_async(self._ref, self._args_ref, w.data_ptr() if need else None, need,
                                             _stream_of(q.device, stream))
         if rc:
             L.check(rc, "bs_kv_attend_async")
         return out if lse is False else (out, lse)
+
+    def _counted_work(self, need: int, stream) -> torch.Tensor:
+        """A workspace for attend, its counters zeroed.  Under capture zeroing
+        is recorded but not run, so no other call may count on it: the call
+        then has a workspace of its own in the graph's memory, whose counters
+        each replay zeroes first (a call before the capture spares that)."""
+        with _on(stream):
+            if _capturing(self.k.device):
+                w = torch.empty(need, dtype=torch.uint8, device=self.k.device)
+                w[:4096].zero_()
+                return w
+        self._attend_work = _grown(self._attend_work, need, self.k.device, stream, self._kept, zero=True)
+        return self._attend_work
 
     def check(self) -> None:
         """Raise if a call met one of the conditions that bs.h lists, and clear

@@ -118,3 +118,32 @@ def test_calls_that_share_a_workspace_enqueue_their_launches_one_after_another(s
             plan.gemm_lora(_bf16(n, 2048), 32, 2048, pack, batch)
 
     _run(pages, pages, products, products)
+
+
+def test_counters_zeroed_in_a_capture_serve_no_other_call(stub, monkeypatch):
+    """A recorded fill has not run when the next call is made."""
+    given = []
+    stub(lambda name, args: given.append((args[2], args[3])))
+    cache = kv.KvCache(1, 1, 64, 16, 8, 400, device="cpu")
+    q, ids = _bf16(2, 4, 64), torch.zeros(2, dtype=torch.int32)
+    recording = [True]
+    monkeypatch.setattr(kv, "_capturing", lambda device: recording[0], raising=False)
+    made, empty = [], torch.empty
+    monkeypatch.setattr(torch, "empty", lambda *a, **k: made.append(empty(*a, **k)) or made[-1])
+    cache.attend(0, q, ids)
+    cache.attend(0, q, ids)
+    assert cache._attend_work is None and given[0][1] > 4096
+    of = {t.data_ptr(): t for t in made}
+    assert given[0][0] != given[1][0]
+    for at, size in given:
+        assert of[at].numel() == size and not of[at][:4096].any()
+    recording[0] = False
+    cache.attend(0, q, ids)
+    w = cache._attend_work
+    assert given[2][0] == w.data_ptr() and not w[:4096].any()
+    recording[0] = True                              # large enough and zeroed before: captured calls take it, too
+    cache.attend(0, q, ids)
+    assert given[3][0] == w.data_ptr()
+    q, ids = _bf16(8, 64, 64), torch.zeros(8, dtype=torch.int32)
+    cache.attend(0, q, ids)
+    assert given[4][1] > w.numel() and given[4][0] != w.data_ptr() and cache._attend_work is w
