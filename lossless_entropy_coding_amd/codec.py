@@ -42,6 +42,14 @@ def _on(stream):
     return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
 
 
+def _same_device(device: torch.device, **tensors) -> None:
+    """Raise unless every tensor is on `device`: the library takes addresses,
+    and a kernel that follows another device's faults."""
+    for name, t in tensors.items():
+        if t.device != device:
+            raise ValueError(f"{name} is on {t.device}, not on {device}")
+
+
 def _capturing(device: torch.device) -> bool:
     """Whether the current stream's work is being recorded into a graph."""
     return device.type == "cuda" and torch.cuda.is_current_stream_capturing()
@@ -588,6 +596,7 @@ class FixedPlan:
         if x.dtype not in (torch.bfloat16, torch.int16) or x.dim() != 2 or x.shape[1] != cols or not x.is_contiguous():
             raise ValueError(f"x must be a contiguous (tokens, {cols}) bfloat16 tensor")
         batch.check_for(pack, x.shape[0])
+        _same_device(self.dev.device, x=x, pack=pack.a, batch=batch.dev, out=x if out is None else out)
         if out is None:
             with _on(stream):
                 out = torch.empty(x.shape[0], rows, dtype=torch.float32, device=self.dev.device)

@@ -25,20 +25,13 @@ import threading
 import torch
 
 from . import _lib as L
-from .codec import _capturing, _grown, _on, _stream_of
+from .codec import _capturing, _grown, _on, _same_device, _stream_of
 
 _INT32, _BF16, _FP32 = torch.int32, torch.bfloat16, torch.float32
 
 
 def _wide(head_dim: int) -> int:
     return -(-head_dim // 64) * 64
-
-
-def _ids(t: torch.Tensor, name: str) -> int:
-    """Checks a vector of row numbers, counts or offsets; returns its length."""
-    if t.dtype is not _INT32 or t.dim() != 1 or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous int32 vector on the device")
-    return t.numel()
 
 
 class KvCache:
@@ -76,6 +69,8 @@ class KvCache:
         for name, (t, kind, shape) in want.items():
             if t.dtype != kind or tuple(t.shape) != shape or not t.is_contiguous():
                 raise ValueError(f"{name} must be a contiguous {kind} tensor of shape {shape}")
+        _same_device(k.device, **{name: t for name, (t, _, _) in want.items()})
+        self.device = k.device
         self.k, self.v, self.scale, self.refs, self.table, self.lens = k, v, scale, refs, table, lens
         self.layers, self.n_pages, self.kv_heads, self.page_tokens = layers, n_pages, heads, page
         self.head_dim, self.dtype, self.max_seqs, self.max_pages = head_dim, dtype, lens.numel(), table.shape[1]
@@ -94,55 +89,61 @@ class KvCache:
         self._lock = threading.Lock()
         self._page_need, self._attend_need = {}, {}        # workspace bytes by the sizes of a call
 
+    def _ids(self, t: torch.Tensor, name: str) -> int:
+        """Checks a vector of row numbers, counts or offsets; returns its length."""
+        if t.dtype is not _INT32 or t.dim() != 1 or not t.is_contiguous() or t.device != self.device:
+            raise ValueError(f"{name} must be a contiguous int32 vector on {self.device}")
+        return t.numel()
+
     # ------------------------------------------------------------ pages
     def _work(self, n: int, stream) -> torch.Tensor:
         need = self._page_need.get(n)
         if need is None:
             need = self._page_need[n] = int(L.lib().bs_kv_pages_work_bytes(self._ref, n))
         if self._page_work is None or self._page_work.numel() < need:
-            self._page_work = _grown(self._page_work, need, self.k.device, stream, self._kept)
+            self._page_work = _grown(self._page_work, need, self.device, stream, self._kept)
         return self._page_work
 
     def extend(self, rows: torch.Tensor, counts: torch.Tensor, stream=None) -> None:
         """Make room for counts[i] more tokens in row rows[i] (distinct rows);
         all rows grow, or none (bs_kv_extend_async)."""
-        n = _ids(rows, "rows")
-        if _ids(counts, "counts") != n:
+        n = self._ids(rows, "rows")
+        if self._ids(counts, "counts") != n:
             raise ValueError("one count per row")
         with self._lock:
             w = self._work(n, stream)
             rc = L.lib().bs_kv_extend_async(self._ref, n, rows.data_ptr(), counts.data_ptr(), w.data_ptr(), w.numel(),
-                                            _stream_of(rows.device, stream))
+                                            _stream_of(self.device, stream))
         if rc:
             L.check(rc, "bs_kv_extend_async")
 
     def fork(self, parents: torch.Tensor, children: torch.Tensor, stream=None) -> None:
         """Empty rows children[i] become copies of rows parents[i], sharing
         their whole pages (bs_kv_fork_async)."""
-        n = _ids(parents, "parents")
-        if _ids(children, "children") != n:
+        n = self._ids(parents, "parents")
+        if self._ids(children, "children") != n:
             raise ValueError("one parent per child")
         with self._lock:
             w = self._work(n, stream)
             rc = L.lib().bs_kv_fork_async(self._ref, n, parents.data_ptr(), children.data_ptr(), w.data_ptr(), w.numel(),
-                                          _stream_of(parents.device, stream))
+                                          _stream_of(self.device, stream))
         if rc:
             L.check(rc, "bs_kv_fork_async")
 
     def free(self, rows: torch.Tensor, stream=None) -> None:
         """Empty rows (bs_kv_free_async)."""
-        n = _ids(rows, "rows")
-        rc = L.lib().bs_kv_free_async(self._ref, n, rows.data_ptr(), _stream_of(rows.device, stream))
+        n = self._ids(rows, "rows")
+        rc = L.lib().bs_kv_free_async(self._ref, n, rows.data_ptr(), _stream_of(self.device, stream))
         if rc:
             L.check(rc, "bs_kv_free_async")
 
     def copy_pages(self, source: torch.Tensor, target: torch.Tensor, stream=None) -> None:
         """Copy pages in every layer (bs_kv_copy_pages_async)."""
-        n = _ids(source, "source")
-        if _ids(target, "target") != n:
+        n = self._ids(source, "source")
+        if self._ids(target, "target") != n:
             raise ValueError("one target per source")
         L.check(L.lib().bs_kv_copy_pages_async(self._ref, n, source.data_ptr(), target.data_ptr(),
-                                               _stream_of(source.device, stream)), "bs_kv_copy_pages_async")
+                                               _stream_of(self.device, stream)), "bs_kv_copy_pages_async")
 
     def compact(self, table_out: torch.Tensor | None = None, refs_out: torch.Tensor | None = None, stream=None) -> None:
         """Move the pages in use to the lowest places (bs_kv_compact_async).
@@ -162,9 +163,10 @@ class KvCache:
             for t, like, name in ((table_out, self.table, "table_out"), (refs_out, self.refs, "refs_out")):
                 if t.dtype != like.dtype or t.shape != like.shape or not t.is_contiguous():
                     raise ValueError(f"{name} must be a contiguous int32 tensor of shape {tuple(like.shape)}")
+            _same_device(self.device, table_out=table_out, refs_out=refs_out)
             w = self._work(0, stream)
             L.check(L.lib().bs_kv_compact_async(self._ref, table_out.data_ptr(), refs_out.data_ptr(), w.data_ptr(), w.numel(),
-                                                _stream_of(self.k.device, stream)), "bs_kv_compact_async")
+                                                _stream_of(self.device, stream)), "bs_kv_compact_async")
             if swap:
                 self._spare = (self.table, self.refs)
                 self.table, self.refs = table_out, refs_out
@@ -174,6 +176,8 @@ class KvCache:
     def _tokens(self, t: torch.Tensor, heads: int | None, name: str) -> int:
         """Checks a (tokens, heads, head_dim) tensor with a token's values side
         by side; returns its token stride."""
+        if t.device != self.device:
+            raise ValueError(f"{name} is on {t.device}, the cache on {self.device}")
         if t.dim() != 3 or t.shape[2] != self.head_dim or (heads is not None and t.shape[1] != heads):
             raise ValueError(f"{name} must be (tokens, {heads or 'heads'}, {self.head_dim})")
         n, h, d = t.shape
@@ -185,12 +189,12 @@ class KvCache:
         return h * d if n <= 1 else s[0]
 
     def _rows(self, rows, starts, total, max_new):
-        n = _ids(rows, "rows")
+        n = self._ids(rows, "rows")
         if starts is None:
             if n != total:
                 raise ValueError(f"{total} tokens for {n} rows: give starts")
             return n, 1, None
-        if _ids(starts, "starts") != n + 1:
+        if self._ids(starts, "starts") != n + 1:
             raise ValueError("starts holds one offset per row and the end")
         return n, max(1, min(total, total if max_new is None else max_new)), starts.data_ptr()
 
@@ -207,7 +211,7 @@ class KvCache:
         n, most, at = self._rows(rows, starts, total, max_new)
         rc = L.lib().bs_kv_append_async(self._ref, layer, n, rows.data_ptr(), at, total, most, k.data_ptr(), ks,
                                         v.data_ptr(), vs, L.T_FP32 if kind is _FP32 else L.T_BF16,
-                                        _stream_of(k.device, stream))
+                                        _stream_of(self.device, stream))
         if rc:
             L.check(rc, "bs_kv_append_async")
 
@@ -228,7 +232,7 @@ class KvCache:
         total, heads, _ = shape = q.shape
         if out is None:
             with _on(stream):
-                out = torch.empty(shape, dtype=_BF16, device=q.device)
+                out = torch.empty(shape, dtype=_BF16, device=self.device)
             os = heads * self.head_dim
         elif out.dtype is not _BF16 or out.shape != shape:
             raise ValueError("out must be bfloat16 of q's shape")
@@ -236,9 +240,10 @@ class KvCache:
             os = self._tokens(out, None, "out")
         if lse is True:
             with _on(stream):
-                lse = torch.empty(shape[:2], dtype=_FP32, device=q.device)
-        elif lse is not False and (lse.dtype is not _FP32 or lse.shape != shape[:2] or not lse.is_contiguous()):
-            raise ValueError("lse must be a contiguous float32 tensor of (tokens, heads)")
+                lse = torch.empty(shape[:2], dtype=_FP32, device=self.device)
+        elif lse is not False and (lse.dtype is not _FP32 or lse.shape != shape[:2] or not lse.is_contiguous() or
+                                   lse.device != self.device):
+            raise ValueError(f"lse must be a contiguous float32 tensor of (tokens, heads) on {self.device}")
         if window < 0 or sinks < 0 or max_len < 0:
             raise ValueError("window, sinks and max_len are not negative")
         n, most, at = self._rows(rows, starts, total, max_new)
@@ -259,7 +264,7 @@ class KvCache:
             if need and (w is None or w.numel() < need):
                 w = self._counted_work(need, stream)
             rc = L.lib().bs_kv_attend_async(self._ref, self._args_ref, w.data_ptr() if need else None, need,
-                                            _stream_of(q.device, stream))
+                                            _stream_of(self.device, stream))
         if rc:
             L.check(rc, "bs_kv_attend_async")
         return out if lse is False else (out, lse)
@@ -270,11 +275,11 @@ class KvCache:
         then has a workspace of its own in the graph's memory, whose counters
         each replay zeroes first (a call before the capture spares that)."""
         with _on(stream):
-            if _capturing(self.k.device):
-                w = torch.empty(need, dtype=torch.uint8, device=self.k.device)
+            if _capturing(self.device):
+                w = torch.empty(need, dtype=torch.uint8, device=self.device)
                 w[:4096].zero_()
                 return w
-        self._attend_work = _grown(self._attend_work, need, self.k.device, stream, self._kept, zero=True)
+        self._attend_work = _grown(self._attend_work, need, self.device, stream, self._kept, zero=True)
         return self._attend_work
 
     def check(self) -> None:

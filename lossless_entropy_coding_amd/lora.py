@@ -17,7 +17,7 @@ import threading
 import torch
 
 from . import _lib as L
-from .codec import _grown, _on, _stream_of
+from .codec import _grown, _on, _same_device, _stream_of
 
 
 class LoraPack:
@@ -77,6 +77,7 @@ class LoraPack:
         if out.dtype != y.dtype or out.shape != y.shape or out.stride() != y.stride():
             raise ValueError("out must have y's shape, type and strides")
         batch.check_for(self, x.shape[0])
+        _same_device(self.a.device, x=x, y=y, out=out, batch=batch.dev)
         if x.shape[0] == 0:
             return out
         with self._lock:
@@ -112,6 +113,7 @@ class LoraBatch:
         """Another assignment of as many tokens (the buffer stays, as a captured graph needs)."""
         if adapter_of.dtype != torch.int32 or adapter_of.numel() != self.tokens or not adapter_of.is_contiguous():
             raise ValueError(f"adapter_of must be a contiguous int32 vector of {self.tokens}")
+        _same_device(self.dev.device, adapter_of=adapter_of)
         rc = L.lib().bs_lora_batch_async(adapter_of.data_ptr(), self.tokens, self.adapters, self.dev.data_ptr(),
                                          4 * self.dev.numel(), _stream_of(adapter_of.device, stream))
         L.check(rc, "bs_lora_batch_async")

@@ -147,3 +147,54 @@ def test_counters_zeroed_in_a_capture_serve_no_other_call(stub, monkeypatch):
     q, ids = _bf16(8, 64, 64), torch.zeros(8, dtype=torch.int32)
     cache.attend(0, q, ids)
     assert given[4][1] > w.numel() and given[4][0] != w.data_ptr() and cache._attend_work is w
+
+
+def _away(t):
+    return t.to("meta")
+
+
+def test_tensors_on_another_device_are_refused(stub):
+    """Every argument in turn on a device that is not the cache's, the pack's
+    or the plan's: nothing reaches the library."""
+    launched = []
+    stub(lambda name, args: launched.append(name))
+    cache = kv.KvCache(1, 2, 64, 16, 8, 4, device="cpu")
+    ids, starts = torch.zeros(2, dtype=torch.int32), torch.tensor([0, 1, 2], dtype=torch.int32)
+    k, q, lse = _bf16(2, 2, 64), _bf16(2, 4, 64), torch.zeros(2, 4)
+    pack = lora.LoraPack([(_bf16(4, 2048), _bf16(32, 4), 1.0)], device="cpu")
+    plan = codec.FixedPlan(codec.fixed_encode(np.full(32 * 2048, 0x3F80, np.uint16)), device="cpu")
+    batch = lora.LoraBatch(ids, 1)
+    x, y = _bf16(2, 2048), torch.zeros(2, 32)
+    calls = [
+        (cache.extend, dict(rows=ids, counts=ids)), (cache.fork, dict(parents=ids, children=ids)), (cache.free, dict(rows=ids)),
+        (cache.copy_pages, dict(source=ids, target=ids)),
+        (cache.compact, dict(table_out=cache.table.clone(), refs_out=cache.refs.clone())),
+        (cache.append, dict(layer=0, k=k, v=k, rows=ids, starts=starts)),
+        (cache.attend, dict(layer=0, q=q, rows=ids, starts=starts, out=q.clone(), lse=lse)),
+        (pack.add, dict(y=y, x=x, batch=batch, out=y.clone())), (batch.update, dict(adapter_of=ids)),
+        (plan.gemm_lora, dict(x=x, rows=32, cols=2048, pack=pack, batch=batch, out=y)),
+    ]
+    for call, args in calls:
+        del launched[:]
+        call(**args, stream=None)
+        assert len(launched) == 1, call
+        for name in [n for n, v in args.items() if isinstance(v, torch.Tensor)]:
+            with pytest.raises(ValueError, match="meta|on cpu"):
+                call(**{**args, name: _away(args[name])})
+            assert len(launched) == 1, (call, name)
+    far = lora.LoraPack([(_bf16(4, 2048), _bf16(32, 4), 1.0)], device="cpu")
+    far.a = _away(far.a)
+    other = lora.LoraBatch(ids, 1)
+    other.dev = _away(other.dev)
+    del launched[:]
+    for args in (dict(pack=far, batch=batch), dict(pack=pack, batch=other)):
+        with pytest.raises(ValueError, match="meta"):
+            plan.gemm_lora(x, 32, 2048, **args)
+    with pytest.raises(ValueError, match="meta"):
+        pack.add(y, x, other)
+    parts = dict(k=cache.k, v=cache.v, scale=cache.scale, refs=cache.refs, table=cache.table, lens=cache.lens)
+    kv.KvCache.over(**parts, head_dim=64)
+    for name in parts:
+        with pytest.raises(ValueError, match="meta|on cpu"):
+            kv.KvCache.over(**{**parts, name: _away(parts[name])}, head_dim=64)
+    assert not launched
