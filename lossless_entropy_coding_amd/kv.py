@@ -255,16 +255,18 @@ class KvCache:
             a.q_stride, a.out_stride, a.scale, a.softcap, a.window, a.sinks = qs, os, scale, softcap, window, sinks
             sizes = (n, heads, total, most, max_len, window, sinks)
             need = self._attend_need.get(sizes)
-            if need is None:
-                if len(self._attend_need) > 4096:              # lengths that grow token by token
-                    self._attend_need.clear()
+            known = need is not None
+            if not known:
                 need = int(L.lib().bs_kv_attend_work_bytes(self._ref, self._args_ref))
-                self._attend_need[sizes] = need
             w = self._attend_work
             if need and (w is None or w.numel() < need):
                 w = self._counted_work(need, stream)
             rc = L.lib().bs_kv_attend_async(self._ref, self._args_ref, w.data_ptr() if need else None, need,
                                             _stream_of(self.device, stream))
+            if not rc and not known:                       # a refused call's size is 0, whatever its rows need
+                if len(self._attend_need) > 4096:          # lengths that grow token by token
+                    self._attend_need.clear()
+                self._attend_need[sizes] = need
         if rc:
             L.check(rc, "bs_kv_attend_async")
         return out if lse is False else (out, lse)

@@ -198,3 +198,25 @@ def test_tensors_on_another_device_are_refused(stub):
         with pytest.raises(ValueError, match="meta|on cpu"):
             kv.KvCache.over(**{**parts, name: _away(parts[name])}, head_dim=64)
     assert not launched
+
+
+def test_a_refused_attention_leaves_later_ones_their_workspace(stub):
+    """The library's own checks, with nothing launched where they pass."""
+    given = []
+    real = L.lib()
+
+    def seen(name, args):
+        a = args[1]._obj
+        if a.layer >= 2 or a.softcap < 0 or a.out_stride < 256:
+            return real.bs_kv_attend_async(*args)
+        given.append(args[3])
+        return 0
+    stub(seen)
+    cache = kv.KvCache(2, 1, 64, 16, 8, 400, device="cpu")
+    q, ids = _bf16(2, 4, 64), torch.zeros(2, dtype=torch.int32)
+    for bad in (dict(layer=9), dict(layer=0, softcap=-1.0), dict(layer=0, out=_bf16(4, 64).expand(2, 4, 64))):
+        with pytest.raises(L.BSError):
+            cache.attend(q=q, rows=ids, **bad)
+    cache.attend(1, q, ids)
+    cache.attend(0, q, ids)
+    assert len(given) == 2 and given[0] == given[1] > 4096
