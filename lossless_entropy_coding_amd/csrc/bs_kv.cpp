@@ -299,7 +299,7 @@ bs_status bs_kv_attend_async(const bs_kv_cache* cache, const bs_kv_attend_args* 
 
 uint64_t bs_kv_pages_work_bytes(const bs_kv_cache* cache, uint32_t n) {
     bsd::KvView v;
-    if (view(cache, v) != BS_OK) return 0;
+    if (view(cache, v) != BS_OK || n > kGridYZ) return 0;
     return page_work(v, n);
 }
 

@@ -165,7 +165,7 @@ bs_status bs_lora_batch_async(const int32_t* d_adapter_of, uint32_t tokens, uint
 }
 
 uint64_t bs_lora_work_bytes(const bs_lora_pack* pack, uint32_t tokens) {
-    if (check_pack(pack) != BS_OK || !check_tokens(tokens)) return 0;
+    if (check_pack(pack) != BS_OK || !check_tokens(tokens) || !check_grid(pack, tokens)) return 0;
     return inner_bytes(pack, tokens);
 }
 
@@ -207,6 +207,7 @@ bs_status bs_lora_add_async(const bs_lora_pack* pack, const int32_t* d_batch, ui
 
 uint64_t bs_fixed_gemm_lora_work_bytes(uint64_t rows, uint64_t cols, uint32_t batch, const bs_lora_pack* pack) {
     if (check_pack(pack) != BS_OK || batch == 0 || batch > 64) return 0;
+    if (pack->rows != rows || pack->cols != cols || cols % 2048) return 0;
     return align_up(shares_bytes(rows, cols, batch), 256) + inner_bytes(pack, batch) + x_bytes(rows, cols, batch);
 }
 

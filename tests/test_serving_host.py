@@ -204,3 +204,16 @@ def test_reference_codes():
     assert list(S.round_to_code(np.array([0.5, 1.5, -2.5, 126.5, 127]), "int8").view(np.int8)) == [0, 2, -2, 126, 127]
     for kind, q in S.LARGEST.items():
         assert S.scale_for(q, kind) == 1.0 and S.scale_for(np.nextafter(q, 999), kind) == 2.0 and S.scale_for(0.0, kind) == 2.0 ** -60
+
+
+def test_workspace_sizes_of_refused_shapes_are_zero():
+    lib, p = L.lib(), _pack(rows=32, cols=4096)
+    size = lambda rows, cols, n=4, p=p: int(lib.bs_fixed_gemm_lora_work_bytes(rows, cols, n, C.byref(p)))   # noqa: E731
+    assert size(32, 4096) > 0 and size(32, 4096, 64) > 0
+    for shape in ((16, 4096), (32, 2048), (64, 2048), (1 << 60, 4096), (32, 1 << 60), (0, 4096), (32, 0), (32, 4096, 0)):
+        assert size(*shape) == 0, shape
+    for cols in (3584, 4095, 32, 2047):
+        assert size(32, cols, 4, _pack(rows=32, cols=cols)) == 0, cols
+    # 2^24 tokens of 2^26 - 1 rows: more workgroups than a launch takes
+    assert lib.bs_lora_work_bytes(C.byref(_pack(rows=(1 << 26) - 1)), 1 << 24) == 0
+    assert lib.bs_kv_pages_work_bytes(C.byref(_cache()), 65535) > 0 and lib.bs_kv_pages_work_bytes(C.byref(_cache()), 65536) == 0
