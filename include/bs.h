@@ -596,7 +596,8 @@ uint64_t bs_lora_work_bytes(const bs_lora_pack* pack, uint32_t tokens);
  * the same buffer or two that do not overlap.  Sums are held in fp32 in one
  * fixed order (the same result on every run) and y is rounded once.  Two
  * kernel launches on `stream`; calls that share d_work (16-B aligned) must
- * not overlap.  Errors: BS_E_INVAL, BS_E_HIP. */
+ * not overlap.  Errors: BS_E_INVAL (a workspace that overlaps x or y among
+ * them), BS_E_HIP. */
 bs_status bs_lora_add_async(const bs_lora_pack* pack, const int32_t* d_batch, uint32_t tokens, const void* d_x,
                             uint64_t x_stride, const void* d_y_in, void* d_y_out, uint64_t y_stride, uint32_t y_type,
                             void* d_work, uint64_t work_bytes, void* stream);
@@ -607,8 +608,8 @@ bs_status bs_lora_add_async(const bs_lora_pack* pack, const int32_t* d_batch, ui
  * columns are shared out over workgroups, by the launch that adds the
  * shares.  Entries of tokens without an adapter equal bs_fixed_gemm_async's
  * within the fp32 bound (bit for bit where the shares are the same).  d_work: 256-B aligned, at least
- * bs_fixed_gemm_lora_work_bytes (0: a shape or pack that is refused).  Other
- * arguments and errors as for bs_fixed_gemm_async and bs_lora_add_async. */
+ * bs_fixed_gemm_lora_work_bytes (0: a shape or pack that is refused), none of
+ * it in X or Y.  Other arguments and errors as for bs_fixed_gemm_async and bs_lora_add_async. */
 uint64_t bs_fixed_gemm_lora_work_bytes(uint64_t rows, uint64_t cols, uint32_t batch, const bs_lora_pack* pack);
 bs_status bs_fixed_gemm_lora_async(const bs_fixed_info* info, const void* d_blob, uint64_t rows, uint64_t cols,
                                    uint32_t batch, const void* d_x, float* d_y, uint32_t* d_status,
@@ -750,7 +751,8 @@ typedef struct {
  * d_work (16-B aligned): bs_kv_attend_work_bytes, which gives 0 where rows
  * need not be split; without it (NULL) they are not.  Its first 4096 bytes
  * are zero before the first call that is given it, and every call leaves
- * them so; calls that share it must not overlap. */
+ * them so; calls that share it must not overlap, nor it the queries or
+ * results. */
 bs_status bs_kv_attend_async(const bs_kv_cache* cache, const bs_kv_attend_args* args, void* d_work, uint64_t work_bytes,
                              void* stream);
 uint64_t bs_kv_attend_work_bytes(const bs_kv_cache* cache, const bs_kv_attend_args* args);

@@ -35,6 +35,16 @@ void sha256(const void* data, uint64_t n, uint8_t out[32]);
 
 inline uint64_t align_up(uint64_t v, uint64_t a) { return (v + a - 1) / a * a; }
 
+// whether na bytes from a and nb bytes from b share any
+inline bool overlap(const void* a, uint64_t na, const void* b, uint64_t nb) {
+    const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+    return na && nb && x < y + nb && y < x + na;
+}
+
+// bytes from the first element of the first of n rows to the last of the
+// last: rows of `row` elements of el bytes, `stride` elements apart
+inline uint64_t extent(uint64_t n, uint64_t stride, uint64_t row, uint64_t el) { return n ? ((n - 1) * stride + row) * el : 0; }
+
 // host worker threads: `req`, or the hardware's count when 0
 inline uint32_t pick_threads(uint32_t req) {
     uint32_t hw = std::thread::hardware_concurrency();

@@ -23,11 +23,6 @@ bs_status launched(int e, const char* what) {
 
 bool aligned(const void* p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 
-bool overlap(const void* a, uint64_t na, const void* b, uint64_t nb) {
-    const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
-    return x < y + nb && y < x + na;
-}
-
 // a checked view of the caller's cache
 bs_status view(const bs_kv_cache* c, bsd::KvView& v) {
     if (!c) { set_error("NULL cache"); return BS_E_INVAL; }
@@ -288,6 +283,13 @@ bs_status bs_kv_attend_async(const bs_kv_cache* cache, const bs_kv_attend_args* 
         if (work_bytes < part_bytes(a, splits)) {
             set_error("workspace of %llu B, %llu B needed", (unsigned long long)work_bytes,
                       (unsigned long long)part_bytes(a, splits));
+            return BS_E_INVAL;
+        }
+        const uint64_t need = part_bytes(a, splits), row = (uint64_t)a.heads * a.c.dim;
+        if (overlap(d_work, need, a.out, extent(a.total, a.out_stride, row, 2)) ||
+            overlap(d_work, need, a.q, extent(a.total, a.q_stride, row, 2)) ||
+            (a.lse && overlap(d_work, need, a.lse, 4ull * a.total * a.heads))) {
+            set_error("the workspace overlaps queries or results");
             return BS_E_INVAL;
         }
         a.splits = splits;

@@ -193,6 +193,12 @@ bs_status bs_lora_add_async(const bs_lora_pack* pack, const int32_t* d_batch, ui
                   (unsigned long long)inner_bytes(pack, tokens));
         return BS_E_INVAL;
     }
+    const uint64_t need = inner_bytes(pack, tokens), ny = extent(tokens, y_stride, pack->rows, el);
+    if (overlap(d_work, need, d_x, extent(tokens, x_stride, pack->cols, 2)) || overlap(d_work, need, d_y_in, ny) ||
+        overlap(d_work, need, d_y_out, ny)) {
+        set_error("the workspace overlaps X or Y");
+        return BS_E_INVAL;
+    }
     bsd::LoraArgs a;
     fill(pack, d_batch, tokens, d_x, x_stride, (float*)d_work, a);
     a.y_in = d_y_in;
@@ -225,9 +231,14 @@ bs_status bs_fixed_gemm_lora_async(const bs_fixed_info* info, const void* d_blob
     if (batch == 0 || batch > 64) { set_error("batch %u outside 1..64", batch); return BS_E_INVAL; }
     if (!d_batch || !d_work) { set_error("NULL argument"); return BS_E_INVAL; }
     if (!aligned(d_batch, 16) || !aligned(d_work, 256) || !aligned(d_y, 4)) { set_error("a misaligned buffer"); return BS_E_INVAL; }
-    if (work_bytes < bs_fixed_gemm_lora_work_bytes(rows, cols, batch, pack)) {
-        set_error("workspace of %llu B, %llu B needed", (unsigned long long)work_bytes,
-                  (unsigned long long)bs_fixed_gemm_lora_work_bytes(rows, cols, batch, pack));
+    const uint64_t need = bs_fixed_gemm_lora_work_bytes(rows, cols, batch, pack);
+    if (work_bytes < need) {
+        set_error("workspace of %llu B, %llu B needed", (unsigned long long)work_bytes, (unsigned long long)need);
+        return BS_E_INVAL;
+    }
+    // all of it: the shares, the inner products and X in operand order
+    if (overlap(d_work, need, d_y, 4ull * batch * rows) || overlap(d_work, need, d_x, 2ull * batch * cols)) {
+        set_error("the workspace overlaps X or Y");
         return BS_E_INVAL;
     }
     const uint64_t split = shares_bytes(rows, cols, batch);

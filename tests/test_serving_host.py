@@ -217,3 +217,32 @@ def test_workspace_sizes_of_refused_shapes_are_zero():
     # 2^24 tokens of 2^26 - 1 rows: more workgroups than a launch takes
     assert lib.bs_lora_work_bytes(C.byref(_pack(rows=(1 << 26) - 1)), 1 << 24) == 0
     assert lib.bs_kv_pages_work_bytes(C.byref(_cache()), 65535) > 0 and lib.bs_kv_pages_work_bytes(C.byref(_cache()), 65536) == 0
+
+
+def test_workspaces_over_inputs_or_results_are_refused():
+    """Every part of a workspace, at its first and its last bytes.  Nothing is launched: the addresses are made up."""
+    from lossless_entropy_coding_amd import codec
+    lib, at, words = L.lib(), 1 << 30, 1 << 28           # buffers 256 MiB apart
+    X, Y, W, O, B = at, at + words, at + 2 * words, at + 3 * words, at + 4 * words
+
+    def refused(call, size, *others):
+        for other, n in others:
+            for w in (other, other + n // 256 * 256 - 256 if n >= 256 else other, (other - size) // 256 * 256 + 256):
+                assert call(w) == L.BS_E_INVAL, (hex(w), hex(other), n, size)
+    for rows, cols, n in ((32, 4096, 4), (32, 2048, 33), (64, 14336, 64), (4096, 2048, 1)):   # shares or none, X laid out or not
+        blob = codec.fixed_encode(np.full(rows * cols, 0x3F80, np.uint16))
+        info, p = codec.fixed_info(blob), _pack(rows=rows, cols=cols, d_a=B, d_b=B)
+        size = int(lib.bs_fixed_gemm_lora_work_bytes(rows, cols, n, C.byref(p)))
+        refused(lambda w: lib.bs_fixed_gemm_lora_async(C.byref(info), B, rows, cols, n, X, Y, None, C.byref(p), B, w, size, None),
+                size, (X, 2 * n * cols), (Y, 4 * n * rows))
+    p = _pack(rows=100, cols=200)
+    size = int(lib.bs_lora_work_bytes(C.byref(p), 70))
+    refused(lambda w: lib.bs_lora_add_async(C.byref(p), B, 70, X, 333, Y, O, 120, 1, w, size, None), size,
+            (X, 2 * (69 * 333 + 200)), (Y, 2 * (69 * 120 + 100)), (O, 2 * (69 * 120 + 100)))
+    c = _cache(max_pages=1 << 16, d_k=B, d_v=B)
+    a = L.KvAttendArgs(*[dict(layer=0, n_seqs=2, heads=4, total_q=2, max_new=1, max_len=0, d_seqs=B, d_starts=None, d_q=X, d_out=Y,
+                              d_lse=O, q_stride=300, out_stride=400, scale=0.0, softcap=0.0, window=0, sinks=0)[n]
+                         for n, _ in L.KvAttendArgs._fields_])
+    size = int(lib.bs_kv_attend_work_bytes(C.byref(c), C.byref(a)))
+    refused(lambda w: lib.bs_kv_attend_async(C.byref(c), C.byref(a), w, size, None), size,
+            (X, 2 * 556), (Y, 2 * 656), (O, 32))
