@@ -387,14 +387,17 @@ __global__ __launch_bounds__(256) void append_kernel(KvAppend a) {
 // ------------------------------------------------------------------ pages
 constexpr uint32_t kScan = 1024;             // threads of the allocating workgroup
 
-// exclusive prefix over the workgroup of v, and its total
-__device__ __forceinline__ uint32_t block_prefix(uint32_t v, uint32_t* sums, uint32_t& total) {
+// exclusive prefix over the workgroup of v, and its total.  Sums stop at `cap`
+// (a total of less than cap is exact, and so are its prefixes): up to 1024
+// rows of up to 2^27 pages each would pass 32 bits
+__device__ __forceinline__ uint32_t block_prefix(uint32_t v, uint32_t* sums, uint32_t& total, uint32_t cap = 1u << 30) {
     const uint32_t t = threadIdx.x, lane = t & 63u, w = t >> 6;
+    v = min(v, cap);
     uint32_t x = v;
 #pragma unroll
     for (int s = 1; s < 64; s <<= 1) {
         const uint32_t y = __shfl_up(x, s);
-        if (lane >= (uint32_t)s) x += y;
+        if (lane >= (uint32_t)s) x = min(x + y, cap);
     }
     __syncthreads();
     if (lane == 63) sums[w] = x;
@@ -402,8 +405,8 @@ __device__ __forceinline__ uint32_t block_prefix(uint32_t v, uint32_t* sums, uin
     uint32_t before = 0, all = 0;
     for (uint32_t i = 0; i < blockDim.x / 64; i++) {
         const uint32_t y = sums[i];
-        if (i < w) before += y;
-        all += y;
+        if (i < w) before = min(before + y, cap);
+        all = min(all + y, cap);
     }
     total = all;
     return before + x - v;
@@ -479,13 +482,13 @@ __global__ __launch_bounds__(kScan) void alloc_kernel(KvPages p) {
         }
         if (err) atomicOr(&bad, err);
         uint32_t sum;
-        const uint32_t at = block_prefix(need, sums, sum);
+        const uint32_t at = block_prefix(need, sums, sum, c.n_pages + 1);
         if (i < p.n) {
             offs[i] = (int32_t)(total + at);
             lens[i] = had;
         }
         total += sum;
-        if (total > c.n_pages) {               // the same in every thread; keeps the sum from wrapping
+        if (total > c.n_pages) {               // the same in every thread
             if (t == 0) atomicOr(&bad, (uint32_t)kStPages);
             break;
         }

@@ -74,3 +74,22 @@ def test_attention_first_called_in_a_capture():
         got = twin.attend(0, q, rows)
         torch.cuda.synchronize()
         assert torch.equal(got, want[4][0])
+
+
+def test_growth_by_more_pages_than_32_bits_count():
+    """1024 rows of 2^22 pages each: the pages wanted are 2^32, a sum that wraps
+    to 0 would let the rows grow with no pages of their own."""
+    n, pages = 1024, 1 << 22
+    cache = kv.KvCache(1, 1, 1, 64, n, pages, page_tokens=16)
+    rows = torch.arange(n, dtype=torch.int32, device="cuda")
+    for last in (16 * pages, 16 * pages - 15, 1, 0):
+        counts = torch.full((n,), 16 * pages, dtype=torch.int32, device="cuda")
+        counts[-1] = last
+        cache.extend(rows, counts)
+        torch.cuda.synchronize()
+        assert int(cache.status.item()) == 1, last
+        cache.status.zero_()
+        assert not cache.lens.any() and not cache.refs.any()
+    cache.extend(rows[:64], torch.ones(64, dtype=torch.int32, device="cuda"))
+    cache.check()
+    assert torch.equal(cache.table[:64, 0], rows[:64]) and bool((cache.refs == 1).all())
