@@ -596,20 +596,22 @@ class FixedPlan:
         if x.dtype not in (torch.bfloat16, torch.int16) or x.dim() != 2 or x.shape[1] != cols or not x.is_contiguous():
             raise ValueError(f"x must be a contiguous (tokens, {cols}) bfloat16 tensor")
         batch.check_for(pack, x.shape[0])
-        _same_device(self.dev.device, x=x, pack=pack.a, batch=batch.dev, out=x if out is None else out)
+        at = self.dev.device
+        if x.device != at or pack.device != at or batch.dev.device != at or (out is not None and out.device != at):
+            _same_device(at, x=x, pack=pack.a, batch=batch.dev, out=x if out is None else out)
         if out is None:
             with _on(stream):
-                out = torch.empty(x.shape[0], rows, dtype=torch.float32, device=self.dev.device)
+                out = torch.empty(x.shape[0], rows, dtype=torch.float32, device=at)
         elif out.dtype != torch.float32 or tuple(out.shape) != (x.shape[0], rows) or not out.is_contiguous():
             raise ValueError(f"out must be a contiguous ({x.shape[0]}, {rows}) float32 tensor")
         with self._lora_lock:
             need = int(L.lib().bs_fixed_gemm_lora_work_bytes(rows, cols, x.shape[0], pack.ref))
             if self._lora_work is None or self._lora_work.numel() < need:
-                self._lora_work = _grown(self._lora_work, need, self.dev.device, stream, self._lora_kept)
+                self._lora_work = _grown(self._lora_work, need, at, stream, self._lora_kept)
             rc = L.lib().bs_fixed_gemm_lora_async(C.byref(self.info), self.dev.data_ptr(), rows, cols, x.shape[0],
                                                   x.data_ptr(), out.data_ptr(), self.status.data_ptr() if status else None,
                                                   pack.ref, batch.dev.data_ptr(), self._lora_work.data_ptr(),
-                                                  self._lora_work.numel(), _stream_of(x.device, stream))
+                                                  self._lora_work.numel(), _stream_of(at, stream))
         if rc:
             L.check(rc, "bs_fixed_gemm_lora_async")
         return out

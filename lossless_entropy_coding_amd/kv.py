@@ -176,15 +176,16 @@ class KvCache:
     def _tokens(self, t: torch.Tensor, heads: int | None, name: str) -> int:
         """Checks a (tokens, heads, head_dim) tensor with a token's values side
         by side; returns its token stride."""
+        shape = t.shape
+        if len(shape) != 3 or shape[2] != self.head_dim or (heads is not None and shape[1] != heads):
+            raise ValueError(f"{name} must be (tokens, {heads or 'heads'}, {self.head_dim})")
         if t.device != self.device:
             raise ValueError(f"{name} is on {t.device}, the cache on {self.device}")
-        if t.dim() != 3 or t.shape[2] != self.head_dim or (heads is not None and t.shape[1] != heads):
-            raise ValueError(f"{name} must be (tokens, {heads or 'heads'}, {self.head_dim})")
-        n, h, d = t.shape
+        n, h, d = shape
         if t.is_contiguous():
             return h * d
         s = t.stride()
-        if t.numel() and ((d > 1 and s[2] != 1) or (h > 1 and s[1] != d)):
+        if n and ((d > 1 and s[2] != 1) or (h > 1 and s[1] != d)):
             raise ValueError(f"the values of a token must be side by side in {name}")
         return h * d if n <= 1 else s[0]
 

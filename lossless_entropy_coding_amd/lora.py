@@ -48,6 +48,7 @@ class LoraPack:
         self.a = rows_of_a.view(len(adapters), self.rank // 16, 16, steps, 4, 8).permute(0, 1, 3, 4, 2, 5).contiguous()
         self.ranks = torch.tensor(ranks, dtype=torch.int32, device=device)
         self.factor = torch.tensor([float(s) for _, _, s in adapters], dtype=torch.float32, device=device)
+        self.device = self.a.device
         self.c = L.LoraPack(self.adapters, self.rank, rows, cols, self.a.data_ptr(), self.b.data_ptr(),
                             self.ranks.data_ptr(), self.factor.data_ptr())
         self.ref = C.byref(self.c)
@@ -77,19 +78,20 @@ class LoraPack:
         if out.dtype != y.dtype or out.shape != y.shape or out.stride() != y.stride():
             raise ValueError("out must have y's shape, type and strides")
         batch.check_for(self, x.shape[0])
-        _same_device(self.a.device, x=x, y=y, out=out, batch=batch.dev)
+        if x.device != self.device or y.device != self.device or out.device != self.device or batch.dev.device != self.device:
+            _same_device(self.device, x=x, y=y, out=out, batch=batch.dev)
         if x.shape[0] == 0:
             return out
         with self._lock:
             need = self.work_bytes(x.shape[0])
             if self._work is None or self._work.numel() < need:
-                self._work = _grown(self._work, need, self.a.device, stream, self._kept)
+                self._work = _grown(self._work, need, self.device, stream, self._kept)
             one = x.shape[0] == 1
             rc = L.lib().bs_lora_add_async(self.ref, batch.dev.data_ptr(), x.shape[0], x.data_ptr(),
                                            self.cols if one else x.stride(0), y.data_ptr(), out.data_ptr(),
                                            self.rows if one else y.stride(0),
                                            L.T_FP32 if y.dtype == torch.float32 else L.T_BF16, self._work.data_ptr(),
-                                           self._work.numel(), _stream_of(x.device, stream))
+                                           self._work.numel(), _stream_of(self.device, stream))
         if rc:
             L.check(rc, "bs_lora_add_async")
         return out

@@ -183,7 +183,7 @@ def test_tensors_on_another_device_are_refused(stub):
                 call(**{**args, name: _away(args[name])})
             assert len(launched) == 1, (call, name)
     far = lora.LoraPack([(_bf16(4, 2048), _bf16(32, 4), 1.0)], device="cpu")
-    far.a = _away(far.a)
+    far.a, far.device = _away(far.a), torch.device("meta")
     other = lora.LoraBatch(ids, 1)
     other.dev = _away(other.dev)
     del launched[:]
