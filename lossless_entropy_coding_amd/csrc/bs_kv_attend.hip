@@ -216,7 +216,7 @@ __device__ __forceinline__ void part_write(const KvAttend& a, uint32_t tok, uint
 
 __device__ __forceinline__ void out_write(const KvAttend& a, uint32_t tok, uint32_t qh, uint32_t ch, float top, float total, f32x4 v) {
     const uint32_t dim = a.c.dim;
-    const float inv = total > 0.f ? 1.f / total : 0.f;
+    const float inv = total == 0.f ? 0.f : 1.f / total;             // a sum of NaN is no empty row's: NaN stays
     uint16_t* op = a.out + (uint64_t)tok * a.out_stride + (uint64_t)qh * dim;
     const uint32_t lo = pack_bf16(v[0] * inv, v[1] * inv), hi = pack_bf16(v[2] * inv, v[3] * inv);
     if (a.out8 && ch + 4 <= dim) {
@@ -227,7 +227,7 @@ __device__ __forceinline__ void out_write(const KvAttend& a, uint32_t tok, uint3
         if (ch + 2 < dim) op[ch + 2] = (uint16_t)hi;
         if (ch + 3 < dim) op[ch + 3] = (uint16_t)(hi >> 16);
     }
-    if (a.lse && ch == 0) a.lse[(uint64_t)tok * a.heads + qh] = total > 0.f ? (top + __builtin_amdgcn_logf(total)) * kLn2 : -__builtin_inff();
+    if (a.lse && ch == 0) a.lse[(uint64_t)tok * a.heads + qh] = total == 0.f ? -__builtin_inff() : (top + __builtin_amdgcn_logf(total)) * kLn2;
 }
 
 // Four channels of a row from its n parts, in order, 8 loads at a time.

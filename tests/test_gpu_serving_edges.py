@@ -93,3 +93,41 @@ def test_growth_by_more_pages_than_32_bits_count():
     cache.extend(rows[:64], torch.ones(64, dtype=torch.int32, device="cuda"))
     cache.check()
     assert torch.equal(cache.table[:64, 0], rows[:64]) and bool((cache.refs == 1).all())
+
+
+@pytest.mark.parametrize("new", [1, 70])
+@pytest.mark.parametrize("dim,dtype", [(64, "e4m3"), (80, "int8"), (256, "e4m3")])
+def test_queries_that_are_not_finite(dim, dtype, new):
+    """A query with a NaN gives NaN, its logarithm too, where it sees a token,
+    and so does one with an infinity (infinity less infinity in the softmax)
+    unless a cap makes its logits finite; 0 and -infinity where it sees none.
+    The queries beside it, in its tile and its sequence, are right.  Split and
+    unsplit."""
+    print("not finite", dim, dtype, new, flush=True)
+    rng = np.random.default_rng(dim + new)
+    lens, heads = [5000, 3, 200], 4
+    cache, model = _filled(rng, lens, kv_heads=2, head_dim=dim, dtype=dtype)
+    starts = [0, new, 2 * new, 3 * new]
+    at = _ids(*starts)
+    q = _bf16(rng, 3 * new, heads, dim).cuda()
+    odd = q.clone()
+    bad = {(0, 1): "nan", (new - 1, 2): "inf", (2 * new, 0): "-inf", (3 * new - 1, 3): "nan"}
+    if new > 3:
+        bad[(new, 0)] = "nan"                        # before the row's first token
+    for (t, h), x in bad.items():
+        odd[t, h, dim - 1] = float(x)
+    for kw in ({}, dict(window=300, sinks=2), dict(softcap=10.0), dict(scale=-0.5)):
+        got, lse = cache.attend(0, odd, _ids(0, 1, 2), at, max_new=new, lse=True, **kw)
+        cache.check()
+        hit = torch.zeros(3 * new, heads, dtype=torch.bool, device="cuda")
+        nans = hit.clone()
+        for (t, h), x in bad.items():
+            hit[t, h] = True
+            nans[t, h] = x == "nan" or "softcap" not in kw
+        out, ref, slack, spread = model.attend(0, _f64(q), [0, 1, 2], starts, **kw)
+        blind = torch.from_numpy(np.isneginf(ref)).cuda()
+        assert bool(blind[new, 0]) == (new > 3) and torch.equal(torch.isneginf(lse), blind) and not got[blind].any()
+        assert torch.isnan(got[nans & ~blind]).all() and torch.isnan(lse[nans & ~blind]).all()
+        rest = (~hit & ~blind).cpu().numpy()
+        assert np.all((np.abs(_f64(got) - out) <= S.attend_bound(out, slack, spread))[rest])
+        assert np.all((np.abs(_f64(lse) - np.where(rest, ref, 0)) <= slack + 2.0 ** -20 * (1 + np.abs(ref)))[rest])
