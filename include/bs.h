@@ -744,10 +744,12 @@ typedef struct {
 
 /* Attention of new tokens over the cache, their own keys and values included:
  * query j of n new ones of a row of length L stands at place L - n + j and
- * sees the tokens up to it.  A query that sees nothing gives 0 and a
- * logarithm of -infinity; one whose logits are not numbers gives NaN twice.  Scores and sums are held in fp32; probabilities
- * enter the second product in BF16, the type of the result.  What slots past
- * a row's length hold does not matter.  The same result on every run.
+ * sees the tokens up to it, except those whose entry of the table names no page
+ * (BS_KV_BAD_ID).  A query that sees nothing gives 0 and a logarithm of
+ * -infinity; one whose logits are not numbers gives NaN twice.  Scores and
+ * sums are held in fp32; probabilities enter the second product in BF16, the
+ * type of the result.  What slots past a row's length hold does not matter.
+ * The same result on every run.
  * d_work (16-B aligned): bs_kv_attend_work_bytes, which gives 0 where rows
  * need not be split; without it (NULL) they are not.  Its first 4096 bytes
  * are zero before the first call that is given it, and every call leaves

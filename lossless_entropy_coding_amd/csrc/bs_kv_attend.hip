@@ -561,7 +561,12 @@ __global__ __launch_bounds__(512, 2) void attend_rows_kernel(KvAttend a, uint32_
 #pragma unroll
         for (int d = 0; d < 4 * DW; d++) o[n][d] = f32x4{0.f, 0.f, 0.f, 0.f};
         mx[n] = -__builtin_inff();
-        sum[n] = 0.f;
+        // 0, or NaN for a query that holds a NaN or an infinity (0 times it) and sees a token
+        f32x4 z = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (uint32_t x = 0; x < 2 * DW; x++)
+            z = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, v4u{0u, 0u, 0u, 0u}), q[n][x >> 1][x & 1], z, 0, 0, 0);
+        sum[n] = pos[n] >= 0 ? z[0] : 0.f;
     }
     const int32_t* trow = c.table + (uint64_t)(uint32_t)max(sq.row, 0) * c.max_pages;
     const uint64_t hoff = (uint64_t)head * c.page * c.wide;
@@ -607,7 +612,8 @@ __global__ __launch_bounds__(512, 2) void attend_rows_kernel(KvAttend a, uint32_
             for (uint32_t d = 0; d < DW; d++) x.r[d] = *(const v4u*)(kp + 64 * d);
         }
     };
-    // operand 2 (part DW + d) of its side, and the next one
+    // operand 2 (part DW + d) of its side, and the next one.  Keys that have no
+    // page become NaN, and with them their logits: the softmax leaves these out.
     auto stage_store = [&](uint32_t i, Next& x, uint32_t d) {
         if (i >= i1) return;
         if (x.keep < 16) {
@@ -615,10 +621,11 @@ __global__ __launch_bounds__(512, 2) void attend_rows_kernel(KvAttend a, uint32_
             for (int w = 0; w < 4; w++) {
                 const int32_t nb = (int32_t)x.keep - 4 * w;
                 x.r[d][w] &= nb >= 4 ? ~0u : nb <= 0 ? 0u : (1u << (8 * nb)) - 1u;
+                if (E4M3 && !vside) x.r[d][w] = 0x7F7F7F7Fu;         // the code of NaN
             }
         }
         uint8_t* to = buf[(i - i0) & 1u][(vside ? kFrags : 0) + 2 * (part * DW + d)] + 16 * lane;
-        const float f = x.keep ? x.scale : 1.f;
+        const float f = x.keep ? x.scale : E4M3 || vside ? 1.f : __builtin_nanf("");
         *(bf16x8*)to = widen8<E4M3>(x.r[d].x, x.r[d].y, f);
         *(bf16x8*)(to + 1024) = widen8<E4M3>(x.r[d].z, x.r[d].w, f);
     };
@@ -756,6 +763,9 @@ __global__ __launch_bounds__(512, 2) void attend_rows_kernel(KvAttend a, uint32_
                     tot += x[e];
                 }
                 if (__builtin_amdgcn_ballot_w64(!(tot <= kGrow)) != 0) {
+                    // NaN: a token without a page (a query's own NaN is in its sum already)
+#pragma unroll
+                    for (uint32_t e = 0; e < 16; e++) p[e] = fmaxf(p[e], -__builtin_inff());
                     float top = p[0];
 #pragma unroll
                     for (uint32_t e = 1; e < 16; e++) top = fmaxf(top, p[e]);

@@ -172,10 +172,11 @@ class Cache:
             out.append(values(np.ascontiguousarray(c), self.kind) * float(self.scale[layer, p, head, side]))
         return np.concatenate(out)[:n, :self.dim] if out else np.zeros((0, self.dim))
 
-    def attend(self, layer, q, rows, starts=None, scale=0.0, window=0, sinks=0, softcap=0.0):
+    def attend(self, layer, q, rows, starts=None, scale=0.0, window=0, sinks=0, softcap=0.0, gone=()):
         """(out, lse, slack, spread): for each query the result, the logarithm
         of the softmax sum, the most that fp32 sums can move a logit, and the
-        probability-weighted magnitude of the values."""
+        probability-weighted magnitude of the values.  gone: (row, column)
+        entries of the table whose tokens are left out."""
         starts = list(range(len(rows) + 1)) if starts is None else starts
         scale = scale or 1.0 / math.sqrt(self.dim)
         out, spread = np.zeros(q.shape), np.zeros(q.shape)
@@ -188,7 +189,7 @@ class Cache:
                 for j in range(count):
                     at = n - count + j
                     t = np.arange(n)
-                    seen = t <= at
+                    seen = (t <= at) & ~np.isin(t // self.page, [c for x, c in gone if x == r])
                     if window:
                         seen &= (t > at - window) | (t < sinks)
                     if not seen.any():

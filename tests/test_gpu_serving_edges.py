@@ -131,3 +131,31 @@ def test_queries_that_are_not_finite(dim, dtype, new):
         rest = (~hit & ~blind).cpu().numpy()
         assert np.all((np.abs(_f64(got) - out) <= S.attend_bound(out, slack, spread))[rest])
         assert np.all((np.abs(_f64(lse) - np.where(rest, ref, 0)) <= slack + 2.0 ** -20 * (1 + np.abs(ref)))[rest])
+
+
+@pytest.mark.parametrize("new", [1, 70])
+@pytest.mark.parametrize("dim,page,dtype", [(64, 64, "int8"), (128, 16, "e4m3"), (256, 32, "int8")])
+def test_tokens_without_a_page_are_left_out(dim, page, dtype, new):
+    """Few and many rows: entries past the pool, in the middle, at the first and the last page, and a whole row of them."""
+    print("no page", dim, page, dtype, new, flush=True)
+    rng = np.random.default_rng(dim + new)
+    lens, heads = [700, 90, 150], 4
+    cache, model = _filled(rng, lens, kv_heads=2, head_dim=dim, page_tokens=page, dtype=dtype)
+    last = (lens[0] - 1) // page
+    gone = {(0, 0): -1, (0, 2): 1 << 30, (0, 3): cache.n_pages, (0, last): -(1 << 31)}
+    gone.update({(1, c): -7 for c in range(-(-lens[1] // page))})
+    for (r, c), e in gone.items():
+        cache.table[r, c] = e
+    at = [0, new, 2 * new, 3 * new]
+    q = _bf16(rng, 3 * new, heads, dim)
+    for kw in ({}, dict(window=200, sinks=page), dict(softcap=20.0)):
+        got, lse = cache.attend(0, q.cuda(), _ids(0, 1, 2), _ids(*at), max_new=new, lse=True, **kw)
+        torch.cuda.synchronize()
+        assert int(cache.status.item()) == 4
+        cache.status.zero_()
+        out, ref, slack, spread = model.attend(0, _f64(q), [0, 1, 2], at, gone=list(gone), **kw)
+        g, l = _f64(got), _f64(lse)
+        empty = np.isneginf(ref)
+        assert empty[new:2 * new].all() and np.array_equal(empty, np.isneginf(l)) and np.all(g[empty] == 0)
+        assert np.all(np.abs(g - out) <= S.attend_bound(out, slack, spread)), float(np.abs(g - out).max())
+        assert np.all(np.abs(l[~empty] - ref[~empty]) <= slack[~empty] + 2.0 ** -20 * (1 + np.abs(ref[~empty])))
