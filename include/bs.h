@@ -737,7 +737,7 @@ typedef struct {
     float* d_lse;               /* NULL, or [total_q][heads]: the natural logarithm of the softmax sum */
     uint64_t q_stride, out_stride;
     float scale;                /* of q k (0: 1 / sqrt(head_dim)) */
-    float softcap;              /* 0: none; else logits become softcap tanh(logit / softcap) */
+    float softcap;              /* 0 or infinity: none; else logits become softcap tanh(logit / softcap) */
     uint32_t window;            /* 0: all tokens up to the query's own; else the last `window` of them, */
     uint32_t sinks;             /* and the first `sinks` tokens of the row */
 } bs_kv_attend_args;

@@ -144,7 +144,9 @@ bs_status attend_args(const bs_kv_cache* cache, const bs_kv_attend_args* x, bsd:
     a.q_stride = x->q_stride;
     a.out_stride = x->out_stride;
     a.qscale = x->scale > 0.f || x->scale < 0.f ? x->scale : 1.f / __builtin_sqrtf((float)a.c.dim);
-    a.softcap = x->softcap;
+    // above 2^100 (infinity, too) c tanh(x / c) is x to fp32's precision, and
+    // below 2^-100 every capped logit is 0 to it: neither overflows a constant
+    a.softcap = x->softcap > 0x1p100f ? 0.f : x->softcap > 0.f ? std::max(x->softcap, 0x1p-100f) : 0.f;
     a.window = x->window;
     a.sinks = x->sinks;
     a.aligned = aligned(x->d_q, 16) && x->q_stride % 8 == 0 && a.c.dim % 8 == 0;

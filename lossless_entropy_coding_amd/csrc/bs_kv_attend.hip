@@ -61,6 +61,25 @@ constexpr float kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
+// Soft cap: top tanh(y), y = t ln2 / 2, top the cap in powers of 2.  The
+// kernels' own form, top - 2 top / (2^t + 1), is right to 2^-22 of the cap,
+// whatever the logit: up to a cap of 256 that is 2^-14, far below the BF16
+// rounding of a probability.  Above (CAP), the series to y^7 takes over below
+// 1/4 (the next term is 2^-21.5 of it there), so that the error is 2^-20 of
+// the logit.  Where rows are many it costs a third more (2 prompts of 2048
+// tokens over 8000, 40 heads on 8 of 128 channels, e4m3: 827 us with a cap of
+// 256 or less, 1112 above; 4 x 131071 tokens of int8: 208 either way), and in
+// one kernel with the other form it would slow that down, too (827 us to
+// 875): hence kernels of their own.
+constexpr float kShortCap = 256.f;
+
+__device__ __forceinline__ float capped(float t, float top) {
+    const float e = top - 2.f * top * __builtin_amdgcn_rcpf(exp2_fast(t) + 1.f);
+    const float y = t * (0.5f * kLn2), y2 = y * y;
+    const float p = top * y * (1.f + y2 * (-1.f / 3 + y2 * (2.f / 15 + y2 * (-17.f / 315))));
+    return fabsf(y) < 0.25f ? p : e;
+}
+
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
     const bf16x2 r = {(__bf16)a, (__bf16)b};
     return __builtin_bit_cast(uint32_t, r);
@@ -271,7 +290,7 @@ __device__ __forceinline__ void join_row(const KvAttend& a, uint32_t tok, uint32
 // products' accumulators out of the AGPRs: with them there, the compiler here
 // reads a product's later elements at a block's join without the wait that
 // it puts before the first, and they come back stale.
-template <int DW, bool E4M3, int NW>
+template <int DW, bool E4M3, int NW, bool CAP>
 __global__ __launch_bounds__(64 * NW, 2) void attend_kernel(KvAttend a, uint32_t row_tiles) {
     const KvView& c = a.c;
     constexpr uint32_t D = 64 * DW;
@@ -377,7 +396,8 @@ __global__ __launch_bounds__(64 * NW, 2) void attend_kernel(KvAttend a, uint32_t
 #pragma unroll
             for (uint32_t e = 0; e < 4; e++) {
                 float x = s[h][e] * ks;
-                if (a.softcap > 0.f) x = cap_out * (1.f - 2.f * __builtin_amdgcn_rcpf(exp2_fast(x * cap_in) + 1.f));
+                if (CAP) x = capped(x * cap_in, cap_out);
+                else if (a.softcap > 0.f) x = cap_out * (1.f - 2.f * __builtin_amdgcn_rcpf(exp2_fast(x * cap_in) + 1.f));
                 const int32_t tk = (int32_t)(cv + 4 * h + e);
                 const bool seen = okv && tk <= pos &&
                                   (a.window == 0 || (int64_t)tk > (int64_t)pos - (int64_t)a.window || (uint32_t)tk < a.sinks);
@@ -501,7 +521,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attend_kernel(KvAttend a, uint32_t
 // 2 to 15% slower.
 constexpr float kGrow = 1024.f;
 
-template <int DW, bool E4M3, int NR>
+template <int DW, bool E4M3, int NR, bool CAP>
 __global__ __launch_bounds__(512, 2) void attend_rows_kernel(KvAttend a, uint32_t row_blocks, uint32_t combos) {
     const KvView& c = a.c;
     constexpr uint32_t D = 64 * DW, kFrags = 8 * DW;                // 1-KiB operands of a side of a tile
@@ -739,7 +759,10 @@ __global__ __launch_bounds__(512, 2) void attend_rows_kernel(KvAttend a, uint32_
                 float p[16];
 #pragma unroll
                 for (uint32_t e = 0; e < 16; e++) p[e] = s[n][e >> 2][e & 3];
-                if (a.softcap > 0.f) {
+                if (CAP) {
+#pragma unroll
+                    for (uint32_t e = 0; e < 16; e++) p[e] = capped(p[e] * cap_in, cap_out);
+                } else if (a.softcap > 0.f) {
 #pragma unroll
                     for (uint32_t e = 0; e < 16; e++)
                         p[e] = cap_out - 2.f * cap_out * __builtin_amdgcn_rcpf(exp2_fast(p[e] * cap_in) + 1.f);
@@ -829,24 +852,29 @@ __global__ __launch_bounds__(64) void join_kernel(KvAttend a, uint32_t block_row
 template <int DW>
 constexpr int kRowTiles = DW <= 2 ? 2 : 1;
 
-template <int DW>
+template <int DW, bool E4M3, bool CAP>
 int launch(const KvAttend& a, hipStream_t st) {
     if (a.many) {
         constexpr int NR = kRowTiles<DW>;
         const uint32_t row_blocks = (uint32_t)(((uint64_t)a.max_new * a.group + 128 * NR - 1) / (128 * NR));
         const uint32_t combos = a.n_seqs * a.c.kv_heads;
         const dim3 grid((combos + 7) / 8 * 8 * row_blocks, a.splits);
-        if (a.c.type == 1) hipLaunchKernelGGL((attend_rows_kernel<DW, true, NR>), grid, dim3(512), 0, st, a, row_blocks, combos);
-        else hipLaunchKernelGGL((attend_rows_kernel<DW, false, NR>), grid, dim3(512), 0, st, a, row_blocks, combos);
+        hipLaunchKernelGGL((attend_rows_kernel<DW, E4M3, NR, CAP>), grid, dim3(512), 0, st, a, row_blocks, combos);
         constexpr uint32_t heads = 64 / (16 * DW) > 0 ? 64 / (16 * DW) : 1;
         if (a.splits > 1) hipLaunchKernelGGL(join_kernel<DW>, dim3(a.n_seqs * a.max_new, (a.heads + heads - 1) / heads), dim3(64), 0, st, a, 128u * NR);
         return (int)hipGetLastError();
     }
     const uint32_t row_tiles = (a.max_new * a.group + 15) / 16;
     const dim3 grid(a.n_seqs * row_tiles, a.c.kv_heads, a.splits);
-    if (a.c.type == 1) hipLaunchKernelGGL((attend_kernel<DW, true, 4>), grid, dim3(256), 0, st, a, row_tiles);
-    else hipLaunchKernelGGL((attend_kernel<DW, false, 4>), grid, dim3(256), 0, st, a, row_tiles);
+    hipLaunchKernelGGL((attend_kernel<DW, E4M3, 4, CAP>), grid, dim3(256), 0, st, a, row_tiles);
     return (int)hipGetLastError();
+}
+
+template <int DW>
+int launch(const KvAttend& a, hipStream_t st) {
+    const bool cap = a.softcap > kShortCap;
+    if (a.c.type == 1) return cap ? launch<DW, true, true>(a, st) : launch<DW, true, false>(a, st);
+    return cap ? launch<DW, false, true>(a, st) : launch<DW, false, false>(a, st);
 }
 
 }  // namespace

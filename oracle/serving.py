@@ -200,7 +200,8 @@ class Cache:
                         loose = np.abs(k[seen]) @ np.abs(x) * abs(scale) * (self.dim + 8) * 2.0 ** -24 + np.abs(logit) * 2.0 ** -21
                         if softcap:
                             logit = softcap * np.tanh(logit / softcap)
-                            loose = loose + softcap * 2.0 ** -20
+                            # an error in proportion to the cap where that is small, else to the capped logit
+                            loose = loose + (softcap * 2.0 ** -20 if softcap <= 256 else np.abs(logit) * 2.0 ** -19)
                         top = logit.max()
                         p = np.exp(logit - top)
                         total = p.sum()

@@ -159,3 +159,24 @@ def test_tokens_without_a_page_are_left_out(dim, page, dtype, new):
         assert empty[new:2 * new].all() and np.array_equal(empty, np.isneginf(l)) and np.all(g[empty] == 0)
         assert np.all(np.abs(g - out) <= S.attend_bound(out, slack, spread)), float(np.abs(g - out).max())
         assert np.all(np.abs(l[~empty] - ref[~empty]) <= slack[~empty] + 2.0 ** -20 * (1 + np.abs(ref[~empty])))
+
+
+@pytest.mark.parametrize("new,dim,dtype", [(1, 64, "int8"), (70, 128, "e4m3"), (9, 256, "e4m3"), (80, 80, "int8")])
+def test_soft_caps_of_any_size(new, dim, dtype):
+    """Logits of up to hundreds under caps from far below to far above them: the
+    error is a share of the capped logit (of the cap up to 256), so that a cap
+    far above the logits leaves them as they are."""
+    print("caps", new, dim, dtype, flush=True)
+    rng = np.random.default_rng(dim + new)
+    lens = [400, 90]
+    cache, model = _filled(rng, lens, kv_heads=1, head_dim=dim, dtype=dtype)
+    q = _bf16(rng, 2 * new, 2, dim, size=20.0)
+    at = [0, new, 2 * new]
+    for cap in (1e-42, 1e-35, 1e-3, 30.0, 256.0, 257.0, 1e3, 1e4, 1e6, 1e20, 3e38, float("inf")):
+        for scale in (0.0, -0.3, 1e-3):
+            got, lse = cache.attend(0, q.cuda(), _ids(0, 1), _ids(*at), max_new=new, softcap=cap, scale=scale, lse=True)
+            cache.check()
+            out, ref, slack, spread = model.attend(0, _f64(q), [0, 1], at, scale=scale,
+                                                   softcap=0.0 if cap == float("inf") else float(np.float32(cap)))
+            assert np.all(np.abs(_f64(got) - out) <= S.attend_bound(out, slack, spread)), (cap, scale)
+            assert np.all(np.abs(_f64(lse) - ref) <= slack + 2.0 ** -20 * (1 + np.abs(ref))), (cap, scale)
