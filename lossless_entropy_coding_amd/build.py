@@ -7,6 +7,7 @@ from __future__ import annotations
 import argparse
 import concurrent.futures
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -27,6 +28,25 @@ HIP_FLAGS = ["-O3", "-fPIC", "-std=c++17", f"--offload-arch={ARCH}", "-Wall",
              "-I", CSRC, "-I", INCLUDE]
 
 
+# the compiler's report of each kernel's registers
+REPORT = "-Rpass-analysis=kernel-resource-usage"
+
+
+def check_registers(src: str, report: str, kernels: bool = True) -> None:
+    """Raise if a kernel of `src` has accumulation registers (AGPRs).  A matrix
+    product's result that is kept in them and read where two blocks join comes
+    back stale from this compiler in its later elements, so every kernel's
+    launch bounds keep it to 256 registers, where results stay in VGPRs.  Nothing
+    else would show that another compiler or a larger kernel has undone it."""
+    names = re.findall(r"Function Name: (\S+)", report)
+    agprs = [int(n) for n in re.findall(r"\bAGPRs: (\d+)", report)]
+    if len(names) != len(agprs) or (kernels and not names):
+        raise RuntimeError(f"{src}: the compiler reported {len(agprs)} AGPR counts for {len(names)} kernels")
+    used = [f"{k} ({n})" for k, n in zip(names, agprs) if n]
+    if used:
+        raise RuntimeError(f"{src}: kernels with accumulation registers, in which results can come back stale: {', '.join(used)}")
+
+
 def hipcc() -> str:
     for cand in (shutil.which("hipcc"), "/opt/rocm/bin/hipcc"):
         if cand and os.path.exists(cand):
@@ -45,12 +65,17 @@ def build_lib(asm_dir: str | None = None, verbose: bool = False) -> str:
                 cmd += ["-save-temps=obj"]
                 cmd[cmd.index("-o") + 1] = os.path.join(asm_dir, src + ".o")
                 obj = os.path.join(asm_dir, src + ".o")
+            if src.endswith(".hip"):
+                cmd.append(REPORT)
             if verbose:
                 print(" ".join(cmd), flush=True)
             r = subprocess.run(cmd, capture_output=True, text=True)
             if r.returncode != 0:
                 sys.stderr.write(r.stdout + r.stderr)
                 raise RuntimeError(f"compiling {src} failed")
+            if src.endswith(".hip"):
+                with open(os.path.join(CSRC, src)) as f:
+                    check_registers(src, r.stderr, "__global__" in f.read())
             return obj
 
         with concurrent.futures.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 1)) as pool:
