@@ -28,6 +28,7 @@ from . import _lib as L
 from .codec import _capturing, _grown, _on, _same_device, _stream_of
 
 _INT32, _BF16, _FP32 = torch.int32, torch.bfloat16, torch.float32
+_MAX = (1 << 32) - 1             # of the library's 32-bit numbers, which take a larger one's low bits
 
 
 def _wide(head_dim: int) -> int:
@@ -210,7 +211,7 @@ class KvCache:
             raise ValueError("k and v must have one shape and be bfloat16 or float32")
         ks, vs, total = self._tokens(k, self.kv_heads, "k"), self._tokens(v, self.kv_heads, "v"), k.shape[0]
         n, most, at = self._rows(rows, starts, total, max_new)
-        rc = L.lib().bs_kv_append_async(self._ref, layer, n, rows.data_ptr(), at, total, most, k.data_ptr(), ks,
+        rc = L.lib().bs_kv_append_async(self._ref, layer if 0 <= layer < _MAX else _MAX, n, rows.data_ptr(), at, total, most, k.data_ptr(), ks,
                                         v.data_ptr(), vs, L.T_FP32 if kind is _FP32 else L.T_BF16,
                                         _stream_of(self.device, stream))
         if rc:
@@ -247,10 +248,12 @@ class KvCache:
             raise ValueError(f"lse must be a contiguous float32 tensor of (tokens, heads) on {self.device}")
         if window < 0 or sinks < 0 or max_len < 0:
             raise ValueError("window, sinks and max_len are not negative")
+        window, sinks, max_len = min(window, _MAX), min(sinks, _MAX), min(max_len, _MAX)   # rows are shorter
         n, most, at = self._rows(rows, starts, total, max_new)
         with self._lock:
             a = self._args
-            a.layer, a.n_seqs, a.heads, a.total_q, a.max_new, a.max_len = layer, n, heads, total, most, max_len
+            a.layer, a.n_seqs, a.heads = layer if 0 <= layer < _MAX else _MAX, n, heads
+            a.total_q, a.max_new, a.max_len = total, most, max_len
             a.d_seqs, a.d_starts, a.d_q, a.d_out = rows.data_ptr(), at, q.data_ptr(), out.data_ptr()
             a.d_lse = None if lse is False else lse.data_ptr()
             a.q_stride, a.out_stride, a.scale, a.softcap, a.window, a.sinks = qs, os, scale, softcap, window, sinks

@@ -180,3 +180,17 @@ def test_soft_caps_of_any_size(new, dim, dtype):
                                                    softcap=0.0 if cap == float("inf") else float(np.float32(cap)))
             assert np.all(np.abs(_f64(got) - out) <= S.attend_bound(out, slack, spread)), (cap, scale)
             assert np.all(np.abs(_f64(lse) - ref) <= slack + 2.0 ** -20 * (1 + np.abs(ref))), (cap, scale)
+
+
+@pytest.mark.parametrize("new", [1, 70])
+def test_windows_and_sinks_past_every_row(new):
+    rng = np.random.default_rng(new)
+    cache, _ = _filled(rng, [500, 80], kv_heads=1, head_dim=64)
+    q, at = _bf16(rng, 2 * new, 4, 64).cuda(), _ids(0, new, 2 * new)
+    want = cache.attend(0, q, _ids(0, 1), at, max_new=new)
+    for kw in (dict(window=1 << 32), dict(window=(1 << 31) - 1, sinks=1 << 40), dict(window=1, sinks=(1 << 32) - 1),
+               dict(window=(1 << 32) + 1, max_len=1 << 32)):
+        got = cache.attend(0, q, _ids(0, 1), at, max_new=new, **kw)
+        cache.check()
+        # the tiles may be dealt to workgroups in another way, so sums may round otherwise
+        assert float((got.float() - want.float()).abs().max()) <= 2.0 ** -7 * float(want.float().abs().max()), kw

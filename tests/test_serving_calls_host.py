@@ -220,3 +220,26 @@ def test_a_refused_attention_leaves_later_ones_their_workspace(stub):
     cache.attend(1, q, ids)
     cache.attend(0, q, ids)
     assert len(given) == 2 and given[0] == given[1] > 4096
+
+
+def test_numbers_past_32_bits_keep_their_meaning(stub):
+    """A window of 2^32 tokens is all of them, not none of its high bits; a layer of 2^32 is no layer."""
+    given, real = [], L.lib()
+
+    def seen(name, args):
+        if (args[1] if name == "bs_kv_append_async" else args[1]._obj.layer) >= 2:
+            return getattr(real, name)(*args)            # refused
+        given.append(args)
+    stub(seen)
+    cache = kv.KvCache(2, 1, 64, 16, 8, 4, device="cpu")
+    q, ids = _bf16(2, 4, 64), torch.zeros(2, dtype=torch.int32)
+    for big in (1 << 32, (1 << 32) + 5, 1 << 70):
+        cache.attend(0, q, ids, window=big, sinks=big, max_len=big)
+        a = given.pop()[1]._obj
+        assert a.window == a.sinks == a.max_len == (1 << 32) - 1
+        for layer in (big, -big, -1, 2):
+            with pytest.raises(L.BSError, match="layer"):
+                cache.attend(layer, q, ids)
+            with pytest.raises(L.BSError, match="layer"):
+                cache.append(layer, _bf16(2, 1, 64), _bf16(2, 1, 64), ids)
+    assert not given
