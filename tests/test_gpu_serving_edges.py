@@ -194,3 +194,109 @@ def test_windows_and_sinks_past_every_row(new):
         cache.check()
         # the tiles may be dealt to workgroups in another way, so sums may round otherwise
         assert float((got.float() - want.float()).abs().max()) <= 2.0 ** -7 * float(want.float().abs().max()), kw
+
+
+@pytest.mark.parametrize("dtype", ["e4m3", "int8"])
+@pytest.mark.parametrize("dim", [64, 65, 128, 129, 192, 200, 256])
+def test_many_rows_split_and_joined(dim, dtype):
+    """Prompts long enough for several splits, at head sizes of every width of the join."""
+    print("split prompts", dim, dtype, flush=True)
+    rng = np.random.default_rng(dim)
+    lens, new, heads = [3000, 700], [70, 90], 3
+    cache, model = _filled(rng, lens, kv_heads=1, head_dim=dim, dtype=dtype)
+    at = [0, 70, 160]
+    q = _bf16(rng, 160, heads, dim)
+    for kw in ({}, dict(window=1500, sinks=3), dict(softcap=30.0)):
+        cache._attend_work = None
+        got, lse = cache.attend(0, q.cuda(), _ids(0, 1), _ids(*at), max_new=90, lse=True, **kw)
+        cache.check()
+        assert cache._attend_work.numel() >= 4 * 160 * heads * 2 * (-(-dim // 64) * 64 + 4), "not split"
+        out, ref, slack, spread = model.attend(0, _f64(q), [0, 1], at, **kw)
+        assert np.all(np.abs(_f64(got) - out) <= S.attend_bound(out, slack, spread)), float(np.abs(_f64(got) - out).max())
+        assert np.all(np.abs(_f64(lse) - ref) <= slack + 2.0 ** -20 * (1 + np.abs(ref)))
+
+
+def _bits(cache):
+    torch.cuda.synchronize()
+    return {n: getattr(cache, n).clone().view(torch.uint8).cpu() for n in ("k", "v", "scale", "refs", "table", "lens")}
+
+
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("dim,page", [(64, 16), (80, 32), (256, 128)])
+def test_refused_appends_write_nothing(dim, page, f32):
+    """Token ranges, rows and table entries that do not exist: no byte of the
+    cache changes but those of the good rows' own pages, which get the data
+    that they hold already."""
+    rng = np.random.default_rng(dim)
+    kw = dict(layers=2, kv_heads=2, head_dim=dim, n_pages=12, max_seqs=3, max_pages=6, page_tokens=page, dtype="e4m3")
+    cache = kv.KvCache(**kw)
+    for n in ("k", "v"):
+        t = getattr(cache, n)
+        t.copy_(torch.from_numpy(rng.integers(0, 256, tuple(t.shape)).astype(np.uint8)))
+    cache.scale.fill_(float("nan"))
+    cache.extend(_ids(1, 2), _ids(20, 10))
+    x = _bf16(rng, 40, 2, dim).cuda()
+    x = x.float() * 1.001 if f32 else x
+    cache.append(1, x[:30], x[:30], _ids(1, 2), _ids(0, 20, 30))
+    cache.check()
+    before = _bits(cache)
+    for rows, starts in (((1, 0), (0, 21, 30)), ((1, 0), (0, 20, 31)), ((1, 0), (5, 0, 30)), ((1, 0), (-1, 19, 29)),
+                         ((3, -1), (0, 1, 2)), ((1 << 30, 0), (0, 1, 1)), ((1, 2), (0, 20, 31)), ((1, 2), (0, 20, 41))):
+        cache.append(1, x, x, _ids(*rows), _ids(*starts))
+        with pytest.raises(RuntimeError, match="does not exist"):
+            cache.check()
+        after = _bits(cache)
+        assert all(torch.equal(before[n], after[n]) for n in before), (rows, starts)
+    for entry in (-5, -1, 12, 1 << 30, -(1 << 31)):
+        own = cache.table[1].clone()
+        last = (20 - 1) // page
+        cache.table[1, last] = entry
+        before = _bits(cache)
+        cache.append(1, x[19:31], x[19:31], _ids(1, 2), _ids(0, 1, 11))      # the good row's own data again
+        if entry == 12:
+            cache.append(0, x[:20], x[:20], _ids(1), _ids(0, 20), max_new=20)
+        with pytest.raises(RuntimeError, match="does not exist"):
+            cache.check()
+        good = set() if entry != 12 else {(0, int(p)) for p in own[:last]}   # whole pages before the bad one
+        after = _bits(cache)
+        for n in ("k", "v", "scale"):
+            same = (before[n] == after[n]).flatten(2).all(dim=2)
+            for layer, p in good:
+                same[layer, p] = True
+            assert bool(same.all()), (entry, n)
+        assert all(torch.equal(before[n], after[n]) for n in ("refs", "table", "lens"))
+        cache.table[1].copy_(own)
+
+
+def test_two_threads_over_one_cache():
+    """Attention, adapters and pages from threads that share a cache, a pack and a stream."""
+    import threading
+    from lossless_entropy_coding_amd import lora
+    rng = np.random.default_rng(51)
+    cache, _ = _filled(rng, [3000, 500, 90, 40], kv_heads=1, head_dim=64)
+    pack = lora.LoraPack([(_bf16(rng, 16, 96), _bf16(rng, 40, 16), 0.5)])
+    work = []
+    for i in range(4):
+        n = 1 + i
+        q, rows = _bf16(rng, 64 * n, 8, 64).cuda(), _ids(*range(n))
+        at = _ids(*range(0, 64 * n + 1, 64))
+        x, batch = _bf16(rng, 30 + i, 96).cuda(), lora.LoraBatch(torch.zeros(30 + i, dtype=torch.int32, device="cuda"), 1)
+        y = torch.zeros(30 + i, 40, device="cuda")
+        call = lambda q=q, rows=rows, at=at, x=x, batch=batch, y=y: (   # noqa: E731
+            cache.attend(0, q, rows, at, max_new=64), pack.add(y, x, batch, out=torch.empty_like(y)))
+        work.append((call, call()))
+    torch.cuda.synchronize()
+    wrong = []
+
+    def go(call, want):
+        for _ in range(50):
+            got = call()
+            if not all(torch.equal(a, b) for a, b in zip(got, want)):
+                wrong.append(1)
+    threads = [threading.Thread(target=go, args=w) for w in work]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
+    cache.check()
