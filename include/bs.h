@@ -747,7 +747,8 @@ typedef struct {
  * sees the tokens up to it, except those whose entry of the table names no page
  * (BS_KV_BAD_ID).  A query that sees nothing gives 0 and a logarithm of
  * -infinity; one whose logits are not numbers gives NaN twice.  Scores and
- * sums are held in fp32; probabilities enter the second product in BF16, the
+ * sums are held in fp32; probabilities enter the second product in 16
+ * significant bits, or, from max_new x heads / kv_heads = 64 on, in BF16, the
  * type of the result.  What slots past a row's length hold does not matter.
  * The same result on every run.
  * d_work (16-B aligned): bs_kv_attend_work_bytes, which gives 0 where rows

@@ -10,11 +10,21 @@
 //                   products are exact and summed in fp32; the page's scale
 //                   multiplies the sum.
 //   O^T += V^T P^T  A = 16 channels x 32 tokens, B = 32 tokens x 16 rows.
-//                   P (times the scale of V's page, a power of two) is
-//                   rounded to BF16, the type of the result: the rounding
-//                   errors of the tokens are independent, so the sum's is
-//                   below the result's own.  The sum of P is kept in fp32
-//                   from the unrounded values.
+//                   P (times the scale of V's page, a power of two) enters
+//                   as two BF16 numbers, 16 significant bits, where rows are
+//                   few: the products are exact and the result is the fp32
+//                   form's to its own rounding (1e-4 of it apart on 4 x 131071
+//                   tokens and on 64 windows, where one BF16 number gave 1e-3
+//                   to 2e-3), for 0.3 to 1% of the time where HBM bounds it,
+//                   0.3 us of a lone short row's 10.5.  Where rows are many
+//                   the matrix products would take half as long again and
+//                   the registers do not hold the second part: P is rounded
+//                   to BF16, the type of the result.  The tokens' rounding
+//                   errors are independent, and their sum is about as large
+//                   as the result's own rounding (two prompts of 2048 tokens
+//                   over 8000: 2.3e-3 from the 64-bit result, the fp32 form
+//                   1.6e-3).  The sum of P is kept in fp32 from the unrounded
+//                   values.
 //
 // The tokens of a 64-token tile are dealt to the four 16-token steps of S^T
 // such that lane group g (lanes 16 g ..) ends up with tokens 16 g .. 16 g +
@@ -433,15 +443,27 @@ __global__ __launch_bounds__(64 * NW, 2) void attend_kernel(KvAttend a, uint32_t
             part += p[e];
         }
         sum += part;
-        bf16x8 pb[2];
+        // P in two BF16 parts
+        bf16x8 pb[2], pl[2];
 #pragma unroll
-        for (int y = 0; y < 2; y++)
-            pb[y] = __builtin_bit_cast(bf16x8, v4u{pack_bf16(p[8 * y] * vs, p[8 * y + 1] * vs), pack_bf16(p[8 * y + 2] * vs, p[8 * y + 3] * vs),
-                                                   pack_bf16(p[8 * y + 4] * vs, p[8 * y + 5] * vs), pack_bf16(p[8 * y + 6] * vs, p[8 * y + 7] * vs)});
+        for (int y = 0; y < 2; y++) {
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int e = 0; e < 4; e++) {
+                const float u = p[8 * y + 2 * e] * vs, v = p[8 * y + 2 * e + 1] * vs;
+                hi[e] = pack_bf16(u, v);
+                lo[e] = pack_bf16(u - __builtin_bit_cast(float, hi[e] << 16), v - __builtin_bit_cast(float, hi[e] & 0xFFFF0000u));
+            }
+            pb[y] = __builtin_bit_cast(bf16x8, v4u{hi[0], hi[1], hi[2], hi[3]});
+            pl[y] = __builtin_bit_cast(bf16x8, v4u{lo[0], lo[1], lo[2], lo[3]});
+        }
 #pragma unroll
         for (int d = 0; d < 4 * DW; d++) {
-            o[d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen8<E4M3>(vr[d].x, vr[d].y), pb[0], o[d], 0, 0, 0);
-            o[d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen8<E4M3>(vr[d].z, vr[d].w), pb[1], o[d], 0, 0, 0);
+            const bf16x8 v0 = widen8<E4M3>(vr[d].x, vr[d].y), v1 = widen8<E4M3>(vr[d].z, vr[d].w);
+            o[d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v0, pl[0], o[d], 0, 0, 0);
+            o[d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v1, pl[1], o[d], 0, 0, 0);
+            o[d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v0, pb[0], o[d], 0, 0, 0);
+            o[d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v1, pb[1], o[d], 0, 0, 0);
         }
     }
     if (bad && c.status) atomicOr(c.status, 4u);

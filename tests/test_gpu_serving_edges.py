@@ -300,3 +300,25 @@ def test_two_threads_over_one_cache():
         t.join()
     assert not wrong
     cache.check()
+
+
+@pytest.mark.parametrize("new,dim,heads,dtype", [(1, 64, 4, "int8"), (1, 256, 2, "e4m3"), (3, 128, 20, "e4m3"), (15, 80, 4, "int8"),
+                                                 (1, 192, 63, "e4m3")])
+def test_few_rows_hold_probabilities_in_16_bits(new, dim, heads, dtype):
+    """Values of either sign that nearly cancel: a probability's error shows
+    beside the result's own rounding.  Each part of P is rounded by at most
+    2^-8 of it (8 significant bits), the two by 2^-16; its product with a code
+    is exact; fp32 sums are in the logits' slack, which counts twice."""
+    print("probabilities", new, dim, heads, dtype, flush=True)
+    rng = np.random.default_rng(dim + heads)
+    lens = [5000, 70, 1]
+    cache, model = _filled(rng, lens, kv_heads=1, head_dim=dim, dtype=dtype)
+    q = _bf16(rng, 3 * new, heads, dim)
+    at = [0, new, 2 * new, 3 * new]
+    for kw in ({}, dict(window=700, sinks=4), dict(softcap=30.0)):
+        got = cache.attend(0, q.cuda(), _ids(0, 1, 2), _ids(*at), max_new=new, **kw)
+        cache.check()
+        out, ref, slack, spread = model.attend(0, _f64(q), [0, 1, 2], at, **kw)
+        slack = np.where(np.isneginf(ref), 0, slack)
+        bound = (2.0 ** -16 + 2.02 * slack[..., None]) * spread + 2.0 ** -8 * 1.01 * np.abs(out) + 1e-30
+        assert np.all(np.abs(_f64(got) - out) <= bound), (kw, float((np.abs(_f64(got) - out) / bound).max()))
