@@ -178,7 +178,6 @@ __global__ __launch_bounds__(256, 2) void inner_kernel(LoraArgs p) {
         bf16x8 xv[U], av[U][RT];
 #pragma unroll
         for (uint32_t u = 0; u < U; u++) {
-            // steps past the last: zeros of x against the last one's A
             const uint32_t c = c0 + 32 * u;
             const uint32_t st = min(U * k + u, steps - 1);
             xv[u] = load_x(p, xp, c);
@@ -187,10 +186,12 @@ __global__ __launch_bounds__(256, 2) void inner_kernel(LoraArgs p) {
                 if (r < nr) av[u][r] = *(const bf16x8*)(ap + ((uint64_t)r * steps + st) * 512);
         }
 #pragma unroll
-        for (uint32_t u = 0; u < U; u++)
+        for (uint32_t u = 0; u < U; u++) {
+            if (U * k + u >= steps) break;       // 0 of x times an infinity of the last step's A would be NaN
 #pragma unroll
             for (uint32_t r = 0; r < RT; r++)
                 if (r < nr) acc[r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av[u][r], xv[u], acc[r], 0, 0, 0);
+        }
     }
     if (wave > 0) {
 #pragma unroll
