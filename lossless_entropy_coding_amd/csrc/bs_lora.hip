@@ -163,7 +163,7 @@ __global__ __launch_bounds__(256, 2) void inner_kernel(LoraArgs p) {
     Tile tl;
     if (!get_tile(p, blockIdx.x - packs, tl) || tl.adapter < 0) return;
     __shared__ f32x4 red[3][RT][64];
-    const uint32_t nr = min((uint32_t)(p.ranks[tl.adapter] + 15) / 16, (uint32_t)RT);
+    const uint32_t rank = (uint32_t)p.ranks[tl.adapter], nr = min((rank + 15) / 16, (uint32_t)RT);
     const uint32_t tok = token_at(p, tl.first + min(m, tl.count - 1));
     const uint16_t* xp = p.x + (uint64_t)tok * p.x_stride;
     const uint32_t steps = p.cols_pad / 32;
@@ -207,6 +207,9 @@ __global__ __launch_bounds__(256, 2) void inner_kernel(LoraArgs p) {
             f32x4 s = acc[r];
 #pragma unroll
             for (int w = 0; w < 3; w++) s += red[w][r][lane];
+            // past the adapter's rank A's zeros times an infinity of x are NaN
+#pragma unroll
+            for (uint32_t e = 0; e < 4; e++) s[e] = 16 * r + 4 * g + e < rank ? s[e] : 0.f;
             *(f32x4*)(tp + 16 * r + 4 * g) = s;
         }
     }

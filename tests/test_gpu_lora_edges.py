@@ -32,3 +32,24 @@ def test_infinite_weights_stay_infinite(rank, cols):
         plan = codec.FixedPlan(codec.fixed_encode(np.full(rows * cols, 0x3C00, np.uint16)))
         got = plan.gemm_lora(x.cuda(), rows, cols, pack, batch)
         assert torch.equal(torch.isinf(got), torch.isinf(want)) and not torch.isnan(got).any()
+
+
+@pytest.mark.parametrize("rank", [1, 4, 15, 16, 17, 33, 65, 128])
+def test_infinite_tokens_stay_infinite(rank):
+    """An infinity of x times positive weights is one: the ranks that storage
+    adds to an adapter's own add nothing.  Another adapter of the pack has the
+    full rank of the storage."""
+    rows, cols, inf = 64, 2048, float("inf")
+    one = lambda *shape: torch.full(shape, 0.5, dtype=torch.bfloat16)   # noqa: E731
+    full = next(r for r in (16, 32, 64, 128) if r >= rank)
+    pack = lora.LoraPack([(one(rank, cols), one(rows, rank), 1.0), (one(full, cols), one(rows, full), -1.0)])
+    of = [0, 1, -1, 0, 0, 1]
+    batch = lora.LoraBatch(torch.tensor(of, dtype=torch.int32, device="cuda"), 2)
+    x = torch.ones(6, cols, dtype=torch.bfloat16)
+    x[0, 5], x[1, cols - 1], x[2, 0] = inf, inf, inf
+    for y32 in (True, False):
+        got = pack.add(torch.zeros(6, rows, device="cuda", dtype=torch.float32 if y32 else torch.bfloat16), x.cuda(), batch).float()
+        assert bool((got[0] == inf).all() and (got[1] == -inf).all() and (got[2] == 0).all()) and torch.isfinite(got[3:]).all()
+    plan = codec.FixedPlan(codec.fixed_encode(np.full(rows * cols, 0x3C00, np.uint16)))
+    got = plan.gemm_lora(x.cuda(), rows, cols, pack, batch)
+    assert bool((got[[0, 2]] == inf).all()) and torch.isnan(got[1]).all() and torch.isfinite(got[3:]).all()
