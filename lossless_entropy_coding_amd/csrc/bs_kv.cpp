@@ -13,7 +13,7 @@ using namespace bs;
 
 namespace {
 
-constexpr uint64_t kGridX = 0x7FFFFFFFull, kGridYZ = 65535;
+constexpr uint64_t kGridYZ = 65535, kThreads = 0xFFFFFFFFull;   // workgroups of a grid's y and z, threads of its x
 
 bs_status launched(int e, const char* what) {
     if (e == 0) return BS_OK;
@@ -153,8 +153,12 @@ bs_status attend_args(const bs_kv_cache* cache, const bs_kv_attend_args* x, bsd:
     const uint64_t row_tiles = ((uint64_t)a.max_new * a.group + 15) / 16;
     a.out8 = aligned(x->d_out, 8) && x->out_stride % 4 == 0 && a.c.dim % 4 == 0;
     a.many = (uint64_t)a.max_new * a.group >= 64;
-    if ((uint64_t)a.max_new * a.group > 0x7FFFFFFFull || row_tiles * a.n_seqs * a.c.kv_heads > kGridX / 8 || (uint64_t)a.n_seqs * a.max_new > kGridX) {
-        set_error("%u sequences of %u new tokens are too many for one call", a.n_seqs, a.max_new);
+    // workgroups of the kernel for few rows, of the one for many, and of its join
+    const uint64_t block = a.c.wide <= 128 ? 256 : 128, row_blocks = ((uint64_t)a.max_new * a.group + block - 1) / block;
+    const uint64_t few = row_tiles * a.n_seqs, many = ((uint64_t)a.n_seqs * a.c.kv_heads + 7) / 8 * 8 * row_blocks;
+    if ((uint64_t)a.max_new * a.group > 0x7FFFFFFFull ||
+        (a.many ? many > kThreads / 512 || (uint64_t)a.n_seqs * a.max_new > kThreads / 64 : few > kThreads / 256)) {
+        set_error("%u sequences of up to %u new tokens are too many for one call (max_new: the most of one row)", a.n_seqs, a.max_new);
         return BS_E_INVAL;
     }
     const uint32_t cap = a.c.max_pages * a.c.page;
@@ -233,7 +237,7 @@ bs_status bs_kv_append_async(const bs_kv_cache* cache, uint32_t layer, uint32_t 
     if (n_seqs > kGridYZ) { set_error("%u sequences in one call (at most 65535)", n_seqs); return BS_E_INVAL; }
     if (total > 0x7FFFFFFFu || max_new == 0 || max_new > total) { set_error("max_new %u of %u tokens", max_new, total); return BS_E_INVAL; }
     const uint64_t touch = ((uint64_t)max_new + 2ull * a.c.page - 2) >> a.c.lp;
-    if (touch * 2 * a.c.kv_heads > kGridX / 256) { set_error("max_new %u is too many tokens for one call", max_new); return BS_E_INVAL; }
+    if (touch * 2 * a.c.kv_heads > kThreads / 256) { set_error("max_new %u is too many tokens for one call", max_new); return BS_E_INVAL; }
     if (!d_starts && (total != n_seqs || max_new != 1)) {
         set_error("%u tokens for %u sequences without starts", total, n_seqs);
         return BS_E_INVAL;
@@ -344,6 +348,7 @@ bs_status bs_kv_compact_async(const bs_kv_cache* cache, int32_t* d_table_out, in
     const bs_status rc = page_call(cache, 0, nullptr, false, nullptr, true, d_work, work_bytes, p);
     if (rc != BS_OK) return rc;
     if (!d_table_out || !d_refs_out) { set_error("NULL argument"); return BS_E_INVAL; }
+    if (p.c.max_seqs > kThreads / 256) { set_error("%u rows (at most 2^24 - 1)", p.c.max_seqs); return BS_E_INVAL; }
     const uint64_t tb = 4ull * p.c.max_seqs * p.c.max_pages, rb = 4ull * p.c.n_pages;
     if (overlap(d_table_out, tb, p.c.table, tb) || overlap(d_refs_out, rb, p.c.refs, rb) ||
         overlap(d_table_out, tb, d_refs_out, rb)) {

@@ -55,9 +55,10 @@ bool check_tokens(uint64_t tokens) {
     return false;
 }
 
-// the outer product's grid: tiles times blocks of 256 rows or more
+// the outer product's grid: tiles times blocks of up to 1024 rows (with as
+// many tiles as this), 256 threads each, below 2^32 in all
 bool check_grid(const bs_lora_pack* p, uint32_t tokens) {
-    if ((uint64_t)max_tiles(tokens, p->adapters) * ((p->rows + 255) / 256) <= 0x7FFFFFFFull) return true;
+    if ((uint64_t)max_tiles(tokens, p->adapters) * ((p->rows + 1023) / 1024) < (1u << 24)) return true;
     set_error("%u tokens of %u rows are too many for one call", tokens, p->rows);
     return false;
 }

@@ -246,3 +246,22 @@ def test_workspaces_over_inputs_or_results_are_refused():
     size = int(lib.bs_kv_attend_work_bytes(C.byref(c), C.byref(a)))
     refused(lambda w: lib.bs_kv_attend_async(C.byref(c), C.byref(a), w, size, None), size,
             (X, 2 * 556), (Y, 2 * 656), (O, 32))
+
+
+def test_calls_of_more_threads_than_a_launch_takes_are_refused():
+    """Up front and by name, not by the launch: a grid has less than 2^32 threads in x."""
+    lib, big = L.lib(), _cache(kv_heads=8, max_pages=4096, max_seqs=4096, page_tokens=64)
+    args = lambda **kw: L.KvAttendArgs(*[{**dict(layer=0, n_seqs=2048, heads=40, total_q=1 << 16, max_new=1 << 16, max_len=0, d_seqs=AT,   # noqa: E731
+                                              d_starts=AT, d_q=AT, d_out=AT, d_lse=None, q_stride=40 * 64, out_stride=40 * 64, scale=0.0,
+                                              softcap=0.0, window=0, sinks=0), **kw}[n] for n, _ in L.KvAttendArgs._fields_])
+    for kw in (dict(), dict(n_seqs=1 << 23, total_q=1 << 23, max_new=16), dict(n_seqs=1 << 24, total_q=1 << 24, max_new=1, heads=40),
+               dict(n_seqs=1 << 20, total_q=1 << 21, max_new=200, heads=8)):
+        assert lib.bs_kv_attend_async(C.byref(big), C.byref(args(**kw)), None, 0, None) == L.BS_E_INVAL, kw
+        assert b"too many" in lib.bs_last_error()
+    assert lib.bs_kv_attend_work_bytes(C.byref(big), C.byref(args(n_seqs=4, total_q=256, max_new=64))) > 0
+    wide = _cache(max_seqs=1 << 24, max_pages=1)
+    w = int(lib.bs_kv_pages_work_bytes(C.byref(wide), 0))
+    assert lib.bs_kv_compact_async(C.byref(wide), 1 << 40, 1 << 41, AT, w, None) == L.BS_E_INVAL
+    # 2^24 tokens are 2^20 tiles and one begun for each adapter
+    assert lib.bs_lora_work_bytes(C.byref(_pack(rows=15 * 1024)), 1 << 24) > 0
+    assert lib.bs_lora_work_bytes(C.byref(_pack(rows=16 * 1024)), 1 << 24) == 0
