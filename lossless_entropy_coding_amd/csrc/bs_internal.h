@@ -106,11 +106,11 @@ uint64_t plan_device_bytes(const bs_plan* plan);   // device memory the plan all
 uint64_t plan_status_words(const bs_plan* plan);   // status words a full decode writes
 uint32_t plan_records(const bs_plan* plan);
 
-// bs_fixed_gemm_async with adapters whose inner products are in lora->t: the
-// product adds them where it is not split; the split product's second half
-// (given a workspace and cols >= 4096) stays in the workspace, batch x rows
-// floats, for the caller to add into Y (bs_fixed.cpp).  lora NULL: the plain
-// product.  check_only: nothing is enqueued.
+// bs_fixed_gemm_async with adapters whose inner products are in lora->t.  In
+// one share (lora->nparts 0) the product adds them in its epilogue.  Else the
+// sums of the shares after the first stay in the workspace, nparts times batch
+// x rows floats, for the caller's next launch to add into Y with the adapters'
+// part.  lora NULL: the plain product.  check_only: nothing is enqueued.
 bs_status fixed_gemm(const bs_fixed_info* info, const void* d_blob, uint64_t rows, uint64_t cols, uint32_t batch,
                      const void* d_x, float* d_y, uint32_t* d_status, void* d_work, uint64_t work_bytes,
                      const bsd::LoraArgs* lora, bool check_only, void* stream);

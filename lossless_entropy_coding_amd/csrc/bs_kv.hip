@@ -616,8 +616,8 @@ __global__ __launch_bounds__(256) void copy_kernel(KvPages p, uint32_t parts) {
 }
 
 // ---------------------------------------------------------------- compact
-// work: [0] pages in use, [1] pages to move, [2] pages in use below [0],
-// [4 ..] block counts, then the list of movers and the list of holes
+// work: [0] pages in use, [1] pages to move, [4 ..] block counts, then the list
+// of movers and the list of holes
 constexpr uint32_t kCompactBlock = 4096;
 
 __device__ __forceinline__ uint32_t live_count(const KvView& c, uint32_t lo, uint32_t hi, uint32_t* sums) {

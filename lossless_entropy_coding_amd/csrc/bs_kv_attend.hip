@@ -295,15 +295,15 @@ __device__ __forceinline__ void join_row(const KvAttend& a, uint32_t tok, uint32
     out_write(a, tok, qh, ch, top, total, o);
 }
 
-// grid: (sequences * row tiles, key heads, splits); NW waves.  The bound of
+// grid: (sequences * row tiles, key heads, splits); four waves.  The bound of
 // two waves per SIMD keeps the kernel within 256 registers and so the
 // products' accumulators out of the AGPRs: with them there, the compiler here
 // reads a product's later elements at a block's join without the wait that
 // it puts before the first, and they come back stale.
-template <int DW, bool E4M3, int NW, bool CAP>
-__global__ __launch_bounds__(64 * NW, 2) void attend_kernel(KvAttend a, uint32_t row_tiles) {
+template <int DW, bool E4M3, bool CAP>
+__global__ __launch_bounds__(256, 2) void attend_kernel(KvAttend a, uint32_t row_tiles) {
     const KvView& c = a.c;
-    constexpr uint32_t D = 64 * DW;
+    constexpr uint32_t D = 64 * DW, NW = 4;
     // values loaded with the keys; the rest follow when the keys' registers
     // are free (all at once, head_dim 256 spills registers)
     constexpr uint32_t kFirst = DW >= 3 ? 2 * DW : 4 * DW;
@@ -485,11 +485,11 @@ __global__ __launch_bounds__(64 * NW, 2) void attend_kernel(KvAttend a, uint32_t
         const uint32_t n = i / (D / 4), ch = 4 * (i % (D / 4));
         float top = -__builtin_inff(), total = 0.f;
 #pragma unroll
-        for (int w = 0; w < NW; w++) top = fmaxf(top, ml[w][0][n]);
+        for (uint32_t w = 0; w < NW; w++) top = fmaxf(top, ml[w][0][n]);
         const float sub = top == -__builtin_inff() ? 0.f : top;
         f32x4 v = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int w = 0; w < NW; w++) {
+        for (uint32_t w = 0; w < NW; w++) {
             const float f = exp2_fast(ml[w][0][n] - sub);
             total += f * ml[w][1][n];
             v += f * *(const f32x4*)&os[w][n][ch];
@@ -888,7 +888,7 @@ int launch(const KvAttend& a, hipStream_t st) {
     }
     const uint32_t row_tiles = (a.max_new * a.group + 15) / 16;
     const dim3 grid(a.n_seqs * row_tiles, a.c.kv_heads, a.splits);
-    hipLaunchKernelGGL((attend_kernel<DW, E4M3, 4, CAP>), grid, dim3(256), 0, st, a, row_tiles);
+    hipLaunchKernelGGL((attend_kernel<DW, E4M3, CAP>), grid, dim3(256), 0, st, a, row_tiles);
     return (int)hipGetLastError();
 }
 
