@@ -387,28 +387,30 @@ __global__ __launch_bounds__(256) void append_kernel(KvAppend a) {
 // ------------------------------------------------------------------ pages
 constexpr uint32_t kScan = 1024;             // threads of the allocating workgroup
 
-// exclusive prefix over the workgroup of v, and its total.  Sums stop at `cap`
-// (a total of less than cap is exact, and so are its prefixes): up to 1024
-// rows of up to 2^27 pages each would pass 32 bits
-__device__ __forceinline__ uint32_t block_prefix(uint32_t v, uint32_t* sums, uint32_t& total, uint32_t cap = 1u << 30) {
+// exclusive prefix over the workgroup of v, and its total.  CAP: sums stop at
+// `cap` (at most 2^28 + 1; less than cap is exact, and so are its prefixes):
+// 1024 rows of up to 2^27 pages each would pass 32 bits
+template <bool CAP = false>
+__device__ __forceinline__ uint32_t block_prefix(uint32_t v, uint32_t* sums, uint32_t& total, uint32_t cap = 0) {
     const uint32_t t = threadIdx.x, lane = t & 63u, w = t >> 6;
-    v = min(v, cap);
+    if (CAP) v = min(v, cap);
     uint32_t x = v;
 #pragma unroll
     for (int s = 1; s < 64; s <<= 1) {
         const uint32_t y = __shfl_up(x, s);
-        if (lane >= (uint32_t)s) x = min(x + y, cap);
+        if (lane >= (uint32_t)s) x = CAP ? min(x + y, cap) : x + y;
     }
     __syncthreads();
     if (lane == 63) sums[w] = x;
     __syncthreads();
-    uint32_t before = 0, all = 0;
+    uint32_t before = 0;                         // of up to 15 waves
+    std::conditional_t<CAP, uint64_t, uint32_t> all = 0;
     for (uint32_t i = 0; i < blockDim.x / 64; i++) {
         const uint32_t y = sums[i];
-        if (i < w) before = min(before + y, cap);
-        all = min(all + y, cap);
+        if (i < w) before += y;
+        all += y;
     }
-    total = all;
+    total = CAP ? (uint32_t)min((uint64_t)all, (uint64_t)cap) : (uint32_t)all;
     return before + x - v;
 }
 
@@ -482,7 +484,7 @@ __global__ __launch_bounds__(kScan) void alloc_kernel(KvPages p) {
         }
         if (err) atomicOr(&bad, err);
         uint32_t sum;
-        const uint32_t at = block_prefix(need, sums, sum, c.n_pages + 1);
+        const uint32_t at = block_prefix<true>(need, sums, sum, c.n_pages + 1);
         if (i < p.n) {
             offs[i] = (int32_t)(total + at);
             lens[i] = had;
