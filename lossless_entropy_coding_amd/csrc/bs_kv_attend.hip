@@ -13,18 +13,18 @@
 //                   P (times the scale of V's page, a power of two) enters
 //                   as two BF16 numbers, 16 significant bits, where rows are
 //                   few: the products are exact and the result is the fp32
-//                   form's to its own rounding (1e-4 of it apart on 4 x 131071
-//                   tokens and on 64 windows, where one BF16 number gave 1e-3
-//                   to 2e-3), for 0.3 to 1% of the time where HBM bounds it,
-//                   0.3 us of a lone short row's 10.5.  Where rows are many
-//                   the matrix products would take half as long again and
-//                   the registers do not hold the second part: P is rounded
-//                   to BF16, the type of the result.  The tokens' rounding
-//                   errors are independent, and their sum is about as large
-//                   as the result's own rounding (two prompts of 2048 tokens
-//                   over 8000: 2.3e-3 from the 64-bit result, the fp32 form
-//                   1.6e-3).  The sum of P is kept in fp32 from the unrounded
-//                   values.
+//                   form's to its own rounding (1e-4 of it apart or less on
+//                   777, 64 x 4096 and 4 x 131071 tokens, where one BF16
+//                   number gave 1e-3 to 2e-3).  It costs up to 1.5% where HBM
+//                   or drafts bound it and 0.2 us of a lone short row's 10.5.
+//                   Where rows are many the matrix products would take half
+//                   as long again and the registers do not hold the second
+//                   part: P is rounded to BF16, the type of the result.  The
+//                   tokens' rounding errors are independent, and their sum is
+//                   about as large as the result's own rounding (two prompts
+//                   of up to 2048 tokens over 8000: 2.3e-3 from the 64-bit
+//                   result, the fp32 form 1.7e-3).  The sum of P is kept in
+//                   fp32 from the unrounded values.
 //
 // The tokens of a 64-token tile are dealt to the four 16-token steps of S^T
 // such that lane group g (lanes 16 g ..) ends up with tokens 16 g .. 16 g +
@@ -42,13 +42,13 @@
 //
 // What bounds it, measured:
 // few rows: the cache's bytes.  4 sequences of 131071 tokens (40 heads on 8 of
-//   128 channels, int8): 1.07 GB in 200 us, 5.4 TB/s.  64 ragged sequences
-//   with a window of 4096 (16 heads on 8 of 256 channels, e4m3): 750 MB in 156
-//   us, 4.8 TB/s.  A large copy moves 4.8 TB/s here.  A lone short row is a
+//   128 channels, int8): 1.07 GB in 203 us, 5.3 TB/s.  64 ragged sequences
+//   with a window of 4096 (16 heads on 8 of 256 channels, e4m3): 750 MB in 159
+//   us, 4.7 TB/s.  A large copy moves 4.8 TB/s here.  A lone short row is a
 //   chain of dependent loads (row, page, keys, values, join): 777 tokens, 11 us.
-// many rows (attend_rows_kernel): the waves' instructions.  2 prompts of 2048
-//   new tokens over 8000 (40 heads on 8 of 128 channels, e4m3): 540 us, 820
-//   TFLOP/s; a large library product reaches 1430.
+// many rows (attend_rows_kernel): 2 prompts of up to 2048 new tokens over 8000
+//   (40 heads on 8 of 128 channels, e4m3): 536 us, 827 TFLOP/s; a large
+//   library product reaches 1430.  See there.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -536,11 +536,13 @@ __global__ __launch_bounds__(256, 2) void attend_kernel(KvAttend a, uint32_t row
 // scales go into the operands.  The exponentials are taken against the
 // maximum of earlier tiles, as long as a lane's 16 of them sum to 2^10 or
 // less (as exact in fp32 and BF16 as below 1); then neither the tile's
-// maximum nor a scaling of the result is needed.  The VALU bounds the loop:
-// 16 exponentials take as long as 64 other instructions.  The matrix cores are
-// busy for 40% of the clocks in which a CU has work.  Dealing tiles evenly to
-// one workgroup per CU, 8-bit operands in LDS and reading two tiles ahead were
-// 2 to 15% slower.
+// maximum nor a scaling of the result is needed.  Neither unit is full: of the
+// SIMDs' time in CUs that have work, matrix instructions take 41% and issued
+// vector instructions (an exponential as long as four others) 56%, LDS reads
+// 26% of the CUs', with no bank conflicts.  The first two nearly add up to the
+// whole, so the halves of the waves overlap less than they are meant to; why
+// is not found.  Dealing tiles evenly to one workgroup per CU, 8-bit operands
+// in LDS and reading two tiles ahead were 2 to 15% slower.
 constexpr float kGrow = 1024.f;
 
 template <int DW, bool E4M3, int NR, bool CAP>

@@ -77,13 +77,13 @@ uint32_t share_rule(const bs_lora_pack* p, uint32_t tiles) {
 // CU takes one workgroup (32 rows and a share) at a time, so the time goes by
 // rounds of workgroups times the panels of a share (and a quarter of a panel to
 // start each): the shares that make it least, the fewest of these, at most 8
-// (each is a pass over Y in the last launch).  54 tokens on 163 x 14336: 63 us
-// with two shares, 38 with seven (both before X was laid out; 32 since); 26 on
-// 5182 x 12288: 66 us with two, 55 with three; 64 on 3584 x 14336: 54 with two,
-// a fifth more with three, a second round.  From 8 tokens on at least two, as
-// in the plain product; below, one wherever that is as fast, since the
-// product's epilogue then adds the adapters (4 tokens on 2000 x 4096: 17.1 us
-// with one, 18.8 with two).
+// (each is a pass over Y in the last launch).  In all, 8 adapters of rank 16,
+// us: 54 tokens on 163 x 14336 take 51 with two shares, 36 with four, 32 with
+// seven; 26 on 5182 x 12288 66 with two, 54 with three, 70 with four; 64 on
+// 3584 x 14336 54 with two and 65, a second round, with three.  From 8 tokens
+// on at least two, as in the plain product; below, one wherever that is as
+// fast, since the product's epilogue then adds the adapters (4 tokens on 2000
+// x 4096: 17.0 with one, 18.2 with two).
 uint32_t panel_shares(uint64_t rows, uint64_t cols, uint32_t tokens) {
     int cus = 0;
     if (bsk_device_cus(&cus) != 0 || cus <= 0) cus = 256;
