@@ -550,6 +550,7 @@ __global__ __launch_bounds__(512, 2) void attend_rows_kernel(KvAttend a, uint32_
     const KvView& c = a.c;
     constexpr uint32_t D = 64 * DW, kFrags = 8 * DW;                // 1-KiB operands of a side of a tile
     __shared__ __attribute__((aligned(16))) uint8_t buf[2][2 * kFrags][1024];
+    __shared__ float least[8][NR][16];                              // of each row: -infinity, NaN where its query is not finite
 
     const uint32_t t = threadIdx.x, lane = t & 63u, m = lane & 15u, g = lane >> 4;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(t >> 6);
@@ -605,12 +606,13 @@ __global__ __launch_bounds__(512, 2) void attend_rows_kernel(KvAttend a, uint32_
 #pragma unroll
         for (int d = 0; d < 4 * DW; d++) o[n][d] = f32x4{0.f, 0.f, 0.f, 0.f};
         mx[n] = -__builtin_inff();
-        // 0, or NaN for a query that holds a NaN or an infinity (0 times it) and sees a token
+        sum[n] = 0.f;
+        // 0, or NaN for a query that holds a NaN or an infinity (0 times it)
         f32x4 z = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (uint32_t x = 0; x < 2 * DW; x++)
             z = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, v4u{0u, 0u, 0u, 0u}), q[n][x >> 1][x & 1], z, 0, 0, 0);
-        sum[n] = pos[n] >= 0 ? z[0] : 0.f;
+        if (g == 0) least[wave][n][m] = z[0] == 0.f ? -__builtin_inff() : z[0];
     }
     const int32_t* trow = c.table + (uint64_t)(uint32_t)max(sq.row, 0) * c.max_pages;
     const uint64_t hoff = (uint64_t)head * c.page * c.wide;
@@ -810,9 +812,10 @@ __global__ __launch_bounds__(512, 2) void attend_rows_kernel(KvAttend a, uint32_
                     tot += x[e];
                 }
                 if (__builtin_amdgcn_ballot_w64(!(tot <= kGrow)) != 0) {
-                    // NaN: a token without a page (a query's own NaN is in its sum already)
+                    // NaN of a finite query: a token without a page (the larger of two NaN is NaN)
+                    const float low = least[wave][n][m];
 #pragma unroll
-                    for (uint32_t e = 0; e < 16; e++) p[e] = fmaxf(p[e], -__builtin_inff());
+                    for (uint32_t e = 0; e < 16; e++) p[e] = fmaxf(p[e], low);
                     float top = p[0];
 #pragma unroll
                     for (uint32_t e = 1; e < 16; e++) top = fmaxf(top, p[e]);

@@ -322,3 +322,30 @@ def test_few_rows_hold_probabilities_in_16_bits(new, dim, heads, dtype):
         slack = np.where(np.isneginf(ref), 0, slack)
         bound = (2.0 ** -16 + 2.02 * slack[..., None]) * spread + 2.0 ** -8 * 1.01 * np.abs(out) + 1e-30
         assert np.all(np.abs(_f64(got) - out) <= bound), (kw, float((np.abs(_f64(got) - out) / bound).max()))
+
+
+@pytest.mark.parametrize("cap", [30.0, 300.0])
+@pytest.mark.parametrize("new,dim", [(1, 64), (70, 128), (70, 256)])
+def test_capped_logits_of_an_infinite_query(new, dim, cap):
+    """Keys that are positive in every channel times an infinity are infinite,
+    capped to c, and so all alike: the result is the mean of the values."""
+    rng = np.random.default_rng(dim)
+    lens = [300, 90]
+    cache, model = _filled(rng, lens, kv_heads=1, head_dim=dim)
+    k = _bf16(rng, sum(lens), 1, dim).abs() + 0.5
+    v = _bf16(rng, sum(lens), 1, dim)
+    cache.append(0, k.cuda(), v.cuda(), _ids(0, 1), _ids(0, 300, 390))
+    model.append(0, _f64(k), _f64(v), [0, 1], [0, 300, 390])
+    q = _bf16(rng, 2 * new, 2, dim)
+    q[:, 0, 3], q[:, 1, dim - 1] = float("inf"), float("-inf")
+    got, lse = cache.attend(0, q.cuda(), _ids(0, 1), _ids(0, new, 2 * new), max_new=new, softcap=cap, lse=True)
+    cache.check()
+    for r, n in enumerate(lens):
+        values = model.tokens(0, r, 0, 1)
+        for j in range(new):
+            see = n - new + j + 1
+            want, spread = values[:see].mean(axis=0), np.abs(values[:see]).mean(axis=0)
+            for h, sign in ((0, 1), (1, -1)):
+                bound = (2.0 ** -8 * 1.01 + 2.0 ** -14) * spread + 2.0 ** -8 * 1.01 * np.abs(want)
+                assert np.all(np.abs(_f64(got[r * new + j, h]) - want) <= bound), (r, j, h)
+                assert abs(float(lse[r * new + j, h]) - (sign * cap + np.log(see))) <= 2.0 ** -20 * (cap + 10)
