@@ -1,0 +1,520 @@
+"""Cases of the operators that carry several continuations of one prompt (samples, beams, drafts) over the paged 8-bit
+key/value cache: attention that reads a group's common tokens once, the plan of a step's tokens, the choice of the best
+continuations, and the move of the cache's rows to the beams that were chosen.
+
+Each case runs in one of two ways.  With `own` false, `run` computes the operator in its plain form: elementary torch
+operations.  With `own` true, it makes the calls that a user of the package makes.  Both work on the tensors that
+`prepare` makes from the seed.
+
+What the operators compute:
+
+attend  softmax(q k / sqrt(dim)) v over the tokens a query sees: those up to its own place, of these the last `window`
+        (0: all) and the first `sinks`; with `softcap` c the logits are c tanh(logit / c).  The rows of a group have
+        their first tokens on the same pages.
+batch   What a step needs to know of its tokens, from how many each row has: the rows' offsets into the tokens, each
+        token's place in its row and its slot of the pool (page * page tokens + place in the page), the rows' pages side
+        by side, and of each row the first row of its group and how many leading tokens the whole group has on the same
+        pages (a multiple of 64).
+select  Of the continuations of a request's beams, score + log softmax(logits)[token], the `keep` best: by score, of
+        equal ones the lowest beam, then the lowest token.  Logits of -infinity are not chosen; a beam with a score of
+        -infinity or NaN, or whose logits hold NaN or +infinity, has no continuations; a beam that is done has one, the
+        end token at its score.  Where there are too few, token and beam are -1 and the score is -infinity.
+reorder Rows take, all at once, the tokens of their parents' rows.  Whole pages are shared; a last, partly filled page
+        goes to one child (the parent's own row if it is its own child, else the first) and is copied for the others, to
+        the lowest pages that were free.  Entries of the table past a row's pages keep what they held.
+
+The cache: k [layers, pages, kv_heads, page, D] and v [layers, pages, kv_heads, D, page] bytes (D: dim rounded up to a
+multiple of 64, zeros past dim), scale [layers, pages, kv_heads, 2] fp32, refs [pages], table [rows, pages per row] and
+lens [rows] int32.
+"""
+import math
+import random
+
+import torch
+
+own = False
+
+LARGEST = {"e4m3": 448.0, "int8": 127.0}
+
+
+def listed():
+    return [
+        # one user's four beams, a few words into their answer to a short prompt: the latency of a step
+        {"name": "attend four beams", "op": "attend", "groups": 1, "rows": 4, "prefix": 600, "own": 24, "new": 1, "heads": 16,
+         "kv_heads": 8, "dim": 256, "page": 16, "type": "e4m3", "window": 0, "sinks": 0, "softcap": 50.0, "ragged": 1},
+        # many samples of one long prompt (the 27.7B checkpoint's heads)
+        {"name": "attend samples", "op": "attend", "groups": 1, "rows": 32, "prefix": 8000, "own": 600, "new": 1, "heads": 40,
+         "kv_heads": 8, "dim": 128, "page": 64, "type": "int8", "window": 0, "sinks": 0, "softcap": 0.0, "ragged": 2},
+        # requests under four system prompts, on a layer with a sliding window (Gemma-2-9B-shaped heads)
+        {"name": "attend system prompts", "op": "attend", "groups": 4, "rows": 32, "prefix": 4099, "own": 1021, "new": 1,
+         "heads": 16, "kv_heads": 8, "dim": 256, "page": 64, "type": "e4m3", "window": 4096, "sinks": 4, "softcap": 50.0,
+         "ragged": 3},
+        # drafted tokens of several continuations of a long document
+        {"name": "attend drafts", "op": "attend", "groups": 1, "rows": 8, "prefix": 100003, "own": 300, "new": 4, "heads": 40,
+         "kv_heads": 8, "dim": 128, "page": 32, "type": "e4m3", "window": 0, "sinks": 0, "softcap": 0.0, "ragged": 4},
+        # the tokens of a decode step: eight requests with eight continuations each
+        {"name": "batch a step", "op": "batch", "groups": 8, "rows": 8, "prefix": 8000, "own": 192, "new": 1, "page": 64,
+         "ragged": 5},
+        # the prompts of many requests under one system prompt, in one step
+        {"name": "batch prompts", "op": "batch", "groups": 1, "rows": 96, "prefix": 2048, "own": 8191, "new": 8191, "page": 16,
+         "ragged": 6},
+        # one user's beams, over the vocabulary of the 256000 x 3584 embedding
+        {"name": "select one user", "op": "select", "batch": 1, "beams": 4, "keep": 4, "vocab": 256000, "half": False,
+         "softcap": 0.0, "allowed": 0, "done": 0.0, "ragged": 7},
+        # a full batch of beams over the same vocabulary, with the final soft cap of that shape's models
+        {"name": "select full batch", "op": "select", "batch": 64, "beams": 8, "keep": 8, "vocab": 256000, "half": True,
+         "softcap": 30.0, "allowed": 0, "done": 0.1, "ragged": 8},
+        # answers bound to a grammar: few tokens are allowed, twice as many candidates as beams are kept, odd vocabulary
+        {"name": "select constrained", "op": "select", "batch": 16, "beams": 5, "keep": 10, "vocab": 50257, "half": False,
+         "softcap": 0.0, "allowed": 40, "done": 0.2, "ragged": 9},
+        # one user's beams after a step, through all layers of a model
+        {"name": "reorder one user", "op": "reorder", "layers": 42, "batch": 1, "beams": 4, "context": 700, "own": 25,
+         "kv_heads": 8, "dim": 256, "page": 16, "type": "e4m3", "ragged": 10},
+        # a full batch of beams after a step
+        {"name": "reorder full batch", "op": "reorder", "layers": 12, "batch": 64, "beams": 8, "context": 1500, "own": 61,
+         "kv_heads": 8, "dim": 128, "page": 16, "type": "int8", "ragged": 11},
+    ]
+
+
+def _log(rng, lo, hi):
+    return int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))
+
+
+def draw(rng):
+    op = rng.choice(["attend", "attend", "attend", "batch", "select", "select", "reorder"])
+    ragged = rng.randint(1, 1 << 20)
+    if op == "attend":
+        kv_heads, dim = rng.choice([1, 2, 4, 8]), rng.choice([64, 80, 96, 128, 256])
+        groups, group = _log(rng, 1, 8), rng.choice([1, 2, 4, 5])
+        rows = _log(rng, 1, 128 // groups)
+        wider = max(1, kv_heads * dim // 1024)
+        own_ = _log(rng, 1, 1024 // wider)
+        new = 1 if rng.random() < 0.7 else min(own_, _log(rng, 2, 8))
+        prefix = _log(rng, 16, min(100003, (150000 // wider - groups * rows * own_ // 2) // groups, 24000000 // (groups * rows * new * wider)))
+        return {"op": op, "groups": groups, "rows": rows, "prefix": prefix, "own": own_, "new": new, "heads": kv_heads * group,
+                "kv_heads": kv_heads, "dim": dim, "page": rng.choice([16, 32, 64, 128]), "type": rng.choice(["e4m3", "int8"]),
+                "window": rng.choice([0, 0, _log(rng, 1, 8192)]), "sinks": rng.choice([0, 4]),
+                "softcap": rng.choice([0.0, 50.0]), "ragged": ragged}
+    if op == "batch":
+        groups = _log(rng, 1, 16)
+        rows = _log(rng, 1, 96 // groups)
+        new = 1 if rng.random() < 0.5 else _log(rng, 2, 8191)
+        return {"op": op, "groups": groups, "rows": rows, "prefix": _log(rng, 16, 32000 // groups), "own": new + _log(rng, 1, 500) - 1,
+                "new": new, "page": rng.choice([16, 32, 64, 128, 256]), "ragged": ragged}
+    if op == "select":
+        vocab, batch = _log(rng, 1000, 256000), _log(rng, 1, 64)
+        beams = min(_log(rng, 1, 16), 131072000 // (batch * vocab))
+        return {"op": op, "batch": batch, "beams": max(1, beams), "keep": max(1, beams) * rng.choice([1, 2]), "vocab": vocab,
+                "half": vocab * batch * beams > 65536000 or rng.random() < 0.5, "softcap": rng.choice([0.0, 30.0]),
+                "allowed": rng.choice([0, 0, _log(rng, 1, 100)]), "done": rng.choice([0.0, 0.2]), "ragged": ragged}
+    layers, kv_heads, dim, page = _log(rng, 1, 42), rng.choice([1, 2, 4, 8]), rng.choice([64, 96, 128, 256]), rng.choice([16, 32, 64])
+    batch, beams, context = _log(rng, 1, 64), _log(rng, 1, 8), _log(rng, 1, 1500)
+    own_ = _log(rng, 1, 61)
+    while layers * kv_heads * _wide(dim) * batch * (context + beams * (own_ + 2 * page)) > 12 * 8 * 128 * 64 * (1500 + 8 * 93):
+        layers, batch = max(1, layers // 2), max(1, batch - batch // 4)
+        if layers == batch == 1:
+            context = max(1, context // 2)
+    return {"op": op, "layers": layers, "batch": batch, "beams": beams, "context": context, "own": own_, "kv_heads": kv_heads,
+            "dim": dim, "page": page, "type": rng.choice(["e4m3", "int8"]), "ragged": ragged}
+
+
+# ---------------------------------------------------------------- shapes that a case stands for
+def _wide(dim):
+    return -(-dim // 64) * 64
+
+
+def _own_lengths(case, n):
+    """Tokens of each row after the common ones: the longest first, the others spread over an eighth to the whole of it."""
+    rng = random.Random(case["ragged"])
+    top, least = case["own"], case.get("new", 1)
+    return [top] + [max(min(least, top), min(top, _log(rng, max(1, top // 8), top))) for _ in range(n - 1)]
+
+
+def _new_counts(case, n):
+    if case["new"] == 1:
+        return [1] * n
+    rng = random.Random(case["ragged"] + 1)
+    return [min(case["new"], x) - (rng.randrange(max(1, x // 2)) if i and case["new"] >= x else 0)
+            for i, x in enumerate(_own_lengths(case, n))]
+
+
+def _parents(case):
+    """The beam that each row goes on from: a request's best beams have most children, some have none."""
+    rng, got = random.Random(case["ragged"] + 2), []
+    for b in range(case["batch"]):
+        got += [b * case["beams"] + min(rng.randrange(case["beams"]), rng.randrange(case["beams"])) for _ in range(case["beams"])]
+    return got
+
+
+def _done(case):
+    rng = random.Random(case["ragged"] + 3)
+    return [int(rng.random() < case["done"]) for _ in range(case["batch"] * case["beams"])]
+
+
+def work(case):
+    op = case["op"]
+    if op == "attend":
+        n = case["groups"] * case["rows"]
+        lens, new = [case["prefix"] + x for x in _own_lengths(case, n)], _new_counts(case, n)
+        common = case["prefix"] // case["page"] * case["page"]
+        w, s, pairs, seen = case["window"] or 1 << 40, case["sinks"] if case["window"] else 0, 0, 0
+        for g in range(case["groups"]):
+            from_, top = common, 0           # of the common tokens, those that some row of the group sees
+            for length, q in list(zip(lens, new))[g * case["rows"]:(g + 1) * case["rows"]]:
+                for p in range(length - q, length):
+                    pairs += min(p + 1, w) + min(s, max(0, p + 1 - w))
+                first = max(0, length - q + 1 - w)
+                from_, top = min(from_, first), max(top, min(s, first))
+                seen += length - max(common, first) + max(0, min(s, first) - common)
+            seen += common - from_ + min(top, from_)
+        rows = sum(new) * case["heads"]
+        return {"bytes": seen * case["kv_heads"] * case["dim"] * 2 + rows * case["dim"] * 4 + 4 * rows,
+                "flops": 4 * pairs * case["heads"] * case["dim"]}
+    if op == "batch":
+        n = case["groups"] * case["rows"]
+        pages = sum(-(-(case["prefix"] + x) // case["page"]) for x in _own_lengths(case, n))
+        width = -(-(case["prefix"] + case["own"]) // case["page"])
+        return {"bytes": 4 * pages + 4 * n * width + 12 * sum(_new_counts(case, n)) + 28 * n, "flops": 0}
+    if op == "select":
+        rows = len(_done(case)) - sum(_done(case))
+        return {"bytes": rows * case["vocab"] * (2 if case["half"] else 4) + 8 * len(_done(case)) + 16 * case["batch"] * case["keep"],
+                "flops": 3 * rows * case["vocab"]}
+    lens, page, parents = _beam_lengths(case), case["page"], _parents(case)
+    heirs = {p for p in parents if lens[p] % page}
+    copies = sum(lens[p] % page > 0 for p in parents) - len(heirs)
+    one = 2 * case["kv_heads"] * (page * case["dim"] + 4) * case["layers"]
+    return {"bytes": 2 * copies * one + 8 * sum(-(-lens[p] // page) for i, p in enumerate(parents) if p != i) + 12 * len(lens), "flops": 0}
+
+
+def _beam_lengths(case):
+    """All beams of a request are as long as each other; requests are not."""
+    rng, got = random.Random(case["ragged"]), []
+    for b in range(case["batch"]):
+        got += [case["context"] + (case["own"] if b == 0 else _log(rng, 1, case["own"]))] * case["beams"]
+    return got
+
+
+# ---------------------------------------------------------------- inputs
+def _gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def _ints(values):
+    return torch.tensor(values, dtype=torch.int32, device="cuda")
+
+
+def _starts(counts):
+    return _ints([0] + torch.tensor(counts).cumsum(0).tolist())
+
+
+def _heads_like(g, *shape):
+    """Keys or values as projections give them: channels of differing size, now and then a large one."""
+    dim = shape[-1]
+    size = torch.exp(0.4 * torch.randn(dim, generator=g, device="cuda"))
+    size[torch.rand(dim, generator=g, device="cuda") < 0.02] *= 6.0
+    return torch.randn(*shape, generator=g, device="cuda") * size
+
+
+def _values(codes, kind):
+    """The values that 8-bit codes stand for, before their scale."""
+    return codes.view(torch.float8_e4m3fn if kind == "e4m3" else torch.int8).float()
+
+
+def _codes(x, kind):
+    """Values within the type's range to the nearest code, ties to even."""
+    if kind == "e4m3":
+        return x.clamp(-448.0, 448.0).to(torch.float8_e4m3fn).view(torch.uint8)
+    return x.round().clamp(-127.0, 127.0).to(torch.int8).view(torch.uint8)
+
+
+def _scale_for(amax, kind):
+    """The least power of two s >= 2^-60 with amax <= LARGEST s, exactly."""
+    m, e = torch.frexp(amax / 2.0 ** (9 if kind == "e4m3" else 7))
+    e = e + (m > (0.875 if kind == "e4m3" else 127.0 / 128.0)).int()
+    e = torch.where(amax > 0, e, torch.full_like(e, -60)).clamp_min(-60)
+    return ((e + 127) << 23).view(torch.float32)
+
+
+def _branched(g, groups, rows, common, lens, page, spare):
+    """A table for `groups` of `rows` rows each whose first `common` tokens (whole pages) are on the same pages, on randomly
+    placed pages of a pool that has `spare` more; with the pages' counts."""
+    whole = common // page
+    need = [-(-n // page) - whole for n in lens]
+    pages = groups * whole + sum(need) + spare
+    order = torch.randperm(pages, generator=g, device="cuda").to(torch.int32)
+    table = torch.full((len(lens), max(need) + whole + 1), -1, dtype=torch.int32, device="cuda")
+    refs = torch.zeros(pages, dtype=torch.int32, device="cuda")
+    at = 0
+    for i, n in enumerate(need):
+        if i % rows == 0:
+            mine = order[at:at + whole]
+            refs[mine.long()] = rows
+            at += whole
+        table[i, :whole] = mine
+        table[i, whole:whole + n] = order[at:at + n]
+        refs[order[at:at + n].long()] = 1
+        at += n
+    return table, refs
+
+
+def _filled(case, g, pages):
+    """Keys, values and scales of one layer, every slot of every page as after an append."""
+    page, h, dim, kind = case["page"], case["kv_heads"], case["dim"], case["type"]
+    wide = _wide(dim)
+    k = torch.zeros(1, pages, h, page, wide, dtype=torch.uint8, device="cuda")
+    v = torch.zeros(1, pages, h, wide, page, dtype=torch.uint8, device="cuda")
+    scale = torch.empty(1, pages, h, 2, device="cuda")
+    for side in range(2):
+        x = _heads_like(g, pages, h, page, dim)
+        scale[0, :, :, side] = _scale_for(x.abs().amax((2, 3)), kind)
+        codes = _codes(x / scale[0, :, :, side, None, None], kind)
+        if side == 0:
+            k[0, ..., :dim] = codes
+        else:
+            v[0, ..., :dim, :] = codes.transpose(2, 3)
+    return {"k": k, "v": v, "scale": scale}
+
+
+def _inputs(case, seed):
+    g, op = _gen(seed), case["op"]
+    if op in ("attend", "batch"):
+        n, page = case["groups"] * case["rows"], case["page"]
+        lens, new = [case["prefix"] + x for x in _own_lengths(case, n)], _new_counts(case, n)
+        common = case["prefix"] // page * page
+        table, refs = _branched(g, case["groups"], case["rows"], common, lens, page, 5)
+        s = {"table": table, "refs": refs, "lens": _ints(lens), "seqs": _ints(list(range(n))), "counts": _ints(new),
+             "groups": _ints([i * case["rows"] for i in range(case["groups"] + 1)]), "total": sum(new), "most": max(new),
+             "longest": max(lens)}
+        if op == "attend":
+            s.update(_filled(case, g, len(refs)))
+            s["starts"], s["common"] = _starts(new), common
+            s["q"] = torch.randn(sum(new), case["heads"], case["dim"], generator=g, device="cuda").bfloat16()
+        else:           # the rows are not in the order of the cache
+            order = torch.randperm(n, generator=g, device="cuda")
+            s["table"][order], s["lens"][order] = s["table"].clone(), s["lens"].clone()
+            s["seqs"] = order.int()
+        return s
+    if op == "select":
+        rows, vocab = case["batch"] * case["beams"], case["vocab"]
+        x = 2.5 * torch.randn(rows, vocab, generator=g, device="cuda")
+        at = torch.randint(0, vocab, (rows, 8), generator=g, device="cuda")       # words that stand out
+        x.scatter_add_(1, at, 6.0 + 6.0 * torch.rand(rows, 8, generator=g, device="cuda"))
+        if case["allowed"]:
+            some = torch.randint(0, vocab, (rows, case["allowed"]), generator=g, device="cuda")
+            x = torch.full_like(x, -math.inf).scatter_(1, some, x.gather(1, some))
+        return {"logits": x.bfloat16() if case["half"] else x, "done": _ints(_done(case)),
+                "scores": -20.0 * torch.rand(case["batch"], case["beams"], generator=g, device="cuda")}
+    lens, page, h, wide = _beam_lengths(case), case["page"], case["kv_heads"], _wide(case["dim"])
+    table, refs = _branched(g, case["batch"], case["beams"], case["context"] // page * page, lens, page, 2 * len(lens) + 3)
+    shape = (case["layers"], len(refs), h)
+    # what the pages hold is only moved
+    bytes_ = lambda *more: torch.randint(0, 256, shape + more, generator=g, device="cuda", dtype=torch.uint8)   # noqa: E731
+    return {"k": bytes_(page, wide), "v": bytes_(wide, page), "scale": torch.rand(shape + (2,), generator=g, device="cuda"),
+            "refs": refs, "table": table, "lens": _ints(lens), "seqs": _ints(list(range(len(lens)))), "parents": _ints(_parents(case))}
+
+
+def prepare(case, seed):
+    s = _inputs(case, seed)
+    s["case"] = case
+    if own:       # what a serving program keeps between calls: the cache's handle, the step's plan, the beams' handle
+        from lossless_entropy_coding_amd import beam, kv
+        if case["op"] == "select":
+            s["beams"] = beam.Beams(case["batch"], case["beams"], keep=case["keep"], eos=2)
+            return s
+        if case["op"] == "batch":      # no keys or values are looked at: the least that a cache can hold
+            n, page = len(s["refs"]), case["page"]
+            s["k"], s["v"] = (torch.zeros(1, n, 1, *x, dtype=torch.uint8, device="cuda") for x in ((page, 64), (64, page)))
+            s["scale"] = torch.zeros(1, n, 1, 2, device="cuda")
+        s["cache"] = kv.KvCache.over(s["k"], s["v"], s["scale"], s["refs"], s["table"], s["lens"],
+                                     head_dim=case.get("dim", 64), dtype=case.get("type", "e4m3"))
+        if case["op"] in ("attend", "batch"):
+            s["batch"] = kv.KvBatch(s["cache"], s["seqs"], s["counts"], groups=s["groups"], total=s["total"],
+                                    max_new=s["most"], max_len=s["longest"])
+    return s
+
+
+# ---------------------------------------------------------------- the plain forms
+def _side(s, case, ids, side):
+    """Keys (0) or values (1) of pages ids [.., w]: [.., h, w * page, dim] fp32."""
+    x = s["k"][0, ids] if side == 0 else s["v"][0, ids].transpose(-1, -2)
+    x = _values(x.contiguous(), case["type"])[..., :case["dim"]] * s["scale"][0, ids, :, side][..., None, None]
+    return x.transpose(1, 2).reshape(len(ids), case["kv_heads"], -1, case["dim"])
+
+
+def _attend_plain(s, case):
+    page, dim, h, n, most = case["page"], case["dim"], case["kv_heads"], len(s["lens"]), s["most"]
+    group, groups, rows, whole = case["heads"] // h, case["groups"], case["rows"], s["common"] // page
+    pages = s["table"].clamp_min(0).long()
+    # the common tokens once for each group, the others row by row
+    kp, vp = (_side(s, case, pages[::rows, :whole], i) for i in (0, 1))                   # [groups, h, common, dim]
+    ks, vs = (_side(s, case, pages[:, whole:], i) for i in (0, 1))                        # [n, h, others, dim]
+    lens, count = s["lens"], s["counts"]
+    t = torch.arange(s["common"] + ks.shape[2], device="cuda")
+    j = torch.arange(most, device="cuda")
+    token = (s["starts"][:-1, None] + j[None, :]).clamp_max(s["total"] - 1)               # [n, most]
+    q = s["q"][token.long()].float().reshape(n, most, h, group, dim).permute(0, 2, 3, 1, 4).reshape(n, h, group * most, dim)
+    together = q.reshape(groups, rows, h, group * most, dim).transpose(1, 2).reshape(groups, h, -1, dim)
+    first = (together @ kp.transpose(2, 3)).reshape(groups, h, rows, group * most, -1).transpose(1, 2)
+    logit = torch.cat([first.reshape(n, h, group * most, -1), q @ ks.transpose(2, 3)], 3) * dim ** -0.5
+    if case["softcap"]:
+        logit = case["softcap"] * torch.tanh(logit / case["softcap"])
+    place = lens[:, None] - count[:, None] + j[None, :]                                   # [n, most]
+    seen = t[None, None, :] <= place[:, :, None]
+    if case["window"]:
+        seen &= (t[None, None, :] > place[:, :, None] - case["window"]) | (t < case["sinks"])[None, None, :]
+    logit = logit.reshape(n, h, group, most, -1).masked_fill(~seen[:, None, None], -math.inf).reshape(n, h, group * most, -1)
+    top = logit.amax(-1, keepdim=True).clamp_min(-3e38)
+    p = torch.exp(logit - top)
+    total = p.sum(-1, keepdim=True)
+    p = p / total.clamp_min(1e-38)
+    stack = p[..., :s["common"]].reshape(groups, rows, h, group * most, -1).transpose(1, 2).reshape(groups, h, rows * group * most, -1)
+    out = (stack @ vp).reshape(groups, h, rows, group * most, dim).transpose(1, 2).reshape(n, h, group * most, dim)
+    vs = torch.where((t[s["common"]:] < lens[:, None])[:, None, :, None], vs, torch.zeros((), device="cuda"))
+    out = out + p[..., s["common"]:] @ vs
+    out = out.reshape(n, h, group, most, dim).permute(0, 3, 1, 2, 4).reshape(n, most, h * group, dim)
+    lse = (top + total.log()).reshape(n, h, group, most).permute(0, 3, 1, 2).reshape(n, most, h * group)
+    real = j[None, :] < count[:, None]
+    return {"out": out[real].bfloat16(), "lse": lse[real]}
+
+
+def _batch_plain(s, case):
+    page, rows = case["page"], s["seqs"].long()
+    starts = torch.nn.functional.pad(s["counts"].cumsum(0), (1, 0)).int()
+    t = torch.arange(s["total"], device="cuda")
+    of = torch.searchsorted(starts[1:].contiguous(), t.int(), right=True)
+    place = (s["lens"][rows[of]] - starts[of + 1] + t).int()
+    slot = s["table"][rows[of], (place // page).long()].long() * page + place % page
+    lens = s["lens"][rows]
+    col = torch.arange(-(-s["longest"] // page), device="cuda")[None, :]
+    table = torch.where(col * page < lens[:, None], s["table"][rows][:, :col.shape[1]], -1)
+    lead = s["groups"][torch.searchsorted(s["groups"][1:].contiguous(), torch.arange(len(rows), device="cuda", dtype=torch.int32), right=True)]
+    same = ((table == table[lead.long()]) & (table >= 0)).int().cumprod(1).sum(1) * page
+    same = torch.minimum(same, lens) // 64 * 64
+    shared = torch.full_like(lens, 1 << 30).scatter_reduce(0, lead.long(), same.int(), "amin")[lead.long()]
+    return {"starts": starts, "places": place, "slots": slot, "table": table, "lead": lead, "shared": shared}
+
+
+def _select_plain(s, case):
+    """Each beam's best tokens by logit (as whole numbers with the token in the low bits, so that ties go to the lowest), then
+    the best of all beams.  What is next to a border decides whole numbers, so differences, sums and scores have 64 bits."""
+    b, w, keep, vocab = case["batch"], case["beams"], case["keep"], case["vocab"]
+    x = s["logits"].float()
+    bits = x.view(torch.int32).long()
+    key = torch.where(bits >= 0, bits, -(bits & 0x7FFFFFFF)) << 32
+    key += (1 << 32) - 1 - torch.arange(vocab, device="cuda")
+    n = min(keep, vocab)
+    token = (1 << 32) - 1 - (key.topk(n, 1).values & 0xFFFFFFFF)
+    y = x.double()
+    if case["softcap"]:
+        y = case["softcap"] * torch.tanh(y / case["softcap"])
+    top = y.amax(1, keepdim=True)
+    lse = top + torch.exp((y - top).float()).sum(1, keepdim=True, dtype=torch.float64).log()
+    score = s["scores"].double().reshape(-1, 1) + y.gather(1, token) - lse
+    done = s["done"][:, None] != 0
+    score = torch.where(done, -math.inf, score)
+    score[:, :1] = torch.where(done, s["scores"].double().reshape(-1, 1), score[:, :1])
+    token = torch.where(done, 2, token)
+    # of equal scores the lowest beam, then the lowest token
+    at = torch.argsort(token, dim=1, stable=True)
+    score, token = score.gather(1, at).reshape(b, w * n), token.gather(1, at).reshape(b, w * n)
+    got = torch.argsort(score, dim=1, descending=True, stable=True)[:, :keep]
+    score, token = score.gather(1, got), token.gather(1, got)
+    parent = got // n + w * torch.arange(b, device="cuda")[:, None]
+    none = score == -math.inf
+    ended = (done[parent.clamp_min(0), 0] | (token == 2)) & ~none
+    return {"scores": score.float(), "tokens": torch.where(none, -1, token).int(), "parents": torch.where(none, -1, parent).int(),
+            "done": ended.int()}
+
+
+def _reorder_plain(s, case):
+    page, table, refs, lens, rows = case["page"], s["table"], s["refs"], s["lens"], s["seqs"].long()
+    src = s["parents"].long()
+    i = torch.arange(len(rows), device="cuda")
+    col = torch.arange(table.shape[1], device="cuda")[None, :]
+    before, old = table[rows], lens[rows]
+    new = old[src]
+    whole, part = new // page, new % page > 0
+    heir = torch.full_like(i, 1 << 30).scatter_reduce(0, src, torch.where(src == i, -1, i), "amin")[src]
+    copy = part & ~((src == i) | (heir == i))
+    free = torch.argsort((refs != 0).int(), stable=True)
+    to = free[(copy.cumsum(0) - 1).clamp_min(0)]
+    last = before[src, whole.clamp_max(table.shape[1] - 1).long()].long()
+    at, fresh = last[copy], to[copy]
+    s["k"][:, fresh], s["v"][:, fresh], s["scale"][:, fresh] = s["k"][:, at], s["v"][:, at], s["scale"][:, at]
+    held = col * page < new[:, None]
+    after = torch.where(held, before[src], before)
+    after = torch.where((col == whole[:, None]) & copy[:, None], to[:, None].int(), after)
+    gone = col * page < old[:, None]
+    refs.scatter_add_(0, before.clamp_min(0).long().reshape(-1), -gone.int().reshape(-1))
+    refs.scatter_add_(0, after.clamp_min(0).long().reshape(-1), held.int().reshape(-1))
+    table[rows] = after
+    lens[rows] = new
+    return {name: s[name] for name in ("k", "v", "scale", "refs", "table", "lens")}
+
+
+def run(s):
+    case, op = s["case"], s["case"]["op"]
+    if not own:
+        return {"attend": _attend_plain, "batch": _batch_plain, "select": _select_plain, "reorder": _reorder_plain}[op](s, case)
+    if op == "attend":
+        out, lse = s["cache"].attend_shared(0, s["q"], s["batch"], window=case["window"], sinks=case["sinks"],
+                                            softcap=case["softcap"], lse=True)
+        return {"out": out, "lse": lse}
+    if op == "batch":
+        b = s["batch"]
+        b.update(s["seqs"], s["counts"], groups=s["groups"])
+        return {"starts": b.starts, "places": b.places, "slots": b.slots, "table": b.table, "lead": b.lead, "shared": b.shared}
+    if op == "select":
+        got = s["beams"].select(s["logits"], s["scores"], done=s["done"], softcap=case["softcap"])
+        return {"scores": got.scores, "tokens": got.tokens, "parents": got.parents, "done": got.done}
+    s["cache"].reorder(s["seqs"], s["parents"])
+    return {name: s[name] for name in ("k", "v", "scale", "refs", "table", "lens")}
+
+
+# ---------------------------------------------------------------- 64 bits, from the definitions
+def exact(case, seed):
+    """What `run` returns, one row and head, or one request, at a time.  Places, pages and moves have no such value."""
+    op = case["op"]
+    if op in ("batch", "reorder"):
+        return None
+    s = _inputs(case, seed)
+    if op == "select":
+        scores = torch.full((case["batch"], case["keep"]), -math.inf, dtype=torch.float64, device="cuda")
+        w = case["beams"]
+        for b in range(case["batch"]):
+            x = s["logits"][b * w:(b + 1) * w].double()
+            if case["softcap"]:
+                x = torch.tanh(x / case["softcap"]) * case["softcap"]
+            x = torch.log_softmax(x, 1) + s["scores"][b].double()[:, None]
+            for i in range(w):
+                if s["done"][b * w + i]:
+                    x[i] = -math.inf
+                    x[i, 2] = s["scores"][b, i].double()
+            best = x.reshape(-1).topk(min(case["keep"], x.numel())).values
+            scores[b, :len(best)] = best
+        return {"scores": scores, "tokens": None, "parents": None, "done": None}
+    group, page, dim, kind = case["heads"] // case["kv_heads"], case["page"], case["dim"], case["type"]
+    lens, starts = s["lens"].tolist(), s["starts"].tolist()
+    out = torch.zeros(s["q"].shape, dtype=torch.float64, device="cuda")
+    lse = torch.zeros(s["q"].shape[:2], dtype=torch.float64, device="cuda")
+    for i, n in enumerate(lens):
+        a, b = starts[i], starts[i + 1]
+        ids = s["table"][i, :-(-n // page)].long()
+        t = torch.arange(n, device="cuda")
+        place = (n - (b - a) + torch.arange(b - a, device="cuda"))[:, None]
+        hidden = t[None, :] > place
+        if case["window"]:
+            hidden |= (t[None, :] <= place - case["window"]) & (t[None, :] >= case["sinks"])
+        for h in range(case["kv_heads"]):
+            k = _values(s["k"][0, ids, h], kind).double() * s["scale"][0, ids, h, 0].double()[:, None, None]
+            v = _values(s["v"][0, ids, h].transpose(1, 2).contiguous(), kind).double() * s["scale"][0, ids, h, 1].double()[:, None, None]
+            k, v = k.reshape(-1, k.shape[-1])[:n, :dim], v.reshape(-1, v.shape[-1])[:n, :dim]
+            x = s["q"][a:b, h * group:(h + 1) * group].double().transpose(0, 1)
+            logit = x @ k.T / math.sqrt(dim)
+            if case["softcap"]:
+                logit = case["softcap"] * torch.tanh(logit / case["softcap"])
+            logit = logit.masked_fill(hidden[None], -math.inf)
+            total = torch.logsumexp(logit, -1, keepdim=True)
+            lse[a:b, h * group:(h + 1) * group] = total[..., 0].T
+            out[a:b, h * group:(h + 1) * group] = (torch.exp(logit - total).nan_to_num(0.0) @ v).transpose(0, 1)
+    return {"out": out, "lse": lse}
