@@ -90,7 +90,8 @@ def draw(rng):
         wider = max(1, kv_heads * dim // 1024)
         own_ = _log(rng, 1, 1024 // wider)
         new = 1 if rng.random() < 0.7 else min(own_, _log(rng, 2, 8))
-        prefix = _log(rng, 16, min(100003, (150000 // wider - groups * rows * own_ // 2) // groups, 24000000 // (groups * rows * new * wider)))
+        most = (150000 // wider - groups * rows * own_ // 2) // groups
+        prefix = _log(rng, 16, min(100003, most, 24000000 // (groups * rows * new * wider)))
         return {"op": op, "groups": groups, "rows": rows, "prefix": prefix, "own": own_, "new": new, "heads": kv_heads * group,
                 "kv_heads": kv_heads, "dim": dim, "page": rng.choice([16, 32, 64, 128]), "type": rng.choice(["e4m3", "int8"]),
                 "window": rng.choice([0, 0, _log(rng, 1, 8192)]), "sinks": rng.choice([0, 4]),
@@ -110,7 +111,8 @@ def draw(rng):
     layers, kv_heads, dim, page = _log(rng, 1, 42), rng.choice([1, 2, 4, 8]), rng.choice([64, 96, 128, 256]), rng.choice([16, 32, 64])
     batch, beams, context = _log(rng, 1, 64), _log(rng, 1, 8), _log(rng, 1, 1500)
     own_ = _log(rng, 1, 61)
-    while layers * kv_heads * _wide(dim) * batch * (context + beams * (own_ + 2 * page)) > 12 * 8 * 128 * 64 * (1500 + 8 * 93):
+    size = lambda: layers * kv_heads * _wide(dim) * batch    # noqa: E731
+    while size() * (context + beams * (own_ + 2 * page)) > 12 * 8 * 128 * 64 * (1500 + 8 * 93) or size() * beams * page > 12 * 8 * 128 * 64 * 8 * 16:
         layers, batch = max(1, layers // 2), max(1, batch - batch // 4)
         if layers == batch == 1:
             context = max(1, context // 2)
@@ -387,7 +389,8 @@ def _batch_plain(s, case):
     lens = s["lens"][rows]
     col = torch.arange(-(-s["longest"] // page), device="cuda")[None, :]
     table = torch.where(col * page < lens[:, None], s["table"][rows][:, :col.shape[1]], -1)
-    lead = s["groups"][torch.searchsorted(s["groups"][1:].contiguous(), torch.arange(len(rows), device="cuda", dtype=torch.int32), right=True)]
+    i = torch.arange(len(rows), dtype=torch.int32, device="cuda")
+    lead = s["groups"][torch.searchsorted(s["groups"][1:].contiguous(), i, right=True)]
     same = ((table == table[lead.long()]) & (table >= 0)).int().cumprod(1).sum(1) * page
     same = torch.minimum(same, lens) // 64 * 64
     shared = torch.full_like(lens, 1 << 30).scatter_reduce(0, lead.long(), same.int(), "amin")[lead.long()]
