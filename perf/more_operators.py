@@ -409,7 +409,7 @@ def _select_plain(s, case):
     token = (1 << 32) - 1 - (key.topk(n, 1).values & 0xFFFFFFFF)
     y = x.double()
     if case["softcap"]:
-        y = case["softcap"] * torch.tanh(y / case["softcap"])
+        y = torch.where(x.isinf(), y, case["softcap"] * torch.tanh(y / case["softcap"]))      # what is masked stays so
     top = y.amax(1, keepdim=True)
     lse = top + torch.exp((y - top).float()).sum(1, keepdim=True, dtype=torch.float64).log()
     score = s["scores"].double().reshape(-1, 1) + y.gather(1, token) - lse
@@ -487,7 +487,7 @@ def exact(case, seed):
         for b in range(case["batch"]):
             x = s["logits"][b * w:(b + 1) * w].double()
             if case["softcap"]:
-                x = torch.tanh(x / case["softcap"]) * case["softcap"]
+                x = (torch.tanh(x / case["softcap"]) * case["softcap"]).masked_fill(x == -math.inf, -math.inf)
             x = torch.log_softmax(x, 1) + s["scores"][b].double()[:, None]
             for i in range(w):
                 if s["done"][b * w + i]:
