@@ -760,6 +760,48 @@ bs_status bs_kv_attend_async(const bs_kv_cache* cache, const bs_kv_attend_args* 
                              void* stream);
 uint64_t bs_kv_attend_work_bytes(const bs_kv_cache* cache, const bs_kv_attend_args* args);
 
+/* ------------------------------------------- continuations of many beams
+ *
+ * Of all continuations of a request's beams, a beam's score plus the log
+ * probability of one more token, the best `keep`: by score, of equal ones the
+ * lowest beam, then the lowest token.
+ *
+ *   score_w + y_wv - log sum_v exp(y_wv),  y = logit, or softcap tanh(logit / softcap)
+ *
+ * A beam's tokens are ordered by their logits.  A logit of -infinity is a
+ * token that is not allowed (under a soft cap, too).  A beam whose score is
+ * not finite, or whose logits hold a NaN or +infinity, has no continuations;
+ * its logits are not read in the first case.  A beam that is done has one, the
+ * token eos at its own score, and its logits are not read.  Where there are
+ * too few, the score is -infinity, token and parent are -1 and done is 0.
+ * Scores are computed in 64 bits and rounded once (the exponentials of a sum
+ * in 32, the sum's error is 2^-20 or less). */
+typedef struct {
+    uint32_t batch, beams;      /* requests, and beams of each (1..64); batch * beams up to 65535 */
+    uint32_t keep;              /* continuations of a request, 1..128 */
+    uint32_t vocab;             /* 1..2^20 */
+    uint32_t type;              /* BS_T_BF16 or BS_T_FP32 */
+    int32_t eos;                /* the token that ends a beam, negative: none */
+    float softcap;              /* 0 or infinity: none */
+    uint32_t reserved;          /* 0 */
+    uint64_t row_stride;        /* elements between rows of logits */
+    const void* d_logits;       /* [batch * beams][vocab], any alignment of its type's */
+    const float* d_scores;      /* [batch * beams] */
+    const int32_t* d_done;      /* NULL, or [batch * beams]: not 0 where the beam is done (eos is then given) */
+    float* d_scores_out;        /* all four [batch][keep], best first */
+    int32_t* d_tokens;
+    int32_t* d_parents;         /* the beam's row of the logits */
+    int32_t* d_done_out;        /* 1 where the token is eos or the beam was done */
+} bs_beam_args;
+
+/* Two kernel launches on `stream`, no allocation, the same result on every
+ * run.  d_work: bs_beam_work_bytes (0: arguments that are refused; pointers
+ * are not looked at), 16-B aligned; calls that share it must not overlap.
+ * Results overlap neither the inputs, the workspace nor each other.  Errors:
+ * BS_E_INVAL, BS_E_HIP. */
+uint64_t bs_beam_work_bytes(const bs_beam_args* args);
+bs_status bs_beam_select_async(const bs_beam_args* args, void* d_work, uint64_t work_bytes, void* stream);
+
 /* ------------------------------------------------------- layer streaming
  *
  * Layers streamed on demand under a budget of device memory [Gemma 2 9B

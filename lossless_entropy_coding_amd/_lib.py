@@ -118,6 +118,13 @@ class KvAttendArgs(C.Structure):
                 ("sinks", C.c_uint32)]
 
 
+class BeamArgs(C.Structure):
+    _fields_ = [("batch", C.c_uint32), ("beams", C.c_uint32), ("keep", C.c_uint32), ("vocab", C.c_uint32), ("type", C.c_uint32),
+                ("eos", C.c_int32), ("softcap", C.c_float), ("reserved", C.c_uint32), ("row_stride", C.c_uint64),
+                ("d_logits", C.c_void_p), ("d_scores", C.c_void_p), ("d_done", C.c_void_p), ("d_scores_out", C.c_void_p),
+                ("d_tokens", C.c_void_p), ("d_parents", C.c_void_p), ("d_done_out", C.c_void_p)]
+
+
 # every symbol declared in include/bs.h, with (restype, argtypes)
 SIGNATURES = {
     "bs_params_default": (None, [C.POINTER(Params)]),
@@ -193,6 +200,8 @@ SIGNATURES = {
                                      C.c_uint32, C.c_void_p, C.c_uint64, C.c_void_p, C.c_uint64, C.c_uint32, C.c_void_p]),
     "bs_kv_attend_async": (C.c_int, [C.POINTER(KvCache), C.POINTER(KvAttendArgs), C.c_void_p, C.c_uint64, C.c_void_p]),
     "bs_kv_attend_work_bytes": (C.c_uint64, [C.POINTER(KvCache), C.POINTER(KvAttendArgs)]),
+    "bs_beam_work_bytes": (C.c_uint64, [C.POINTER(BeamArgs)]),
+    "bs_beam_select_async": (C.c_int, [C.POINTER(BeamArgs), C.c_void_p, C.c_uint64, C.c_void_p]),
     "bs_plan_waves_per_block": (C.c_uint32, [C.c_void_p]),
     "bs_plan_packs": (C.c_uint32, [C.c_void_p, C.c_uint32, C.c_uint32]),
     "bs_verify": (C.c_int, [C.c_void_p, C.c_uint32, C.c_uint32, C.c_void_p, C.c_void_p, C.c_void_p, C.c_uint32,

@@ -234,3 +234,57 @@ def lora(y, x, of, adapters):
         rounds = x.shape[1] + 64 + 3 * 128 + 16
         loose[t] += rounds * 2.0 ** -24 * abs(s) * (np.abs(B) @ mag)
     return out, 2 * loose
+
+
+def select(logits, scores, beams, keep, done=None, eos=-1, softcap=0.0):
+    """(scores, tokens, parents, done, gaps, loose) of the best continuations:
+    logits (batch * beams, vocab) float64, scores (batch * beams).  gaps: how
+    far each kept score is from the next one of its request (0: a tie); loose:
+    the most that fp32 exponentials and sums can move a score.
+
+    A term exp(t), t <= 0, is off by 2^-24 (2 |t| + 2) of itself: t and its
+    product with log2 e are rounded, the exponential is right to one step.  A
+    thread adds up to 64 terms one by one, then come 14 more additions, and the
+    score is rounded to fp32.  Under a soft cap c of up to 256 the capped logit
+    is off by 2^-21 c, above by 2^-19 of itself."""
+    rows, vocab = logits.shape
+    batch = rows // beams
+    out = np.full((batch, keep), -np.inf), np.full((batch, keep), -1, np.int32), np.full((batch, keep), -1, np.int32), \
+        np.zeros((batch, keep), np.int32)
+    gaps, loose = np.full((batch, keep), np.inf), np.zeros(batch)
+    for b in range(batch):
+        all_, token, parent = [np.zeros(0)], [np.zeros(0, np.int64)], [np.zeros(0, np.int64)]
+        for w in range(b * beams, (b + 1) * beams):
+            s = float(scores[w])
+            if not math.isfinite(s):
+                continue
+            if done is not None and done[w]:
+                all_.append(np.array([s]))
+                token.append(np.array([eos]))
+                parent.append(np.array([w]))
+                continue
+            x = logits[w]
+            ok = x > -np.inf
+            if np.isnan(x).any() or (x == np.inf).any() or not ok.any():
+                continue
+            y = softcap * np.tanh(x[ok] / softcap) if softcap else x[ok]
+            top = y.max()
+            p = np.exp(y - top)
+            lse = top + math.log(p.sum())
+            off = 2.0 ** -24 * (2 * float(p @ (top - y)) / p.sum() + 80)
+            if softcap:
+                off += softcap * 2.0 ** -21 if softcap <= 256 else float(np.abs(y).max()) * 2.0 ** -19
+            loose[b] = max(loose[b], off)
+            # the order within a beam is the logits' own, ties to the lowest token
+            at = np.argsort(-x[ok], kind="stable")[:keep + 1]
+            all_.append(s + y[at] - lse)
+            token.append(np.flatnonzero(ok)[at])
+            parent.append(np.full(len(at), w))
+        all_, token, parent = np.concatenate(all_), np.concatenate(token), np.concatenate(parent)
+        at = np.argsort(-all_, kind="stable")
+        n = min(keep, len(at))
+        out[0][b, :n], out[1][b, :n], out[2][b, :n] = all_[at[:n]], token[at[:n]], parent[at[:n]]
+        out[3][b, :n] = [int(t == eos or (done is not None and done[p] != 0)) for t, p in zip(token[at[:n]], parent[at[:n]])]
+        m = max(0, min(n, len(at) - 1))
+        gaps[b, :m] = all_[at[:m]] - all_[at[1:m + 1]]
+    return *out, gaps, loose
