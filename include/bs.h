@@ -714,6 +714,65 @@ bs_status bs_kv_compact_async(const bs_kv_cache* cache, int32_t* d_table_out, in
 /* Workspace of the calls above for n rows or pairs (0: a shape they refuse). */
 uint64_t bs_kv_pages_work_bytes(const bs_kv_cache* cache, uint32_t n);
 
+/* Rows d_rows[i] (distinct) take the tokens of rows d_rows[d_parents[i]], all
+ * at once; -1: the row becomes empty.  n is at most 4096.  Whole pages are
+ * shared.  A last, partly filled page stays with one child, the parent's own
+ * row if it is its own child, else the first; each other child gets a copy, in
+ * every layer, on the lowest page that was free before the call, in the order
+ * of the list.  Pages that no row holds any more are free after the call.
+ * Entries of the table past a row's pages keep what they held.  All or none,
+ * as for bs_kv_extend_async.  Two kernel launches; d_work:
+ * bs_kv_reorder_work_bytes(cache, n) (0: a shape that is refused), 16-B
+ * aligned. */
+bs_status bs_kv_reorder_async(const bs_kv_cache* cache, uint32_t n, const int32_t* d_rows, const int32_t* d_parents,
+                              void* d_work, uint64_t work_bytes, void* stream);
+uint64_t bs_kv_reorder_work_bytes(const bs_kv_cache* cache, uint32_t n);
+
+/* The plan of a step's tokens: made once a step, after the rows have grown,
+ * it serves every layer, and holds until rows are extended, forked, freed,
+ * reordered or compacted.  Row i of n_seqs has count[i] new tokens, its last
+ * ones; the rows' tokens follow each other.  Groups are runs of rows, from
+ * d_groups[g] to d_groups[g + 1] - 1, whose first tokens are (or may be) on
+ * the same pages.  All buffers are the caller's, written by
+ * bs_kv_batch_async:
+ *   d_rows   [n_seqs]      the rows
+ *   d_starts [n_seqs + 1]  offsets of the rows' tokens (as d_starts of
+ *                          bs_kv_append_async and bs_kv_attend_async)
+ *   d_places [total]       each token's place in its row, -1: it has none
+ *   d_slots  [total]       its slot of the pool, page * page_tokens + the place
+ *                          in the page, -1: it has none
+ *   d_table  [n_seqs][width]  the rows' pages, -1 past them
+ *   d_lead   [n_seqs]      the first row (0..n_seqs - 1) of the row's group, i
+ *                          itself for a row of no group
+ *   d_shared [n_seqs]      how many leading tokens all rows of the group have on
+ *                          the same pages, rounded down to a multiple of 64
+ *   d_info   [n_groups + 1][4]  for bs_kv_attend_shared_async; 16-B aligned, its
+ *                          first word is 0 before the first call and between calls
+ * A row that does not exist, a count that is negative, above max_new or the
+ * row's length, counts that do not add up to total, offsets of groups that do
+ * not ascend: flagged (BS_KV_BAD_ID); tokens without a place or page get -1. */
+typedef struct {
+    uint32_t n_seqs;            /* up to 16384 */
+    uint32_t n_groups;          /* up to 16384 */
+    uint32_t total, max_new;    /* tokens in all, and the most of one row */
+    uint32_t width;             /* columns of d_table; 0: none */
+    uint32_t reserved;          /* 0 */
+    int32_t* d_rows;
+    int32_t* d_starts;
+    int32_t* d_places;
+    int64_t* d_slots;
+    int32_t* d_table;
+    int32_t* d_lead;
+    int32_t* d_shared;
+    int32_t* d_info;
+} bs_kv_batch;
+
+/* Make the plan from d_seqs [n_seqs] (a row may be named more than once),
+ * d_counts [n_seqs] (NULL: one token each) and d_groups [n_groups + 1] (NULL:
+ * one group of all rows, n_groups 1).  One kernel launch. */
+bs_status bs_kv_batch_async(const bs_kv_cache* cache, const bs_kv_batch* batch, const int32_t* d_seqs,
+                            const int32_t* d_counts, const int32_t* d_groups, void* stream);
+
 /* Store the keys and values of the last tokens of rows d_seqs[i] (distinct,
  * already extended) in layer `layer`: tokens d_starts[i] .. d_starts[i + 1] -
  * 1 of the input are the last ones of row d_seqs[i] (d_starts NULL: one token

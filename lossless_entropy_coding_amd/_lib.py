@@ -118,6 +118,13 @@ class KvAttendArgs(C.Structure):
                 ("sinks", C.c_uint32)]
 
 
+class KvBatch(C.Structure):
+    _fields_ = [("n_seqs", C.c_uint32), ("n_groups", C.c_uint32), ("total", C.c_uint32), ("max_new", C.c_uint32),
+                ("width", C.c_uint32), ("reserved", C.c_uint32), ("d_rows", C.c_void_p), ("d_starts", C.c_void_p),
+                ("d_places", C.c_void_p), ("d_slots", C.c_void_p), ("d_table", C.c_void_p), ("d_lead", C.c_void_p),
+                ("d_shared", C.c_void_p), ("d_info", C.c_void_p)]
+
+
 class BeamArgs(C.Structure):
     _fields_ = [("batch", C.c_uint32), ("beams", C.c_uint32), ("keep", C.c_uint32), ("vocab", C.c_uint32), ("type", C.c_uint32),
                 ("eos", C.c_int32), ("softcap", C.c_float), ("reserved", C.c_uint32), ("row_stride", C.c_uint64),
@@ -202,6 +209,9 @@ SIGNATURES = {
     "bs_kv_attend_work_bytes": (C.c_uint64, [C.POINTER(KvCache), C.POINTER(KvAttendArgs)]),
     "bs_beam_work_bytes": (C.c_uint64, [C.POINTER(BeamArgs)]),
     "bs_beam_select_async": (C.c_int, [C.POINTER(BeamArgs), C.c_void_p, C.c_uint64, C.c_void_p]),
+    "bs_kv_reorder_async": (C.c_int, [C.POINTER(KvCache), C.c_uint32, C.c_void_p, C.c_void_p, C.c_void_p, C.c_uint64, C.c_void_p]),
+    "bs_kv_reorder_work_bytes": (C.c_uint64, [C.POINTER(KvCache), C.c_uint32]),
+    "bs_kv_batch_async": (C.c_int, [C.POINTER(KvCache), C.POINTER(KvBatch), C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p]),
     "bs_plan_waves_per_block": (C.c_uint32, [C.c_void_p]),
     "bs_plan_packs": (C.c_uint32, [C.c_void_p, C.c_uint32, C.c_uint32]),
     "bs_verify": (C.c_int, [C.c_void_p, C.c_uint32, C.c_uint32, C.c_void_p, C.c_void_p, C.c_void_p, C.c_uint32,

@@ -14,6 +14,7 @@ using namespace bs;
 namespace {
 
 constexpr uint64_t kGridYZ = 65535, kThreads = 0xFFFFFFFFull;   // workgroups of a grid's y and z, threads of its x
+constexpr uint32_t kBatchRows = 16384;       // of a plan, whose every workgroup adds up the counts before its own
 
 bs_status launched(int e, const char* what) {
     if (e == 0) return BS_OK;
@@ -197,6 +198,34 @@ bs_status page_call(const bs_kv_cache* cache, uint32_t n, const void* a, bool tw
     return BS_OK;
 }
 
+uint64_t reorder_work(const bsd::KvView& v, uint64_t n) { return align_up(4 * (2 + 6 * n + v.max_seqs), 256); }
+
+// a plan's sizes and buffers
+bs_status check_batch(const bs_kv_batch* b) {
+    if (!b) { set_error("NULL plan"); return BS_E_INVAL; }
+    if (b->n_seqs > kBatchRows || b->n_groups > kBatchRows) {
+        set_error("%u rows in %u groups (at most %u)", b->n_seqs, b->n_groups, kBatchRows);
+        return BS_E_INVAL;
+    }
+    if (b->total > 0x7FFFFFFFu || (b->n_seqs == 0 && b->total) || (b->total && (b->max_new == 0 || b->max_new > b->total))) {
+        set_error("%u tokens of %u rows, at most %u of one", b->total, b->n_seqs, b->max_new);
+        return BS_E_INVAL;
+    }
+    if (b->reserved) { set_error("reserved must be 0"); return BS_E_INVAL; }
+    if (b->n_seqs == 0) return BS_OK;
+    if (!b->d_rows || !b->d_starts || (b->total && (!b->d_places || !b->d_slots)) || (b->width && !b->d_table) || !b->d_lead || !b->d_shared ||
+        !b->d_info) {
+        set_error("NULL buffer in the plan");
+        return BS_E_INVAL;
+    }
+    if (!aligned(b->d_rows, 4) || !aligned(b->d_starts, 4) || !aligned(b->d_places, 4) || !aligned(b->d_slots, 8) || !aligned(b->d_table, 4) ||
+        !aligned(b->d_lead, 4) || !aligned(b->d_shared, 4) || !aligned(b->d_info, 16)) {
+        set_error("a misaligned buffer in the plan");
+        return BS_E_INVAL;
+    }
+    return BS_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -359,6 +388,71 @@ bs_status bs_kv_compact_async(const bs_kv_cache* cache, int32_t* d_table_out, in
     p.table_out = d_table_out;
     p.refs_out = d_refs_out;
     return launched(bsk_kv_compact(&p, stream), "compact");
+}
+
+uint64_t bs_kv_reorder_work_bytes(const bs_kv_cache* cache, uint32_t n) {
+    bsd::KvView v;
+    if (view(cache, v) != BS_OK || n > bsd::kKvReorder) return 0;
+    return reorder_work(v, n);
+}
+
+bs_status bs_kv_reorder_async(const bs_kv_cache* cache, uint32_t n, const int32_t* d_rows, const int32_t* d_parents,
+                              void* d_work, uint64_t work_bytes, void* stream) {
+    bsd::KvPages p;
+    memset(&p, 0, sizeof p);
+    const bs_status rc = view(cache, p.c);
+    if (rc != BS_OK) return rc;
+    if (n > bsd::kKvReorder) { set_error("%u rows in one call (at most %u)", n, bsd::kKvReorder); return BS_E_INVAL; }
+    if (n == 0) return BS_OK;
+    if (!d_rows || !d_parents || !aligned(d_rows, 4) || !aligned(d_parents, 4)) { set_error("NULL or misaligned rows or parents"); return BS_E_INVAL; }
+    if (!d_work || !aligned(d_work, 16)) { set_error("a 16-B aligned workspace is needed"); return BS_E_INVAL; }
+    if (work_bytes < reorder_work(p.c, n)) {
+        set_error("workspace of %llu B, %llu B needed", (unsigned long long)work_bytes, (unsigned long long)reorder_work(p.c, n));
+        return BS_E_INVAL;
+    }
+    if (overlap(d_work, reorder_work(p.c, n), d_rows, 4ull * n) || overlap(d_work, reorder_work(p.c, n), d_parents, 4ull * n)) {
+        set_error("the workspace overlaps rows or parents");
+        return BS_E_INVAL;
+    }
+    p.n = n;
+    p.a = d_rows;
+    p.b = d_parents;
+    p.work = (int32_t*)d_work;
+    return launched(bsk_kv_reorder(&p, stream), "reorder");
+}
+
+bs_status bs_kv_batch_async(const bs_kv_cache* cache, const bs_kv_batch* batch, const int32_t* d_seqs,
+                            const int32_t* d_counts, const int32_t* d_groups, void* stream) {
+    bsd::KvBatch b;
+    memset(&b, 0, sizeof b);
+    const bs_status rc = view(cache, b.c);
+    if (rc != BS_OK) return rc;
+    const bs_status at = check_batch(batch);
+    if (at != BS_OK) return at;
+    if (batch->n_seqs == 0) return BS_OK;
+    if (!d_seqs || !aligned(d_seqs, 4) || !aligned(d_counts, 4) || !aligned(d_groups, 4)) { set_error("NULL or misaligned rows, counts or groups"); return BS_E_INVAL; }
+    if (!d_counts && batch->total != batch->n_seqs) {
+        set_error("%u tokens for %u rows without counts", batch->total, batch->n_seqs);
+        return BS_E_INVAL;
+    }
+    if (!d_groups && batch->n_groups != 1) { set_error("%u groups without their offsets", batch->n_groups); return BS_E_INVAL; }
+    b.n = batch->n_seqs;
+    b.groups = batch->n_groups;
+    b.total = batch->total;
+    b.max_new = batch->max_new;
+    b.width = batch->width;
+    b.seqs = d_seqs;
+    b.counts = d_counts;
+    b.offs = d_groups;
+    b.rows = batch->d_rows;
+    b.starts = batch->d_starts;
+    b.places = batch->d_places;
+    b.slots = batch->d_slots;
+    b.table = batch->d_table;
+    b.lead = batch->d_lead;
+    b.shared = batch->d_shared;
+    b.info = batch->d_info;
+    return launched(bsk_kv_batch(&b, stream), "batch");
 }
 
 }  // extern "C"

@@ -726,6 +726,161 @@ __global__ __launch_bounds__(256) void compact_table_kernel(KvPages p, uint32_t 
     }
 }
 
+// ---------------------------------------------------------------- reorder
+// Rows a[i] take the tokens of rows a[b[i]] (b[i] = -1: none), all at once.
+// work: [0] 1 if the call goes through, [1] copies, then for each i the row's
+// length before and after, the page of its own copy (-1: none), then the
+// copies' sources and targets, the free pages found, and for each row of the
+// cache who names it.
+struct Reorder {
+    int32_t *before, *after, *own, *from, *to, *list, *who;
+    __device__ __forceinline__ explicit Reorder(const KvPages& p) {
+        before = p.work + 2;
+        after = before + p.n;
+        own = after + p.n;
+        from = own + p.n;
+        to = from + p.n;
+        list = to + p.n;
+        who = list + p.n;
+    }
+};
+
+// One workgroup: checks, lengths, and which children get a page of their own.
+// A parent's partly filled page goes to the parent's own row, if that is one
+// of its children, else to its first child; the others copy it.
+__global__ __launch_bounds__(kScan) void reorder_plan_kernel(KvPages p) {
+    const KvView& c = p.c;
+    __shared__ uint32_t sums[kScan / 64];
+    __shared__ uint32_t bad;
+    __shared__ int32_t heir[kKvReorder];
+    const uint32_t t = threadIdx.x;
+    const Reorder w(p);
+    if (t == 0) bad = 0;
+    for (uint32_t i = t; i < p.n; i += kScan) {
+        const int32_t r = p.a[i];
+        heir[i] = 0x7FFFFFFF;
+        if (r >= 0 && (uint32_t)r < c.max_seqs) w.who[r] = (int32_t)i;
+    }
+    __syncthreads();
+    for (uint32_t i = t; i < p.n; i += kScan) {
+        const int32_t r = p.a[i], q = p.b[i];
+        uint32_t err = 0;
+        int32_t had = 0;
+        if (r < 0 || (uint32_t)r >= c.max_seqs || q < -1 || q >= (int32_t)p.n) {
+            err = kStId;
+        } else {
+            if (w.who[r] != (int32_t)i) err = kStId;             // named twice
+            had = max(c.lens[r], 0);
+            if ((uint64_t)(uint32_t)had > (uint64_t)c.max_pages << c.lp) err |= kStRow;
+            if (q >= 0) atomicMin(heir + q, q == (int32_t)i ? -1 : (int32_t)i);
+        }
+        w.before[i] = had;
+        if (err) atomicOr(&bad, err);
+    }
+    __syncthreads();
+    uint32_t total = 0;
+    if (bad == 0) {                                              // the same in every thread
+        for (uint32_t base = 0; base < p.n; base += kScan) {
+            const uint32_t i = base + t;
+            uint32_t need = 0;
+            int32_t len = 0, src = -1;
+            if (i < p.n) {
+                const int32_t q = p.b[i];
+                if (q >= 0) {
+                    len = w.before[q];
+                    if (((uint32_t)len & (c.page - 1)) && q != (int32_t)i && heir[q] != (int32_t)i) {
+                        need = 1;
+                        src = c.table[(uint64_t)(uint32_t)p.a[q] * c.max_pages + ((uint32_t)len >> c.lp)];
+                    }
+                }
+            }
+            uint32_t sum;
+            const uint32_t at = total + block_prefix(need, sums, sum);
+            if (i < p.n) {
+                w.after[i] = len;
+                w.own[i] = need ? (int32_t)at : -1;
+                if (need) w.from[at] = src;
+            }
+            if (need && (src < 0 || (uint32_t)src >= c.n_pages)) atomicOr(&bad, (uint32_t)kStId);
+            total += sum;
+        }
+    }
+    __syncthreads();
+    const bool early = bad != 0;
+    const uint32_t got = early ? 0 : find_free(c, total, w.list, sums);
+    __syncthreads();
+    const bool ok = !early && got == total;
+    if (t == 0) {
+        p.work[0] = ok;
+        p.work[1] = (int32_t)total;
+        if (!ok) flag(c.status, early ? bad : (uint32_t)kStPages);
+    }
+    if (!ok) return;
+    for (uint32_t i = t; i < p.n; i += kScan) {
+        const int32_t at = w.own[i];
+        if (at >= 0) {
+            w.own[i] = w.list[at];
+            w.to[at] = w.list[at];
+        }
+        c.lens[p.a[i]] = w.after[i];
+    }
+}
+
+// The first `tables` workgroups move the rows of the table, 2^lc columns of
+// all rows each: a column of a row depends on no other column, so its old
+// entries go to LDS first and nothing is overwritten too early.  Pages' counts
+// change where an entry does: the rows of a beam search have most in common.
+// The other workgroups copy pages.
+__global__ __launch_bounds__(256) void reorder_move_kernel(KvPages p, uint32_t tables, uint32_t lc, uint32_t parts) {
+    const KvView& c = p.c;
+    __shared__ int32_t entry[kKvReorder];
+    if (!p.work[0]) return;
+    const Reorder w(p);
+    const uint32_t t = threadIdx.x;
+    if (blockIdx.x >= tables) {
+        const uint32_t step = gridDim.x - tables, each = c.layers * parts, tasks = (uint32_t)p.work[1] * each;
+        for (uint32_t x = blockIdx.x - tables; x < tasks; x += step) {
+            const uint32_t k = x / each, l = x % each;
+            copy_page(c, l / parts, (uint32_t)w.from[k], (uint32_t)w.to[k], l % parts, parts);
+        }
+        return;
+    }
+    constexpr int32_t kNone = -0x7FFFFFFF - 1;                   // no entry of a row
+    const uint32_t c0 = blockIdx.x << lc, many = p.n << lc;
+    int any = 0;
+    for (uint32_t i = t; i < p.n; i += 256) any |= pages_of(c, (uint32_t)max(w.before[i], w.after[i])) > c0;
+    if (!__syncthreads_or(any)) return;
+    for (uint32_t x = t; x < many; x += 256) {
+        const uint32_t i = x >> lc, col = c0 + (x & ((1u << lc) - 1));
+        entry[x] = col < pages_of(c, (uint32_t)w.before[i]) ? c.table[(uint64_t)(uint32_t)p.a[i] * c.max_pages + col] : kNone;
+    }
+    __syncthreads();
+    for (uint32_t x = t; x < many; x += 256) {
+        const uint32_t i = x >> lc, in = x & ((1u << lc) - 1), col = c0 + in;
+        const int32_t q = p.b[i], had = entry[x];
+        const uint32_t len = (uint32_t)w.after[i];
+        int32_t now = kNone;
+        if (q >= 0 && col < pages_of(c, len)) {
+            const int32_t own = w.own[i];
+            now = own >= 0 && col == len >> c.lp ? own : entry[((uint32_t)q << lc) + in];
+        }
+        if (now == had) continue;
+        if (had != kNone) {
+            if (had < 0 || (uint32_t)had >= c.n_pages) {
+                flag(c.status, kStId);
+            } else if (atomicSub(c.refs + had, 1) <= 0) {
+                atomicAdd(c.refs + had, 1);
+                flag(c.status, kStCount);
+            }
+        }
+        if (now != kNone) {
+            if (now < 0 || (uint32_t)now >= c.n_pages) flag(c.status, kStId);
+            else atomicAdd(c.refs + now, 1);
+            c.table[(uint64_t)(uint32_t)p.a[i] * c.max_pages + col] = now;
+        }
+    }
+}
+
 // workgroups per page and layer: 16 B per thread and side, at most 8 of them
 uint32_t copy_parts(const KvView& c) {
     return (uint32_t)std::max<uint64_t>(1, std::min<uint64_t>(8, c.side_bytes / 16 / 256));
@@ -780,5 +935,16 @@ extern "C" int bsk_kv_compact(const KvPages* p, void* stream) {
     const uint32_t most = std::min<uint32_t>((p->c.n_pages + 1) / 2, 1024);
     hipLaunchKernelGGL(compact_move_kernel, dim3(p->c.layers * parts + 1, most), dim3(256), 0, st, *p, blocks, parts);
     hipLaunchKernelGGL(compact_table_kernel, dim3(p->c.max_seqs), dim3(256), 0, st, *p, blocks);
+    return (int)hipGetLastError();
+}
+
+extern "C" int bsk_kv_reorder(const KvPages* p, void* stream) {
+    hipStream_t st = (hipStream_t)stream;
+    hipLaunchKernelGGL(reorder_plan_kernel, dim3(1), dim3(kScan), 0, st, *p);
+    uint32_t lc = 0;
+    while (lc < 8 && p->n << (lc + 1) <= kKvReorder) lc++;
+    const uint32_t tables = (p->c.max_pages + (1u << lc) - 1) >> lc, parts = copy_parts(p->c);
+    const uint32_t copies = (uint32_t)std::min<uint64_t>((uint64_t)p->n * p->c.layers * parts, 8192);
+    hipLaunchKernelGGL(reorder_move_kernel, dim3(tables + copies), dim3(256), 0, st, *p, tables, lc, parts);
     return (int)hipGetLastError();
 }

@@ -1,0 +1,163 @@
+// bs_kv_batch.hip -- the plan of a step's tokens over the paged key/value
+// cache (gfx950): offsets, places and slots of the tokens, the rows' pages side
+// by side, and how many leading tokens the rows of a group have in common.
+//
+// One launch, some workgroups to a row: each adds up the counts before its
+// own (a few thousand at most, from the L2), so no workgroup waits for
+// another.  A row is compared with the first of its group, page by page; the
+// workgroup that ends last takes the least of each group.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "bs_kv_device.h"
+
+using namespace bsd;
+
+namespace {
+
+constexpr uint32_t kThreads = 256, kWaves = kThreads / 64;
+constexpr uint32_t kSlice = 1024;            // tokens, and columns, of a workgroup
+constexpr uint32_t kMaxParts = 64;
+
+__device__ __forceinline__ void flag(uint32_t* status, uint32_t bit) {
+    if (status) atomicOr(status, bit);
+}
+
+__device__ __forceinline__ void store_through(int32_t* p, int32_t v) {
+    __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// grid: (rows, parts)
+__global__ __launch_bounds__(kThreads) void batch_kernel(KvBatch b) {
+    const KvView& c = b.c;
+    __shared__ uint64_t sums[kWaves];
+    __shared__ uint32_t least[kWaves], last;
+    const uint32_t t = threadIdx.x, lane = t & 63u, wave = t >> 6, i = blockIdx.x, part = blockIdx.y;
+    const int32_t r = b.seqs[i];
+    const bool known = r >= 0 && (uint32_t)r < c.max_seqs;
+    const int32_t* trow = c.table + (uint64_t)(known ? (uint32_t)r : 0u) * c.max_pages;
+    const uint32_t cap = c.max_pages << c.lp;
+    const uint32_t len = known ? min((uint32_t)max(c.lens[r], 0), cap) : 0u;
+    const uint32_t held = (len + c.page - 1) >> c.lp;
+
+    // the tokens before the row's own; what is negative counts as none
+    const int32_t given = b.counts ? b.counts[i] : 1;
+    uint64_t before = i;
+    if (b.counts) {
+        uint64_t x = 0;
+        for (uint32_t j = t; j < i; j += kThreads) x += (uint32_t)max(b.counts[j], 0);
+#pragma unroll
+        for (int s = 32; s; s >>= 1) x += __shfl_xor(x, s);
+        if (lane == 0) sums[wave] = x;
+        __syncthreads();
+        before = sums[0] + sums[1] + sums[2] + sums[3];
+    }
+    const uint32_t count = (uint32_t)max(given, 0);
+    const uint32_t s0 = (uint32_t)min(before, (uint64_t)b.total), s1 = (uint32_t)min(before + count, (uint64_t)b.total);
+    uint32_t err = !known || given < 0 || count > b.max_new || count > len || before + count > b.total || (i + 1 == b.n && s1 != b.total) ? 4u : 0u;
+
+    for (uint32_t s = s0 + part * kThreads + t; s < s1; s += gridDim.y * kThreads) {
+        const int64_t place = (int64_t)len - (int64_t)count + (int64_t)(s - s0);
+        int64_t slot = -1;
+        if (place >= 0) {
+            const int32_t pg = trow[place >> c.lp];
+            if (pg >= 0 && (uint32_t)pg < c.n_pages) slot = ((int64_t)pg << c.lp) + (place & (c.page - 1));
+            else err = 4u;
+        }
+        b.places[s] = place >= 0 ? (int32_t)place : -1;
+        b.slots[s] = slot;
+    }
+    if (i + 1 == b.n)                                               // tokens of no row
+        for (uint32_t s = s1 + part * kThreads + t; s < b.total; s += gridDim.y * kThreads) {
+            b.places[s] = -1;
+            b.slots[s] = -1;
+        }
+    for (uint32_t j = part * kThreads + t; j < b.width; j += gridDim.y * kThreads)
+        b.table[(uint64_t)i * b.width + j] = j < held ? trow[j] : -1;
+    if (err) flag(c.status, err);
+    if (part != 0) return;
+
+    // the row's group: the last that begins at i or before
+    uint32_t lo = 0, hi = b.groups, first = 0;
+    bool grouped = true;
+    if (b.offs) {
+        while (lo < hi) {
+            const uint32_t mid = (lo + hi) / 2;
+            if (b.offs[mid] <= (int32_t)i) lo = mid + 1;
+            else hi = mid;
+        }
+        const int32_t f = lo ? b.offs[lo - 1] : -1;
+        grouped = lo && f >= 0 && f <= (int32_t)i && (int32_t)i < b.offs[lo];
+        first = grouped ? (uint32_t)f : i;
+    }
+    const int32_t fr = b.seqs[first];
+    uint32_t same = 0;
+    if (grouped && known && fr >= 0 && (uint32_t)fr < c.max_seqs) {
+        const int32_t* frow = c.table + (uint64_t)(uint32_t)fr * c.max_pages;
+        const uint32_t both = min(len, min((uint32_t)max(c.lens[fr], 0), cap)), pages = (both + c.page - 1) >> c.lp;
+        uint32_t stop = pages;                                      // the first page that differs
+        for (uint32_t j0 = 0; j0 < pages; j0 += 4 * kThreads) {
+            int32_t x[4], y[4];
+#pragma unroll
+            for (uint32_t u = 0; u < 4; u++) {
+                const uint32_t j = min(j0 + u * kThreads + t, pages - 1);
+                x[u] = trow[j];
+                y[u] = frow[j];
+            }
+#pragma unroll
+            for (uint32_t u = 0; u < 4; u++)
+                if (x[u] != y[u] || x[u] < 0 || (uint32_t)x[u] >= c.n_pages) stop = min(stop, min(j0 + u * kThreads + t, pages - 1));
+        }
+#pragma unroll
+        for (int s = 32; s; s >>= 1) stop = min(stop, (uint32_t)__shfl_xor((int)stop, s));
+        if (lane == 0) least[wave] = stop;
+        __syncthreads();
+        stop = min(min(least[0], least[1]), min(least[2], least[3]));
+        same = (uint32_t)min((uint64_t)both, (uint64_t)stop << c.lp) & ~(kKvTile - 1);
+    }
+    if (t == 0) {
+        b.rows[i] = r;
+        b.lead[i] = (int32_t)first;
+        store_through(b.shared + i, (int32_t)same);
+        store_through(b.starts + i, (int32_t)s0);
+        if (i + 1 == b.n) store_through(b.starts + b.n, (int32_t)s1);
+    }
+    // the last of the rows' workgroups; the counter is 0 between calls
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup");
+    __builtin_amdgcn_s_waitcnt(0);
+    __syncthreads();
+    if (t == 0) last = __hip_atomic_fetch_add((uint32_t*)b.info, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == b.n - 1;
+    __syncthreads();
+    if (!last) return;
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
+    for (uint32_t g = wave; g < b.groups; g += kWaves) {
+        const int32_t f = b.offs ? b.offs[g] : 0, e = b.offs ? b.offs[g + 1] : (int32_t)b.n;
+        const uint32_t from = (uint32_t)min(max(f, 0), (int32_t)b.n), to = (uint32_t)min(max(e, (int32_t)from), (int32_t)b.n);
+        if (((uint32_t)f != from || (uint32_t)e != to) && lane == 0) flag(c.status, 4u);
+        uint32_t few = ~0u;
+        for (uint32_t j = from + lane; j < to; j += 64) few = min(few, (uint32_t)b.shared[j]);
+#pragma unroll
+        for (int s = 32; s; s >>= 1) few = min(few, (uint32_t)__shfl_xor((int)few, s));
+        if (from == to) few = 0;
+        for (uint32_t j = from + lane; j < to; j += 64) b.shared[j] = (int32_t)few;
+        if (lane == 0) {
+            int32_t* to4 = b.info + 4 * (g + 1);
+            to4[0] = b.starts[from];
+            to4[1] = b.starts[to];
+            to4[2] = (int32_t)few;
+            to4[3] = from < to ? b.seqs[from] : -1;
+        }
+    }
+    if (t == 0) __hip_atomic_store((uint32_t*)b.info, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+}  // namespace
+
+extern "C" int bsk_kv_batch(const KvBatch* b, void* stream) {
+    const uint32_t most = std::max(std::min(b->max_new, b->total), b->width);
+    const uint32_t parts = std::min(kMaxParts, std::max(1u, (most + kSlice - 1) / kSlice));
+    hipLaunchKernelGGL(batch_kernel, dim3(b->n, parts), dim3(kThreads), 0, (hipStream_t)stream, *b);
+    return (int)hipGetLastError();
+}

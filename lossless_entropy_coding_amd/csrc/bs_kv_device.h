@@ -60,11 +60,30 @@ struct KvAttend {
     float* part;                // splits > 1: [total * heads][splits][wide + 4]: the result, its maximum and sum, 2 unused
 };
 
+// the plan of a step's tokens (bs_kv_batch of bs.h)
+struct KvBatch {
+    KvView c;
+    uint32_t n, groups, total, max_new, width;
+    const int32_t* seqs;
+    const int32_t* counts;      // null: one each
+    const int32_t* offs;        // null: one group of all rows
+    int32_t* rows;
+    int32_t* starts;
+    int32_t* places;
+    int64_t* slots;
+    int32_t* table;
+    int32_t* lead;
+    int32_t* shared;
+    int32_t* info;
+};
+
+constexpr uint32_t kKvReorder = 4096;        // rows of a reorder at most
+
 struct KvPages {
     KvView c;
     uint32_t n;                 // rows or pairs
-    const int32_t* a;           // rows (extend, free), sources (fork), source pages (copy)
-    const int32_t* b;           // counts (extend), children (fork), destination pages (copy)
+    const int32_t* a;           // rows (extend, free, reorder), sources (fork), source pages (copy)
+    const int32_t* b;           // counts (extend), children (fork), destination pages (copy), parents (reorder)
     int32_t* work;
     int32_t* table_out;         // compact
     int32_t* refs_out;
@@ -81,4 +100,6 @@ int bsk_kv_fork(const bsd::KvPages* p, void* stream);
 int bsk_kv_free(const bsd::KvPages* p, void* stream);
 int bsk_kv_copy(const bsd::KvPages* p, void* stream);
 int bsk_kv_compact(const bsd::KvPages* p, void* stream);
+int bsk_kv_reorder(const bsd::KvPages* p, void* stream);
+int bsk_kv_batch(const bsd::KvBatch* b, void* stream);
 }

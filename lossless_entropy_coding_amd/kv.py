@@ -88,7 +88,7 @@ class KvCache:
         # the argument block and the workspaces are one call's at a time: held
         # until the C call, which lets other threads run, has enqueued its work
         self._lock = threading.Lock()
-        self._page_need, self._attend_need = {}, {}        # workspace bytes by the sizes of a call
+        self._page_need, self._reorder_need, self._attend_need = {}, {}, {}        # workspace bytes by the sizes of a call
 
     def _ids(self, t: torch.Tensor, name: str) -> int:
         """Checks a vector of row numbers, counts or offsets; returns its length."""
@@ -137,6 +137,26 @@ class KvCache:
         rc = L.lib().bs_kv_free_async(self._ref, n, rows.data_ptr(), _stream_of(self.device, stream))
         if rc:
             L.check(rc, "bs_kv_free_async")
+
+    def reorder(self, rows: torch.Tensor, parents: torch.Tensor, stream=None) -> None:
+        """Rows rows[i] (distinct) take the tokens of rows[parents[i]], all at
+        once (-1: the row becomes empty); whole pages are shared
+        (bs_kv_reorder_async).  After a choice of beams, parents are its
+        Best.parents where the rows are in the order of the logits."""
+        n = self._ids(rows, "rows")
+        if self._ids(parents, "parents") != n:
+            raise ValueError("one parent per row")
+        with self._lock:
+            need = self._reorder_need.get(n)
+            if need is None:
+                need = self._reorder_need[n] = int(L.lib().bs_kv_reorder_work_bytes(self._ref, n))
+            w = self._page_work
+            if w is None or w.numel() < need:
+                w = self._page_work = _grown(w, need, self.device, stream, self._kept)
+            rc = L.lib().bs_kv_reorder_async(self._ref, n, rows.data_ptr(), parents.data_ptr(), w.data_ptr(), w.numel(),
+                                             _stream_of(self.device, stream))
+        if rc:
+            L.check(rc, "bs_kv_reorder_async")
 
     def copy_pages(self, source: torch.Tensor, target: torch.Tensor, stream=None) -> None:
         """Copy pages in every layer (bs_kv_copy_pages_async)."""
@@ -295,3 +315,61 @@ class KvCache:
         if bits:
             self.status.zero_()
             raise RuntimeError("key/value cache: " + "; ".join(v for b, v in L.KV_STATUS.items() if bits & b))
+
+
+class KvBatch:
+    """The plan of a step's tokens (bs_kv_batch), made once a step, after
+    extend, for all layers.  Row rows[i] of the cache has counts[i] new tokens
+    (without counts one each), its last ones, side by side in the step's
+    tensors; groups: offsets into rows of the runs of rows that go on from one
+    prompt (without: one group of all rows).
+
+    starts (rows + 1), places and slots (tokens; int64 slots), table (rows,
+    pages of max_len), lead and shared (rows) are int32 tensors on the device
+    as bs.h describes them, written by the call and each update().  append and
+    attend take `starts`, a rotary embedding `places`, kernels of one's own
+    `slots` and `table`, and KvCache.attend_shared all of it."""
+
+    def __init__(self, cache: KvCache, rows: torch.Tensor, counts: torch.Tensor | None = None, groups: torch.Tensor | None = None,
+                 total: int | None = None, max_new: int | None = None, max_len: int = 0, stream=None):
+        """total: tokens in all, needed with counts; max_new: the most of one
+        row, if it is known; max_len: how long the rows are at most (0: as the
+        cache allows), which decides the width of table."""
+        n = rows.numel()
+        if counts is None:
+            total, max_new = n if total is None else total, 1 if max_new is None else max_new
+        elif total is None:
+            raise ValueError("with counts the number of tokens must be given (total)")
+        if not 0 <= total < 1 << 31 or max_len < 0:
+            raise ValueError("total goes from 0 to 2^31 - 1, max_len is not negative")
+        self.cache, self.n, self.total = cache, n, total
+        self.max_new = max(1, min(total, total if max_new is None else max_new))
+        self.n_groups = 1 if groups is None else max(groups.numel() - 1, 0)
+        self.max_len = min(max_len or cache.max_pages * cache.page_tokens, cache.max_pages * cache.page_tokens)
+        width = -(-self.max_len // cache.page_tokens)
+        self._counted = counts is not None
+        sizes = [4 * (self.n_groups + 1), 2 * total, n + 1, total, n * width, n, n, n]
+        with _on(stream):        # zeroed: the plan's counter is 0 before its first call
+            info, slots, self.starts, self.places, table, self.lead, self.shared, self.rows = \
+                torch.zeros(sum(sizes), dtype=_INT32, device=cache.device).split(sizes)
+        self.slots, self.table = slots.view(torch.int64), table.view(n, width)
+        self.c = L.KvBatch(n, self.n_groups, total, self.max_new, width, 0, self.rows.data_ptr(), self.starts.data_ptr(),
+                           self.places.data_ptr(), slots.data_ptr(), table.data_ptr(), self.lead.data_ptr(),
+                           self.shared.data_ptr(), info.data_ptr())
+        self._info, self.ref = info, C.byref(self.c)
+        self.update(rows, counts, groups, stream)
+
+    def update(self, rows: torch.Tensor, counts: torch.Tensor | None = None, groups: torch.Tensor | None = None, stream=None) -> None:
+        """The plan of another step with as many rows, tokens and groups
+        (bs_kv_batch_async); the buffers stay, as a captured graph needs."""
+        cache = self.cache
+        if cache._ids(rows, "rows") != self.n:
+            raise ValueError(f"{self.n} rows")
+        if (counts is not None) != self._counted or (counts is not None and cache._ids(counts, "counts") != self.n):
+            raise ValueError("one count per row" if self._counted else "a plan made without counts has one token per row")
+        if (1 if groups is None else cache._ids(groups, "groups") - 1) != self.n_groups:
+            raise ValueError(f"offsets of {self.n_groups} groups")
+        rc = L.lib().bs_kv_batch_async(cache._ref, self.ref, rows.data_ptr(), None if counts is None else counts.data_ptr(),
+                                       None if groups is None else groups.data_ptr(), _stream_of(cache.device, stream))
+        if rc:
+            L.check(rc, "bs_kv_batch_async")

@@ -134,6 +134,57 @@ class Cache:
                 table[r, j] = to[int(self.table[r, j])]
         self.refs, self.table = refs, table
 
+    def reorder(self, rows, parents):
+        """Rows take their parents' tokens, all at once."""
+        heir = {}
+        for i, q in enumerate(parents):
+            if q >= 0 and (q not in heir or q == i):
+                heir[q] = i
+        old = [[int(x) for x in self.table[r, :self.pages(self.lens[r])]] for r in rows]
+        lens = [int(self.lens[r]) for r in rows]
+        copies = [i for i, q in enumerate(parents) if q >= 0 and lens[q] % self.page and heir[q] != i]
+        got = self._free(len(copies))
+        if got is None:
+            self.status |= 1
+            return
+        for i, (r, q) in enumerate(zip(rows, parents)):
+            new = list(old[q]) if q >= 0 else []
+            if i in copies:
+                to = got.pop(0)
+                for a in (self.k, self.v, self.scale):
+                    a[:, to] = a[:, new[-1]]
+                new[-1] = to
+            for x in new:
+                self.refs[x] += 1
+            self.table[r, :len(new)] = new
+            self.lens[r] = lens[q] if q >= 0 else 0
+        for pages in old:
+            for x in pages:
+                self.refs[x] -= 1
+
+    def batch(self, rows, counts, groups, total, width):
+        """The plan of a step's tokens: (starts, places, slots, table, lead, shared)."""
+        starts = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+        places, slots = np.full(total, -1, np.int32), np.full(total, -1, np.int64)
+        table, lead, shared = np.full((len(rows), width), -1, np.int32), np.arange(len(rows), dtype=np.int32), np.zeros(len(rows), np.int32)
+        pages = [[int(x) for x in self.table[r, :self.pages(self.lens[r])]] for r in rows]
+        for i, r in enumerate(rows):
+            table[i, :len(pages[i])] = pages[i][:width]
+            for j in range(counts[i]):
+                at = int(self.lens[r]) - counts[i] + j
+                places[starts[i] + j] = at
+                slots[starts[i] + j] = pages[i][at // self.page] * self.page + at % self.page
+        for a, b in zip(groups, groups[1:]):
+            least = 1 << 30
+            for i in range(a, b):
+                lead[i] = a
+                n = 0
+                while n < min(len(pages[i]), len(pages[a])) and pages[i][n] == pages[a][n]:
+                    n += 1
+                least = min(least, n * self.page, int(self.lens[rows[i]]))
+            shared[a:b] = least // 64 * 64
+        return starts, places, slots, table, lead, shared
+
     def append(self, layer, k, v, rows, starts=None):
         """k, v: (tokens, heads, dim) float64 values of the inputs."""
         starts = list(range(len(rows) + 1)) if starts is None else starts
