@@ -819,6 +819,24 @@ bs_status bs_kv_attend_async(const bs_kv_cache* cache, const bs_kv_attend_args* 
                              void* stream);
 uint64_t bs_kv_attend_work_bytes(const bs_kv_cache* cache, const bs_kv_attend_args* args);
 
+/* Attention of a plan's tokens: as bs_kv_attend_async on the plan's rows and
+ * offsets, to rounding, with the tokens that a group's rows have in common
+ * (d_shared) read once for all of them.  Of args, n_seqs, total_q, max_new,
+ * d_seqs and d_starts are the plan's and not looked at.  A token that the plan
+ * gives no place sees nothing.  Rows' own tokens and the groups' common ones
+ * are split over workgroups, and a second launch adds a row's parts: scores
+ * and sums are held in fp32, probabilities enter the second product in 16
+ * significant bits.  The same result on every run.  From max_new x heads /
+ * kv_heads = 64 on, a row alone fills the matrix instructions: the call is
+ * then bs_kv_attend_async.
+ * d_work (16-B aligned): bs_kv_attend_shared_work_bytes (0: a shape that is
+ * refused, or one that needs none).  Its first 4096 bytes are zero before the
+ * first call that is given it, and every call leaves them so; calls that
+ * share it must not overlap, nor it the queries, results or the plan. */
+bs_status bs_kv_attend_shared_async(const bs_kv_cache* cache, const bs_kv_attend_args* args, const bs_kv_batch* batch,
+                                    void* d_work, uint64_t work_bytes, void* stream);
+uint64_t bs_kv_attend_shared_work_bytes(const bs_kv_cache* cache, const bs_kv_attend_args* args, const bs_kv_batch* batch);
+
 /* ------------------------------------------- continuations of many beams
  *
  * Of all continuations of a request's beams, a beam's score plus the log

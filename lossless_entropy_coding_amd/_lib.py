@@ -212,6 +212,9 @@ SIGNATURES = {
     "bs_kv_reorder_async": (C.c_int, [C.POINTER(KvCache), C.c_uint32, C.c_void_p, C.c_void_p, C.c_void_p, C.c_uint64, C.c_void_p]),
     "bs_kv_reorder_work_bytes": (C.c_uint64, [C.POINTER(KvCache), C.c_uint32]),
     "bs_kv_batch_async": (C.c_int, [C.POINTER(KvCache), C.POINTER(KvBatch), C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p]),
+    "bs_kv_attend_shared_async": (C.c_int, [C.POINTER(KvCache), C.POINTER(KvAttendArgs), C.POINTER(KvBatch), C.c_void_p,
+                                            C.c_uint64, C.c_void_p]),
+    "bs_kv_attend_shared_work_bytes": (C.c_uint64, [C.POINTER(KvCache), C.POINTER(KvAttendArgs), C.POINTER(KvBatch)]),
     "bs_plan_waves_per_block": (C.c_uint32, [C.c_void_p]),
     "bs_plan_packs": (C.c_uint32, [C.c_void_p, C.c_uint32, C.c_uint32]),
     "bs_verify": (C.c_int, [C.c_void_p, C.c_uint32, C.c_uint32, C.c_void_p, C.c_void_p, C.c_void_p, C.c_uint32,

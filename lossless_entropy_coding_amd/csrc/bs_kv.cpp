@@ -167,6 +167,63 @@ bs_status attend_args(const bs_kv_cache* cache, const bs_kv_attend_args* x, bsd:
     return BS_OK;
 }
 
+bs_status check_batch(const bs_kv_batch* b);
+
+// attention of a plan's tokens: `plain` is what it is as attention of rows by themselves
+struct Shared {
+    bs_kv_attend_args plain;
+    bsd::KvShared s;
+    uint32_t chunk, splits;     // of the attention of rows by themselves
+    uint64_t need;              // bytes of workspace
+};
+
+uint64_t part_bytes(const bsd::KvAttend& a, uint32_t splits);
+
+bs_status shared_args(const bs_kv_cache* cache, const bs_kv_attend_args* x, const bs_kv_batch* b, Shared& y) {
+    memset(&y, 0, sizeof y);
+    const bs_status rc = check_batch(b);
+    if (rc != BS_OK) return rc;
+    if (!x) { set_error("NULL argument"); return BS_E_INVAL; }
+    y.plain = *x;
+    y.plain.n_seqs = b->n_seqs;
+    y.plain.total_q = b->total;
+    y.plain.max_new = b->max_new;
+    y.plain.d_seqs = b->d_rows;
+    y.plain.d_starts = b->d_starts;
+    bsd::KvShared& s = y.s;
+    const bs_status at = attend_args(cache, &y.plain, s.a, y.chunk, y.splits);
+    if (at != BS_OK || b->n_seqs == 0 || b->total == 0) return at;
+    if (s.a.many) {
+        y.need = part_bytes(s.a, y.splits);
+        return BS_OK;
+    }
+    s.places = b->d_places;
+    s.shared = b->d_shared;
+    s.info = b->d_info;
+    s.groups = b->n_groups;
+    const uint64_t block = bsd::kKvBlock;
+    s.blocks = (uint32_t)(((uint64_t)b->total * s.a.group + (uint64_t)b->n_groups * (block - 1)) / block);
+    if (b->n_groups == 0) s.blocks = 0;
+    s.row_blocks = (uint32_t)(((uint64_t)b->max_new * s.a.group + block - 1) / block);
+    // splits: a workgroup to a CU of each kind, and a tile at least to each of
+    // its eight waves.  How long the common tokens are is the GPU's to know:
+    // either kind may have all of them.
+    int cus = 0;
+    if (bsk_device_cus(&cus) != 0 || cus <= 0) cus = 256;
+    const uint32_t cap = s.a.c.max_pages * s.a.c.page, len = x->max_len && x->max_len < cap ? x->max_len : cap;
+    const uint64_t most = std::max<uint64_t>(1, ((uint64_t)len + 8 * bsd::kKvTile - 1) / (8 * bsd::kKvTile));
+    const uint64_t pre = std::max<uint64_t>(1, (uint64_t)s.blocks * s.a.c.kv_heads), own = (uint64_t)b->n_seqs * s.row_blocks * s.a.c.kv_heads;
+    s.pre = (uint32_t)std::min(most, ((uint64_t)cus + pre - 1) / pre);
+    s.own = (uint32_t)std::min(most, ((uint64_t)cus + own - 1) / own);
+    if ((((uint64_t)s.a.c.kv_heads * s.pre + 7) / 8 * 8 * s.blocks + own * s.own) > kThreads / 512 ||
+        (uint64_t)b->n_seqs * b->max_new > kThreads / 64) {
+        set_error("%u rows of up to %u new tokens are too many for one call (max_new: the most of one row)", b->n_seqs, b->max_new);
+        return BS_E_INVAL;
+    }
+    y.need = 4ull * (bsd::kKvCounters + (uint64_t)b->total * s.a.heads * (s.pre + s.own) * (s.a.c.wide + 4));
+    return BS_OK;
+}
+
 uint64_t part_bytes(const bsd::KvAttend& a, uint32_t splits) {
     return splits > 1 ? 4ull * (bsd::kKvCounters + (uint64_t)a.total * a.heads * splits * (a.c.wide + 4)) : 0;
 }
@@ -388,6 +445,38 @@ bs_status bs_kv_compact_async(const bs_kv_cache* cache, int32_t* d_table_out, in
     p.table_out = d_table_out;
     p.refs_out = d_refs_out;
     return launched(bsk_kv_compact(&p, stream), "compact");
+}
+
+uint64_t bs_kv_attend_shared_work_bytes(const bs_kv_cache* cache, const bs_kv_attend_args* args, const bs_kv_batch* batch) {
+    Shared y;
+    return shared_args(cache, args, batch, y) == BS_OK ? y.need : 0;
+}
+
+bs_status bs_kv_attend_shared_async(const bs_kv_cache* cache, const bs_kv_attend_args* args, const bs_kv_batch* batch,
+                                    void* d_work, uint64_t work_bytes, void* stream) {
+    Shared y;
+    const bs_status rc = shared_args(cache, args, batch, y);
+    if (rc != BS_OK) return rc;
+    if (batch->n_seqs == 0 || batch->total == 0) return BS_OK;
+    bsd::KvAttend& a = y.s.a;
+    if (a.many) return bs_kv_attend_async(cache, &y.plain, d_work, work_bytes, stream);
+    if (!a.q || !a.out) { set_error("NULL argument"); return BS_E_INVAL; }
+    if (!aligned(a.q, 2) || !aligned(a.out, 2) || !aligned(a.lse, 4)) { set_error("misaligned queries or results"); return BS_E_INVAL; }
+    if (!d_work || !aligned(d_work, 16)) { set_error("a 16-B aligned workspace is needed"); return BS_E_INVAL; }
+    if (work_bytes < y.need) {
+        set_error("workspace of %llu B, %llu B needed", (unsigned long long)work_bytes, (unsigned long long)y.need);
+        return BS_E_INVAL;
+    }
+    const uint64_t row = (uint64_t)a.heads * a.c.dim, n = batch->n_seqs;
+    if (overlap(d_work, y.need, a.out, extent(a.total, a.out_stride, row, 2)) || overlap(d_work, y.need, a.q, extent(a.total, a.q_stride, row, 2)) ||
+        (a.lse && overlap(d_work, y.need, a.lse, 4ull * a.total * a.heads)) || overlap(d_work, y.need, batch->d_rows, 4 * n) ||
+        overlap(d_work, y.need, batch->d_starts, 4 * n + 4) || overlap(d_work, y.need, batch->d_places, 4ull * batch->total) ||
+        overlap(d_work, y.need, batch->d_shared, 4 * n) || overlap(d_work, y.need, batch->d_info, 16ull * (batch->n_groups + 1))) {
+        set_error("the workspace overlaps queries, results or the plan");
+        return BS_E_INVAL;
+    }
+    a.part = (float*)d_work + bsd::kKvCounters;
+    return launched(bsk_kv_shared(&y.s, stream), "attention of groups");
 }
 
 uint64_t bs_kv_reorder_work_bytes(const bs_kv_cache* cache, uint32_t n) {

@@ -8,6 +8,7 @@ namespace bsd {
 
 constexpr uint32_t kKvCounters = 1024;       // words before a workspace's partial results
 constexpr uint32_t kKvTile = 64;             // tokens that a wave takes at a time (4 chunks of 16)
+constexpr uint32_t kKvBlock = 32;            // rows of a workgroup of the attention of groups
 
 // one cache as a kernel sees it (layouts in bs.h)
 struct KvView {
@@ -60,6 +61,19 @@ struct KvAttend {
     float* part;                // splits > 1: [total * heads][splits][wide + 4]: the result, its maximum and sum, 2 unused
 };
 
+// attention of rows in groups that share their first tokens: a's rows, offsets
+// and queries are a plan's; part: [total * heads][pre + own splits][wide + 4]
+struct KvShared {
+    KvAttend a;
+    const int32_t* places;
+    const int32_t* shared;
+    const int32_t* info;        // [groups + 1][4], from the second: first and end token, common tokens, row
+    uint32_t groups;
+    uint32_t blocks;            // row blocks of all groups at most
+    uint32_t row_blocks;        // of one row's own tokens
+    uint32_t pre, own;          // splits of a group's common tokens, and of a row's own
+};
+
 // the plan of a step's tokens (bs_kv_batch of bs.h)
 struct KvBatch {
     KvView c;
@@ -102,4 +116,5 @@ int bsk_kv_copy(const bsd::KvPages* p, void* stream);
 int bsk_kv_compact(const bsd::KvPages* p, void* stream);
 int bsk_kv_reorder(const bsd::KvPages* p, void* stream);
 int bsk_kv_batch(const bsd::KvBatch* b, void* stream);
+int bsk_kv_shared(const bsd::KvShared* s, void* stream);
 }

@@ -248,27 +248,7 @@ class KvCache:
         known (it decides how the work is split, not the result).  Returns
         the result (q's shape, bfloat16), and with lse the logarithms of the
         softmax sums (tokens, heads) as float32."""
-        if q.dtype is not _BF16:
-            raise ValueError("q must be bfloat16")
-        qs = os = self._tokens(q, None, "q")
-        total, heads, _ = shape = q.shape
-        if out is None:
-            with _on(stream):
-                out = torch.empty(shape, dtype=_BF16, device=self.device)
-            os = heads * self.head_dim
-        elif out.dtype is not _BF16 or out.shape != shape:
-            raise ValueError("out must be bfloat16 of q's shape")
-        else:
-            os = self._tokens(out, None, "out")
-        if lse is True:
-            with _on(stream):
-                lse = torch.empty(shape[:2], dtype=_FP32, device=self.device)
-        elif lse is not False and (lse.dtype is not _FP32 or lse.shape != shape[:2] or not lse.is_contiguous() or
-                                   lse.device != self.device):
-            raise ValueError(f"lse must be a contiguous float32 tensor of (tokens, heads) on {self.device}")
-        if window < 0 or sinks < 0 or max_len < 0:
-            raise ValueError("window, sinks and max_len are not negative")
-        window, sinks, max_len = min(window, _MAX), min(sinks, _MAX), min(max_len, _MAX)   # rows are shorter
+        total, heads, qs, os, out, lse, window, sinks, max_len = self._results(q, out, lse, window, sinks, max_len, stream)
         n, most, at = self._rows(rows, starts, total, max_new)
         with self._lock:
             a = self._args
@@ -294,6 +274,66 @@ class KvCache:
         if rc:
             L.check(rc, "bs_kv_attend_async")
         return out if lse is False else (out, lse)
+
+    def attend_shared(self, layer: int, q: torch.Tensor, batch: "KvBatch", scale: float = 0.0, window: int = 0, sinks: int = 0,
+                      softcap: float = 0.0, out: torch.Tensor | None = None, lse: bool | torch.Tensor = False, stream=None):
+        """attend of the tokens of a plan, reading the tokens that the rows of
+        a group have in common once for all of them
+        (bs_kv_attend_shared_async): q (batch.total, heads, head_dim) in the
+        plan's order; the other arguments and the results are attend's.  The
+        plan is this cache's and holds until its rows change."""
+        if batch.cache is not self:
+            raise ValueError("the plan is another cache's")
+        total, heads, qs, os, out, lse, window, sinks, max_len = self._results(q, out, lse, window, sinks, batch.max_len, stream)
+        if total != batch.total:
+            raise ValueError(f"{total} tokens, {batch.total} in the plan")
+        with self._lock:
+            a = self._args
+            a.layer, a.heads, a.max_len = layer if 0 <= layer < _MAX else _MAX, heads, max_len
+            a.d_q, a.d_out, a.d_lse = q.data_ptr(), out.data_ptr(), None if lse is False else lse.data_ptr()
+            a.q_stride, a.out_stride, a.scale, a.softcap, a.window, a.sinks = qs, os, scale, softcap, window, sinks
+            sizes = (batch.n, batch.n_groups, heads, total, batch.max_new, max_len, window, sinks)
+            need = self._attend_need.get(sizes)
+            known = need is not None
+            if not known:
+                need = int(L.lib().bs_kv_attend_shared_work_bytes(self._ref, self._args_ref, batch.ref))
+            w = self._attend_work
+            if need and (w is None or w.numel() < need):
+                w = self._counted_work(need, stream)
+            rc = L.lib().bs_kv_attend_shared_async(self._ref, self._args_ref, batch.ref, w.data_ptr() if need else None, need,
+                                                   _stream_of(self.device, stream))
+            if not rc and not known:
+                if len(self._attend_need) > 4096:
+                    self._attend_need.clear()
+                self._attend_need[sizes] = need
+        if rc:
+            L.check(rc, "bs_kv_attend_shared_async")
+        return out if lse is False else (out, lse)
+
+    def _results(self, q, out, lse, window, sinks, max_len, stream):
+        """Checks of what attention reads and writes, and memory for its results."""
+        if q.dtype is not _BF16:
+            raise ValueError("q must be bfloat16")
+        qs = os = self._tokens(q, None, "q")
+        shape = q.shape
+        if out is None:
+            with _on(stream):
+                out = torch.empty(shape, dtype=_BF16, device=self.device)
+            os = shape[1] * self.head_dim
+        elif out.dtype is not _BF16 or out.shape != shape:
+            raise ValueError("out must be bfloat16 of q's shape")
+        else:
+            os = self._tokens(out, None, "out")
+        if lse is True:
+            with _on(stream):
+                lse = torch.empty(shape[:2], dtype=_FP32, device=self.device)
+        elif lse is not False and (lse.dtype is not _FP32 or lse.shape != shape[:2] or not lse.is_contiguous() or
+                                   lse.device != self.device):
+            raise ValueError(f"lse must be a contiguous float32 tensor of (tokens, heads) on {self.device}")
+        if window < 0 or sinks < 0 or max_len < 0:
+            raise ValueError("window, sinks and max_len are not negative")
+        # rows are shorter than the largest numbers that the library takes
+        return shape[0], shape[1], qs, os, out, lse, min(window, _MAX), min(sinks, _MAX), min(max_len, _MAX)
 
     def _counted_work(self, need: int, stream) -> torch.Tensor:
         """A workspace for attend, its counters zeroed.  Under capture zeroing
