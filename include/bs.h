@@ -746,8 +746,8 @@ uint64_t bs_kv_reorder_work_bytes(const bs_kv_cache* cache, uint32_t n);
  *                          itself for a row of no group
  *   d_shared [n_seqs]      how many leading tokens all rows of the group have on
  *                          the same pages, rounded down to a multiple of 64
- *   d_info   [n_groups + 1][4]  for bs_kv_attend_shared_async; 16-B aligned, its
- *                          first word is 0 before the first call and between calls
+ *   d_info   [4 + 8 (n_groups + n_seqs)]  for bs_kv_attend_shared_async; 16-B aligned,
+ *                          its first word is 0 before the first call and between calls
  * A row that does not exist, a count that is negative, above max_new or the
  * row's length, counts that do not add up to total, offsets of groups that do
  * not ascend: flagged (BS_KV_BAD_ID); tokens without a place or page get -1. */
@@ -826,9 +826,10 @@ uint64_t bs_kv_attend_work_bytes(const bs_kv_cache* cache, const bs_kv_attend_ar
  * gives no place sees nothing.  Rows' own tokens and the groups' common ones
  * are split over workgroups, and a second launch adds a row's parts: scores
  * and sums are held in fp32, probabilities enter the second product in 16
- * significant bits.  The same result on every run.  From max_new x heads /
- * kv_heads = 64 on, a row alone fills the matrix instructions: the call is
- * then bs_kv_attend_async.
+ * significant bits, or, for the common tokens of a group of 64 tokens x heads
+ * / kv_heads or more, in BF16.  The same result on every run.  From max_new x
+ * heads / kv_heads = 64 on, a row alone fills the matrix instructions: the
+ * call is then bs_kv_attend_async.
  * d_work (16-B aligned): bs_kv_attend_shared_work_bytes (0: a shape that is
  * refused, or one that needs none).  Its first 4096 bytes are zero before the
  * first call that is given it, and every call leaves them so; calls that

@@ -198,24 +198,26 @@ bs_status shared_args(const bs_kv_cache* cache, const bs_kv_attend_args* x, cons
         return BS_OK;
     }
     s.places = b->d_places;
-    s.shared = b->d_shared;
     s.info = b->d_info;
     s.groups = b->n_groups;
-    const uint64_t block = bsd::kKvBlock;
-    s.blocks = (uint32_t)(((uint64_t)b->total * s.a.group + (uint64_t)b->n_groups * (block - 1)) / block);
-    if (b->n_groups == 0) s.blocks = 0;
-    s.row_blocks = (uint32_t)(((uint64_t)b->max_new * s.a.group + block - 1) / block);
-    // splits: a workgroup to a CU of each kind, and a tile at least to each of
-    // its eight waves.  How long the common tokens are is the GPU's to know:
+    // row blocks: of 16 rows, or 32 in stacks of kKvStack or more with head_dim
+    // up to 128 (a smaller stack has at most two more than it would have then)
+    const uint64_t rows = (uint64_t)b->total * s.a.group, groups = b->n_groups;
+    uint64_t blocks = (rows + 15 * groups) / 16;
+    if (s.a.c.wide <= 128) blocks = std::min(blocks, (rows + 31 * groups) / 32 + 2 * groups);
+    s.blocks = groups ? (uint32_t)blocks : 0;
+    s.row_blocks = (uint32_t)(((uint64_t)b->max_new * s.a.group + 15) / 16);
+    // splits: two workgroups to a CU of each kind, and a tile at least to each
+    // of their four waves.  How long the common tokens are is the GPU's to know:
     // either kind may have all of them.
     int cus = 0;
     if (bsk_device_cus(&cus) != 0 || cus <= 0) cus = 256;
     const uint32_t cap = s.a.c.max_pages * s.a.c.page, len = x->max_len && x->max_len < cap ? x->max_len : cap;
-    const uint64_t most = std::max<uint64_t>(1, ((uint64_t)len + 8 * bsd::kKvTile - 1) / (8 * bsd::kKvTile));
+    const uint64_t most = std::max<uint64_t>(1, ((uint64_t)len + 4 * bsd::kKvTile - 1) / (4 * bsd::kKvTile));
     const uint64_t pre = std::max<uint64_t>(1, (uint64_t)s.blocks * s.a.c.kv_heads), own = (uint64_t)b->n_seqs * s.row_blocks * s.a.c.kv_heads;
-    s.pre = (uint32_t)std::min(most, ((uint64_t)cus + pre - 1) / pre);
-    s.own = (uint32_t)std::min(most, ((uint64_t)cus + own - 1) / own);
-    if ((((uint64_t)s.a.c.kv_heads * s.pre + 7) / 8 * 8 * s.blocks + own * s.own) > kThreads / 512 ||
+    s.pre = (uint32_t)std::min(most, std::max<uint64_t>(1, 2 * (uint64_t)cus / pre));
+    s.own = (uint32_t)std::min(most, std::max<uint64_t>(1, 2 * (uint64_t)cus / own));
+    if ((((uint64_t)s.a.c.kv_heads * s.pre + 7) / 8 * 8 * s.blocks + own * s.own) > kThreads / 256 ||
         (uint64_t)b->n_seqs * b->max_new > kThreads / 64) {
         set_error("%u rows of up to %u new tokens are too many for one call (max_new: the most of one row)", b->n_seqs, b->max_new);
         return BS_E_INVAL;
@@ -471,7 +473,7 @@ bs_status bs_kv_attend_shared_async(const bs_kv_cache* cache, const bs_kv_attend
     if (overlap(d_work, y.need, a.out, extent(a.total, a.out_stride, row, 2)) || overlap(d_work, y.need, a.q, extent(a.total, a.q_stride, row, 2)) ||
         (a.lse && overlap(d_work, y.need, a.lse, 4ull * a.total * a.heads)) || overlap(d_work, y.need, batch->d_rows, 4 * n) ||
         overlap(d_work, y.need, batch->d_starts, 4 * n + 4) || overlap(d_work, y.need, batch->d_places, 4ull * batch->total) ||
-        overlap(d_work, y.need, batch->d_shared, 4 * n) || overlap(d_work, y.need, batch->d_info, 16ull * (batch->n_groups + 1))) {
+        overlap(d_work, y.need, batch->d_info, 16 + 32 * (batch->n_groups + n))) {
         set_error("the workspace overlaps queries, results or the plan");
         return BS_E_INVAL;
     }

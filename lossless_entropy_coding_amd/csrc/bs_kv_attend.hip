@@ -308,8 +308,6 @@ __global__ __launch_bounds__(256, 2) void attend_kernel(KvAttend a, uint32_t row
 // whole, so the halves of the waves overlap less than they are meant to; why
 // is not found.  Dealing tiles evenly to one workgroup per CU, 8-bit operands
 // in LDS and reading two tiles ahead were 2 to 15% slower.
-constexpr float kGrow = 1024.f;
-
 template <int DW, bool E4M3, int NR, bool CAP>
 __global__ __launch_bounds__(512, 2) void attend_rows_kernel(KvAttend a, uint32_t row_blocks, uint32_t combos) {
     const KvView& c = a.c;

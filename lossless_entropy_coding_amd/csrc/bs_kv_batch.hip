@@ -117,12 +117,20 @@ __global__ __launch_bounds__(kThreads) void batch_kernel(KvBatch b) {
         stop = min(min(least[0], least[1]), min(least[2], least[3]));
         same = (uint32_t)min((uint64_t)both, (uint64_t)stop << c.lp) & ~(kKvTile - 1);
     }
+    int32_t* mine = b.info + 4 + 8 * (b.groups + i);
     if (t == 0) {
         b.rows[i] = r;
         b.lead[i] = (int32_t)first;
         store_through(b.shared + i, (int32_t)same);
         store_through(b.starts + i, (int32_t)s0);
         if (i + 1 == b.n) store_through(b.starts + b.n, (int32_t)s1);
+        const bool any = known && count && len;
+        store_through(mine, (int32_t)s0);
+        store_through(mine + 1, (int32_t)s1);
+        store_through(mine + 2, (int32_t)same);
+        store_through(mine + 3, known ? r : 0);                     // its tokens have no place
+        store_through(mine + 4, any ? (int32_t)(len - min(count, len)) : 0x7FFFFFFF);
+        store_through(mine + 5, any ? (int32_t)len - 1 : -1);
     }
     // the last of the rows' workgroups; the counter is 0 between calls
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup");
@@ -136,18 +144,32 @@ __global__ __launch_bounds__(kThreads) void batch_kernel(KvBatch b) {
         const int32_t f = b.offs ? b.offs[g] : 0, e = b.offs ? b.offs[g + 1] : (int32_t)b.n;
         const uint32_t from = (uint32_t)min(max(f, 0), (int32_t)b.n), to = (uint32_t)min(max(e, (int32_t)from), (int32_t)b.n);
         if (((uint32_t)f != from || (uint32_t)e != to) && lane == 0) flag(c.status, 4u);
-        uint32_t few = ~0u;
-        for (uint32_t j = from + lane; j < to; j += 64) few = min(few, (uint32_t)b.shared[j]);
+        const int32_t* rec = b.info + 4 + 8 * b.groups;
+        int32_t few = 0x7FFFFFFF, low = 0x7FFFFFFF, high = -1;
+        for (uint32_t j = from + lane; j < to; j += 64) {
+            few = min(few, rec[8 * j + 2]);
+            low = min(low, rec[8 * j + 4]);
+            high = max(high, rec[8 * j + 5]);
+        }
 #pragma unroll
-        for (int s = 32; s; s >>= 1) few = min(few, (uint32_t)__shfl_xor((int)few, s));
+        for (int s = 32; s; s >>= 1) {
+            few = min(few, __shfl_xor(few, s));
+            low = min(low, __shfl_xor(low, s));
+            high = max(high, __shfl_xor(high, s));
+        }
         if (from == to) few = 0;
-        for (uint32_t j = from + lane; j < to; j += 64) b.shared[j] = (int32_t)few;
+        for (uint32_t j = from + lane; j < to; j += 64) {
+            b.shared[j] = few;
+            b.info[4 + 8 * (b.groups + j) + 2] = few;
+        }
         if (lane == 0) {
-            int32_t* to4 = b.info + 4 * (g + 1);
-            to4[0] = b.starts[from];
-            to4[1] = b.starts[to];
-            to4[2] = (int32_t)few;
-            to4[3] = from < to ? b.seqs[from] : -1;
+            int32_t* of = b.info + 4 + 8 * g;
+            of[0] = b.starts[from];
+            of[1] = b.starts[to];
+            of[2] = few;
+            of[3] = from < to ? max(b.seqs[from], 0) : -1;
+            of[4] = low;
+            of[5] = high;
         }
     }
     if (t == 0) __hip_atomic_store((uint32_t*)b.info, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);

@@ -8,7 +8,7 @@ namespace bsd {
 
 constexpr uint32_t kKvCounters = 1024;       // words before a workspace's partial results
 constexpr uint32_t kKvTile = 64;             // tokens that a wave takes at a time (4 chunks of 16)
-constexpr uint32_t kKvBlock = 32;            // rows of a workgroup of the attention of groups
+constexpr uint32_t kKvStack = 64;            // stacked rows from which on probabilities are in BF16
 
 // one cache as a kernel sees it (layouts in bs.h)
 struct KvView {
@@ -66,8 +66,8 @@ struct KvAttend {
 struct KvShared {
     KvAttend a;
     const int32_t* places;
-    const int32_t* shared;
-    const int32_t* info;        // [groups + 1][4], from the second: first and end token, common tokens, row
+    const int32_t* info;        // 4 words, then 8 of each group and row: first and end token, common tokens, row of the
+                                // table, least and largest place, 2 unused
     uint32_t groups;
     uint32_t blocks;            // row blocks of all groups at most
     uint32_t row_blocks;        // of one row's own tokens

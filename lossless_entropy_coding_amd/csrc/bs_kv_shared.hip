@@ -10,11 +10,14 @@
 //
 //   o = sum_i 2^(m_i - m) o_i / sum_i 2^(m_i - m) l_i,   m = max_i m_i.
 //
-// A workgroup takes 32 stacked rows and some tiles of 64 tokens, its eight
-// waves one tile each in turn.  Products and the lanes' tokens are those of the
+// A workgroup takes 16 stacked rows, 32 in stacks of 64 rows or more with
+// head_dim up to 128, and some tiles of 64 tokens, its four waves one tile each
+// in turn.  Products and the lanes' tokens are those of the
 // kernel for few rows (bs_kv_attend.hip): S^T = K Q^T, O^T += V^T P^T, keys and
 // values straight from memory to the registers of the wave that multiplies
-// them.  Here an operand made of 8-bit codes meets two row tiles of 16.
+// them.  With 32 rows an operand made of 8-bit codes meets two row tiles, and P
+// is rounded to BF16, as in the kernel for many rows; else it enters in two
+// BF16 parts.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -26,8 +29,18 @@ using namespace bsd;
 
 namespace {
 
-constexpr uint32_t kWaves = 8;
-constexpr uint32_t kRowTiles = kKvBlock / 16;
+constexpr uint32_t kWaves = 4;
+
+// row tiles of a workgroup of a large stack: two where the accumulators leave
+// room for a tile's keys and values in flight (head_dim up to 128)
+template <int DW>
+constexpr uint32_t kRowTiles = DW <= 2 ? 2 : 1;
+
+// rows of a workgroup of a stack
+template <uint32_t NR>
+__device__ __forceinline__ uint32_t block_rows(uint32_t rows) {
+    return NR > 1 && rows >= kKvStack ? 16 * NR : 16;
+}
 
 // the tiles of a part: a0 .. a0 + na - 1, then b0 ..
 struct Part {
@@ -47,52 +60,57 @@ __device__ __forceinline__ Part get_part(const KvAttend& a, int32_t lo, int32_t 
     return p;
 }
 
-__device__ __forceinline__ int32_t row_min(int32_t x) {
-#pragma unroll
-    for (int s = 8; s; s >>= 1) x = min(x, __shfl_xor(x, s));
-    return x;
-}
-
-__device__ __forceinline__ int32_t row_max(int32_t x) {
-#pragma unroll
-    for (int s = 8; s; s >>= 1) x = max(x, __shfl_xor(x, s));
-    return x;
-}
-
 // a workgroup's rows and tokens
 struct Job {
     uint32_t first, rows, r0;       // first token of the stack, its rows, the block's first
     uint32_t head, split, splits, slot;
     uint32_t cut;                   // tiles in common
     int32_t row;                    // of the table
+    int32_t lo, hi;                 // places of the stack
     bool before, valid;
 };
 
-// which group and block of 32 rows: the blocks of the groups one after the other
+// a record of the plan, checked: its rows, 0 for one that does not hold
+__device__ __forceinline__ uint32_t record_rows(const KvShared& s, int4 x, uint32_t most) {
+    const bool ok = x.x >= 0 && x.y >= x.x && (uint32_t)x.y <= s.a.total && (uint32_t)(x.y - x.x) <= most && x.z >= 0 && x.w >= 0 &&
+                    (uint32_t)x.w < s.a.c.max_seqs;
+    return ok ? (uint32_t)(x.y - x.x) * s.a.group : 0u;
+}
+
+// which group and block of rows: the blocks of the groups one after the other
+template <uint32_t NR>
 __device__ __forceinline__ bool find_block(const KvShared& s, uint32_t block, Job& j) {
     const uint32_t lane = threadIdx.x & 63u;
     uint32_t seen = 0;
     for (uint32_t base = 0; base < s.groups; base += 64) {
         const uint32_t g = base + lane;
         int4 x = make_int4(0, 0, 0, -1);
-        if (g < s.groups) x = *(const int4*)(s.info + 4 * (g + 1));
-        const bool ok = x.x >= 0 && x.y >= x.x && (uint32_t)x.y <= s.a.total && x.z > 0 && x.w >= 0 && (uint32_t)x.w < s.a.c.max_seqs;
-        const uint32_t rows = ok ? (uint32_t)(x.y - x.x) * s.a.group : 0u;
-        uint32_t n = (rows + kKvBlock - 1) / kKvBlock;
-        const uint32_t mine = n;
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const uint32_t y = __shfl_up(n, d);
-            if (lane >= (uint32_t)d) n += y;
+        int2 y = make_int2(0, -1);
+        if (g < s.groups) {
+            x = *(const int4*)(s.info + 4 + 8 * g);
+            y = *(const int2*)(s.info + 8 + 8 * g);
         }
-        const uint64_t in = __builtin_amdgcn_ballot_w64(block < seen + n);
+        const uint32_t rows = x.z >= (int32_t)kKvTile ? record_rows(s, x, s.a.total) : 0u;
+        const uint32_t mine = NR > 1 && rows >= kKvStack ? (rows + 16 * NR - 1) / (16 * NR) : (rows + 15) / 16;
+        uint32_t n = mine;
+        if (s.groups > 1) {
+#pragma unroll
+            for (int d = 1; d < 64; d <<= 1) {
+                const uint32_t z = __shfl_up(n, d);
+                if (lane >= (uint32_t)d) n += z;
+            }
+        }
+        const uint64_t in = __builtin_amdgcn_ballot_w64(g < s.groups && block < seen + n);
         if (in) {
             const int who = (int)__builtin_ctzll(in);
-            j.first = (uint32_t)__shfl(x.x, who);
-            j.rows = (uint32_t)__shfl((int)rows, who);
-            j.r0 = (block - seen - (uint32_t)__shfl((int)(n - mine), who)) * kKvBlock;
-            j.cut = (uint32_t)__shfl(x.z, who) / kKvTile;
-            j.row = __shfl(x.w, who);
+            auto of = [&](int32_t v) { return __builtin_amdgcn_readlane(v, who); };
+            j.first = (uint32_t)of(x.x);
+            j.rows = (uint32_t)of((int32_t)rows);
+            j.r0 = (block - seen - (uint32_t)of((int32_t)(n - mine))) * block_rows<NR>(j.rows);
+            j.cut = (uint32_t)of(x.z) / kKvTile;
+            j.row = of(x.w);
+            j.lo = of(y.x);
+            j.hi = of(y.y);
             return true;
         }
         seen += (uint32_t)__shfl((int)n, 63);
@@ -102,18 +120,17 @@ __device__ __forceinline__ bool find_block(const KvShared& s, uint32_t block, Jo
 
 // grid: workgroups of the groups' common tokens (row blocks of a key head and
 // split follow each other on one XCD, whose L2 they share), then those of the
-// rows' own tokens
+// rows' own tokens.  Two waves to a SIMD: 256 registers, and no AGPRs.
 template <int DW, bool E4M3, bool CAP>
 __global__ __launch_bounds__(64 * kWaves, 2) void shared_kernel(KvShared s, uint32_t common) {
     const KvAttend& a = s.a;
     const KvView& c = a.c;
-    constexpr uint32_t D = 64 * DW, NR = kRowTiles;
-    // steps of keys and channel blocks of values that are loaded at a time: all
-    // at once, beside the results of 32 rows, head_dim 256 spills registers
-    constexpr uint32_t KS = DW >= 3 ? 2 : 4, VS = DW >= 3 ? 2 * DW : 4 * DW;
-    __shared__ __attribute__((aligned(16))) uint8_t qs[NR][2 * DW][1024];
+    constexpr uint32_t D = 64 * DW, NR = kRowTiles<DW>;
+    // Q as operands of the product, later the waves' results
     __shared__ __attribute__((aligned(16))) f32x4 os[kWaves / 2][NR][4 * DW][64];
     __shared__ float ml[kWaves / 2][NR][2][64];
+    static_assert(sizeof os >= NR * 2 * DW * 1024, "Q fits");
+    uint8_t* qs = (uint8_t*)os;
 
     const uint32_t t = threadIdx.x, lane = t & 63u, m = lane & 15u, g = lane >> 4;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(t >> 6);
@@ -125,81 +142,120 @@ __global__ __launch_bounds__(64 * kWaves, 2) void shared_kernel(KvShared s, uint
         j.splits = s.pre;
         j.slot = 0;
         j.before = true;
-        j.valid = j.split < s.pre && find_block(s, at % s.blocks, j);
+        j.valid = j.split < s.pre && find_block<NR>(s, at % s.blocks, j);
     } else {
         uint32_t x = blockIdx.x - common;
         j.head = x % c.kv_heads;
         x /= c.kv_heads;
-        j.r0 = x % s.row_blocks * kKvBlock;
+        j.r0 = x % s.row_blocks * 16;
         x /= s.row_blocks;
         const uint32_t seq = x % a.n_seqs;
         j.split = x / a.n_seqs;
         j.splits = s.own;
         j.slot = s.pre;
         j.before = false;
-        const int32_t s0 = a.starts[seq], s1 = a.starts[seq + 1];
-        j.row = a.seqs[seq];
-        j.cut = (uint32_t)max(s.shared[seq], 0) / kKvTile;
-        j.valid = s0 >= 0 && s1 >= s0 && (uint32_t)s1 <= a.total && (uint32_t)(s1 - s0) <= a.max_new;
-        if (!j.valid && t == 0 && j.r0 == 0 && j.split == 0 && c.status) atomicOr(c.status, 4u);
-        j.first = (uint32_t)s0;
-        j.rows = j.valid ? (uint32_t)(s1 - s0) * a.group : 0u;
-        if (j.row < 0 || (uint32_t)j.row >= c.max_seqs) {           // the plan has given its tokens no place
-            if (t == 0 && j.r0 == 0 && j.split == 0 && c.status) atomicOr(c.status, 4u);
-            j.row = 0;
-        }
-        j.valid = j.valid && j.r0 < j.rows;
+        const int32_t* at = s.info + 4 + 8 * (s.groups + seq);
+        const int4 r = *(const int4*)at;
+        const int2 y = *(const int2*)(at + 4);
+        j.first = (uint32_t)r.x;
+        j.rows = record_rows(s, r, a.max_new);
+        j.cut = (uint32_t)r.z / kKvTile;
+        j.row = r.w;
+        j.lo = y.x;
+        j.hi = y.y;
+        j.valid = j.r0 < j.rows;
     }
     if (!j.valid) return;
-    const uint32_t nrows = min(kKvBlock, j.rows - j.r0);
-    const bool two = nrows > 16;
-
-    // this lane's rows: row m of each row tile
-    uint32_t tok[NR], qh[NR];
-    int32_t pos[NR];
-    const int32_t cap = (int32_t)(c.max_pages << c.lp);
-#pragma unroll
-    for (uint32_t n = 0; n < NR; n++) {
-        const uint32_t r = j.r0 + min(16 * n + m, nrows - 1);
-        tok[n] = j.first + r / a.group;
-        qh[n] = j.head * a.group + r % a.group;
-        pos[n] = min(s.places[tok[n]], cap - 1);
-    }
-    int32_t lo = 0x7FFFFFFF, hi = -1;
-#pragma unroll
-    for (uint32_t n = 0; n < NR; n++) {
-        if (pos[n] >= 0) lo = min(lo, pos[n]);
-        hi = max(hi, pos[n]);
-    }
-    const bool every = __builtin_amdgcn_ballot_w64(pos[0] < 0 || pos[NR - 1] < 0) == 0;
-    lo = __builtin_amdgcn_readfirstlane(row_min(lo));
-    hi = __builtin_amdgcn_readfirstlane(row_max(hi));
-    const Part pt = get_part(a, lo, hi, j.cut, j.before);
+    const bool tall = NR > 1 && j.before && j.rows >= kKvStack;
+    const uint32_t nrows = min(tall ? 16 * NR : 16u, j.rows - j.r0);
+    j.hi = min(j.hi, (int32_t)(c.max_pages << c.lp) - 1);
+    const Part pt = get_part(a, j.lo, j.hi, j.cut, j.before);
     const uint32_t chunk = max(kWaves, (pt.n + j.splits - 1) / j.splits);
     const uint32_t i0 = j.split * chunk;
     if (j.split > 0 && i0 >= pt.n) return;
     const uint32_t i1 = min(pt.n, i0 + chunk), parts = (pt.n + chunk - 1) / chunk;
     const int32_t* trow = c.table + (uint64_t)(uint32_t)j.row * c.max_pages;
     const uint64_t hoff = (uint64_t)j.head * c.page * c.wide;
-    const uint32_t end = (uint32_t)(hi + 1);                        // tokens past it are seen by no row
-    auto pages = [&](uint32_t i, int32_t& pk, int32_t& pv) {
+    const uint32_t end = (uint32_t)(j.hi + 1);                      // tokens past it are seen by no row
+
+    // Entries of the table, then keys, then values are loaded a step ahead:
+    // keys of the wave's next tile when this one's are multiplied, its values
+    // when this one's are, into the same registers.
+    int32_t pk = -1, pv = -1;                                       // entries of the tile to be loaded
+    auto entries = [&](uint32_t i) {
         pk = pv = -1;
         if (i >= i1) return;
         const uint32_t tile0 = pt.at(i) * kKvTile, ck = tile0 + 16 * (m >> 2), cv = tile0 + 16 * g;
         if (ck < end) pk = trow[ck >> c.lp];
         if (cv < end) pv = trow[cv >> c.lp];
     };
-    int32_t pk1, pv1;
-    pages(i0 + wave, pk1, pv1);
-    if (wave < NR && (wave == 0 || two)) {
+    entries(i0 + wave);
+
+    // this lane's rows: row m of each row tile
+    uint32_t tok[NR], qh[NR];
+    int32_t pos[NR];
+#pragma unroll
+    for (uint32_t n = 0; n < NR; n++) {
+        const uint32_t r = j.r0 + min(16 * n + m, nrows - 1);
+        tok[n] = j.first + r / a.group;
+        qh[n] = j.head * a.group + r % a.group;
+        pos[n] = s.places[tok[n]];
+    }
+    if (wave < NR) {
         bf16x8 q[DW][2];
         load_q<DW>(a, wave ? tok[NR - 1] : tok[0], wave ? qh[NR - 1] : qh[0], g, q);
+        const uint32_t sign = a.qscale < 0.f ? 0x80008000u : 0u;    // the scale's sign goes into Q
 #pragma unroll
-        for (uint32_t x = 0; x < 2 * DW; x++) *(bf16x8*)(qs[wave][x] + 16 * lane) = q[x >> 1][x & 1];
+        for (uint32_t x = 0; x < 2 * DW; x++)
+            *(v4u*)(qs + (wave * 2 * DW + x) * 1024 + 16 * lane) = __builtin_bit_cast(v4u, q[x >> 1][x & 1]) ^ sign;
     }
+
+    // Above head_dim 192 a whole tile's values do not fit beside its keys: the
+    // second half of them takes the registers of keys 0 and 1 of each four
+    // between their product and the next tile's.
+    constexpr bool HALF = DW >= 4;
+    constexpr uint32_t VS = HALF ? 2 * DW : 4 * DW;
+    v4u kr[4][DW], vr[VS];
+    struct Tile {
+        const uint8_t *k, *v;
+        float ks, vs;           // scales of the lane's pages
+        bool ok;                // its own tokens have a page
+    };
+    Tile now{}, next{};
+    auto locate = [&](uint32_t i) {
+        const uint32_t tile0 = pt.at(i) * kKvTile, ck = tile0 + 16 * (m >> 2), cv = tile0 + 16 * g;
+        next.ok = (uint32_t)pv < c.n_pages;
+        const uint32_t ik = (uint32_t)pk < c.n_pages ? (uint32_t)pk : 0u, iv = next.ok ? (uint32_t)pv : 0u;
+        next.k = a.k + (uint64_t)ik * c.side_bytes + hoff + (uint64_t)((ck + (m & 3u)) & (c.page - 1)) * D + 16 * g;
+        next.v = a.v + (uint64_t)iv * c.side_bytes + hoff + (uint64_t)m * c.page + (cv & (c.page - 1));
+        // e4m3: the scale of keys goes into the operand, so it is that of the
+        // operand's token; int8: into the product, so that of the product's
+        next.ks = a.scale[((uint64_t)(E4M3 ? ik : iv) * c.kv_heads + j.head) * 2];
+        next.vs = a.scale[((uint64_t)iv * c.kv_heads + j.head) * 2 + 1];
+    };
+    auto load_keys = [&](const Tile& from, uint32_t h0, uint32_t h1) {
+#pragma unroll
+        for (uint32_t h = h0; h < h1; h++)
+#pragma unroll
+            for (uint32_t x = 0; x < DW; x++) kr[h][x] = *(const v4u*)(from.k + 4 * h * D + 64 * x);
+    };
+    auto load_values = [&](const Tile& from) {
+#pragma unroll
+        for (uint32_t d = 0; d < VS; d++) vr[d] = *(const v4u*)(from.v + (uint64_t)(16 * d) * c.page);
+    };
+    if (i0 + wave < i1) {
+        locate(i0 + wave);
+        load_keys(next, HALF ? 2 : 0, 4);
+        if (HALF) load_keys(next, 0, 2);
+        load_values(next);
+        now = next;
+        entries(i0 + wave + kWaves);
+    }
+    const bool every = __builtin_amdgcn_ballot_w64(pos[0] < 0 || pos[NR - 1] < 0) == 0;
     __syncthreads();
-    const float sc = a.softcap > 0.f ? a.qscale : a.qscale * kLog2e;
-    const float cap_in = a.softcap > 0.f ? 2.f * kLog2e / a.softcap : 0.f, cap_out = a.softcap * kLog2e;
+    // to powers of 2 (at least 2^-120: a masked logit times it stays -infinity)
+    const float mul = a.softcap > 0.f ? 1.f : fmaxf(kLog2e * fabsf(a.qscale), 0x1p-120f);
+    const float cap_in = a.softcap > 0.f ? 2.f * kLog2e / a.softcap * fabsf(a.qscale) : 0.f, cap_out = a.softcap * kLog2e;
 
     f32x4 o[NR][4 * DW];
     float mx[NR], sum[NR];
@@ -212,72 +268,75 @@ __global__ __launch_bounds__(64 * kWaves, 2) void shared_kernel(KvShared s, uint
     }
     uint32_t bad = 0;
 
-    auto tile = [&](uint32_t i, auto count) {
+    // one tile: N row tiles, P in one or two BF16 parts
+    auto tile = [&](uint32_t i, auto count, auto twice) {
         constexpr uint32_t N = decltype(count)::value;
-        const uint32_t tile0 = pt.at(i) * kKvTile;
-        const uint32_t ck = tile0 + 16 * (m >> 2), cv = tile0 + 16 * g;
-        const bool okk = (uint32_t)pk1 < c.n_pages, okv = (uint32_t)pv1 < c.n_pages;
-        if (cv < end && !okv) bad = 1;
-        const uint32_t ipk = okk ? (uint32_t)pk1 : 0u, ipv = okv ? (uint32_t)pv1 : 0u;
-        const uint8_t* kp = a.k + (uint64_t)ipk * c.side_bytes + hoff + (uint64_t)((ck + (m & 3u)) & (c.page - 1)) * D + 16 * g;
-        const uint8_t* vp = a.v + (uint64_t)ipv * c.side_bytes + hoff + (uint64_t)m * c.page + (cv & (c.page - 1));
-        v4u kr[KS][DW], vr[VS];
-        auto load_keys = [&](uint32_t h0) {
-#pragma unroll
-            for (uint32_t h = 0; h < KS; h++)
-#pragma unroll
-                for (uint32_t x = 0; x < DW; x++) kr[h][x] = *(const v4u*)(kp + 4 * (h0 + h) * D + 64 * x);
-        };
-        auto load_values = [&](uint32_t d0) {
-#pragma unroll
-            for (uint32_t d = 0; d < VS; d++) vr[d] = *(const v4u*)(vp + (uint64_t)(16 * (d0 + d)) * c.page);
-        };
-        load_keys(0);
-        const float* sp = a.scale + ((uint64_t)ipv * c.kv_heads + j.head) * 2;
-        const float ks = sp[0] * sc, vs = okv ? sp[1] : 0.f;
-        if (VS == 4 * DW) load_values(0);
-        pages(i + kWaves, pk1, pv1);
-
+        constexpr bool TWO = decltype(twice)::value;
+        const uint32_t tile0 = pt.at(i) * kKvTile, cv = tile0 + 16 * g;
+        const bool more = i + kWaves < i1;
         f32x4 sx[N][4];
+        auto qk = [&](uint32_t h0, uint32_t h1) {
 #pragma unroll
-        for (uint32_t h = 0; h < 4; h++) {
-            if (KS < 4 && h == KS) {
-                __builtin_amdgcn_sched_barrier(0);
-                load_keys(h);
-            }
+            for (uint32_t h = h0; h < h1; h++)
 #pragma unroll
-            for (uint32_t n = 0; n < N; n++) sx[n][h] = f32x4{0.f, 0.f, 0.f, 0.f};
+                for (uint32_t n = 0; n < N; n++) sx[n][h] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (uint32_t x = 0; x < DW; x++) {
-                const v4u kc = kr[h % KS][x];
-                const bf16x8 k0 = widen8<E4M3>(kc.x, kc.y), k1 = widen8<E4M3>(kc.z, kc.w);
+                bf16x8 q[N][2];
 #pragma unroll
-                for (uint32_t n = 0; n < N; n++) {
-                    const bf16x8 q0 = *(const bf16x8*)(qs[n][2 * x] + 16 * lane), q1 = *(const bf16x8*)(qs[n][2 * x + 1] + 16 * lane);
-                    sx[n][h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k0, q0, sx[n][h], 0, 0, 0);
-                    sx[n][h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k1, q1, sx[n][h], 0, 0, 0);
+                for (uint32_t n = 0; n < N; n++)
+#pragma unroll
+                    for (uint32_t y = 0; y < 2; y++) q[n][y] = *(const bf16x8*)(qs + (n * 2 * DW + 2 * x + y) * 1024 + 16 * lane);
+#pragma unroll
+                for (uint32_t h = h0; h < h1; h++) {
+                    const v4u kc = kr[h][x];
+                    const float f = E4M3 ? now.ks : 1.f;
+                    const bf16x8 k0 = widen8<E4M3>(kc.x, kc.y, f), k1 = widen8<E4M3>(kc.z, kc.w, f);
+#pragma unroll
+                    for (uint32_t n = 0; n < N; n++) sx[n][h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k0, q[n][0], sx[n][h], 0, 0, 0);
+#pragma unroll
+                    for (uint32_t n = 0; n < N; n++) sx[n][h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k1, q[n][1], sx[n][h], 0, 0, 0);
                 }
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        };
+        if (HALF) {
+            qk(2, 4);
+            if (more) {
+                locate(i + kWaves);
+                load_keys(next, 2, 4);
+            }
+            qk(0, 2);
+#pragma unroll
+            for (uint32_t d = 0; d < VS; d++) kr[d / DW][d % DW] = *(const v4u*)(now.v + (uint64_t)(16 * (VS + d)) * c.page);
+        } else {
+            qk(0, 4);
+            if (more) {
+                locate(i + kWaves);
+                load_keys(next, 0, 4);
             }
         }
-        if (VS < 4 * DW) {
-            __builtin_amdgcn_sched_barrier(0);
-            load_values(0);
-        }
+        __builtin_amdgcn_sched_barrier(0);
+        const bool okv = now.ok;
+        const float kscale = now.ks, vscale = okv ? now.vs : 0.f;
+        if (cv < end && !okv) bad = 1;
         // what every row sees needs no mask
-        bool all = every && (int32_t)(tile0 + kKvTile - 1) <= lo && __builtin_amdgcn_ballot_w64(!okv) == 0;
-        if (a.window) all = all && ((int64_t)tile0 > (int64_t)hi - (int64_t)a.window || tile0 + kKvTile <= a.sinks);
+        bool all = every && (int32_t)(tile0 + kKvTile - 1) <= j.lo && __builtin_amdgcn_ballot_w64(!okv) == 0;
+        if (a.window) all = all && ((int64_t)tile0 > (int64_t)j.hi - (int64_t)a.window || tile0 + kKvTile <= a.sinks);
         bf16x8 pb[N][2], pl[N][2];
 #pragma unroll
         for (uint32_t n = 0; n < N; n++) {
             // step h's element e is token cv + 4 h + e
             float p[16];
-            float top = -__builtin_inff();
 #pragma unroll
-            for (uint32_t e = 0; e < 16; e++) {
-                float x = sx[n][e >> 2][e & 3] * ks;
-                if (CAP) x = capped(x * cap_in, cap_out);
-                else if (a.softcap > 0.f) x = cap_out * (1.f - 2.f * __builtin_amdgcn_rcpf(exp2_fast(x * cap_in) + 1.f));
-                p[e] = x;
+            for (uint32_t e = 0; e < 16; e++) p[e] = E4M3 ? sx[n][e >> 2][e & 3] : sx[n][e >> 2][e & 3] * kscale;
+            if (CAP) {
+#pragma unroll
+                for (uint32_t e = 0; e < 16; e++) p[e] = capped(p[e] * cap_in, cap_out);
+            } else if (a.softcap > 0.f) {
+#pragma unroll
+                for (uint32_t e = 0; e < 16; e++)
+                    p[e] = cap_out - 2.f * cap_out * __builtin_amdgcn_rcpf(exp2_fast(p[e] * cap_in) + 1.f);
             }
             if (!all) {
 #pragma unroll
@@ -288,87 +347,105 @@ __global__ __launch_bounds__(64 * kWaves, 2) void shared_kernel(KvShared s, uint
                     p[e] = seen ? p[e] : -__builtin_inff();
                 }
             }
+            // against the maximum so far; only where a row's sum shows that it
+            // has been passed by far (or there is none yet: the sum is then
+            // infinite or NaN) is the new one looked for
+            float x[16], tot = 0.f;
 #pragma unroll
-            for (uint32_t e = 0; e < 16; e++) top = fmaxf(top, p[e]);
-            top = fmaxf(max_groups(top), mx[n]);
-            const float sub = top == -__builtin_inff() ? 0.f : top;
-            if (__builtin_amdgcn_ballot_w64(top > mx[n]) != 0) {
+            for (uint32_t e = 0; e < 16; e++) {
+                x[e] = exp2_fast(p[e] * mul - mx[n]);
+                tot += x[e];
+            }
+            if (__builtin_amdgcn_ballot_w64(!(tot <= kGrow)) != 0) {
+                float top = p[0];
+#pragma unroll
+                for (uint32_t e = 1; e < 16; e++) top = fmaxf(top, p[e]);
+                const float now = fmaxf(max_groups(top * mul), mx[n]), sub = now == -__builtin_inff() ? 0.f : now;
                 const float alpha = exp2_fast(mx[n] - sub);
-                mx[n] = top;
+                mx[n] = now;
                 sum[n] *= alpha;
 #pragma unroll
                 for (int d = 0; d < 4 * DW; d++) o[n][d] *= alpha;
-            }
-            float part = 0.f;
+                tot = 0.f;
 #pragma unroll
-            for (int e = 0; e < 16; e++) {
-                p[e] = exp2_fast(p[e] - sub);
-                part += p[e];
+                for (uint32_t e = 0; e < 16; e++) {
+                    x[e] = exp2_fast(p[e] * mul - sub);
+                    tot += x[e];
+                }
             }
-            sum[n] += part;
-            // P in two BF16 parts
+            sum[n] += tot;
 #pragma unroll
             for (int y = 0; y < 2; y++) {
                 uint32_t up[4], low[4];
 #pragma unroll
                 for (int e = 0; e < 4; e++) {
-                    const float u = p[8 * y + 2 * e] * vs, v = p[8 * y + 2 * e + 1] * vs;
+                    const float f = E4M3 ? 1.f : vscale, u = x[8 * y + 2 * e] * f, v = x[8 * y + 2 * e + 1] * f;
                     up[e] = pack_bf16(u, v);
-                    low[e] = pack_bf16(u - __builtin_bit_cast(float, up[e] << 16), v - __builtin_bit_cast(float, up[e] & 0xFFFF0000u));
+                    if (TWO) low[e] = pack_bf16(u - __builtin_bit_cast(float, up[e] << 16), v - __builtin_bit_cast(float, up[e] & 0xFFFF0000u));
                 }
                 pb[n][y] = __builtin_bit_cast(bf16x8, v4u{up[0], up[1], up[2], up[3]});
-                pl[n][y] = __builtin_bit_cast(bf16x8, v4u{low[0], low[1], low[2], low[3]});
+                if (TWO) pl[n][y] = __builtin_bit_cast(bf16x8, v4u{low[0], low[1], low[2], low[3]});
             }
+            __builtin_amdgcn_sched_barrier(0);
         }
+        // what no row sees may hold anything: its values count as 0
+        const bool cut = cv + 16 > end || !okv;
+        const int32_t left = okv ? (int32_t)(end - cv) : 0;          // tokens of the chunk that are kept
+        auto pv_block = [&](v4u w, uint32_t d) {
+            if (cut) {
 #pragma unroll
-        for (uint32_t d0 = 0; d0 < 4 * DW; d0 += VS) {
-            if (d0) {
-                __builtin_amdgcn_sched_barrier(0);
-                load_values(d0);
-            }
-            // what no row sees may hold anything: its values count as 0
-            if (cv + 16 > end || !okv) {
-                const int32_t left = okv ? (int32_t)(end - cv) : 0;  // tokens of the chunk that are kept
-#pragma unroll
-                for (uint32_t d = 0; d < VS; d++)
-#pragma unroll
-                    for (int w = 0; w < 4; w++) {
-                        const int32_t nb = left - 4 * w;
-                        const uint32_t mask = nb >= 4 ? ~0u : nb <= 0 ? 0u : (1u << (8 * nb)) - 1u;
-                        vr[d][w] &= mask;
-                    }
-            }
-#pragma unroll
-            for (uint32_t d = 0; d < VS; d++) {
-                const bf16x8 v0 = widen8<E4M3>(vr[d].x, vr[d].y), v1 = widen8<E4M3>(vr[d].z, vr[d].w);
-#pragma unroll
-                for (uint32_t n = 0; n < N; n++) {
-                    f32x4& to = o[n][d0 + d];
-                    to = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v0, pl[n][0], to, 0, 0, 0);
-                    to = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v1, pl[n][1], to, 0, 0, 0);
-                    to = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v0, pb[n][0], to, 0, 0, 0);
-                    to = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v1, pb[n][1], to, 0, 0, 0);
+                for (int e = 0; e < 4; e++) {
+                    const int32_t nb = left - 4 * e;
+                    w[e] &= nb >= 4 ? ~0u : nb <= 0 ? 0u : (1u << (8 * nb)) - 1u;
                 }
             }
+            const float f = E4M3 ? vscale : 1.f;
+            const bf16x8 v0 = widen8<E4M3>(w.x, w.y, f), v1 = widen8<E4M3>(w.z, w.w, f);
+            if (TWO) {
+#pragma unroll
+                for (uint32_t n = 0; n < N; n++) o[n][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v0, pl[n][0], o[n][d], 0, 0, 0);
+#pragma unroll
+                for (uint32_t n = 0; n < N; n++) o[n][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v1, pl[n][1], o[n][d], 0, 0, 0);
+            }
+#pragma unroll
+            for (uint32_t n = 0; n < N; n++) o[n][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v0, pb[n][0], o[n][d], 0, 0, 0);
+#pragma unroll
+            for (uint32_t n = 0; n < N; n++) o[n][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v1, pb[n][1], o[n][d], 0, 0, 0);
+            if (d & 1) __builtin_amdgcn_sched_barrier(0);
+        };
+#pragma unroll
+        for (uint32_t d = 0; d < VS; d++) pv_block(vr[d], d);
+        if (more) load_values(next);
+        if (HALF) {
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (uint32_t d = 0; d < VS; d++) pv_block(kr[d / DW][d % DW], VS + d);
+            if (more) load_keys(next, 0, 2);
         }
+        now = next;
+        if (more) entries(i + 2 * kWaves);
+        __builtin_amdgcn_sched_barrier(0);
     };
-    if (two) {
-        for (uint32_t i = i0 + wave; i < i1; i += kWaves) tile(i, std::integral_constant<uint32_t, NR>{});
+    // Two row tiles share an operand, and P enters in one part, in large
+    // stacks; what would be a third form (two row tiles, P in two parts) makes
+    // the compiler spill registers in all of them.
+    if (tall) {
+        for (uint32_t i = i0 + wave; i < i1; i += kWaves) tile(i, std::integral_constant<uint32_t, NR>{}, std::integral_constant<bool, NR == 1>{});
     } else {
-        for (uint32_t i = i0 + wave; i < i1; i += kWaves) tile(i, std::integral_constant<uint32_t, 1>{});
+        for (uint32_t i = i0 + wave; i < i1; i += kWaves) tile(i, std::integral_constant<uint32_t, 1>{}, std::true_type{});
     }
     if (bad && c.status) atomicOr(c.status, 4u);
 
     // join the waves that had tiles, always in the same pairs
-    const uint32_t busy = min(kWaves, i1 - i0);
-    const uint32_t tiles = two ? NR : 1;
+    const uint32_t busy = min(kWaves, i1 - i0), high = (nrows + 15) / 16;
+    __syncthreads();                                                // Q is not needed any more
 #pragma unroll
     for (uint32_t half = kWaves / 2; half; half >>= 1) {
         if (busy <= half) continue;
         if (wave >= half && wave < 2 * half && wave < busy) {
 #pragma unroll
             for (uint32_t n = 0; n < NR; n++) {
-                if (n >= tiles) break;
+                if (n >= high) break;
                 ml[wave - half][n][0][lane] = mx[n];
                 ml[wave - half][n][1][lane] = sum[n];
 #pragma unroll
@@ -379,7 +456,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void shared_kernel(KvShared s, uint
         if (wave < half && wave + half < busy) {
 #pragma unroll
             for (uint32_t n = 0; n < NR; n++) {
-                if (n >= tiles) break;
+                if (n >= high) break;
                 const float other = ml[wave][n][0][lane], top = fmaxf(mx[n], other), sub = top == -__builtin_inff() ? 0.f : top;
                 const float f = exp2_fast(mx[n] - sub), h = exp2_fast(other - sub);
                 mx[n] = top;
@@ -411,12 +488,11 @@ __global__ __launch_bounds__(64) void shared_join_kernel(KvShared s) {
     constexpr uint32_t D = 64 * DW, kLanes = 16 * DW, kHeads = 64 / kLanes > 0 ? 64 / kLanes : 1;
     const uint32_t seq = blockIdx.x / a.max_new, i = blockIdx.x % a.max_new;
     const uint32_t qh = blockIdx.y * kHeads + threadIdx.x / kLanes, ch = 4 * (threadIdx.x % kLanes);
-    const int32_t s0 = a.starts[seq], s1 = a.starts[seq + 1];
-    if (s0 < 0 || s1 < s0 || (uint32_t)s1 > a.total || (uint32_t)(s1 - s0) > a.max_new) return;
-    if (i >= (uint32_t)(s1 - s0) || qh >= a.heads || threadIdx.x >= kHeads * kLanes) return;
-    const uint32_t tok = (uint32_t)s0 + i;
+    const int4 r = *(const int4*)(s.info + 4 + 8 * (s.groups + seq));
+    if (i * a.group >= record_rows(s, r, a.max_new) || qh >= a.heads || threadIdx.x >= kHeads * kLanes) return;
+    const uint32_t tok = (uint32_t)r.x + i;
     const float* pp = a.part + ((uint64_t)tok * a.heads + qh) * (s.pre + s.own) * (D + 4);
-    const bool grouped = s.shared[seq] >= (int32_t)kKvTile;
+    const bool grouped = r.z >= (int32_t)kKvTile;
     const float n0 = pp[D + 2], n1 = pp[s.pre * (D + 4) + D + 2];
     const uint32_t pre = grouped ? min(__builtin_bit_cast(uint32_t, n0), s.pre) : 0u;
     const uint32_t n = pre + min(__builtin_bit_cast(uint32_t, n1), s.own);

@@ -388,7 +388,7 @@ class KvBatch:
         self.max_len = min(max_len or cache.max_pages * cache.page_tokens, cache.max_pages * cache.page_tokens)
         width = -(-self.max_len // cache.page_tokens)
         self._counted = counts is not None
-        sizes = [4 * (self.n_groups + 1), 2 * total, n + 1, total, n * width, n, n, n]
+        sizes = [4 + 8 * (self.n_groups + n), 2 * total, n + 1, total, n * width, n, n, n]
         with _on(stream):        # zeroed: the plan's counter is 0 before its first call
             info, slots, self.starts, self.places, table, self.lead, self.shared, self.rows = \
                 torch.zeros(sum(sizes), dtype=_INT32, device=cache.device).split(sizes)

@@ -231,14 +231,15 @@ def test_plans_that_no_longer_hold_read_nothing_out_of_range():
     b = kv.KvBatch(cache, _ids(*rows))
     cache.free(_ids(*rows))
     cache.attend_shared(0, q, b)
-    for name, value in (("places", 1 << 30), ("shared", 1 << 30), ("rows", 99), ("rows", -1), ("starts", 99)):
+    for value in (1 << 30, -5):
         b.update(_ids(*rows))
-        getattr(b, name).fill_(value)
+        b.places.fill_(value)
         cache.attend_shared(0, q, b)
-    b.update(_ids(*rows))
-    for column, value in ((0, 77), (1, 1 << 20), (2, 1 << 30), (3, 1 << 20), (0, -9)):
-        b._info.view(-1, 4)[1:, column] = value
-        cache.attend_shared(0, q, b)
+    for word in range(6):
+        for value in (77, 1 << 20, 1 << 30, -9):
+            b.update(_ids(*rows))
+            b._info[4:].view(-1, 8)[:, word] = value
+            cache.attend_shared(0, q, b)
     torch.cuda.synchronize()
 
 
