@@ -39,14 +39,15 @@ bs_status shape(const bs_beam_args* x, bsd::BeamArgs& a) {
     // below 2^-100 every capped logit is 0: neither overflows a constant
     a.softcap = x->softcap > 0x1p100f ? 0.f : x->softcap > 0.f ? std::max(x->softcap, 0x1p-100f) : 0.f;
     a.stride = x->row_stride;
-    // A part of a row is 512 threads times 1, 2, 4 or 8 vectors.  Small parts
+    // A part of a row is 512 threads times 1, 2 or 4 vectors (8 of fp32 where 64
+    // parts of 4 do not hold a row).  Small parts
     // spread few rows over the GPU, large ones cost less per logit (a part's
     // reductions and list are the same for all): small ones as long as there
     // are no more than some 8 workgroups to a CU, and at most 64 to a row.
     const uint32_t per = a.half ? 8 : 4;
     for (a.vectors = 1;; a.vectors *= 2) {
         a.chunks = (x->vocab + per - 1 + bsd::kBeamThreads * per * a.vectors - 1) / (bsd::kBeamThreads * per * a.vectors);
-        if (a.vectors == 8 || (a.chunks <= bsd::kBeamChunks && (uint64_t)a.chunks * a.batch * a.beams <= 2048)) break;
+        if (a.chunks <= bsd::kBeamChunks && (a.vectors >= 4 || (uint64_t)a.chunks * a.batch * a.beams <= 2048)) break;
     }
     return BS_OK;
 }

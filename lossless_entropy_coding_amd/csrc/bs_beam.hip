@@ -26,6 +26,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "bs_beam_device.h"
 
 using namespace bsd;
@@ -45,14 +47,34 @@ __device__ __forceinline__ float dpp(float x) {
     return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), CTRL, 0xF, 0xF, true));
 }
 
+// x of this lane and of the one 32 (16) away, in either order
+struct Pair {
+    float a, b;
+};
+
+__device__ __forceinline__ Pair swap32(float x) {
+    const uint32_t u = __builtin_bit_cast(uint32_t, x);
+    auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    const uint32_t a = r[0], b = r[1];
+    return Pair{__builtin_bit_cast(float, a), __builtin_bit_cast(float, b)};
+}
+
+__device__ __forceinline__ Pair swap16(float x) {
+    const uint32_t u = __builtin_bit_cast(uint32_t, x);
+    auto r = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+    const uint32_t a = r[0], b = r[1];
+    return Pair{__builtin_bit_cast(float, a), __builtin_bit_cast(float, b)};
+}
+
 // the maximum (sum) over a wave, in every lane
 __device__ __forceinline__ float wave_max(float x) {
     x = fmaxf(x, dpp<0x128>(x));             // rotations of a row of 16 by 8, 4, 2, 1
     x = fmaxf(x, dpp<0x124>(x));
     x = fmaxf(x, dpp<0x122>(x));
     x = fmaxf(x, dpp<0x121>(x));
-    x = fmaxf(x, __shfl_xor(x, 16));
-    return fmaxf(x, __shfl_xor(x, 32));
+    Pair p = swap16(x);
+    p = swap32(fmaxf(p.a, p.b));
+    return fmaxf(p.a, p.b);
 }
 
 __device__ __forceinline__ float wave_sum(float x) {
@@ -60,8 +82,9 @@ __device__ __forceinline__ float wave_sum(float x) {
     x += dpp<0x124>(x);
     x += dpp<0x122>(x);
     x += dpp<0x121>(x);
-    x += __shfl_xor(x, 16);
-    return x + __shfl_xor(x, 32);
+    Pair p = swap16(x);
+    p = swap32(p.a + p.b);
+    return p.a + p.b;
 }
 
 __device__ __forceinline__ double wave_sum(double x) {
@@ -79,15 +102,18 @@ __device__ __forceinline__ double wave_max(double x) {
     return x;
 }
 
-// The exponential of a logit against a part's reference.  Without a cap (CAP
-// 0) the reference is the largest logit.  With one of up to 256 (CAP 1), y =
-// c - 2 c r, r = 1 / (e^(2 x / c) + 1), and exp(y - y_ref) = 2^(ref - B r) with
-// B = 2 c log2 e and ref = B r of the largest logit: one rounding, and what ref
-// loses to it is the same in every term.  Its error grows with the cap, so
-// above (CAP 2) the series of tanh to the seventh power takes over where x is
-// below c / 4 (the next term is 2^-21.5 of it there), and ref is y of the
-// largest logit.
-constexpr float kShortCap = 256.f;
+// The exponential of a logit against a part's reference.
+//   CAP 0 (no cap): 2^((x - m) L), L = log2 e in fp32, m the largest logit.
+//   CAP 1 (c up to 40): y = c - 2 c r, r = 1 / (e^(2 x / c) + 1); 2^(-B r), B = 2
+//     c log2 e in fp32, which is e^(y - c): no less than 2^-116, so that it
+//     needs no maximum.
+//   CAP 2: 2^((y - y(m)) L).  Where x is below c / 4 y is the series of tanh to
+//     the seventh power (the next term is 2^-21.5 of it there): the other
+//     form's error is 2^-22 of the cap, whatever the logit.
+// reference() is, in 64 bits, what the exponential of the part's largest logit
+// was taken against, with what B lost to rounding: the loss is then none
+// there, and small near it.
+constexpr float kShortCap = 40.f;
 
 struct Capped {
     float c, in, b;
@@ -98,15 +124,36 @@ struct Capped {
         const float p = x * (1.f + u2 * (-1.f / 3 + u2 * (2.f / 15 + u2 * (-17.f / 315))));
         return fabsf(u) < 0.25f ? p : c - 2.f * c * r(x);
     }
-    template <int CAP>
-    __device__ __forceinline__ float ref(float top) const { return CAP == 0 ? top : CAP == 1 ? b * r(top) : y(top); }
 };
+
+// what against() takes of the largest logit
+template <int CAP>
+__device__ __forceinline__ float ref_of(const Capped& k, float top) {
+    return CAP == 0 ? top : CAP == 1 ? 0.f : k.y(top);
+}
 
 template <int CAP>
 __device__ __forceinline__ float against(const Capped& k, float x, float ref) {
-    if (CAP == 0) return __builtin_amdgcn_exp2f((x - ref) * kLog2e);
-    const float t = CAP == 1 ? __builtin_fmaf(-k.b, k.r(x), ref) : (k.y(x) - ref) * kLog2e;
-    return x == minus_inf() ? 0.f : __builtin_amdgcn_exp2f(t);
+    if (CAP == 1) return __builtin_amdgcn_exp2f(k.r(x) * -k.b);
+    return __builtin_amdgcn_exp2f(((CAP == 0 ? x : k.y(x)) - ref) * kLog2e);
+}
+
+// a capped logit in 64 bits, and r of CAP 1 (whose c is small: c - 2 c r loses
+// nothing to speak of near 0)
+struct Exact {
+    double y, r;
+};
+
+template <int CAP>
+__device__ __forceinline__ Exact exact(const Capped& k, float x) {
+    if (CAP == 0) return Exact{(double)x, 0.};
+    const double c = k.c, r = 1. / (exp(2. / c * (double)x) + 1.);
+    return Exact{CAP == 1 ? c - 2. * c * r : c * tanh((double)x / c), r};
+}
+
+template <int CAP>
+__device__ __forceinline__ double reference(const Capped& k, float top, const Exact& e) {
+    return CAP == 1 ? e.y + (double)k.b * 0.6931471805599453 * e.r : (double)ref_of<CAP>(k, top);
 }
 
 // larger logits first, of equal ones the lower token
@@ -120,10 +167,16 @@ __device__ __forceinline__ uint32_t ordered(float x) {
     return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
 }
 
+// the logit of such a number (what would be below -infinity is -infinity)
+__device__ __forceinline__ float unordered(uint32_t o) {
+    const uint32_t u = o & 0x80000000u ? o ^ 0x80000000u : ~o;
+    return fmaxf(__builtin_bit_cast(float, u), minus_inf());
+}
+
 // grid: (parts, rows)
 template <bool HALF, int NV, int CAP>
-__global__ __launch_bounds__(kBeamThreads) void beam_rows_kernel(BeamArgs a) {
-    constexpr uint32_t VE = HALF ? 8 : 4, E = NV * VE, CH = kBeamThreads * E, NW = kBeamThreads / 64;
+__global__ __launch_bounds__(kBeamThreads, CAP == 2 ? 4 : 6) void beam_rows_kernel(BeamArgs a) {
+    constexpr uint32_t VE = HALF ? 8 : 4, CH = kBeamThreads * NV * VE, NW = kBeamThreads / 64, NL = NV < 4 ? NV : 4;
     __shared__ __attribute__((aligned(16))) float maxima[kBeamThreads];
     __shared__ float sums[NW];
     __shared__ float bound;
@@ -138,56 +191,105 @@ __global__ __launch_bounds__(kBeamThreads) void beam_rows_kernel(BeamArgs a) {
 
     // p counts from the 16-B boundary at or before the row's first logit
     constexpr uint32_t esize = HALF ? 2 : 4;
-    const uint8_t* base = (const uint8_t*)a.logits + (uint64_t)row * a.stride * esize;
-    const uint32_t skip = ((uint32_t)(uintptr_t)base & 15u) / esize, stop = a.vocab + skip;
-    base -= skip * esize;
-    const uint32_t p0 = chunk * CH + t * VE;
-    v4u x[NV];
+    const uint64_t from = (uint64_t)row * a.stride * esize;
+    const uint32_t skip = ((uint32_t)((uintptr_t)a.logits + from) & 15u) / esize, stop = a.vocab + skip;
+    const uint8_t* const base = (const uint8_t*)a.logits + from - skip * esize;
+    const bool inside = chunk * CH >= skip && chunk * CH + CH <= stop;
+    uint32_t again = 0;                                              // 0, but see forget()
+    auto place = [&](uint32_t j) { return chunk * CH + (j * kBeamThreads + t) * VE + again; };
+    auto load = [&](uint32_t j) { return *(const v4u*)(base + (uint64_t)place(j) * esize); };
+    // the same where the part reaches past the row: -infinity there
+    auto load_edge = [&](uint32_t j) {
+        const uint32_t p = place(j);
+        if (p >= skip && p + VE <= stop) return load(j);
+        v4u x;
 #pragma unroll
-    for (uint32_t j = 0; j < NV; j++) {
-        const uint32_t p = p0 + j * kBeamThreads * VE;
-        if (p >= skip && p + VE <= stop) {
-            x[j] = *(const v4u*)(base + (uint64_t)p * esize);
-            continue;
-        }
-#pragma unroll
-        for (uint32_t w = 0; w < 4; w++) {                           // the ends of a row, and what is past it
+        for (uint32_t w = 0; w < 4; w++) {
             if (HALF) {
                 const uint32_t e = p + 2 * w;
                 const uint32_t lo = e >= skip && e < stop ? ((const uint16_t*)base)[e] : 0xFF80u;
                 const uint32_t hi = e + 1 >= skip && e + 1 < stop ? ((const uint16_t*)base)[e + 1] : 0xFF80u;
-                x[j][w] = lo | hi << 16;
+                x[w] = lo | hi << 16;
             } else {
                 const uint32_t e = p + w;
-                x[j][w] = e >= skip && e < stop ? ((const uint32_t*)base)[e] : 0xFF800000u;
+                x[w] = e >= skip && e < stop ? ((const uint32_t*)base)[e] : 0xFF800000u;
             }
         }
-    }
-    auto logit = [&](uint32_t e) {                                   // e-th of the thread's
-        const uint32_t w = HALF ? x[e / 8][e % 8 / 2] : x[e / 4][e % 4];
+        return x;
+    };
+    // The compiler is not to keep what it has read for when it is read again:
+    // it would take the registers of the waves that hide the loads.
+    auto forget = [&]() { asm volatile("" : "+v"(again)); };
+    auto logit = [&](const v4u& x, uint32_t e) {                     // e-th of a vector
+        const uint32_t w = HALF ? x[e / 2] : x[e];
         return __builtin_bit_cast(float, HALF ? (e & 1 ? w & 0xFFFF0000u : w << 16) : w);
     };
-    auto token = [&](uint32_t e) { return p0 + (e / VE) * kBeamThreads * VE + e % VE - skip; };
 
-    float mine = minus_inf();
+    // One pass: each vector's largest logit, the thread's, and its sum against
+    // it.  What was read is not kept: few logits are needed again.
+    const Capped k(a.softcap);
+    float sum = 0.f, best[NV], mine = minus_inf(), ref = 0.f;
+    auto take = [&](const v4u& x) {
+        float most = minus_inf();
 #pragma unroll
-    for (uint32_t e = 0; e < E; e++) mine = fmaxf(mine, logit(e));
+        for (uint32_t e = 0; e < VE; e += 2) most = fmaxf(fmaxf(logit(x, e), logit(x, e + 1)), most);
+        if (CAP != 1) {
+            const float now = fmaxf(mine, most), to = now > minus_inf() ? ref_of<CAP>(k, now) : 0.f;
+            sum *= mine > minus_inf() ? __builtin_amdgcn_exp2f((ref - to) * kLog2e) : 1.f;   // nothing yet, or NaN
+            ref = to;
+        }
+        mine = fmaxf(mine, most);
+#pragma unroll
+        for (uint32_t e = 0; e < VE; e++) {
+            const float v = logit(x, e), f = against<CAP>(k, v, ref);
+            sum += CAP == 2 && v == minus_inf() ? 0.f : f;
+        }
+        return most;
+    };
+    if (inside) {
+        v4u x[NL], y[NL];
+#pragma unroll
+        for (uint32_t j = 0; j < NL; j++) x[j] = load(j);
+#pragma unroll
+        for (uint32_t j0 = 0; j0 < NV; j0 += NL) {
+            if (j0 + NL < NV) {
+#pragma unroll
+                for (uint32_t j = 0; j < NL; j++) y[j] = load(j0 + NL + j);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+#pragma unroll
+            for (uint32_t j = 0; j < NL; j++) {
+                best[j0 + j] = take(x[j]);
+                __builtin_amdgcn_sched_barrier(0);                   // few logits at a time: registers for more waves
+            }
+#pragma unroll
+            for (uint32_t j = 0; j < NL; j++) x[j] = y[j];
+        }
+    } else {
+#pragma unroll 1
+        for (uint32_t j = 0; j < NV; j++) take(load_edge(j));
+    }
     maxima[t] = mine;
     __syncthreads();
     float group = maxima[lane];
 #pragma unroll
     for (uint32_t w = 1; w < NW; w++) group = fmaxf(group, maxima[64 * w + lane]);
     const float top = wave_max(group);
-    // the bound of the list: of equal maxima the lower place counts as the larger
+    // The bound of the list: the K-th largest maximum.  Of 64 groups, its upper
+    // 26 bits as a whole number that grows with it, the others 0: with the lane
+    // in their place no two are equal, and a comparison is one instruction.
     if (a.best <= 16) {
         if (wave == 0) {
+            __shared__ __attribute__((aligned(16))) uint32_t keys[64];
+            const uint32_t key = (ordered(group) & ~63u) | lane;
+            keys[lane] = key;
             uint32_t rank = 0;
 #pragma unroll
-            for (uint32_t i = 0; i < 64; i++) {
-                const float o = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, group), i));
-                rank += o > group || (o == group && i < lane);
+            for (uint32_t i = 0; i < 64; i += 4) {
+                const uint4 o = *(const uint4*)(keys + i);
+                rank += (o.x > key) + (o.y > key) + (o.z > key) + (o.w > key);
             }
-            if (rank == a.best - 1) bound = group;
+            if (rank == a.best - 1) bound = unordered(key & ~63u);
         }
     } else {
         uint32_t rank = 0;
@@ -198,43 +300,63 @@ __global__ __launch_bounds__(kBeamThreads) void beam_rows_kernel(BeamArgs a) {
         }
         if (rank == a.best - 1) bound = mine;
     }
-    const Capped k(a.softcap);
-    const float ref = k.ref<CAP>(top);
-    float sum = 0.f;
-    if (top > minus_inf()) {
+    if (CAP != 1) {
+        if (mine > minus_inf()) sum *= __builtin_amdgcn_exp2f((ref - ref_of<CAP>(k, top)) * kLog2e);
+    } else if (2.f * k.c * (1.f - k.r(top)) < 32.f) {
+        // A logit of -infinity has counted as e^(-2 c).  Where the largest is no
+        // more than e^32 of that, a part of 32768 of them would show (2^-30).
+        sum = 0.f;
+        forget();
+#pragma unroll 1
+        for (uint32_t j = 0; j < NV; j++) {
+            const v4u x = load_edge(j);
 #pragma unroll
-        for (uint32_t e = 0; e < E; e++) sum += against<CAP>(k, logit(e), ref);
-    } else {                                                         // nothing is left, or all of it is NaN
-#pragma unroll
-        for (uint32_t e = 0; e < E; e++) sum += logit(e) == minus_inf() ? 0.f : __builtin_nanf("");
+            for (uint32_t e = 0; e < VE; e++) {
+                const float v = logit(x, e), f = against<1>(k, v, 0.f);
+                sum += v == minus_inf() ? 0.f : f;
+            }
+        }
     }
     sum = wave_sum(sum);
     if (lane == 0) sums[wave] = sum;
     __syncthreads();
     const float least = bound;
-    if (mine >= least && mine > minus_inf()) {
+    forget();
+    auto pick = [&](const v4u& x, uint32_t j) {
 #pragma unroll
-        for (uint32_t e = 0; e < E; e++) {
-            const float f = logit(e);
+        for (uint32_t e = 0; e < VE; e++) {
+            const float f = logit(x, e);
             if (f >= least && f > minus_inf()) {
                 const uint32_t at = atomicAdd(&count, 1u);
-                if (at < kList) list[at] = BeamBest{f, token(e)};
+                if (at < kList) list[at] = BeamBest{f, place(j) + e - skip};
             }
         }
+    };
+    if (inside) {
+#pragma unroll
+        for (uint32_t j = 0; j < NV; j++)
+            if (best[j] >= least && best[j] > minus_inf()) pick(load(j), j);
+    } else if (mine >= least && mine > minus_inf()) {
+#pragma unroll 1
+        for (uint32_t j = 0; j < NV; j++) pick(load_edge(j), j);
     }
     __syncthreads();
     uint32_t n = count;
     if (n > kList) {
-        // more than the list holds: the K-th largest logit bit by bit, then
-        // among those equal to it the last token that is taken
+        // More than the list holds: the K-th largest logit bit by bit, then
+        // among those equal to it the last token that is taken.
         uint32_t turn = 0;
-        auto how_many = [&](auto test) {                             // of the part's logits; every thread takes part
-            uint32_t c = 0;
-#pragma unroll
-            for (uint32_t e = 0; e < E; e++) {
-                const float f = logit(e);
-                c += f > minus_inf() && test(ordered(f), token(e));
+        const uint32_t first = max(chunk * CH, skip), end = min(chunk * CH + CH, stop);
+        auto each = [&](auto&& f) {
+            for (uint32_t p = first + t; p < end; p += kBeamThreads) {
+                const uint32_t w = HALF ? (uint32_t)((const uint16_t*)base)[p] << 16 : ((const uint32_t*)base)[p];
+                const float v = __builtin_bit_cast(float, w);
+                if (v > minus_inf()) f(v, p - skip);
             }
+        };
+        auto how_many = [&](auto&& test) {                           // of the part's logits; every thread takes part
+            uint32_t c = 0;
+            each([&](float v, uint32_t id) { c += test(ordered(v), id); });
 #pragma unroll
             for (int s = 32; s; s >>= 1) c += __shfl_xor(c, s);
             if (lane == 0) atomicAdd(&total[turn & 1], c);
@@ -253,12 +375,10 @@ __global__ __launch_bounds__(kBeamThreads) void beam_rows_kernel(BeamArgs a) {
             if (how_many([&](uint32_t o, uint32_t v) { return o == key && v < (last | bit); }) < equal) last |= bit;
         if (t == 0) count = 0;
         __syncthreads();
-#pragma unroll
-        for (uint32_t e = 0; e < E; e++) {
-            const float f = logit(e);
-            const uint32_t o = ordered(f), v = token(e);
-            if (f > minus_inf() && (o > key || (o == key && v <= last))) list[atomicAdd(&count, 1u)] = BeamBest{f, v};
-        }
+        each([&](float v, uint32_t id) {
+            const uint32_t o = ordered(v);
+            if (o > key || (o == key && id <= last)) list[atomicAdd(&count, 1u)] = BeamBest{v, id};
+        });
         __syncthreads();
         n = count;
     }
@@ -266,14 +386,20 @@ __global__ __launch_bounds__(kBeamThreads) void beam_rows_kernel(BeamArgs a) {
     for (uint32_t i = t; i < n; i += kBeamThreads) {
         const BeamBest b = list[i];
         uint32_t rank = 0;
-        for (uint32_t j = 0; j < n; j++) rank += better(list[j], b);
+        for (uint32_t j0 = 0; j0 < n; j0 += 8) {                     // (the list's length is a multiple of 8)
+            BeamBest o[8];
+#pragma unroll
+            for (uint32_t j = 0; j < 8; j++) o[j] = list[j0 + j];
+#pragma unroll
+            for (uint32_t j = 0; j < 8; j++) rank += j0 + j < n && better(o[j], b);
+        }
         if (rank < a.best) a.bests[at * a.best + rank] = b;
     }
     if (t == 0) {
         float s = 0.f;
 #pragma unroll
         for (uint32_t w = 0; w < NW; w++) s += sums[w];
-        a.parts[at] = BeamPart{top, ref, s, min(n, a.best)};
+        a.parts[at] = BeamPart{top, s, min(n, a.best), 0u};
     }
 }
 
@@ -289,34 +415,38 @@ __global__ __launch_bounds__(kBeamThreads) void beam_merge_kernel(BeamArgs a) {
     double* scores = (double*)dynamic;
     uint32_t* tokens = (uint32_t*)(scores + a.beams * a.best);
     const Capped k(a.softcap);
-    const double c = a.softcap;
-    auto cap = [&](double x) { return CAP ? c * tanh(x / c) : x; };
 
     for (uint32_t w = wave; w < a.beams; w += NW) {
         const uint32_t row = row0 + w;
+        // all that the beam may need is asked for at once
         const float score = a.scores[row];
+        const int32_t ended = a.done ? a.done[row] : 0;
+        const uint64_t mine0 = (uint64_t)row * a.chunks + min(lane, a.chunks - 1);
+        BeamPart p = a.parts[mine0];
+        const BeamBest* from = a.bests + mine0 * a.best;
+        BeamBest early[kHeads];
+#pragma unroll
+        for (uint32_t i = 0; i < kHeads; i++) early[i] = from[min(i, a.best - 1)];
         double* list = scores + w * a.best;
         uint32_t* ids = tokens + w * a.best;
         uint32_t n = 0;
         if (!(fabsf(score) < __builtin_inff())) {
-        } else if (a.done && a.done[row] != 0) {
+        } else if (ended != 0) {
             if (lane == 0) {
                 list[0] = score;
                 ids[0] = (uint32_t)a.eos;
             }
             n = 1;
         } else {
-            BeamPart p{minus_inf(), 0.f, 0.f, 0u};
-            const BeamBest* from = a.bests + ((uint64_t)row * a.chunks + lane) * a.best;
-            if (lane < a.chunks) {
-                p = a.parts[(uint64_t)row * a.chunks + lane];
-                for (uint32_t i = 0; i < min(p.n, kHeads); i++) heads[wave][lane][i] = from[i];
-            }
+            if (lane >= a.chunks) p = BeamPart{minus_inf(), 0.f, 0u, 0u};
+#pragma unroll
+            for (uint32_t i = 0; i < kHeads; i++) heads[wave][lane][i] = early[i];
             const float top = wave_max(p.max);
             const bool sound = fabsf(p.sum) < __builtin_inff() && p.max < __builtin_inff();
             if (__builtin_amdgcn_ballot_w64(!sound) == 0 && top > minus_inf()) {
-                const double ytop = cap(top), ref = CAP == 1 ? c - 2. * c * ((double)p.ref / (double)k.b) : (double)p.ref;
-                const double part = p.max > minus_inf() ? exp(ref - ytop) : 0.;
+                const Exact best = exact<CAP>(k, p.max > minus_inf() ? p.max : top);
+                const double ytop = wave_max(best.y);
+                const double part = p.max > minus_inf() ? exp(reference<CAP>(k, p.max, best) - ytop) : 0.;
                 double sum = wave_sum((double)p.sum * part);
                 // the best of all parts: a lane's own next one, `at` of its list
                 uint32_t at = 0;
@@ -347,9 +477,10 @@ __global__ __launch_bounds__(kBeamThreads) void beam_merge_kernel(BeamArgs a) {
                 double y[2];
 #pragma unroll
                 for (uint32_t h = 0; h < 2; h++) {
-                    y[h] = cap(mine[h]);
+                    if (64 * h >= n) break;
+                    y[h] = exact<CAP>(k, mine[h]).y;
                     if (CAP) {
-                        const float rf = __shfl(p.ref, of[h]);
+                        const float rf = ref_of<CAP>(k, __shfl(p.max, of[h]));
                         const double f = __shfl(part, of[h]);
                         const double more = exp(y[h] - ytop) - (double)against<CAP>(k, mine[h], rf) * f;
                         sum += wave_sum(64 * h + lane < n ? more : 0.);
@@ -367,32 +498,53 @@ __global__ __launch_bounds__(kBeamThreads) void beam_merge_kernel(BeamArgs a) {
         if (lane == 0) found[w] = n;
     }
     __syncthreads();
+    const double inf = __builtin_inf();
+    auto write = [&](uint32_t rank, double score, int32_t v, uint32_t w) {
+        const uint64_t to = (uint64_t)blockIdx.x * a.keep + rank;
+        a.scores_out[to] = (float)score;
+        a.tokens[to] = v;
+        a.parents[to] = (int32_t)(row0 + w);
+        a.done_out[to] = v == a.eos || (a.done && a.done[row0 + w] != 0);
+    };
+    auto nothing = [&](uint32_t rank) {
+        const uint64_t to = (uint64_t)blockIdx.x * a.keep + rank;
+        a.scores_out[to] = minus_inf();
+        a.tokens[to] = a.parents[to] = -1;
+        a.done_out[to] = 0;
+    };
+    const uint32_t all = a.beams * a.best;
+    if (all <= kBeamThreads / 2) {
+        // few: each finds its place by counting those before it
+        if (t >= all) return;
+        const uint32_t w = t / a.best, at = t % a.best;
+        const double mine = at < found[w] ? scores[t] : -inf;
+        uint32_t rank = 0;
+        for (uint32_t o = 0, i = 0; o < a.beams; o++) {
+            const uint32_t n = found[o];
+            for (uint32_t x = 0; x < a.best; x++, i++) rank += x < n && (scores[i] > mine || (scores[i] == mine && i < t));
+        }
+        uint32_t total = 0;
+        for (uint32_t o = 0; o < a.beams; o++) total += found[o];
+        if (at < found[w] && rank < a.keep) write(rank, mine, (int32_t)tokens[t], w);
+        for (uint32_t i = total + t; i < a.keep; i += all) nothing(i);
+        return;
+    }
     if (wave != 0) return;
     // the beams' lists, a lane each
     const uint32_t n = lane < a.beams ? found[lane] : 0u;
-    const double inf = __builtin_inf();
     uint32_t at = 0;
     double head = n ? scores[lane * a.best] : -inf;
     for (uint32_t i = 0; i < a.keep; i++) {
         const double m = wave_max(head);
-        const uint64_t to = (uint64_t)blockIdx.x * a.keep + i;
         if (!(m > -inf)) {
-            if (lane == 0) {
-                a.scores_out[to] = minus_inf();
-                a.tokens[to] = a.parents[to] = -1;
-                a.done_out[to] = 0;
-            }
+            if (lane == 0) nothing(i);
             continue;
         }
         const uint32_t who = (uint32_t)__builtin_ctzll(__builtin_amdgcn_ballot_w64(head == m));
         if (lane == who) {
-            const int32_t v = (int32_t)tokens[lane * a.best + at];
+            write(i, m, (int32_t)tokens[lane * a.best + at], lane);
             at++;
             head = at < n ? scores[lane * a.best + at] : -inf;
-            a.scores_out[to] = (float)m;
-            a.tokens[to] = v;
-            a.parents[to] = (int32_t)(row0 + lane);
-            a.done_out[to] = v == a.eos || (a.done && a.done[row0 + lane] != 0);
         }
     }
 }
@@ -404,7 +556,8 @@ void rows(const BeamArgs& a, hipStream_t st) {
         case 1: hipLaunchKernelGGL((beam_rows_kernel<HALF, 1, CAP>), grid, block, 0, st, a); break;
         case 2: hipLaunchKernelGGL((beam_rows_kernel<HALF, 2, CAP>), grid, block, 0, st, a); break;
         case 4: hipLaunchKernelGGL((beam_rows_kernel<HALF, 4, CAP>), grid, block, 0, st, a); break;
-        default: hipLaunchKernelGGL((beam_rows_kernel<HALF, 8, CAP>), grid, block, 0, st, a); break;
+        case 8: hipLaunchKernelGGL((beam_rows_kernel<HALF, 8, CAP>), grid, block, 0, st, a); break;
+        default: hipLaunchKernelGGL((beam_rows_kernel<HALF, 16, CAP>), grid, block, 0, st, a); break;
     }
 }
 

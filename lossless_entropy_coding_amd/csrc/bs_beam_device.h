@@ -12,9 +12,9 @@ constexpr uint32_t kBeamChunks = 64;         // parts of a row at most: one to a
 // what the first launch leaves of a part of a row, before its best logits
 struct BeamPart {
     float max;       // the largest logit, uncapped
-    float ref;       // what the exponentials are taken against (see bs_beam.hip)
-    float sum;       // of the exponentials; not finite where a logit is not
+    float sum;       // of the exponentials against it (see bs_beam.hip); not finite where a logit is not
     uint32_t n;      // how many of the best follow
+    uint32_t unused;
 };
 
 struct BeamBest {

@@ -181,15 +181,16 @@ __global__ __launch_bounds__(64 * kWaves, 2) void shared_kernel(KvShared s, uint
     // Entries of the table, then keys, then values are loaded a step ahead:
     // keys of the wave's next tile when this one's are multiplied, its values
     // when this one's are, into the same registers.
+    // (Always the same loads in the same order, so that waiting for keys never
+    // waits for values: entries come before those, and where there is no tile
+    // or token the last one is read again.)
     int32_t pk = -1, pv = -1;                                       // entries of the tile to be loaded
     auto entries = [&](uint32_t i) {
-        pk = pv = -1;
-        if (i >= i1) return;
-        const uint32_t tile0 = pt.at(i) * kKvTile, ck = tile0 + 16 * (m >> 2), cv = tile0 + 16 * g;
-        if (ck < end) pk = trow[ck >> c.lp];
-        if (cv < end) pv = trow[cv >> c.lp];
+        const uint32_t tile0 = pt.at(min(i, i1 - 1)) * kKvTile, last = (end - 1) >> c.lp;
+        pk = trow[min((tile0 + 16 * (m >> 2)) >> c.lp, last)];
+        pv = trow[min((tile0 + 16 * g) >> c.lp, last)];
     };
-    entries(i0 + wave);
+    if (i0 < i1) entries(i0 + wave);
 
     // this lane's rows: row m of each row tile
     uint32_t tok[NR], qh[NR];
@@ -224,8 +225,8 @@ __global__ __launch_bounds__(64 * kWaves, 2) void shared_kernel(KvShared s, uint
     Tile now{}, next{};
     auto locate = [&](uint32_t i) {
         const uint32_t tile0 = pt.at(i) * kKvTile, ck = tile0 + 16 * (m >> 2), cv = tile0 + 16 * g;
-        next.ok = (uint32_t)pv < c.n_pages;
-        const uint32_t ik = (uint32_t)pk < c.n_pages ? (uint32_t)pk : 0u, iv = next.ok ? (uint32_t)pv : 0u;
+        next.ok = cv < end && (uint32_t)pv < c.n_pages;
+        const uint32_t ik = (uint32_t)pk < c.n_pages ? (uint32_t)pk : 0u, iv = (uint32_t)pv < c.n_pages ? (uint32_t)pv : 0u;
         next.k = a.k + (uint64_t)ik * c.side_bytes + hoff + (uint64_t)((ck + (m & 3u)) & (c.page - 1)) * D + 16 * g;
         next.v = a.v + (uint64_t)iv * c.side_bytes + hoff + (uint64_t)m * c.page + (cv & (c.page - 1));
         // e4m3: the scale of keys goes into the operand, so it is that of the
@@ -247,9 +248,9 @@ __global__ __launch_bounds__(64 * kWaves, 2) void shared_kernel(KvShared s, uint
         locate(i0 + wave);
         load_keys(next, HALF ? 2 : 0, 4);
         if (HALF) load_keys(next, 0, 2);
+        entries(i0 + wave + kWaves);
         load_values(next);
         now = next;
-        entries(i0 + wave + kWaves);
     }
     const bool every = __builtin_amdgcn_ballot_w64(pos[0] < 0 || pos[NR - 1] < 0) == 0;
     __syncthreads();
@@ -305,6 +306,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void shared_kernel(KvShared s, uint
             if (more) {
                 locate(i + kWaves);
                 load_keys(next, 2, 4);
+                entries(i + 2 * kWaves);
             }
             qk(0, 2);
 #pragma unroll
@@ -314,6 +316,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void shared_kernel(KvShared s, uint
             if (more) {
                 locate(i + kWaves);
                 load_keys(next, 0, 4);
+                entries(i + 2 * kWaves);
             }
         }
         __builtin_amdgcn_sched_barrier(0);
@@ -389,16 +392,20 @@ __global__ __launch_bounds__(64 * kWaves, 2) void shared_kernel(KvShared s, uint
             __builtin_amdgcn_sched_barrier(0);
         }
         // what no row sees may hold anything: its values count as 0
-        const bool cut = cv + 16 > end || !okv;
         const int32_t left = okv ? (int32_t)(end - cv) : 0;          // tokens of the chunk that are kept
-        auto pv_block = [&](v4u w, uint32_t d) {
-            if (cut) {
+        if (__builtin_amdgcn_ballot_w64(left < 16) != 0) {
+            uint32_t mask[4];
 #pragma unroll
-                for (int e = 0; e < 4; e++) {
-                    const int32_t nb = left - 4 * e;
-                    w[e] &= nb >= 4 ? ~0u : nb <= 0 ? 0u : (1u << (8 * nb)) - 1u;
-                }
+            for (int e = 0; e < 4; e++) mask[e] = left >= 4 * e + 4 ? ~0u : left <= 4 * e ? 0u : (1u << (8 * (left - 4 * e))) - 1u;
+            const v4u keep = {mask[0], mask[1], mask[2], mask[3]};
+#pragma unroll
+            for (uint32_t d = 0; d < VS; d++) vr[d] &= keep;
+            if (HALF) {
+#pragma unroll
+                for (uint32_t d = 0; d < VS; d++) kr[d / DW][d % DW] &= keep;
             }
+        }
+        auto pv_block = [&](v4u w, uint32_t d) {
             const float f = E4M3 ? vscale : 1.f;
             const bf16x8 v0 = widen8<E4M3>(w.x, w.y, f), v1 = widen8<E4M3>(w.z, w.w, f);
             if (TWO) {
@@ -423,7 +430,6 @@ __global__ __launch_bounds__(64 * kWaves, 2) void shared_kernel(KvShared s, uint
             if (more) load_keys(next, 0, 2);
         }
         now = next;
-        if (more) entries(i + 2 * kWaves);
         __builtin_amdgcn_sched_barrier(0);
     };
     // Two row tiles share an operand, and P enters in one part, in large
