@@ -43,11 +43,11 @@ bs_status shape(const bs_beam_args* x, bsd::BeamArgs& a) {
     // parts of 4 do not hold a row).  Small parts
     // spread few rows over the GPU, large ones cost less per logit (a part's
     // reductions and list are the same for all): small ones as long as there
-    // are no more than some 8 workgroups to a CU, and at most 64 to a row.
+    // are no more than five workgroups to a CU, and at most 64 to a row.
     const uint32_t per = a.half ? 8 : 4;
     for (a.vectors = 1;; a.vectors *= 2) {
         a.chunks = (x->vocab + per - 1 + bsd::kBeamThreads * per * a.vectors - 1) / (bsd::kBeamThreads * per * a.vectors);
-        if (a.chunks <= bsd::kBeamChunks && (a.vectors >= 4 || (uint64_t)a.chunks * a.batch * a.beams <= 2048)) break;
+        if (a.chunks <= bsd::kBeamChunks && (a.vectors >= 4 || (uint64_t)a.chunks * a.batch * a.beams <= 1280)) break;
     }
     return BS_OK;
 }

@@ -291,14 +291,18 @@ __global__ __launch_bounds__(kBeamThreads, CAP == 2 ? 4 : 6) void beam_rows_kern
             }
             if (rank == a.best - 1) bound = unordered(key & ~63u);
         }
-    } else {
-        uint32_t rank = 0;
-        for (uint32_t i = 0; i < kBeamThreads; i += 4) {
-            const float4 o = *(const float4*)(maxima + i);
-            rank += (o.x > mine || (o.x == mine && i < t)) + (o.y > mine || (o.y == mine && i + 1 < t)) +
-                    (o.z > mine || (o.z == mine && i + 2 < t)) + (o.w > mine || (o.w == mine && i + 3 < t));
+    } else if (wave == 0) {
+        // of all threads', the upper 22 bits, one after the other
+        uint32_t keys[NW], key = 0;
+#pragma unroll
+        for (uint32_t w = 0; w < NW; w++) keys[w] = ordered(maxima[64 * w + lane]);
+        for (uint32_t bit = 1u << 31; bit >= 1u << 10; bit >>= 1) {
+            uint32_t n = 0;
+#pragma unroll
+            for (uint32_t w = 0; w < NW; w++) n += (uint32_t)__builtin_popcountll(__builtin_amdgcn_ballot_w64(keys[w] >= (key | bit)));
+            if (n >= a.best) key |= bit;
         }
-        if (rank == a.best - 1) bound = mine;
+        if (lane == 0) bound = unordered(key);
     }
     if (CAP != 1) {
         if (mine > minus_inf()) sum *= __builtin_amdgcn_exp2f((ref - ref_of<CAP>(k, top)) * kLog2e);
@@ -450,20 +454,21 @@ __global__ __launch_bounds__(kBeamThreads) void beam_merge_kernel(BeamArgs a) {
                 double sum = wave_sum((double)p.sum * part);
                 // the best of all parts: a lane's own next one, `at` of its list
                 uint32_t at = 0;
-                float head = p.n ? heads[wave][lane][0].logit : minus_inf();
+                BeamBest next = early[0];
+                float head = p.n ? next.logit : minus_inf();
                 float mine[2] = {0.f, 0.f};                          // best `lane` and `lane + 64`, their tokens and parts
                 uint32_t id[2] = {0, 0}, of[2] = {0, 0};
                 for (n = 0; n < a.best; n++) {
                     const float m = wave_max(head);
                     if (m == minus_inf()) break;
                     const uint32_t who = (uint32_t)__builtin_ctzll(__builtin_amdgcn_ballot_w64(head == m));   // lower lanes, lower tokens
-                    uint32_t v = 0;
+                    const uint32_t v = (uint32_t)__builtin_amdgcn_readlane((int)next.token, who);
                     if (lane == who) {
-                        v = (at < kHeads ? heads[wave][lane][at] : from[at]).token;
                         at++;
-                        head = at < p.n ? (at < kHeads ? heads[wave][lane][at] : from[at]).logit : minus_inf();
+                        next = heads[wave][lane][min(at, kHeads - 1)];
+                        if (at >= kHeads && at < p.n) next = from[at];
+                        head = at < p.n ? next.logit : minus_inf();
                     }
-                    v = (uint32_t)__builtin_amdgcn_readlane((int)v, who);
                     if (lane == n) {
                         mine[0] = m;
                         id[0] = v;
@@ -495,6 +500,7 @@ __global__ __launch_bounds__(kBeamThreads) void beam_merge_kernel(BeamArgs a) {
                     }
             }
         }
+        for (uint32_t i = n + lane; i < a.best; i += 64) list[i] = -__builtin_inf();
         if (lane == 0) found[w] = n;
     }
     __syncthreads();
@@ -513,20 +519,31 @@ __global__ __launch_bounds__(kBeamThreads) void beam_merge_kernel(BeamArgs a) {
         a.done_out[to] = 0;
     };
     const uint32_t all = a.beams * a.best;
-    if (all <= kBeamThreads / 2) {
-        // few: each finds its place by counting those before it
-        if (t >= all) return;
-        const uint32_t w = t / a.best, at = t % a.best;
-        const double mine = at < found[w] ? scores[t] : -inf;
-        uint32_t rank = 0;
-        for (uint32_t o = 0, i = 0; o < a.beams; o++) {
-            const uint32_t n = found[o];
-            for (uint32_t x = 0; x < a.best; x++, i++) rank += x < n && (scores[i] > mine || (scores[i] == mine && i < t));
+    if (all <= kBeamThreads) {
+        // few: each finds its place by counting those before it, shared out
+        // over some threads side by side
+        uint32_t ls = 0;
+        while (ls < 6 && all << (ls + 1) <= kBeamThreads) ls++;
+        const uint32_t i = t >> ls, each = (all + (1u << ls) - 1) >> ls, from = (t & ((1u << ls) - 1)) * each, to = min(all, from + each);
+        const double mine = i < all ? scores[i] : -inf;
+        uint32_t rank = 0, total = 0;
+        for (uint32_t j0 = from; j0 < to; j0 += 4) {
+            double o[4];
+#pragma unroll
+            for (uint32_t j = 0; j < 4; j++) o[j] = scores[min(j0 + j, all - 1)];
+#pragma unroll
+            for (uint32_t j = 0; j < 4; j++) {
+                rank += j0 + j < to && (o[j] > mine || (o[j] == mine && j0 + j < i));
+                total += j0 + j < to && o[j] > -inf;
+            }
         }
-        uint32_t total = 0;
-        for (uint32_t o = 0; o < a.beams; o++) total += found[o];
-        if (at < found[w] && rank < a.keep) write(rank, mine, (int32_t)tokens[t], w);
-        for (uint32_t i = total + t; i < a.keep; i += all) nothing(i);
+        for (uint32_t d = 1; d < 1u << ls; d <<= 1) {
+            rank += (uint32_t)__shfl_xor((int)rank, (int)d);
+            total += (uint32_t)__shfl_xor((int)total, (int)d);
+        }
+        if (i >= all || from) return;
+        if (mine > -inf && rank < a.keep) write(rank, mine, (int32_t)tokens[i], i / a.best);
+        for (uint32_t x = total + i; x < a.keep; x += all) nothing(x);
         return;
     }
     if (wave != 0) return;
