@@ -209,13 +209,17 @@ bs_status shared_args(const bs_kv_cache* cache, const bs_kv_attend_args* x, cons
     s.row_blocks = (uint32_t)(((uint64_t)b->max_new * s.a.group + 15) / 16);
     // splits: two workgroups to a CU of each kind, and a tile at least to each
     // of their four waves.  How long the common tokens are is the GPU's to know:
-    // either kind may have all of them.
+    // either kind may have all of them.  The groups are taken to be alike.  Where
+    // the rows alone fill the GPU, the common tokens are split half as often
+    // (128 rows in 4 groups: 4 splits 96 us, 2 91).
     int cus = 0;
     if (bsk_device_cus(&cus) != 0 || cus <= 0) cus = 256;
     const uint32_t cap = s.a.c.max_pages * s.a.c.page, len = x->max_len && x->max_len < cap ? x->max_len : cap;
     const uint64_t most = std::max<uint64_t>(1, ((uint64_t)len + 4 * bsd::kKvTile - 1) / (4 * bsd::kKvTile));
-    const uint64_t pre = std::max<uint64_t>(1, (uint64_t)s.blocks * s.a.c.kv_heads), own = (uint64_t)b->n_seqs * s.row_blocks * s.a.c.kv_heads;
-    s.pre = (uint32_t)std::min(most, std::max<uint64_t>(1, 2 * (uint64_t)cus / pre));
+    const uint64_t stack = (rows + std::max<uint64_t>(1, groups) - 1) / std::max<uint64_t>(1, groups);
+    const uint64_t tall = s.a.c.wide <= 128 && stack >= bsd::kKvStack ? 32 : 16;
+    const uint64_t pre = std::max<uint64_t>(1, groups * ((stack + tall - 1) / tall) * s.a.c.kv_heads), own = (uint64_t)b->n_seqs * s.row_blocks * s.a.c.kv_heads;
+    s.pre = (uint32_t)std::min(most, std::max<uint64_t>(1, (own >= 2 * (uint64_t)cus ? 1 : 2) * (uint64_t)cus / pre));
     s.own = (uint32_t)std::min(most, std::max<uint64_t>(1, 2 * (uint64_t)cus / own));
     if ((((uint64_t)s.a.c.kv_heads * s.pre + 7) / 8 * 8 * s.blocks + own * s.own) > kThreads / 256 ||
         (uint64_t)b->n_seqs * b->max_new > kThreads / 64) {

@@ -66,7 +66,7 @@ __global__ __launch_bounds__(kThreads) void batch_kernel(KvBatch b) {
             if (pg >= 0 && (uint32_t)pg < c.n_pages) slot = ((int64_t)pg << c.lp) + (place & (c.page - 1));
             else err = 4u;
         }
-        b.places[s] = place >= 0 ? (int32_t)place : -1;
+        b.places[s] = place >= 0 && count <= b.max_new ? (int32_t)place : -1;   // (attention leaves longer rows out)
         b.slots[s] = slot;
     }
     if (i + 1 == b.n)                                               // tokens of no row
@@ -140,10 +140,14 @@ __global__ __launch_bounds__(kThreads) void batch_kernel(KvBatch b) {
     __syncthreads();
     if (!last) return;
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
+    // groups that overlap have nothing in common: a token is to be in one at most
+    int wrong = 0;
+    for (uint32_t g = t; b.offs && g < b.groups; g += kThreads) wrong |= b.offs[g] < 0 || b.offs[g + 1] < b.offs[g] || b.offs[g + 1] > (int32_t)b.n;
+    wrong = __syncthreads_or(wrong);
+    if (wrong && t == 0) flag(c.status, 4u);
     for (uint32_t g = wave; g < b.groups; g += kWaves) {
         const int32_t f = b.offs ? b.offs[g] : 0, e = b.offs ? b.offs[g + 1] : (int32_t)b.n;
         const uint32_t from = (uint32_t)min(max(f, 0), (int32_t)b.n), to = (uint32_t)min(max(e, (int32_t)from), (int32_t)b.n);
-        if (((uint32_t)f != from || (uint32_t)e != to) && lane == 0) flag(c.status, 4u);
         const int32_t* rec = b.info + 4 + 8 * b.groups;
         int32_t few = 0x7FFFFFFF, low = 0x7FFFFFFF, high = -1;
         for (uint32_t j = from + lane; j < to; j += 64) {
@@ -157,7 +161,7 @@ __global__ __launch_bounds__(kThreads) void batch_kernel(KvBatch b) {
             low = min(low, __shfl_xor(low, s));
             high = max(high, __shfl_xor(high, s));
         }
-        if (from == to) few = 0;
+        if (from == to || wrong) few = 0;
         for (uint32_t j = from + lane; j < to; j += 64) {
             b.shared[j] = few;
             b.info[4 + 8 * (b.groups + j) + 2] = few;

@@ -12,10 +12,9 @@
 //
 // A workgroup takes 16 stacked rows, 32 in stacks of 64 rows or more with
 // head_dim up to 128, and some tiles of 64 tokens, its four waves one tile each
-// in turn.  Products and the lanes' tokens are those of the
-// kernel for few rows (bs_kv_attend.hip): S^T = K Q^T, O^T += V^T P^T, keys and
-// values straight from memory to the registers of the wave that multiplies
-// them.  With 32 rows an operand made of 8-bit codes meets two row tiles, and P
+// in turn.  Products and the lanes' tokens are those of the kernel for few
+// rows (bs_kv_attend.hip): S^T = K Q^T, O^T += V^T P^T, keys and values straight
+// from memory to the registers of the wave that multiplies them.  With 32 rows an operand made of 8-bit codes meets two row tiles, and P
 // is rounded to BF16, as in the kernel for many rows; else it enters in two
 // BF16 parts.
 #include <hip/hip_runtime.h>
@@ -290,7 +289,10 @@ __global__ __launch_bounds__(64 * kWaves, 2) void shared_kernel(KvShared s, uint
                     for (uint32_t y = 0; y < 2; y++) q[n][y] = *(const bf16x8*)(qs + (n * 2 * DW + 2 * x + y) * 1024 + 16 * lane);
 #pragma unroll
                 for (uint32_t h = h0; h < h1; h++) {
-                    const v4u kc = kr[h][x];
+                    v4u kc = kr[h][x];
+                    // (left to itself, the compiler takes int8 codes apart where
+                    // they are loaded, and spills what it makes of them)
+                    if (!E4M3) asm volatile("" : "+v"(kc));
                     const float f = E4M3 ? now.ks : 1.f;
                     const bf16x8 k0 = widen8<E4M3>(kc.x, kc.y, f), k1 = widen8<E4M3>(kc.z, kc.w, f);
 #pragma unroll
@@ -498,32 +500,47 @@ __global__ __launch_bounds__(64) void shared_join_kernel(KvShared s) {
     if (i * a.group >= record_rows(s, r, a.max_new) || qh >= a.heads || threadIdx.x >= kHeads * kLanes) return;
     const uint32_t tok = (uint32_t)r.x + i;
     const float* pp = a.part + ((uint64_t)tok * a.heads + qh) * (s.pre + s.own) * (D + 4);
-    const bool grouped = r.z >= (int32_t)kKvTile;
-    const float n0 = pp[D + 2], n1 = pp[s.pre * (D + 4) + D + 2];
-    const uint32_t pre = grouped ? min(__builtin_bit_cast(uint32_t, n0), s.pre) : 0u;
-    const uint32_t n = pre + min(__builtin_bit_cast(uint32_t, n1), s.own);
-    auto part = [&](uint32_t x) { return pp + (x < pre ? x : s.pre + (x - pre)) * (D + 4); };
+    const bool grouped = r.z >= (int32_t)kKvTile && s.places[tok] >= 0;
+    const uint32_t slots = s.pre + s.own;
+    uint32_t pre = 0, own = 0;
     float top = -__builtin_inff(), total = 0.f;
     f32x4 o = f32x4{0.f, 0.f, 0.f, 0.f};
-    for (uint32_t x0 = 0; x0 < n; x0 += 8) {
-        f32x4 v[8], h[8];
-        float most = top;
+    // eight places at a time; the first eight are read, used or not, while the
+    // numbers of parts are
+    const float n0 = pp[D + 2], n1 = pp[s.pre * (D + 4) + D + 2];
+    for (uint32_t x0 = 0; x0 < slots; x0 += 8) {
+        if (x0 && x0 >= pre && (x0 + 8 <= s.pre || x0 >= s.pre + own)) continue;
+        f32x4 v[8];
+        float f[8], l[8], most = top;
 #pragma unroll
         for (uint32_t u = 0; u < 8; u++) {
-            const float* px = part(min(x0 + u, n - 1));
+            const float* px = pp + min(x0 + u, slots - 1) * (D + 4);
             v[u] = *(const f32x4*)(px + ch);
-            h[u] = *(const f32x4*)(px + D);
+            f[u] = px[D];
+            l[u] = px[D + 1];
+        }
+        if (x0 == 0) {
+            pre = grouped ? min(__builtin_bit_cast(uint32_t, n0), s.pre) : 0u;
+            own = min(__builtin_bit_cast(uint32_t, n1), s.own);
         }
 #pragma unroll
-        for (uint32_t u = 0; u < 8; u++) most = fmaxf(most, h[u][0]);
-        const float sub = most == -__builtin_inff() ? 0.f : most, f = exp2_fast(top - sub);
+        for (uint32_t u = 0; u < 8; u++) {
+            const uint32_t x = x0 + u;
+            const bool used = x < pre || (x >= s.pre && x < s.pre + own);
+            f[u] = used ? f[u] : -__builtin_inff();
+            l[u] = used ? l[u] : 0.f;
+#pragma unroll
+            for (int e = 0; e < 4; e++) v[u][e] = used ? v[u][e] : 0.f;
+            most = fmaxf(most, f[u]);
+        }
+        const float sub = most == -__builtin_inff() ? 0.f : most, g = exp2_fast(top - sub);
         top = most;
-        total *= f;
-        o *= f;
+        total *= g;
+        o *= g;
 #pragma unroll
         for (uint32_t u = 0; u < 8; u++) {
-            const float w = x0 + u < n ? exp2_fast(h[u][0] - sub) : 0.f;
-            total += w * h[u][1];
+            const float w = exp2_fast(f[u] - sub);
+            total += w * l[u];
             o += w * v[u];
         }
     }
