@@ -872,9 +872,11 @@ typedef struct {
     int32_t* d_done_out;        /* 1 where the token is eos or the beam was done */
 } bs_beam_args;
 
-/* Two kernel launches on `stream`, no allocation, the same result on every
- * run.  d_work: bs_beam_work_bytes (0: arguments that are refused; pointers
- * are not looked at), 16-B aligned; calls that share it must not overlap.
+/* One or two kernel launches on `stream`, no allocation, the same result on
+ * every run.  d_work: bs_beam_work_bytes (0: arguments that are refused;
+ * pointers are not looked at), 16-B aligned; its first 4096 bytes are zero
+ * before the first call that is given it, and every call leaves them so; calls
+ * that share it must not overlap.
  * Results overlap neither the inputs, the workspace nor each other.  Errors:
  * BS_E_INVAL, BS_E_HIP. */
 uint64_t bs_beam_work_bytes(const bs_beam_args* args);

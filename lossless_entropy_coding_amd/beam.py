@@ -22,7 +22,7 @@ from typing import NamedTuple
 import torch
 
 from . import _lib as L
-from .codec import _grown, _on, _same_device, _stream_of
+from .codec import _capturing, _grown, _on, _same_device, _stream_of
 
 
 class Best(NamedTuple):
@@ -84,11 +84,23 @@ class Beams:
                 need = int(L.lib().bs_beam_work_bytes(self._ref))
                 if need:
                     self._need[(vocab, kind)] = need
-            if self._work is None or self._work.numel() < need:
-                self._work = _grown(self._work, need, self.device, stream, self._kept)
-            rc = L.lib().bs_beam_select_async(self._ref, self._work.data_ptr(), self._work.numel(),
-                                              _stream_of(self.device, stream))
+            w = self._work
+            if w is None or w.numel() < need:
+                w = self._counted_work(need, stream)
+            rc = L.lib().bs_beam_select_async(self._ref, w.data_ptr(), w.numel(), _stream_of(self.device, stream))
         if rc:
             L.check(rc, "bs_beam_select_async")
         s, t, p, d = got.unbind(0)
         return Best(s.view(torch.float32), t, p, d)
+
+    def _counted_work(self, need: int, stream) -> torch.Tensor:
+        """A workspace, its counters zeroed.  Under capture zeroing is recorded
+        but not run: the call then has a workspace of its own in the graph's
+        memory, zeroed by each replay (a call before the capture spares that)."""
+        with _on(stream):
+            if _capturing(self.device):
+                w = torch.empty(max(need, 4096), dtype=torch.uint8, device=self.device)
+                w[:4096].zero_()
+                return w
+        self._work = _grown(self._work, need, self.device, stream, self._kept, zero=True)
+        return self._work

@@ -14,8 +14,10 @@ namespace {
 
 bool aligned(const void* p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 
-// the call's sizes, checked; pointers are not looked at
-bs_status shape(const bs_beam_args* x, bsd::BeamArgs& a) {
+constexpr uint64_t kOne = 320;
+
+// the call's sizes, checked; pointers are not looked at.  one: a single launch.
+bs_status shape(const bs_beam_args* x, bsd::BeamArgs& a, bool& one) {
     memset(&a, 0, sizeof a);
     if (!x) { set_error("NULL argument"); return BS_E_INVAL; }
     if (x->beams == 0 || x->beams > 64 || x->keep == 0 || x->keep > 128) {
@@ -40,22 +42,28 @@ bs_status shape(const bs_beam_args* x, bsd::BeamArgs& a) {
     a.softcap = x->softcap > 0x1p100f ? 0.f : x->softcap > 0.f ? std::max(x->softcap, 0x1p-100f) : 0.f;
     a.stride = x->row_stride;
     // A part of a row is 512 threads times 1, 2 or 4 vectors (8 of fp32 where 64
-    // parts of 4 do not hold a row).  Small parts
-    // spread few rows over the GPU, large ones cost less per logit (a part's
-    // reductions and list are the same for all): small ones as long as there
-    // are no more than five workgroups to a CU, and at most 64 to a row.
+    // parts of 4 do not hold a row).  Small parts spread few rows over the GPU,
+    // large ones cost less per logit (a part's reductions and list are the same
+    // for all).  Up to kOne parts one launch does all (see beam_both_kernel);
+    // above, small parts as long as there are no more than five workgroups to a
+    // CU.
     const uint32_t per = a.half ? 8 : 4;
-    for (a.vectors = 1;; a.vectors *= 2) {
-        a.chunks = (x->vocab + per - 1 + bsd::kBeamThreads * per * a.vectors - 1) / (bsd::kBeamThreads * per * a.vectors);
-        if (a.chunks <= bsd::kBeamChunks && (a.vectors >= 4 || (uint64_t)a.chunks * a.batch * a.beams <= 1280)) break;
-    }
+    auto cut = [&](uint64_t most) {
+        for (a.vectors = 1;; a.vectors *= 2) {
+            a.chunks = (x->vocab + per - 1 + bsd::kBeamThreads * per * a.vectors - 1) / (bsd::kBeamThreads * per * a.vectors);
+            const uint64_t all = (uint64_t)a.chunks * a.batch * a.beams;
+            if (a.chunks <= bsd::kBeamChunks && (all <= most || a.vectors >= 4)) return all <= most && a.vectors <= 2;
+        }
+    };
+    one = cut(kOne);
+    if (!one) cut(1280);
     return BS_OK;
 }
 
 uint64_t parts_bytes(const bsd::BeamArgs& a) { return align_up((uint64_t)a.batch * a.beams * a.chunks * sizeof(bsd::BeamPart), 256); }
 
 uint64_t work_bytes_of(const bsd::BeamArgs& a) {
-    return align_up(parts_bytes(a) + (uint64_t)a.batch * a.beams * a.chunks * a.best * sizeof(bsd::BeamBest), 256);
+    return 4 * bsd::kBeamCounters + align_up(parts_bytes(a) + (uint64_t)a.batch * a.beams * a.chunks * a.best * sizeof(bsd::BeamBest), 256);
 }
 
 }  // namespace
@@ -64,12 +72,14 @@ extern "C" {
 
 uint64_t bs_beam_work_bytes(const bs_beam_args* args) {
     bsd::BeamArgs a;
-    return shape(args, a) == BS_OK ? std::max<uint64_t>(work_bytes_of(a), 256) : 0;
+    bool one;
+    return shape(args, a, one) == BS_OK ? work_bytes_of(a) : 0;
 }
 
 bs_status bs_beam_select_async(const bs_beam_args* args, void* d_work, uint64_t work_bytes, void* stream) {
     bsd::BeamArgs a;
-    const bs_status rc = shape(args, a);
+    bool one;
+    const bs_status rc = shape(args, a, one);
     if (rc != BS_OK) return rc;
     if (a.batch == 0) return BS_OK;
     const bs_beam_args& x = *args;
@@ -103,8 +113,9 @@ bs_status bs_beam_select_async(const bs_beam_args* args, void* d_work, uint64_t 
     a.tokens = x.d_tokens;
     a.parents = x.d_parents;
     a.done_out = x.d_done_out;
-    a.parts = (bsd::BeamPart*)d_work;
-    a.bests = (bsd::BeamBest*)((uint8_t*)d_work + parts_bytes(a));
+    a.counters = one ? (uint32_t*)d_work : nullptr;
+    a.parts = (bsd::BeamPart*)((uint32_t*)d_work + bsd::kBeamCounters);
+    a.bests = (bsd::BeamBest*)((uint8_t*)a.parts + parts_bytes(a));
     const int e = bsk_beam_select(&a, stream);
     if (e == 0) return BS_OK;
     set_error("selection launch: %s", hipGetErrorString((hipError_t)e));

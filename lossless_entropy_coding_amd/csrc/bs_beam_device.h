@@ -6,7 +6,8 @@
 
 namespace bsd {
 
-constexpr uint32_t kBeamThreads = 512;       // of a workgroup of the first launch
+constexpr uint32_t kBeamThreads = 512;       // of a workgroup
+constexpr uint32_t kBeamCounters = 1024;     // words before a workspace's parts
 constexpr uint32_t kBeamChunks = 64;         // parts of a row at most: one to a lane of the second launch
 
 // what the first launch leaves of a part of a row, before its best logits
@@ -37,6 +38,7 @@ struct BeamArgs {
     int32_t* tokens;
     int32_t* parents;
     int32_t* done_out;
+    uint32_t* counters;         // of the requests, where one launch does all; else null
     BeamPart* parts;            // [batch * beams][chunks]
     BeamBest* bests;            // [batch * beams][chunks][best], best first
 };
