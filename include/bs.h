@@ -857,7 +857,7 @@ uint64_t bs_kv_attend_shared_work_bytes(const bs_kv_cache* cache, const bs_kv_at
 typedef struct {
     uint32_t batch, beams;      /* requests, and beams of each (1..64); batch * beams up to 65535 */
     uint32_t keep;              /* continuations of a request, 1..128 */
-    uint32_t vocab;             /* 1..2^20 */
+    uint32_t vocab;             /* 1..1000000 */
     uint32_t type;              /* BS_T_BF16 or BS_T_FP32 */
     int32_t eos;                /* the token that ends a beam, negative: none */
     float softcap;              /* 0 or infinity: none */

@@ -25,7 +25,7 @@ bs_status shape(const bs_beam_args* x, bsd::BeamArgs& a, bool& one) {
         return BS_E_INVAL;
     }
     if ((uint64_t)x->batch * x->beams > 65535) { set_error("%u requests of %u beams (65535 beams in all)", x->batch, x->beams); return BS_E_INVAL; }
-    if (x->vocab == 0 || x->vocab > (1u << 20)) { set_error("%u tokens (1..2^20)", x->vocab); return BS_E_INVAL; }
+    if (x->vocab == 0 || x->vocab > 1000000) { set_error("%u tokens (1..1000000)", x->vocab); return BS_E_INVAL; }
     if (x->type != BS_T_BF16 && x->type != BS_T_FP32) { set_error("logits of type %u", x->type); return BS_E_INVAL; }
     if (x->row_stride < x->vocab || x->row_stride > (1ull << 40)) { set_error("row stride %llu", (unsigned long long)x->row_stride); return BS_E_INVAL; }
     if (!(x->softcap >= 0.f)) { set_error("softcap %g", x->softcap); return BS_E_INVAL; }

@@ -178,3 +178,16 @@ def test_streams_captures_and_more_calls_of_one_handle():
 def test_empty_batches():
     got = beam.Beams(0, 4).select(torch.zeros(0, 10, device="cuda"), torch.zeros(0, device="cuda"))
     assert got.scores.shape == (0, 4)
+
+
+@pytest.mark.parametrize("half,vocab", [(True, 1000000), (False, 1000000), (False, 524285), (True, 262145)])
+def test_the_largest_vocabularies(half, vocab):
+    """Up to 64 parts of a row, of the largest size."""
+    x, s = _logits(vocab, 4, vocab, half)
+    x[:, -1] += 9.0
+    x[:, 0] += 8.0
+    _check(x, s, 4, 5)
+    flat = torch.empty(4 * vocab + 3, dtype=x.dtype, device="cuda")
+    rows = flat[3:].view(4, vocab)
+    rows.copy_(x)
+    _check(x, s, 4, 5, got=beam.Beams(1, 4, keep=5).select(rows, torch.tensor(s).cuda()))
