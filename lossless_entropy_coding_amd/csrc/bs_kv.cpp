@@ -531,6 +531,16 @@ bs_status bs_kv_batch_async(const bs_kv_cache* cache, const bs_kv_batch* batch, 
         return BS_E_INVAL;
     }
     if (!d_groups && batch->n_groups != 1) { set_error("%u groups without their offsets", batch->n_groups); return BS_E_INVAL; }
+    const uint64_t n = batch->n_seqs, total = batch->total;
+    const struct { const void* p; uint64_t bytes; } in[] = {{d_seqs, 4 * n}, {d_counts, 4 * n}, {d_groups, 4ull * batch->n_groups + 4}},
+        out[] = {{batch->d_starts, 4 * n + 4}, {batch->d_places, 4 * total}, {batch->d_slots, 8 * total}, {batch->d_table, 4 * n * batch->width},
+                 {batch->d_lead, 4 * n}, {batch->d_shared, 4 * n}, {batch->d_info, 16 + 32 * (batch->n_groups + n)}, {batch->d_rows, 4 * n}};
+    for (const auto& x : in)
+        for (const auto& y : out)
+            if (x.p && y.p && overlap(x.p, x.bytes, y.p, y.bytes) && !(x.p == d_seqs && y.p == d_seqs)) {   // a plan's own rows may be given
+                set_error("the plan overlaps rows, counts or groups");
+                return BS_E_INVAL;
+            }
     b.n = batch->n_seqs;
     b.groups = batch->n_groups;
     b.total = batch->total;

@@ -168,6 +168,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void shared_kernel(KvShared s, uint
     const bool tall = NR > 1 && j.before && j.rows >= kKvStack;
     const uint32_t nrows = min(tall ? 16 * NR : 16u, j.rows - j.r0);
     j.hi = min(j.hi, (int32_t)(c.max_pages << c.lp) - 1);
+    j.lo = min(j.lo, max(j.hi, 0));
     const Part pt = get_part(a, j.lo, j.hi, j.cut, j.before);
     const uint32_t chunk = max(kWaves, (pt.n + j.splits - 1) / j.splits);
     const uint32_t i0 = j.split * chunk;

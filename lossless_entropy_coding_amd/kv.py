@@ -281,7 +281,9 @@ class KvCache:
         a group have in common once for all of them
         (bs_kv_attend_shared_async): q (batch.total, heads, head_dim) in the
         plan's order; the other arguments and the results are attend's.  The
-        plan is this cache's and holds until its rows change."""
+        plan is this cache's and holds until its rows change.  Where
+        batch.max_new x heads / kv_heads is 64 or more it is attend itself, so
+        a plan with counts should say its max_new."""
         if batch.cache is not self:
             raise ValueError("the plan is another cache's")
         total, heads, qs, os, out, lse, window, sinks, max_len = self._results(q, out, lse, window, sinks, batch.max_len, stream)

@@ -41,8 +41,8 @@ def test_moves_that_are_refused():
 
 
 # --------------------------------------------------------------------- plans
-PLAN = dict(n_seqs=3, n_groups=2, total=5, max_new=2, width=4, reserved=0, d_rows=AT, d_starts=AT, d_places=AT, d_slots=AT, d_table=AT,
-            d_lead=AT, d_shared=AT, d_info=AT)
+PLAN = dict(n_seqs=3, n_groups=2, total=5, max_new=2, width=4, reserved=0, **{n: AT + 1024 * (i + 1) for i, n in enumerate(
+    ("d_rows", "d_starts", "d_places", "d_slots", "d_table", "d_lead", "d_shared", "d_info"))})
 
 
 def _plan(**kw):
@@ -50,7 +50,7 @@ def _plan(**kw):
 
 
 BAD_PLAN = [dict(n_seqs=16385), dict(n_groups=16385), dict(total=1 << 31), dict(max_new=0), dict(max_new=6), dict(n_seqs=0), dict(reserved=1)] + \
-    [{n: None} for n in PLAN if n.startswith("d_")] + [{n: AT + 2} for n in PLAN if n.startswith("d_")] + [dict(d_slots=AT + 4), dict(d_info=AT + 8)]
+    [{n: None} for n in PLAN if n.startswith("d_")] + [{n: AT + 16386} for n in PLAN if n.startswith("d_")] + [dict(d_slots=AT + 16388), dict(d_info=AT + 16392)]
 
 
 @pytest.mark.parametrize("kw", BAD_PLAN, ids=[str(k) for k in BAD_PLAN])
@@ -66,8 +66,14 @@ def test_plan_calls_that_are_refused():
     c, f = _cache(), L.lib().bs_kv_batch_async
     assert f(C.byref(c), None, AT, AT, AT, None) == L.BS_E_INVAL
     assert f(C.byref(_cache(type=0)), C.byref(_plan()), AT, AT, AT, None) == L.BS_E_INVAL
-    for args in ((None, AT, AT), (AT + 2, AT, AT), (AT, AT + 1, AT), (AT, AT, AT + 2), (AT, None, AT), (AT, AT, None)):
+    for args in ((None, AT, AT), (AT + 2, AT, AT), (AT, AT + 1, AT), (AT, AT, AT + 2), (AT, None, AT), (AT, AT, None), (AT, AT, AT + 1020)):
         assert f(C.byref(c), C.byref(_plan()), *args, None) == L.BS_E_INVAL, args
+    for name in PLAN:                                            # inputs in the plan's own buffers
+        if name.startswith("d_"):
+            for at in range(3):
+                args = [AT, AT + 256, AT + 512]
+                args[at] = PLAN[name] + 4
+                assert f(C.byref(c), C.byref(_plan()), *args, None) == L.BS_E_INVAL, (name, at)
     none = _plan(n_seqs=0, total=0, d_rows=None, d_starts=None, d_info=None)
     assert f(C.byref(c), C.byref(none), None, None, None, None) == L.BS_OK
 
