@@ -853,8 +853,9 @@ uint64_t bs_kv_attend_shared_work_bytes(const bs_kv_cache* cache, const bs_kv_at
  * its logits are not read in the first case.  A beam that is done has one, the
  * token eos at its own score, and its logits are not read.  Where there are
  * too few, the score is -infinity, token and parent are -1 and done is 0.
- * Scores are computed in 64 bits and rounded once (the exponentials of a sum
- * in 32, the sum's error is 2^-20 or less). */
+ * Scores are computed in 64 bits and rounded once.  A sum's exponentials are
+ * fp32: it is right to 2^-17 of itself, under a soft cap (or 256, if that is
+ * less) to 2^-21 of the cap more. */
 typedef struct {
     uint32_t batch, beams;      /* requests, and beams of each (1..64); batch * beams up to 65535 */
     uint32_t keep;              /* continuations of a request, 1..128 */

@@ -61,7 +61,7 @@ class Beams:
         rows, kind = self.batch * self.beams, logits.dtype
         if logits.dim() != 2 or logits.shape[0] != rows or (kind is not torch.bfloat16 and kind is not torch.float32):
             raise ValueError(f"logits must be ({rows}, vocab) bfloat16 or float32")
-        vocab = logits.shape[1]
+        vocab = min(logits.shape[1], (1 << 32) - 1)      # the library's 32-bit number would take a larger one's low bits
         if logits.stride(1) != 1 and vocab > 1 and rows:
             raise ValueError("the logits of a beam must be side by side")
         if scores.dtype is not torch.float32 or scores.numel() != rows or not scores.is_contiguous():

@@ -728,6 +728,8 @@ __global__ __launch_bounds__(256) void compact_table_kernel(KvPages p, uint32_t 
 
 // ---------------------------------------------------------------- reorder
 // Rows a[i] take the tokens of rows a[b[i]] (b[i] = -1: none), all at once.
+// 4 rows through 42 layers 10.3 us, two launches; 512 rows through 12 layers
+// 42 us, most of it copies at 5 TB/s of read and written bytes.
 // work: [0] 1 if the call goes through, [1] copies, then for each i the row's
 // length before and after, the page of its own copy (-1: none), then the
 // copies' sources and targets, the free pages found, and for each row of the

@@ -7,7 +7,7 @@
 // another.  A row is compared with the first of its group, page by page; the
 // workgroup that ends last takes the least of each group.  Where a plan is
 // small, each row's workgroup compares its whole group instead, and none is
-// the last: 64 rows of 127 pages 8.9 -> 6.5 us, chains of dependent loads
+// the last: 64 rows of 127 pages 8.9 -> 6.1 us, chains of dependent loads
 // either way; for more pages than kSmall the reads would be repeated too often.
 #include <hip/hip_runtime.h>
 #include <stdint.h>

@@ -12,6 +12,13 @@ keys and values and attends:
         cache.append(layer, k, v, rows)
         out = cache.attend(layer, q, rows)
 
+Rows that go on from one prompt (fork) attend together, with the step's plan,
+and follow the beams that a search chooses:
+
+    step = KvBatch(cache, rows, groups=groups)
+    out = cache.attend_shared(layer, q, step)
+    cache.reorder(rows, parents)
+
 Everything is enqueued on the current (or given) stream and nothing
 synchronises except check().  The cache keeps its workspaces, so its calls go
 on one stream, or on several that wait for each other.  Threads may share a

@@ -258,6 +258,12 @@ def test_what_the_choice_checks_and_sends(calls):
             beam.Beams(**{**dict(batch=2, beams=3, device="cpu"), **kw})
 
 
+def test_vocabularies_past_32_bits_are_refused(calls):
+    b = beam.Beams(1, 1, device="cpu")
+    b.select(torch.empty(1, (1 << 32) + 5, dtype=torch.bfloat16), torch.zeros(1))        # memory that nothing touches
+    assert calls[-1][1][0]._obj.vocab == (1 << 32) - 1 and L.lib().bs_beam_work_bytes(b._ref) == 0
+
+
 # ---------------------------------------------------------------- references
 def test_the_reference_of_the_choice_is_the_definition():
     """Against a full sort of all continuations of a small case, and known answers."""
