@@ -25,8 +25,8 @@
 // cap is lost in the reciprocal of tanh: there the terms of a beam's best
 // tokens, those that its sum is made of, are put right in 64 bits.
 //
-// 512 beams, a tenth of them done, 256000 BF16 logits, a soft cap: 86 us, of
-// which launch 1 is 76 (3.1 TB/s; at a copy's rate it would take 50).  A logit
+// 512 beams, a tenth of them done, 256000 BF16 logits, a soft cap: 75 us, of
+// which launch 1 is 66 (3.6 TB/s; at a copy's rate it would take 50).  A logit
 // takes three transcendentals there, which issue at a quarter rate.  Few rows are bound by the launches; one user's four beams take
 // one launch (beam_both_kernel) and 12 us.
 #include <hip/hip_runtime.h>
@@ -200,13 +200,14 @@ __device__ __forceinline__ void read_part(const BeamArgs& a, uint32_t row, uint3
     __shared__ __attribute__((aligned(16))) float maxima[kBeamThreads];
     __shared__ float sums[NW];
     __shared__ float bound;
-    __shared__ uint32_t count, total[2];
+    __shared__ uint32_t count, total[2], vectors, low;
+    __shared__ uint16_t some[kBeamThreads * NV];
     __shared__ BeamBest list[kList];
 
     const uint32_t t = threadIdx.x, lane = t & 63u, wave = __builtin_amdgcn_readfirstlane(t >> 6);
     if (a.done && a.done[row] != 0) return;
     if (!(fabsf(a.scores[row]) < __builtin_inff())) return;          // such beams have no continuations
-    if (t == 0) count = total[0] = total[1] = 0;
+    if (t == 0) count = total[0] = total[1] = vectors = 0;
 
     // p counts from the 16-B boundary at or before the row's first logit
     constexpr uint32_t esize = HALF ? 2 : 4;
@@ -290,10 +291,13 @@ __device__ __forceinline__ void read_part(const BeamArgs& a, uint32_t row, uint3
     }
     maxima[t] = mine;
     __syncthreads();
-    float group = maxima[lane];
+    float group = 0.f, top = 0.f;
+    if (CAP != 1 || wave == 0) {
+        group = maxima[lane];
 #pragma unroll
-    for (uint32_t w = 1; w < NW; w++) group = fmaxf(group, maxima[64 * w + lane]);
-    const float top = wave_max(group);
+        for (uint32_t w = 1; w < NW; w++) group = fmaxf(group, maxima[64 * w + lane]);
+        top = wave_max(group);
+    }
     // The bound of the list: the K-th largest maximum.  Of 64 groups, its upper
     // 26 bits as a whole number that grows with it, the others 0: with the lane
     // in their place no two are equal, and a comparison is one instruction.
@@ -325,11 +329,18 @@ __device__ __forceinline__ void read_part(const BeamArgs& a, uint32_t row, uint3
     }
     if (CAP != 1) {
         if (mine > minus_inf()) sum *= __builtin_amdgcn_exp2f((ref - ref_of<CAP>(k, top)) * kLog2e);
-    } else if (2.f * k.c * (1.f - k.r(top)) < 32.f) {
+    } else if (t == 0) {
+        low = 2.f * k.c * (1.f - k.r(top)) < 32.f;
+    }
+    sum = wave_sum(sum);
+    if (lane == 0) sums[wave] = sum;
+    __syncthreads();
+    const float least = bound;
+    forget();
+    if (CAP == 1 && low) {
         // A logit of -infinity has counted as e^(-2 c).  Where the largest is no
         // more than e^32 of that, a part of 32768 of them would show (2^-30).
         sum = 0.f;
-        forget();
 #pragma unroll 1
         for (uint32_t j = 0; j < NV; j++) {
             const v4u x = load_edge(j);
@@ -339,29 +350,35 @@ __device__ __forceinline__ void read_part(const BeamArgs& a, uint32_t row, uint3
                 sum += v == minus_inf() ? 0.f : f;
             }
         }
+        sum = wave_sum(sum);
+        if (lane == 0) sums[wave] = sum;
+        forget();
     }
-    sum = wave_sum(sum);
-    if (lane == 0) sums[wave] = sum;
-    __syncthreads();
-    const float least = bound;
-    forget();
-    auto pick = [&](const v4u& x, uint32_t j) {
+    auto pick = [&](const v4u& x, uint32_t first) {
 #pragma unroll
         for (uint32_t e = 0; e < VE; e++) {
             const float f = logit(x, e);
             if (f >= least && f > minus_inf()) {
                 const uint32_t at = atomicAdd(&count, 1u);
-                if (at < kList) list[at] = BeamBest{f, place(j) + e - skip};
+                if (at < kList) list[at] = BeamBest{f, first + e - skip};
             }
         }
     };
     if (inside) {
+        // The few vectors with such logits side by side first, so that one wave
+        // looks through them all (with each by its own wave they took a tenth
+        // of the kernel's instructions).
 #pragma unroll
         for (uint32_t j = 0; j < NV; j++)
-            if (best[j] >= least && best[j] > minus_inf()) pick(load(j), j);
+            if (best[j] >= least && best[j] > minus_inf()) some[atomicAdd(&vectors, 1u)] = (uint16_t)(j * kBeamThreads + t);
+        __syncthreads();
+        for (uint32_t i = t; i < vectors; i += kBeamThreads) {
+            const uint32_t p = chunk * CH + some[i] * VE;
+            pick(*(const v4u*)(base + (uint64_t)p * esize), p);
+        }
     } else if (mine >= least && mine > minus_inf()) {
 #pragma unroll 1
-        for (uint32_t j = 0; j < NV; j++) pick(load_edge(j), j);
+        for (uint32_t j = 0; j < NV; j++) pick(load_edge(j), place(j));
     }
     __syncthreads();
     uint32_t n = count;
@@ -589,7 +606,12 @@ __device__ __forceinline__ void choose(const BeamArgs& a, uint32_t request) {
 // grid: (parts, rows)
 template <bool HALF, int NV, int CAP>
 __global__ __launch_bounds__(kBeamThreads, CAP == 2 ? 4 : 6) void beam_rows_kernel(BeamArgs a) {
-    read_part<HALF, NV, CAP, false>(a, blockIdx.y, blockIdx.x);
+    // Workgroups go to the eight XCDs in turn, and a row's last part, which
+    // reaches past the row's end, takes longest: rows begin at different parts,
+    // so that those are dealt evenly, whatever power of two their number holds
+    // (512 rows of 16 parts: 86 us where one XCD had all last parts, 75).
+    const uint32_t step = min(a.chunks & (0u - a.chunks), 8u);
+    read_part<HALF, NV, CAP, false>(a, blockIdx.y, (blockIdx.x + blockIdx.y * step / 8) % a.chunks);
 }
 
 // grid: requests
