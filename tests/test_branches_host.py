@@ -53,7 +53,7 @@ BAD_PLAN = [dict(n_seqs=16385), dict(n_groups=16385), dict(total=1 << 31), dict(
     [{n: None} for n in PLAN if n.startswith("d_")] + [{n: AT + 16386} for n in PLAN if n.startswith("d_")] + [dict(d_slots=AT + 16388), dict(d_info=AT + 16392)]
 
 
-@pytest.mark.parametrize("kw", BAD_PLAN, ids=[str(k) for k in BAD_PLAN])
+@pytest.mark.parametrize("kw", BAD_PLAN, ids=lambda kw: "-".join(kw))
 def test_plans_that_are_refused(kw):
     c, lib = _cache(), L.lib()
     assert lib.bs_kv_batch_async(C.byref(c), C.byref(_plan(**kw)), AT, AT, AT, None) == L.BS_E_INVAL
@@ -134,7 +134,7 @@ BAD_CALL = [{n: None} for n in BEAM if n.startswith("d_") and n != "d_done"] + \
      dict(d_tokens=AT + 10241), dict(d_scores_out=AT + 8192), dict(d_tokens=AT), dict(d_parents=AT + 10240), dict(d_done_out=AT + 13312, d_done=AT + 13312, eos=2)]
 
 
-@pytest.mark.parametrize("kw", BAD_SHAPE + BAD_CALL, ids=[str(k) for k in BAD_SHAPE + BAD_CALL])
+@pytest.mark.parametrize("kw", BAD_SHAPE + BAD_CALL, ids=lambda kw: "-".join(kw))
 def test_choices_that_are_refused(kw):
     lib, w = L.lib(), AT + 65536
     need = int(lib.bs_beam_work_bytes(C.byref(_beam())))
