@@ -26,9 +26,10 @@
 // tokens, those that its sum is made of, are put right in 64 bits.
 //
 // 512 beams, a tenth of them done, 256000 BF16 logits, a soft cap: 75 us, of
-// which launch 1 is 66 (3.6 TB/s; at a copy's rate it would take 50).  A logit
-// takes three transcendentals there, which issue at a quarter rate.  Few rows are bound by the launches; one user's four beams take
-// one launch (beam_both_kernel) and 12 us.
+// which launch 1 is 66 (3.6 TB/s; at a copy's rate it would take 50).  Vector
+// instructions issue 89% of a busy CU's time: 13 to a logit, of which three
+// transcendentals take the time of six.  Few rows are bound by the launches;
+// one user's four beams take one launch (beam_both_kernel) and 12 us.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
