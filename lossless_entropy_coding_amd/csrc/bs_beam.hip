@@ -25,9 +25,9 @@
 // cap is lost in the reciprocal of tanh: there the terms of a beam's best
 // tokens, those that its sum is made of, are put right in 64 bits.
 //
-// 512 beams, a tenth of them done, 256000 BF16 logits, a soft cap: 75 us, of
-// which launch 1 is 66 (3.6 TB/s; at a copy's rate it would take 50).  Vector
-// instructions issue 89% of a busy CU's time: 13 to a logit, of which three
+// 512 beams, a tenth of them done, 256000 BF16 logits, a soft cap: 73 us, of
+// which launch 1 is 64 (3.7 TB/s; at a copy's rate it would take 50).  Vector
+// instructions issue 88% of a busy CU's time: 13 to a logit, of which three
 // transcendentals take the time of six.  Few rows are bound by the launches;
 // one user's four beams take one launch (beam_both_kernel) and 12 us.
 #include <hip/hip_runtime.h>
@@ -287,8 +287,25 @@ __device__ __forceinline__ void read_part(const BeamArgs& a, uint32_t row, uint3
             for (uint32_t j = 0; j < NL; j++) x[j] = y[j];
         }
     } else {
+        // whole vectors together, as above, then the one or two that are cut (one
+        // after the other: 512 rows of 256000 75 us, 73)
+        v4u x[NL];
+        auto whole = [&](uint32_t j) { return place(j) >= skip && place(j) + VE <= stop; };
 #pragma unroll 1
-        for (uint32_t j = 0; j < NV; j++) take(load_edge(j));
+        for (uint32_t j0 = 0; j0 < NV; j0 += NL) {
+#pragma unroll
+            for (uint32_t j = 0; j < NL; j++)
+                if (whole(j0 + j)) x[j] = load(j0 + j);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (uint32_t j = 0; j < NL; j++) {
+                if (whole(j0 + j)) take(x[j]);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+#pragma unroll 1
+        for (uint32_t j = 0; j < NV; j++)
+            if (!whole(j) && place(j) < stop && place(j) + VE > skip) take(load_edge(j));
     }
     maxima[t] = mine;
     __syncthreads();
