@@ -546,11 +546,13 @@ __device__ __forceinline__ void choose(const BeamArgs& a, uint32_t request) {
                         sum += wave_sum(64 * h + lane < n ? more : 0.);
                     }
                 }
-                const double base = (double)score - ytop - log(sum);
+                // (differences of logits first: a row may hold the type's lowest
+                // value everywhere, beside which a score would be lost)
+                const double base = (double)score - log(sum);
 #pragma unroll
                 for (uint32_t h = 0; h < 2; h++)
                     if (64 * h + lane < n) {
-                        list[64 * h + lane] = base + y[h];
+                        list[64 * h + lane] = base + (y[h] - ytop);
                         ids[64 * h + lane] = id[h];
                     }
             }

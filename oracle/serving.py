@@ -321,14 +321,14 @@ def select(logits, scores, beams, keep, done=None, eos=-1, softcap=0.0):
             y = softcap * np.tanh(x[ok] / softcap) if softcap else x[ok]
             top = y.max()
             p = np.exp(y - top)
-            lse = top + math.log(p.sum())
+            log_sum = math.log(p.sum())                  # against the largest: a score is not added to a large logit
             off = 2.0 ** -24 * (2 * float(p @ (top - y)) / p.sum() + 80)
             if softcap:
                 off += softcap * 2.0 ** -21 if softcap <= 256 else float(np.abs(y).max()) * 2.0 ** -19
             loose[b] = max(loose[b], off)
             # the order within a beam is the logits' own, ties to the lowest token
             at = np.argsort(-x[ok], kind="stable")[:keep + 1]
-            all_.append(s + y[at] - lse)
+            all_.append(s + ((y[at] - top) - log_sum))
             token.append(np.flatnonzero(ok)[at])
             parent.append(np.full(len(at), w))
         all_, token, parent = np.concatenate(all_), np.concatenate(token), np.concatenate(parent)

@@ -1,0 +1,34 @@
+"""Rows of logits at the ends of their type, and equal scores, on the GPU."""
+import math
+
+import pytest
+import torch
+
+from lossless_entropy_coding_amd import beam
+from test_gpu_beam import INF, _check, _logits
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("half", [True, False])
+@pytest.mark.parametrize("vocab", [300, 40000])
+def test_rows_of_large_logits_keep_their_scores(half, vocab):
+    """Rows whose mask, the type's lowest value, leaves nothing are uniform over all tokens, and those that are large
+    everywhere are as the same ones near 0: a score is not lost beside its logits."""
+    dt = torch.bfloat16 if half else torch.float32
+    x, s = _logits(vocab, 6, vocab, half)
+    x[0] = torch.finfo(dt).min
+    x[1, ::7] = torch.finfo(dt).min
+    x[2] = torch.finfo(dt).max
+    x[3] = 1e12
+    x[4] = -1e20
+    x[4, :3] = 1e30
+    for beams, keep in ((1, 2), (2, 5), (6, 7)):
+        _check(x, s, beams, keep)
+        _check(x, s, beams, keep, softcap=30.0)
+    got = beam.Beams(6, 1, keep=1).select(x.cuda(), torch.tensor(s).cuda())
+    # the sum is right to 2^-17, and a score of up to 32 is rounded to 2^-20
+    for row, tokens in ((0, vocab), (2, vocab), (3, vocab), (4, 3)):
+        assert abs(float(got.scores[row, 0]) - (s[row] - math.log(tokens))) <= 2.0 ** -17 + 2.0 ** -20
+    got = beam.Beams(6, 1, keep=1).select(x.cuda(), torch.tensor(s).cuda(), softcap=1e30)
+    assert abs(float(got.scores[0, 0]) - (s[0] - math.log(vocab))) <= 2.0 ** -17 + 2.0 ** -20
