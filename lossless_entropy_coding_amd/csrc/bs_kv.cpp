@@ -537,7 +537,7 @@ bs_status bs_kv_batch_async(const bs_kv_cache* cache, const bs_kv_batch* batch, 
                  {batch->d_lead, 4 * n}, {batch->d_shared, 4 * n}, {batch->d_info, 16 + 32 * (batch->n_groups + n)}, {batch->d_rows, 4 * n}};
     for (const auto& x : in)
         for (const auto& y : out)
-            if (x.p && y.p && overlap(x.p, x.bytes, y.p, y.bytes) && !(x.p == d_seqs && y.p == d_seqs)) {   // a plan's own rows may be given
+            if (x.p && y.p && overlap(x.p, x.bytes, y.p, y.bytes) && !(&x == in && x.p == batch->d_rows && y.p == batch->d_rows)) {   // a plan's own rows may be given
                 set_error("the plan overlaps rows, counts or groups");
                 return BS_E_INVAL;
             }

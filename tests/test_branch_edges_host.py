@@ -1,11 +1,14 @@
 """Corners of the operators for several continuations that need no GPU: buffers
 that lie over each other, workspaces, the references at the ends of a type."""
+import ctypes as C
 import math
 
 import numpy as np
 import pytest
 
+from lossless_entropy_coding_amd import _lib as L
 from oracle import serving as S
+from test_branches_host import AT, PLAN, _cache, _plan
 
 
 # --------------------------------------------------------------------- beams
@@ -17,3 +20,21 @@ def test_the_reference_keeps_scores_beside_large_logits(value):
     out, tok, par, _, _, _ = S.select(x, np.array([-5.0, -40.0]), 2, 3)
     np.testing.assert_allclose(out, [[-5.0 - math.log(50)] * 3], rtol=1e-12)
     assert tok.tolist() == [[0, 1, 2]] and par.tolist() == [[0, 0, 0]]
+
+
+# --------------------------------------------------------------------- plans
+BUFFERS = [n for n in PLAN if n.startswith("d_")]
+
+
+@pytest.mark.parametrize("name", BUFFERS)
+@pytest.mark.parametrize("which", ["rows", "counts", "groups"])
+def test_inputs_that_are_the_plans_own_buffers(name, which):
+    """From a buffer's first byte on; only the plan's own rows may be given as rows."""
+    if (name, which) == ("d_rows", "rows"):
+        return
+    args = {"rows": AT, "counts": AT + 256, "groups": AT + 512, which: PLAN[name]}
+    assert L.lib().bs_kv_batch_async(C.byref(_cache()), C.byref(_plan()), *args.values(), None) == L.BS_E_INVAL
+    # nor do the rows make it right that another input is there, too
+    if which != "rows":
+        args["rows"] = PLAN["d_rows"]
+        assert L.lib().bs_kv_batch_async(C.byref(_cache()), C.byref(_plan()), *args.values(), None) == L.BS_E_INVAL
