@@ -770,7 +770,8 @@ typedef struct {
 /* Make the plan from d_seqs [n_seqs] (a row may be named more than once),
  * d_counts [n_seqs] (NULL: one token each) and d_groups [n_groups + 1] (NULL:
  * one group of all rows, n_groups 1), none of them in the plan's buffers
- * (d_seqs may be d_rows).  One kernel launch. */
+ * (d_seqs may be d_rows), which overlap neither each other nor the cache's
+ * table and lengths.  One kernel launch. */
 bs_status bs_kv_batch_async(const bs_kv_cache* cache, const bs_kv_batch* batch, const int32_t* d_seqs,
                             const int32_t* d_counts, const int32_t* d_groups, void* stream);
 

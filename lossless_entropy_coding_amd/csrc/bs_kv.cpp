@@ -289,6 +289,23 @@ bs_status check_batch(const bs_kv_batch* b) {
     return BS_OK;
 }
 
+struct Range {
+    const void* p;
+    uint64_t bytes;
+};
+
+bool over(const Range& a, const Range& b) { return a.p && b.p && overlap(a.p, a.bytes, b.p, b.bytes); }
+
+// a plan's buffers, its rows first
+struct Plan {
+    static constexpr int kBuffers = 8;
+    Range at[kBuffers];
+    explicit Plan(const bs_kv_batch& b)
+        : at{{b.d_rows, 4ull * b.n_seqs}, {b.d_starts, 4ull * b.n_seqs + 4}, {b.d_places, 4ull * b.total}, {b.d_slots, 8ull * b.total},
+             {b.d_table, 4ull * b.n_seqs * b.width}, {b.d_lead, 4ull * b.n_seqs}, {b.d_shared, 4ull * b.n_seqs},
+             {b.d_info, 16 + 32 * ((uint64_t)b.n_groups + b.n_seqs)}} {}
+};
+
 }  // namespace
 
 extern "C" {
@@ -531,16 +548,17 @@ bs_status bs_kv_batch_async(const bs_kv_cache* cache, const bs_kv_batch* batch, 
         return BS_E_INVAL;
     }
     if (!d_groups && batch->n_groups != 1) { set_error("%u groups without their offsets", batch->n_groups); return BS_E_INVAL; }
-    const uint64_t n = batch->n_seqs, total = batch->total;
-    const struct { const void* p; uint64_t bytes; } in[] = {{d_seqs, 4 * n}, {d_counts, 4 * n}, {d_groups, 4ull * batch->n_groups + 4}},
-        out[] = {{batch->d_starts, 4 * n + 4}, {batch->d_places, 4 * total}, {batch->d_slots, 8 * total}, {batch->d_table, 4 * n * batch->width},
-                 {batch->d_lead, 4 * n}, {batch->d_shared, 4 * n}, {batch->d_info, 16 + 32 * (batch->n_groups + n)}, {batch->d_rows, 4 * n}};
-    for (const auto& x : in)
-        for (const auto& y : out)
-            if (x.p && y.p && overlap(x.p, x.bytes, y.p, y.bytes) && !(&x == in && x.p == batch->d_rows && y.p == batch->d_rows)) {   // a plan's own rows may be given
-                set_error("the plan overlaps rows, counts or groups");
-                return BS_E_INVAL;
-            }
+    const uint64_t n = batch->n_seqs;
+    const Range in[] = {{d_seqs, 4 * n}, {d_counts, 4 * n}, {d_groups, 4ull * batch->n_groups + 4},
+                        {cache->d_table, 4ull * b.c.max_seqs * b.c.max_pages}, {cache->d_lens, 4ull * b.c.max_seqs}};
+    const Plan out(*batch);
+    for (int i = 0; i < Plan::kBuffers; i++) {
+        bool bad = false;
+        for (const Range& x : in)                                // a plan's own rows may be given
+            bad = bad || (over(x, out.at[i]) && !(&x == in && i == 0 && d_seqs == batch->d_rows));
+        for (int j = 0; j < i; j++) bad = bad || over(out.at[j], out.at[i]);
+        if (bad) { set_error("a buffer of the plan overlaps another of the call, or the cache's"); return BS_E_INVAL; }
+    }
     b.n = batch->n_seqs;
     b.groups = batch->n_groups;
     b.total = batch->total;

@@ -38,3 +38,17 @@ def test_inputs_that_are_the_plans_own_buffers(name, which):
     if which != "rows":
         args["rows"] = PLAN["d_rows"]
         assert L.lib().bs_kv_batch_async(C.byref(_cache()), C.byref(_plan()), *args.values(), None) == L.BS_E_INVAL
+
+
+@pytest.mark.parametrize("name", BUFFERS)
+def test_plans_whose_buffers_lie_over_others(name):
+    """Over each other, or over what the call reads of the cache."""
+    f, cache = L.lib().bs_kv_batch_async, _cache(d_table=AT + 32768, d_lens=AT + 40960)
+    sizes = {"d_rows": 12, "d_starts": 16, "d_places": 20, "d_slots": 40, "d_table": 48, "d_lead": 12, "d_shared": 12, "d_info": 176}
+    for other in BUFFERS:
+        if other != name:
+            last = PLAN[other] + (sizes[other] - 1) // 16 * 16
+            for at in (PLAN[other], last):
+                assert f(C.byref(cache), C.byref(_plan(**{name: at})), AT, AT + 256, AT + 512, None) == L.BS_E_INVAL, (other, at)
+    for at in (AT + 32768, AT + 32768 + 48, AT + 40960):         # 4 rows of 4 pages, 4 lengths
+        assert f(C.byref(cache), C.byref(_plan(**{name: at})), AT, AT + 256, AT + 512, None) == L.BS_E_INVAL, at
