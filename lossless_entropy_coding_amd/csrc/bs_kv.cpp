@@ -482,6 +482,8 @@ bs_status bs_kv_attend_shared_async(const bs_kv_cache* cache, const bs_kv_attend
     if (rc != BS_OK) return rc;
     if (batch->n_seqs == 0 || batch->total == 0) return BS_OK;
     bsd::KvAttend& a = y.s.a;
+    for (const Range& x : Plan(*batch).at)
+        if (over(x, Range{d_work, y.need})) { set_error("the workspace overlaps the plan"); return BS_E_INVAL; }
     if (a.many) return bs_kv_attend_async(cache, &y.plain, d_work, work_bytes, stream);
     if (!a.q || !a.out) { set_error("NULL argument"); return BS_E_INVAL; }
     if (!aligned(a.q, 2) || !aligned(a.out, 2) || !aligned(a.lse, 4)) { set_error("misaligned queries or results"); return BS_E_INVAL; }
@@ -490,12 +492,10 @@ bs_status bs_kv_attend_shared_async(const bs_kv_cache* cache, const bs_kv_attend
         set_error("workspace of %llu B, %llu B needed", (unsigned long long)work_bytes, (unsigned long long)y.need);
         return BS_E_INVAL;
     }
-    const uint64_t row = (uint64_t)a.heads * a.c.dim, n = batch->n_seqs;
+    const uint64_t row = (uint64_t)a.heads * a.c.dim;
     if (overlap(d_work, y.need, a.out, extent(a.total, a.out_stride, row, 2)) || overlap(d_work, y.need, a.q, extent(a.total, a.q_stride, row, 2)) ||
-        (a.lse && overlap(d_work, y.need, a.lse, 4ull * a.total * a.heads)) || overlap(d_work, y.need, batch->d_rows, 4 * n) ||
-        overlap(d_work, y.need, batch->d_starts, 4 * n + 4) || overlap(d_work, y.need, batch->d_places, 4ull * batch->total) ||
-        overlap(d_work, y.need, batch->d_info, 16 + 32 * (batch->n_groups + n))) {
-        set_error("the workspace overlaps queries, results or the plan");
+        (a.lse && overlap(d_work, y.need, a.lse, 4ull * a.total * a.heads))) {
+        set_error("the workspace overlaps queries or results");
         return BS_E_INVAL;
     }
     a.part = (float*)d_work + bsd::kKvCounters;

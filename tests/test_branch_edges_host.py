@@ -8,7 +8,7 @@ import pytest
 
 from lossless_entropy_coding_amd import _lib as L
 from oracle import serving as S
-from test_branches_host import AT, PLAN, _cache, _plan
+from test_branches_host import AT, PLAN, _attend, _cache, _plan
 
 
 # --------------------------------------------------------------------- beams
@@ -52,3 +52,16 @@ def test_plans_whose_buffers_lie_over_others(name):
                 assert f(C.byref(cache), C.byref(_plan(**{name: at})), AT, AT + 256, AT + 512, None) == L.BS_E_INVAL, (other, at)
     for at in (AT + 32768, AT + 32768 + 48, AT + 40960):         # 4 rows of 4 pages, 4 lengths
         assert f(C.byref(cache), C.byref(_plan(**{name: at})), AT, AT + 256, AT + 512, None) == L.BS_E_INVAL, at
+
+
+# ------------------------------------------------------- attention of groups
+@pytest.mark.parametrize("name", BUFFERS)
+@pytest.mark.parametrize("many", [False, True])
+def test_workspaces_that_lie_over_the_plan(name, many):
+    lib, cache = L.lib(), _cache(max_pages=4096)
+    at = dict(total=40, max_new=32) if many else {}
+    plan = _plan(**at)
+    need, work = int(lib.bs_kv_attend_shared_work_bytes(C.byref(cache), C.byref(_attend()), C.byref(plan))), 1 << 40
+    assert need > 4096
+    bad = _plan(**at, **{name: work + 4096})
+    assert lib.bs_kv_attend_shared_async(C.byref(cache), C.byref(_attend()), C.byref(bad), work, need, None) == L.BS_E_INVAL
