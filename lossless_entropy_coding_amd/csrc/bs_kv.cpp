@@ -219,7 +219,7 @@ bs_status shared_args(const bs_kv_cache* cache, const bs_kv_attend_args* x, cons
     const uint64_t stack = (rows + std::max<uint64_t>(1, groups) - 1) / std::max<uint64_t>(1, groups);
     const uint64_t tall = s.a.c.wide <= 128 && stack >= bsd::kKvStack ? 32 : 16;
     const uint64_t pre = std::max<uint64_t>(1, groups * ((stack + tall - 1) / tall) * s.a.c.kv_heads), own = (uint64_t)b->n_seqs * s.row_blocks * s.a.c.kv_heads;
-    s.pre = (uint32_t)std::min(most, std::max<uint64_t>(1, (own >= 2 * (uint64_t)cus ? 1 : 2) * (uint64_t)cus / pre));
+    s.pre = groups ? (uint32_t)std::min(most, std::max<uint64_t>(1, (own >= 2 * (uint64_t)cus ? 1 : 2) * (uint64_t)cus / pre)) : 0;
     s.own = (uint32_t)std::min(most, std::max<uint64_t>(1, 2 * (uint64_t)cus / own));
     if ((((uint64_t)s.a.c.kv_heads * s.pre + 7) / 8 * 8 * s.blocks + own * s.own) > kThreads / 256 ||
         (uint64_t)b->n_seqs * b->max_new > kThreads / 64) {

@@ -71,7 +71,7 @@ struct KvShared {
     uint32_t groups;
     uint32_t blocks;            // row blocks of all groups at most
     uint32_t row_blocks;        // of one row's own tokens
-    uint32_t pre, own;          // splits of a group's common tokens, and of a row's own
+    uint32_t pre, own;          // splits of a group's common tokens (0: there are no groups), and of a row's own
 };
 
 // the plan of a step's tokens (bs_kv_batch of bs.h)

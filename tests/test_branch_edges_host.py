@@ -65,3 +65,13 @@ def test_workspaces_that_lie_over_the_plan(name, many):
     assert need > 4096
     bad = _plan(**at, **{name: work + 4096})
     assert lib.bs_kv_attend_shared_async(C.byref(cache), C.byref(_attend()), C.byref(bad), work, need, None) == L.BS_E_INVAL
+
+
+@pytest.mark.parametrize("rows", [1, 7, 512, 4096])
+@pytest.mark.parametrize("pages", [1, 100, 8192])
+def test_no_groups_need_no_more_workspace_than_one(rows, pages):
+    lib, cache = L.lib(), _cache(kv_heads=8, head_dim=128, max_pages=pages)
+    args = _attend(heads=40, q_stride=5120, out_stride=5120)
+    need = [int(lib.bs_kv_attend_shared_work_bytes(C.byref(cache), C.byref(args), C.byref(_plan(n_seqs=rows, total=rows, max_new=1, n_groups=n))))
+            for n in (0, 1)]
+    assert 4096 < need[0] <= need[1]
