@@ -153,13 +153,14 @@ __global__ __launch_bounds__(kThreads) void batch_kernel(KvBatch b, int small) {
 
     for (uint32_t s = s0 + part * kThreads + t; s < s1; s += gridDim.y * kThreads) {
         const int64_t place = (int64_t)len - (int64_t)count + (int64_t)(s - s0);
+        const bool has = place >= 0 && count <= b.max_new;           // (attention leaves longer rows out)
         int64_t slot = -1;
-        if (place >= 0) {
+        if (has) {
             const int32_t pg = trow[place >> c.lp];
             if (pg >= 0 && (uint32_t)pg < c.n_pages) slot = ((int64_t)pg << c.lp) + (place & (c.page - 1));
             else err = 4u;
         }
-        b.places[s] = place >= 0 && count <= b.max_new ? (int32_t)place : -1;   // (attention leaves longer rows out)
+        b.places[s] = has ? (int32_t)place : -1;
         b.slots[s] = slot;
     }
     if (i + 1 == b.n)                                               // tokens of no row
