@@ -33,6 +33,9 @@ __device__ __forceinline__ void store_through(int32_t* p, int32_t v) {
 }
 
 constexpr uint32_t kSmall = 8192, kSmallRows = 512;   // pages of all rows, and rows and groups
+// Pages that all rows have room for: rows may be longer than the plan's table is
+// wide, and their pages are to be counted in 32 bits and read in a few ms.
+constexpr uint64_t kSmallRoom = 1ull << 22;
 
 __device__ __forceinline__ int32_t wave_min(int32_t x) {
 #pragma unroll
@@ -277,7 +280,8 @@ __global__ __launch_bounds__(kThreads) void batch_kernel(KvBatch b, int small) {
 extern "C" int bsk_kv_batch(const KvBatch* b, void* stream) {
     const uint32_t most = std::max(std::min(b->max_new, b->total), b->width);
     const uint32_t parts = std::min(kMaxParts, std::max(1u, (most + kSlice - 1) / kSlice));
-    const int small = (uint64_t)b->n * b->width <= kSmall && b->width && b->n <= kSmallRows && b->groups <= kSmallRows;
+    const int small = (uint64_t)b->n * b->width <= kSmall && b->width && b->n <= kSmallRows && b->groups <= kSmallRows &&
+                      (uint64_t)b->n * b->c.max_pages <= kSmallRoom;
     hipLaunchKernelGGL(batch_kernel, dim3(b->n, parts), dim3(kThreads), 0, (hipStream_t)stream, *b, small);
     return (int)hipGetLastError();
 }

@@ -34,3 +34,18 @@ def test_a_plan_of_its_own_rows():
         with pytest.raises(Exception, match="overlaps"):
             b.update(own, groups=_ids(0, 3, 6))
     cache.check()
+
+
+def test_plans_of_rows_far_longer_than_said():
+    """width and max_len decide the size of the table and no more: rows of 2^27 tokens, named 512 times in all, whose pages differ from
+    the first one on."""
+    t = lambda *s, k=torch.int32: torch.zeros(*s, dtype=k, device="cuda")     # noqa: E731
+    table = t(2, 1 << 23)
+    table[1] = 1
+    cache = kv.KvCache.over(t(1, 2, 1, 16, 64, k=torch.uint8), t(1, 2, 1, 64, 16, k=torch.uint8), t(1, 2, 1, 2, k=torch.float32),
+                            t(2), table, t(2).fill_(1 << 27), head_dim=8)
+    b = kv.KvBatch(cache, _ids(*[0, 1] * 256), max_len=16)
+    assert int(b.shared.abs().max()) == 0 and b.places.unique().tolist() == [(1 << 27) - 1] and b.table.flatten().tolist() == [0, 1] * 256
+    b.update(_ids(*[1] * 512))
+    assert b.shared.unique().tolist() == [1 << 27]
+    cache.check()
