@@ -829,11 +829,11 @@ __global__ __launch_bounds__(kScan) void reorder_plan_kernel(KvPages p) {
 }
 
 // The first `tables` workgroups move the rows of the table, 2^lc columns of
-// all rows each: a column of a row depends on no other column, so its old
+// all rows at a time: a column of a row depends on no other column, so its old
 // entries go to LDS first and nothing is overwritten too early.  Pages' counts
 // change where an entry does: the rows of a beam search have most in common.
 // The other workgroups copy pages.
-__global__ __launch_bounds__(256) void reorder_move_kernel(KvPages p, uint32_t tables, uint32_t lc, uint32_t parts) {
+__global__ __launch_bounds__(256) void reorder_move_kernel(KvPages p, uint32_t tables, uint32_t blocks, uint32_t lc, uint32_t parts) {
     const KvView& c = p.c;
     __shared__ int32_t entry[kKvReorder];
     if (!p.work[0]) return;
@@ -848,61 +848,64 @@ __global__ __launch_bounds__(256) void reorder_move_kernel(KvPages p, uint32_t t
         return;
     }
     constexpr int32_t kNone = -0x7FFFFFFF - 1;                   // no entry of a row
-    const uint32_t c0 = blockIdx.x << lc, many = p.n << lc;
-    int any = 0;
-    for (uint32_t i = t; i < p.n; i += 256) any |= pages_of(c, (uint32_t)max(w.before[i], w.after[i])) > c0;
-    if (!__syncthreads_or(any)) return;
-    // four entries of a thread at a time, their loads together
-    constexpr uint32_t U = 4;
-    for (uint32_t x0 = t; x0 < many; x0 += U * 256) {
-        int32_t r[U], len[U], got[U];
+    const uint32_t many = p.n << lc;
+    for (uint32_t block = blockIdx.x; block < blocks; block += tables) {
+        const uint32_t c0 = block << lc;
+        int any = 0;
+        for (uint32_t i = t; i < p.n; i += 256) any |= pages_of(c, (uint32_t)max(w.before[i], w.after[i])) > c0;
+        if (!__syncthreads_or(any)) return;
+        // four entries of a thread at a time, their loads together
+        constexpr uint32_t U = 4;
+        for (uint32_t x0 = t; x0 < many; x0 += U * 256) {
+            int32_t r[U], len[U], got[U];
 #pragma unroll
-        for (uint32_t u = 0; u < U; u++) {
-            const uint32_t i = min(x0 + u * 256, many - 1) >> lc;
-            r[u] = p.a[i];
-            len[u] = w.before[i];
-        }
-#pragma unroll
-        for (uint32_t u = 0; u < U; u++) {
-            const uint32_t x = min(x0 + u * 256, many - 1), col = c0 + (x & ((1u << lc) - 1));
-            got[u] = col < pages_of(c, (uint32_t)len[u]) ? c.table[(uint64_t)(uint32_t)r[u] * c.max_pages + col] : kNone;
-        }
-#pragma unroll
-        for (uint32_t u = 0; u < U; u++)
-            if (x0 + u * 256 < many) entry[x0 + u * 256] = got[u];
-    }
-    __syncthreads();
-    for (uint32_t x0 = t; x0 < many; x0 += U * 256) {
-        int32_t r[U], q[U], len[U], own[U];
-#pragma unroll
-        for (uint32_t u = 0; u < U; u++) {
-            const uint32_t i = min(x0 + u * 256, many - 1) >> lc;
-            r[u] = p.a[i];
-            q[u] = p.b[i];
-            len[u] = w.after[i];
-            own[u] = w.own[i];
-        }
-#pragma unroll
-        for (uint32_t u = 0; u < U; u++) {
-            const uint32_t x = x0 + u * 256, in = x & ((1u << lc) - 1), col = c0 + in;
-            if (x >= many) break;
-            const int32_t had = entry[x];
-            int32_t now = kNone;
-            if (q[u] >= 0 && col < pages_of(c, (uint32_t)len[u]))
-                now = own[u] >= 0 && col == (uint32_t)len[u] >> c.lp ? own[u] : entry[((uint32_t)q[u] << lc) + in];
-            if (now == had) continue;
-            if (had != kNone) {
-                if (had < 0 || (uint32_t)had >= c.n_pages) {
-                    flag(c.status, kStId);
-                } else if (atomicSub(c.refs + had, 1) <= 0) {
-                    atomicAdd(c.refs + had, 1);
-                    flag(c.status, kStCount);
-                }
+            for (uint32_t u = 0; u < U; u++) {
+                const uint32_t i = min(x0 + u * 256, many - 1) >> lc;
+                r[u] = p.a[i];
+                len[u] = w.before[i];
             }
-            if (now != kNone) {
-                if (now < 0 || (uint32_t)now >= c.n_pages) flag(c.status, kStId);
-                else atomicAdd(c.refs + now, 1);
-                c.table[(uint64_t)(uint32_t)r[u] * c.max_pages + col] = now;
+#pragma unroll
+            for (uint32_t u = 0; u < U; u++) {
+                const uint32_t x = min(x0 + u * 256, many - 1), col = c0 + (x & ((1u << lc) - 1));
+                got[u] = col < pages_of(c, (uint32_t)len[u]) ? c.table[(uint64_t)(uint32_t)r[u] * c.max_pages + col] : kNone;
+            }
+#pragma unroll
+            for (uint32_t u = 0; u < U; u++)
+                if (x0 + u * 256 < many) entry[x0 + u * 256] = got[u];
+        }
+        __syncthreads();
+        for (uint32_t x0 = t; x0 < many; x0 += U * 256) {
+            int32_t r[U], q[U], len[U], own[U];
+#pragma unroll
+            for (uint32_t u = 0; u < U; u++) {
+                const uint32_t i = min(x0 + u * 256, many - 1) >> lc;
+                r[u] = p.a[i];
+                q[u] = p.b[i];
+                len[u] = w.after[i];
+                own[u] = w.own[i];
+            }
+#pragma unroll
+            for (uint32_t u = 0; u < U; u++) {
+                const uint32_t x = x0 + u * 256, in = x & ((1u << lc) - 1), col = c0 + in;
+                if (x >= many) break;
+                const int32_t had = entry[x];
+                int32_t now = kNone;
+                if (q[u] >= 0 && col < pages_of(c, (uint32_t)len[u]))
+                    now = own[u] >= 0 && col == (uint32_t)len[u] >> c.lp ? own[u] : entry[((uint32_t)q[u] << lc) + in];
+                if (now == had) continue;
+                if (had != kNone) {
+                    if (had < 0 || (uint32_t)had >= c.n_pages) {
+                        flag(c.status, kStId);
+                    } else if (atomicSub(c.refs + had, 1) <= 0) {
+                        atomicAdd(c.refs + had, 1);
+                        flag(c.status, kStCount);
+                    }
+                }
+                if (now != kNone) {
+                    if (now < 0 || (uint32_t)now >= c.n_pages) flag(c.status, kStId);
+                    else atomicAdd(c.refs + now, 1);
+                    c.table[(uint64_t)(uint32_t)r[u] * c.max_pages + col] = now;
+                }
             }
         }
     }
@@ -970,8 +973,9 @@ extern "C" int bsk_kv_reorder(const KvPages* p, void* stream) {
     hipLaunchKernelGGL(reorder_plan_kernel, dim3(1), dim3(kScan), 0, st, *p);
     uint32_t lc = 0;
     while (lc < 8 && p->n << (lc + 1) <= 1024) lc++;                 // four entries to a thread, where rows are that few
-    const uint32_t tables = (p->c.max_pages + (1u << lc) - 1) >> lc, parts = copy_parts(p->c);
+    // (rows of up to 2^27 pages: a workgroup for each few columns would pass the threads of a launch)
+    const uint32_t blocks = (p->c.max_pages + (1u << lc) - 1) >> lc, tables = std::min(blocks, 1u << 16), parts = copy_parts(p->c);
     const uint32_t copies = (uint32_t)std::min<uint64_t>((uint64_t)p->n * p->c.layers * parts, 8192);
-    hipLaunchKernelGGL(reorder_move_kernel, dim3(tables + copies), dim3(256), 0, st, *p, tables, lc, parts);
+    hipLaunchKernelGGL(reorder_move_kernel, dim3(tables + copies), dim3(256), 0, st, *p, tables, blocks, lc, parts);
     return (int)hipGetLastError();
 }

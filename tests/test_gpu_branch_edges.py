@@ -5,7 +5,7 @@ import torch
 
 from lossless_entropy_coding_amd import kv
 from test_gpu_branches import _branched, _plan_same
-from test_gpu_kv import _ids
+from test_gpu_kv import _ids, _pair, _same
 
 pytestmark = pytest.mark.gpu
 
@@ -49,3 +49,40 @@ def test_plans_of_rows_far_longer_than_said():
     b.update(_ids(*[1] * 512))
     assert b.shared.unique().tolist() == [1 << 27]
     cache.check()
+
+
+# ------------------------------------------------------------------- reorder
+def test_moves_of_rows_of_many_pages():
+    """More blocks of columns than a launch has workgroups for: each takes several."""
+    rng = np.random.default_rng(5)
+    cache, model = _pair(layers=1, kv_heads=1, head_dim=8, n_pages=3000, max_seqs=520, max_pages=66000, page_tokens=16, dtype="int8")
+    rows = [int(r) for r in rng.permutation(520)]
+    model.lens[rows] = [65990 * 16 - 3, 65537 * 16] + [int(c) for c in rng.integers(0, 40, 518)]
+    for r in rows:                                               # pages of any row, the last thousand are free
+        held = model.table[r, :model.pages(model.lens[r])]
+        held[:] = rng.integers(0, 2000, len(held))
+        np.add.at(model.refs, held, 1)
+    for name in ("table", "lens", "refs"):
+        getattr(cache, name).copy_(torch.from_numpy(getattr(model, name)))
+    for step in range(3):
+        parents = [int(q) for q in rng.permutation(520)]
+        parents[7], parents[8] = parents[int(rng.integers(0, 7))], -1
+        cache.reorder(_ids(*rows), _ids(*parents))
+        model.reorder(rows, parents)
+        _same(cache, model)
+        assert model.status == 0 and int(model.lens.max()) > 65536 * 16
+
+
+def test_moves_in_the_widest_table_are_checked():
+    """As many columns as a table can have, for as many rows as a call takes (named more than once, so nothing moves)."""
+    t = lambda *s, k=torch.int32: torch.zeros(*s, dtype=k, device="cuda")     # noqa: E731
+    cache = kv.KvCache.over(t(1, 4, 1, 16, 64, k=torch.uint8), t(1, 4, 1, 64, 16, k=torch.uint8), t(1, 4, 1, 2, k=torch.float32),
+                            t(4), t(1, (1 << 27) - 16), t(1).fill_(40), head_dim=8)
+    for n in (129, 4096):
+        cache.reorder(t(n), t(n))
+        torch.cuda.synchronize()
+        assert int(cache.status.item()) == 4 and cache.lens.tolist() == [40]
+        cache.status.zero_()
+    cache.reorder(t(1), t(1).fill_(-1))
+    torch.cuda.synchronize()
+    assert cache.lens.tolist() == [0]
