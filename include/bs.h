@@ -748,6 +748,10 @@ uint64_t bs_kv_reorder_work_bytes(const bs_kv_cache* cache, uint32_t n);
  *                          the same pages, rounded down to a multiple of 64
  *   d_info   [4 + 8 (n_groups + n_seqs)]  for bs_kv_attend_shared_async; 16-B aligned,
  *                          its first word is 0 before the first call and between calls
+ * A row that has fewer than 64 tokens in common with its group's first one (a
+ * beam that was emptied and grows anew) makes d_shared 0, but stands alone in
+ * attention (d_info): the others read their common tokens together, if they
+ * are two at least and half of the group.
  * A row that does not exist, a count that is negative, above max_new or the
  * row's length, counts that do not add up to total, offsets of groups that do
  * not ascend: flagged (BS_KV_BAD_ID); tokens without a place or page get -1. */
@@ -823,7 +827,7 @@ uint64_t bs_kv_attend_work_bytes(const bs_kv_cache* cache, const bs_kv_attend_ar
 
 /* Attention of a plan's tokens: as bs_kv_attend_async on the plan's rows and
  * offsets, to rounding, with the tokens that a group's rows have in common
- * (d_shared) read once for all of them.  Of args, n_seqs, total_q, max_new,
+ * read once for all of them.  Of args, n_seqs, total_q, max_new,
  * d_seqs and d_starts are the plan's and not looked at.  A token that the plan
  * gives no place sees nothing.  Rows' own tokens and the groups' common ones
  * are split over workgroups, and a second launch adds a row's parts: scores

@@ -7,7 +7,7 @@
 // another.  A row is compared with the first of its group, page by page; the
 // workgroup that ends last takes the least of each group.  Where a plan is
 // small, each row's workgroup compares its whole group instead, and none is
-// the last: 64 rows of 127 pages 8.9 -> 6.1 us, chains of dependent loads
+// the last: 64 rows of 127 pages 8.9 -> 6.2 us, chains of dependent loads
 // either way; for more pages than kSmall the reads would be repeated too often.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -49,6 +49,16 @@ __device__ __forceinline__ void record(int32_t* to, int32_t s0, int32_t s1, int3
     *(int4*)(to + 4) = make_int4(low, high, 0, 0);
 }
 
+// A group's common tokens, as attention takes them: `few`, the least of those
+// `members` of its n rows that have a tile or more in common with the first.  A
+// row that has not (a beam that was emptied and grew anew) stands alone and
+// costs the others nothing, unless most rows do: all rows of a group are
+// multiplied with its common tokens.  (32 samples over 8000 tokens, one of them
+// ended: attention 34 us, 69 with each row by itself.)
+__device__ __forceinline__ int32_t in_common(uint32_t n, uint32_t members, int32_t few) {
+    return members == n || (members >= 2 && members >= n - members) ? few : 0;
+}
+
 // A small plan's groups: the row's own, `from` .. `to` - 1 (none where from ==
 // to); `first` token of row i, `wrong` where the groups do not ascend.
 __device__ __forceinline__ void small_groups(const KvBatch& b, uint32_t i, uint32_t from, uint32_t to, uint32_t first, uint32_t end, int32_t row,
@@ -59,6 +69,20 @@ __device__ __forceinline__ void small_groups(const KvBatch& b, uint32_t i, uint3
     const uint32_t t = threadIdx.x, lane = t & 63u, wave = t >> 6, n = to - from, cap = c.max_pages << c.lp;
     int wrong = 0;
     for (uint32_t g = t; b.offs && g < b.groups; g += kThreads) wrong |= b.offs[g] < 0 || b.offs[g + 1] < b.offs[g] || b.offs[g + 1] > (int32_t)b.n;
+    // the least of the waves' numbers, in every thread
+    auto join = [&](int32_t few, int32_t lo, int32_t hi) {
+        few = wave_min(few);
+        lo = wave_min(lo);
+        hi = wave_min(-hi);
+        if (lane == 0) {
+            least[0][wave] = few;
+            least[1][wave] = lo;
+            least[2][wave] = hi;
+        }
+        __syncthreads();
+        if (t < 3) least[t][0] = min(min(least[t][0], least[t][1]), min(least[t][2], least[t][3]));
+        __syncthreads();
+    };
     // the group's rows, their lengths and places
     int32_t few = 0x7FFFFFFF, lo = 0x7FFFFFFF, hi = -1;
     uint32_t tokens = 0;
@@ -77,38 +101,55 @@ __device__ __forceinline__ void small_groups(const KvBatch& b, uint32_t i, uint3
         }
     }
     wrong = __syncthreads_or(wrong);
-    if (n) {
-        const uint32_t pages = ((uint32_t)lens[0] + c.page - 1) >> c.lp;
-        const int32_t* lead = c.table + (uint64_t)(uint32_t)rows[0] * c.max_pages;
-        for (uint32_t x = t; x < n * pages; x += kThreads) {
-            const uint32_t j = x / pages, col = x % pages;
-            const int32_t a = lead[col], d = c.table[(uint64_t)(uint32_t)rows[j] * c.max_pages + col];
-            // past a shorter row's end the entry may be anything: its length says less already
-            if (a != d || a < 0 || (uint32_t)a >= c.n_pages) few = min(few, (int32_t)(col << c.lp));
-        }
-    }
-    few = wave_min(few);
-    lo = wave_min(lo);
-    hi = -wave_min(-hi);
+    const uint32_t pages = n ? ((uint32_t)lens[0] + c.page - 1) >> c.lp : 0u;
+    const int32_t* lead = c.table + (uint64_t)(uint32_t)(n ? rows[0] : 0) * c.max_pages;
+    // (past a shorter row's end the entry may be anything: its length says less already)
+    auto differ = [&](uint32_t j, uint32_t col) {
+        const int32_t a = lead[col], d = c.table[(uint64_t)(uint32_t)rows[j] * c.max_pages + col];
+        return a != d || a < 0 || (uint32_t)a >= c.n_pages;
+    };
+    for (uint32_t x = t; x < n * pages; x += kThreads)
+        if (differ(x / pages, x % pages)) few = min(few, (int32_t)(x % pages << c.lp));
 #pragma unroll
     for (int s = 32; s; s >>= 1) tokens += __shfl_xor(tokens, s);
-    if (lane == 0) {
-        least[0][wave] = few;
-        least[1][wave] = lo;
-        least[2][wave] = -hi;
-        many[wave] = tokens;
-    }
-    __syncthreads();
-    if (t < 3) least[t][0] = min(min(least[t][0], least[t][1]), min(least[t][2], least[t][3]));
-    __syncthreads();
+    if (lane == 0) many[wave] = tokens;
+    join(few, lo, hi);
     const int32_t shared = n && !wrong ? least[0][0] & ~(int32_t)(kKvTile - 1) : 0;
+    int32_t most = shared, mine = shared;
+    if (__builtin_expect(n > 1 && !wrong && shared == 0, 0)) {
+        // some row has no tile in common with the first: again, a wave to a row
+        __shared__ int32_t own;
+        __shared__ uint32_t some[kWaves];
+        uint32_t members = 0;
+        few = lo = 0x7FFFFFFF, hi = -1;
+        for (uint32_t j = wave; j < n; j += kWaves) {
+            const int32_t len = lens[j];
+            int32_t s = min(len, lens[0]);
+            for (uint32_t col = lane; col < pages; col += 64)
+                if (differ(j, col)) s = min(s, (int32_t)(col << c.lp));
+            s = wave_min(s) & ~(int32_t)(kKvTile - 1);
+            if (lane == 0 && j == i - from) own = s;
+            if (s == 0) continue;
+            members++;
+            few = min(few, s);
+            const int32_t cnt = b.counts ? max(b.counts[from + j], 0) : 1;
+            if (cnt) {
+                lo = min(lo, len - min(cnt, len));
+                hi = max(hi, len - 1);
+            }
+        }
+        if (lane == 0) some[wave] = members;
+        join(few, lo, hi);
+        most = in_common(n, some[0] + some[1] + some[2] + some[3], least[0][0]);
+        mine = own ? most : 0;
+    }
     if (t == 0) {
         b.rows[i] = b.seqs[i];
         b.lead[i] = (int32_t)(n ? from : i);
         b.shared[i] = shared;
         b.starts[i] = (int32_t)first;
         if (i + 1 == b.n) b.starts[b.n] = (int32_t)end;
-        record(b.info + 4 + 8 * (b.groups + i), (int32_t)first, (int32_t)end, shared, row, low, high);
+        record(b.info + 4 + 8 * (b.groups + i), (int32_t)first, (int32_t)end, mine, row, low, high);
         if (i == 0 && wrong) flag(c.status, 4u);
     }
     // records of the groups: their first rows write them, the first row of all
@@ -120,7 +161,7 @@ __device__ __forceinline__ void small_groups(const KvBatch& b, uint32_t i, uint3
         if (wrong || f == e) {
             if (i == 0) record(to4, 0, 0, 0, -1, 0x7FFFFFFF, -1);
         } else if (f == (int32_t)i) {
-            record(to4, (int32_t)first, (int32_t)min(stop, (uint64_t)b.total), shared, rows[0], least[1][0], -least[2][0]);
+            record(to4, (int32_t)first, (int32_t)min(stop, (uint64_t)b.total), most, rows[0], least[1][0], -least[2][0]);
         }
     }
 }
@@ -252,22 +293,42 @@ __global__ __launch_bounds__(kThreads) void batch_kernel(KvBatch b, int small) {
         const int32_t f = b.offs ? b.offs[g] : 0, e = b.offs ? b.offs[g + 1] : (int32_t)b.n;
         const uint32_t from = (uint32_t)min(max(f, 0), (int32_t)b.n), to = (uint32_t)min(max(e, (int32_t)from), (int32_t)b.n);
         const int32_t* rec = b.info + 4 + 8 * b.groups;
+        const uint32_t n = to - from;
         int32_t few = 0x7FFFFFFF, low = 0x7FFFFFFF, high = -1;
-        for (uint32_t j = from + lane; j < to; j += 64) {
-            few = min(few, rec[8 * j + 2]);
-            low = min(low, rec[8 * j + 4]);
-            high = max(high, rec[8 * j + 5]);
-        }
+        // of the rows that have `least` tokens in common with the first: how
+        // many they all have, and the places of their new ones
+        auto join = [&](int32_t least) {
+            few = low = 0x7FFFFFFF, high = -1;
+            uint32_t members = 0;
+            for (uint32_t j = from + lane; j < to; j += 64) {
+                const int32_t s = rec[8 * j + 2], l = rec[8 * j + 4], h = rec[8 * j + 5];
+                const bool in = s >= least;
+                members += in;
+                few = min(few, in ? s : 0x7FFFFFFF);
+                low = min(low, in ? l : 0x7FFFFFFF);
+                high = max(high, in ? h : -1);
+            }
 #pragma unroll
-        for (int s = 32; s; s >>= 1) {
-            few = min(few, __shfl_xor(few, s));
-            low = min(low, __shfl_xor(low, s));
-            high = max(high, __shfl_xor(high, s));
+            for (int s = 32; s; s >>= 1) {
+                few = min(few, __shfl_xor(few, s));
+                low = min(low, __shfl_xor(low, s));
+                high = max(high, __shfl_xor(high, s));
+            }
+            return members;
+        };
+        join(0);
+        if (n == 0 || wrong) few = 0;
+        const int32_t all = few;
+        const bool apart = n > 1 && !wrong && few == 0;              // some row has no tile in common with the first
+        if (__builtin_expect(apart, 0)) {
+            uint32_t members = join(kKvTile);
+#pragma unroll
+            for (int s = 32; s; s >>= 1) members += __shfl_xor(members, s);
+            few = in_common(n, members, few);
         }
-        if (from == to || wrong) few = 0;
         for (uint32_t j = from + lane; j < to; j += 64) {
-            b.shared[j] = few;
-            b.info[4 + 8 * (b.groups + j) + 2] = few;
+            b.shared[j] = all;
+            if (!apart || rec[8 * j + 2]) b.info[4 + 8 * (b.groups + j) + 2] = few;
         }
         if (lane == 0)
             record(b.info + 4 + 8 * g, b.starts[from], b.starts[to], few, from < to ? max(b.seqs[from], 0) : -1, low, high);
