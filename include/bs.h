@@ -848,11 +848,12 @@ uint64_t bs_kv_attend_shared_work_bytes(const bs_kv_cache* cache, const bs_kv_at
  *
  * Of all continuations of a request's beams, a beam's score plus the log
  * probability of one more token, the best `keep`: by score, of equal ones the
- * lowest beam, then the lowest token.
+ * lowest beam, and within a beam by logit, of equal ones the lowest token.
  *
  *   score_w + y_wv - log sum_v exp(y_wv),  y = logit, or softcap tanh(logit / softcap)
  *
- * A beam's tokens are ordered by their logits.  A logit of -infinity is a
+ * (Under a soft cap logits beyond some 19 times the cap have equal scores in 64
+ * bits; the larger logit still comes first.)  A logit of -infinity is a
  * token that is not allowed (under a soft cap, too).  A beam whose score is
  * not finite, or whose logits hold a NaN or +infinity, has no continuations;
  * its logits are not read in the first case.  A beam that is done has one, the

@@ -56,8 +56,9 @@ class Beams:
         """The best continuations (bs_beam_select_async): logits (batch *
         beams, vocab) bfloat16 or float32, rows may be strided; scores float32
         and done int32 (not 0: the beam has ended) of batch * beams values.
-        softcap c: logits become c tanh(logit / c).  Calls go on one stream,
-        from any thread."""
+        softcap c: logits become c tanh(logit / c).  Of equal scores the
+        lowest beam comes first, within a beam the larger logit, then the lower
+        token.  Calls go on one stream, from any thread."""
         rows, kind = self.batch * self.beams, logits.dtype
         if logits.dim() != 2 or logits.shape[0] != rows or (kind is not torch.bfloat16 and kind is not torch.float32):
             raise ValueError(f"logits must be ({rows}, vocab) bfloat16 or float32")

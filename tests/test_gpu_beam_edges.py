@@ -32,3 +32,21 @@ def test_rows_of_large_logits_keep_their_scores(half, vocab):
         assert abs(float(got.scores[row, 0]) - (s[row] - math.log(tokens))) <= 2.0 ** -17 + 2.0 ** -20
     got = beam.Beams(6, 1, keep=1).select(x.cuda(), torch.tensor(s).cuda(), softcap=1e30)
     assert abs(float(got.scores[0, 0]) - (s[0] - math.log(vocab))) <= 2.0 ** -17 + 2.0 ** -20
+
+
+@pytest.mark.parametrize("half", [True, False])
+@pytest.mark.parametrize("softcap", [0.5, 30.0, 300.0])
+@pytest.mark.parametrize("keep", [1, 2, 5, 40])
+def test_saturated_logits_keep_their_order(half, softcap, keep):
+    """Where tanh is 1 in 64 bits scores are equal, and a beam's tokens still go by their logits, beams by their number."""
+    dt = torch.bfloat16 if half else torch.float32
+    x = torch.zeros(4, 3000)
+    for row in range(4):
+        x[row, torch.arange(50) * 53 + row] = softcap * (32 + torch.arange(50).roll(11 * row))     # all apart in 8 bits
+    x[1] = x[0]
+    x = x.to(dt)
+    got = beam.Beams(2, 2, keep=keep).select(x.cuda(), torch.zeros(4, device="cuda"), softcap=softcap)
+    best = x[0].float().argsort(descending=True, stable=True)[:keep].tolist()
+    assert got.scores[0].unique().numel() == 1
+    assert got.parents[0].tolist() == [0] * keep and got.tokens[0].tolist() == best
+    _check(x, [0.0, 0.0, -1.0, -2.0], 2, keep, softcap=softcap)
