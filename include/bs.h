@@ -828,8 +828,10 @@ uint64_t bs_kv_attend_work_bytes(const bs_kv_cache* cache, const bs_kv_attend_ar
 /* Attention of a plan's tokens: as bs_kv_attend_async on the plan's rows and
  * offsets, to rounding, with the tokens that a group's rows have in common
  * read once for all of them.  Of args, n_seqs, total_q, max_new,
- * d_seqs and d_starts are the plan's and not looked at.  A token that the plan
- * gives no place sees nothing.  Rows' own tokens and the groups' common ones
+ * d_seqs and d_starts are the plan's and not looked at.  Of a row that has more
+ * new tokens than it holds, the first see nothing.  Results of a row with more
+ * than max_new, and of tokens behind the last row's, are left as they were (the
+ * plan is flagged).  Rows' own tokens and the groups' common ones
  * are split over workgroups, and a second launch adds a row's parts: scores
  * and sums are held in fp32, probabilities enter the second product in 16
  * significant bits, or, for the common tokens of a group of 64 tokens x heads

@@ -1,8 +1,11 @@
 """Corners of the attention of groups, on the GPU."""
 import numpy as np
 import pytest
+import torch
 
-from test_gpu_kv import _fill, _ids
+from lossless_entropy_coding_amd import kv
+from oracle import serving as S
+from test_gpu_kv import _bf16, _f64, _fill, _ids
 from test_gpu_shared import _branch, _check
 
 pytestmark = pytest.mark.gpu
@@ -57,3 +60,22 @@ def test_two_rows_of_which_one_stands_alone():
         _, b, _, _ = _check(cache, model, rng, rows, [1] * 3, groups, 2)
         alone = [192, 64, 0] if groups == [1, 1, 1] else [0, 0, 0] if groups[0] > 1 else [192, 0, 0]
         assert b.shared.tolist() == alone and b._info[4:].view(-1, 8)[len(groups):, 2].tolist() == alone
+
+
+@pytest.mark.parametrize("heads", [2, 64])
+def test_rows_with_more_tokens_than_max_new_are_left_as_they_were(heads):
+    """For few and for many rows of queries; the others have their results."""
+    rng = np.random.default_rng(heads)
+    cache, model, rows, _ = _branch(rng, 16, 64, 1, "e4m3", [4], [200], 20)
+    q = _bf16(rng, 10, heads, 64)
+    b = kv.KvBatch(cache, _ids(*rows), _ids(1, 4, 2, 1), total=10, max_new=2)       # two tokens of no row
+    assert int(cache.status.item()) == 4
+    cache.status.zero_()
+    out, lse = torch.full((10, heads, 64), 3.0, dtype=torch.bfloat16, device="cuda"), torch.full((10, heads), 5.0, device="cuda")
+    cache.attend_shared(0, q.cuda(), b, out=out, lse=lse)
+    left = [1, 2, 3, 4, 8, 9]
+    assert (out[left] == 3).all() and (lse[left] == 5).all()
+    done = [0, 5, 6, 7]
+    want, ref, slack, spread = model.attend(0, _f64(q)[done], [rows[0], rows[2], rows[3]], [0, 1, 3, 4])
+    assert np.all(np.abs(_f64(out[done]) - want) <= S.attend_bound(want, slack, spread))
+    assert np.all(np.abs(_f64(lse[done]) - ref) <= slack + 2.0 ** -20 * (1 + np.abs(ref)))
