@@ -831,13 +831,13 @@ uint64_t bs_kv_attend_work_bytes(const bs_kv_cache* cache, const bs_kv_attend_ar
  * d_seqs and d_starts are the plan's and not looked at.  Of a row that has more
  * new tokens than it holds, the first see nothing.  Results of a row with more
  * than max_new, and of tokens behind the last row's, are left as they were (the
- * plan is flagged).  Rows' own tokens and the groups' common ones
- * are split over workgroups, and a second launch adds a row's parts: scores
- * and sums are held in fp32, probabilities enter the second product in 16
- * significant bits, or, for the common tokens of a group of 64 tokens x heads
- * / kv_heads or more, in BF16.  The same result on every run.  From max_new x
- * heads / kv_heads = 64 on, a row alone fills the matrix instructions: the
- * call is then bs_kv_attend_async.
+ * plan is flagged).  Rows' own tokens and the groups' common ones are split
+ * over workgroups, and a second launch adds a row's parts: scores and sums are
+ * held in fp32, probabilities enter the second product in 16 significant bits,
+ * or, with head_dim up to 128, for the common tokens of a group of 64 tokens x
+ * heads / kv_heads or more, in BF16.  The same result on every run.  From
+ * max_new x heads / kv_heads = 64 on, a row alone fills the matrix
+ * instructions: the call is then bs_kv_attend_async.
  * d_work (16-B aligned): bs_kv_attend_shared_work_bytes (0: a shape that is
  * refused, or one that needs none).  Its first 4096 bytes are zero before the
  * first call that is given it, and every call leaves them so; calls that
