@@ -51,6 +51,76 @@ def test_plans_of_rows_far_longer_than_said():
     cache.check()
 
 
+@pytest.mark.parametrize("times", [1, 100])
+@pytest.mark.parametrize("common", [100, 30000])
+def test_groups_that_do_not_hold(common, times):
+    """In plans of every size, rows named once or many times: flagged, nothing in common (a token counted twice would be seen
+    twice), attention still right, and the next plan is whole again."""
+    _, cache, model, order = _branched(8, 16, 1, 6, common, 10)
+    rng = np.random.default_rng(0)
+    cache.k.random_(0, 60)
+    cache.v.random_(0, 60)
+    cache.scale.fill_(2.0 ** -5)
+    rows, n = order * times, 6 * times
+    q = torch.from_numpy(rng.standard_normal((n, 2, 8)).astype(np.float32)).bfloat16().cuda()
+    want = cache.attend(0, q, _ids(*rows))
+    whole = model.batch(rows, [1] * n, [0, n], n, cache.max_pages)
+    for offs in ([0, 4 * times, 2 * times, n], [0, 5, 3, n], [-5, 2, n], [0, n + 1], [0, 1 << 30], [n, 0], [3, -(1 << 31), n], [1, n, 2]):
+        b = kv.KvBatch(cache, _ids(*rows), groups=_ids(*offs))
+        torch.cuda.synchronize()
+        assert int(cache.status.item()) == 4, offs
+        cache.status.zero_()
+        assert int(b.shared.abs().max()) == 0 and int(b._info[4:].view(-1, 8)[:, 2].abs().max()) == 0, offs
+        _plan_same(b, (*whole[:4], b.lead.cpu().numpy(), np.zeros(n, np.int32)))
+        assert int(b.lead.min()) >= 0 and (b.lead.cpu().numpy() <= np.arange(n)).all()
+        got = cache.attend_shared(0, q, b)
+        assert (got.float() - want.float()).abs().max() <= 2.0 ** -7 * want.float().abs().max(), offs
+        good = sorted([0, n] + [int(x) for x in rng.integers(0, n + 1, len(offs) - 2)])
+        b.update(_ids(*rows), groups=_ids(*good))
+        _plan_same(b, model.batch(rows, [1] * n, good, n, cache.max_pages))
+        got = cache.attend_shared(0, q, b)
+        assert (got.float() - want.float()).abs().max() <= 2.0 ** -7 * want.float().abs().max(), good
+    cache.check()
+
+
+@pytest.mark.parametrize("times", [1, 100])
+@pytest.mark.parametrize("common", [100, 30000])
+def test_rows_and_counts_that_do_not_hold(common, times):
+    """In plans of every size: flagged, unknown rows have no place and nothing in common, the others keep what is theirs."""
+    _, cache, model, order = _branched(9, 16, 1, 6, common, 10)
+    rows, n = order * times, 6 * times
+    counts = [1] * n
+    most = cache.max_pages
+
+    def flagged(rows, counts, total):
+        b = kv.KvBatch(cache, _ids(*rows), _ids(*counts), total=total)
+        first = [t.clone() for t in (b.starts, b.places, b.slots, b.table, b.lead, b.shared, b._info)]
+        b.update(_ids(*rows), _ids(*counts))                        # the same again: nothing is left over
+        torch.cuda.synchronize()
+        assert int(cache.status.item()) == 4 and int(b._info[0]) == 0
+        assert all(torch.equal(x, y) for x, y in zip(first, (b.starts, b.places, b.slots, b.table, b.lead, b.shared, b._info)))
+        cache.status.zero_()
+        return b
+    for bad in (7, -1, 1 << 30, -(1 << 31)):                        # rows 0..6 exist
+        b = flagged([rows[0], bad] + rows[2:], counts, n)
+        assert int(b.places[1]) == int(b.slots[1]) == -1 and (b.table[1] == -1).all() and int(b.shared.max()) == 0
+        want = model.batch(rows, counts, [0, n], n, most)
+        assert b.places[2:].tolist() == want[1][2:].tolist() and b.slots[2:].tolist() == want[2][2:].tolist()
+        b = flagged([bad] + rows[1:], counts, n)                    # the group's first
+        assert int(b.shared.max()) == 0 and int(b._info[4:].view(-1, 8)[:, 2].max()) == 0
+    b = flagged(rows, [1, -3, 2] + counts[3:], n)
+    assert b.starts[:4].tolist() == [0, 1, 1, 3]
+    b = flagged(rows, [1] * (n - 1) + [1 << 30], n)
+    assert b.starts[-2:].tolist() == [n - 1, n]
+    b = flagged(rows, counts, n + 2)
+    assert b.places[n:].tolist() == [-1, -1] and b.slots[n:].tolist() == [-1, -1]
+    b = flagged(rows, [2] * n, 2 * n - 1)
+    assert int(b.starts[n]) == 2 * n - 1
+    b = kv.KvBatch(cache, _ids(*rows))
+    _plan_same(b, model.batch(rows, counts, [0, n], n, most))
+    cache.check()
+
+
 # ------------------------------------------------------------------- reorder
 def test_moves_of_rows_of_many_pages():
     """More blocks of columns than a launch has workgroups for: each takes several."""
