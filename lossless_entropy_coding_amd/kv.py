@@ -92,8 +92,9 @@ class KvCache:
         self._page_work, self._attend_work, self._kept = None, None, []
         self._ref, self._args = C.byref(self.c), L.KvAttendArgs()
         self._args_ref = C.byref(self._args)
-        # the argument block and the workspaces are one call's at a time: held
-        # until the C call, which lets other threads run, has enqueued its work
+        # the argument block, the workspaces and the table's address are one
+        # call's at a time: held until the C call, which lets other threads run,
+        # has enqueued its work (and compact has the new table in its place)
         self._lock = threading.Lock()
         self._page_need, self._reorder_need, self._attend_need = {}, {}, {}        # workspace bytes by the sizes of a call
 
@@ -141,7 +142,8 @@ class KvCache:
     def free(self, rows: torch.Tensor, stream=None) -> None:
         """Empty rows (bs_kv_free_async)."""
         n = self._ids(rows, "rows")
-        rc = L.lib().bs_kv_free_async(self._ref, n, rows.data_ptr(), _stream_of(self.device, stream))
+        with self._lock:
+            rc = L.lib().bs_kv_free_async(self._ref, n, rows.data_ptr(), _stream_of(self.device, stream))
         if rc:
             L.check(rc, "bs_kv_free_async")
 
@@ -170,8 +172,9 @@ class KvCache:
         n = self._ids(source, "source")
         if self._ids(target, "target") != n:
             raise ValueError("one target per source")
-        L.check(L.lib().bs_kv_copy_pages_async(self._ref, n, source.data_ptr(), target.data_ptr(),
-                                               _stream_of(self.device, stream)), "bs_kv_copy_pages_async")
+        with self._lock:
+            L.check(L.lib().bs_kv_copy_pages_async(self._ref, n, source.data_ptr(), target.data_ptr(),
+                                                   _stream_of(self.device, stream)), "bs_kv_copy_pages_async")
 
     def compact(self, table_out: torch.Tensor | None = None, refs_out: torch.Tensor | None = None, stream=None) -> None:
         """Move the pages in use to the lowest places (bs_kv_compact_async).
@@ -238,9 +241,9 @@ class KvCache:
             raise ValueError("k and v must have one shape and be bfloat16 or float32")
         ks, vs, total = self._tokens(k, self.kv_heads, "k"), self._tokens(v, self.kv_heads, "v"), k.shape[0]
         n, most, at = self._rows(rows, starts, total, max_new)
-        rc = L.lib().bs_kv_append_async(self._ref, layer if 0 <= layer < _MAX else _MAX, n, rows.data_ptr(), at, total, most, k.data_ptr(), ks,
-                                        v.data_ptr(), vs, L.T_FP32 if kind is _FP32 else L.T_BF16,
-                                        _stream_of(self.device, stream))
+        with self._lock:
+            rc = L.lib().bs_kv_append_async(self._ref, layer if 0 <= layer < _MAX else _MAX, n, rows.data_ptr(), at, total, most, k.data_ptr(),
+                                            ks, v.data_ptr(), vs, L.T_FP32 if kind is _FP32 else L.T_BF16, _stream_of(self.device, stream))
         if rc:
             L.check(rc, "bs_kv_append_async")
 
@@ -420,7 +423,8 @@ class KvBatch:
             raise ValueError("one count per row" if self._counted else "a plan made without counts has one token per row")
         if (1 if groups is None else cache._ids(groups, "groups") - 1) != self.n_groups:
             raise ValueError(f"offsets of {self.n_groups} groups")
-        rc = L.lib().bs_kv_batch_async(cache._ref, self.ref, rows.data_ptr(), None if counts is None else counts.data_ptr(),
-                                       None if groups is None else groups.data_ptr(), _stream_of(cache.device, stream))
+        with cache._lock:
+            rc = L.lib().bs_kv_batch_async(cache._ref, self.ref, rows.data_ptr(), None if counts is None else counts.data_ptr(),
+                                           None if groups is None else groups.data_ptr(), _stream_of(cache.device, stream))
         if rc:
             L.check(rc, "bs_kv_batch_async")

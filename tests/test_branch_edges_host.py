@@ -2,11 +2,14 @@
 that lie over each other, workspaces, the references at the ends of a type."""
 import ctypes as C
 import math
+import threading
 
 import numpy as np
 import pytest
+import torch
 
 from lossless_entropy_coding_amd import _lib as L
+from lossless_entropy_coding_amd import kv
 from oracle import serving as S
 from test_branches_host import AT, PLAN, _attend, _cache, _plan
 
@@ -75,3 +78,38 @@ def test_no_groups_need_no_more_workspace_than_one(rows, pages):
     need = [int(lib.bs_kv_attend_shared_work_bytes(C.byref(cache), C.byref(args), C.byref(_plan(n_seqs=rows, total=rows, max_new=1, n_groups=n))))
             for n in (0, 1)]
     assert 4096 < need[0] <= need[1]
+
+
+# ------------------------------------------------------------------- threads
+def _i(*v):
+    return torch.tensor(v, dtype=torch.int32)
+
+
+@pytest.mark.parametrize("name", ["bs_kv_batch_async", "bs_kv_append_async", "bs_kv_free_async", "bs_kv_copy_pages_async", "bs_kv_extend_async"])
+def test_no_call_comes_between_a_compaction_and_its_table(name, monkeypatch):
+    """Another thread's call is enqueued before the pages move, or after the cache has their new table."""
+    real, seen, late = L.lib(), [], []
+
+    class Stub:
+        def __getattr__(self, f):
+            if f == "bs_kv_compact_async":
+                def compact(*args):
+                    late.append(threading.Thread(target=calls[name]))
+                    late[0].start()
+                    late[0].join(0.2)
+                    return 0
+                return compact
+            if f.startswith("bs_kv_") and f.endswith("_async"):
+                return lambda cache, *args: seen.append((f, cache._obj.d_table)) or 0
+            return getattr(real, f)
+    monkeypatch.setattr(L, "lib", lambda: Stub())
+    monkeypatch.setattr(kv, "_stream_of", lambda device, stream: 0)
+    cache = kv.KvCache(1, 1, 64, 16, 4, 4, page_tokens=16, device="cpu")
+    plan, x = kv.KvBatch(cache, _i(0, 1)), torch.zeros(2, 1, 64, dtype=torch.bfloat16)
+    calls = {"bs_kv_batch_async": lambda: plan.update(_i(0, 1)), "bs_kv_append_async": lambda: cache.append(0, x, x, _i(0, 1)),
+             "bs_kv_free_async": lambda: cache.free(_i(0)), "bs_kv_copy_pages_async": lambda: cache.copy_pages(_i(0), _i(1)),
+             "bs_kv_extend_async": lambda: cache.extend(_i(0), _i(1))}
+    old = cache.table.data_ptr()
+    cache.compact()
+    late[0].join(10)
+    assert cache.table.data_ptr() != old and seen[-1] == (name, cache.table.data_ptr())
