@@ -66,8 +66,8 @@ struct KvAttend {
 struct KvShared {
     KvAttend a;
     const int32_t* places;
-    const int32_t* info;        // 4 words, then 8 of each group and row: first and end token, common tokens, row of the
-                                // table, least and largest place, 2 unused
+    const int32_t* info;        // 4 words, then 8 of each group and row: first and end token, common tokens (0: the row stands
+                                // alone), row of the table, least and largest place (of those that do not), 2 unused
     uint32_t groups;
     uint32_t blocks;            // row blocks of all groups at most
     uint32_t row_blocks;        // of one row's own tokens

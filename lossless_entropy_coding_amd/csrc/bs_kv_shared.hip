@@ -22,7 +22,7 @@
 //   4 x 32 rows on 4099 tokens and up to 1021 more, a window of 4096, 16 query
 //     heads on 8 of 256, e4m3: 90 us, 241 (bytes: most are the rows' own)
 //   32 rows on 8000 and up to 600 more, 40 heads on 8 of 128, int8: 33 us, 83
-//   8 rows of 4 new tokens on 100003, 40 heads on 8 of 128, e4m3: 108 us, 342
+//   8 rows of 4 new tokens on 100003, 40 heads on 8 of 128, e4m3: 107 us, 342
 //     (a busy CU's matrix instructions take 32% of its SIMDs' time, the vector
 //     ones 57%, and they hardly overlap)
 // A row's parts joined in this launch by the workgroup that ends last took

@@ -293,9 +293,10 @@ class KvCache:
         plan's order; the other arguments and the results are attend's.  The
         plan is this cache's and holds until its rows change.  Where
         batch.max_new x heads / kv_heads is 64 or more it is attend itself, so
-        a plan with counts should say its max_new.  Where few tokens are read
-        (rows x kv_heads x length / 64 below about 500) attend is as fast or
-        up to 2 us faster, since it takes one launch."""
+        a plan with counts should say its max_new.  Where little is read attend
+        is faster, since it takes one launch: by up to 1.2 us (2.4 outside a
+        graph) where rows x kv_heads x length / 64 is below about 500, and for
+        rows of up to some 150 tokens by 1.4 us (few rows) to 8 (64 rows)."""
         if batch.cache is not self:
             raise ValueError("the plan is another cache's")
         total, heads, qs, os, out, lse, window, sinks, max_len = self._results(q, out, lse, window, sinks, batch.max_len, stream)
@@ -376,7 +377,10 @@ class KvBatch:
     extend, for all layers.  Row rows[i] of the cache has counts[i] new tokens
     (without counts one each), its last ones, side by side in the step's
     tensors; groups: offsets into rows of the runs of rows that go on from one
-    prompt (without: one group of all rows).
+    prompt (without: one group of all rows).  A row that has fewer than 64
+    tokens in common with its group's first one, as a beam that was emptied and
+    grows anew, stands alone in attention; the others go on together if they
+    are two at least and half of the group.
 
     starts (rows + 1), places and slots (tokens; int64 slots), table (rows,
     pages of max_len), lead and shared (rows) are int32 tensors on the device
