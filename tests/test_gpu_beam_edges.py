@@ -50,3 +50,25 @@ def test_saturated_logits_keep_their_order(half, softcap, keep):
     assert got.scores[0].unique().numel() == 1
     assert got.parents[0].tolist() == [0] * keep and got.tokens[0].tolist() == best
     _check(x, [0.0, 0.0, -1.0, -2.0], 2, keep, softcap=softcap)
+
+
+def test_the_most_beams_of_a_call():
+    """65535 of them, one to a request and 64; a few requests are looked at."""
+    for batch, beams, vocab in ((65535, 1, 19), (1023, 64, 130)):
+        x, s = _logits(batch, batch * beams, vocab, True)
+        got = beam.Beams(batch, beams, keep=3).select(x.cuda(), torch.tensor(s).cuda())
+        for at in (0, 1, batch // 2, batch - 1):
+            part = type(got)(*(t[at:at + 1] for t in got))
+            part = part._replace(parents=part.parents - at * beams)
+            rows = slice(at * beams, (at + 1) * beams)
+            _check(x[rows], s[rows], beams, 3, got=part)
+
+
+@pytest.mark.parametrize("half", [True, False])
+def test_rows_more_than_4_gib_apart(half):
+    x, s = _logits(3, 4, 5001, half)
+    stride = (1 << 31) + 7 if half else (1 << 30) + 5
+    flat = torch.empty(3 * stride + 5001, dtype=x.dtype, device="cuda")
+    rows = flat.as_strided((4, 5001), (stride, 1))
+    rows.copy_(x)
+    _check(x, s, 2, 4, got=beam.Beams(2, 2, keep=4).select(rows, torch.tensor(s).cuda()))

@@ -3,9 +3,10 @@ import numpy as np
 import pytest
 import torch
 
-from lossless_entropy_coding_amd import kv
+from lossless_entropy_coding_amd import beam, kv
 from oracle import serving as S
-from test_gpu_kv import _bf16, _f64, _fill, _ids
+from test_gpu_beam import _check as _choices
+from test_gpu_kv import _bf16, _f64, _fill, _ids, _same
 from test_gpu_shared import _branch, _check
 
 pytestmark = pytest.mark.gpu
@@ -79,3 +80,63 @@ def test_rows_with_more_tokens_than_max_new_are_left_as_they_were(heads):
     want, ref, slack, spread = model.attend(0, _f64(q)[done], [rows[0], rows[2], rows[3]], [0, 1, 3, 4])
     assert np.all(np.abs(_f64(out[done]) - want) <= S.attend_bound(want, slack, spread))
     assert np.all(np.abs(_f64(lse[done]) - ref) <= slack + 2.0 ** -20 * (1 + np.abs(ref)))
+
+
+@pytest.mark.parametrize("dim,kv_heads,heads", [(64, 2, 2), (128, 1, 3)])
+def test_many_groups(dim, kv_heads, heads):
+    """More groups than a wave looks through at a time, some of them empty, of one row, or without common tokens."""
+    rng = np.random.default_rng(dim)
+    sizes = [int(x) for x in rng.integers(1, 4, 150)]
+    cache, model, rows, _ = _branch(rng, 16, dim, kv_heads, "e4m3", sizes, [int(x) for x in rng.integers(1, 260, 150)], 20)
+    n = sum(sizes)
+    _check(cache, model, rng, rows, [1] * n, sizes, heads)
+    groups = []
+    for x in sizes:
+        groups += [0] * int(rng.integers(0, 3)) + [x]
+    _check(cache, model, rng, rows, [1] * n, groups + [0], heads, window=70)
+    counts = [int(min(c, model.lens[r])) for r, c in zip(rows, rng.integers(0, 4, n))]
+    _check(cache, model, rng, rows, counts, sizes, heads, softcap=20.0)
+
+
+@pytest.mark.parametrize("dim,heads,rows,new", [(64, 63, 3, 1), (192, 31, 4, 2), (256, 9, 30, 7), (128, 21, 10, 3), (192, 1, 90, 1)])
+def test_stacks_of_every_shape(dim, heads, rows, new):
+    """Query heads that leave a row of tiles unfilled, just below what goes to the attention of many rows, and large stacks at
+    the widths that take 16 rows at a time."""
+    rng = np.random.default_rng(dim + heads)
+    cache, model, order, _ = _branch(rng, 32, dim, 1, "int8", [rows], [500], 60)
+    counts = [int(c) for c in rng.integers(0, new + 1, rows)]
+    counts[rows // 2] = new
+    for kw in ({}, dict(window=77, sinks=5)):
+        _check(cache, model, rng, order, counts, [rows], heads, **kw)
+
+
+def test_everything_first_called_in_a_capture():
+    """Plan, attention, selection and move without a call before the capture: their workspaces are the graph's, and every
+    replay has them as a first call does."""
+    rng = np.random.default_rng(3)
+    cache, model, rows, _ = _branch(rng, 16, 64, 1, "e4m3", [4], [300], 40)
+    ids, q = _ids(*rows), torch.zeros(4, 2, 64, dtype=torch.bfloat16, device="cuda")
+    x, scores, parents = torch.zeros(4, 9000, device="cuda"), torch.zeros(4, device="cuda"), _ids(0, 1, 2, 3)
+    beams, graph, side = beam.Beams(1, 4), torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        with torch.cuda.graph(graph, stream=side):
+            plan = kv.KvBatch(cache, ids)
+            got, lse = cache.attend_shared(0, q, plan, lse=True)
+            best = beams.select(x, scores)
+            cache.reorder(ids, parents)
+    torch.cuda.synchronize()
+    for step in range(5):
+        new = _bf16(rng, 4, 2, 64)
+        y = torch.from_numpy(rng.standard_normal((4, 9000)).astype(np.float32))
+        s = [-float(v) for v in rng.random(4)]
+        moved = [int(p) for p in rng.integers(0, 4, 4)]
+        q.copy_(new), x.copy_(y), scores.copy_(torch.tensor(s)), parents.copy_(_ids(*moved))
+        graph.replay()
+        torch.cuda.synchronize()
+        out, ref, slack, spread = model.attend(0, _f64(new), rows)
+        assert np.all(np.abs(_f64(got) - out) <= S.attend_bound(out, slack, spread)), step
+        _choices(y, s, 4, 4, got=best)
+        model.reorder(rows, moved)
+        _same(cache, model, ("refs", "table", "lens"))
+        _fill(cache, model, rng, rows, [1, 2, 17, 1])                # eager work between the replays
